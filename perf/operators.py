@@ -22,8 +22,9 @@ that count any):
 States in 8 bits: blocks of 256 values with one float scale, the largest magnitude of the block. m is held
 as a signed code c that stands for scale c |c| / 127^2, v as a code c that stands for scale (c / 255)^4;
 each takes the code whose value, for v whose value's root, is nearest, and a v above zero takes one at least.
-m' and v' that are to be held so are formed and compared in 64 bits, so that the choice next to a border
-is the same for everybody.
+m' and v' that are to be held so are formed and compared in 64 bits, each operation rounded by itself, so that
+the choice next to a border is the same for everybody (with b1 = 0.9 a block's largest often lies halfway
+between two floats).
 """
 import math
 
@@ -284,11 +285,12 @@ def _encode_v(v):
 
 def _decode_m(c, scale):
     c = c.double().view(-1, BLOCK)
-    return (c * c.abs() * (scale.double() / 127.0 ** 2)[:, None]).view(-1)
+    return (c * c.abs() * (scale.double() * (1.0 / 127.0 ** 2))[:, None]).view(-1)
 
 
 def _decode_v(c, scale):
-    return (c.double().view(-1, BLOCK) ** 4 * (scale.double() / 255.0 ** 4)[:, None]).view(-1)
+    square = c.double().view(-1, BLOCK).square()
+    return (square * square * (scale.double() * (1.0 / 255.0 ** 4))[:, None]).view(-1)
 
 
 def _plain_adamw(s):
@@ -303,7 +305,7 @@ def _plain_adamw(s):
     if eight:
         g = g.double()
         m = _decode_m(s["m"], s["m_scale"]) * BETA1 + g * (1.0 - BETA1)
-        v = _decode_v(s["v"], s["v_scale"]) * BETA2 + g * g * (1.0 - BETA2)
+        v = _decode_v(s["v"], s["v_scale"]) * BETA2 + (g * g) * (1.0 - BETA2)
         s["m"], s["m_scale"] = _encode_m(m)
         s["v"], s["v_scale"] = _encode_v(v)
         m, v = m.float(), v.float()
@@ -385,14 +387,15 @@ def exact(case, seed):
         g = g * clip[1].float()  # held as a float
     t = s["step"] + 1
     old = s["master"] if case["master"] else s["param"]
-    if case["bits"] == 8:
-        share = s["m"].to(torch.float64) / 127
-        m = share * share.abs() * s["m_scale"].to(torch.float64).repeat_interleave(BLOCK)
-        v = (s["v"].to(torch.float64) / 255) ** 4 * s["v_scale"].to(torch.float64).repeat_interleave(BLOCK)
+    if case["bits"] == 8:  # whole numbers times the share of the scale that one of them stands for
+        one = (s["m_scale"].to(torch.float64) * (1 / 127 ** 2)).repeat_interleave(BLOCK)
+        m = one * (s["m"].long() * s["m"].long().abs()).to(torch.float64)
+        one = (s["v_scale"].to(torch.float64) * (1 / 255 ** 4)).repeat_interleave(BLOCK)
+        v = one * (s["v"].long() ** 4).to(torch.float64)
     else:
         m, v = s["m"].to(torch.float64), s["v"].to(torch.float64)
-    m = torch.lerp(g, m, BETA1)
-    v = torch.lerp(g * g, v, BETA2)
+    m = BETA1 * m + (1 - BETA1) * g
+    v = BETA2 * v + (1 - BETA2) * (g * g)
     step = (m / (1 - BETA1 ** t)) / ((v / (1 - BETA2 ** t)).sqrt() + EPS)
     decay = [0.0 if i % 3 == 0 else DECAY for i in range(len(s["sizes"]))]
     lengths = torch.tensor([-(-n // ALIGN) * ALIGN for n in s["sizes"]], device=DEV)
