@@ -56,6 +56,9 @@ extern "C" {
 
 #define MOE_NO_CAPACITY (-1)
 #define MOE_MAX_EXPERTS 1024
+#define MOE_MAX_SEQS 65536                         /* sequences of one balance loss */
+#define MOE_MAX_TENSOR_VALUES ((int64_t)1 << 33)   /* values of one optimizer tensor */
+#define MOE_ADAMW_BLOCK 256                        /* values that share a scale in 8-bit optimizer states */
 
 typedef enum moe_status {
   MOE_OK = 0,
@@ -414,6 +417,155 @@ size_t moe_backward_workspace_size(const moe_desc *desc);
  * launches on `stream` (capturable into a HIP graph). */
 moe_status moe_backward(const moe_desc *desc, const moe_weights *weights, const void *x, const moe_routing *routing,
                         const void *dy, void *dx, moe_grads *grads, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* moe_backward with a gradient on the router's logits added to the gates': the losses that
+ * depend on the logits themselves (moe_balance_loss) reach dw_router and dx this way.
+ *   dlogits [T, E] float (as moe_balance_loss or moe_balance_loss_backward writes it)
+ * The sum dl is rounded to bf16 for the two products with it, as in moe_backward.  Other
+ * arguments, results and errors as for moe_backward; dlogits of zeros gives its results. */
+moe_status moe_backward_with_dlogits(const moe_desc *desc, const moe_weights *weights, const void *x,
+                                     const moe_routing *routing, const void *dy, const float *dlogits, void *dx,
+                                     moe_grads *grads, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------- balance loss with gradient */
+
+/* Workspace bytes of moe_balance_loss; 0 for an invalid descriptor or num_seqs. */
+size_t moe_balance_workspace_size(const moe_desc *desc, int32_t num_seqs);
+
+/* Load-balancing loss ([SMoE] "Маршрутизация токена и auxiliary loss") sequence by sequence,
+ * the router's z loss, per-expert counts and, if asked for, the gradient of their sum on the
+ * logits, all in one pass over the logits.  With N_s the counted tokens of sequence s, N
+ * those of all sequences and S' the sequences that count any:
+ *   c_si = assignments of counted tokens to expert i (router choice, before capacity)
+ *   f_si = c_si / (k N_s),  P_si = 1/N_s sum_t softmax(l_t)_i,  z_t = log sum_i exp(l_ti)
+ *   losses[0] = alpha E / S' sum_s sum_i f_si P_si
+ *   losses[1] = z_coeff / N sum_t z_t^2
+ *   dlogits_ti = p_ti (alpha E / (S' N_s) (f_si - sum_j f_sj p_tj) + 2 z_coeff / N z_t)
+ * (f held fixed: counts are piecewise constant).  One sequence of all tokens gives
+ * moe_router_aux_loss's value.  Only descriptor fields num_tokens, num_experts and top_k
+ * matter.
+ *   logits      [T, E] float; -inf is an expert with probability 0; a counted token with
+ *               no finite logit has no probabilities: it adds nothing to P and the z loss
+ *               and gets a zero gradient (its ids are counted)
+ *   topk_ids    [T, k] int32; ids outside [0, E) are not counted
+ *   token_mask  [T] uint8 or NULL: zero = not counted (padding); its logits may hold
+ *               anything, NaN included
+ *   seq_offsets [num_seqs + 1] int32 or NULL (one sequence of all T tokens, num_seqs 1):
+ *               non-decreasing within [0, T] (precondition); sequence s holds tokens
+ *               seq_offsets[s] .. seq_offsets[s + 1] - 1, possibly none; tokens before the
+ *               first and behind the last sequence are not counted
+ *   counts      [num_seqs, E] int32, written
+ *   seq_tokens  [num_seqs] int32, written: N_s
+ *   mean_probs  [num_seqs, E] float, written: P (zeros where N_s is 0)
+ *   losses      [2] float, written; 0 when nothing is counted
+ *   dlogits     [T, E] float or NULL, written in full: zero for tokens not counted
+ *   ws          at least moe_balance_workspace_size(desc, num_seqs) bytes
+ * Sums in fixed orders (bit-reproducible).  Only kernel launches on `stream`. */
+moe_status moe_balance_loss(const moe_desc *desc, const float *logits, const int32_t *topk_ids,
+                            const uint8_t *token_mask, const int32_t *seq_offsets, int32_t num_seqs, float alpha,
+                            float z_coeff, int32_t *counts, int32_t *seq_tokens, float *mean_probs, float *losses,
+                            float *dlogits, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* The gradient alone, for upstream gradients known only after the forward pass:
+ *   dlogits = dloss[0] * d losses[0] / d logits + dloss[1] * d losses[1] / d logits
+ *   counts, seq_tokens  as moe_balance_loss wrote them
+ *   dloss               [2] float (device) or NULL (both 1)
+ *   dlogits             [T, E] float, written in full
+ * Other arguments as for moe_balance_loss; no workspace. */
+moe_status moe_balance_loss_backward(const moe_desc *desc, const float *logits, const uint8_t *token_mask,
+                                     const int32_t *seq_offsets, int32_t num_seqs, const int32_t *counts,
+                                     const int32_t *seq_tokens, float alpha, float z_coeff, const float *dloss,
+                                     float *dlogits, hipStream_t stream);
+
+/* --------------------------------------------------------- gradient norm and AdamW step */
+
+/* One gradient tensor of n values (0 <= n <= MOE_MAX_TENSOR_VALUES). */
+typedef struct moe_grad_view {
+  const void *grad; /* [n] dtype (device); may be NULL when n == 0 */
+  int64_t n;
+  int32_t dtype; /* moe_dtype */
+  int32_t reserved;
+} moe_grad_view;
+
+/* Workspace bytes of moe_grad_norm for these tensors; 0 for invalid ones.  Host only. */
+size_t moe_grad_norm_workspace_size(const moe_grad_view *grads, int32_t num_tensors);
+
+/* Norm over every value of every tensor, and the factor that clips it:
+ *   out[0] = sqrt(sum g^2),  out[1] = min(1, max_norm / (out[0] + 1e-6))
+ * summed in 64 bits in a fixed order.  A norm that is not finite has out[1] = NaN, which
+ * moe_adamw_step takes as "leave everything as it is".  out stays on the device:
+ * moe_adamw_hparams.norm takes it as it is.
+ *   grads     HOST array of num_tensors views (read during the call only)
+ *   max_norm  above 0; infinity: no clipping
+ *   out       [2] float, written
+ *   ws        at least moe_grad_norm_workspace_size(grads, num_tensors) bytes
+ * Only kernel launches on `stream`. */
+moe_status moe_grad_norm(const moe_grad_view *grads, int32_t num_tensors, float max_norm, float *out, void *ws,
+                         size_t ws_bytes, hipStream_t stream);
+
+/* One parameter tensor of n values with its gradient and optimizer state (device pointers).
+ * States in 8 bits: each MOE_ADAMW_BLOCK consecutive values (the last block may hold fewer)
+ * share one float scale, the block's largest magnitude; a code c of m (int8) stands for
+ * m_scale c |c| / 127^2, a code c of v (uint8) for v_scale (c / 255)^4.  Each takes the code
+ * whose value (for v: whose value's root) is nearest, and a v above zero one at least.  m'
+ * and v' are formed and compared in 64 bits, every operation of the formulas rounded by
+ * itself (m_scale * (1 / 127^2) and v_scale * (1 / 255^4) first), so that codes and scales
+ * are the same for any program that follows them.  A block whose largest is below the smallest normal float is held as zeros;
+ * one with a value that is not finite gets a NaN scale.  Zeros everywhere are the initial
+ * state of both forms. */
+typedef struct moe_adamw_tensor {
+  void *param;      /* [n] param_dtype, updated */
+  const void *grad; /* [n] grad_dtype */
+  float *master;    /* [n] float copy of a bf16 parameter, updated, with param its rounding
+                       (param is not read then); NULL: none -- the bf16 value itself is updated
+                       and rounded to nearest, so that steps below half its last place are lost */
+  void *m, *v;      /* [n] float, or int8 / uint8 codes; updated */
+  float *m_scale;   /* [ceil(n / MOE_ADAMW_BLOCK)] for 8-bit states; unused otherwise */
+  float *v_scale;
+  int64_t n;           /* 0 <= n <= MOE_MAX_TENSOR_VALUES; 0: the tensor is passed over */
+  int32_t param_dtype; /* moe_dtype; MOE_DTYPE_F32 takes no master */
+  int32_t grad_dtype;  /* moe_dtype */
+  int32_t state_bits;  /* 32 or 8 */
+  float weight_decay;  /* finite, >= 0 */
+} moe_adamw_tensor;
+
+typedef struct moe_adamw_hparams {
+  double lr, beta1, beta2, eps; /* lr >= 0; betas in [0, 1); eps > 0 */
+  int64_t step;                 /* t >= 1, the number of this step */
+  /* Optional device scalars, read when the step runs (a captured step then follows them on
+   * every replay): lr and t in the place of the two fields above (a t below 1 counts as 1),
+   * and moe_grad_norm's `out`, whose out[1] every gradient is multiplied by.  When out[1] is
+   * NaN the step writes nothing. */
+  const float *lr_dev;     /* [1] or NULL */
+  const int64_t *step_dev; /* [1] or NULL */
+  const float *norm;       /* [2] or NULL */
+} moe_adamw_hparams;
+
+/* The conditions on a list of tensors that moe_adamw_step checks (pointers, alignment,
+ * types, sizes), and that no buffer that the step writes overlaps another buffer of the
+ * list.  Host only, no device access.  moe_adamw_step itself checks this last only among
+ * the parameters (the same tensor twice), in the debug build in full. */
+moe_status moe_adamw_check_tensors(const moe_adamw_tensor *tensors, int32_t num_tensors);
+
+/* One AdamW step (decoupled weight decay) of every tensor, in a launch per 40 tensors:
+ *   g' = out[1] g;  m' = b1 m + (1 - b1) g';  v' = b2 v + (1 - b2) g'^2
+ *   w' = w (1 - lr wd) - lr / (1 - b1^t) m' / (sqrt(v') / sqrt(1 - b2^t) + eps)
+ * in float (8-bit states: m' and v' in 64 bits), w' rounded once to param_dtype.
+ * A gradient that is not finite makes its value's state and parameter so.  Values past n
+ * are not touched.  Tile-major weight copies are the caller's to rewrite
+ * (moe_tile_expert_weights).
+ *   tensors  HOST array of num_tensors descriptors (read during the call only)
+ * Only kernel launches on `stream`. */
+moe_status moe_adamw_step(const moe_adamw_tensor *tensors, int32_t num_tensors, const moe_adamw_hparams *hparams,
+                          hipStream_t stream);
+
+/* 8-bit states as the floats they stand for (checkpoints, inspection).
+ *   tensors  as for moe_adamw_step, every one with state_bits 8; param, grad and master are
+ *            not looked at
+ *   m_out, v_out  HOST arrays of num_tensors device pointers to [n] float; NULL (the array or
+ *            an entry): not wanted */
+moe_status moe_adamw_read_states(const moe_adamw_tensor *tensors, int32_t num_tensors, float *const *m_out,
+                                 float *const *v_out, hipStream_t stream);
 
 /* Bytes of the tile-major copy of num_experts experts' gate_up (which = 0) or down
  * (which = 1) weights for desc's shapes: per expert, ceil(f / 128) gate_up tiles (128 gate

@@ -2,11 +2,14 @@
 // the forward pass.  Declarations and contracts are in include/moe.h.
 #include "moe.h"
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <exception>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "kernels.hpp"
@@ -956,17 +959,10 @@ moe::GroupedGemmArgs gemm_args(int32_t G, int64_t rows_max, int32_t group_rows_m
   return a;
 }
 
-}  // namespace
-
-extern "C" {
-
-size_t moe_backward_workspace_size(const moe_desc *desc) {
-  if (check_bwd_desc(desc) != MOE_OK) return 0;
-  return bwd_layout(*desc).total;
-}
-
-moe_status moe_backward(const moe_desc *desc, const moe_weights *weights, const void *x, const moe_routing *routing,
-                        const void *dy, void *dx, moe_grads *grads, void *ws, size_t ws_bytes, hipStream_t stream) {
+// moe_backward; dlogits [T, E]: a gradient on the router's logits to be added, or NULL.
+moe_status backward(const moe_desc *desc, const moe_weights *weights, const void *x, const moe_routing *routing,
+                    const void *dy, const float *dlogits, void *dx, moe_grads *grads, void *ws, size_t ws_bytes,
+                    hipStream_t stream) {
   MOE_TRY(check_bwd_desc(desc));
   const moe_desc &D = *desc;
   if (!weights) return fail(MOE_ERR_INVALID, "weights is NULL");
@@ -1091,7 +1087,7 @@ moe_status moe_backward(const moe_desc *desc, const moe_weights *weights, const 
 
   // ---- router: dl from the gate gradients; dW_r = dl^T x, dx += dl W_r
   MOE_TRY(hcall(moe::launch_gates_bwd(ids, gates, at<float>(ws, L.dpart), f / 16, serving, slot, offsets, T, E, k,
-                                      (int)L.Epad, at<float>(ws, L.dl), W(L.dl16), stream),
+                                      (int)L.Epad, dlogits, at<float>(ws, L.dl), W(L.dl16), stream),
               "gate backward"));
   MOE_TRY(hcall(moe::launch_transpose_bf16(W(L.dl16), 0, T, (int)L.Epad, 1, nullptr, nullptr, nullptr, 0, L.Tpad,
                                          W(L.dlT), L.Tpad, 0, stream),
@@ -1174,6 +1170,293 @@ moe_status moe_backward(const moe_desc *desc, const moe_weights *weights, const 
   // ---- dx: the expert rows of each token, the router term and the shared expert's
   MOE_TRY(hcall(moe::launch_dx_gather(W(L.dxr), R, serving, slot, offsets, T, d, k, W(L.dxrt), dxs, dx, stream), "dx"));
   return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_backward_workspace_size(const moe_desc *desc) {
+  if (check_bwd_desc(desc) != MOE_OK) return 0;
+  return bwd_layout(*desc).total;
+}
+
+moe_status moe_backward(const moe_desc *desc, const moe_weights *weights, const void *x, const moe_routing *routing,
+                        const void *dy, void *dx, moe_grads *grads, void *ws, size_t ws_bytes, hipStream_t stream) {
+  return backward(desc, weights, x, routing, dy, nullptr, dx, grads, ws, ws_bytes, stream);
+}
+
+moe_status moe_backward_with_dlogits(const moe_desc *desc, const moe_weights *weights, const void *x,
+                                     const moe_routing *routing, const void *dy, const float *dlogits, void *dx,
+                                     moe_grads *grads, void *ws, size_t ws_bytes, hipStream_t stream) {
+  MOE_TRY(check_bwd_desc(desc));
+  if (desc->num_tokens > 0) MOE_TRY(check_ptr(dlogits, "dlogits"));
+  return backward(desc, weights, x, routing, dy, dlogits, dx, grads, ws, ws_bytes, stream);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------- balance loss, gradient norm, AdamW
+
+namespace {
+
+moe_status check_num_seqs(int32_t num_seqs, const int32_t *seq_offsets) {
+  if (num_seqs < 1 || num_seqs > MOE_MAX_SEQS)
+    return fail(MOE_ERR_INVALID, "num_seqs %d outside [1, %d]", num_seqs, MOE_MAX_SEQS);
+  if (!seq_offsets && num_seqs != 1)
+    return fail(MOE_ERR_INVALID, "num_seqs %d without seq_offsets (NULL means one sequence)", num_seqs);
+  return check_opt_ptr(seq_offsets, "seq_offsets");
+}
+
+moe_status check_coeff(float c, const char *name) {
+  return std::isfinite(c) ? MOE_OK : fail(MOE_ERR_INVALID, "%s is not finite", name);
+}
+
+moe_status check_grads(const moe_grad_view *grads, int32_t num) {
+  if (num < 0) return fail(MOE_ERR_INVALID, "num_tensors %d < 0", num);
+  if (num > 0 && !grads) return fail(MOE_ERR_INVALID, "grads is NULL");
+  for (int32_t i = 0; i < num; ++i) {
+    const moe_grad_view &g = grads[i];
+    if (g.n < 0) return fail(MOE_ERR_INVALID, "grads[%d].n %lld < 0", i, (long long)g.n);
+    if (g.n > MOE_MAX_TENSOR_VALUES) return fail(MOE_ERR_UNSUPPORTED, "grads[%d] holds more than 2^33 values", i);
+    if (g.dtype != MOE_DTYPE_F32 && g.dtype != MOE_DTYPE_BF16)
+      return fail(MOE_ERR_UNSUPPORTED, "grads[%d].dtype %d", i, g.dtype);
+    if (g.n == 0) continue;
+    if (!g.grad) return fail(MOE_ERR_INVALID, "grads[%d].grad is NULL", i);
+    if (!aligned16(g.grad)) return fail(MOE_ERR_INVALID, "grads[%d].grad is not 16-byte aligned", i);
+  }
+  return MOE_OK;
+}
+
+std::vector<moe::NormTensor> norm_tensors(const moe_grad_view *grads, int32_t num) {
+  std::vector<moe::NormTensor> t(num);
+  for (int32_t i = 0; i < num; ++i) t[i] = {grads[i].grad, grads[i].n, grads[i].dtype == MOE_DTYPE_F32, 0};
+  return t;
+}
+
+// A buffer of a moe_adamw_tensor: what it is called, where it is, its bytes, and whether the
+// step writes it.
+struct Buffer {
+  const char *name;
+  const void *p;
+  size_t bytes;
+  bool written;
+  bool state;  // m, v and their scales
+};
+int adamw_buffers(const moe_adamw_tensor &t, Buffer (&b)[7]) {
+  const size_t n = (size_t)t.n, blocks = (n + MOE_ADAMW_BLOCK - 1) / MOE_ADAMW_BLOCK;
+  const size_t state = t.state_bits == 8 ? 1 : 4;
+  int c = 0;
+  b[c++] = {"param", t.param, n * elem_bytes(t.param_dtype), true, false};
+  b[c++] = {"grad", t.grad, n * elem_bytes(t.grad_dtype), false, false};
+  b[c++] = {"m", t.m, n * state, true, true};
+  b[c++] = {"v", t.v, n * state, true, true};
+  if (t.state_bits == 8) {
+    b[c++] = {"m_scale", t.m_scale, blocks * 4, true, true};
+    b[c++] = {"v_scale", t.v_scale, blocks * 4, true, true};
+  }
+  if (t.master) b[c++] = {"master", t.master, n * 4, true, false};
+  return c;
+}
+
+// state_only: param, grad and master are not looked at.
+moe_status check_adamw(const moe_adamw_tensor *tensors, int32_t num, bool state_only) {
+  if (num < 0) return fail(MOE_ERR_INVALID, "num_tensors %d < 0", num);
+  if (num > 0 && !tensors) return fail(MOE_ERR_INVALID, "tensors is NULL");
+  for (int32_t i = 0; i < num; ++i) {
+    const moe_adamw_tensor &t = tensors[i];
+    if (t.n < 0) return fail(MOE_ERR_INVALID, "tensors[%d].n %lld < 0", i, (long long)t.n);
+    if (t.n > MOE_MAX_TENSOR_VALUES) return fail(MOE_ERR_UNSUPPORTED, "tensors[%d] holds more than 2^33 values", i);
+    if (t.state_bits != 32 && t.state_bits != 8)
+      return fail(MOE_ERR_UNSUPPORTED, "tensors[%d].state_bits %d: 32 or 8", i, t.state_bits);
+    if (!state_only) {
+      for (int32_t dt : {t.param_dtype, t.grad_dtype})
+        if (dt != MOE_DTYPE_F32 && dt != MOE_DTYPE_BF16) return fail(MOE_ERR_UNSUPPORTED, "tensors[%d]: dtype %d", i, dt);
+      if (t.master && t.param_dtype == MOE_DTYPE_F32)
+        return fail(MOE_ERR_INVALID, "tensors[%d]: a float parameter takes no master copy", i);
+      if (!(t.weight_decay >= 0.f) || !std::isfinite(t.weight_decay))
+        return fail(MOE_ERR_INVALID, "tensors[%d].weight_decay must be finite and >= 0", i);
+    }
+    if (t.n == 0) continue;
+    Buffer b[7];
+    const int c = adamw_buffers(t, b);
+    for (int j = 0; j < c; ++j) {
+      if (state_only && !b[j].state) continue;
+      if (!b[j].p) return fail(MOE_ERR_INVALID, "tensors[%d].%s is NULL", i, b[j].name);
+      if (!aligned16(b[j].p)) return fail(MOE_ERR_INVALID, "tensors[%d].%s is not 16-byte aligned", i, b[j].name);
+    }
+  }
+  return MOE_OK;
+}
+
+std::vector<moe::AdamTensor> adam_tensors(const moe_adamw_tensor *tensors, int32_t num) {
+  std::vector<moe::AdamTensor> t(num);
+  for (int32_t i = 0; i < num; ++i) {
+    const moe_adamw_tensor &s = tensors[i];
+    t[i] = {s.param, s.grad, s.master, s.m, s.v, s.m_scale, s.v_scale, s.n, s.weight_decay,
+            s.param_dtype == MOE_DTYPE_F32, s.grad_dtype == MOE_DTYPE_F32, s.state_bits == 8, 0};
+  }
+  return t;
+}
+
+// Whether two of the ranges overlap of which one at least is written.
+moe_status check_disjoint(std::vector<std::pair<Buffer, int32_t>> &all) {
+  std::sort(all.begin(), all.end(), [](const auto &a, const auto &b) { return a.first.p < b.first.p; });
+  const uint8_t *end_any = nullptr, *end_written = nullptr;  // ends of the ranges so far
+  for (const auto &x : all) {
+    const uint8_t *p = static_cast<const uint8_t *>(x.first.p);
+    if (p < (x.first.written ? end_any : end_written))
+      return fail(MOE_ERR_INVALID, "tensors[%d].%s overlaps another buffer of the list", x.second, x.first.name);
+    end_any = std::max(end_any, p + x.first.bytes);
+    if (x.first.written) end_written = std::max(end_written, p + x.first.bytes);
+  }
+  return MOE_OK;
+}
+
+moe_status check_adamw_disjoint(const moe_adamw_tensor *tensors, int32_t num, bool params_only) {
+  std::vector<std::pair<Buffer, int32_t>> all;
+  all.reserve(params_only ? num : 7 * (size_t)num);
+  for (int32_t i = 0; i < num; ++i) {
+    if (tensors[i].n == 0) continue;
+    Buffer b[7];
+    const int c = adamw_buffers(tensors[i], b);
+    for (int j = 0; j < (params_only ? 1 : c); ++j) all.push_back({b[j], i});
+  }
+  return check_disjoint(all);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_balance_workspace_size(const moe_desc *desc, int32_t num_seqs) {
+  if (check_desc(desc) != MOE_OK || num_seqs < 1 || num_seqs > MOE_MAX_SEQS) return 0;
+  return std::max<size_t>(moe::balance_workspace_bytes(desc->num_tokens, desc->num_experts, num_seqs), kAlign);
+}
+
+moe_status moe_balance_loss(const moe_desc *desc, const float *logits, const int32_t *topk_ids,
+                            const uint8_t *token_mask, const int32_t *seq_offsets, int32_t num_seqs, float alpha,
+                            float z_coeff, int32_t *counts, int32_t *seq_tokens, float *mean_probs, float *losses,
+                            float *dlogits, void *ws, size_t ws_bytes, hipStream_t stream) {
+  MOE_TRY(check_desc(desc));
+  const moe_desc &D = *desc;
+  MOE_TRY(check_num_seqs(num_seqs, seq_offsets));
+  MOE_TRY(check_coeff(alpha, "alpha"));
+  MOE_TRY(check_coeff(z_coeff, "z_coeff"));
+  if (D.num_tokens == 0) return ok();
+  MOE_TRY(check_ptr(logits, "logits"));
+  MOE_TRY(check_ptr(topk_ids, "topk_ids"));
+  MOE_TRY(check_opt_ptr(token_mask, "token_mask"));
+  MOE_TRY(check_ptr(counts, "counts"));
+  MOE_TRY(check_ptr(seq_tokens, "seq_tokens"));
+  MOE_TRY(check_ptr(mean_probs, "mean_probs"));
+  MOE_TRY(check_ptr(losses, "losses"));
+  MOE_TRY(check_opt_ptr(dlogits, "dlogits"));
+  const size_t need = moe_balance_workspace_size(desc, num_seqs);
+  if (!ws || ws_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "moe_balance_loss needs %zu workspace bytes, got %zu", need,
+                ws ? ws_bytes : (size_t)0);
+  MOE_TRY(check_ptr(ws, "ws"));
+  const moe::BalanceCall c{logits,       topk_ids,      token_mask, seq_offsets, nullptr, dlogits,
+                           D.num_tokens, D.num_experts, D.top_k,    num_seqs,    alpha,   z_coeff};
+  MOE_TRY_HIP(moe::launch_balance_loss(c, counts, seq_tokens, mean_probs, losses, ws, stream), "balance loss");
+  return ok();
+}
+
+moe_status moe_balance_loss_backward(const moe_desc *desc, const float *logits, const uint8_t *token_mask,
+                                     const int32_t *seq_offsets, int32_t num_seqs, const int32_t *counts,
+                                     const int32_t *seq_tokens, float alpha, float z_coeff, const float *dloss,
+                                     float *dlogits, hipStream_t stream) {
+  MOE_TRY(check_desc(desc));
+  const moe_desc &D = *desc;
+  MOE_TRY(check_num_seqs(num_seqs, seq_offsets));
+  MOE_TRY(check_coeff(alpha, "alpha"));
+  MOE_TRY(check_coeff(z_coeff, "z_coeff"));
+  if (D.num_tokens == 0) return ok();
+  MOE_TRY(check_ptr(logits, "logits"));
+  MOE_TRY(check_opt_ptr(token_mask, "token_mask"));
+  MOE_TRY(check_ptr(counts, "counts"));
+  MOE_TRY(check_ptr(seq_tokens, "seq_tokens"));
+  MOE_TRY(check_opt_ptr(dloss, "dloss"));
+  MOE_TRY(check_ptr(dlogits, "dlogits"));
+  const moe::BalanceCall c{logits,       nullptr,       token_mask, seq_offsets, dloss, dlogits,
+                           D.num_tokens, D.num_experts, D.top_k,    num_seqs,    alpha, z_coeff};
+  MOE_TRY_HIP(moe::launch_balance_backward(c, counts, seq_tokens, stream), "balance loss backward");
+  return ok();
+}
+
+size_t moe_grad_norm_workspace_size(const moe_grad_view *grads, int32_t num_tensors) try {
+  if (check_grads(grads, num_tensors) != MOE_OK) return 0;
+  const auto t = norm_tensors(grads, num_tensors);
+  return align_up(moe::grad_norm_workspace_bytes(t.data(), num_tensors));
+} catch (const std::exception &) {
+  return 0;
+}
+
+moe_status moe_grad_norm(const moe_grad_view *grads, int32_t num_tensors, float max_norm, float *out, void *ws,
+                         size_t ws_bytes, hipStream_t stream) try {
+  MOE_TRY(check_grads(grads, num_tensors));
+  if (!(max_norm > 0.f)) return fail(MOE_ERR_INVALID, "max_norm must be above 0 (infinity: no clipping)");
+  MOE_TRY(check_ptr(out, "out"));
+  const auto t = norm_tensors(grads, num_tensors);
+  const size_t need = align_up(moe::grad_norm_workspace_bytes(t.data(), num_tensors));
+  if (!ws || ws_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "moe_grad_norm needs %zu workspace bytes, got %zu", need, ws ? ws_bytes : (size_t)0);
+  MOE_TRY(check_ptr(ws, "ws"));
+  MOE_TRY_HIP(moe::launch_grad_norm(t.data(), num_tensors, max_norm, out, ws, stream), "gradient norm");
+  return ok();
+} catch (const std::exception &e) {
+  return fail(MOE_ERR_INVALID, "moe_grad_norm: %s", e.what());
+}
+
+moe_status moe_adamw_check_tensors(const moe_adamw_tensor *tensors, int32_t num_tensors) try {
+  MOE_TRY(check_adamw(tensors, num_tensors, false));
+  MOE_TRY(check_adamw_disjoint(tensors, num_tensors, false));
+  return ok();
+} catch (const std::exception &e) {
+  return fail(MOE_ERR_INVALID, "moe_adamw_check_tensors: %s", e.what());
+}
+
+moe_status moe_adamw_step(const moe_adamw_tensor *tensors, int32_t num_tensors, const moe_adamw_hparams *hparams,
+                          hipStream_t stream) try {
+  if (!hparams) return fail(MOE_ERR_INVALID, "hparams is NULL");
+  const moe_adamw_hparams &H = *hparams;
+  if (!H.lr_dev && !(H.lr >= 0.0 && std::isfinite(H.lr))) return fail(MOE_ERR_INVALID, "lr must be finite and >= 0");
+  if (!(H.beta1 >= 0.0 && H.beta1 < 1.0) || !(H.beta2 >= 0.0 && H.beta2 < 1.0))
+    return fail(MOE_ERR_INVALID, "beta1 and beta2 must lie in [0, 1)");
+  if (!(H.eps > 0.0) || !std::isfinite(H.eps)) return fail(MOE_ERR_INVALID, "eps must be finite and above 0");
+  if (!H.step_dev && H.step < 1) return fail(MOE_ERR_INVALID, "step %lld < 1", (long long)H.step);
+  MOE_TRY(check_opt_ptr(H.lr_dev, "lr_dev"));
+  MOE_TRY(check_opt_ptr(H.step_dev, "step_dev"));
+  MOE_TRY(check_opt_ptr(H.norm, "norm"));
+  MOE_TRY(check_adamw(tensors, num_tensors, false));
+#ifdef MOE_DEBUG_CHECKS
+  MOE_TRY(check_adamw_disjoint(tensors, num_tensors, false));
+#else
+  MOE_TRY(check_adamw_disjoint(tensors, num_tensors, true));  // the same tensor twice
+#endif
+  const auto t = adam_tensors(tensors, num_tensors);
+  const moe::AdamScalars h{H.lr, H.beta1, H.beta2, H.eps, H.step, H.lr_dev, H.step_dev, H.norm ? H.norm + 1 : nullptr};
+  MOE_TRY_HIP(moe::launch_adamw(t.data(), num_tensors, h, stream), "AdamW step");
+  return ok();
+} catch (const std::exception &e) {
+  return fail(MOE_ERR_INVALID, "moe_adamw_step: %s", e.what());
+}
+
+moe_status moe_adamw_read_states(const moe_adamw_tensor *tensors, int32_t num_tensors, float *const *m_out,
+                                 float *const *v_out, hipStream_t stream) try {
+  MOE_TRY(check_adamw(tensors, num_tensors, true));
+  for (int32_t i = 0; i < num_tensors; ++i) {
+    if (tensors[i].state_bits != 8)
+      return fail(MOE_ERR_INVALID, "tensors[%d]: states in 32 bits need no reading", i);
+    if (m_out && m_out[i]) MOE_TRY(check_ptr(m_out[i], "m_out"));
+    if (v_out && v_out[i]) MOE_TRY(check_ptr(v_out[i], "v_out"));
+  }
+  const auto t = adam_tensors(tensors, num_tensors);
+  MOE_TRY_HIP(moe::launch_adamw_read(t.data(), num_tensors, m_out, v_out, stream), "AdamW states");
+  return ok();
+} catch (const std::exception &e) {
+  return fail(MOE_ERR_INVALID, "moe_adamw_read_states: %s", e.what());
 }
 
 }  // extern "C"

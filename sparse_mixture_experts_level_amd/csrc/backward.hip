@@ -125,15 +125,18 @@ __global__ __launch_bounds__(256) void fill_u32_kernel(uint32_t *__restrict__ p,
 // dl[t][ids_j] = g_j (dg_j - sum_j' g_j' dg_j'), zero elsewhere; written as float [T, E]
 // and as bf16 [T, Epad] (zero padded).  dg_j = dL/dg_j is the sum of the nb block dot
 // products dH' . H of the assignment's row in dpart (0 when dropped), added lane-strided
-// and then in a fixed butterfly: the same value in every lane.
+// and then in a fixed butterfly: the same value in every lane.  extra [T, E], when given, is
+// the gradient of other losses on the logits (the balance loss), added before the rounding
+// to bf16: a term far below a selected expert's gate gradient is rounded with it, to
+// nearest, while the experts a token did not select carry it with full relative precision.
 __global__ __launch_bounds__(256) void gates_bwd_kernel(const int32_t *__restrict__ ids,
                                                         const float *__restrict__ gates,
                                                         const float *__restrict__ dpart, int nb,
                                                         const int32_t *__restrict__ serving,
                                                         const int32_t *__restrict__ slot,
                                                         const int32_t *__restrict__ offsets, int T, int E, int k,
-                                                        int Epad, float *__restrict__ dl,
-                                                        bf16_t *__restrict__ dl16) {
+                                                        int Epad, const float *__restrict__ extra,
+                                                        float *__restrict__ dl, bf16_t *__restrict__ dl16) {
   constexpr int QMAX = (MOE_MAX_EXPERTS_DEV + 63) / 64;  // experts per lane
   const int lane = threadIdx.x & 63;
   const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -175,7 +178,8 @@ __global__ __launch_bounds__(256) void gates_bwd_kernel(const int32_t *__restric
   for (int q = 0; q < QMAX; ++q) {
     const int e = lane + 64 * q;
     if (e >= Epad) break;
-    const float v = my_sel[q] ? my_g[q] * (my_dg[q] - s) : 0.0f;
+    float v = my_sel[q] ? my_g[q] * (my_dg[q] - s) : 0.0f;
+    if (extra && e < E) v += extra[(size_t)t * E + e];
     if (e < E) dl[(size_t)t * E + e] = v;
     dl16[(size_t)t * Epad + e] = f32_to_bf16(v);
   }
@@ -469,11 +473,11 @@ hipError_t launch_fill_u32(void *p, int64_t n_words, uint32_t v, hipStream_t s) 
 }
 
 hipError_t launch_gates_bwd(const int32_t *ids, const float *gates, const float *dpart, int nb, const int32_t *serving,
-                            const int32_t *slot, const int32_t *offsets, int T, int E, int k, int Epad, float *dl,
-                            void *dl16, hipStream_t s) {
+                            const int32_t *slot, const int32_t *offsets, int T, int E, int k, int Epad,
+                            const float *extra, float *dl, void *dl16, hipStream_t s) {
   if (Epad > MOE_MAX_EXPERTS_DEV + 63) return hipErrorInvalidValue;
   hipLaunchKernelGGL(gates_bwd_kernel, dim3((unsigned)((T + 3) / 4)), dim3(256), 0, s, ids, gates, dpart, nb, serving,
-                     slot, offsets, T, E, k, Epad, dl, static_cast<bf16_t *>(dl16));
+                     slot, offsets, T, E, k, Epad, extra, dl, static_cast<bf16_t *>(dl16));
   return hipGetLastError();
 }
 

@@ -165,6 +165,54 @@ size_t aux_loss_workspace_bytes(int T, int E);
 hipError_t launch_aux_loss(const float *logits, const int32_t *counts, int T, int E, int k, float alpha, float *loss,
                            float *partial_ws, hipStream_t s);
 
+// ---- balance and z losses with their gradient (balance_loss.hip)
+struct BalanceCall {
+  const float *logits;
+  const int32_t *ids;   // unused by the backward launch
+  const uint8_t *mask;  // or NULL
+  const int32_t *off;   // [S + 1] or NULL: one sequence of all T tokens (S == 1)
+  const float *dloss;   // [2] or NULL
+  float *dlogits;       // or NULL
+  int T, E, k, S;
+  float alpha, beta;
+};
+size_t balance_workspace_bytes(int T, int E, int S);
+hipError_t launch_balance_loss(const BalanceCall &c, int32_t *counts, int32_t *seq_tokens, float *mean_probs,
+                               float *losses, void *ws, hipStream_t s);
+hipError_t launch_balance_backward(const BalanceCall &c, const int32_t *counts, const int32_t *seq_tokens,
+                                   hipStream_t s);
+
+// ---- gradient norm and AdamW over many tensors (optimizer.hip)
+constexpr int kAdamBlock = 256;  // values that share a scale in 8-bit states
+struct NormTensor {
+  const void *grad;
+  int64_t n;
+  int32_t f32;  // 1: float, 0: bf16
+  int32_t pad;
+};
+size_t grad_norm_workspace_bytes(const NormTensor *t, int count);
+// out[0] = the norm, out[1] = min(1, max_norm / (norm + 1e-6)), NaN when the norm is not finite.
+hipError_t launch_grad_norm(const NormTensor *t, int count, float max_norm, float *out, void *ws, hipStream_t s);
+struct AdamTensor {
+  void *param;
+  const void *grad;
+  float *master;
+  void *m, *v;
+  float *m_scale, *v_scale;  // 8-bit states
+  int64_t n;
+  float decay;       // weight decay
+  uint8_t param_f32, grad_f32, eight, pad;
+};
+struct AdamScalars {
+  double lr, beta1, beta2, eps;
+  int64_t step;
+  const float *lr_dev;
+  const int64_t *step_dev;
+  const float *grad_scale;
+};
+hipError_t launch_adamw(const AdamTensor *t, int count, const AdamScalars &h, hipStream_t s);
+hipError_t launch_adamw_read(const AdamTensor *t, int count, float *const *m_out, float *const *v_out, hipStream_t s);
+
 // ---- small utilities (combine.hip)
 hipError_t launch_fill_i32(int32_t *p, int n, int32_t v0, int32_t step, hipStream_t s);
 
@@ -180,11 +228,12 @@ hipError_t launch_transpose_bf16(const void *in, int64_t in_stride_b, int64_t ro
 // poff[g] = sum over g' < g of ceil32(off[g'+1] - off[g']), poff[G] = total
 hipError_t launch_pad_offsets(const int32_t *off, int G, int32_t *poff, hipStream_t s);
 hipError_t launch_fill_u32(void *p, int64_t n_words, uint32_t v, hipStream_t s);
-// dl (float [T, E]) and dl16 (bf16 [T, Epad]) from the gate gradients: dg of each kept
+// dl (float [T, E]) and dl16 (bf16 [T, Epad]) from the gate gradients, plus extra [T, E] (a
+// gradient of other losses on the logits) unless NULL: dg of each kept
 // assignment is the sum of the nb block partials [rows, nb] of its row in dpart.
 hipError_t launch_gates_bwd(const int32_t *ids, const float *gates, const float *dpart, int nb, const int32_t *serving,
-                            const int32_t *slot, const int32_t *offsets, int T, int E, int k, int Epad, float *dl,
-                            void *dl16, hipStream_t s);
+                            const int32_t *slot, const int32_t *offsets, int T, int E, int k, int Epad,
+                            const float *extra, float *dl, void *dl16, hipStream_t s);
 // row_gate[offsets[serving[i]] + slot[i]] = gates[i] for every kept assignment i < n.
 hipError_t launch_row_gate(const int32_t *serving, const int32_t *slot, const int32_t *offsets, const float *gates,
                            int64_t n, float *row_gate, hipStream_t s);

@@ -33,7 +33,12 @@ SYMBOLS = [
     "moe_combine_unpermute", "moe_router_aux_loss", "moe_forward", "moe_forward_expert_shard",
     "moe_backward_workspace_size", "moe_backward", "moe_tiled_weights_bytes", "moe_tile_expert_weights",
     "moe_check_topk_ids", "moe_debug_checks", "moe_forward_staged", "moe_forward_noalloc",
+    "moe_backward_with_dlogits", "moe_balance_workspace_size", "moe_balance_loss", "moe_balance_loss_backward",
+    "moe_grad_norm_workspace_size", "moe_grad_norm", "moe_adamw_check_tensors", "moe_adamw_step",
+    "moe_adamw_read_states",
 ]
+MOE_MAX_SEQS = 65536
+MOE_ADAMW_BLOCK = 256
 MOE_NOALLOC_WORKSPACE_BYTES = 128 << 20
 
 # moe_stage: the stages moe_forward_staged marks, in launch order
@@ -70,6 +75,24 @@ class MoeRouting(ctypes.Structure):
     _fields_ = [("logits", ctypes.c_void_p), ("topk_ids", ctypes.c_void_p), ("topk_gates", ctypes.c_void_p),
                 ("expert_counts", ctypes.c_void_p), ("expert_offsets", ctypes.c_void_p), ("slot", ctypes.c_void_p),
                 ("row_token", ctypes.c_void_p), ("assigned_ids", ctypes.c_void_p)]
+
+
+class MoeGradView(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class MoeAdamwTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n", ctypes.c_int64), ("param_dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("state_bits", ctypes.c_int32), ("weight_decay", ctypes.c_float)]
+
+
+class MoeAdamwHparams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int64), ("lr_dev", ctypes.c_void_p),
+                ("step_dev", ctypes.c_void_p), ("norm", ctypes.c_void_p)]
 
 
 _lib = None
@@ -140,6 +163,21 @@ def _load(path: str) -> ctypes.CDLL:
     L.moe_tile_expert_weights.restype = st
     L.moe_check_topk_ids.argtypes, L.moe_check_topk_ids.restype = [dp, vp], st
     L.moe_debug_checks.argtypes, L.moe_debug_checks.restype = [], i32
+    f32, gp, tp = ctypes.c_float, ctypes.POINTER(MoeGradView), ctypes.POINTER(MoeAdamwTensor)
+    L.moe_backward_with_dlogits.argtypes = [dp, ctypes.POINTER(MoeWeights), vp, ctypes.POINTER(MoeRouting), vp, vp, vp,
+                                            ctypes.POINTER(MoeGrads), vp, sz, vp]
+    L.moe_backward_with_dlogits.restype = st
+    L.moe_balance_workspace_size.argtypes, L.moe_balance_workspace_size.restype = [dp, i32], sz
+    L.moe_balance_loss.argtypes = [dp, vp, vp, vp, vp, i32, f32, f32, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.moe_balance_loss.restype = st
+    L.moe_balance_loss_backward.argtypes = [dp, vp, vp, vp, i32, vp, vp, f32, f32, vp, vp, vp]
+    L.moe_balance_loss_backward.restype = st
+    L.moe_grad_norm_workspace_size.argtypes, L.moe_grad_norm_workspace_size.restype = [gp, i32], sz
+    L.moe_grad_norm.argtypes, L.moe_grad_norm.restype = [gp, i32, f32, vp, vp, sz, vp], st
+    L.moe_adamw_check_tensors.argtypes, L.moe_adamw_check_tensors.restype = [tp, i32], st
+    L.moe_adamw_step.argtypes, L.moe_adamw_step.restype = [tp, i32, ctypes.POINTER(MoeAdamwHparams), vp], st
+    L.moe_adamw_read_states.argtypes = [tp, i32, ctypes.POINTER(vp), ctypes.POINTER(vp), vp]
+    L.moe_adamw_read_states.restype = st
     return L
 
 
@@ -317,12 +355,23 @@ def tiled_weights(desc, w_gate_up, w_down, stream=None):
     return gu, dn
 
 
+def _shared_desc(desc) -> MoeDesc:
+    """The shared expert as a layer of one expert of width d_ff_shared."""
+    one = MoeDesc(**{n: getattr(desc, n) for n, _ in MoeDesc._fields_})
+    one.num_experts, one.top_k, one.d_ff, one.d_ff_shared, one.capacity = 1, 1, desc.d_ff_shared, 0, MOE_NO_CAPACITY
+    return one
+
+
 def tiled_shared_weights(desc, w_shared_gate_up, w_shared_down, stream=None):
     """The tile-major copies of the shared expert's [2 f_s, d] and [d, f_s] weights: one expert
     of width d_ff_shared."""
-    one = MoeDesc(**{n: getattr(desc, n) for n, _ in MoeDesc._fields_})
-    one.num_experts, one.top_k, one.d_ff, one.d_ff_shared, one.capacity = 1, 1, desc.d_ff_shared, 0, MOE_NO_CAPACITY
-    return tiled_weights(one, w_shared_gate_up.unsqueeze(0), w_shared_down.unsqueeze(0), stream=stream)
+    return tiled_weights(_shared_desc(desc), w_shared_gate_up.unsqueeze(0), w_shared_down.unsqueeze(0), stream=stream)
+
+
+def tile_shared_weights(desc, w_shared_gate_up, w_shared_down, w_gate_up_tiled, w_down_tiled, stream=None) -> None:
+    """Rewrites the copies that tiled_shared_weights() returned."""
+    moe_tile_expert_weights(_shared_desc(desc), 1, w_shared_gate_up.unsqueeze(0), w_shared_down.unsqueeze(0),
+                            w_gate_up_tiled, w_down_tiled, stream=stream)
 
 
 def _weights(w_router, w_gate_up, w_down, w_shared_gate_up, w_shared_down, tiled, shared_tiled=None):
@@ -402,14 +451,231 @@ def moe_backward_workspace_size(desc: MoeDesc) -> int:
 
 
 def moe_backward(desc, w_router, w_gate_up, w_down, x, routing: dict, dy, dx, grads: dict, ws,
-                 w_shared_gate_up=None, w_shared_down=None, stream=None, tiled=None, shared_tiled=None) -> None:
+                 w_shared_gate_up=None, w_shared_down=None, stream=None, tiled=None, shared_tiled=None,
+                 dlogits=None) -> None:
+    """dlogits: a gradient [T, E] float on the router's logits (moe_balance_loss) to add to the
+    gates' (moe_backward_with_dlogits)."""
     W = _weights(w_router, w_gate_up, w_down, w_shared_gate_up, w_shared_down, tiled, shared_tiled)
     R = MoeRouting(*(_ptr(routing.get(n)) for n, _ in MoeRouting._fields_))
     G = MoeGrads(*(_ptr(grads.get(n)) for n, _ in MoeGrads._fields_))
+    if dlogits is not None:
+        _tensor(dlogits, "dlogits", torch.float32, (desc.num_tokens, desc.num_experts))
+        _check(lib().moe_backward_with_dlogits(ctypes.byref(desc), ctypes.byref(W), _ptr(x), ctypes.byref(R), _ptr(dy),
+                                               _ptr(dlogits), _ptr(dx), ctypes.byref(G), _ptr(ws),
+                                               0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)),
+               "moe_backward_with_dlogits")
+        return
     _check(lib().moe_backward(ctypes.byref(desc), ctypes.byref(W), _ptr(x), ctypes.byref(R), _ptr(dy), _ptr(dx),
                               ctypes.byref(G), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
                               _stream(stream)),
            "moe_backward")
+
+
+# ------------------------------------------------------------------- balance loss with gradient
+
+def _tensor(t, name: str, dtypes, shape=None):
+    """Data pointer of a contiguous tensor of one of `dtypes` (and of `shape`) on the current
+    device; None stays None."""
+    if t is None:
+        return None
+    if t.dtype not in (dtypes if isinstance(dtypes, tuple) else (dtypes,)):
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtypes}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}; the library runs on the current GPU")
+    return t.data_ptr()
+
+
+def _num_seqs(seq_offsets) -> int:
+    return 1 if seq_offsets is None else seq_offsets.numel() - 1
+
+
+def moe_balance_workspace_size(desc: MoeDesc, num_seqs: int = 1) -> int:
+    return int(lib().moe_balance_workspace_size(ctypes.byref(desc), int(num_seqs)))
+
+
+def moe_balance_loss(desc, logits, topk_ids, alpha, z_coeff, counts, seq_tokens, mean_probs, losses, ws,
+                     token_mask=None, seq_offsets=None, dlogits=None, stream=None) -> None:
+    """counts [S, E] int32, seq_tokens [S] int32, mean_probs [S, E], losses [2] (balance, z) and, if
+    given, dlogits [T, E] are written; S = 1, or seq_offsets.numel() - 1."""
+    T, E, k, S = desc.num_tokens, desc.num_experts, desc.top_k, _num_seqs(seq_offsets)
+    _check(lib().moe_balance_loss(
+        ctypes.byref(desc), _tensor(logits, "logits", torch.float32, (T, E)),
+        _tensor(topk_ids, "topk_ids", torch.int32, (T, k)),
+        _tensor(token_mask, "token_mask", (torch.uint8, torch.bool), (T,)),
+        _tensor(seq_offsets, "seq_offsets", torch.int32, (S + 1,)), S, float(alpha), float(z_coeff),
+        _tensor(counts, "counts", torch.int32, (S, E)), _tensor(seq_tokens, "seq_tokens", torch.int32, (S,)),
+        _tensor(mean_probs, "mean_probs", torch.float32, (S, E)), _tensor(losses, "losses", torch.float32, (2,)),
+        _tensor(dlogits, "dlogits", torch.float32, (T, E)), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+        _stream(stream)), "moe_balance_loss")
+
+
+def moe_balance_loss_backward(desc, logits, counts, seq_tokens, alpha, z_coeff, dlogits, token_mask=None,
+                              seq_offsets=None, dloss=None, stream=None) -> None:
+    """dlogits from the forward's counts and seq_tokens; dloss [2]: upstream gradients (None: ones)."""
+    T, E, S = desc.num_tokens, desc.num_experts, _num_seqs(seq_offsets)
+    _check(lib().moe_balance_loss_backward(
+        ctypes.byref(desc), _tensor(logits, "logits", torch.float32, (T, E)),
+        _tensor(token_mask, "token_mask", (torch.uint8, torch.bool), (T,)),
+        _tensor(seq_offsets, "seq_offsets", torch.int32, (S + 1,)), S, _tensor(counts, "counts", torch.int32, (S, E)),
+        _tensor(seq_tokens, "seq_tokens", torch.int32, (S,)), float(alpha), float(z_coeff),
+        _tensor(dloss, "dloss", torch.float32, (2,)), _tensor(dlogits, "dlogits", torch.float32, (T, E)),
+        _stream(stream)), "moe_balance_loss_backward")
+
+
+# --------------------------------------------------------------- gradient norm and AdamW step
+
+class GradList:
+    """Gradient tensors with the host array of views that moe_grad_norm takes (grad_list())."""
+
+    def __init__(self, grads):
+        self.grads = list(grads)
+        self.views = (MoeGradView * max(len(self.grads), 1))()
+        for i, g in enumerate(self.grads):
+            self.views[i] = MoeGradView(_tensor(g, f"grads[{i}]", (torch.float32, torch.bfloat16)), g.numel(),
+                                        dtype_code(g.dtype), 0)
+
+    def __len__(self):
+        return len(self.grads)
+
+
+def grad_list(grads) -> GradList:
+    return GradList(grads)
+
+
+def moe_grad_norm_workspace_size(grads: GradList) -> int:
+    return int(lib().moe_grad_norm_workspace_size(grads.views, len(grads)))
+
+
+def moe_grad_norm(grads: GradList, max_norm: float, out, ws, stream=None) -> None:
+    """out [2] float: the norm over every gradient, and min(1, max_norm / (norm + 1e-6))."""
+    _check(lib().moe_grad_norm(grads.views, len(grads), float(max_norm), _tensor(out, "out", torch.float32, (2,)),
+                               _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)),
+           "moe_grad_norm")
+
+
+def moe_adamw_check_tensors(tensors, num_tensors: int) -> None:
+    _check(lib().moe_adamw_check_tensors(tensors, int(num_tensors)), "moe_adamw_check_tensors")
+
+
+def moe_adamw_step(tensors, num_tensors: int, hparams: MoeAdamwHparams, stream=None) -> None:
+    _check(lib().moe_adamw_step(tensors, num_tensors, ctypes.byref(hparams), _stream(stream)), "moe_adamw_step")
+
+
+def moe_adamw_read_states(tensors, num_tensors: int, m_out=None, v_out=None, stream=None) -> None:
+    """m_out, v_out: per tensor a float tensor or None; None: not wanted."""
+    def pointers(outs, name):
+        if outs is None:
+            return None
+        if len(outs) != num_tensors:
+            raise ValueError(f"{name} holds {len(outs)} tensors, expected {num_tensors}")
+        return (ctypes.c_void_p * max(num_tensors, 1))(*[
+            None if o is None else _tensor(o.view(-1), f"{name}[{i}]", torch.float32, (tensors[i].n,))
+            for i, o in enumerate(outs)])
+    _check(lib().moe_adamw_read_states(tensors, num_tensors, pointers(m_out, "m_out"), pointers(v_out, "v_out"),
+                                       _stream(stream)), "moe_adamw_read_states")
+
+
+class MoEAdamW:
+    """AdamW over a list of parameter tensors with fixed gradient tensors (moe_adamw_step), after
+    clipping by the gradients' norm when max_grad_norm is given (moe_grad_norm).
+
+    Parameters and gradients are float or bf16; weight_decay is one value or one per tensor.
+    state_bits 32 or 8; master_weights keeps a float copy of each bf16 parameter.  `states`
+    (one dict of m, v, m_scale, v_scale, master per tensor) takes existing state tensors
+    instead of new zeros; `step` is the number of steps already done.  With capturable=True
+    the step number and lr live on the device, so that a step captured into a HIP graph
+    counts on at every replay; set the rate with set_lr() then.
+
+    Tensors are used on the stream of the call; allocation happens here, never in step()."""
+
+    def __init__(self, params, grads, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, max_grad_norm=None,
+                 state_bits=32, master_weights=False, states=None, step=0, capturable=False):
+        self.params, self.grads = list(params), list(grads)
+        n = len(self.params)
+        if len(self.grads) != n or (states is not None and len(states) != n):
+            raise ValueError("params, grads and states must have one entry per tensor")
+        if state_bits not in (32, 8):
+            raise ValueError(f"state_bits {state_bits}: 32 or 8")
+        decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n
+        if len(decay) != n:
+            raise ValueError("weight_decay must be one value or one per tensor")
+        self.state_bits, self.max_grad_norm, self.step_count = state_bits, max_grad_norm, int(step)
+        self.states = states if states is not None else [self._new_state(p, master_weights) for p in self.params]
+        self.tensors = (MoeAdamwTensor * max(n, 1))()
+        fp = (torch.float32, torch.bfloat16)
+        kinds = (torch.float32, torch.float32) if state_bits == 32 else (torch.int8, torch.uint8)
+        for i, (p, g, s) in enumerate(zip(self.params, self.grads, self.states)):
+            if p.numel() != g.numel():
+                raise ValueError(f"params[{i}] holds {p.numel()} values, grads[{i}] {g.numel()}")
+            size, blocks = (p.numel(),), (-(-p.numel() // MOE_ADAMW_BLOCK),)
+
+            def ptr(name, kind, shape):
+                t = s.get(name)
+                return None if t is None else _tensor(t.view(-1), f"states[{i}].{name}", kind, shape)
+            self.tensors[i] = MoeAdamwTensor(
+                _tensor(p, f"params[{i}]", fp), _tensor(g, f"grads[{i}]", fp), ptr("master", torch.float32, size),
+                ptr("m", kinds[0], size), ptr("v", kinds[1], size),
+                ptr("m_scale", torch.float32, blocks) if state_bits == 8 else None,
+                ptr("v_scale", torch.float32, blocks) if state_bits == 8 else None,
+                p.numel(), dtype_code(p.dtype), dtype_code(g.dtype), state_bits, float(decay[i]))
+        moe_adamw_check_tensors(self.tensors, n)
+        self.hparams = MoeAdamwHparams(float(lr), float(betas[0]), float(betas[1]), float(eps), self.step_count, None,
+                                       None, None)
+        device = self.params[0].device if n else "cuda"
+        self.capturable = capturable
+        if capturable:
+            self.lr_dev = torch.full((1,), float(lr), dtype=torch.float32, device=device)
+            self.step_dev = torch.full((1,), self.step_count, dtype=torch.int64, device=device)
+            self.hparams.lr_dev, self.hparams.step_dev = self.lr_dev.data_ptr(), self.step_dev.data_ptr()
+        self.grad_norm = None  # [2]: the norm before clipping, the factor applied
+        if max_grad_norm is not None:
+            self._grad_list = grad_list(self.grads)
+            self._ws = workspace(moe_grad_norm_workspace_size(self._grad_list), device)
+            self.grad_norm = torch.zeros(2, dtype=torch.float32, device=device)
+            self.hparams.norm = self.grad_norm.data_ptr()
+
+    def _new_state(self, p, master_weights):
+        z = lambda shape, dt: torch.zeros(shape, dtype=dt, device=p.device)  # noqa: E731
+        if self.state_bits == 32:
+            s = {"m": z(p.shape, torch.float32), "v": z(p.shape, torch.float32)}
+        else:
+            blocks = -(-p.numel() // MOE_ADAMW_BLOCK)
+            s = {"m": z(p.shape, torch.int8), "v": z(p.shape, torch.uint8), "m_scale": z((blocks,), torch.float32),
+                 "v_scale": z((blocks,), torch.float32)}
+        if master_weights and p.dtype != torch.float32:
+            s["master"] = p.detach().float()
+        return s
+
+    def set_lr(self, lr: float) -> None:
+        self.hparams.lr = float(lr)
+        if self.capturable:
+            self.lr_dev.fill_(float(lr))
+
+    def step(self, stream=None) -> None:
+        n = len(self.params)
+        if self.capturable:
+            if stream is not None:
+                raise ValueError("a capturable step runs on the current stream")
+            self.step_dev.add_(1)
+        elif torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("a captured step would repeat its step number: construct MoEAdamW with capturable=True")
+        if self.max_grad_norm is not None:
+            moe_grad_norm(self._grad_list, self.max_grad_norm, self.grad_norm, self._ws, stream=stream)
+        self.hparams.step = self.step_count + 1
+        moe_adamw_step(self.tensors, n, self.hparams, stream=stream)
+        self.step_count += 1
+
+    def read_states(self, m_out=None, v_out=None, stream=None):
+        """8-bit states as the floats they stand for, into the given tensors or new ones."""
+        if m_out is None and v_out is None:
+            m_out, v_out = ([torch.empty(p.shape, dtype=torch.float32, device=p.device) for p in self.params]
+                            for _ in range(2))
+        moe_adamw_read_states(self.tensors, len(self.params), m_out, v_out, stream=stream)
+        return m_out, v_out
 
 
 class MoELayer:
@@ -457,3 +723,68 @@ class MoELayer:
                     routing=self.routing if with_routing else None, w_shared_gate_up=i.w_shared_gate_up,
                     w_shared_down=i.w_shared_down, stream=stream, tiled=self.tiled, shared_tiled=self.shared_tiled)
         return self.out
+
+
+class MoETrainer:
+    """One bf16 layer's training step: moe_forward, the balance and z losses with their gradient
+    (moe_balance_loss), moe_backward_with_dlogits, the clipped AdamW step, and the tile-major copies
+    rewritten from the new weights.
+
+    Buffers are allocated here, once; the optimizer's options (lr, weight_decay, max_grad_norm,
+    state_bits, master_weights, capturable, ...) are MoEAdamW's.  The router is not decayed unless
+    weight_decay is given per tensor (router, gate_up, down[, shared gate_up, shared down])."""
+
+    def __init__(self, inputs, capacity, device="cuda", fill_order="token", overflow="drop", tiled=False,
+                 shared_tiled=False, alpha=0.01, z_coeff=0.001, seq_offsets=None, token_mask=None, weight_decay=0.01,
+                 **adamw):
+        w = inputs.workload
+        self.layer = MoELayer(inputs, capacity, device, fill_order, overflow, tiled, shared_tiled)
+        desc = self.layer.desc
+        if desc.dtype != MOE_DTYPE_BF16:
+            raise ValueError("training is implemented for bf16 layers")
+        T, E, S = w.num_tokens, w.num_experts, _num_seqs(seq_offsets)
+        self.alpha, self.z_coeff, self.seq_offsets, self.token_mask = alpha, z_coeff, seq_offsets, token_mask
+        f32 = dict(dtype=torch.float32, device=device)
+        i32 = dict(dtype=torch.int32, device=device)
+        self.counts, self.seq_tokens = torch.zeros((S, E), **i32), torch.zeros((S,), **i32)
+        self.mean_probs, self.losses = torch.zeros((S, E), **f32), torch.zeros((2,), **f32)
+        self.dlogits = torch.zeros((T, E), **f32)
+        self.dx = torch.zeros_like(inputs.x)
+        names = ["router", "gate_up", "down"] + (["shared_gate_up", "shared_down"] if w.d_ff_shared else [])
+        weights = [getattr(inputs, "w_" + n) for n in names]
+        self.grads = {"dw_" + n: torch.zeros(p.shape, dtype=torch.float32 if n == "router" else p.dtype, device=device)
+                      for n, p in zip(names, weights)}
+        self.balance_ws = workspace(moe_balance_workspace_size(desc, S), device)
+        self.backward_ws = workspace(moe_backward_workspace_size(desc), device)
+        if not isinstance(weight_decay, (list, tuple)):
+            weight_decay = [0.0] + [weight_decay] * (len(names) - 1)
+        self.optimizer = MoEAdamW(weights, [self.grads["dw_" + n] for n in names], weight_decay=weight_decay, **adamw)
+
+    def forward(self):
+        return self.layer.forward(with_routing=True)
+
+    def backward(self, dy):
+        """Gradients of sum(dy * out) + losses[0] + losses[1] of the last forward; returns dx."""
+        i, r, desc = self.layer.inputs, self.layer.routing, self.layer.desc
+        moe_balance_loss(desc, r["logits"], r["topk_ids"], self.alpha, self.z_coeff, self.counts, self.seq_tokens,
+                         self.mean_probs, self.losses, self.balance_ws, token_mask=self.token_mask,
+                         seq_offsets=self.seq_offsets, dlogits=self.dlogits)
+        moe_backward(desc, i.w_router, i.w_gate_up, i.w_down, i.x, r, dy, self.dx, self.grads, self.backward_ws,
+                     w_shared_gate_up=i.w_shared_gate_up, w_shared_down=i.w_shared_down, tiled=self.layer.tiled,
+                     shared_tiled=self.layer.shared_tiled, dlogits=self.dlogits)
+        return self.dx
+
+    def step(self) -> None:
+        self.optimizer.step()
+        i, L = self.layer.inputs, self.layer
+        if L.tiled is not None:
+            moe_tile_expert_weights(L.desc, i.w_gate_up.shape[0], i.w_gate_up, i.w_down, *L.tiled)
+        if L.shared_tiled is not None:
+            tile_shared_weights(L.desc, i.w_shared_gate_up, i.w_shared_down, *L.shared_tiled)
+
+    def train_step(self, dy):
+        """forward, backward(dy), step; returns the forward's out."""
+        out = self.forward()
+        self.backward(dy)
+        self.step()
+        return out
