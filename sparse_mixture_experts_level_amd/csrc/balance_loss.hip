@@ -20,6 +20,8 @@ namespace moe {
 namespace {
 
 constexpr int BL_COUNT_THREADS = 1024;
+constexpr int BL_WAVES = 8, BL_THREADS = 64 * BL_WAVES;  // main pass
+constexpr int BL_BINS = 4096;                            // LDS bins of a block that counts
 
 struct Span {
   int seq;    // -1: none
@@ -79,41 +81,81 @@ __device__ __forceinline__ Span find_span(const int32_t *off, int S, int T, int 
   return r;
 }
 
-// Counts of one chunk: part[block][0..E-1] choices, part[block][E] counted tokens.  Each
-// expert has `copies` bins, taken by lane, so that a wavefront whose tokens all chose one
-// expert does not add 64 times to one address.
+// Sum of each value over the block's threads, returned to thread 0 (s_red: two doubles a wave).
+template <int WAVES>
+__device__ __forceinline__ void block_sum2(double &x, double &y, double (*s_red)[2]) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) {
+    x += __shfl_xor(x, o, 64);
+    y += __shfl_xor(y, o, 64);
+  }
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) {
+    s_red[threadIdx.x >> 6][0] = x;
+    s_red[threadIdx.x >> 6][1] = y;
+  }
+  __syncthreads();
+  x = y = 0;
+  if (threadIdx.x == 0)
+    for (int w = 0; w < WAVES; ++w) {
+      x += s_red[w][0];
+      y += s_red[w][1];
+    }
+}
+
+// ---------------------------------------------------------------------------------- counts
+
+// Choices and counted tokens of tokens [begin, end) into bins in LDS: bins[copies][E], then
+// one for the tokens.  Each expert has `copies` bins, taken by lane, so that a wavefront whose
+// tokens all chose one expert does not add 64 times to one address.  Ends synchronised, with
+// the experts' sums in bins[0 .. E - 1] and the tokens in bins[copies * E].
+template <int THREADS>
+__device__ __forceinline__ void count_chunk_lds(int32_t *bins, int copies, const int32_t *ids, const uint8_t *mask,
+                                                int begin, int end, int E, int k) {
+  for (int i = threadIdx.x; i < copies * E + 1; i += THREADS) bins[i] = 0;
+  __syncthreads();
+  int32_t *mine = bins + (threadIdx.x & (copies - 1)) * E;
+  const int32_t *src = ids + (size_t)begin * k;
+  const uint32_t n = (uint32_t)(end - begin) * (uint32_t)k;
+  int tokens = 0;
+  if (mask) {
+    for (uint32_t i = threadIdx.x; i < n; i += THREADS) {
+      const int e = src[i];
+      if (mask[begin + i / (uint32_t)k] != 0 && e >= 0 && e < E) atomicAdd(&mine[e], 1);
+    }
+    for (int t = begin + (int)threadIdx.x; t < end; t += THREADS) tokens += mask[t] != 0;
+  } else {
+    for (uint32_t i = threadIdx.x; i < n; i += THREADS) {
+      const int e = src[i];
+      if (e >= 0 && e < E) atomicAdd(&mine[e], 1);
+    }
+    if (threadIdx.x == 0) tokens = end - begin;
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) tokens += __shfl_xor(tokens, o, 64);
+  if ((threadIdx.x & 63) == 0 && tokens) atomicAdd(&bins[copies * E], tokens);
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += THREADS) {
+    int c = 0;
+    for (int q = 0; q < copies; ++q) c += bins[q * E + e];
+    bins[e] = c;  // column e belongs to this thread
+  }
+  __syncthreads();
+}
+
+// Counts of one chunk: part[block][0..E-1] choices, part[block][E] counted tokens.
 __global__ __launch_bounds__(BL_COUNT_THREADS) void balance_count_kernel(const int32_t *__restrict__ ids,
                                                                          const uint8_t *__restrict__ mask,
                                                                          const int32_t *__restrict__ off, int T, int E,
                                                                          int k, int S, int chunk, int copies,
                                                                          int32_t *__restrict__ part) {
-  extern __shared__ int32_t s_bins[];  // [copies][E], then 1
+  extern __shared__ int32_t s_mem[];
   int total = 0;
   const Span sp = find_span(off, S, T, chunk, blockIdx.x, total);
   if (sp.seq < 0) return;  // equal in every thread
-  for (int i = threadIdx.x; i < copies * E + 1; i += BL_COUNT_THREADS) s_bins[i] = 0;
-  __syncthreads();
-  int32_t *bins = s_bins + (threadIdx.x & (copies - 1)) * E;
-  const int64_t i0 = (int64_t)sp.begin * k, i1 = (int64_t)sp.end * k;
-  for (int64_t i = i0 + threadIdx.x; i < i1; i += BL_COUNT_THREADS) {
-    const int t = (int)(i / k);
-    const int e = ids[i];
-    if (mask && mask[t] == 0) continue;
-    if (e >= 0 && e < E) atomicAdd(&bins[e], 1);
-  }
-  int mine = 0;
-  for (int t = sp.begin + (int)threadIdx.x; t < sp.end; t += BL_COUNT_THREADS) mine += !mask || mask[t] != 0;
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) mine += __shfl_xor(mine, o, 64);
-  if ((threadIdx.x & 63) == 0 && mine) atomicAdd(&s_bins[copies * E], mine);
-  __syncthreads();
+  count_chunk_lds<BL_COUNT_THREADS>(s_mem, copies, ids, mask, sp.begin, sp.end, E, k);
   int32_t *out = part + (size_t)blockIdx.x * (E + 1);
-  for (int e = threadIdx.x; e < E; e += BL_COUNT_THREADS) {
-    int c = 0;
-    for (int q = 0; q < copies; ++q) c += s_bins[q * E + e];
-    out[e] = c;
-  }
-  if (threadIdx.x == 0) out[E] = s_bins[copies * E];
+  for (int e = threadIdx.x; e <= E; e += BL_COUNT_THREADS) out[e] = s_mem[e < E ? e : copies * E];
 }
 
 // One block a sequence: its counts and counted tokens from the chunks', and the index of its
@@ -140,11 +182,12 @@ __global__ __launch_bounds__(256) void balance_tables_kernel(const int32_t *__re
   }
   int b, e;
   seq_range(off, T, s, b, e);
-  const int n = (e - b + chunk - 1) / chunk;
+  // (offsets that run backwards could name more chunks than there are)
+  const int n = min((e - b + chunk - 1) / chunk, max(blocks - first, 0));
   for (int i = threadIdx.x; i <= E; i += 256) {
     int c = 0;
-    // (offsets that run backwards could name more chunks than there are)
-    for (int q = 0; q < n && first + q < blocks; ++q) c += part[(size_t)(first + q) * (E + 1) + i];
+#pragma unroll 8
+    for (int q = 0; q < n; ++q) c += part[(size_t)(first + q) * (E + 1) + i];
     if (i < E)
       counts[(size_t)s * E + i] = c;
     else
@@ -156,34 +199,68 @@ __global__ __launch_bounds__(256) void balance_tables_kernel(const int32_t *__re
   }
 }
 
+// ------------------------------------------------------------------------------- main pass
+
 struct BalanceArgs {
   const float *logits;
+  const int32_t *ids;  // the block counts for itself (one sequence of few choices), or NULL
   const uint8_t *mask;
   const int32_t *off;
-  const int32_t *counts;
-  const int32_t *seq_tokens;
+  int32_t *counts;
+  int32_t *seq_tokens;
   const float *dloss;  // upstream gradients of the two losses, or NULL (ones)
   float *dlogits;      // or NULL
   float *part;         // [blocks][E]: column sums of p
   double *zpart;       // [blocks]: sums of z^2 (a finite z's square can pass the largest float)
-  int T, E, k, S, chunk;
+  int32_t *first_main;
+  uint32_t *ticket;
+  float *mean_probs, *losses;
+  int T, E, k, S, chunk, copies;
+  int one;  // the only block: it finishes too
   float alpha, beta;
 };
 
-// A token's row in LPT lanes of NV groups of four values each; 64 / LPT tokens a wavefront.
-// With VEC (E a multiple of 4) a group is one 16-byte load; otherwise its values lie LPT
-// apart, so that each load of a group still covers neighbouring words.
-template <int LPT, int NV, bool VEC, bool LOSS>
-__global__ __launch_bounds__(256) void balance_main_kernel(BalanceArgs a) {
+// Reductions over groups of LPT neighbouring lanes, the result in every lane: lane moves
+// within a row of 16 (lane ^ 1, lane ^ 2, then half-row and row mirrors, which pair equal
+// values), then rows and halves of the wavefront exchanged.
+template <int CTRL>
+__device__ __forceinline__ float lane_move(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, false));
+}
+template <int LPT, typename Op>
+__device__ __forceinline__ float group_reduce(float v, Op op) {
+  if constexpr (LPT >= 2) v = op(v, lane_move<0xb1>(v));
+  if constexpr (LPT >= 4) v = op(v, lane_move<0x4e>(v));
+  if constexpr (LPT >= 8) v = op(v, lane_move<0x141>(v));
+  if constexpr (LPT >= 16) v = op(v, lane_move<0x140>(v));
+  if constexpr (LPT >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
+  if constexpr (LPT >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
+  return v;
+}
+
+// A token's row in LPT lanes of VPL values each, 64 / LPT tokens a wavefront, NT such groups
+// of tokens at a time (their loads and lane moves in flight together).  With VEC (E a
+// multiple of 4) a lane's values are 16-byte groups; otherwise they lie LPT apart, so that
+// each load still covers neighbouring words.
+template <int LPT, int VPL, bool VEC, bool LOSS>
+__global__ __launch_bounds__(BL_THREADS) void balance_main_kernel(BalanceArgs a) {
   constexpr int TPW = 64 / LPT;
-  __shared__ float s_acc[LOSS ? 4 : 1][LOSS ? LPT * NV * 4 : 1];
-  __shared__ double s_z[4];
+  constexpr int NT = VPL <= 4 ? 4 : VPL <= 8 ? 2 : 1;
+  extern __shared__ int32_t s_mem[];  // counting bins, then the waves' column sums [BL_WAVES][E]
+  __shared__ double s_red[BL_WAVES][2];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int li = lane & (LPT - 1), sub = lane / LPT;
   const int E = a.E;
-  auto expert = [&](int v, int i) { return VEC ? 4 * (li + LPT * v) + i : li + LPT * (4 * v + i); };
+  auto expert = [&](int v) { return VEC ? 4 * (li + LPT * (v / 4)) + v % 4 : li + LPT * v; };
   int total = 0;
   const Span sp = find_span(a.off, a.S, a.T, a.chunk, blockIdx.x, total);
+  if (LOSS && blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;  // of the finishing pass
   if (sp.seq < 0) {
     // blocks past the last chunk: rows outside every sequence get a zero gradient
     if (a.dlogits && a.off) {
@@ -191,222 +268,323 @@ __global__ __launch_bounds__(256) void balance_main_kernel(BalanceArgs a) {
       seq_range(a.off, a.T, 0, b0, e0);
       seq_range(a.off, a.T, a.S - 1, b1, e1);
       const int64_t lead = (int64_t)b0 * E, tail = (int64_t)(a.T - e1) * E;
-      const int64_t step = (int64_t)(gridDim.x - total) * 256;
-      for (int64_t i = (int64_t)(blockIdx.x - total) * 256 + threadIdx.x; i < lead + tail; i += step)
+      const int64_t step = (int64_t)(gridDim.x - total) * BL_THREADS;
+      for (int64_t i = (int64_t)(blockIdx.x - total) * BL_THREADS + threadIdx.x; i < lead + tail; i += step)
         a.dlogits[i < lead ? i : i - lead + (int64_t)e1 * E] = 0.f;
     }
-    return;
+    if (!(LOSS && a.ids && blockIdx.x == 0)) return;  // block 0 counts also where there are no rows
   }
-  // sequences that count a token, tokens in all
-  int live = 0, all = 0;
-  for (int s = lane; s < a.S; s += 64) {
-    const int n = a.seq_tokens[s];
-    live += n > 0;
-    all += n;
-  }
+  // sequences that count a token, tokens in all, this sequence's
+  int live = 0, all = 0, ns = 0;
+  float f[VPL];
+  if (LOSS && a.ids) {
+    int b, e;
+    seq_range(a.off, a.T, 0, b, e);
+    count_chunk_lds<BL_THREADS>(s_mem, a.copies, a.ids, a.mask, b, e, E, a.k);
+    ns = all = s_mem[a.copies * E];
+    live = ns > 0;
+    if (blockIdx.x == 0) {
+      for (int i = threadIdx.x; i < E; i += BL_THREADS) a.counts[i] = s_mem[i];
+      if (threadIdx.x == 0) {
+        a.seq_tokens[0] = ns;
+        a.first_main[0] = 0;
+        a.first_main[1] = (e - b + a.chunk - 1) / a.chunk;
+      }
+    }
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) {
-    live += __shfl_xor(live, o, 64);
-    all += __shfl_xor(all, o, 64);
+    for (int v = 0; v < VPL; ++v) f[v] = expert(v) < E ? (float)s_mem[expert(v)] : 0.f;
+    __syncthreads();
+  } else {
+    for (int s = lane; s < a.S; s += 64) {
+      const int n = a.seq_tokens[s];
+      live += n > 0;
+      all += n;
+    }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) {
+      live += __shfl_xor(live, o, 64);
+      all += __shfl_xor(all, o, 64);
+    }
+    ns = a.seq_tokens[sp.seq];
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) f[v] = expert(v) < E ? (float)a.counts[(size_t)sp.seq * E + expert(v)] : 0.f;
   }
-  const int ns = a.seq_tokens[sp.seq];
   const float up0 = a.dloss ? a.dloss[0] : 1.f, up1 = a.dloss ? a.dloss[1] : 1.f;
   const float ca = up0 * (a.alpha * (float)E / ((float)max(live, 1) * (float)max(ns, 1)));
   const float cb = up1 * (2.f * a.beta / (float)max(all, 1));
   const float fden = (float)max(ns, 1) * (float)a.k;
-  float f[NV][4], acc[NV][4];
+  float acc[VPL];
   double zacc = 0.;
 #pragma unroll
-  for (int v = 0; v < NV; ++v)
+  for (int v = 0; v < VPL; ++v) {
+    f[v] /= fden;
+    acc[v] = 0.f;
+  }
+  for (int t0 = sp.begin + wave * (NT * TPW); t0 < sp.end; t0 += BL_WAVES * NT * TPW) {
+    float l[NT][VPL];
+    bool counted[NT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = expert(v, i);
-      f[v][i] = e < E ? (float)a.counts[(size_t)sp.seq * E + e] / fden : 0.f;
-      acc[v][i] = 0.f;
+    for (int n = 0; n < NT; ++n) {
+      const int t = t0 + n * TPW + sub;
+      counted[n] = t < sp.end && (!a.mask || a.mask[t] != 0);
     }
-  for (int t0 = sp.begin + wave * TPW; t0 < sp.end; t0 += 4 * TPW) {
-    const int t = t0 + sub;
-    const bool in = t < sp.end;
-    const bool counted = in && (!a.mask || a.mask[t] != 0);
-    const float *row = a.logits + (size_t)t * E;
-    float l[NV][4];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
+    for (int n = 0; n < NT; ++n) {
+      const float *row = a.logits + (size_t)(t0 + n * TPW + sub) * E;
       if constexpr (VEC) {
-        f32x4 q = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        if (counted && expert(v, 0) < E) q = *reinterpret_cast<const f32x4 *>(row + expert(v, 0));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) l[v][i] = q[i];
+        for (int v = 0; v < VPL; v += 4) {
+          f32x4 q = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          if (counted[n] && expert(v) < E) q = *reinterpret_cast<const f32x4 *>(row + expert(v));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) l[n][v + i] = q[i];
+        }
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) l[v][i] = counted && expert(v, i) < E ? row[expert(v, i)] : -INFINITY;
+        for (int v = 0; v < VPL; ++v) l[n][v] = counted[n] && expert(v) < E ? row[expert(v)] : -INFINITY;
       }
     }
-    float m = -INFINITY;
+    float base[NT], sum[NT], dot[NT];
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+    for (int n = 0; n < NT; ++n) {
+      float m = l[n][0];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) m = fmaxf(m, l[v][i]);
-#pragma unroll
-    for (int o = LPT / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-    // a row without any finite logit (or an uncounted one) has sum 0: no probabilities
-    const float base = m == -INFINITY ? 0.f : m;
-    float sum = 0.f, dot = 0.f;
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        l[v][i] = __expf(l[v][i] - base);
-        sum += l[v][i];
-        dot += l[v][i] * f[v][i];
-      }
-#pragma unroll
-    for (int o = LPT / 2; o >= 1; o >>= 1) {
-      sum += __shfl_xor(sum, o, 64);
-      dot += __shfl_xor(dot, o, 64);
+      for (int v = 1; v < VPL; ++v) m = fmaxf(m, l[n][v]);
+      m = group_reduce<LPT>(m, [](float x, float y) { return fmaxf(x, y); });
+      // a row without any finite logit (or an uncounted one) has sum 0: no probabilities
+      base[n] = m == -INFINITY ? 0.f : m;
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const float z = sum == 0.f ? 0.f : base + __logf(sum);
-    dot *= inv;
-    if constexpr (LOSS) zacc += li == 0 ? (double)z * (double)z : 0.;
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+    for (int n = 0; n < NT; ++n) {
+      sum[n] = dot[n] = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        l[v][i] *= inv;
-        if constexpr (LOSS) acc[v][i] += l[v][i];
+      for (int v = 0; v < VPL; ++v) {
+        l[n][v] = __expf(l[n][v] - base[n]);
+        sum[n] += l[n][v];
+        dot[n] += l[n][v] * f[v];
       }
-    if (a.dlogits && in) {
-      float *drow = a.dlogits + (size_t)t * E;
+      sum[n] = group_reduce<LPT>(sum[n], [](float x, float y) { return x + y; });
+      dot[n] = group_reduce<LPT>(dot[n], [](float x, float y) { return x + y; });
+    }
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        f32x4 q;
+    for (int n = 0; n < NT; ++n) {
+      const int t = t0 + n * TPW + sub;
+      const float inv = sum[n] == 0.f ? 0.f : 1.f / sum[n];
+      const float z = sum[n] == 0.f ? 0.f : base[n] + __logf(sum[n]);
+      const float shift = ca * (dot[n] * inv) - cb * z;
+      if constexpr (LOSS) zacc += li == 0 ? (double)z * (double)z : 0.;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = l[v][i] * (ca * (f[v][i] - dot) + cb * z);
+      for (int v = 0; v < VPL; ++v) {
+        l[n][v] *= inv;
+        if constexpr (LOSS) acc[v] += l[n][v];
+      }
+      if (a.dlogits && t < sp.end) {
+        float *drow = a.dlogits + (size_t)t * E;
         if constexpr (VEC) {
-          if (expert(v, 0) < E) *reinterpret_cast<f32x4 *>(drow + expert(v, 0)) = q;
+#pragma unroll
+          for (int v = 0; v < VPL; v += 4) {
+            f32x4 q;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q[i] = l[n][v + i] * (ca * f[v + i] - shift);
+            if (expert(v) < E) *reinterpret_cast<f32x4 *>(drow + expert(v)) = q;
+          }
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (expert(v, i) < E) drow[expert(v, i)] = q[i];
+          for (int v = 0; v < VPL; ++v)
+            if (expert(v) < E) drow[expert(v)] = l[n][v] * (ca * f[v] - shift);
         }
       }
     }
   }
   if constexpr (LOSS) {
+    float *s_acc = reinterpret_cast<float *>(s_mem);
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+    for (int v = 0; v < VPL; ++v) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int o = LPT; o < 64; o <<= 1) acc[v] += __shfl_xor(acc[v], o, 64);
+      if (sub == 0 && expert(v) < E) s_acc[wave * E + expert(v)] = acc[v];
+    }
+    double unused = 0;
+    block_sum2<BL_WAVES>(zacc, unused, s_red);  // synchronises: the column sums are visible after it
+    if (!a.one) {
+      if (threadIdx.x == 0) a.zpart[blockIdx.x] = zacc;
+      float *out = a.part + (size_t)blockIdx.x * E;
+      for (int e = threadIdx.x; e < E; e += BL_THREADS) {
+        float p = 0;
 #pragma unroll
-        for (int o = LPT; o < 64; o <<= 1) acc[v][i] += __shfl_xor(acc[v][i], o, 64);
-        if (sub == 0 && expert(v, i) < E) s_acc[wave][expert(v, i)] = acc[v][i];
+        for (int w = 0; w < BL_WAVES; ++w) p += s_acc[w * E + e];
+        out[e] = p;
       }
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) zacc += __shfl_xor(zacc, o, 64);
-    if (lane == 0) s_z[wave] = zacc;
-    __syncthreads();
-    if (threadIdx.x == 0) a.zpart[blockIdx.x] = (s_z[0] + s_z[1]) + (s_z[2] + s_z[3]);
-    float *out = a.part + (size_t)blockIdx.x * E;
-    for (int e = threadIdx.x; e < E; e += 256) out[e] = (s_acc[0][e] + s_acc[1][e]) + (s_acc[2][e] + s_acc[3][e]);
+      return;
+    }
+    double bal = 0;
+    for (int e = threadIdx.x; e < E; e += BL_THREADS) {
+      double p = 0;
+      for (int w = 0; w < BL_WAVES; ++w) p += s_acc[w * E + e];
+      p = ns > 0 ? p / ns : 0.0;
+      a.mean_probs[e] = (float)p;
+      bal += p * ((double)a.counts[e] / ((double)max(ns, 1) * a.k));
+    }
+    block_sum2<BL_WAVES>(bal, unused, s_red);
+    if (threadIdx.x == 0) {
+      a.losses[0] = (float)((double)a.alpha * E * bal);
+      a.losses[1] = (float)((double)a.beta * zacc / max(ns, 1));
+    }
   }
 }
 
-// One block: the mean probabilities and the two losses from the main pass's partial sums, in
-// 64 bits.
-__global__ __launch_bounds__(1024) void balance_finish_kernel(const float *__restrict__ part,
-                                                              const double *__restrict__ zpart,
-                                                              const int32_t *__restrict__ first_main,
-                                                              const int32_t *__restrict__ counts,
-                                                              const int32_t *__restrict__ seq_tokens, int E, int k,
-                                                              int S, float alpha, float beta,
-                                                              float *__restrict__ mean_probs,
-                                                              float *__restrict__ losses) {
-  __shared__ double s_bal[1024], s_z[1024];
-  __shared__ int s_live, s_all;
-  if (threadIdx.x == 0) s_live = s_all = 0;
-  __syncthreads();
-  int live = 0, all = 0;
-  for (int s = threadIdx.x; s < S; s += 1024) {
-    live += seq_tokens[s] > 0;
-    all += seq_tokens[s];
-  }
-  if (live) atomicAdd(&s_live, live);
-  if (all) atomicAdd(&s_all, all);
+// ---------------------------------------------------------------------------------- finish
+
+constexpr int BL_FIN_THREADS = 1024, BL_FIN_WAVES = BL_FIN_THREADS / 64;
+
+// One block a sequence: its mean probabilities and its terms of the losses, in 64 bits; the
+// block that finishes last adds the sequences' terms in order.  `cols` threads (a power of
+// two) stand on neighbouring experts, the others on further blocks of the main pass.
+__global__ __launch_bounds__(BL_FIN_THREADS) void balance_finish_kernel(
+    const float *__restrict__ part, const double *__restrict__ zpart, const int32_t *__restrict__ first_main,
+    const int32_t *__restrict__ counts, const int32_t *__restrict__ seq_tokens, int E, int k, int S, int cols,
+    float alpha, float beta, float *__restrict__ mean_probs, double *terms, uint32_t *ticket,
+    float *__restrict__ losses) {
+  __shared__ double s_p[BL_FIN_THREADS];
+  __shared__ double s_red[BL_FIN_WAVES][2];
+  __shared__ int s_last;
+  const int s = blockIdx.x;
+  const int b0 = first_main[s], b1 = first_main[s + 1], n = seq_tokens[s];
+  const int col = threadIdx.x & (cols - 1), row = threadIdx.x / cols, rows = BL_FIN_THREADS / cols;
   double bal = 0, z = 0;
-  for (int64_t i = threadIdx.x; i < (int64_t)S * E; i += 1024) {
-    const int s = (int)(i / E), e = (int)(i - (int64_t)s * E);
+  for (int e0 = 0; e0 < E; e0 += cols) {
+    const int e = e0 + col;
     double p = 0;
-    for (int b = first_main[s]; b < first_main[s + 1]; ++b) p += part[(size_t)b * E + e];
-    const int n = seq_tokens[s];
-    const double P = n > 0 ? p / n : 0.0;
-    mean_probs[i] = (float)P;
-    if (n > 0) bal += P * ((double)counts[i] / ((double)n * k));
-  }
-  for (int b = threadIdx.x; b < first_main[S]; b += 1024) z += zpart[b];
-  s_bal[threadIdx.x] = bal;
-  s_z[threadIdx.x] = z;
-  __syncthreads();
-  for (int o = 512; o >= 1; o >>= 1) {
-    if (threadIdx.x < o) {
-      s_bal[threadIdx.x] += s_bal[threadIdx.x + o];
-      s_z[threadIdx.x] += s_z[threadIdx.x + o];
+    if (e < E) {
+#pragma unroll 8
+      for (int b = b0 + row; b < b1; b += rows) p += part[(size_t)b * E + e];
+    }
+    s_p[threadIdx.x] = p;
+    __syncthreads();
+    if (row == 0 && e < E) {
+      for (int r = 1; r < rows; ++r) p += s_p[r * cols + col];
+      p = n > 0 ? p / n : 0.0;
+      mean_probs[(size_t)s * E + e] = (float)p;
+      bal += p * ((double)counts[(size_t)s * E + e] / ((double)max(n, 1) * k));
     }
     __syncthreads();
   }
+  for (int b = b0 + (int)threadIdx.x; b < b1; b += BL_FIN_THREADS) z += zpart[b];
+  block_sum2<BL_FIN_WAVES>(bal, z, s_red);
+  if (S == 1) {
+    if (threadIdx.x == 0) {
+      losses[0] = (float)((double)alpha * E * bal);
+      losses[1] = (float)((double)beta * z / max(n, 1));
+    }
+    return;
+  }
   if (threadIdx.x == 0) {
-    losses[0] = (float)((double)alpha * E * s_bal[0] / max(s_live, 1));
-    losses[1] = (float)((double)beta * s_z[0] / max(s_all, 1));
+    __hip_atomic_store(&terms[2 * s], bal, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(&terms[2 * s + 1], z, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __threadfence();
+    s_last = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)S - 1;
+  }
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  double live = 0, all = 0;
+  bal = z = 0;
+  for (int q = threadIdx.x; q < S; q += BL_FIN_THREADS) {
+    bal += __hip_atomic_load(&terms[2 * q], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    z += __hip_atomic_load(&terms[2 * q + 1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    live += seq_tokens[q] > 0;
+    all += seq_tokens[q];
+  }
+  block_sum2<BL_FIN_WAVES>(bal, z, s_red);
+  block_sum2<BL_FIN_WAVES>(live, all, s_red);
+  if (threadIdx.x == 0) {
+    losses[0] = (float)((double)alpha * E * bal / max(live, 1.0));
+    losses[1] = (float)((double)beta * z / max(all, 1.0));
   }
 }
 
-int count_chunk(int T) { return std::max(1024, (T + 63) / 64); }
-int main_chunk(int T) { return std::max(32, (T + 511) / 512); }
+// Lanes a token takes: a power of two with at most four values each, 64 past that.
+int lanes_per_token(int E) {
+  int l = 1;
+  while (l < 64 && 4 * l < E) l *= 2;
+  return l;
+}
+
+int count_chunk(int T) { return std::max(256, (T + 255) / 256); }
+// Tokens of a block of the main pass: one round of its wavefronts at least.
+int main_chunk(int T, int E) {
+  const int tpw = 64 / lanes_per_token(E), nt = E <= 256 ? 4 : E <= 512 ? 2 : 1;
+  return std::max(BL_WAVES * tpw * nt, (T + 511) / 512);
+}
 
 // Chunks of the two passes: sequences cut into whole chunks, at most one partial chunk each,
 // and in the main pass one block more for the rows outside every sequence.
 int count_blocks(int T, int S, bool off) { return (T + count_chunk(T) - 1) / count_chunk(T) + (off ? S : 0); }
-int main_blocks(int T, int S, bool off) { return (T + main_chunk(T) - 1) / main_chunk(T) + (off ? S + 1 : 0); }
+int main_blocks(int T, int E, int S, bool off) {
+  return (T + main_chunk(T, E) - 1) / main_chunk(T, E) + (off ? S + 1 : 0);
+}
+
+int bin_copies(int E) {
+  int copies = 1;
+  while (copies < 64 && copies * 2 * E <= BL_BINS) copies *= 2;
+  return copies;
+}
 
 template <bool LOSS>
-hipError_t launch_main(const BalanceArgs &a, hipStream_t s) {
-  const dim3 grid((unsigned)main_blocks(a.T, a.S, a.off != nullptr));
+hipError_t launch_main(const BalanceArgs &a, int blocks, hipStream_t s) {
   const int E = a.E;
-#define BL_CASE(L, N)                                                                             \
-  do {                                                                                            \
-    if (E % 4 == 0)                                                                               \
-      hipLaunchKernelGGL((balance_main_kernel<L, N, true, LOSS>), grid, dim3(256), 0, s, a);      \
-    else                                                                                          \
-      hipLaunchKernelGGL((balance_main_kernel<L, N, false, LOSS>), grid, dim3(256), 0, s, a);     \
-    return hipGetLastError();                                                                     \
+  const size_t lds = LOSS ? std::max((size_t)BL_WAVES * E * 4, a.ids ? ((size_t)a.copies * E + 1) * 4 : (size_t)0) : 0;
+#define BL_LAUNCH(L, V, VEC)                                                                                        \
+  do {                                                                                                              \
+    hipLaunchKernelGGL((balance_main_kernel<L, V, VEC, LOSS>), dim3((unsigned)blocks), dim3(BL_THREADS), lds, s, a); \
+    return hipGetLastError();                                                                                       \
   } while (0)
-  if (E <= 4) BL_CASE(1, 1);
-  if (E <= 8) BL_CASE(2, 1);
-  if (E <= 16) BL_CASE(4, 1);
-  if (E <= 32) BL_CASE(8, 1);
-  if (E <= 64) BL_CASE(16, 1);
-  if (E <= 128) BL_CASE(32, 1);
-  if (E <= 256) BL_CASE(64, 1);
-  if (E <= 512) BL_CASE(64, 2);
-  BL_CASE(64, 4);
+#define BL_CASE(L)                          \
+  do {                                      \
+    if (E % 4 == 0) BL_LAUNCH(L, 4, true);  \
+    if (E <= 3 * L) BL_LAUNCH(L, 3, false); \
+    BL_LAUNCH(L, 4, false);                 \
+  } while (0)
+  switch (lanes_per_token(E)) {
+    case 1: BL_CASE(1);
+    case 2: BL_CASE(2);
+    case 4: BL_CASE(4);
+    case 8: BL_CASE(8);
+    case 16: BL_CASE(16);
+    case 32: BL_CASE(32);
+  }
+  if (E <= 256) BL_CASE(64);
+  if (E <= 512) {
+    if (E % 4 == 0) BL_LAUNCH(64, 8, true);
+    BL_LAUNCH(64, 8, false);
+  }
+  if (E % 4 == 0) BL_LAUNCH(64, 16, true);
+  BL_LAUNCH(64, 16, false);
 #undef BL_CASE
+#undef BL_LAUNCH
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 struct BalanceWs {
-  size_t count_part, main_part, z_part, first_main, total;
+  size_t count_part, main_part, z_part, first_main, terms, ticket, total;
 };
 BalanceWs balance_ws(int T, int E, int S) {
   BalanceWs w;
-  const size_t cb = count_blocks(T, S, true), mb = main_blocks(T, S, true);
+  const size_t cb = count_blocks(T, S, true), mb = main_blocks(T, E, S, true);
   w.count_part = 0;
   w.main_part = align256(cb * (E + 1) * 4);
   w.z_part = w.main_part + align256(mb * E * 4);
   w.first_main = w.z_part + align256(mb * 8);
-  w.total = w.first_main + align256(((size_t)S + 1) * 4);
+  w.terms = w.first_main + align256(((size_t)S + 1) * 4);
+  w.ticket = w.terms + align256((size_t)S * 16);
+  w.total = w.ticket + 256;
   return w;
 }
+
+// One sequence with at most this many choices is counted by every block of the main pass for
+// itself.
+constexpr int64_t kSelfCount = 16384;
 
 }  // namespace
 
@@ -417,35 +595,71 @@ hipError_t launch_balance_loss(const BalanceCall &c, int32_t *counts, int32_t *s
   const BalanceWs w = balance_ws(c.T, c.E, c.S);
   uint8_t *base = static_cast<uint8_t *>(ws);
   int32_t *cpart = reinterpret_cast<int32_t *>(base + w.count_part);
-  float *mpart = reinterpret_cast<float *>(base + w.main_part);
-  double *zpart = reinterpret_cast<double *>(base + w.z_part);
-  int32_t *first_main = reinterpret_cast<int32_t *>(base + w.first_main);
-  const int cc = count_chunk(c.T), mc = main_chunk(c.T);
-  const int cb = count_blocks(c.T, c.S, c.off != nullptr), mb = main_blocks(c.T, c.S, c.off != nullptr);
-  int copies = 1;
-  while (copies < 64 && copies * 2 * c.E <= 4096) copies *= 2;
-  hipLaunchKernelGGL(balance_count_kernel, dim3((unsigned)cb), dim3(BL_COUNT_THREADS),
-                     (copies * c.E + 1) * 4, s, c.ids, c.mask, c.off, c.T, c.E, c.k, c.S, cc, copies, cpart);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(balance_tables_kernel, dim3((unsigned)c.S), dim3(256), 0, s, c.off, c.T, c.E, c.S, cc, mc, cb, mb, cpart,
-                     counts, seq_tokens, first_main);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  BalanceArgs a{c.logits, c.mask, c.off, counts, seq_tokens, c.dloss, c.dlogits, mpart, zpart, c.T, c.E, c.k, c.S, mc,
-                c.alpha,  c.beta};
-  e = launch_main<true>(a, s);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(balance_finish_kernel, dim3(1), dim3(1024), 0, s, mpart, zpart, first_main, counts, seq_tokens, c.E, c.k,
-                     c.S, c.alpha, c.beta, mean_probs, losses);
+  const bool off = c.off != nullptr;
+  const int cc = count_chunk(c.T), mc = main_chunk(c.T, c.E);
+  const int cb = count_blocks(c.T, c.S, off), mb = main_blocks(c.T, c.E, c.S, off);
+  const int copies = bin_copies(c.E);
+  BalanceArgs a{};
+  a.logits = c.logits;
+  a.mask = c.mask;
+  a.off = c.off;
+  a.counts = counts;
+  a.seq_tokens = seq_tokens;
+  a.dloss = c.dloss;
+  a.dlogits = c.dlogits;
+  a.part = reinterpret_cast<float *>(base + w.main_part);
+  a.zpart = reinterpret_cast<double *>(base + w.z_part);
+  a.first_main = reinterpret_cast<int32_t *>(base + w.first_main);
+  a.ticket = reinterpret_cast<uint32_t *>(base + w.ticket);
+  a.mean_probs = mean_probs;
+  a.losses = losses;
+  a.T = c.T;
+  a.E = c.E;
+  a.k = c.k;
+  a.S = c.S;
+  a.chunk = mc;
+  a.copies = copies;
+  a.alpha = c.alpha;
+  a.beta = c.beta;
+  hipError_t e;
+  if (c.S == 1 && (int64_t)c.T * c.k <= kSelfCount) {
+    a.ids = c.ids;
+    a.one = mb == 1;
+  } else {
+    hipLaunchKernelGGL(balance_count_kernel, dim3((unsigned)cb), dim3(BL_COUNT_THREADS), (copies * c.E + 1) * 4, s,
+                       c.ids, c.mask, c.off, c.T, c.E, c.k, c.S, cc, copies, cpart);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipLaunchKernelGGL(balance_tables_kernel, dim3((unsigned)c.S), dim3(256), 0, s, c.off, c.T, c.E, c.S, cc, mc, cb,
+                       mb, cpart, counts, seq_tokens, a.first_main);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if ((e = launch_main<true>(a, mb, s)) != hipSuccess || a.one) return e;
+  int cols = 1;
+  while (cols < BL_FIN_THREADS && cols < c.E) cols *= 2;
+  hipLaunchKernelGGL(balance_finish_kernel, dim3((unsigned)c.S), dim3(BL_FIN_THREADS), 0, s, a.part, a.zpart,
+                     a.first_main, counts, seq_tokens, c.E, c.k, c.S, cols, c.alpha, c.beta, mean_probs,
+                     reinterpret_cast<double *>(base + w.terms), a.ticket, losses);
   return hipGetLastError();
 }
 
 hipError_t launch_balance_backward(const BalanceCall &c, const int32_t *counts, const int32_t *seq_tokens,
                                    hipStream_t s) {
-  BalanceArgs a{c.logits, c.mask, c.off, counts, seq_tokens, c.dloss, c.dlogits, nullptr, nullptr, c.T, c.E, c.k, c.S,
-                main_chunk(c.T), c.alpha, c.beta};
-  return launch_main<false>(a, s);
+  BalanceArgs a{};
+  a.logits = c.logits;
+  a.mask = c.mask;
+  a.off = c.off;
+  a.counts = const_cast<int32_t *>(counts);  // read only without the loss
+  a.seq_tokens = const_cast<int32_t *>(seq_tokens);
+  a.dloss = c.dloss;
+  a.dlogits = c.dlogits;
+  a.T = c.T;
+  a.E = c.E;
+  a.k = c.k;
+  a.S = c.S;
+  a.chunk = main_chunk(c.T, c.E);
+  a.alpha = c.alpha;
+  a.beta = c.beta;
+  return launch_main<false>(a, main_blocks(c.T, c.E, c.S, c.off != nullptr), s);
 }
 
 }  // namespace moe
