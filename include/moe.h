@@ -530,7 +530,7 @@ typedef struct moe_adamw_tensor {
 } moe_adamw_tensor;
 
 typedef struct moe_adamw_hparams {
-  double lr, beta1, beta2, eps; /* lr >= 0; betas in [0, 1); eps > 0 */
+  double lr, beta1, beta2, eps; /* lr >= 0; betas in [0, 1); eps a normal float above 0 */
   int64_t step;                 /* t >= 1, the number of this step */
   /* Optional device scalars, read when the step runs (a captured step then follows them on
    * every replay): lr and t in the place of the two fields above (a t below 1 counts as 1),
@@ -547,7 +547,7 @@ typedef struct moe_adamw_hparams {
  * the parameters (the same tensor twice), in the debug build in full. */
 moe_status moe_adamw_check_tensors(const moe_adamw_tensor *tensors, int32_t num_tensors);
 
-/* One AdamW step (decoupled weight decay) of every tensor, in a launch per 40 tensors:
+/* One AdamW step (decoupled weight decay) of every tensor, in a launch per 48 tensors:
  *   g' = out[1] g;  m' = b1 m + (1 - b1) g';  v' = b2 v + (1 - b2) g'^2
  *   w' = w (1 - lr wd) - lr / (1 - b1^t) m' / (sqrt(v') / sqrt(1 - b2^t) + eps)
  * in float (8-bit states: m' and v' in 64 bits), w' rounded once to param_dtype.

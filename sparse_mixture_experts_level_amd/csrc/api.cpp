@@ -3,6 +3,7 @@
 #include "moe.h"
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -1424,7 +1425,8 @@ moe_status moe_adamw_step(const moe_adamw_tensor *tensors, int32_t num_tensors, 
   if (!H.lr_dev && !(H.lr >= 0.0 && std::isfinite(H.lr))) return fail(MOE_ERR_INVALID, "lr must be finite and >= 0");
   if (!(H.beta1 >= 0.0 && H.beta1 < 1.0) || !(H.beta2 >= 0.0 && H.beta2 < 1.0))
     return fail(MOE_ERR_INVALID, "beta1 and beta2 must lie in [0, 1)");
-  if (!(H.eps > 0.0) || !std::isfinite(H.eps)) return fail(MOE_ERR_INVALID, "eps must be finite and above 0");
+  if (!(H.eps >= (double)FLT_MIN && H.eps <= (double)FLT_MAX))
+    return fail(MOE_ERR_INVALID, "eps must lie within the normal floats (above 1.2e-38)");
   if (!H.step_dev && H.step < 1) return fail(MOE_ERR_INVALID, "step %lld < 1", (long long)H.step);
   MOE_TRY(check_opt_ptr(H.lr_dev, "lr_dev"));
   MOE_TRY(check_opt_ptr(H.step_dev, "step_dev"));

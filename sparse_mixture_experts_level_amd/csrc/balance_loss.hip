@@ -211,9 +211,9 @@ struct BalanceArgs {
   const float *dloss;  // upstream gradients of the two losses, or NULL (ones)
   float *dlogits;      // or NULL
   float *part;         // [blocks][E]: column sums of p
-  double *zpart;       // [blocks]: sums of z^2 (a finite z's square can pass the largest float)
+  double *sums;        // [blocks][2]: sum of sum_i f_i p_ti / N_s, sum of z^2 (a finite z's square can pass
+                       // the largest float)
   int32_t *first_main;
-  uint32_t *ticket;
   float *mean_probs, *losses;
   int T, E, k, S, chunk, copies;
   int one;  // the only block: it finishes too
@@ -260,7 +260,6 @@ __global__ __launch_bounds__(BL_THREADS) void balance_main_kernel(BalanceArgs a)
   auto expert = [&](int v) { return VEC ? 4 * (li + LPT * (v / 4)) + v % 4 : li + LPT * v; };
   int total = 0;
   const Span sp = find_span(a.off, a.S, a.T, a.chunk, blockIdx.x, total);
-  if (LOSS && blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;  // of the finishing pass
   if (sp.seq < 0) {
     // blocks past the last chunk: rows outside every sequence get a zero gradient
     if (a.dlogits && a.off) {
@@ -274,6 +273,32 @@ __global__ __launch_bounds__(BL_THREADS) void balance_main_kernel(BalanceArgs a)
     }
     if (!(LOSS && a.ids && blockIdx.x == 0)) return;  // block 0 counts also where there are no rows
   }
+  float l[NT][VPL];
+  bool counted[NT];
+  // rows of uncounted tokens are read and not looked at: the loads do not wait for the mask
+  auto load = [&](int t0) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int t = t0 + n * TPW + sub;
+      const bool in = t < sp.end;
+      const float *row = a.logits + (size_t)t * E;
+      counted[n] = in && (!a.mask || a.mask[t] != 0);
+      if constexpr (VEC) {
+#pragma unroll
+        for (int v = 0; v < VPL; v += 4) {
+          f32x4 q = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          if (in && expert(v) < E) q = *reinterpret_cast<const f32x4 *>(row + expert(v));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) l[n][v + i] = q[i];
+        }
+      } else {
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) l[n][v] = in && expert(v) < E ? row[expert(v)] : -INFINITY;
+      }
+    }
+  };
+  const int t_first = sp.begin + wave * (NT * TPW);
+  load(t_first);  // in flight while the tables are read
   // sequences that count a token, tokens in all, this sequence's
   int live = 0, all = 0, ns = 0;
   float f[VPL];
@@ -314,42 +339,23 @@ __global__ __launch_bounds__(BL_THREADS) void balance_main_kernel(BalanceArgs a)
   const float cb = up1 * (2.f * a.beta / (float)max(all, 1));
   const float fden = (float)max(ns, 1) * (float)a.k;
   float acc[VPL];
-  double zacc = 0.;
+  double bacc = 0., zacc = 0.;
 #pragma unroll
   for (int v = 0; v < VPL; ++v) {
     f[v] /= fden;
     acc[v] = 0.f;
   }
-  for (int t0 = sp.begin + wave * (NT * TPW); t0 < sp.end; t0 += BL_WAVES * NT * TPW) {
-    float l[NT][VPL];
-    bool counted[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int t = t0 + n * TPW + sub;
-      counted[n] = t < sp.end && (!a.mask || a.mask[t] != 0);
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const float *row = a.logits + (size_t)(t0 + n * TPW + sub) * E;
-      if constexpr (VEC) {
-#pragma unroll
-        for (int v = 0; v < VPL; v += 4) {
-          f32x4 q = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          if (counted[n] && expert(v) < E) q = *reinterpret_cast<const f32x4 *>(row + expert(v));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) l[n][v + i] = q[i];
-        }
-      } else {
-#pragma unroll
-        for (int v = 0; v < VPL; ++v) l[n][v] = counted[n] && expert(v) < E ? row[expert(v)] : -INFINITY;
-      }
-    }
+  for (int t0 = t_first; t0 < sp.end; t0 += BL_WAVES * NT * TPW) {
+    if (t0 != t_first) load(t0);
     float base[NT], sum[NT], dot[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float m = l[n][0];
+      float m = -INFINITY;
 #pragma unroll
-      for (int v = 1; v < VPL; ++v) m = fmaxf(m, l[n][v]);
+      for (int v = 0; v < VPL; ++v) {
+        l[n][v] = counted[n] ? l[n][v] : -INFINITY;
+        m = fmaxf(m, l[n][v]);
+      }
       m = group_reduce<LPT>(m, [](float x, float y) { return fmaxf(x, y); });
       // a row without any finite logit (or an uncounted one) has sum 0: no probabilities
       base[n] = m == -INFINITY ? 0.f : m;
@@ -371,8 +377,14 @@ __global__ __launch_bounds__(BL_THREADS) void balance_main_kernel(BalanceArgs a)
       const int t = t0 + n * TPW + sub;
       const float inv = sum[n] == 0.f ? 0.f : 1.f / sum[n];
       const float z = sum[n] == 0.f ? 0.f : base[n] + __logf(sum[n]);
-      const float shift = ca * (dot[n] * inv) - cb * z;
-      if constexpr (LOSS) zacc += li == 0 ? (double)z * (double)z : 0.;
+      const float mean_f = dot[n] * inv;  // sum_i f_i p_i
+      const float shift = ca * mean_f - cb * z;
+      if constexpr (LOSS) {
+        if (li == 0) {
+          bacc += (double)mean_f;
+          zacc += (double)z * (double)z;
+        }
+      }
 #pragma unroll
       for (int v = 0; v < VPL; ++v) {
         l[n][v] *= inv;
@@ -404,102 +416,74 @@ __global__ __launch_bounds__(BL_THREADS) void balance_main_kernel(BalanceArgs a)
       for (int o = LPT; o < 64; o <<= 1) acc[v] += __shfl_xor(acc[v], o, 64);
       if (sub == 0 && expert(v) < E) s_acc[wave * E + expert(v)] = acc[v];
     }
-    double unused = 0;
-    block_sum2<BL_WAVES>(zacc, unused, s_red);  // synchronises: the column sums are visible after it
-    if (!a.one) {
-      if (threadIdx.x == 0) a.zpart[blockIdx.x] = zacc;
-      float *out = a.part + (size_t)blockIdx.x * E;
-      for (int e = threadIdx.x; e < E; e += BL_THREADS) {
-        float p = 0;
-#pragma unroll
-        for (int w = 0; w < BL_WAVES; ++w) p += s_acc[w * E + e];
-        out[e] = p;
-      }
-      return;
-    }
-    double bal = 0;
+    block_sum2<BL_WAVES>(bacc, zacc, s_red);  // synchronises: the column sums are visible after it
+    const float per = a.one ? 1.f / (float)max(ns, 1) : 1.f;
+    float *out = a.one ? a.mean_probs : a.part + (size_t)blockIdx.x * E;
     for (int e = threadIdx.x; e < E; e += BL_THREADS) {
-      double p = 0;
+      float p = 0;
+#pragma unroll
       for (int w = 0; w < BL_WAVES; ++w) p += s_acc[w * E + e];
-      p = ns > 0 ? p / ns : 0.0;
-      a.mean_probs[e] = (float)p;
-      bal += p * ((double)a.counts[e] / ((double)max(ns, 1) * a.k));
+      out[e] = p * per;
     }
-    block_sum2<BL_WAVES>(bal, unused, s_red);
     if (threadIdx.x == 0) {
-      a.losses[0] = (float)((double)a.alpha * E * bal);
-      a.losses[1] = (float)((double)a.beta * zacc / max(ns, 1));
+      bacc /= max(ns, 1);
+      if (a.one) {
+        a.losses[0] = (float)((double)a.alpha * E * bacc);
+        a.losses[1] = (float)((double)a.beta * zacc / max(ns, 1));
+      } else {
+        a.sums[2 * (size_t)blockIdx.x] = bacc;
+        a.sums[2 * (size_t)blockIdx.x + 1] = zacc;
+      }
     }
   }
 }
 
 // ---------------------------------------------------------------------------------- finish
 
-constexpr int BL_FIN_THREADS = 1024, BL_FIN_WAVES = BL_FIN_THREADS / 64;
+constexpr int BL_FIN_THREADS = 512, BL_FIN_WAVES = BL_FIN_THREADS / 64;
 
-// One block a sequence: its mean probabilities and its terms of the losses, in 64 bits; the
-// block that finishes last adds the sequences' terms in order.  `cols` threads (a power of
-// two) stand on neighbouring experts, the others on further blocks of the main pass.
+// Block s < S * parts: `cols` (a power of two) of a sequence's mean probabilities, threads on
+// neighbouring experts and on further blocks of the main pass.  The last block: the two
+// losses, since sum_i f_si P_si is the mean over the sequence's tokens of sum_i f_si p_ti.
 __global__ __launch_bounds__(BL_FIN_THREADS) void balance_finish_kernel(
-    const float *__restrict__ part, const double *__restrict__ zpart, const int32_t *__restrict__ first_main,
-    const int32_t *__restrict__ counts, const int32_t *__restrict__ seq_tokens, int E, int k, int S, int cols,
-    float alpha, float beta, float *__restrict__ mean_probs, double *terms, uint32_t *ticket,
-    float *__restrict__ losses) {
+    const float *__restrict__ part, const double *__restrict__ sums, const int32_t *__restrict__ first_main,
+    const int32_t *__restrict__ seq_tokens, int E, int S, int cols, int parts, float alpha, float beta,
+    float *__restrict__ mean_probs, float *__restrict__ losses) {
   __shared__ double s_p[BL_FIN_THREADS];
   __shared__ double s_red[BL_FIN_WAVES][2];
-  __shared__ int s_last;
-  const int s = blockIdx.x;
-  const int b0 = first_main[s], b1 = first_main[s + 1], n = seq_tokens[s];
-  const int col = threadIdx.x & (cols - 1), row = threadIdx.x / cols, rows = BL_FIN_THREADS / cols;
-  double bal = 0, z = 0;
-  for (int e0 = 0; e0 < E; e0 += cols) {
-    const int e = e0 + col;
-    double p = 0;
-    if (e < E) {
-#pragma unroll 8
-      for (int b = b0 + row; b < b1; b += rows) p += part[(size_t)b * E + e];
+  if (blockIdx.x == (unsigned)(S * parts)) {
+    double bal = 0, z = 0, live = 0, all = 0;
+    const int nb = first_main[S];
+    for (int b = threadIdx.x; b < nb; b += BL_FIN_THREADS) {
+      bal += sums[2 * (size_t)b];
+      z += sums[2 * (size_t)b + 1];
     }
-    s_p[threadIdx.x] = p;
-    __syncthreads();
-    if (row == 0 && e < E) {
-      for (int r = 1; r < rows; ++r) p += s_p[r * cols + col];
-      p = n > 0 ? p / n : 0.0;
-      mean_probs[(size_t)s * E + e] = (float)p;
-      bal += p * ((double)counts[(size_t)s * E + e] / ((double)max(n, 1) * k));
+    for (int q = threadIdx.x; q < S; q += BL_FIN_THREADS) {
+      live += seq_tokens[q] > 0;
+      all += seq_tokens[q];
     }
-    __syncthreads();
-  }
-  for (int b = b0 + (int)threadIdx.x; b < b1; b += BL_FIN_THREADS) z += zpart[b];
-  block_sum2<BL_FIN_WAVES>(bal, z, s_red);
-  if (S == 1) {
+    block_sum2<BL_FIN_WAVES>(bal, z, s_red);
+    if (S > 1) block_sum2<BL_FIN_WAVES>(live, all, s_red);
     if (threadIdx.x == 0) {
-      losses[0] = (float)((double)alpha * E * bal);
-      losses[1] = (float)((double)beta * z / max(n, 1));
+      losses[0] = (float)((double)alpha * E * bal / max(S > 1 ? live : 1.0, 1.0));
+      losses[1] = (float)((double)beta * z / max(all, 1.0));
     }
     return;
   }
-  if (threadIdx.x == 0) {
-    __hip_atomic_store(&terms[2 * s], bal, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __hip_atomic_store(&terms[2 * s + 1], z, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __threadfence();
-    s_last = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)S - 1;
+  const int s = blockIdx.x / parts;
+  const int b0 = first_main[s], b1 = first_main[s + 1], n = seq_tokens[s];
+  const int col = threadIdx.x & (cols - 1), row = threadIdx.x / cols, rows = BL_FIN_THREADS / cols;
+  const int e = (blockIdx.x - s * parts) * cols + col;
+  double p = 0;
+  if (e < E) {
+#pragma unroll 8
+    for (int b = b0 + row; b < b1; b += rows) p += part[(size_t)b * E + e];
   }
+  s_p[threadIdx.x] = p;
   __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  double live = 0, all = 0;
-  bal = z = 0;
-  for (int q = threadIdx.x; q < S; q += BL_FIN_THREADS) {
-    bal += __hip_atomic_load(&terms[2 * q], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    z += __hip_atomic_load(&terms[2 * q + 1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    live += seq_tokens[q] > 0;
-    all += seq_tokens[q];
-  }
-  block_sum2<BL_FIN_WAVES>(bal, z, s_red);
-  block_sum2<BL_FIN_WAVES>(live, all, s_red);
-  if (threadIdx.x == 0) {
-    losses[0] = (float)((double)alpha * E * bal / max(live, 1.0));
-    losses[1] = (float)((double)beta * z / max(all, 1.0));
+  if (row == 0 && e < E) {
+    for (int r = 1; r < rows; ++r) p += s_p[r * cols + col];
+    mean_probs[(size_t)s * E + e] = (float)(p / max(n, 1));
   }
 }
 
@@ -512,16 +496,16 @@ int lanes_per_token(int E) {
 
 int count_chunk(int T) { return std::max(256, (T + 255) / 256); }
 // Tokens of a block of the main pass: one round of its wavefronts at least.
-int main_chunk(int T, int E) {
-  const int tpw = 64 / lanes_per_token(E), nt = E <= 256 ? 4 : E <= 512 ? 2 : 1;
-  return std::max(BL_WAVES * tpw * nt, (T + 511) / 512);
+int main_chunk(int T, int E, bool loss) {
+  const int tpw = 64 / lanes_per_token(E), nt = E <= 256 ? 4 : E <= 512 ? 2 : 1, blocks = loss ? 512 : 2048;
+  return std::max(BL_WAVES * tpw * nt, (T + blocks - 1) / blocks);
 }
 
 // Chunks of the two passes: sequences cut into whole chunks, at most one partial chunk each,
 // and in the main pass one block more for the rows outside every sequence.
 int count_blocks(int T, int S, bool off) { return (T + count_chunk(T) - 1) / count_chunk(T) + (off ? S : 0); }
-int main_blocks(int T, int E, int S, bool off) {
-  return (T + main_chunk(T, E) - 1) / main_chunk(T, E) + (off ? S + 1 : 0);
+int main_blocks(int T, int E, int S, bool off, bool loss) {
+  return (T + main_chunk(T, E, loss) - 1) / main_chunk(T, E, loss) + (off ? S + 1 : 0);
 }
 
 int bin_copies(int E) {
@@ -567,18 +551,16 @@ hipError_t launch_main(const BalanceArgs &a, int blocks, hipStream_t s) {
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 struct BalanceWs {
-  size_t count_part, main_part, z_part, first_main, terms, ticket, total;
+  size_t count_part, main_part, sums, first_main, total;
 };
 BalanceWs balance_ws(int T, int E, int S) {
   BalanceWs w;
-  const size_t cb = count_blocks(T, S, true), mb = main_blocks(T, E, S, true);
+  const size_t cb = count_blocks(T, S, true), mb = main_blocks(T, E, S, true, true);
   w.count_part = 0;
   w.main_part = align256(cb * (E + 1) * 4);
-  w.z_part = w.main_part + align256(mb * E * 4);
-  w.first_main = w.z_part + align256(mb * 8);
-  w.terms = w.first_main + align256(((size_t)S + 1) * 4);
-  w.ticket = w.terms + align256((size_t)S * 16);
-  w.total = w.ticket + 256;
+  w.sums = w.main_part + align256(mb * E * 4);
+  w.first_main = w.sums + align256(mb * 16);
+  w.total = w.first_main + align256(((size_t)S + 1) * 4);
   return w;
 }
 
@@ -596,8 +578,8 @@ hipError_t launch_balance_loss(const BalanceCall &c, int32_t *counts, int32_t *s
   uint8_t *base = static_cast<uint8_t *>(ws);
   int32_t *cpart = reinterpret_cast<int32_t *>(base + w.count_part);
   const bool off = c.off != nullptr;
-  const int cc = count_chunk(c.T), mc = main_chunk(c.T, c.E);
-  const int cb = count_blocks(c.T, c.S, off), mb = main_blocks(c.T, c.E, c.S, off);
+  const int cc = count_chunk(c.T), mc = main_chunk(c.T, c.E, true);
+  const int cb = count_blocks(c.T, c.S, off), mb = main_blocks(c.T, c.E, c.S, off, true);
   const int copies = bin_copies(c.E);
   BalanceArgs a{};
   a.logits = c.logits;
@@ -608,9 +590,8 @@ hipError_t launch_balance_loss(const BalanceCall &c, int32_t *counts, int32_t *s
   a.dloss = c.dloss;
   a.dlogits = c.dlogits;
   a.part = reinterpret_cast<float *>(base + w.main_part);
-  a.zpart = reinterpret_cast<double *>(base + w.z_part);
+  a.sums = reinterpret_cast<double *>(base + w.sums);
   a.first_main = reinterpret_cast<int32_t *>(base + w.first_main);
-  a.ticket = reinterpret_cast<uint32_t *>(base + w.ticket);
   a.mean_probs = mean_probs;
   a.losses = losses;
   a.T = c.T;
@@ -635,10 +616,10 @@ hipError_t launch_balance_loss(const BalanceCall &c, int32_t *counts, int32_t *s
   }
   if ((e = launch_main<true>(a, mb, s)) != hipSuccess || a.one) return e;
   int cols = 1;
-  while (cols < BL_FIN_THREADS && cols < c.E) cols *= 2;
-  hipLaunchKernelGGL(balance_finish_kernel, dim3((unsigned)c.S), dim3(BL_FIN_THREADS), 0, s, a.part, a.zpart,
-                     a.first_main, counts, seq_tokens, c.E, c.k, c.S, cols, c.alpha, c.beta, mean_probs,
-                     reinterpret_cast<double *>(base + w.terms), a.ticket, losses);
+  while (cols < 32 && cols < c.E) cols *= 2;
+  const int parts = (c.E + cols - 1) / cols;
+  hipLaunchKernelGGL(balance_finish_kernel, dim3((unsigned)(c.S * parts + 1)), dim3(BL_FIN_THREADS), 0, s, a.part,
+                     a.sums, a.first_main, seq_tokens, c.E, c.S, cols, parts, c.alpha, c.beta, mean_probs, losses);
   return hipGetLastError();
 }
 
@@ -656,10 +637,10 @@ hipError_t launch_balance_backward(const BalanceCall &c, const int32_t *counts, 
   a.E = c.E;
   a.k = c.k;
   a.S = c.S;
-  a.chunk = main_chunk(c.T, c.E);
+  a.chunk = main_chunk(c.T, c.E, false);
   a.alpha = c.alpha;
   a.beta = c.beta;
-  return launch_main<false>(a, main_blocks(c.T, c.E, c.S, c.off != nullptr), s);
+  return launch_main<false>(a, main_blocks(c.T, c.E, c.S, c.off != nullptr, false), s);
 }
 
 }  // namespace moe

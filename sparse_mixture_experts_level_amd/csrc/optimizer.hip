@@ -32,41 +32,152 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int64_t kMaxBlocks = 1 << 23;  // blocks a launch: below 2^32 threads
 
+// Index of the block's tensor: the last of `count` whose first block is not past this one.
+__device__ __forceinline__ int find_tensor(const int32_t *first, int count) {
+  const int lane = threadIdx.x & 63;
+  int found = -1;
+  for (int c = 0; c < count; c += 64) {
+    const bool at = c + lane < count && first[c + lane] <= (int)blockIdx.x;
+    found += __popcll(__ballot(at));
+  }
+  return __builtin_amdgcn_readfirstlane(found);
+}
+
+// --------------------------------------------------------------------- groups of values
+
+// Four or eight neighbouring values of a tensor as floats; `p` points at them, 16-byte
+// aligned for floats and for eight bf16, 8-byte for four bf16.
+template <int N>
+struct Vals {
+  float v[N];
+};
+__device__ __forceinline__ f32x4 ld_f32x4(const float *p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(p));
+}
+__device__ __forceinline__ void st_f32x4(float *p, f32x4 v) {
+  __builtin_nontemporal_store(v, reinterpret_cast<f32x4 *>(p));
+}
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+template <int N>
+__device__ __forceinline__ Vals<N> load_vals(const float *p) {
+  Vals<N> r;
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    const f32x4 q = ld_f32x4(p + i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.v[i + j] = q[j];
+  }
+  return r;
+}
+template <int N>
+__device__ __forceinline__ Vals<N> load_vals(const bf16_t *p) {
+  Vals<N> r;
+  uint32_t w[N / 2];
+  if constexpr (N == 8) {
+    const u32x4 q = ldg16_nt(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = q[i];
+  } else {
+    const u32x2 q = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(p));
+    w[0] = q[0];
+    w[1] = q[1];
+  }
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    r.v[2 * i] = __uint_as_float(w[i] << 16);
+    r.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+  return r;
+}
+template <int N>
+__device__ __forceinline__ void store_vals(float *p, const Vals<N> &x) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) st_f32x4(p + i, f32x4{x.v[i], x.v[i + 1], x.v[i + 2], x.v[i + 3]});
+}
+template <int N>
+__device__ __forceinline__ void store_vals(bf16_t *p, const Vals<N> &x) {
+  uint32_t w[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) w[i] = pack_bf16x2(x.v[2 * i], x.v[2 * i + 1]);
+  if constexpr (N == 8)
+    stg16_nt(p, u32x4{w[0], w[1], w[2], w[3]});
+  else
+    __builtin_nontemporal_store(u32x2{w[0], w[1]}, reinterpret_cast<u32x2 *>(p));
+}
+// The first `n` of them (n < N).
+template <int N, typename T>
+__device__ __forceinline__ Vals<N> load_some(const T *p, int n) {
+  Vals<N> r;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    r.v[i] = 0.f;
+    if (i < n) {
+      if constexpr (sizeof(T) == 4)
+        r.v[i] = p[i];
+      else
+        r.v[i] = bf16_to_f32(p[i]);
+    }
+  }
+  return r;
+}
+template <int N, typename T>
+__device__ __forceinline__ void store_some(T *p, const Vals<N> &x, int n) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (i < n) store_out(p + i, x.v[i]);
+}
+template <int N, typename T>
+__device__ __forceinline__ Vals<N> load_n(const T *p, int n) {
+  return n >= N ? load_vals<N>(p) : load_some<N>(p, n);
+}
+template <int N, typename T>
+__device__ __forceinline__ void store_n(T *p, const Vals<N> &x, int n) {
+  if (n >= N)
+    store_vals<N>(p, x);
+  else
+    store_some<N>(p, x, n);
+}
+
 // ------------------------------------------------------------------------ gradient norm
 
-constexpr int kNormTensors = 64;
+constexpr int kNormTensors = 192;
 struct NormArgs {
-  NormTensor t[kNormTensors];
-  int32_t first[kNormTensors];  // first block of each tensor
+  const void *grad[kNormTensors];
+  int64_t n[kNormTensors];         // values, negative (~n): floats
+  int32_t first[kNormTensors];     // first block of each tensor
   int32_t count;
-  int32_t chunk;  // values a block
+  int32_t chunk;  // values a block, a multiple of 2048
   double *part;
 };
 
-__device__ __forceinline__ int find_tensor(const int32_t *first, int count) {
-  const int lane = threadIdx.x & 63;
-  const bool at = lane < count && first[lane] <= (int)blockIdx.x;
-  return __builtin_amdgcn_readfirstlane(__popcll(__ballot(at)) - 1);
+template <typename T>
+__device__ __forceinline__ double chunk_squares(const T *g, int64_t i0, int64_t i1) {
+  double sum = 0;
+  int64_t i = i0 + threadIdx.x * 8;
+#pragma unroll 4
+  for (; i + 8 <= i1; i += kThreads * 8) {
+    const Vals<8> x = load_vals<8>(g + i);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += (double)x.v[j] * (double)x.v[j];
+  }
+  if (i < i1) {
+    const Vals<8> x = load_some<8>(g + i, (int)(i1 - i));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += (double)x.v[j] * (double)x.v[j];
+  }
+  return sum;
 }
 
 // Sum of squares of one chunk, in 64 bits.
 __global__ __launch_bounds__(kThreads) void grad_norm_kernel(NormArgs a) {
   __shared__ double s_sum[kThreads / 64];
   const int ti = find_tensor(a.first, a.count);
-  const NormTensor t = a.t[ti];
+  const int64_t code = a.n[ti], n = code < 0 ? ~code : code;
   const int64_t i0 = (int64_t)(blockIdx.x - a.first[ti]) * a.chunk;
-  const int64_t i1 = min(t.n, i0 + a.chunk);
-  double sum = 0;
-  if (t.f32) {
-    const float *g = static_cast<const float *>(t.grad);
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) sum += (double)g[i] * (double)g[i];
-  } else {
-    const bf16_t *g = static_cast<const bf16_t *>(t.grad);
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) {
-      const double x = bf16_to_f32(g[i]);
-      sum += x * x;
-    }
-  }
+  const int64_t i1 = min(n, i0 + a.chunk);
+  double sum = code < 0 ? chunk_squares(static_cast<const float *>(a.grad[ti]), i0, i1)
+                        : chunk_squares(static_cast<const bf16_t *>(a.grad[ti]), i0, i1);
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
   if ((threadIdx.x & 63) == 0) s_sum[threadIdx.x >> 6] = sum;
@@ -78,6 +189,7 @@ __global__ __launch_bounds__(1024) void grad_norm_finish_kernel(const double *__
                                                                 float max_norm, float *__restrict__ out) {
   __shared__ double s_sum[16];
   double sum = 0;
+#pragma unroll 4
   for (int64_t i = threadIdx.x; i < n; i += 1024) sum += part[i];
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
@@ -103,7 +215,7 @@ int64_t norm_chunk(const NormTensor *t, int count) {
 
 // ---------------------------------------------------------------------------- AdamW step
 
-constexpr int kAdamTensors = 40;
+constexpr int kAdamTensors = 48;  // 3.9 KB of kernel arguments
 struct AdamArgs {
   AdamTensor t[kAdamTensors];
   int32_t first[kAdamTensors];
@@ -111,7 +223,9 @@ struct AdamArgs {
   int32_t pad;
   AdamScalars h;
   double log_beta1, log_beta2;
+  float step, inv_bc2;  // from the host's lr and t
 };
+static_assert(sizeof(AdamArgs) <= 4096 && sizeof(NormArgs) <= 4096, "kernel arguments");
 
 struct Rates {
   float step;      // lr / (1 - b1^t)
@@ -123,52 +237,113 @@ struct Rates {
 // False: a gradient scale that is not a number (the norm was not finite) leaves everything.
 __device__ __forceinline__ bool rates(const AdamArgs &a, float decay, Rates &r) {
   double lr = a.h.lr;
-  int64_t t = a.h.step;
-  if (a.h.lr_dev) lr = (double)*a.h.lr_dev;
-  if (a.h.step_dev) t = max(*a.h.step_dev, (int64_t)1);
-  r.step = (float)(lr / -expm1((double)t * a.log_beta1));
-  r.inv_bc2 = (float)(1.0 / sqrt(-expm1((double)t * a.log_beta2)));
+  r.step = a.step;
+  r.inv_bc2 = a.inv_bc2;
+  if (a.h.lr_dev || a.h.step_dev) {  // equal for the whole launch
+    __shared__ float s_rates[2];
+    if (a.h.lr_dev) lr = (double)*a.h.lr_dev;
+    if (threadIdx.x < 64) {  // some hundred instructions: for one wavefront
+      const int64_t t = a.h.step_dev ? max(*a.h.step_dev, (int64_t)1) : a.h.step;
+      s_rates[0] = (float)(lr / -expm1((double)t * a.log_beta1));
+      s_rates[1] = (float)(1.0 / sqrt(-expm1((double)t * a.log_beta2)));
+    }
+    __syncthreads();
+    r.step = s_rates[0];
+    r.inv_bc2 = s_rates[1];
+  }
   r.keep = (float)(1.0 - lr * (double)decay);
   r.gscale = a.h.grad_scale ? *a.h.grad_scale : 1.f;
   return r.gscale == r.gscale;
 }
 
-__device__ __forceinline__ float load_grad(const AdamTensor &t, int64_t i) {
-  return t.grad_f32 ? static_cast<const float *>(t.grad)[i] : bf16_to_f32(static_cast<const bf16_t *>(t.grad)[i]);
-}
-__device__ __forceinline__ float load_weight(const AdamTensor &t, int64_t i) {
-  if (t.master) return t.master[i];
-  return t.param_f32 ? static_cast<const float *>(t.param)[i] : bf16_to_f32(static_cast<const bf16_t *>(t.param)[i]);
-}
-__device__ __forceinline__ void store_weight(const AdamTensor &t, int64_t i, float w) {
-  if (t.master) t.master[i] = w;
-  if (t.param_f32)
-    static_cast<float *>(t.param)[i] = w;
-  else
-    static_cast<bf16_t *>(t.param)[i] = f32_to_bf16(w);
+// The weight after a step, from m' and the root of v' (hardware reciprocal: one in the last
+// place, as the root; the step is some percent of a weight at most).
+__device__ __forceinline__ float next_weight(float w, float m, float root, const Rates &r, float eps) {
+  const float u = m * __builtin_amdgcn_rcpf(root * r.inv_bc2 + eps);
+  return w * r.keep - r.step * u;
 }
 
 constexpr int kAdamChunk = 2048;  // values a block
+
+// States in 32 bits: four values a thread, twice.  G: gradients' type; P: parameters'; MASTER:
+// the float copy is read instead of the parameter.
+template <typename G, typename P, bool MASTER>
+__device__ __forceinline__ void adamw32(const AdamArgs &a, const AdamTensor &t, const Rates &r, int64_t i0) {
+  constexpr int U = kAdamChunk / (4 * kThreads);
+  const float b1 = (float)a.h.beta1, b2 = (float)a.h.beta2, c1 = (float)(1.0 - a.h.beta1),
+              c2 = (float)(1.0 - a.h.beta2), eps = (float)a.h.eps;
+  const G *pg = static_cast<const G *>(t.grad);
+  P *pp = static_cast<P *>(t.param);
+  float *pm = static_cast<float *>(t.m), *pv = static_cast<float *>(t.v);
+  auto run = [&](auto whole) {
+    Vals<4> g[U], m[U], v[U], w[U];
+    int n[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int64_t i = i0 + (k * kThreads + (int)threadIdx.x) * 4;
+      n[k] = whole ? 4 : (int)min(max(t.n - i, (int64_t)0), (int64_t)4);
+      if (n[k] == 0) continue;
+      g[k] = load_n<4>(pg + i, n[k]);
+      m[k] = load_n<4>(pm + i, n[k]);
+      v[k] = load_n<4>(pv + i, n[k]);
+      if constexpr (MASTER)
+        w[k] = load_n<4>(t.master + i, n[k]);
+      else
+        w[k] = load_n<4>(pp + i, n[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int64_t i = i0 + (k * kThreads + (int)threadIdx.x) * 4;
+      if (n[k] == 0) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float gs = g[k].v[j] * r.gscale;
+        m[k].v[j] = b1 * m[k].v[j] + c1 * gs;
+        v[k].v[j] = b2 * v[k].v[j] + c2 * (gs * gs);
+        w[k].v[j] = next_weight(w[k].v[j], m[k].v[j], sqrtf(v[k].v[j]), r, eps);
+      }
+      store_n<4>(pm + i, m[k], n[k]);
+      store_n<4>(pv + i, v[k], n[k]);
+      if constexpr (MASTER) store_n<4>(t.master + i, w[k], n[k]);
+      store_n<4>(pp + i, w[k], n[k]);
+    }
+  };
+  struct Yes { constexpr operator bool() const { return true; } };
+  struct No { constexpr operator bool() const { return false; } };
+  if (i0 + kAdamChunk <= t.n)
+    run(Yes{});
+  else
+    run(No{});
+}
+
+// The types are equal for a whole block, so one launch takes tensors of every kind.
+#define ADAM_BY_TYPE(F, ...)                                  \
+  do {                                                        \
+    if (t.master) {                                           \
+      if (t.grad_f32)                                         \
+        F<float, bf16_t, true>(__VA_ARGS__);                  \
+      else                                                    \
+        F<bf16_t, bf16_t, true>(__VA_ARGS__);                 \
+    } else if (t.param_f32) {                                 \
+      if (t.grad_f32)                                         \
+        F<float, float, false>(__VA_ARGS__);                  \
+      else                                                    \
+        F<bf16_t, float, false>(__VA_ARGS__);                 \
+    } else {                                                  \
+      if (t.grad_f32)                                         \
+        F<float, bf16_t, false>(__VA_ARGS__);                 \
+      else                                                    \
+        F<bf16_t, bf16_t, false>(__VA_ARGS__);                \
+    }                                                         \
+  } while (0)
 
 __global__ __launch_bounds__(kThreads) void adamw32_kernel(AdamArgs a) {
   const int ti = find_tensor(a.first, a.count);
   const AdamTensor t = a.t[ti];
   Rates r;
   if (!rates(a, t.decay, r)) return;
-  const float b1 = (float)a.h.beta1, b2 = (float)a.h.beta2, c1 = (float)(1.0 - a.h.beta1),
-              c2 = (float)(1.0 - a.h.beta2), eps = (float)a.h.eps;
   const int64_t i0 = (int64_t)(blockIdx.x - a.first[ti]) * kAdamChunk;
-  const int64_t i1 = min(t.n, i0 + kAdamChunk);
-  float *pm = static_cast<float *>(t.m), *pv = static_cast<float *>(t.v);
-  for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) {
-    const float g = load_grad(t, i) * r.gscale;
-    const float m = b1 * pm[i] + c1 * g;
-    const float v = b2 * pv[i] + c2 * (g * g);
-    pm[i] = m;
-    pv[i] = v;
-    const float u = m / (sqrtf(v) * r.inv_bc2 + eps);
-    store_weight(t, i, load_weight(t, i) * r.keep - r.step * u);
-  }
+  ADAM_BY_TYPE(adamw32, a, t, r, i0);
 }
 
 constexpr double kPerM = 1.0 / 16129.0, kPerV = 1.0 / 4228250625.0;  // 1 / 127^2, 1 / 255^4
@@ -176,41 +351,52 @@ constexpr double kPerM = 1.0 / 16129.0, kPerV = 1.0 / 4228250625.0;  // 1 / 127^
 // m' and v' in 64 bits from the values held, every operation rounded by itself.
 __device__ __forceinline__ double next_m(int code, double scale, double g, double b1, double c1) {
 #pragma clang fp contract(off)
-  const double old = (double)(code * abs(code)) * scale;
+  const float c = (float)code;
+  const double old = (double)(c * fabsf(c)) * scale;  // the square is exact in a float
   const double a = b1 * old, b = c1 * g;
   return a + b;
 }
 __device__ __forceinline__ double next_v(uint32_t code, double scale, double g, double b2, double c2) {
 #pragma clang fp contract(off)
-  const double old = (double)(code * code * (code * code)) * scale;
+  const float c = (float)code;
+  const double square = (double)(c * c);  // exact, and its own square in 64 bits too
+  const double old = (square * square) * scale;
   const double gg = g * g;
   const double a = b2 * old, b = c2 * gg;
   return a + b;
 }
 
-// The code whose square is nearest to u (u >= 0, at most top^2 and a little).
-__device__ __forceinline__ int nearest_root(double u, int top) {
-  int c = (int)(__builtin_amdgcn_sqrtf(fmaxf((float)u - 0.25f, 0.f)) + 0.5f);
-  c = min(c, top);
-  // the float's error can put c one off at a border; the border itself is exact in 64 bits
-  if (c > 0 && u < (double)(c * (c - 1)) + 0.5) --c;
-  if (c < top && u >= (double)(c * (c + 1)) + 0.5) ++c;
-  return c;
-}
-// The same with u given squared.
-__device__ __forceinline__ int nearest_fourth_root(double uu, int top) {
-  int c = (int)(__builtin_amdgcn_sqrtf(fmaxf(__builtin_amdgcn_sqrtf((float)uu) - 0.25f, 0.f)) + 0.5f);
-  c = min(c, top);
-  const double lo = (double)(c * (c - 1)) + 0.5, hi = (double)(c * (c + 1)) + 0.5;
-  if (c > 0 && uu < lo * lo) --c;
-  else if (c < top && uu >= hi * hi) ++c;
-  return c;
+// The code c <= top whose square is nearest to u, where uf is u as a float within `off` of
+// it, relative.  The float decides unless a border c (c - 1) + 1/2 or c (c + 1) + 1/2 is that
+// near; then border(x), which says in 64 bits whether u is at or past x, does.
+template <typename Border>
+__device__ __forceinline__ int nearest_root(float uf, float off, int top, Border border) {
+  float c = rintf(__builtin_amdgcn_sqrtf(fmaxf(uf - 0.25f, 0.f)));
+  c = fminf(c, (float)top);
+  const float inside = c - fabsf((uf - c * c) - 0.5f);  // distance from the nearer border
+  if (!(inside > off * uf)) {
+    // also where a root's last place put c one off, and for c = 0, whose lower border is none
+    const float lower = c * (c - 1.f) + 0.5f, upper = c * (c + 1.f) + 0.5f;
+    if (c > 0.f && !border((double)lower))
+      c -= 1.f;
+    else if (c < (float)top && border((double)upper))
+      c += 1.f;
+  }
+  return (int)c;
 }
 
-__device__ __forceinline__ uint32_t max32(uint32_t v) {  // over the 32 lanes of a half wavefront
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o, 64));
-  return v;
+// Largest of 32 neighbouring lanes' values, in every lane.
+template <int CTRL>
+__device__ __forceinline__ uint32_t lane_max(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false));
+}
+__device__ __forceinline__ uint32_t max32(uint32_t v) {
+  v = lane_max<0xb1>(v);   // lane ^ 1
+  v = lane_max<0x4e>(v);   // lane ^ 2
+  v = lane_max<0x141>(v);  // the halves of 8
+  v = lane_max<0x140>(v);  // the halves of 16
+  const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  return max((uint32_t)r[0], (uint32_t)r[1]);
 }
 
 // The scale held for a block whose largest magnitude has these bits: zero below the smallest
@@ -220,62 +406,122 @@ __device__ __forceinline__ float held_scale(uint32_t bits) {
   return bits < 0x00800000u ? 0.f : __uint_as_float(bits);
 }
 
-// Eight values a thread, 32 threads a block of 256 values.
-__global__ __launch_bounds__(kThreads) void adamw8_kernel(AdamArgs a) {
-  const int ti = find_tensor(a.first, a.count);
-  const AdamTensor t = a.t[ti];
-  Rates r;
-  if (!rates(a, t.decay, r)) return;
+// Codes of eight neighbouring values.
+struct Codes {
+  uint32_t w[2];
+  __device__ __forceinline__ uint32_t u(int j) const { return (w[j >> 2] >> (8 * (j & 3))) & 0xffu; }
+  __device__ __forceinline__ int s(int j) const { return (int)(w[j >> 2] << (24 - 8 * (j & 3))) >> 24; }
+};
+__device__ __forceinline__ Codes load_codes(const uint8_t *p, int n) {
+  Codes c{{0u, 0u}};
+  if (n >= 8) {
+    const u32x2 q = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(p));
+    c.w[0] = q[0];
+    c.w[1] = q[1];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) c.w[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
+  }
+  return c;
+}
+__device__ __forceinline__ void store_codes(uint8_t *p, const Codes &c, int n) {
+  if (n >= 8) {
+    __builtin_nontemporal_store(u32x2{c.w[0], c.w[1]}, reinterpret_cast<u32x2 *>(p));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) p[j] = (uint8_t)c.u(j);
+  }
+}
+
+// States in 8 bits: eight values a thread, 32 threads a block of 256 values.
+template <typename G, typename P, bool MASTER>
+__device__ __forceinline__ void adamw8(const AdamArgs &a, const AdamTensor &t, const Rates &r, int64_t i0) {
   const double b1 = a.h.beta1, b2 = a.h.beta2, c1 = 1.0 - b1, c2 = 1.0 - b2;
   const float eps = (float)a.h.eps;
-  const int64_t i = (int64_t)(blockIdx.x - a.first[ti]) * kAdamChunk + threadIdx.x * 8;
-  const int64_t q = i / kAdamBlock;
-  const bool any = i < t.n;
-  int8_t *pm = static_cast<int8_t *>(t.m);
-  uint8_t *pv = static_cast<uint8_t *>(t.v);
-  const bool blk = q * kAdamBlock < t.n;
-  const double sm = blk ? (double)t.m_scale[q] * kPerM : 0.0, sv = blk ? (double)t.v_scale[q] * kPerV : 0.0;
+  const int64_t i = i0 + threadIdx.x * 8, q = i / kAdamBlock;
+  const int n = (int)min(max(t.n - i, (int64_t)0), (int64_t)8);
+  uint8_t *pm = static_cast<uint8_t *>(t.m) + i, *pv = static_cast<uint8_t *>(t.v) + i;
+  P *pp = static_cast<P *>(t.param) + i;
+  Vals<8> g{}, w{};
+  Codes cm{{0u, 0u}}, cv{{0u, 0u}};
+  double sm = 0, sv = 0;
+  if (n > 0) {
+    g = load_n<8>(static_cast<const G *>(t.grad) + i, n);
+    cm = load_codes(pm, n);
+    cv = load_codes(pv, n);
+    if constexpr (MASTER)
+      w = load_n<8>(t.master + i, n);
+    else
+      w = load_n<8>(pp, n);
+    sm = (double)t.m_scale[q] * kPerM;
+    sv = (double)t.v_scale[q] * kPerV;
+  }
   double m[8], v[8];
   uint32_t bm = 0, bv = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    m[j] = v[j] = 0;
-    if (any && i + j < t.n) {
-      const double g = (double)load_grad(t, i + j) * (double)r.gscale;
-      const int cm = pm[i + j];
-      const uint32_t cv = pv[i + j];
-      m[j] = next_m(cm, sm, g, b1, c1);
-      v[j] = next_v(cv, sv, g, b2, c2);
+    const double gs = (double)g.v[j] * (double)r.gscale;
+    m[j] = next_m(cm.s(j), sm, gs, b1, c1);
+    v[j] = next_v(cv.u(j), sv, gs, b2, c2);
+    if (j < n) {
       bm = max(bm, __float_as_uint((float)m[j]) & 0x7fffffffu);
       bv = max(bv, __float_as_uint((float)v[j]) & 0x7fffffffu);
     }
   }
   const float hm = held_scale(max32(bm)), hv = held_scale(max32(bv));
-  if (!any) return;
+  if (n <= 0) return;
   if ((threadIdx.x & 31) == 0) {
     t.m_scale[q] = hm;
     t.v_scale[q] = hv;
   }
   const double im = hm > 0.f ? 16129.0 / (double)hm : 0.0, iv = hv > 0.f ? 4228250625.0 / (double)hv : 0.0;
+  // u as floats: |m'| im is off by three roundings (2^-24 each); for v' the root of v' (one
+  // in the last place, and half of v's rounding) times that of 1 / scale (the same) and 255^2
+  // by eight of them.  In blocks whose scale is near the smallest floats, where these factors
+  // would leave the floats' range, u itself is formed in 64 bits first.
+  const bool tiny_m = !(hm > 0x1p-90f), tiny_v = !(hv > 0x1p-90f);
+  const float imf = tiny_m ? 0.f : (float)im;
+  const float ivf = tiny_v ? 0.f : __builtin_amdgcn_sqrtf((float)(1.0 / (double)hv)) * 65025.f;
+  Codes nm{{0u, 0u}}, nv{{0u, 0u}};
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    if (i + j >= t.n) break;
     const float mf = (float)m[j], vf = (float)v[j];
-    const float u = mf / (sqrtf(vf) * r.inv_bc2 + eps);
-    store_weight(t, i + j, load_weight(t, i + j) * r.keep - r.step * u);
-    const int cm = hm > 0.f ? nearest_root(fabs(m[j]) * im, 127) : 0;
-    pm[i + j] = (int8_t)(m[j] < 0 ? -cm : cm);
-    int cv = hv > 0.f ? nearest_fourth_root(v[j] * iv, 255) : 0;
-    if (hv > 0.f && v[j] > 0) cv = max(cv, 1);
-    pv[i + j] = (uint8_t)cv;
+    float root = __builtin_amdgcn_sqrtf(vf);
+    if (vf < 0x1p-96f && vf > 0.f) root = sqrtf(vf);  // the instruction is not exact near the smallest floats
+    w.v[j] = next_weight(w.v[j], mf, root, r, eps);
+    float u = fabsf(mf) * imf;
+    if (tiny_m) u = (float)(fabs(m[j]) * im);
+    int c = nearest_root(u, 4e-7f, 127, [&](double x) { return fabs(m[j]) * im >= x; });
+    c = hm > 0.f ? (mf < 0.f ? -c : c) : 0;
+    nm.w[j >> 2] |= ((uint32_t)c & 0xffu) << (8 * (j & 3));
+    u = root * ivf;
+    if (tiny_v) u = __builtin_amdgcn_sqrtf((float)(v[j] * iv));
+    c = nearest_root(u, 6e-7f, 255, [&](double x) { return v[j] * iv >= x * x; });
+    c = hv > 0.f ? max(c, v[j] > 0 ? 1 : 0) : 0;
+    nv.w[j >> 2] |= (uint32_t)c << (8 * (j & 3));
   }
+  if constexpr (MASTER) store_n<8>(t.master + i, w, n);
+  store_n<8>(pp, w, n);
+  store_codes(pm, nm, n);
+  store_codes(pv, nv, n);
 }
+
+__global__ __launch_bounds__(kThreads) void adamw8_kernel(AdamArgs a) {
+  const int ti = find_tensor(a.first, a.count);
+  const AdamTensor t = a.t[ti];
+  Rates r;
+  if (!rates(a, t.decay, r)) return;
+  const int64_t i0 = (int64_t)(blockIdx.x - a.first[ti]) * kAdamChunk;
+  ADAM_BY_TYPE(adamw8, a, t, r, i0);
+}
+#undef ADAM_BY_TYPE
 
 // ------------------------------------------------------------- 8-bit states read as floats
 
 struct ReadTensor {
-  const int8_t *m;
-  const uint8_t *v;
+  const uint8_t *m, *v;
   const float *m_scale, *v_scale;
   float *m_out, *v_out;
   int64_t n;
@@ -285,21 +531,48 @@ struct ReadArgs {
   int32_t first[kAdamTensors];
   int32_t count;
 };
+static_assert(sizeof(ReadArgs) <= 4096, "kernel arguments");
 
+// Four values a thread, twice.
 __global__ __launch_bounds__(kThreads) void adamw_read_kernel(ReadArgs a) {
   const int ti = find_tensor(a.first, a.count);
   const ReadTensor t = a.t[ti];
   const int64_t i0 = (int64_t)(blockIdx.x - a.first[ti]) * kAdamChunk;
-  const int64_t i1 = min(t.n, i0 + kAdamChunk);
-  for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) {
-    const int64_t q = i / kAdamBlock;
+#pragma unroll
+  for (int k = 0; k < kAdamChunk / (4 * kThreads); ++k) {
+    const int64_t i = i0 + (k * kThreads + (int)threadIdx.x) * 4, q = i / kAdamBlock;
+    const int n = (int)min(max(t.n - i, (int64_t)0), (int64_t)4);
+    if (n == 0) continue;
+    auto codes = [&](const uint8_t *p) {
+      uint32_t w = 0;
+      if (n == 4) return __builtin_nontemporal_load(reinterpret_cast<const uint32_t *>(p + i));
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < n) w |= (uint32_t)p[i + j] << (8 * j);
+      return w;
+    };
     if (t.m_out) {
-      const int c = t.m[i];
-      t.m_out[i] = (float)((double)(c * abs(c)) * ((double)t.m_scale[q] * kPerM));
+      const uint32_t w = codes(t.m);
+      const double scale = (double)t.m_scale[q] * kPerM;
+      Vals<4> x;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float c = (float)((int)(w << (24 - 8 * j)) >> 24);
+        x.v[j] = (float)((double)(c * fabsf(c)) * scale);
+      }
+      store_n<4>(t.m_out + i, x, n);
     }
     if (t.v_out) {
-      const uint32_t c = t.v[i];
-      t.v_out[i] = (float)((double)(c * c * (c * c)) * ((double)t.v_scale[q] * kPerV));
+      const uint32_t w = codes(t.v);
+      const double scale = (double)t.v_scale[q] * kPerV;
+      Vals<4> x;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float c = (float)((w >> (8 * j)) & 0xffu);
+        const double square = (double)(c * c);
+        x.v[j] = (float)((square * square) * scale);
+      }
+      store_n<4>(t.v_out + i, x, n);
     }
   }
 }
@@ -334,7 +607,8 @@ hipError_t launch_grad_norm(const NormTensor *t, int count, float max_norm, floa
       const hipError_t e = flush();
       if (e != hipSuccess) return e;
     }
-    a.t[a.count] = t[i];
+    a.grad[a.count] = t[i].grad;
+    a.n[a.count] = t[i].f32 ? ~t[i].n : t[i].n;
     a.first[a.count++] = (int32_t)blocks;
     blocks += nb;
   }
@@ -349,6 +623,8 @@ hipError_t launch_adamw(const AdamTensor *t, int count, const AdamScalars &h, hi
   a.h = h;
   a.log_beta1 = std::log(h.beta1);
   a.log_beta2 = std::log(h.beta2);
+  a.step = (float)(h.lr / (1.0 - std::pow(h.beta1, (double)h.step)));
+  a.inv_bc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(h.beta2, (double)h.step)));
   for (int eight = 0; eight < 2; ++eight) {
     int64_t blocks = 0;
     a.count = 0;
@@ -397,7 +673,7 @@ hipError_t launch_adamw_read(const AdamTensor *t, int count, float *const *m_out
       const hipError_t e = flush();
       if (e != hipSuccess) return e;
     }
-    a.t[a.count] = ReadTensor{static_cast<const int8_t *>(t[i].m), static_cast<const uint8_t *>(t[i].v),
+    a.t[a.count] = ReadTensor{static_cast<const uint8_t *>(t[i].m), static_cast<const uint8_t *>(t[i].v),
                               t[i].m_scale, t[i].v_scale, mo, vo, t[i].n};
     a.first[a.count++] = (int32_t)blocks;
     blocks += nb;
