@@ -366,23 +366,26 @@ __device__ __forceinline__ double next_v(uint32_t code, double scale, double g, 
   return a + b;
 }
 
-// The code c <= top whose square is nearest to u, where uf is u as a float within `off` of
-// it, relative.  The float decides unless a border c (c - 1) + 1/2 or c (c + 1) + 1/2 is that
-// near; then border(x), which says in 64 bits whether u is at or past x, does.
-template <typename Border>
-__device__ __forceinline__ int nearest_root(float uf, float off, int top, Border border) {
-  float c = rintf(__builtin_amdgcn_sqrtf(fmaxf(uf - 0.25f, 0.f)));
-  c = fminf(c, (float)top);
-  const float inside = c - fabsf((uf - c * c) - 0.5f);  // distance from the nearer border
-  if (!(inside > off * uf)) {
-    // also where a root's last place put c one off, and for c = 0, whose lower border is none
-    const float lower = c * (c - 1.f) + 0.5f, upper = c * (c + 1.f) + 0.5f;
-    if (c > 0.f && !border((double)lower))
-      c -= 1.f;
-    else if (c < (float)top && border((double)upper))
-      c += 1.f;
-  }
-  return (int)c;
+// The code whose square is nearest to u, from u as a float within `off` of it, relative: the
+// c with c (c - 1) + 1/2 <= u < c (c + 1) + 1/2.  `sure` is cleared where a border is that
+// near, and 64 bits have to decide.
+__device__ __forceinline__ float nearest_root(float u, float off, bool &sure) {
+  const float c = rintf(__builtin_amdgcn_sqrtf(fabsf(u - 0.25f)));
+  // distance from the nearer border; code 0 has none below it
+  const float inside = fmaxf(c - fabsf((u - c * c) - 0.5f), 0.4f - u);
+  sure = sure && inside > off * u;
+  return c;
+}
+// The same from u in 64 bits, `at(x)` saying whether it is at or past the border x (u itself
+// may be held squared there).
+template <typename At>
+__device__ __forceinline__ int nearest_root_64(float u, int top, At at) {
+  int c = min((int)rintf(__builtin_amdgcn_sqrtf(fabsf(u - 0.25f))), top);
+  if (c > 0 && !at((double)(c * (c - 1)) + 0.5))
+    --c;
+  else if (c < top && at((double)(c * (c + 1)) + 0.5))
+    ++c;
+  return c;
 }
 
 // Largest of 32 neighbouring lanes' values, in every lane.
@@ -410,6 +413,7 @@ __device__ __forceinline__ float held_scale(uint32_t bits) {
 struct Codes {
   uint32_t w[2];
   __device__ __forceinline__ uint32_t u(int j) const { return (w[j >> 2] >> (8 * (j & 3))) & 0xffu; }
+  __device__ __forceinline__ void put(int j, int c) { w[j >> 2] |= ((uint32_t)c & 0xffu) << (8 * (j & 3)); }
   __device__ __forceinline__ int s(int j) const { return (int)(w[j >> 2] << (24 - 8 * (j & 3))) >> 24; }
 };
 __device__ __forceinline__ Codes load_codes(const uint8_t *p, int n) {
@@ -458,6 +462,7 @@ __device__ __forceinline__ void adamw8(const AdamArgs &a, const AdamTensor &t, c
     sm = (double)t.m_scale[q] * kPerM;
     sv = (double)t.v_scale[q] * kPerV;
   }
+  // (values past the tensor's end stay zero here)
   double m[8], v[8];
   uint32_t bm = 0, bv = 0;
 #pragma unroll
@@ -465,10 +470,8 @@ __device__ __forceinline__ void adamw8(const AdamArgs &a, const AdamTensor &t, c
     const double gs = (double)g.v[j] * (double)r.gscale;
     m[j] = next_m(cm.s(j), sm, gs, b1, c1);
     v[j] = next_v(cv.u(j), sv, gs, b2, c2);
-    if (j < n) {
-      bm = max(bm, __float_as_uint((float)m[j]) & 0x7fffffffu);
-      bv = max(bv, __float_as_uint((float)v[j]) & 0x7fffffffu);
-    }
+    bm = max(bm, __float_as_uint((float)m[j]) & 0x7fffffffu);
+    bv = max(bv, __float_as_uint((float)v[j]) & 0x7fffffffu);
   }
   const float hm = held_scale(max32(bm)), hv = held_scale(max32(bv));
   if (n <= 0) return;
@@ -476,31 +479,50 @@ __device__ __forceinline__ void adamw8(const AdamArgs &a, const AdamTensor &t, c
     t.m_scale[q] = hm;
     t.v_scale[q] = hv;
   }
-  const double im = hm > 0.f ? 16129.0 / (double)hm : 0.0, iv = hv > 0.f ? 4228250625.0 / (double)hv : 0.0;
-  // u as floats: |m'| im is off by three roundings (2^-24 each); for v' the root of v' (one
-  // in the last place, and half of v's rounding) times that of 1 / scale (the same) and 255^2
-  // by eight of them.  In blocks whose scale is near the smallest floats, where these factors
-  // would leave the floats' range, u itself is formed in 64 bits first.
-  const bool tiny_m = !(hm > 0x1p-90f), tiny_v = !(hv > 0x1p-90f);
-  const float imf = tiny_m ? 0.f : (float)im;
-  const float ivf = tiny_v ? 0.f : __builtin_amdgcn_sqrtf((float)(1.0 / (double)hv)) * 65025.f;
+  // Roots are taken of v' times 2^64 in blocks below one, so that the smallest floats, which
+  // the instruction takes for zeros, do not come up.
+  const bool small = hv < 1.f;
+  const double up = small ? 0x1p64 : 1.0;
+  Rates rr = r;
+  rr.inv_bc2 = small ? r.inv_bc2 * 0x1p-32f : r.inv_bc2;
+  // u as floats.  |m'| 127^2 / scale: the reciprocal (one in the last place), two products and
+  // m' rounded, at most 3e-7; for v' the root of v' times 255^2 over the root of scale: two
+  // instructions of one in the last place, two products and half of v's rounding, at most
+  // 4e-7.  A scale of m so small that its reciprocal leaves the floats is for 64 bits.
+  const bool none_m = !(hm > 0.f), none_v = !(hv > 0.f);  // zero or NaN: codes of zero
+  const float imf = none_m ? 0.f : 16129.f * __builtin_amdgcn_rcpf(hm);
+  const float ivf = none_v ? 0.f : 65025.f * __builtin_amdgcn_rsqf(hv) * (small ? 0x1p-32f : 1.f);
+  bool sure_m = none_m || hm > 0x1p-90f, sure_v = true;
   Codes nm{{0u, 0u}}, nv{{0u, 0u}};
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float mf = (float)m[j], vf = (float)v[j];
-    float root = __builtin_amdgcn_sqrtf(vf);
-    if (vf < 0x1p-96f && vf > 0.f) root = sqrtf(vf);  // the instruction is not exact near the smallest floats
-    w.v[j] = next_weight(w.v[j], mf, root, r, eps);
-    float u = fabsf(mf) * imf;
-    if (tiny_m) u = (float)(fabs(m[j]) * im);
-    int c = nearest_root(u, 4e-7f, 127, [&](double x) { return fabs(m[j]) * im >= x; });
-    c = hm > 0.f ? (mf < 0.f ? -c : c) : 0;
-    nm.w[j >> 2] |= ((uint32_t)c & 0xffu) << (8 * (j & 3));
-    u = root * ivf;
-    if (tiny_v) u = __builtin_amdgcn_sqrtf((float)(v[j] * iv));
-    c = nearest_root(u, 6e-7f, 255, [&](double x) { return v[j] * iv >= x * x; });
-    c = hv > 0.f ? max(c, v[j] > 0 ? 1 : 0) : 0;
-    nv.w[j >> 2] |= (uint32_t)c << (8 * (j & 3));
+    const float mf = (float)m[j], root = __builtin_amdgcn_sqrtf((float)(v[j] * up));
+    w.v[j] = next_weight(w.v[j], mf, root, rr, eps);
+    nm.put(j, (int)copysignf(nearest_root(fabsf(mf) * imf, 4e-7f, sure_m), mf));
+    const float c = nearest_root(root * ivf, 6e-7f, sure_v);
+    nv.put(j, (int)fmaxf(c, v[j] > 0 ? 1.f : 0.f));
+  }
+  if (none_m) nm = Codes{{0u, 0u}};
+  if (none_v) nv = Codes{{0u, 0u}};
+  if (!sure_m && !none_m) {
+    const double im = 16129.0 / (double)hm;
+    nm = Codes{{0u, 0u}};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const double u = fabs(m[j]) * im;
+      const int c = nearest_root_64((float)u, 127, [&](double x) { return u >= x; });
+      nm.put(j, m[j] < 0 ? -c : c);
+    }
+  }
+  if (!sure_v && !none_v) {
+    const double iv = 4228250625.0 / (double)hv;
+    nv = Codes{{0u, 0u}};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const double uu = v[j] * iv;
+      const int c = nearest_root_64(__builtin_amdgcn_sqrtf((float)uu), 255, [&](double x) { return uu >= x * x; });
+      nv.put(j, max(c, v[j] > 0 ? 1 : 0));
+    }
   }
   if constexpr (MASTER) store_n<8>(t.master + i, w, n);
   store_n<8>(pp, w, n);
