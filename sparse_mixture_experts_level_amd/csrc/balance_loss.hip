@@ -20,7 +20,7 @@ namespace moe {
 namespace {
 
 constexpr int BL_COUNT_THREADS = 1024;
-constexpr int BL_WAVES = 8, BL_THREADS = 64 * BL_WAVES;  // main pass
+constexpr int BL_WAVES = 4, BL_THREADS = 64 * BL_WAVES;  // main pass
 constexpr int BL_BINS = 4096;                            // LDS bins of a block that counts
 
 struct Span {
@@ -81,11 +81,39 @@ __device__ __forceinline__ Span find_span(const int32_t *off, int S, int T, int 
   return r;
 }
 
+// Reductions over groups of LPT neighbouring lanes, the result in every lane: lane moves
+// within a row of 16 (lane ^ 1, lane ^ 2, then half-row and row mirrors, which pair equal
+// values), then rows and halves of the wavefront exchanged.  T: a 32-bit type.
+template <int CTRL, typename T>
+__device__ __forceinline__ T lane_move(T v) {
+  return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
+}
+template <int LPT, typename T, typename Op>
+__device__ __forceinline__ T group_reduce(T v, Op op) {
+  if constexpr (LPT >= 2) v = op(v, lane_move<0xb1>(v));
+  if constexpr (LPT >= 4) v = op(v, lane_move<0x4e>(v));
+  if constexpr (LPT >= 8) v = op(v, lane_move<0x141>(v));
+  if constexpr (LPT >= 16) v = op(v, lane_move<0x140>(v));
+  if constexpr (LPT >= 32) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    v = op(__builtin_bit_cast(T, (uint32_t)r[0]), __builtin_bit_cast(T, (uint32_t)r[1]));
+  }
+  if constexpr (LPT >= 64) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    v = op(__builtin_bit_cast(T, (uint32_t)r[0]), __builtin_bit_cast(T, (uint32_t)r[1]));
+  }
+  return v;
+}
+constexpr auto add = [](auto x, auto y) { return x + y; };
+
 // Sum of each value over the block's threads, returned to thread 0 (s_red: two doubles a wave).
-template <int WAVES>
+// STEP: only lanes that are multiples of it hold anything.
+template <int WAVES, int STEP = 1>
 __device__ __forceinline__ void block_sum2(double &x, double &y, double (*s_red)[2]) {
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) {
+  for (int o = 32; o >= STEP; o >>= 1) {
     x += __shfl_xor(x, o, 64);
     y += __shfl_xor(y, o, 64);
   }
@@ -118,21 +146,29 @@ __device__ __forceinline__ void count_chunk_lds(int32_t *bins, int copies, const
   const int32_t *src = ids + (size_t)begin * k;
   const uint32_t n = (uint32_t)(end - begin) * (uint32_t)k;
   int tokens = 0;
-  if (mask) {
-    for (uint32_t i = threadIdx.x; i < n; i += THREADS) {
-      const int e = src[i];
-      if (mask[begin + i / (uint32_t)k] != 0 && e >= 0 && e < E) atomicAdd(&mine[e], 1);
-    }
-    for (int t = begin + (int)threadIdx.x; t < end; t += THREADS) tokens += mask[t] != 0;
-  } else {
-    for (uint32_t i = threadIdx.x; i < n; i += THREADS) {
-      const int e = src[i];
-      if (e >= 0 && e < E) atomicAdd(&mine[e], 1);
-    }
-    if (threadIdx.x == 0) tokens = end - begin;
-  }
+  constexpr int B = 8;  // loads in flight
+  for (uint32_t i0 = threadIdx.x; i0 < n; i0 += B * THREADS) {
+    int e[B];
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) tokens += __shfl_xor(tokens, o, 64);
+    for (int j = 0; j < B; ++j) e[j] = i0 + j * THREADS < n ? src[i0 + j * THREADS] : -1;
+    if (mask) {
+      uint8_t in[B];
+#pragma unroll
+      for (int j = 0; j < B; ++j)
+        in[j] = i0 + j * THREADS < n ? mask[begin + (i0 + j * THREADS) / (uint32_t)k] : 0;
+#pragma unroll
+      for (int j = 0; j < B; ++j) e[j] = in[j] ? e[j] : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < B; ++j)
+      if (e[j] >= 0 && e[j] < E) atomicAdd(&mine[e[j]], 1);
+  }
+  if (mask) {
+    for (int t = begin + (int)threadIdx.x; t < end; t += THREADS) tokens += mask[t] != 0;
+  } else if (threadIdx.x == 0) {
+    tokens = end - begin;
+  }
+  tokens = group_reduce<64>(tokens, add);
   if ((threadIdx.x & 63) == 0 && tokens) atomicAdd(&bins[copies * E], tokens);
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += THREADS) {
@@ -143,19 +179,29 @@ __device__ __forceinline__ void count_chunk_lds(int32_t *bins, int copies, const
   __syncthreads();
 }
 
-// Counts of one chunk: part[block][0..E-1] choices, part[block][E] counted tokens.
+// What a counting block wrote: its sequence (-1: none) and the tokens it counted there.
+struct ChunkTokens {
+  int32_t seq, tokens;
+};
+
+// Counts of one chunk: choices in part[block][0..E-1], tokens in chunks[block].
 __global__ __launch_bounds__(BL_COUNT_THREADS) void balance_count_kernel(const int32_t *__restrict__ ids,
                                                                          const uint8_t *__restrict__ mask,
                                                                          const int32_t *__restrict__ off, int T, int E,
                                                                          int k, int S, int chunk, int copies,
-                                                                         int32_t *__restrict__ part) {
+                                                                         int32_t *__restrict__ part,
+                                                                         ChunkTokens *__restrict__ chunks) {
   extern __shared__ int32_t s_mem[];
   int total = 0;
   const Span sp = find_span(off, S, T, chunk, blockIdx.x, total);
-  if (sp.seq < 0) return;  // equal in every thread
+  if (sp.seq < 0) {  // equal in every thread
+    if (threadIdx.x == 0) chunks[blockIdx.x] = ChunkTokens{-1, 0};
+    return;
+  }
   count_chunk_lds<BL_COUNT_THREADS>(s_mem, copies, ids, mask, sp.begin, sp.end, E, k);
-  int32_t *out = part + (size_t)blockIdx.x * (E + 1);
-  for (int e = threadIdx.x; e <= E; e += BL_COUNT_THREADS) out[e] = s_mem[e < E ? e : copies * E];
+  int32_t *out = part + (size_t)blockIdx.x * E;
+  for (int e = threadIdx.x; e < E; e += BL_COUNT_THREADS) out[e] = s_mem[e];
+  if (threadIdx.x == 0) chunks[blockIdx.x] = ChunkTokens{sp.seq, s_mem[copies * E]};
 }
 
 // One block a sequence: its counts and counted tokens from the chunks', and the index of its
@@ -163,6 +209,7 @@ __global__ __launch_bounds__(BL_COUNT_THREADS) void balance_count_kernel(const i
 __global__ __launch_bounds__(256) void balance_tables_kernel(const int32_t *__restrict__ off, int T, int E, int S,
                                                              int chunk, int main_chunk, int blocks, int main_blocks,
                                                              const int32_t *__restrict__ part,
+                                                             const ChunkTokens *__restrict__ chunks,
                                                              int32_t *__restrict__ counts,
                                                              int32_t *__restrict__ seq_tokens,
                                                              int32_t *__restrict__ first_main) {
@@ -184,14 +231,18 @@ __global__ __launch_bounds__(256) void balance_tables_kernel(const int32_t *__re
   seq_range(off, T, s, b, e);
   // (offsets that run backwards could name more chunks than there are)
   const int n = min((e - b + chunk - 1) / chunk, max(blocks - first, 0));
-  for (int i = threadIdx.x; i <= E; i += 256) {
+  for (int i = threadIdx.x; i < E; i += 256) {
     int c = 0;
 #pragma unroll 8
-    for (int q = 0; q < n; ++q) c += part[(size_t)(first + q) * (E + 1) + i];
-    if (i < E)
-      counts[(size_t)s * E + i] = c;
-    else
-      seq_tokens[s] = c;
+    for (int q = 0; q < n; ++q) c += part[(size_t)(first + q) * E + i];
+    counts[(size_t)s * E + i] = c;
+  }
+  if (threadIdx.x < 64) {
+    int c = 0;
+    for (int q = lane; q < n; q += 64) c += chunks[first + q].tokens;
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) c += __shfl_xor(c, o, 64);
+    if (lane == 0) seq_tokens[s] = c;
   }
   if (threadIdx.x == 0) {
     first_main[s] = min(fm, main_blocks);
@@ -200,6 +251,31 @@ __global__ __launch_bounds__(256) void balance_tables_kernel(const int32_t *__re
 }
 
 // ------------------------------------------------------------------------------- main pass
+
+// Chunks of sequence `seq` among the counting blocks' (they are neighbours), its tokens, the
+// tokens and the sequences that count any of all of them (up to 64).
+struct SeqCounts {
+  int first, n, tokens, all, live;
+};
+__device__ __forceinline__ SeqCounts seq_counts(const ChunkTokens *chunks, int blocks, int seq) {
+  const int lane = threadIdx.x & 63;
+  SeqCounts r{0, 0, 0, 0, 0};
+  uint64_t seen = 0;
+  for (int c0 = 0; c0 < blocks; c0 += 64) {
+    const ChunkTokens c = c0 + lane < blocks ? chunks[c0 + lane] : ChunkTokens{-1, 0};
+    const uint64_t mine = __ballot(c.seq == seq);
+    if (mine && r.n == 0) r.first = c0 + __ffsll((unsigned long long)mine) - 1;
+    r.n += __popcll(mine);
+    if (c.seq == seq) r.tokens += c.tokens;
+    r.all += c.tokens;
+    if (c.tokens > 0) seen |= 1ull << c.seq;
+  }
+  r.tokens = group_reduce<64>(r.tokens, add);
+  r.all = group_reduce<64>(r.all, add);
+  const auto either = [](uint32_t x, uint32_t y) { return x | y; };
+  r.live = __popc(group_reduce<64>((uint32_t)seen, either)) + __popc(group_reduce<64>((uint32_t)(seen >> 32), either));
+  return r;
+}
 
 struct BalanceArgs {
   const float *logits;
@@ -213,45 +289,26 @@ struct BalanceArgs {
   float *part;         // [blocks][E]: column sums of p
   double *sums;        // [blocks][2]: sum of sum_i f_i p_ti / N_s, sum of z^2 (a finite z's square can pass
                        // the largest float)
-  int32_t *first_main;
+  const int32_t *cpart;       // the counting blocks' results, added up by each block for itself,
+  const ChunkTokens *chunks;  // or NULL: counts and seq_tokens hold them
+  int cblocks;
   float *mean_probs, *losses;
-  int T, E, k, S, chunk, copies;
+  int T, E, k, S, chunk, copies, cols;
   int one;  // the only block: it finishes too
   float alpha, beta;
 };
 
-// Reductions over groups of LPT neighbouring lanes, the result in every lane: lane moves
-// within a row of 16 (lane ^ 1, lane ^ 2, then half-row and row mirrors, which pair equal
-// values), then rows and halves of the wavefront exchanged.
-template <int CTRL>
-__device__ __forceinline__ float lane_move(float v) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, false));
-}
-template <int LPT, typename Op>
-__device__ __forceinline__ float group_reduce(float v, Op op) {
-  if constexpr (LPT >= 2) v = op(v, lane_move<0xb1>(v));
-  if constexpr (LPT >= 4) v = op(v, lane_move<0x4e>(v));
-  if constexpr (LPT >= 8) v = op(v, lane_move<0x141>(v));
-  if constexpr (LPT >= 16) v = op(v, lane_move<0x140>(v));
-  if constexpr (LPT >= 32) {
-    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = op(__uint_as_float(r[0]), __uint_as_float(r[1]));
-  }
-  if constexpr (LPT >= 64) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = op(__uint_as_float(r[0]), __uint_as_float(r[1]));
-  }
-  return v;
-}
+constexpr int at_once(int values) { return values <= 4 ? 4 : values <= 8 ? 2 : 1; }
 
-// A token's row in LPT lanes of VPL values each, 64 / LPT tokens a wavefront, NT such groups
-// of tokens at a time (their loads and lane moves in flight together).  With VEC (E a
-// multiple of 4) a lane's values are 16-byte groups; otherwise they lie LPT apart, so that
-// each load still covers neighbouring words.
+// A token's row in LPT lanes of up to 16 values each, 64 / LPT tokens a wavefront: few lanes a
+// row, so that the three reductions over a row and the row's own factors cost little beside
+// its values (64 lanes of four values: ...).  With VEC (E a multiple of 4) a lane's values are
+// 16-byte groups; otherwise they lie LPT apart, so that each load still covers neighbouring
+// words.
 template <int LPT, int VPL, bool VEC, bool LOSS>
 __global__ __launch_bounds__(BL_THREADS) void balance_main_kernel(BalanceArgs a) {
   constexpr int TPW = 64 / LPT;
-  constexpr int NT = VPL <= 4 ? 4 : VPL <= 8 ? 2 : 1;
+  constexpr int NT = at_once(VPL);  // tokens a lane at a time
   extern __shared__ int32_t s_mem[];  // counting bins, then the waves' column sums [BL_WAVES][E]
   __shared__ double s_red[BL_WAVES][2];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -312,10 +369,27 @@ __global__ __launch_bounds__(BL_THREADS) void balance_main_kernel(BalanceArgs a)
       for (int i = threadIdx.x; i < E; i += BL_THREADS) a.counts[i] = s_mem[i];
       if (threadIdx.x == 0) {
         a.seq_tokens[0] = ns;
-        a.first_main[0] = 0;
-        a.first_main[1] = (e - b + a.chunk - 1) / a.chunk;
       }
     }
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) f[v] = expert(v) < E ? (float)s_mem[expert(v)] : 0.f;
+    __syncthreads();
+  } else if (LOSS && a.chunks) {
+    for (int e = threadIdx.x; e < E; e += BL_THREADS) s_mem[e] = 0;
+    const SeqCounts sc = seq_counts(a.chunks, a.cblocks, sp.seq);
+    live = sc.live;
+    all = sc.all;
+    ns = sc.tokens;
+    __syncthreads();
+    // threads on neighbouring experts (cols: a power of two), the others on further chunks
+    const int col = threadIdx.x & (a.cols - 1), row = threadIdx.x / a.cols, rows = BL_THREADS / a.cols;
+    for (int e = col; e < E; e += a.cols) {
+      int c = 0;
+#pragma unroll 8
+      for (int q = row; q < sc.n; q += rows) c += a.cpart[(size_t)(sc.first + q) * E + e];
+      atomicAdd(&s_mem[e], c);
+    }
+    __syncthreads();
 #pragma unroll
     for (int v = 0; v < VPL; ++v) f[v] = expert(v) < E ? (float)s_mem[expert(v)] : 0.f;
     __syncthreads();
@@ -325,11 +399,8 @@ __global__ __launch_bounds__(BL_THREADS) void balance_main_kernel(BalanceArgs a)
       live += n > 0;
       all += n;
     }
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) {
-      live += __shfl_xor(live, o, 64);
-      all += __shfl_xor(all, o, 64);
-    }
+    live = group_reduce<64>(live, add);
+    all = group_reduce<64>(all, add);
     ns = a.seq_tokens[sp.seq];
 #pragma unroll
     for (int v = 0; v < VPL; ++v) f[v] = expert(v) < E ? (float)a.counts[(size_t)sp.seq * E + expert(v)] : 0.f;
@@ -369,13 +440,13 @@ __global__ __launch_bounds__(BL_THREADS) void balance_main_kernel(BalanceArgs a)
         sum[n] += l[n][v];
         dot[n] += l[n][v] * f[v];
       }
-      sum[n] = group_reduce<LPT>(sum[n], [](float x, float y) { return x + y; });
-      dot[n] = group_reduce<LPT>(dot[n], [](float x, float y) { return x + y; });
+      sum[n] = group_reduce<LPT>(sum[n], add);
+      dot[n] = group_reduce<LPT>(dot[n], add);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int t = t0 + n * TPW + sub;
-      const float inv = sum[n] == 0.f ? 0.f : 1.f / sum[n];
+      const float inv = sum[n] == 0.f ? 0.f : __builtin_amdgcn_rcpf(sum[n]);  // sum is in [1, E]
       const float z = sum[n] == 0.f ? 0.f : base[n] + __logf(sum[n]);
       const float mean_f = dot[n] * inv;  // sum_i f_i p_i
       const float shift = ca * mean_f - cb * z;
@@ -398,12 +469,12 @@ __global__ __launch_bounds__(BL_THREADS) void balance_main_kernel(BalanceArgs a)
             f32x4 q;
 #pragma unroll
             for (int i = 0; i < 4; ++i) q[i] = l[n][v + i] * (ca * f[v + i] - shift);
-            if (expert(v) < E) *reinterpret_cast<f32x4 *>(drow + expert(v)) = q;
+            if (expert(v) < E) __builtin_nontemporal_store(q, reinterpret_cast<f32x4 *>(drow + expert(v)));
           }
         } else {
 #pragma unroll
           for (int v = 0; v < VPL; ++v)
-            if (expert(v) < E) drow[expert(v)] = l[n][v] * (ca * f[v] - shift);
+            if (expert(v) < E) __builtin_nontemporal_store(l[n][v] * (ca * f[v] - shift), drow + expert(v));
         }
       }
     }
@@ -416,7 +487,7 @@ __global__ __launch_bounds__(BL_THREADS) void balance_main_kernel(BalanceArgs a)
       for (int o = LPT; o < 64; o <<= 1) acc[v] += __shfl_xor(acc[v], o, 64);
       if (sub == 0 && expert(v) < E) s_acc[wave * E + expert(v)] = acc[v];
     }
-    block_sum2<BL_WAVES>(bacc, zacc, s_red);  // synchronises: the column sums are visible after it
+    block_sum2<BL_WAVES, LPT>(bacc, zacc, s_red);  // synchronises: the column sums are visible after it
     const float per = a.one ? 1.f / (float)max(ns, 1) : 1.f;
     float *out = a.one ? a.mean_probs : a.part + (size_t)blockIdx.x * E;
     for (int e = threadIdx.x; e < E; e += BL_THREADS) {
@@ -442,63 +513,138 @@ __global__ __launch_bounds__(BL_THREADS) void balance_main_kernel(BalanceArgs a)
 
 constexpr int BL_FIN_THREADS = 512, BL_FIN_WAVES = BL_FIN_THREADS / 64;
 
+struct FinishArgs {
+  const float *part;
+  const double *sums;
+  const int32_t *off;
+  const int32_t *first_main;  // with the tables, or NULL
+  const int32_t *cpart;       // without them: the counting blocks' results (chunks), or NULL
+  const ChunkTokens *chunks;
+  int32_t *counts, *seq_tokens;
+  float *mean_probs, *losses;
+  int T, E, S, chunk, blocks, cblocks, cols, parts;
+  float alpha, beta;
+};
+
 // Block s < S * parts: `cols` (a power of two) of a sequence's mean probabilities, threads on
 // neighbouring experts and on further blocks of the main pass.  The last block: the two
 // losses, since sum_i f_si P_si is the mean over the sequence's tokens of sum_i f_si p_ti.
-__global__ __launch_bounds__(BL_FIN_THREADS) void balance_finish_kernel(
-    const float *__restrict__ part, const double *__restrict__ sums, const int32_t *__restrict__ first_main,
-    const int32_t *__restrict__ seq_tokens, int E, int S, int cols, int parts, float alpha, float beta,
-    float *__restrict__ mean_probs, float *__restrict__ losses) {
-  __shared__ double s_p[BL_FIN_THREADS];
+__global__ __launch_bounds__(BL_FIN_THREADS) void balance_finish_kernel(FinishArgs a) {
+  __shared__ double s_p[BL_FIN_WAVES][32];
+  __shared__ int s_c[BL_FIN_WAVES][32];
   __shared__ double s_red[BL_FIN_WAVES][2];
-  if (blockIdx.x == (unsigned)(S * parts)) {
-    double bal = 0, z = 0, live = 0, all = 0;
-    const int nb = first_main[S];
-    for (int b = threadIdx.x; b < nb; b += BL_FIN_THREADS) {
-      bal += sums[2 * (size_t)b];
-      z += sums[2 * (size_t)b + 1];
+  const int S = a.S, E = a.E;
+  const bool losses = blockIdx.x == (unsigned)(S * a.parts);
+  const int s = losses ? S - 1 : blockIdx.x / a.parts;
+  // blocks of the main pass: of sequence s, and in all
+  int b0, b1, nb;
+  if (a.first_main) {
+    b0 = a.first_main[s];
+    b1 = a.first_main[s + 1];
+    nb = a.first_main[S];
+  } else {
+    const int lane = threadIdx.x & 63;  // of sequence: S <= 64
+    int b = 0, e = 0;
+    if (lane < S) seq_range(a.off, a.T, lane, b, e);
+    const int n = (e - b + a.chunk - 1) / a.chunk;
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(incl, o, 64);
+      if (lane >= o) incl += v;
     }
-    for (int q = threadIdx.x; q < S; q += BL_FIN_THREADS) {
-      live += seq_tokens[q] > 0;
-      all += seq_tokens[q];
+    // (offsets that run backwards could name more blocks than there are)
+    b0 = min(__shfl(incl - n, s, 64), a.blocks);
+    b1 = min(__shfl(incl, s, 64), a.blocks);
+    nb = min(__shfl(incl, S - 1, 64), a.blocks);
+  }
+  if (losses) {
+    double bal = 0, z = 0, live = 0, all = 0;
+    for (int b = threadIdx.x; b < nb; b += BL_FIN_THREADS) {
+      bal += a.sums[2 * (size_t)b];
+      z += a.sums[2 * (size_t)b + 1];
+    }
+    if (a.chunks) {
+      const SeqCounts sc = seq_counts(a.chunks, a.cblocks, s);
+      if (threadIdx.x == 0) {
+        live = sc.live;
+        all = sc.all;
+      }
+    } else {
+      for (int q = threadIdx.x; q < S; q += BL_FIN_THREADS) {
+        live += a.seq_tokens[q] > 0;
+        all += a.seq_tokens[q];
+      }
     }
     block_sum2<BL_FIN_WAVES>(bal, z, s_red);
-    if (S > 1) block_sum2<BL_FIN_WAVES>(live, all, s_red);
+    block_sum2<BL_FIN_WAVES>(live, all, s_red);
     if (threadIdx.x == 0) {
-      losses[0] = (float)((double)alpha * E * bal / max(S > 1 ? live : 1.0, 1.0));
-      losses[1] = (float)((double)beta * z / max(all, 1.0));
+      a.losses[0] = (float)((double)a.alpha * E * bal / max(live, 1.0));
+      a.losses[1] = (float)((double)a.beta * z / max(all, 1.0));
     }
     return;
   }
-  const int s = blockIdx.x / parts;
-  const int b0 = first_main[s], b1 = first_main[s + 1], n = seq_tokens[s];
-  const int col = threadIdx.x & (cols - 1), row = threadIdx.x / cols, rows = BL_FIN_THREADS / cols;
-  const int e = (blockIdx.x - s * parts) * cols + col;
+  const int col = threadIdx.x & (a.cols - 1), row = threadIdx.x / a.cols, rows = BL_FIN_THREADS / a.cols;
+  const int part = blockIdx.x - s * a.parts, e = part * a.cols + col;
+  SeqCounts sc{0, 0, 0, 0, 0};
+  int n, c = 0;
+  if (a.chunks) {
+    sc = seq_counts(a.chunks, a.cblocks, s);
+    n = sc.tokens;
+    if (part == 0 && threadIdx.x == 0) a.seq_tokens[s] = n;
+  } else {
+    n = a.seq_tokens[s];
+  }
   double p = 0;
   if (e < E) {
 #pragma unroll 8
-    for (int b = b0 + row; b < b1; b += rows) p += part[(size_t)b * E + e];
+    for (int b = b0 + row; b < b1; b += rows) p += a.part[(size_t)b * E + e];
+    for (int q = row; q < sc.n; q += rows) c += a.cpart[(size_t)(sc.first + q) * E + e];
   }
-  s_p[threadIdx.x] = p;
+  // rows of one wavefront (cols <= 32), then one row of each
+  for (int o = 32; o >= a.cols; o >>= 1) {
+    p += __shfl_xor(p, o, 64);
+    c += __shfl_xor(c, o, 64);
+  }
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (lane < a.cols) {
+    s_p[wave][lane] = p;
+    s_c[wave][lane] = c;
+  }
   __syncthreads();
   if (row == 0 && e < E) {
-    for (int r = 1; r < rows; ++r) p += s_p[r * cols + col];
-    mean_probs[(size_t)s * E + e] = (float)(p / max(n, 1));
+    p = 0;
+    c = 0;
+#pragma unroll
+    for (int w = 0; w < BL_FIN_WAVES; ++w) {
+      p += s_p[w][col];
+      c += s_c[w][col];
+    }
+    a.mean_probs[(size_t)s * E + e] = (float)(p / max(n, 1));
+    if (a.chunks) a.counts[(size_t)s * E + e] = c;
   }
 }
 
-// Lanes a token takes: a power of two with at most four values each, 64 past that.
+constexpr int kVecValues = 4, kOddValues = 6;  // values a lane takes at most (16 past 64 lanes)
+// Lanes a token takes: a power of two.
 int lanes_per_token(int E) {
   int l = 1;
-  while (l < 64 && 4 * l < E) l *= 2;
+  while (l < 64 && (E % 4 == 0 ? kVecValues : kOddValues) * l < E) l *= 2;
   return l;
 }
+// Values of a lane, as the kernel is built for.
+int values_per_lane(int E) {
+  const int l = lanes_per_token(E), v = (E + l - 1) / l;
+  if (E % 4 == 0) return v <= 4 ? 4 : v <= 8 ? 8 : v <= 12 ? 12 : 16;
+  return v <= 4 ? 4 : v <= 6 ? 6 : v <= 8 ? 8 : v <= 10 ? 10 : v <= 12 ? 12 : 16;
+}
+int tokens_at_once(int E) { return 64 / lanes_per_token(E) * at_once(values_per_lane(E)); }  // of a wavefront
 
-int count_chunk(int T) { return std::max(256, (T + 255) / 256); }
+int count_chunk(int T) { return std::max(512, (T + 127) / 128); }
 // Tokens of a block of the main pass: one round of its wavefronts at least.
 int main_chunk(int T, int E, bool loss) {
-  const int tpw = 64 / lanes_per_token(E), nt = E <= 256 ? 4 : E <= 512 ? 2 : 1, blocks = loss ? 512 : 2048;
-  return std::max(BL_WAVES * tpw * nt, (T + blocks - 1) / blocks);
+  const int blocks = loss ? 512 : 2048;
+  return std::max(BL_WAVES * tokens_at_once(E), (T + blocks - 1) / blocks);
 }
 
 // Chunks of the two passes: sequences cut into whole chunks, at most one partial chunk each,
@@ -510,7 +656,7 @@ int main_blocks(int T, int E, int S, bool off, bool loss) {
 
 int bin_copies(int E) {
   int copies = 1;
-  while (copies < 64 && copies * 2 * E <= BL_BINS) copies *= 2;
+  while (copies < 8 && copies * 2 * E <= BL_BINS) copies *= 2;
   return copies;
 }
 
@@ -523,27 +669,33 @@ hipError_t launch_main(const BalanceArgs &a, int blocks, hipStream_t s) {
     hipLaunchKernelGGL((balance_main_kernel<L, V, VEC, LOSS>), dim3((unsigned)blocks), dim3(BL_THREADS), lds, s, a); \
     return hipGetLastError();                                                                                       \
   } while (0)
-#define BL_CASE(L)                          \
-  do {                                      \
-    if (E % 4 == 0) BL_LAUNCH(L, 4, true);  \
-    if (E <= 3 * L) BL_LAUNCH(L, 3, false); \
-    BL_LAUNCH(L, 4, false);                 \
-  } while (0)
+  const int v = values_per_lane(E);
+#define BL_CASE(L)                                  \
+  case L:                                           \
+    if (E % 4 == 0) {                               \
+      if (v == 4) BL_LAUNCH(L, 4, true);            \
+      if (v == 8) BL_LAUNCH(L, 8, true);            \
+      if (L < 64) return hipErrorInvalidValue;      \
+      if (v == 12) BL_LAUNCH(64, 12, true);         \
+      BL_LAUNCH(64, 16, true);                      \
+    }                                               \
+    if (v == 4) BL_LAUNCH(L, 4, false);             \
+    if (v == 6) BL_LAUNCH(L, 6, false);             \
+    if (v == 8) BL_LAUNCH(L, 8, false);             \
+    if (v == 10) BL_LAUNCH(L, 10, false);           \
+    if (v == 12) BL_LAUNCH(L, 12, false);           \
+    if (L < 64) return hipErrorInvalidValue;        \
+    BL_LAUNCH(64, 16, false);
   switch (lanes_per_token(E)) {
-    case 1: BL_CASE(1);
-    case 2: BL_CASE(2);
-    case 4: BL_CASE(4);
-    case 8: BL_CASE(8);
-    case 16: BL_CASE(16);
-    case 32: BL_CASE(32);
+    BL_CASE(1)
+    BL_CASE(2)
+    BL_CASE(4)
+    BL_CASE(8)
+    BL_CASE(16)
+    BL_CASE(32)
+    BL_CASE(64)
   }
-  if (E <= 256) BL_CASE(64);
-  if (E <= 512) {
-    if (E % 4 == 0) BL_LAUNCH(64, 8, true);
-    BL_LAUNCH(64, 8, false);
-  }
-  if (E % 4 == 0) BL_LAUNCH(64, 16, true);
-  BL_LAUNCH(64, 16, false);
+  return hipErrorInvalidValue;
 #undef BL_CASE
 #undef BL_LAUNCH
 }
@@ -551,13 +703,14 @@ hipError_t launch_main(const BalanceArgs &a, int blocks, hipStream_t s) {
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 struct BalanceWs {
-  size_t count_part, main_part, sums, first_main, total;
+  size_t count_part, chunks, main_part, sums, first_main, total;
 };
 BalanceWs balance_ws(int T, int E, int S) {
   BalanceWs w;
   const size_t cb = count_blocks(T, S, true), mb = main_blocks(T, E, S, true, true);
   w.count_part = 0;
-  w.main_part = align256(cb * (E + 1) * 4);
+  w.chunks = align256(cb * E * 4);
+  w.main_part = w.chunks + align256(cb * sizeof(ChunkTokens));
   w.sums = w.main_part + align256(mb * E * 4);
   w.first_main = w.sums + align256(mb * 16);
   w.total = w.first_main + align256(((size_t)S + 1) * 4);
@@ -567,6 +720,9 @@ BalanceWs balance_ws(int T, int E, int S) {
 // One sequence with at most this many choices is counted by every block of the main pass for
 // itself.
 constexpr int64_t kSelfCount = 16384;
+// Up to 64 sequences, and at most this many partial counts: every block of the main pass adds
+// up its sequence's for itself, and no launch for the tables is made.
+constexpr int64_t kSelfTables = 32768;
 
 }  // namespace
 
@@ -577,6 +733,7 @@ hipError_t launch_balance_loss(const BalanceCall &c, int32_t *counts, int32_t *s
   const BalanceWs w = balance_ws(c.T, c.E, c.S);
   uint8_t *base = static_cast<uint8_t *>(ws);
   int32_t *cpart = reinterpret_cast<int32_t *>(base + w.count_part);
+  ChunkTokens *chunks = reinterpret_cast<ChunkTokens *>(base + w.chunks);
   const bool off = c.off != nullptr;
   const int cc = count_chunk(c.T), mc = main_chunk(c.T, c.E, true);
   const int cb = count_blocks(c.T, c.S, off), mb = main_blocks(c.T, c.E, c.S, off, true);
@@ -591,7 +748,7 @@ hipError_t launch_balance_loss(const BalanceCall &c, int32_t *counts, int32_t *s
   a.dlogits = c.dlogits;
   a.part = reinterpret_cast<float *>(base + w.main_part);
   a.sums = reinterpret_cast<double *>(base + w.sums);
-  a.first_main = reinterpret_cast<int32_t *>(base + w.first_main);
+  int32_t *first_main = reinterpret_cast<int32_t *>(base + w.first_main);
   a.mean_probs = mean_probs;
   a.losses = losses;
   a.T = c.T;
@@ -603,23 +760,51 @@ hipError_t launch_balance_loss(const BalanceCall &c, int32_t *counts, int32_t *s
   a.alpha = c.alpha;
   a.beta = c.beta;
   hipError_t e;
+  bool tables = false;
   if (c.S == 1 && (int64_t)c.T * c.k <= kSelfCount) {
     a.ids = c.ids;
     a.one = mb == 1;
   } else {
     hipLaunchKernelGGL(balance_count_kernel, dim3((unsigned)cb), dim3(BL_COUNT_THREADS), (copies * c.E + 1) * 4, s,
-                       c.ids, c.mask, c.off, c.T, c.E, c.k, c.S, cc, copies, cpart);
+                       c.ids, c.mask, c.off, c.T, c.E, c.k, c.S, cc, copies, cpart, chunks);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL(balance_tables_kernel, dim3((unsigned)c.S), dim3(256), 0, s, c.off, c.T, c.E, c.S, cc, mc, cb,
-                       mb, cpart, counts, seq_tokens, a.first_main);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (c.S <= 64 && (int64_t)cb * c.E <= kSelfTables) {
+      a.cpart = cpart;
+      a.chunks = chunks;
+      a.cblocks = cb;
+      a.cols = 1;
+      while (a.cols < BL_THREADS && a.cols < c.E) a.cols *= 2;
+    } else {
+      hipLaunchKernelGGL(balance_tables_kernel, dim3((unsigned)c.S), dim3(256), 0, s, c.off, c.T, c.E, c.S, cc, mc, cb,
+                         mb, cpart, chunks, counts, seq_tokens, first_main);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+      tables = true;
+    }
   }
   if ((e = launch_main<true>(a, mb, s)) != hipSuccess || a.one) return e;
-  int cols = 1;
-  while (cols < 32 && cols < c.E) cols *= 2;
-  const int parts = (c.E + cols - 1) / cols;
-  hipLaunchKernelGGL(balance_finish_kernel, dim3((unsigned)(c.S * parts + 1)), dim3(BL_FIN_THREADS), 0, s, a.part,
-                     a.sums, a.first_main, seq_tokens, c.E, c.S, cols, parts, c.alpha, c.beta, mean_probs, losses);
+  FinishArgs f{};
+  f.part = a.part;
+  f.sums = a.sums;
+  f.off = c.off;
+  f.first_main = tables ? first_main : nullptr;
+  f.cpart = a.cpart;
+  f.chunks = a.chunks;
+  f.cblocks = a.cblocks;
+  f.counts = counts;
+  f.seq_tokens = seq_tokens;
+  f.mean_probs = mean_probs;
+  f.losses = losses;
+  f.T = c.T;
+  f.E = c.E;
+  f.S = c.S;
+  f.chunk = mc;
+  f.blocks = mb;
+  f.cols = 1;
+  while (f.cols < 32 && f.cols < c.E) f.cols *= 2;
+  f.parts = (c.E + f.cols - 1) / f.cols;
+  f.alpha = c.alpha;
+  f.beta = c.beta;
+  hipLaunchKernelGGL(balance_finish_kernel, dim3((unsigned)(c.S * f.parts + 1)), dim3(BL_FIN_THREADS), 0, s, f);
   return hipGetLastError();
 }
 
