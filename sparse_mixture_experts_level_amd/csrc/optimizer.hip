@@ -210,7 +210,7 @@ int64_t norm_chunk(const NormTensor *t, int count) {
   int64_t total = 0;
   for (int i = 0; i < count; ++i) total += t[i].n;
   const int64_t c = (total / 2048 + 2047) / 2048 * 2048;
-  return std::min<int64_t>(std::max<int64_t>(c, 2048), 65536);
+  return std::min<int64_t>(std::max<int64_t>(c, 2048), 32768);
 }
 
 // ---------------------------------------------------------------------------- AdamW step
@@ -263,13 +263,13 @@ __device__ __forceinline__ float next_weight(float w, float m, float root, const
   return w * r.keep - r.step * u;
 }
 
-constexpr int kAdamChunk = 2048;  // values a block
+constexpr int kAdam32Chunk = 1024, kAdamChunk = 2048;  // values a block, by the states' bits
 
 // States in 32 bits: four values a thread, twice.  G: gradients' type; P: parameters'; MASTER:
 // the float copy is read instead of the parameter.
 template <typename G, typename P, bool MASTER>
 __device__ __forceinline__ void adamw32(const AdamArgs &a, const AdamTensor &t, const Rates &r, int64_t i0) {
-  constexpr int U = kAdamChunk / (4 * kThreads);
+  constexpr int U = kAdam32Chunk / (4 * kThreads);
   const float b1 = (float)a.h.beta1, b2 = (float)a.h.beta2, c1 = (float)(1.0 - a.h.beta1),
               c2 = (float)(1.0 - a.h.beta2), eps = (float)a.h.eps;
   const G *pg = static_cast<const G *>(t.grad);
@@ -310,7 +310,7 @@ __device__ __forceinline__ void adamw32(const AdamArgs &a, const AdamTensor &t, 
   };
   struct Yes { constexpr operator bool() const { return true; } };
   struct No { constexpr operator bool() const { return false; } };
-  if (i0 + kAdamChunk <= t.n)
+  if (i0 + kAdam32Chunk <= t.n)
     run(Yes{});
   else
     run(No{});
@@ -342,7 +342,7 @@ __global__ __launch_bounds__(kThreads) void adamw32_kernel(AdamArgs a) {
   const AdamTensor t = a.t[ti];
   Rates r;
   if (!rates(a, t.decay, r)) return;
-  const int64_t i0 = (int64_t)(blockIdx.x - a.first[ti]) * kAdamChunk;
+  const int64_t i0 = (int64_t)(blockIdx.x - a.first[ti]) * kAdam32Chunk;
   ADAM_BY_TYPE(adamw32, a, t, r, i0);
 }
 
@@ -419,7 +419,7 @@ struct Codes {
 __device__ __forceinline__ Codes load_codes(const uint8_t *p, int n) {
   Codes c{{0u, 0u}};
   if (n >= 8) {
-    const u32x2 q = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(p));
+    const u32x2 q = *reinterpret_cast<const u32x2 *>(p);
     c.w[0] = q[0];
     c.w[1] = q[1];
   } else {
@@ -431,7 +431,7 @@ __device__ __forceinline__ Codes load_codes(const uint8_t *p, int n) {
 }
 __device__ __forceinline__ void store_codes(uint8_t *p, const Codes &c, int n) {
   if (n >= 8) {
-    __builtin_nontemporal_store(u32x2{c.w[0], c.w[1]}, reinterpret_cast<u32x2 *>(p));
+    *reinterpret_cast<u32x2 *>(p) = u32x2{c.w[0], c.w[1]};
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -567,7 +567,7 @@ __global__ __launch_bounds__(kThreads) void adamw_read_kernel(ReadArgs a) {
     if (n == 0) continue;
     auto codes = [&](const uint8_t *p) {
       uint32_t w = 0;
-      if (n == 4) return __builtin_nontemporal_load(reinterpret_cast<const uint32_t *>(p + i));
+      if (n == 4) return *reinterpret_cast<const uint32_t *>(p + i);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (j < n) w |= (uint32_t)p[i + j] << (8 * j);
@@ -648,6 +648,7 @@ hipError_t launch_adamw(const AdamTensor *t, int count, const AdamScalars &h, hi
   a.step = (float)(h.lr / (1.0 - std::pow(h.beta1, (double)h.step)));
   a.inv_bc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(h.beta2, (double)h.step)));
   for (int eight = 0; eight < 2; ++eight) {
+    const int64_t chunk = eight ? kAdamChunk : kAdam32Chunk;
     int64_t blocks = 0;
     a.count = 0;
     auto flush = [&]() -> hipError_t {
@@ -662,7 +663,7 @@ hipError_t launch_adamw(const AdamTensor *t, int count, const AdamScalars &h, hi
     };
     for (int i = 0; i < count; ++i) {
       if (t[i].eight != eight || t[i].n == 0) continue;
-      const int64_t nb = (t[i].n + kAdamChunk - 1) / kAdamChunk;
+      const int64_t nb = (t[i].n + chunk - 1) / chunk;
       if (a.count == kAdamTensors || blocks + nb > kMaxBlocks) {
         const hipError_t e = flush();
         if (e != hipSuccess) return e;
