@@ -458,7 +458,8 @@ size_t moe_balance_workspace_size(const moe_desc *desc, int32_t num_seqs);
  *   seq_tokens  [num_seqs] int32, written: N_s
  *   mean_probs  [num_seqs, E] float, written: P (zeros where N_s is 0)
  *   losses      [2] float, written; 0 when nothing is counted
- *   dlogits     [T, E] float or NULL, written in full: zero for tokens not counted
+ *   dlogits     [T, E] float or NULL, written in full: zero for tokens not counted; not
+ *               overlapping logits
  *   ws          at least moe_balance_workspace_size(desc, num_seqs) bytes
  * Sums in fixed orders (bit-reproducible).  Only kernel launches on `stream`. */
 moe_status moe_balance_loss(const moe_desc *desc, const float *logits, const int32_t *topk_ids,
@@ -470,7 +471,7 @@ moe_status moe_balance_loss(const moe_desc *desc, const float *logits, const int
  *   dlogits = dloss[0] * d losses[0] / d logits + dloss[1] * d losses[1] / d logits
  *   counts, seq_tokens  as moe_balance_loss wrote them
  *   dloss               [2] float (device) or NULL (both 1)
- *   dlogits             [T, E] float, written in full
+ *   dlogits             [T, E] float, written in full; not overlapping logits
  * Other arguments as for moe_balance_loss; no workspace. */
 moe_status moe_balance_loss_backward(const moe_desc *desc, const float *logits, const uint8_t *token_mask,
                                      const int32_t *seq_offsets, int32_t num_seqs, const int32_t *counts,

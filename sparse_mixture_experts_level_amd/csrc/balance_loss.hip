@@ -307,6 +307,9 @@ constexpr int at_once(int values) { return values <= 4 ? 4 : values <= 8 ? 2 : 1
 // words.
 template <int LPT, int VPL, bool VEC, bool LOSS>
 __global__ __launch_bounds__(BL_THREADS) void balance_main_kernel(BalanceArgs a) {
+  // fused multiply-adds where they are written: with and without the losses the gradient is
+  // the same bit for bit
+#pragma clang fp contract(off)
   constexpr int TPW = 64 / LPT;
   constexpr int NT = at_once(VPL);  // tokens a lane at a time
   extern __shared__ int32_t s_mem[];  // counting bins, then the waves' column sums [BL_WAVES][E]
@@ -438,7 +441,7 @@ __global__ __launch_bounds__(BL_THREADS) void balance_main_kernel(BalanceArgs a)
       for (int v = 0; v < VPL; ++v) {
         l[n][v] = __expf(l[n][v] - base[n]);
         sum[n] += l[n][v];
-        dot[n] += l[n][v] * f[v];
+        dot[n] = __builtin_fmaf(l[n][v], f[v], dot[n]);
       }
       sum[n] = group_reduce<LPT>(sum[n], add);
       dot[n] = group_reduce<LPT>(dot[n], add);
@@ -449,7 +452,7 @@ __global__ __launch_bounds__(BL_THREADS) void balance_main_kernel(BalanceArgs a)
       const float inv = sum[n] == 0.f ? 0.f : __builtin_amdgcn_rcpf(sum[n]);  // sum is in [1, E]
       const float z = sum[n] == 0.f ? 0.f : base[n] + __logf(sum[n]);
       const float mean_f = dot[n] * inv;  // sum_i f_i p_i
-      const float shift = ca * mean_f - cb * z;
+      const float shift = __builtin_fmaf(ca, mean_f, -(cb * z));
       if constexpr (LOSS) {
         if (li == 0) {
           bacc += (double)mean_f;
@@ -468,13 +471,13 @@ __global__ __launch_bounds__(BL_THREADS) void balance_main_kernel(BalanceArgs a)
           for (int v = 0; v < VPL; v += 4) {
             f32x4 q;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) q[i] = l[n][v + i] * (ca * f[v + i] - shift);
+            for (int i = 0; i < 4; ++i) q[i] = l[n][v + i] * __builtin_fmaf(ca, f[v + i], -shift);
             if (expert(v) < E) __builtin_nontemporal_store(q, reinterpret_cast<f32x4 *>(drow + expert(v)));
           }
         } else {
 #pragma unroll
           for (int v = 0; v < VPL; ++v)
-            if (expert(v) < E) __builtin_nontemporal_store(l[n][v] * (ca * f[v] - shift), drow + expert(v));
+            if (expert(v) < E) __builtin_nontemporal_store(l[n][v] * __builtin_fmaf(ca, f[v], -shift), drow + expert(v));
         }
       }
     }

@@ -524,7 +524,8 @@ def moe_balance_loss(desc, logits, topk_ids, alpha, z_coeff, counts, seq_tokens,
         _tensor(counts, "counts", torch.int32, (S, E), dev), _tensor(seq_tokens, "seq_tokens", torch.int32, (S,), dev),
         _tensor(mean_probs, "mean_probs", torch.float32, (S, E), dev),
         _tensor(losses, "losses", torch.float32, (2,), dev), _tensor(dlogits, "dlogits", torch.float32, (T, E), dev),
-        _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)), "moe_balance_loss")
+        _tensor(ws, "ws", torch.uint8, None, dev), 0 if ws is None else ws.numel(), _stream(stream)),
+        "moe_balance_loss")
 
 
 def moe_balance_loss_backward(desc, logits, counts, seq_tokens, alpha, z_coeff, dlogits, token_mask=None,
@@ -543,15 +544,23 @@ def moe_balance_loss_backward(desc, logits, counts, seq_tokens, alpha, z_coeff, 
 
 # --------------------------------------------------------------- gradient norm and AdamW step
 
+def _check_same(tensors, pointers, name: str) -> None:
+    """Raises when a tensor's memory is not where it was when `pointers` were taken."""
+    if [t.data_ptr() for t in tensors] != pointers:
+        raise RuntimeError(f"{name}: a tensor's memory has been replaced; build the list (the optimizer) again")
+
+
 class GradList:
     """Gradient tensors with the host array of views that moe_grad_norm takes (grad_list())."""
 
     def __init__(self, grads):
         self.grads = list(grads)
         self.views = (MoeGradView * max(len(self.grads), 1))()
-        for i, g in enumerate(self.grads):
-            self.views[i] = MoeGradView(_tensor(g, f"grads[{i}]", (torch.float32, torch.bfloat16)), g.numel(),
-                                        dtype_code(g.dtype), 0)
+        dev = _device()
+        self.pointers = [_tensor(g, f"grads[{i}]", (torch.float32, torch.bfloat16), None, dev)
+                         for i, g in enumerate(self.grads)]
+        for i, (g, p) in enumerate(zip(self.grads, self.pointers)):
+            self.views[i] = MoeGradView(p, g.numel(), dtype_code(g.dtype), 0)
 
     def __len__(self):
         return len(self.grads)
@@ -567,9 +576,11 @@ def moe_grad_norm_workspace_size(grads: GradList) -> int:
 
 def moe_grad_norm(grads: GradList, max_norm: float, out, ws, stream=None) -> None:
     """out [2] float: the norm over every gradient, and min(1, max_norm / (norm + 1e-6))."""
-    _check(lib().moe_grad_norm(grads.views, len(grads), float(max_norm), _tensor(out, "out", torch.float32, (2,)),
-                               _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)),
-           "moe_grad_norm")
+    dev = _device()
+    _check_same(grads.grads, grads.pointers, "moe_grad_norm")
+    _check(lib().moe_grad_norm(grads.views, len(grads), max_norm, _tensor(out, "out", torch.float32, (2,), dev),
+                               _tensor(ws, "ws", torch.uint8, None, dev), 0 if ws is None else ws.numel(),
+                               _stream(stream)), "moe_grad_norm")
 
 
 def moe_adamw_check_tensors(tensors, num_tensors: int) -> None:
@@ -599,6 +610,13 @@ def moe_adamw_read_states(tensors, num_tensors: int, m_out=None, v_out=None, str
                                        _stream(stream)), "moe_adamw_read_states")
 
 
+def _capturing(stream) -> bool:
+    if hasattr(stream, "cuda_stream"):
+        with torch.cuda.stream(stream):
+            return torch.cuda.is_current_stream_capturing()
+    return torch.cuda.is_current_stream_capturing()
+
+
 class MoEAdamW:
     """AdamW over a list of parameter tensors with fixed gradient tensors (moe_adamw_step), after
     clipping by the gradients' norm when max_grad_norm is given (moe_grad_norm).
@@ -608,9 +626,12 @@ class MoEAdamW:
     (one dict of m, v, m_scale, v_scale, master per tensor) takes existing state tensors
     instead of new zeros; `step` is the number of steps already done.  With capturable=True
     the step number and lr live on the device, so that a step captured into a HIP graph
-    counts on at every replay; set the rate with set_lr() then.
+    counts on at every replay (step_count only counts calls); set the rate with set_lr() then.
+    A step skipped because the norm was not finite counts too.
 
-    Tensors are used on the stream of the call; allocation happens here, never in step()."""
+    Tensors are used on the stream of the call, on the GPU that is current when the optimizer is
+    built; allocation happens here, never in step().  The tensors' memory must stay where it is
+    (update parameters and gradients in place); step() refuses when it has moved."""
 
     def __init__(self, params, grads, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, max_grad_norm=None,
                  state_bits=32, master_weights=False, states=None, step=0, capturable=False):
@@ -643,6 +664,8 @@ class MoEAdamW:
                 ptr("v_scale", torch.float32, blocks) if state_bits == 8 else None,
                 p.numel(), dtype_code(p.dtype), dtype_code(g.dtype), state_bits, float(decay[i]))
         moe_adamw_check_tensors(self.tensors, n)
+        self._device = _device()
+        self._pointers = [t.data_ptr() for t in self.params], [t.data_ptr() for t in self.grads]
         self.hparams = MoeAdamwHparams(float(lr), float(betas[0]), float(betas[1]), float(eps), self.step_count, None,
                                        None, None)
         device = self.params[0].device if n else "cuda"
@@ -677,11 +700,15 @@ class MoEAdamW:
 
     def step(self, stream=None) -> None:
         n = len(self.params)
+        if _device() != self._device:
+            raise RuntimeError(f"the optimizer's tensors are on GPU {self._device}, which is not the current one")
+        _check_same(self.params, self._pointers[0], "params")
+        _check_same(self.grads, self._pointers[1], "grads")
         if self.capturable:
             if stream is not None:
                 raise ValueError("a capturable step runs on the current stream")
             self.step_dev.add_(1)
-        elif torch.cuda.is_current_stream_capturing():
+        elif _capturing(stream):
             raise RuntimeError("a captured step would repeat its step number: construct MoEAdamW with capturable=True")
         if self.max_grad_norm is not None:
             moe_grad_norm(self._grad_list, self.max_grad_norm, self.grad_norm, self._ws, stream=stream)

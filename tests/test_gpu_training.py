@@ -163,6 +163,10 @@ def test_balance_loss_one_sequence(T, E, k):
     (1500, 24, 3, list(range(0, 1501, 10)), True),         # 150 sequences: more than a wavefront
     (700, 6, 2, [0, 699], False),                          # one sequence and one row behind it
     (2600, 40, 2, [1, 1200, 2500], True),                  # chunks end inside sequences
+    (9000, 8, 4, [0, 4000, 9000], True),                   # counted apart, few experts
+    (12000, 160, 8, list(range(0, 12001, 200)), False),    # 60 sequences, counts added up by each block
+    (7000, 700, 6, [0, 10, 6990], True),                   # ... and through the tables
+    (4200, 4, 1, list(range(0, 4201, 2)), True),           # 2100 sequences of two tokens
 ])
 def test_balance_loss_sequences(T, E, k, off, masked):
     say(f"balance sequences T={T} E={E} k={k} S={len(off) - 1}")
@@ -591,6 +595,81 @@ def test_adamw_refuses_a_capture_that_would_repeat_its_step():
     torch.cuda.synchronize()
     opt.step()
     assert opt.step_count == 1
+
+
+def test_adamw_refuses_moved_tensors_and_another_device():
+    say("adamw refusals of moved tensors")
+    p, g = torch.ones(100, device=DEV), torch.ones(100, device=DEV)
+    opt = ops.MoEAdamW([p], [g], max_grad_norm=1.0, **H)
+    opt.step()
+    kept = p.clone()
+    for t, name in ((p, "params"), (g, "grads")):
+        old = t.data
+        t.data = torch.ones(100, device=DEV)
+        with pytest.raises(RuntimeError, match=name):
+            opt.step()
+        t.data = old
+    with pytest.raises(RuntimeError, match="moe_grad_norm"):
+        lst = ops.grad_list([g])
+        g.data = torch.ones(100, device=DEV)
+        ops.moe_grad_norm(lst, 1.0, torch.zeros(2, device=DEV), ops.workspace(4096))
+    opt._device += 1
+    with pytest.raises(RuntimeError, match="current"):
+        opt.step()
+    assert torch.equal(p, kept) and opt.step_count == 1
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("betas", [(0.0, 0.0), (0.0, 0.99), (0.9, 0.0)])
+def test_adamw_without_memory(bits, betas):
+    """beta1 or beta2 of zero, with the step's number on the host and on the device."""
+    say(f"adamw betas={betas} bits={bits}")
+    got = []
+    for capturable in (False, True):
+        whole, params, grads, states = _make([777], bits, "f", "f", False, seed=40)
+        before = _snapshot(params, grads, states)
+        ops.MoEAdamW(params, grads, lr=2.0 ** -7, betas=betas, eps=1e-8, weight_decay=0.5, state_bits=bits,
+                     states=states, step=2, capturable=capturable).step()
+        torch.cuda.synchronize()
+        got.append([w.clone() for w in whole])
+    s0 = before[0][2]
+    m0 = s0["m"].astype(np.float64) if bits == 32 else oracle.read_m(s0["m"], s0["m_scale"])
+    v0 = s0["v"].astype(np.float64) if bits == 32 else oracle.read_v(s0["v"], s0["v_scale"])
+    g0 = before[0][1].astype(np.float64)
+    w, m, v = oracle.adamw_step(before[0][0], g0, m0, v0, 3, 2.0 ** -7, betas[0], betas[1], 1e-8, 0.5)
+    parts = np.abs(betas[0] * m0) + np.abs((1 - betas[0]) * g0)
+    den = np.sqrt(v) / np.sqrt(1 - betas[1] ** 3) + 1e-8
+    bound = 3 * U * np.abs(before[0][0]) + 16 * U * 2.0 ** -7 / (1 - betas[0] ** 3) * parts / den + 1e-44
+    assert np.all(np.abs(to_np(params[0]) - w) <= bound)
+    if bits == 8:
+        assert np.array_equal(to_np(states[0]["m"]), oracle.held_m(m)[0])
+        assert np.array_equal(to_np(states[0]["v"]), oracle.held_v(v)[0])
+    assert all(torch.equal(a, b) for a, b in zip(*got))  # the same scalars: a rate that is a float
+
+
+def test_adamw_8bit_blocks_of_the_smallest_floats():
+    """Scales from the smallest normal float up to where the float path takes over, and values far below them."""
+    say("adamw 8-bit blocks of tiny values")
+    rng = np.random.default_rng(41)
+    scales = 10.0 ** np.arange(-19, -9, 0.25)  # gradients; their squares reach 1e-38
+    g = np.concatenate([s * rng.standard_normal(256) * np.exp(-rng.random(256) * 9) for s in scales])
+    p, gd = torch.ones(g.size, device=DEV), torch.tensor(g, dtype=torch.float32, device=DEV)
+    opt = ops.MoEAdamW([p], [gd], lr=1e-2, betas=(0.5, 0.5), eps=1e-18, weight_decay=0.0, state_bits=8)
+    for t in (1, 2, 3):
+        before = _snapshot([p], [gd], opt.states)
+        opt.step()
+        torch.cuda.synchronize()
+        s0, s = before[0][2], opt.states[0]
+        m0, v0 = oracle.read_m(s0["m"], s0["m_scale"]), oracle.read_v(s0["v"], s0["v_scale"])
+        g0 = before[0][1].astype(np.float64)
+        w, m, v = oracle.adamw_step(before[0][0], g0, m0, v0, t, 1e-2, 0.5, 0.5, 1e-18, 0.0)
+        (cm, sm), (cv, sv) = oracle.held_m(m), oracle.held_v(v)
+        assert np.array_equal(to_np(s["m_scale"]), sm) and np.array_equal(to_np(s["v_scale"]), sv)
+        assert np.array_equal(to_np(s["m"]), cm) and np.array_equal(to_np(s["v"]), cv)
+        parts = np.abs(0.5 * m0) + np.abs(0.5 * g0)
+        den = np.sqrt(v) / np.sqrt(1 - 0.5 ** t) + 1e-18
+        assert np.all(np.abs(to_np(p) - w) <= 3 * U * np.abs(w) + 16 * U * 1e-2 / (1 - 0.5 ** t) * parts / den)
+        gd.mul_(-0.6)
 
 
 def test_adamw_on_another_stream_and_two_lists_at_once():
