@@ -23,12 +23,6 @@ constexpr int BL_COUNT_THREADS = 1024;
 constexpr int BL_WAVES = 4, BL_THREADS = 64 * BL_WAVES;  // main pass
 constexpr int BL_BINS = 4096;                            // LDS bins of a block that counts
 
-struct Span {
-  int seq;    // -1: none
-  int first;  // index of the sequence's first chunk
-  int begin, end;
-};
-
 __device__ __forceinline__ void seq_range(const int32_t *off, int T, int s, int &b, int &e) {
   if (!off) {
     b = 0;
@@ -40,45 +34,49 @@ __device__ __forceinline__ void seq_range(const int32_t *off, int T, int s, int 
   e = min(max(off[s + 1], b), T);
 }
 
-// Chunk `lin` when every sequence is cut into pieces of `chunk` tokens, numbered sequence
-// after sequence; total chunks in `total` when the chunk is past the last.  One wavefront
-// scans the offsets; equal in every lane.
-__device__ __forceinline__ Span find_span(const int32_t *off, int S, int T, int chunk, int lin, int &total) {
-  Span r{-1, 0, 0, 0};
-  if (S == 1) {
-    int b, e;
-    seq_range(off, T, 0, b, e);
-    total = (e - b + chunk - 1) / chunk;
-    if (lin < total) r = Span{0, 0, b + lin * chunk, min(e, b + (lin + 1) * chunk)};
-    return r;
-  }
+// Every pass cuts the batch into chunks of tokens whatever the sequences; the tokens of one
+// sequence in one chunk are a piece, and a block's work.  With offsets the rows before the
+// first sequence count as sequence -1 and those behind the last as sequence S (they only get
+// their zero gradient), and the piece of sequence s in chunk b has the number b + s + 1:
+// neighbouring pieces differ in one of the two, so numbers do not meet, those of a sequence
+// lie together, and no sum over the sequences before is needed.  Without offsets the pieces
+// are the chunks.
+struct Piece {
+  int seq, begin, end;  // begin == end: no piece has the number
+};
+
+__device__ __forceinline__ int begin_of(const int32_t *off, int T, int s) {  // s in [-1, S]
+  return s < 0 ? 0 : min(max(off[s], 0), T);
+}
+
+// The piece numbered x: the last sequence whose first piece's number is not past x, looked for
+// by one wavefront in 64 places at a time.  Equal in every lane.
+__device__ __forceinline__ Piece find_piece(const int32_t *off, int S, int T, int chunk, int x) {
+  if (!off) return Piece{0, min(x * chunk, T), (int)min((int64_t)(x + 1) * chunk, (int64_t)T)};
   const int lane = threadIdx.x & 63;
-  int base = 0;
-  for (int s0 = 0; s0 < S; s0 += 64) {
-    const int s = s0 + lane;
-    int b = 0, e = 0;
-    if (s < S) seq_range(off, T, s, b, e);
-    const int n = (e - b + chunk - 1) / chunk;
-    int incl = n;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(incl, o, 64);
-      if (lane >= o) incl += v;
-    }
-    const uint64_t hit = __ballot(base + incl > lin);
-    if (hit) {
-      const int l = __ffsll((unsigned long long)hit) - 1;
-      r.seq = s0 + l;
-      r.first = base + __shfl(incl - n, l, 64);
-      const int sb = __shfl(b, l, 64), se = __shfl(e, l, 64);
-      r.begin = sb + (lin - r.first) * chunk;
-      r.end = min(se, r.begin + chunk);
-      return r;
-    }
-    base += __shfl(incl, 63, 64);
+  int lo = -1, n = S + 2;  // among sequences lo .. lo + n - 1
+  int b = 0;
+  while (n > 1) {
+    const int step = (n + 63) / 64, s = lo + lane * step;
+    b = s <= S && lane * step < n ? begin_of(off, T, s) : 0;
+    const bool at = s <= S && lane * step < n && b / chunk + s + 1 <= x;
+    const int last = max(__popcll(__ballot(at)) - 1, 0);
+    n = min(step, n - last * step);
+    lo += last * step;
   }
-  total = base;
-  return r;
+  b = begin_of(off, T, lo);
+  const int e = lo == S ? T : max(min(off[lo + 1], T), b);
+  const int64_t c0 = (int64_t)(x - lo - 1) * chunk;  // the piece's chunk
+  const int begin = (int)min(max(c0, (int64_t)b), (int64_t)T);
+  return Piece{lo, begin, max((int)min(c0 + chunk, (int64_t)e), begin)};
+}
+
+// The numbers of sequence s's pieces (s in [0, S)): first .. first + n - 1.
+__device__ __forceinline__ void seq_pieces(const int32_t *off, int T, int s, int chunk, int &first, int &n) {
+  int b, e;
+  seq_range(off, T, s, b, e);
+  first = b / chunk + (off ? s + 1 : 0);
+  n = e > b ? (e - 1) / chunk - b / chunk + 1 : 0;
 }
 
 // Reductions over groups of LPT neighbouring lanes, the result in every lane: lane moves
@@ -131,6 +129,24 @@ __device__ __forceinline__ void block_sum2(double &x, double &y, double (*s_red)
     }
 }
 
+// Sum of column values p[q * stride] over q = from, from + step, ... < n, eight loads in flight.
+template <typename Sum, typename T>
+__device__ __forceinline__ Sum column_sum(const T *p, size_t stride, int from, int n, int step) {
+  Sum sum = 0;
+  if (from >= n) return sum;
+  p += (size_t)from * stride;
+  const uint32_t inc = (uint32_t)step * (uint32_t)stride;
+  int left = (n - from + step - 1) / step;  // values
+  for (; left > 0; left -= 8, p += 8 * (size_t)inc) {
+    T v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = p[(uint32_t)min(j, left - 1) * inc];  // (the last value again past the end)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += j < left ? (Sum)v[j] : Sum(0);
+  }
+  return sum;
+}
+
 // ---------------------------------------------------------------------------------- counts
 
 // Choices and counted tokens of tokens [begin, end) into bins in LDS: bins[copies][E], then
@@ -150,18 +166,17 @@ __device__ __forceinline__ void count_chunk_lds(int32_t *bins, int copies, const
   for (uint32_t i0 = threadIdx.x; i0 < n; i0 += B * THREADS) {
     int e[B];
 #pragma unroll
-    for (int j = 0; j < B; ++j) e[j] = i0 + j * THREADS < n ? src[i0 + j * THREADS] : -1;
+    for (int j = 0; j < B; ++j) e[j] = src[min(i0 + j * THREADS, n - 1)];  // (no load waits for a condition)
     if (mask) {
       uint8_t in[B];
 #pragma unroll
-      for (int j = 0; j < B; ++j)
-        in[j] = i0 + j * THREADS < n ? mask[begin + (i0 + j * THREADS) / (uint32_t)k] : 0;
+      for (int j = 0; j < B; ++j) in[j] = mask[begin + min(i0 + j * THREADS, n - 1) / (uint32_t)k];
 #pragma unroll
       for (int j = 0; j < B; ++j) e[j] = in[j] ? e[j] : -1;
     }
 #pragma unroll
     for (int j = 0; j < B; ++j)
-      if (e[j] >= 0 && e[j] < E) atomicAdd(&mine[e[j]], 1);
+      if (i0 + j * THREADS < n && e[j] >= 0 && e[j] < E) atomicAdd(&mine[e[j]], 1);
   }
   if (mask) {
     for (int t = begin + (int)threadIdx.x; t < end; t += THREADS) tokens += mask[t] != 0;
@@ -179,103 +194,102 @@ __device__ __forceinline__ void count_chunk_lds(int32_t *bins, int copies, const
   __syncthreads();
 }
 
-// What a counting block wrote: its sequence (-1: none) and the tokens it counted there.
-struct ChunkTokens {
-  int32_t seq, tokens;
+// What a counting block found: counted tokens, and the bit of their sequence (up to 64).
+struct PieceTokens {
+  int32_t tokens, pad;
+  uint64_t seq;
 };
 
-// Counts of one chunk: choices in part[block][0..E-1], tokens in chunks[block].
+// Counts of one piece: choices in part[piece][0..E-1], tokens in tokens[piece].
 __global__ __launch_bounds__(BL_COUNT_THREADS) void balance_count_kernel(const int32_t *__restrict__ ids,
                                                                          const uint8_t *__restrict__ mask,
                                                                          const int32_t *__restrict__ off, int T, int E,
                                                                          int k, int S, int chunk, int copies,
                                                                          int32_t *__restrict__ part,
-                                                                         ChunkTokens *__restrict__ chunks) {
+                                                                         PieceTokens *__restrict__ tokens) {
   extern __shared__ int32_t s_mem[];
-  int total = 0;
-  const Span sp = find_span(off, S, T, chunk, blockIdx.x, total);
-  if (sp.seq < 0) {  // equal in every thread
-    if (threadIdx.x == 0) chunks[blockIdx.x] = ChunkTokens{-1, 0};
+  const Piece pc = find_piece(off, S, T, chunk, blockIdx.x);
+  if (pc.begin >= pc.end || pc.seq < 0 || pc.seq >= S) {  // equal in every thread
+    if (threadIdx.x == 0) tokens[blockIdx.x] = PieceTokens{0, 0, 0};
     return;
   }
-  count_chunk_lds<BL_COUNT_THREADS>(s_mem, copies, ids, mask, sp.begin, sp.end, E, k);
-  int32_t *out = part + (size_t)blockIdx.x * E;
-  for (int e = threadIdx.x; e < E; e += BL_COUNT_THREADS) out[e] = s_mem[e];
-  if (threadIdx.x == 0) chunks[blockIdx.x] = ChunkTokens{sp.seq, s_mem[copies * E]};
+  count_chunk_lds<BL_COUNT_THREADS>(s_mem, copies, ids, mask, pc.begin, pc.end, E, k);
+  for (int e = threadIdx.x; e < E; e += BL_COUNT_THREADS) part[(size_t)blockIdx.x * E + e] = s_mem[e];
+  if (threadIdx.x == 0) {
+    const int n = s_mem[copies * E];
+    tokens[blockIdx.x] = PieceTokens{n, 0, n > 0 && pc.seq < 64 ? 1ull << pc.seq : 0};
+  }
 }
 
-// One block a sequence: its counts and counted tokens from the chunks', and the index of its
-// first block of the main pass.
+// Counted tokens of a sequence from its pieces', in every lane.
+__device__ __forceinline__ int seq_count(const PieceTokens *tokens, int first, int n) {
+  int c = 0;
+  for (int q = threadIdx.x & 63; q < n; q += 64) c += tokens[first + q].tokens;
+  return group_reduce<64>(c, add);
+}
+// Counted tokens of the whole batch and sequences that count any (up to 64).
+__device__ __forceinline__ void batch_count(const PieceTokens *tokens, int n, int &all, int &live) {
+  int c = 0;
+  uint64_t seen = 0;
+  for (int q = threadIdx.x & 63; q < n; q += 64) {
+    const PieceTokens p = tokens[q];
+    c += p.tokens;
+    seen |= p.seq;
+  }
+  all = group_reduce<64>(c, add);
+  const auto either = [](uint32_t x, uint32_t y) { return x | y; };
+  live = __popc(group_reduce<64>((uint32_t)seen, either)) + __popc(group_reduce<64>((uint32_t)(seen >> 32), either));
+}
+
+// The sums of the counting blocks' results.  Block s * parts + q: 64 experts of sequence s, four
+// threads an expert.  The last block: sequences that count a token, and tokens in all.
 __global__ __launch_bounds__(256) void balance_tables_kernel(const int32_t *__restrict__ off, int T, int E, int S,
-                                                             int chunk, int main_chunk, int blocks, int main_blocks,
+                                                             int chunk, int parts, int blocks,
                                                              const int32_t *__restrict__ part,
-                                                             const ChunkTokens *__restrict__ chunks,
+                                                             const PieceTokens *__restrict__ tokens,
                                                              int32_t *__restrict__ counts,
                                                              int32_t *__restrict__ seq_tokens,
-                                                             int32_t *__restrict__ first_main) {
-  const int s = blockIdx.x;
-  const int lane = threadIdx.x & 63;
-  int first = 0, fm = 0;
-  for (int q = lane; q < s; q += 64) {
-    int b, e;
-    seq_range(off, T, q, b, e);
-    first += (e - b + chunk - 1) / chunk;
-    fm += (e - b + main_chunk - 1) / main_chunk;
+                                                             int32_t *__restrict__ totals) {
+  __shared__ int s_c[4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int first, n, c = 0;
+  if (blockIdx.x == (unsigned)(S * parts)) {
+    int live = 0;
+    for (int s = threadIdx.x; s < S; s += 256) {
+      seq_pieces(off, T, s, chunk, first, n);
+      n = min(n, blocks - first);  // (offsets that run backwards could name more pieces)
+      int mine = 0;
+      for (int q = 0; q < n; ++q) mine += tokens[first + q].tokens;
+      c += mine;
+      live += mine > 0;
+    }
+    c = group_reduce<64>(c, add);
+    live = group_reduce<64>(live, add);
+    if (lane == 0) {
+      s_c[wave][0] = live;
+      s_c[wave][1] = c;
+    }
+    __syncthreads();
+    if (threadIdx.x < 2)
+      totals[threadIdx.x] = s_c[0][threadIdx.x] + s_c[1][threadIdx.x] + s_c[2][threadIdx.x] + s_c[3][threadIdx.x];
+    return;
   }
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) {
-    first += __shfl_xor(first, o, 64);
-    fm += __shfl_xor(fm, o, 64);
-  }
-  int b, e;
-  seq_range(off, T, s, b, e);
-  // (offsets that run backwards could name more chunks than there are)
-  const int n = min((e - b + chunk - 1) / chunk, max(blocks - first, 0));
-  for (int i = threadIdx.x; i < E; i += 256) {
-    int c = 0;
-#pragma unroll 8
-    for (int q = 0; q < n; ++q) c += part[(size_t)(first + q) * E + i];
-    counts[(size_t)s * E + i] = c;
-  }
-  if (threadIdx.x < 64) {
-    int c = 0;
-    for (int q = lane; q < n; q += 64) c += chunks[first + q].tokens;
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) c += __shfl_xor(c, o, 64);
-    if (lane == 0) seq_tokens[s] = c;
-  }
-  if (threadIdx.x == 0) {
-    first_main[s] = min(fm, main_blocks);
-    if (s == S - 1) first_main[S] = min(fm + (e - b + main_chunk - 1) / main_chunk, main_blocks);
+  const int s = blockIdx.x / parts, q0 = blockIdx.x - s * parts, e = q0 * 64 + lane;
+  seq_pieces(off, T, s, chunk, first, n);
+  n = min(n, blocks - first);
+  if (e < E) c = column_sum<int>(part + (size_t)first * E + e, E, wave, n, 4);
+  s_c[wave][lane] = c;
+  __syncthreads();
+  if (wave == 0) {
+    if (e < E) counts[(size_t)s * E + e] = s_c[0][lane] + s_c[1][lane] + s_c[2][lane] + s_c[3][lane];
+    if (q0 == 0) {
+      const int t = seq_count(tokens, first, n);
+      if (lane == 0) seq_tokens[s] = t;
+    }
   }
 }
 
 // ------------------------------------------------------------------------------- main pass
-
-// Chunks of sequence `seq` among the counting blocks' (they are neighbours), its tokens, the
-// tokens and the sequences that count any of all of them (up to 64).
-struct SeqCounts {
-  int first, n, tokens, all, live;
-};
-__device__ __forceinline__ SeqCounts seq_counts(const ChunkTokens *chunks, int blocks, int seq) {
-  const int lane = threadIdx.x & 63;
-  SeqCounts r{0, 0, 0, 0, 0};
-  uint64_t seen = 0;
-  for (int c0 = 0; c0 < blocks; c0 += 64) {
-    const ChunkTokens c = c0 + lane < blocks ? chunks[c0 + lane] : ChunkTokens{-1, 0};
-    const uint64_t mine = __ballot(c.seq == seq);
-    if (mine && r.n == 0) r.first = c0 + __ffsll((unsigned long long)mine) - 1;
-    r.n += __popcll(mine);
-    if (c.seq == seq) r.tokens += c.tokens;
-    r.all += c.tokens;
-    if (c.tokens > 0) seen |= 1ull << c.seq;
-  }
-  r.tokens = group_reduce<64>(r.tokens, add);
-  r.all = group_reduce<64>(r.all, add);
-  const auto either = [](uint32_t x, uint32_t y) { return x | y; };
-  r.live = __popc(group_reduce<64>((uint32_t)seen, either)) + __popc(group_reduce<64>((uint32_t)(seen >> 32), either));
-  return r;
-}
 
 struct BalanceArgs {
   const float *logits;
@@ -286,18 +300,25 @@ struct BalanceArgs {
   int32_t *seq_tokens;
   const float *dloss;  // upstream gradients of the two losses, or NULL (ones)
   float *dlogits;      // or NULL
-  float *part;         // [blocks][E]: column sums of p
+  float *part;         // [pieces][E]: column sums of p
   double *sums;        // [blocks][2]: sum of sum_i f_i p_ti / N_s, sum of z^2 (a finite z's square can pass
                        // the largest float)
-  const int32_t *cpart;       // the counting blocks' results, added up by each block for itself,
-  const ChunkTokens *chunks;  // or NULL: counts and seq_tokens hold them
-  int cblocks;
+  // the counting blocks' results, added up by each block for itself, or NULL: counts,
+  // seq_tokens and totals (NULL: seq_tokens) hold the sums
+  const int32_t *cpart;
+  const PieceTokens *ctokens;
+  int cblocks, cchunk;
+  const int32_t *totals;
   float *mean_probs, *losses;
   int T, E, k, S, chunk, copies, cols;
   int one;  // the only block: it finishes too
   float alpha, beta;
 };
 
+// Values of a lane that every row of such a kernel has (values LPT apart; see values_per_lane).
+constexpr int sure_values(int lpt, int values) {
+  return values > 12 ? 12 : values > 4 ? values - 2 : lpt > 1 ? 3 : 0;
+}
 constexpr int at_once(int values) { return values <= 4 ? 4 : values <= 8 ? 2 : 1; }
 
 // A token's row in LPT lanes of up to 16 values each, 64 / LPT tokens a wavefront: few lanes a
@@ -318,108 +339,130 @@ __global__ __launch_bounds__(BL_THREADS) void balance_main_kernel(BalanceArgs a)
   const int li = lane & (LPT - 1), sub = lane / LPT;
   const int E = a.E;
   auto expert = [&](int v) { return VEC ? 4 * (li + LPT * (v / 4)) + v % 4 : li + LPT * v; };
-  int total = 0;
-  const Span sp = find_span(a.off, a.S, a.T, a.chunk, blockIdx.x, total);
-  if (sp.seq < 0) {
-    // blocks past the last chunk: rows outside every sequence get a zero gradient
-    if (a.dlogits && a.off) {
-      int b0, e0, b1, e1;
-      seq_range(a.off, a.T, 0, b0, e0);
-      seq_range(a.off, a.T, a.S - 1, b1, e1);
-      const int64_t lead = (int64_t)b0 * E, tail = (int64_t)(a.T - e1) * E;
-      const int64_t step = (int64_t)(gridDim.x - total) * BL_THREADS;
-      for (int64_t i = (int64_t)(blockIdx.x - total) * BL_THREADS + threadIdx.x; i < lead + tail; i += step)
-        a.dlogits[i < lead ? i : i - lead + (int64_t)e1 * E] = 0.f;
+  const Piece pc = find_piece(a.off, a.S, a.T, a.chunk, blockIdx.x);
+  const bool rows = pc.begin < pc.end && pc.seq >= 0 && pc.seq < a.S;
+  const bool self = LOSS && a.ids;
+  if (!rows) {
+    if (a.dlogits) {  // of no sequence: a zero gradient
+      const int64_t to = (int64_t)pc.end * E;
+      for (int64_t i = (int64_t)pc.begin * E + threadIdx.x; i < to; i += BL_THREADS) a.dlogits[i] = 0.f;
     }
-    if (!(LOSS && a.ids && blockIdx.x == 0)) return;  // block 0 counts also where there are no rows
+    if (LOSS && !a.one && threadIdx.x == 0) a.sums[2 * (size_t)blockIdx.x] = a.sums[2 * (size_t)blockIdx.x + 1] = 0.;
+    if (!(self && blockIdx.x == 0)) return;  // block 0 counts also where it has no rows
   }
   float l[NT][VPL];
   bool counted[NT];
-  // rows of uncounted tokens are read and not looked at: the loads do not wait for the mask
+  // No load waits for a condition: rows of uncounted tokens are read and not looked at, tokens
+  // past the piece and values past the row read the last ones.
   auto load = [&](int t0) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int t = t0 + n * TPW + sub;
-      const bool in = t < sp.end;
+      const int t = min(t0 + n * TPW + sub, pc.end - 1);
       const float *row = a.logits + (size_t)t * E;
-      counted[n] = in && (!a.mask || a.mask[t] != 0);
       if constexpr (VEC) {
 #pragma unroll
         for (int v = 0; v < VPL; v += 4) {
-          f32x4 q = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          if (in && expert(v) < E) q = *reinterpret_cast<const f32x4 *>(row + expert(v));
+          const f32x4 q = *reinterpret_cast<const f32x4 *>(row + min(expert(v), E - 4));
 #pragma unroll
           for (int i = 0; i < 4; ++i) l[n][v + i] = q[i];
         }
       } else {
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) l[n][v] = in && expert(v) < E ? row[expert(v)] : -INFINITY;
-      }
-    }
-  };
-  const int t_first = sp.begin + wave * (NT * TPW);
-  load(t_first);  // in flight while the tables are read
-  // sequences that count a token, tokens in all, this sequence's
-  int live = 0, all = 0, ns = 0;
-  float f[VPL];
-  if (LOSS && a.ids) {
-    int b, e;
-    seq_range(a.off, a.T, 0, b, e);
-    count_chunk_lds<BL_THREADS>(s_mem, a.copies, a.ids, a.mask, b, e, E, a.k);
-    ns = all = s_mem[a.copies * E];
-    live = ns > 0;
-    if (blockIdx.x == 0) {
-      for (int i = threadIdx.x; i < E; i += BL_THREADS) a.counts[i] = s_mem[i];
-      if (threadIdx.x == 0) {
-        a.seq_tokens[0] = ns;
+        for (int v = 0; v < VPL; ++v) l[n][v] = row[v < sure_values(LPT, VPL) ? expert(v) : min(expert(v), E - 1)];
       }
     }
 #pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int t = t0 + n * TPW + sub;
+      counted[n] = t < pc.end;
+      if (a.mask) counted[n] = counted[n] && a.mask[min(t, pc.end - 1)] != 0;
+    }
+  };
+  const int t_first = pc.begin + wave * (NT * TPW);
+  if (rows) load(t_first);  // in flight while the tables are read
+  // sequences that count a token, tokens in all
+  int live = 0, all = 0;
+  if (self) {
+    int b, e;
+    seq_range(a.off, a.T, 0, b, e);
+    count_chunk_lds<BL_THREADS>(s_mem, a.copies, a.ids, a.mask, b, e, E, a.k);
+    all = s_mem[a.copies * E];
+    live = all > 0;
+    if (blockIdx.x == 0) {
+      for (int i = threadIdx.x; i < E; i += BL_THREADS) a.counts[i] = s_mem[i];
+      if (threadIdx.x == 0) a.seq_tokens[0] = all;
+      if (!rows) return;  // equal in every thread
+    }
+  } else if (LOSS && a.ctokens) {
+    batch_count(a.ctokens, a.cblocks, all, live);
+  } else if (LOSS) {
+    live = a.totals[0];
+    all = a.totals[1];
+  } else {
+    if (a.S <= 64) {
+      if (lane < a.S) all = a.seq_tokens[lane];
+      live = group_reduce<64>(all > 0 ? 1 : 0, add);
+      all = group_reduce<64>(all, add);
+    } else {
+      __shared__ int s_tot[BL_WAVES][2];
+      for (int s = threadIdx.x; s < a.S; s += BL_THREADS) {
+        const int n = a.seq_tokens[s];
+        live += n > 0;
+        all += n;
+      }
+      live = group_reduce<64>(live, add);
+      all = group_reduce<64>(all, add);
+      if (lane == 0) {
+        s_tot[wave][0] = live;
+        s_tot[wave][1] = all;
+      }
+      __syncthreads();
+      live = all = 0;
+#pragma unroll
+      for (int w = 0; w < BL_WAVES; ++w) {
+        live += s_tot[w][0];
+        all += s_tot[w][1];
+      }
+    }
+  }
+  const float up0 = a.dloss ? a.dloss[0] : 1.f, up1 = a.dloss ? a.dloss[1] : 1.f;
+  const float cb = up1 * (2.f * a.beta / (float)max(all, 1));
+  // the sequence's counted tokens, and its experts' shares of the choices
+  int ns = all;
+  float f[VPL], acc[VPL];
+  if (self) {
+#pragma unroll
     for (int v = 0; v < VPL; ++v) f[v] = expert(v) < E ? (float)s_mem[expert(v)] : 0.f;
     __syncthreads();
-  } else if (LOSS && a.chunks) {
+  } else if (LOSS && a.ctokens) {
+    int first, n;
+    seq_pieces(a.off, a.T, pc.seq, a.cchunk, first, n);
+    n = min(n, a.cblocks - first);
+    if (a.S > 1) ns = seq_count(a.ctokens, first, n);
     for (int e = threadIdx.x; e < E; e += BL_THREADS) s_mem[e] = 0;
-    const SeqCounts sc = seq_counts(a.chunks, a.cblocks, sp.seq);
-    live = sc.live;
-    all = sc.all;
-    ns = sc.tokens;
     __syncthreads();
-    // threads on neighbouring experts (cols: a power of two), the others on further chunks
-    const int col = threadIdx.x & (a.cols - 1), row = threadIdx.x / a.cols, rows = BL_THREADS / a.cols;
-    for (int e = col; e < E; e += a.cols) {
-      int c = 0;
-#pragma unroll 8
-      for (int q = row; q < sc.n; q += rows) c += a.cpart[(size_t)(sc.first + q) * E + e];
-      atomicAdd(&s_mem[e], c);
-    }
+    // threads on neighbouring experts (cols: a power of two), the others on further pieces
+    const int col = threadIdx.x & (a.cols - 1), row = threadIdx.x / a.cols, step = BL_THREADS / a.cols;
+    for (int e = col; e < E; e += a.cols)
+      atomicAdd(&s_mem[e], column_sum<int>(a.cpart + (size_t)first * E + e, E, row, n, step));
     __syncthreads();
 #pragma unroll
     for (int v = 0; v < VPL; ++v) f[v] = expert(v) < E ? (float)s_mem[expert(v)] : 0.f;
     __syncthreads();
   } else {
-    for (int s = lane; s < a.S; s += 64) {
-      const int n = a.seq_tokens[s];
-      live += n > 0;
-      all += n;
-    }
-    live = group_reduce<64>(live, add);
-    all = group_reduce<64>(all, add);
-    ns = a.seq_tokens[sp.seq];
+    ns = a.seq_tokens[pc.seq];
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) f[v] = expert(v) < E ? (float)a.counts[(size_t)sp.seq * E + expert(v)] : 0.f;
+    for (int v = 0; v < VPL; ++v) f[v] = expert(v) < E ? (float)a.counts[(size_t)pc.seq * E + expert(v)] : 0.f;
   }
-  const float up0 = a.dloss ? a.dloss[0] : 1.f, up1 = a.dloss ? a.dloss[1] : 1.f;
   const float ca = up0 * (a.alpha * (float)E / ((float)max(live, 1) * (float)max(ns, 1)));
-  const float cb = up1 * (2.f * a.beta / (float)max(all, 1));
   const float fden = (float)max(ns, 1) * (float)a.k;
-  float acc[VPL];
   double bacc = 0., zacc = 0.;
 #pragma unroll
   for (int v = 0; v < VPL; ++v) {
     f[v] /= fden;
     acc[v] = 0.f;
   }
-  for (int t0 = t_first; t0 < sp.end; t0 += BL_WAVES * NT * TPW) {
+  for (int t0 = t_first; t0 < pc.end; t0 += BL_WAVES * NT * TPW) {
     if (t0 != t_first) load(t0);
     float base[NT], sum[NT], dot[NT];
 #pragma unroll
@@ -427,7 +470,7 @@ __global__ __launch_bounds__(BL_THREADS) void balance_main_kernel(BalanceArgs a)
       float m = -INFINITY;
 #pragma unroll
       for (int v = 0; v < VPL; ++v) {
-        l[n][v] = counted[n] ? l[n][v] : -INFINITY;
+        l[n][v] = counted[n] && expert(v) < E ? l[n][v] : -INFINITY;
         m = fmaxf(m, l[n][v]);
       }
       m = group_reduce<LPT>(m, [](float x, float y) { return fmaxf(x, y); });
@@ -464,7 +507,8 @@ __global__ __launch_bounds__(BL_THREADS) void balance_main_kernel(BalanceArgs a)
         l[n][v] *= inv;
         if constexpr (LOSS) acc[v] += l[n][v];
       }
-      if (a.dlogits && t < sp.end) {
+      // written once and not read here: past the caches (16384 x 256: 13.0 -> 11.5 us)
+      if (a.dlogits && t < pc.end) {
         float *drow = a.dlogits + (size_t)t * E;
         if constexpr (VEC) {
 #pragma unroll
@@ -477,7 +521,8 @@ __global__ __launch_bounds__(BL_THREADS) void balance_main_kernel(BalanceArgs a)
         } else {
 #pragma unroll
           for (int v = 0; v < VPL; ++v)
-            if (expert(v) < E) __builtin_nontemporal_store(l[n][v] * __builtin_fmaf(ca, f[v], -shift), drow + expert(v));
+            if (expert(v) < E)
+              __builtin_nontemporal_store(l[n][v] * __builtin_fmaf(ca, f[v], -shift), drow + expert(v));
         }
       }
     }
@@ -520,89 +565,64 @@ struct FinishArgs {
   const float *part;
   const double *sums;
   const int32_t *off;
-  const int32_t *first_main;  // with the tables, or NULL
-  const int32_t *cpart;       // without them: the counting blocks' results (chunks), or NULL
-  const ChunkTokens *chunks;
+  const int32_t *cpart;  // the counting blocks' results, or NULL: counts, seq_tokens and totals
+  const PieceTokens *ctokens;  // (NULL: one sequence) hold the sums
+  const int32_t *totals;
   int32_t *counts, *seq_tokens;
   float *mean_probs, *losses;
-  int T, E, S, chunk, blocks, cblocks, cols, parts;
+  int T, E, S, chunk, blocks, cchunk, cblocks, cols, parts;
   float alpha, beta;
 };
 
-// Block s < S * parts: `cols` (a power of two) of a sequence's mean probabilities, threads on
-// neighbouring experts and on further blocks of the main pass.  The last block: the two
-// losses, since sum_i f_si P_si is the mean over the sequence's tokens of sum_i f_si p_ti.
+// Block s < S * parts: `cols` (a power of two, at most 32) of a sequence's mean probabilities,
+// threads on neighbouring experts and on further pieces of the main pass.  The last block: the
+// two losses, since sum_i f_si P_si is the mean over the sequence's tokens of sum_i f_si p_ti.
 __global__ __launch_bounds__(BL_FIN_THREADS) void balance_finish_kernel(FinishArgs a) {
   __shared__ double s_p[BL_FIN_WAVES][32];
   __shared__ int s_c[BL_FIN_WAVES][32];
   __shared__ double s_red[BL_FIN_WAVES][2];
   const int S = a.S, E = a.E;
-  const bool losses = blockIdx.x == (unsigned)(S * a.parts);
-  const int s = losses ? S - 1 : blockIdx.x / a.parts;
-  // blocks of the main pass: of sequence s, and in all
-  int b0, b1, nb;
-  if (a.first_main) {
-    b0 = a.first_main[s];
-    b1 = a.first_main[s + 1];
-    nb = a.first_main[S];
-  } else {
-    const int lane = threadIdx.x & 63;  // of sequence: S <= 64
-    int b = 0, e = 0;
-    if (lane < S) seq_range(a.off, a.T, lane, b, e);
-    const int n = (e - b + a.chunk - 1) / a.chunk;
-    int incl = n;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(incl, o, 64);
-      if (lane >= o) incl += v;
-    }
-    // (offsets that run backwards could name more blocks than there are)
-    b0 = min(__shfl(incl - n, s, 64), a.blocks);
-    b1 = min(__shfl(incl, s, 64), a.blocks);
-    nb = min(__shfl(incl, S - 1, 64), a.blocks);
-  }
-  if (losses) {
-    double bal = 0, z = 0, live = 0, all = 0;
-    for (int b = threadIdx.x; b < nb; b += BL_FIN_THREADS) {
+  if (blockIdx.x == (unsigned)(S * a.parts)) {
+    double bal = 0, z = 0;
+    for (int b = threadIdx.x; b < a.blocks; b += BL_FIN_THREADS) {
       bal += a.sums[2 * (size_t)b];
       z += a.sums[2 * (size_t)b + 1];
     }
-    if (a.chunks) {
-      const SeqCounts sc = seq_counts(a.chunks, a.cblocks, s);
-      if (threadIdx.x == 0) {
-        live = sc.live;
-        all = sc.all;
-      }
+    int live, all;
+    if (a.ctokens) {
+      batch_count(a.ctokens, a.cblocks, all, live);
+    } else if (a.totals) {
+      live = a.totals[0];
+      all = a.totals[1];
     } else {
-      for (int q = threadIdx.x; q < S; q += BL_FIN_THREADS) {
-        live += a.seq_tokens[q] > 0;
-        all += a.seq_tokens[q];
-      }
+      all = a.seq_tokens[0];
+      live = 1;
     }
     block_sum2<BL_FIN_WAVES>(bal, z, s_red);
-    block_sum2<BL_FIN_WAVES>(live, all, s_red);
     if (threadIdx.x == 0) {
-      a.losses[0] = (float)((double)a.alpha * E * bal / max(live, 1.0));
-      a.losses[1] = (float)((double)a.beta * z / max(all, 1.0));
+      a.losses[0] = (float)((double)a.alpha * E * bal / max(live, 1));
+      a.losses[1] = (float)((double)a.beta * z / max(all, 1));
     }
     return;
   }
+  const int s = blockIdx.x / a.parts;
   const int col = threadIdx.x & (a.cols - 1), row = threadIdx.x / a.cols, rows = BL_FIN_THREADS / a.cols;
   const int part = blockIdx.x - s * a.parts, e = part * a.cols + col;
-  SeqCounts sc{0, 0, 0, 0, 0};
-  int n, c = 0;
-  if (a.chunks) {
-    sc = seq_counts(a.chunks, a.cblocks, s);
-    n = sc.tokens;
-    if (part == 0 && threadIdx.x == 0) a.seq_tokens[s] = n;
+  int first, n, cfirst = 0, cn = 0, tokens, c = 0;
+  seq_pieces(a.off, a.T, s, a.chunk, first, n);
+  n = min(n, a.blocks - first);  // (offsets that run backwards could name more pieces)
+  if (a.ctokens) {
+    seq_pieces(a.off, a.T, s, a.cchunk, cfirst, cn);
+    cn = min(cn, a.cblocks - cfirst);
+    tokens = seq_count(a.ctokens, cfirst, cn);
+    if (part == 0 && threadIdx.x == 0) a.seq_tokens[s] = tokens;
   } else {
-    n = a.seq_tokens[s];
+    tokens = a.seq_tokens[s];
   }
   double p = 0;
   if (e < E) {
-#pragma unroll 8
-    for (int b = b0 + row; b < b1; b += rows) p += a.part[(size_t)b * E + e];
-    for (int q = row; q < sc.n; q += rows) c += a.cpart[(size_t)(sc.first + q) * E + e];
+    p = column_sum<double>(a.part + (size_t)first * E + e, E, row, n, rows);
+    if (a.ctokens) c = column_sum<int>(a.cpart + (size_t)cfirst * E + e, E, row, cn, rows);
   }
   // rows of one wavefront (cols <= 32), then one row of each
   for (int o = 32; o >= a.cols; o >>= 1) {
@@ -623,8 +643,8 @@ __global__ __launch_bounds__(BL_FIN_THREADS) void balance_finish_kernel(FinishAr
       p += s_p[w][col];
       c += s_c[w][col];
     }
-    a.mean_probs[(size_t)s * E + e] = (float)(p / max(n, 1));
-    if (a.chunks) a.counts[(size_t)s * E + e] = c;
+    a.mean_probs[(size_t)s * E + e] = (float)(p / max(tokens, 1));
+    if (a.ctokens) a.counts[(size_t)s * E + e] = c;
   }
 }
 
@@ -650,12 +670,8 @@ int main_chunk(int T, int E, bool loss) {
   return std::max(BL_WAVES * tokens_at_once(E), (T + blocks - 1) / blocks);
 }
 
-// Chunks of the two passes: sequences cut into whole chunks, at most one partial chunk each,
-// and in the main pass one block more for the rows outside every sequence.
-int count_blocks(int T, int S, bool off) { return (T + count_chunk(T) - 1) / count_chunk(T) + (off ? S : 0); }
-int main_blocks(int T, int E, int S, bool off, bool loss) {
-  return (T + main_chunk(T, E, loss) - 1) / main_chunk(T, E, loss) + (off ? S + 1 : 0);
-}
+// Numbers of the pieces of T tokens in chunks, with S sequences.
+int pieces(int T, int chunk, int S, bool off) { return (T + chunk - 1) / chunk + (off ? S + 1 : 0); }
 
 int bin_copies(int E) {
   int copies = 1;
@@ -706,17 +722,23 @@ hipError_t launch_main(const BalanceArgs &a, int blocks, hipStream_t s) {
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 struct BalanceWs {
-  size_t count_part, chunks, main_part, sums, first_main, total;
+  size_t count_part, count_tokens, totals, main_part, sums, total;
 };
 BalanceWs balance_ws(int T, int E, int S) {
   BalanceWs w;
-  const size_t cb = count_blocks(T, S, true), mb = main_blocks(T, E, S, true, true);
-  w.count_part = 0;
-  w.chunks = align256(cb * E * 4);
-  w.main_part = w.chunks + align256(cb * sizeof(ChunkTokens));
-  w.sums = w.main_part + align256(mb * E * 4);
-  w.first_main = w.sums + align256(mb * 16);
-  w.total = w.first_main + align256(((size_t)S + 1) * 4);
+  const size_t cb = pieces(T, count_chunk(T), S, true), mb = pieces(T, main_chunk(T, E, true), S, true);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align256(bytes);
+    return here;
+  };
+  w.count_part = take(cb * E * 4);
+  w.count_tokens = take(cb * sizeof(PieceTokens));
+  w.totals = take(8);
+  w.main_part = take(mb * E * 4);
+  w.sums = take(mb * 16);
+  w.total = at;
   return w;
 }
 
@@ -736,10 +758,10 @@ hipError_t launch_balance_loss(const BalanceCall &c, int32_t *counts, int32_t *s
   const BalanceWs w = balance_ws(c.T, c.E, c.S);
   uint8_t *base = static_cast<uint8_t *>(ws);
   int32_t *cpart = reinterpret_cast<int32_t *>(base + w.count_part);
-  ChunkTokens *chunks = reinterpret_cast<ChunkTokens *>(base + w.chunks);
-  const bool off = c.off != nullptr;
+  PieceTokens *ctokens = reinterpret_cast<PieceTokens *>(base + w.count_tokens);
+  int32_t *totals = reinterpret_cast<int32_t *>(base + w.totals);
   const int cc = count_chunk(c.T), mc = main_chunk(c.T, c.E, true);
-  const int cb = count_blocks(c.T, c.S, off), mb = main_blocks(c.T, c.E, c.S, off, true);
+  const int cb = pieces(c.T, cc, c.S, c.off != nullptr), mb = pieces(c.T, mc, c.S, c.off != nullptr);
   const int copies = bin_copies(c.E);
   BalanceArgs a{};
   a.logits = c.logits;
@@ -751,7 +773,6 @@ hipError_t launch_balance_loss(const BalanceCall &c, int32_t *counts, int32_t *s
   a.dlogits = c.dlogits;
   a.part = reinterpret_cast<float *>(base + w.main_part);
   a.sums = reinterpret_cast<double *>(base + w.sums);
-  int32_t *first_main = reinterpret_cast<int32_t *>(base + w.first_main);
   a.mean_probs = mean_probs;
   a.losses = losses;
   a.T = c.T;
@@ -763,25 +784,26 @@ hipError_t launch_balance_loss(const BalanceCall &c, int32_t *counts, int32_t *s
   a.alpha = c.alpha;
   a.beta = c.beta;
   hipError_t e;
-  bool tables = false;
   if (c.S == 1 && (int64_t)c.T * c.k <= kSelfCount) {
     a.ids = c.ids;
     a.one = mb == 1;
   } else {
     hipLaunchKernelGGL(balance_count_kernel, dim3((unsigned)cb), dim3(BL_COUNT_THREADS), (copies * c.E + 1) * 4, s,
-                       c.ids, c.mask, c.off, c.T, c.E, c.k, c.S, cc, copies, cpart, chunks);
+                       c.ids, c.mask, c.off, c.T, c.E, c.k, c.S, cc, copies, cpart, ctokens);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (c.S <= 64 && (int64_t)cb * c.E <= kSelfTables) {
       a.cpart = cpart;
-      a.chunks = chunks;
+      a.ctokens = ctokens;
       a.cblocks = cb;
+      a.cchunk = cc;
       a.cols = 1;
       while (a.cols < BL_THREADS && a.cols < c.E) a.cols *= 2;
     } else {
-      hipLaunchKernelGGL(balance_tables_kernel, dim3((unsigned)c.S), dim3(256), 0, s, c.off, c.T, c.E, c.S, cc, mc, cb,
-                         mb, cpart, chunks, counts, seq_tokens, first_main);
+      const int parts = (c.E + 63) / 64;
+      hipLaunchKernelGGL(balance_tables_kernel, dim3((unsigned)(c.S * parts + 1)), dim3(256), 0, s, c.off, c.T, c.E,
+                         c.S, cc, parts, cb, cpart, ctokens, counts, seq_tokens, totals);
       if ((e = hipGetLastError()) != hipSuccess) return e;
-      tables = true;
+      a.totals = totals;
     }
   }
   if ((e = launch_main<true>(a, mb, s)) != hipSuccess || a.one) return e;
@@ -789,10 +811,11 @@ hipError_t launch_balance_loss(const BalanceCall &c, int32_t *counts, int32_t *s
   f.part = a.part;
   f.sums = a.sums;
   f.off = c.off;
-  f.first_main = tables ? first_main : nullptr;
   f.cpart = a.cpart;
-  f.chunks = a.chunks;
+  f.ctokens = a.ctokens;
   f.cblocks = a.cblocks;
+  f.cchunk = a.cchunk;
+  f.totals = a.totals;
   f.counts = counts;
   f.seq_tokens = seq_tokens;
   f.mean_probs = mean_probs;
@@ -803,7 +826,7 @@ hipError_t launch_balance_loss(const BalanceCall &c, int32_t *counts, int32_t *s
   f.chunk = mc;
   f.blocks = mb;
   f.cols = 1;
-  while (f.cols < 32 && f.cols < c.E) f.cols *= 2;
+  while (f.cols < 16 && f.cols < c.E) f.cols *= 2;
   f.parts = (c.E + f.cols - 1) / f.cols;
   f.alpha = c.alpha;
   f.beta = c.beta;
@@ -828,7 +851,7 @@ hipError_t launch_balance_backward(const BalanceCall &c, const int32_t *counts, 
   a.chunk = main_chunk(c.T, c.E, false);
   a.alpha = c.alpha;
   a.beta = c.beta;
-  return launch_main<false>(a, main_blocks(c.T, c.E, c.S, c.off != nullptr, false), s);
+  return launch_main<false>(a, pieces(c.T, a.chunk, c.S, c.off != nullptr), s);
 }
 
 }  // namespace moe
