@@ -8,8 +8,12 @@
 //   d/dl_ti = p_ti (alpha E / (S' N_s) (f_si - sum_j f_sj p_tj) + 2 beta / N z_t)
 // (f is piecewise constant in the logits; S' sequences count a token, N tokens in all).
 // The gradient needs the counts but not the probabilities' means, so one pass over the
-// logits gives both: it is bound by reading the logits and writing the gradient once.
-// Every sum has a fixed order (bit-reproducible); counts are whole numbers.
+// logits gives both.  Counts come first (their own launch, or inside the main pass), the
+// column sums' ends last.  Large batches are bound by reading the logits and writing the
+// gradient once (gradient of 60001 x 161 alone 18.3 us, 4.2 TB/s; 65536 x 128 14.3 us, 4.7
+// TB/s), smaller ones by the launches and the chains of loads in them (16384 x 256 in nine
+// sequences with the losses 21 us in three launches; 8192 x 64 9.8 us in two; 16 x 32 5.0 us
+// in one).  Every sum has a fixed order (bit-reproducible); counts are whole numbers.
 #include <algorithm>
 
 #include "common.hpp"
@@ -20,7 +24,8 @@ namespace moe {
 namespace {
 
 constexpr int BL_COUNT_THREADS = 1024;
-constexpr int BL_WAVES = 4, BL_THREADS = 64 * BL_WAVES;  // main pass
+// Main pass.  8 wavefronts a block: 60001 x 161 20.7 against 17.5 us, 8192 x 64 12.7 against 11.7.
+constexpr int BL_WAVES = 4, BL_THREADS = 64 * BL_WAVES;
 constexpr int BL_BINS = 4096;                            // LDS bins of a block that counts
 
 __device__ __forceinline__ void seq_range(const int32_t *off, int T, int s, int &b, int &e) {
@@ -321,11 +326,10 @@ constexpr int sure_values(int lpt, int values) {
 }
 constexpr int at_once(int values) { return values <= 4 ? 4 : values <= 8 ? 2 : 1; }
 
-// A token's row in LPT lanes of up to 16 values each, 64 / LPT tokens a wavefront: few lanes a
-// row, so that the three reductions over a row and the row's own factors cost little beside
-// its values (64 lanes of four values: ...).  With VEC (E a multiple of 4) a lane's values are
-// 16-byte groups; otherwise they lie LPT apart, so that each load still covers neighbouring
-// words.
+// A token's row in LPT lanes of VPL values each, 64 / LPT tokens a wavefront, at_once(VPL) such
+// groups of tokens at a time (their loads and lane moves in flight together).  With VEC (E a
+// multiple of 4) a lane's values are 16-byte groups; otherwise they lie LPT apart, so that
+// each load still covers neighbouring words.
 template <int LPT, int VPL, bool VEC, bool LOSS>
 __global__ __launch_bounds__(BL_THREADS) void balance_main_kernel(BalanceArgs a) {
   // fused multiply-adds where they are written: with and without the losses the gradient is
@@ -648,7 +652,11 @@ __global__ __launch_bounds__(BL_FIN_THREADS) void balance_finish_kernel(FinishAr
   }
 }
 
-constexpr int kVecValues = 4, kOddValues = 6;  // values a lane takes at most (16 past 64 lanes)
+// Values a lane takes at most (16 past 64 lanes).  One 16-byte load where rows allow it: 8 values
+// measured 5.9 against 5.1 us on 16 x 32 and 9.5 against 9.3 on 16384 x 256 (gradient alone),
+// 16 values 8.4 and 13.0.  Odd rows, where a value is a load and few lanes save reductions: up
+// to 6 or 8 values 17.6 us on 60001 x 161, up to 4 24.4, up to 12 24.8.
+constexpr int kVecValues = 4, kOddValues = 6;
 // Lanes a token takes: a power of two.
 int lanes_per_token(int E) {
   int l = 1;
@@ -663,8 +671,11 @@ int values_per_lane(int E) {
 }
 int tokens_at_once(int E) { return 64 / lanes_per_token(E) * at_once(values_per_lane(E)); }  // of a wavefront
 
+// Tokens of a counting block: at most 128 results to add up (256 tokens a block: 16384 x 256 21.4
+// against 20.0 us; 1024: 19.7, but 25.3 against 24.0 in nine sequences).
 int count_chunk(int T) { return std::max(512, (T + 127) / 128); }
-// Tokens of a block of the main pass: one round of its wavefronts at least.
+// Tokens of a block of the main pass: one round of its wavefronts at least.  With the losses
+// each block leaves its column sums (512 blocks: 16384 x 256 20.0 us; 256 or 1024: 21.4).
 int main_chunk(int T, int E, bool loss) {
   const int blocks = loss ? 512 : 2048;
   return std::max(BL_WAVES * tokens_at_once(E), (T + blocks - 1) / blocks);
@@ -743,10 +754,12 @@ BalanceWs balance_ws(int T, int E, int S) {
 }
 
 // One sequence with at most this many choices is counted by every block of the main pass for
-// itself.
+// itself, against a launch that counts: 8192 choices 11.7 against 13.4 us, 16384 13.3 against
+// 12.8 (and a launch less for the host), 32768 17.8 against 13.3.
 constexpr int64_t kSelfCount = 16384;
 // Up to 64 sequences, and at most this many partial counts: every block of the main pass adds
-// up its sequence's for itself, and no launch for the tables is made.
+// up its sequence's for itself, and no launch for the tables is made: 65536 x 32 15.9 against
+// 27.1 us, 16384 x 256 20.0 against 21.5, 65536 x 256 (the most) 40.0 against 47.0.
 constexpr int64_t kSelfTables = 32768;
 
 }  // namespace

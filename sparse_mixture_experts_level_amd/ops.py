@@ -195,6 +195,17 @@ def _ptr(t: Optional[torch.Tensor]):
     return t.data_ptr()
 
 
+_have_gpu = False
+
+
+def _device() -> int:
+    """The current GPU; -2 without one (no tensor's device)."""
+    global _have_gpu
+    if not _have_gpu:
+        _have_gpu = torch.cuda.is_available()
+    return torch.cuda.current_device() if _have_gpu else -2
+
+
 # the current stream's handle without building a torch.cuda.Stream (0.1 instead of 2.7 us a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -202,11 +213,10 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 def _stream(stream=None):
     if stream is not None:
         return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
-    if not torch.cuda.is_available():
+    dev = _device()
+    if dev < 0:
         return None
-    if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
-    return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
 
 
 def dtype_code(dt: torch.dtype) -> int:
@@ -481,11 +491,6 @@ def moe_backward(desc, w_router, w_gate_up, w_down, x, routing: dict, dy, dx, gr
 
 # ------------------------------------------------------------------- balance loss with gradient
 
-def _device() -> int:
-    """The current GPU; -2 without one (no tensor's device)."""
-    return torch.cuda.current_device() if torch.cuda.is_available() else -2
-
-
 def _tensor(t, name: str, dtypes, shape=None, dev=None):
     """Data pointer of a contiguous tensor of one of `dtypes` (and of `shape`) on the current
     GPU (`dev`, where the caller has it); None stays None."""
@@ -544,23 +549,19 @@ def moe_balance_loss_backward(desc, logits, counts, seq_tokens, alpha, z_coeff, 
 
 # --------------------------------------------------------------- gradient norm and AdamW step
 
-def _check_same(tensors, pointers, name: str) -> None:
-    """Raises when a tensor's memory is not where it was when `pointers` were taken."""
-    if [t.data_ptr() for t in tensors] != pointers:
-        raise RuntimeError(f"{name}: a tensor's memory has been replaced; build the list (the optimizer) again")
-
-
 class GradList:
-    """Gradient tensors with the host array of views that moe_grad_norm takes (grad_list())."""
+    """Gradient tensors with the host array of views that moe_grad_norm takes (grad_list()).
+
+    The list stands for the memory that the tensors have when it is built, and keeps it alive:
+    write gradients in place, or build the list again."""
 
     def __init__(self, grads):
-        self.grads = list(grads)
+        self.grads = [g.detach() for g in grads]
         self.views = (MoeGradView * max(len(self.grads), 1))()
         dev = _device()
-        self.pointers = [_tensor(g, f"grads[{i}]", (torch.float32, torch.bfloat16), None, dev)
-                         for i, g in enumerate(self.grads)]
-        for i, (g, p) in enumerate(zip(self.grads, self.pointers)):
-            self.views[i] = MoeGradView(p, g.numel(), dtype_code(g.dtype), 0)
+        for i, g in enumerate(self.grads):
+            self.views[i] = MoeGradView(_tensor(g, f"grads[{i}]", (torch.float32, torch.bfloat16), None, dev),
+                                        g.numel(), dtype_code(g.dtype), 0)
 
     def __len__(self):
         return len(self.grads)
@@ -577,7 +578,6 @@ def moe_grad_norm_workspace_size(grads: GradList) -> int:
 def moe_grad_norm(grads: GradList, max_norm: float, out, ws, stream=None) -> None:
     """out [2] float: the norm over every gradient, and min(1, max_norm / (norm + 1e-6))."""
     dev = _device()
-    _check_same(grads.grads, grads.pointers, "moe_grad_norm")
     _check(lib().moe_grad_norm(grads.views, len(grads), max_norm, _tensor(out, "out", torch.float32, (2,), dev),
                                _tensor(ws, "ws", torch.uint8, None, dev), 0 if ws is None else ws.numel(),
                                _stream(stream)), "moe_grad_norm")
@@ -630,12 +630,13 @@ class MoEAdamW:
     A step skipped because the norm was not finite counts too.
 
     Tensors are used on the stream of the call, on the GPU that is current when the optimizer is
-    built; allocation happens here, never in step().  The tensors' memory must stay where it is
-    (update parameters and gradients in place); step() refuses when it has moved."""
+    built; allocation happens here, never in step().  The optimizer reads the memory that the
+    gradients have when it is built, and keeps it alive: write gradients in place.  A parameter
+    whose memory has been replaced since is refused by step()."""
 
     def __init__(self, params, grads, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, max_grad_norm=None,
                  state_bits=32, master_weights=False, states=None, step=0, capturable=False):
-        self.params, self.grads = list(params), list(grads)
+        self.params, self.grads = list(params), [g.detach() for g in grads]
         n = len(self.params)
         if len(self.grads) != n or (states is not None and len(states) != n):
             raise ValueError("params, grads and states must have one entry per tensor")
@@ -665,7 +666,9 @@ class MoEAdamW:
                 p.numel(), dtype_code(p.dtype), dtype_code(g.dtype), state_bits, float(decay[i]))
         moe_adamw_check_tensors(self.tensors, n)
         self._device = _device()
-        self._pointers = [t.data_ptr() for t in self.params], [t.data_ptr() for t in self.grads]
+        self._pointers = list(map(torch.Tensor.data_ptr, self.params))
+        # what the host array points at stays alive, whatever becomes of the caller's tensors
+        self._memory = [t.detach() for s in self.states for t in s.values()] + [p.detach() for p in self.params]
         self.hparams = MoeAdamwHparams(float(lr), float(betas[0]), float(betas[1]), float(eps), self.step_count, None,
                                        None, None)
         device = self.params[0].device if n else "cuda"
@@ -702,8 +705,8 @@ class MoEAdamW:
         n = len(self.params)
         if _device() != self._device:
             raise RuntimeError(f"the optimizer's tensors are on GPU {self._device}, which is not the current one")
-        _check_same(self.params, self._pointers[0], "params")
-        _check_same(self.grads, self._pointers[1], "grads")
+        if list(map(torch.Tensor.data_ptr, self.params)) != self._pointers:
+            raise RuntimeError("a parameter's memory has been replaced: build the optimizer again")
         if self.capturable:
             if stream is not None:
                 raise ValueError("a capturable step runs on the current stream")

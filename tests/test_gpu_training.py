@@ -293,6 +293,40 @@ def test_balance_loss_is_deterministic_and_replays_from_a_graph(T, E, k, S):
             assert torch.equal(want.whole[n], out.whole[n]), (i, n)
 
 
+def test_balance_loss_on_two_streams_and_its_gradient_from_a_graph():
+    """Two batches at once, each with its own buffers; the gradient alone captured and replayed."""
+    say("balance on two streams")
+    runs = []
+    for i, (T, E, k, S) in enumerate([(3000, 48, 2, 3), (5000, 33, 4, 1)]):
+        _, l, ids = _draw(50 + i, T, E, k)
+        off = None if S == 1 else [3, 900, 950, T - 10]
+        runs.append((k, S) + _balance(l, ids, off=off)[:5] + (_balance(l, ids, off=off)[5],))
+    outs, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for (k, S, desc, lg, ig, mg, og, want), st in zip(runs, streams):
+            out = Outputs(lg.shape[0], lg.shape[1], S)
+            ws = ops.workspace(ops.moe_balance_workspace_size(desc, S))
+            st.wait_stream(torch.cuda.current_stream())
+            ops.moe_balance_loss(desc, lg, ig, 0.3, 0.05, out.counts, out.seq_tokens, out.mean_probs, out.losses, ws,
+                                 seq_offsets=og, dlogits=out.dlogits, stream=st)
+            outs.append((want, out, ws))
+    torch.cuda.synchronize()
+    for want, out, _ in outs:
+        assert all(torch.equal(want.whole[n], out.whole[n]) for n in want.whole)
+    k, S, desc, lg, ig, mg, og, want = runs[0]
+    d, up = torch.empty_like(lg), torch.ones(2, device=DEV)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ops.moe_balance_loss_backward(desc, lg, want.counts, want.seq_tokens, 0.3, 0.05, d, seq_offsets=og, dloss=up)
+    for factor in (1.0, 2.0, -0.5):
+        up.fill_(factor)
+        d.fill_(9.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(d, want.dlogits * factor)  # powers of two: exact
+
+
 # ----------------------------------------------------------------------------- gradient norm
 
 def _norm(grads, max_norm):
@@ -515,6 +549,24 @@ def test_adamw_8bit_blocks_of_extremes():
     assert np.allclose(to_np(v_out[0]), oracle.read_v(cv, sv), rtol=4 * U, atol=0, equal_nan=True)
 
 
+def test_adamw_read_states_of_some():
+    say("adamw read states of some tensors")
+    _, params, grads, states = _make([5, 3000, 700], 8, "b", "b", False, seed=60)
+    opt = ops.MoEAdamW(params, grads, state_bits=8, states=states, **H)
+    whole = torch.full((3000 + GUARD,), 7.0, device=DEV)
+    m = [None, whole[:3000], None]
+    assert opt.read_states(m, None)[1] is None
+    torch.cuda.synchronize()
+    want = oracle.read_m(to_np(states[1]["m"]), to_np(states[1]["m_scale"]))
+    assert np.array_equal(to_np(m[1]), want.astype(np.float32)) and torch.all(whole[3000:] == 7)
+    v = [None, None, torch.empty(700, device=DEV)]
+    opt.read_states(None, v)
+    want = oracle.read_v(to_np(states[2]["v"]), to_np(states[2]["v_scale"]))
+    assert np.array_equal(to_np(v[2]), want.astype(np.float32))
+    with pytest.raises(ValueError, match="holds"):
+        opt.read_states([None, whole[:2999], None], None)
+
+
 def test_adamw_nan_gradient_stays_where_it_is():
     say("adamw NaN gradient, 32 bits")
     p, g = torch.ones(1000, device=DEV), torch.full((1000,), 0.1, device=DEV)
@@ -602,17 +654,16 @@ def test_adamw_refuses_moved_tensors_and_another_device():
     p, g = torch.ones(100, device=DEV), torch.ones(100, device=DEV)
     opt = ops.MoEAdamW([p], [g], max_grad_norm=1.0, **H)
     opt.step()
-    kept = p.clone()
-    for t, name in ((p, "params"), (g, "grads")):
-        old = t.data
-        t.data = torch.ones(100, device=DEV)
-        with pytest.raises(RuntimeError, match=name):
-            opt.step()
-        t.data = old
-    with pytest.raises(RuntimeError, match="moe_grad_norm"):
-        lst = ops.grad_list([g])
-        g.data = torch.ones(100, device=DEV)
-        ops.moe_grad_norm(lst, 1.0, torch.zeros(2, device=DEV), ops.workspace(4096))
+    kept, old = p.clone(), p.data
+    p.data = torch.ones(100, device=DEV)
+    with pytest.raises(RuntimeError, match="replaced"):
+        opt.step()
+    p.data = old
+    # gradients: the memory that the list was built with stays alive and is what is read
+    lst, out = ops.grad_list([g]), torch.zeros(2, device=DEV)
+    g.data = torch.full((100,), 7.0, device=DEV)
+    ops.moe_grad_norm(lst, 1.0, out, ops.workspace(ops.moe_grad_norm_workspace_size(lst)))
+    assert float(out[0]) == 10.0
     opt._device += 1
     with pytest.raises(RuntimeError, match="current"):
         opt.step()
@@ -846,7 +897,14 @@ def test_binding_refuses_wrong_tensors():
                              out.losses, ws)
     with pytest.raises(ValueError, match="dtype"):
         ops.moe_balance_loss(desc, l.double(), i, 1.0, 0.0, out.counts, out.seq_tokens, out.mean_probs, out.losses, ws)
+    w = wl.Workload("f32", 8, 16, 2, 1, 16, None, "f32")
+    with pytest.raises(ValueError, match="bf16"):
+        ops.MoETrainer(wl.make_inputs(w, device=DEV), None)
     p = torch.zeros(8, device=DEV)
+    with pytest.raises(ValueError, match="contiguous"):
+        ops.MoEAdamW([torch.zeros((4, 4), device=DEV).t()], [torch.zeros((4, 4), device=DEV)])
+    with pytest.raises(ValueError, match="dtype"):
+        ops.MoEAdamW([p.half()], [p])
     with pytest.raises(ValueError, match="values"):
         ops.MoEAdamW([p], [torch.zeros(9, device=DEV)])
     with pytest.raises(ops.MoEError, match="aligned"):
