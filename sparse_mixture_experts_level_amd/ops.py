@@ -668,7 +668,8 @@ class MoEAdamW:
         self._device = _device()
         self._pointers = list(map(torch.Tensor.data_ptr, self.params))
         # what the host array points at stays alive, whatever becomes of the caller's tensors
-        self._memory = [t.detach() for s in self.states for t in s.values()] + [p.detach() for p in self.params]
+        self._memory = [t.detach() for s in self.states for t in s.values() if t is not None]
+        self._memory += [p.detach() for p in self.params]
         self.hparams = MoeAdamwHparams(float(lr), float(betas[0]), float(betas[1]), float(eps), self.step_count, None,
                                        None, None)
         device = self.params[0].device if n else "cuda"

@@ -567,6 +567,20 @@ def test_adamw_read_states_of_some():
         opt.read_states([None, whole[:2999], None], None)
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_states_may_name_what_they_lack(bits):
+    say(f"adamw states with None bits={bits}")
+    got = []
+    for none in (False, True):
+        whole, params, grads, states = _make([300, 9], bits, "b", "b", False, seed=61)
+        if none:
+            states = [dict(s, master=None, **({} if bits == 8 else dict(m_scale=None, v_scale=None))) for s in states]
+        ops.MoEAdamW(params, grads, state_bits=bits, states=states, **H).step()
+        torch.cuda.synchronize()
+        got.append(whole)
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
 def test_adamw_nan_gradient_stays_where_it_is():
     say("adamw NaN gradient, 32 bits")
     p, g = torch.ones(1000, device=DEV), torch.full((1000,), 0.1, device=DEV)
