@@ -85,7 +85,7 @@ typedef enum moe_overflow {
 
 /* Shape of one MoE layer call. */
 typedef struct moe_desc {
-  int32_t num_tokens;  /* T >= 0; T == 0 makes every call a no-op returning MOE_OK */
+  int32_t num_tokens;  /* T >= 0; T == 0 makes every call but moe_balance_loss a no-op returning MOE_OK */
   int32_t d_model;     /* d >= 1 */
   int32_t d_ff;        /* f >= 1: hidden width of each routed expert */
   int32_t num_experts; /* 1 <= E <= MOE_MAX_EXPERTS */
@@ -459,9 +459,10 @@ size_t moe_balance_workspace_size(const moe_desc *desc, int32_t num_seqs);
  *   mean_probs  [num_seqs, E] float, written: P (zeros where N_s is 0)
  *   losses      [2] float, written; 0 when nothing is counted
  *   dlogits     [T, E] float or NULL, written in full: zero for tokens not counted; not
- *               overlapping logits
+ *               overlapping logits (refused)
  *   ws          at least moe_balance_workspace_size(desc, num_seqs) bytes
- * Sums in fixed orders (bit-reproducible).  Only kernel launches on `stream`. */
+ * An empty batch (T == 0) writes zeros to counts, seq_tokens, mean_probs and losses, and
+ * looks at no other pointer.  Sums in fixed orders (bit-reproducible).  Only kernel launches on `stream`. */
 moe_status moe_balance_loss(const moe_desc *desc, const float *logits, const int32_t *topk_ids,
                             const uint8_t *token_mask, const int32_t *seq_offsets, int32_t num_seqs, float alpha,
                             float z_coeff, int32_t *counts, int32_t *seq_tokens, float *mean_probs, float *losses,
@@ -471,7 +472,7 @@ moe_status moe_balance_loss(const moe_desc *desc, const float *logits, const int
  *   dlogits = dloss[0] * d losses[0] / d logits + dloss[1] * d losses[1] / d logits
  *   counts, seq_tokens  as moe_balance_loss wrote them
  *   dloss               [2] float (device) or NULL (both 1)
- *   dlogits             [T, E] float, written in full; not overlapping logits
+ *   dlogits             [T, E] float, written in full; not overlapping logits (refused)
  * Other arguments as for moe_balance_loss; no workspace. */
 moe_status moe_balance_loss_backward(const moe_desc *desc, const float *logits, const uint8_t *token_mask,
                                      const int32_t *seq_offsets, int32_t num_seqs, const int32_t *counts,
@@ -511,9 +512,10 @@ moe_status moe_grad_norm(const moe_grad_view *grads, int32_t num_tensors, float 
  * whose value (for v: whose value's root) is nearest, and a v above zero one at least.  m'
  * and v' are formed and compared in 64 bits, every operation of the formulas rounded by
  * itself (m_scale * (1 / 127^2) and v_scale * (1 / 255^4) first), so that codes and scales
- * are the same for any program that follows them.  A block whose largest is below the smallest normal float is held as zeros;
- * one with a value that is not finite gets a NaN scale.  Zeros everywhere are the initial
- * state of both forms. */
+ * are the same for any program that follows them.  A block whose largest is below the
+ * smallest normal float is held as zeros; one with a value that is not finite gets a NaN
+ * scale, with which all its values count as NaN from the next step on.  Zeros everywhere are
+ * the initial state of both forms. */
 typedef struct moe_adamw_tensor {
   void *param;      /* [n] param_dtype, updated */
   const void *grad; /* [n] grad_dtype */

@@ -1209,6 +1209,13 @@ moe_status check_num_seqs(int32_t num_seqs, const int32_t *seq_offsets) {
   return check_opt_ptr(seq_offsets, "seq_offsets");
 }
 
+moe_status check_dlogits(const moe_desc &D, const float *logits, const float *dlogits) {
+  const uint8_t *a = reinterpret_cast<const uint8_t *>(logits), *b = reinterpret_cast<const uint8_t *>(dlogits);
+  const size_t bytes = (size_t)D.num_tokens * D.num_experts * 4;
+  if (dlogits && a < b + bytes && b < a + bytes) return fail(MOE_ERR_INVALID, "dlogits overlaps logits");
+  return MOE_OK;
+}
+
 moe_status check_coeff(float c, const char *name) {
   return std::isfinite(c) ? MOE_OK : fail(MOE_ERR_INVALID, "%s is not finite", name);
 }
@@ -1344,15 +1351,23 @@ moe_status moe_balance_loss(const moe_desc *desc, const float *logits, const int
   MOE_TRY(check_num_seqs(num_seqs, seq_offsets));
   MOE_TRY(check_coeff(alpha, "alpha"));
   MOE_TRY(check_coeff(z_coeff, "z_coeff"));
-  if (D.num_tokens == 0) return ok();
-  MOE_TRY(check_ptr(logits, "logits"));
-  MOE_TRY(check_ptr(topk_ids, "topk_ids"));
-  MOE_TRY(check_opt_ptr(token_mask, "token_mask"));
   MOE_TRY(check_ptr(counts, "counts"));
   MOE_TRY(check_ptr(seq_tokens, "seq_tokens"));
   MOE_TRY(check_ptr(mean_probs, "mean_probs"));
   MOE_TRY(check_ptr(losses, "losses"));
+  if (D.num_tokens == 0) {  // nothing is counted
+    const int cells = num_seqs * D.num_experts;
+    MOE_TRY_HIP(moe::launch_fill_i32(counts, cells, 0, 0, stream), "zero counts");
+    MOE_TRY_HIP(moe::launch_fill_i32(seq_tokens, num_seqs, 0, 0, stream), "zero tokens");
+    MOE_TRY_HIP(moe::launch_fill_i32(reinterpret_cast<int32_t *>(mean_probs), cells, 0, 0, stream), "zero means");
+    MOE_TRY_HIP(moe::launch_fill_i32(reinterpret_cast<int32_t *>(losses), 2, 0, 0, stream), "zero losses");
+    return ok();
+  }
+  MOE_TRY(check_ptr(logits, "logits"));
+  MOE_TRY(check_ptr(topk_ids, "topk_ids"));
+  MOE_TRY(check_opt_ptr(token_mask, "token_mask"));
   MOE_TRY(check_opt_ptr(dlogits, "dlogits"));
+  MOE_TRY(check_dlogits(D, logits, dlogits));
   const size_t need = moe_balance_workspace_size(desc, num_seqs);
   if (!ws || ws_bytes < need)
     return fail(MOE_ERR_WORKSPACE, "moe_balance_loss needs %zu workspace bytes, got %zu", need,
@@ -1380,6 +1395,7 @@ moe_status moe_balance_loss_backward(const moe_desc *desc, const float *logits, 
   MOE_TRY(check_ptr(seq_tokens, "seq_tokens"));
   MOE_TRY(check_opt_ptr(dloss, "dloss"));
   MOE_TRY(check_ptr(dlogits, "dlogits"));
+  MOE_TRY(check_dlogits(D, logits, dlogits));
   const moe::BalanceCall c{logits,       nullptr,       token_mask, seq_offsets, dloss, dlogits,
                            D.num_tokens, D.num_experts, D.top_k,    num_seqs,    alpha, z_coeff};
   MOE_TRY_HIP(moe::launch_balance_backward(c, counts, seq_tokens, stream), "balance loss backward");

@@ -9,6 +9,7 @@ instead of falling back to anything else.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -217,6 +218,13 @@ def _stream(stream=None):
     if dev < 0:
         return None
     return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
+def _on(stream):
+    """The context in which `stream` (a torch stream, a raw handle or None) is torch's current one."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream))
 
 
 def dtype_code(dt: torch.dtype) -> int:
@@ -558,9 +566,9 @@ class GradList:
     def __init__(self, grads):
         self.grads = [g.detach() for g in grads]
         self.views = (MoeGradView * max(len(self.grads), 1))()
-        dev = _device()
+        self.device = _device()
         for i, g in enumerate(self.grads):
-            self.views[i] = MoeGradView(_tensor(g, f"grads[{i}]", (torch.float32, torch.bfloat16), None, dev),
+            self.views[i] = MoeGradView(_tensor(g, f"grads[{i}]", (torch.float32, torch.bfloat16), None, self.device),
                                         g.numel(), dtype_code(g.dtype), 0)
 
     def __len__(self):
@@ -578,6 +586,8 @@ def moe_grad_norm_workspace_size(grads: GradList) -> int:
 def moe_grad_norm(grads: GradList, max_norm: float, out, ws, stream=None) -> None:
     """out [2] float: the norm over every gradient, and min(1, max_norm / (norm + 1e-6))."""
     dev = _device()
+    if dev != grads.device:
+        raise RuntimeError(f"the gradients are on GPU {grads.device}, which is not the current one")
     _check(lib().moe_grad_norm(grads.views, len(grads), max_norm, _tensor(out, "out", torch.float32, (2,), dev),
                                _tensor(ws, "ws", torch.uint8, None, dev), 0 if ws is None else ws.numel(),
                                _stream(stream)), "moe_grad_norm")
@@ -611,10 +621,8 @@ def moe_adamw_read_states(tensors, num_tensors: int, m_out=None, v_out=None, str
 
 
 def _capturing(stream) -> bool:
-    if hasattr(stream, "cuda_stream"):
-        with torch.cuda.stream(stream):
-            return torch.cuda.is_current_stream_capturing()
-    return torch.cuda.is_current_stream_capturing()
+    with _on(stream):
+        return torch.cuda.is_current_stream_capturing()
 
 
 class MoEAdamW:
@@ -672,6 +680,11 @@ class MoEAdamW:
         self._memory += [p.detach() for p in self.params]
         self.hparams = MoeAdamwHparams(float(lr), float(betas[0]), float(betas[1]), float(eps), self.step_count, None,
                                        None, None)
+        self._check_lr(lr)
+        if max_grad_norm is not None and not max_grad_norm > 0:
+            raise ValueError(f"max_grad_norm {max_grad_norm}: above 0, or None")
+        self.hparams.step += 1
+        moe_adamw_step(self.tensors, 0, self.hparams)  # of no tensor: only the checks
         device = self.params[0].device if n else "cuda"
         self.capturable = capturable
         if capturable:
@@ -697,15 +710,24 @@ class MoEAdamW:
             s["master"] = p.detach().float()
         return s
 
+    @staticmethod
+    def _check_lr(lr):
+        if not 0 <= lr < float("inf"):
+            raise ValueError(f"lr {lr} must be finite and >= 0")
+
     def set_lr(self, lr: float) -> None:
+        self._check_lr(lr)
         self.hparams.lr = float(lr)
         if self.capturable:
             self.lr_dev.fill_(float(lr))
 
-    def step(self, stream=None) -> None:
-        n = len(self.params)
+    def _check_device(self):
         if _device() != self._device:
             raise RuntimeError(f"the optimizer's tensors are on GPU {self._device}, which is not the current one")
+
+    def step(self, stream=None) -> None:
+        n = len(self.params)
+        self._check_device()
         if list(map(torch.Tensor.data_ptr, self.params)) != self._pointers:
             raise RuntimeError("a parameter's memory has been replaced: build the optimizer again")
         if self.capturable:
@@ -721,10 +743,13 @@ class MoEAdamW:
         self.step_count += 1
 
     def read_states(self, m_out=None, v_out=None, stream=None):
-        """8-bit states as the floats they stand for, into the given tensors or new ones."""
+        """8-bit states as the floats they stand for, into the given tensors or new ones (which
+        belong to `stream`)."""
+        self._check_device()
         if m_out is None and v_out is None:
-            m_out, v_out = ([torch.empty(p.shape, dtype=torch.float32, device=p.device) for p in self.params]
-                            for _ in range(2))
+            with _on(stream):
+                m_out, v_out = ([torch.empty(p.shape, dtype=torch.float32, device=p.device) for p in self.params]
+                                for _ in range(2))
         moe_adamw_read_states(self.tensors, len(self.params), m_out, v_out, stream=stream)
         return m_out, v_out
 

@@ -581,6 +581,48 @@ def test_adamw_states_may_name_what_they_lack(bits):
     assert all(torch.equal(a, b) for a, b in zip(*got))
 
 
+def test_balance_of_an_empty_batch_is_zero():
+    say("balance of no tokens")
+    E, S = 33, 3
+    desc = ops.MoeDesc(num_tokens=0, d_model=64, d_ff=64, num_experts=E, top_k=2, capacity=ops.MOE_NO_CAPACITY)
+    counts = torch.full((S, E), 7, dtype=torch.int32, device=DEV)
+    tokens = torch.full((S,), 7, dtype=torch.int32, device=DEV)
+    probs, losses = torch.full((S, E), 7.0, device=DEV), torch.full((2,), 7.0, device=DEV)
+    none = torch.empty((0, E), device=DEV)
+    ops.moe_balance_loss(desc, none, torch.empty((0, 2), dtype=torch.int32, device=DEV), 0.1, 0.1, counts, tokens, probs,
+                         losses, None, seq_offsets=torch.zeros(S + 1, dtype=torch.int32, device=DEV), dlogits=none)
+    assert not counts.any() and not tokens.any() and not probs.any() and not losses.any()
+
+
+def test_adamw_states_read_on_another_stream():
+    say("adamw read_states on another stream")
+    _, params, grads, states = _make([5000], 8, "b", "b", False, seed=62)
+    opt = ops.MoEAdamW(params, grads, state_bits=8, states=states, **H)
+    opt.step()
+    want = opt.read_states()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for stream in (s, s.cuda_stream):
+        got = opt.read_states(stream=stream)
+        s.synchronize()
+        assert all(torch.equal(a, b) for x, y in zip(want, got) for a, b in zip(x, y))
+
+
+def test_adamw_refuses_wrong_options_when_built():
+    p, g = torch.ones(8, device=DEV), torch.ones(8, device=DEV)
+    for kw, error in [(dict(lr=-1.0), ValueError), (dict(lr=float("nan")), ValueError),
+                      (dict(max_grad_norm=0.0), ValueError), (dict(betas=(1.0, 0.9)), ops.MoEError),
+                      (dict(eps=0.0), ops.MoEError), (dict(step=-1), ops.MoEError)]:
+        for capturable in (False, True):
+            if capturable and "step" in kw:
+                continue
+            with pytest.raises(error):
+                ops.MoEAdamW([p], [g], capturable=capturable, **{**H, **kw})
+    opt = ops.MoEAdamW([p], [g], capturable=True, **H)
+    with pytest.raises(ValueError):
+        opt.set_lr(float("inf"))
+
+
 def test_adamw_nan_gradient_stays_where_it_is():
     say("adamw NaN gradient, 32 bits")
     p, g = torch.ones(1000, device=DEV), torch.full((1000,), 0.1, device=DEV)
@@ -679,8 +721,10 @@ def test_adamw_refuses_moved_tensors_and_another_device():
     ops.moe_grad_norm(lst, 1.0, out, ops.workspace(ops.moe_grad_norm_workspace_size(lst)))
     assert float(out[0]) == 10.0
     opt._device += 1
-    with pytest.raises(RuntimeError, match="current"):
-        opt.step()
+    lst.device += 1
+    for call in (opt.step, opt.read_states, lambda: ops.moe_grad_norm(lst, 1.0, out, opt._ws)):
+        with pytest.raises(RuntimeError, match="current"):
+            call()
     assert torch.equal(p, kept) and opt.step_count == 1
 
 

@@ -148,6 +148,7 @@ def _loss(desc=None, logits=FAKE, ids=FAKE, mask=None, off=None, S=1, alpha=0.1,
     (dict(probs=None), ops.MOE_ERR_INVALID, "mean_probs"),
     (dict(losses=None), ops.MOE_ERR_INVALID, "losses"),
     (dict(dlogits=FAKE + 8), ops.MOE_ERR_INVALID, "dlogits"),
+    (dict(dlogits=FAKE), ops.MOE_ERR_INVALID, "overlaps"),
     (dict(ws=None), ops.MOE_ERR_WORKSPACE, "workspace"),
     (dict(nbytes=8), ops.MOE_ERR_WORKSPACE, "workspace"),
     (dict(desc=_desc(top_k=9)), ops.MOE_ERR_INVALID, "top_k"),
@@ -158,9 +159,10 @@ def test_balance_loss_refusals(kw, status, word):
 
 
 @needs_lib
-def test_balance_of_an_empty_batch_is_a_no_op():
+def test_balance_of_an_empty_batch_needs_its_outputs_only():
     d = _desc(num_tokens=0)
-    assert _loss(d, None, None, counts=None, tokens=None, probs=None, losses=None, ws=None, nbytes=0) == ops.MOE_OK
+    for name in ("counts", "tokens", "probs", "losses"):
+        assert _loss(d, None, None, ws=None, nbytes=0, **{name: None}) == ops.MOE_ERR_INVALID
     L = ops.lib()
     assert L.moe_balance_loss_backward(ctypes.byref(d), None, None, None, 1, None, None, 0.1, 0.1, None, None,
                                        None) == ops.MOE_OK
@@ -174,7 +176,8 @@ def test_balance_backward_refusals():
         return L.moe_balance_loss_backward(ctypes.byref(d), logits, mask, off, S, counts, tokens, alpha, z, dloss, dl,
                                            None)
     for kw, word in [(dict(logits=None), "logits"), (dict(counts=None), "counts"), (dict(tokens=None), "seq_tokens"),
-                     (dict(dl=None), "dlogits"), (dict(dloss=FAKE + 4), "dloss"), (dict(S=3), "seq_offsets"),
+                     (dict(dl=None), "dlogits"), (dict(dl=FAKE), "overlaps"), (dict(dl=FAKE + 16), "overlaps"),
+                     (dict(dl=FAKE - 16), "overlaps"), (dict(dloss=FAKE + 4), "dloss"), (dict(S=3), "seq_offsets"),
                      (dict(alpha=float("inf")), "alpha")]:
         assert call(**kw) == ops.MOE_ERR_INVALID
         assert word in _last()
