@@ -550,7 +550,8 @@ typedef struct moe_adamw_hparams {
  * the parameters (the same tensor twice), in the debug build in full. */
 moe_status moe_adamw_check_tensors(const moe_adamw_tensor *tensors, int32_t num_tensors);
 
-/* One AdamW step (decoupled weight decay) of every tensor, in a launch per 48 tensors:
+/* One AdamW step (decoupled weight decay) of every tensor, 64 tensors (8-bit states: 48) a
+ * launch:
  *   g' = out[1] g;  m' = b1 m + (1 - b1) g';  v' = b2 v + (1 - b2) g'^2
  *   w' = w (1 - lr wd) - lr / (1 - b1^t) m' / (sqrt(v') / sqrt(1 - b2^t) + eps)
  * in float (8-bit states: m' and v' in 64 bits), w' rounded once to param_dtype.
