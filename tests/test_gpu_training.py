@@ -244,6 +244,55 @@ def test_balance_loss_far_logits_and_large_batch():
     _check_balance(l, ids, mask=(rng.random(40000) < 0.9).astype(np.uint8), off=[0, 11, 20000, 39990])
 
 
+@pytest.mark.parametrize("off", [None, [5, 2 ** 20, 2 ** 21 + 70]])
+def test_balance_loss_past_32_bits(off):
+    """More than 2^31 logits: sums against 64 bits, gradients against the same rows alone."""
+    say(f"balance T=2^21+77 E=1024 off={off}")
+    T, E, alpha, z = 2 ** 21 + 77, 1024, 0.3, 0.05
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    lg = torch.randn((T, E), generator=gen, device=DEV)
+    ids = torch.randint(0, E, (T, 1), generator=gen, device=DEV, dtype=torch.int32)
+    S = 1 if off is None else len(off) - 1
+    offs = [0, T] if off is None else off
+    og = None if off is None else torch.tensor(off, dtype=torch.int32, device=DEV)
+    desc, out = ops.make_desc(T, 64, 64, E, 1, None), Outputs(T, E, S)
+    ops.moe_balance_loss(desc, lg, ids, alpha, z, out.counts, out.seq_tokens, out.mean_probs, out.losses,
+                         ops.workspace(ops.moe_balance_workspace_size(desc, S)), seq_offsets=og, dlogits=out.dlogits)
+    torch.cuda.synchronize()
+    out.check_guards()
+    # K = 2 range + 24 as above; a lane adds up at most 4096 rows one after another, each of relative error u
+    K = 2 * float(lg.max() - lg.min()) + 24 + 4096
+    balance, squares, n = 0.0, 0.0, 0
+    for s in range(S):
+        b, e = offs[s], offs[s + 1]
+        assert torch.equal(out.counts[s].long(), torch.bincount(ids[b:e, 0].long(), minlength=E))
+        assert int(out.seq_tokens[s]) == e - b
+        probs = torch.zeros(E, dtype=torch.float64, device=DEV)
+        for i in range(b, e, 1 << 16):
+            l = lg[i:min(i + (1 << 16), e)].double()
+            lse = torch.logsumexp(l, 1)
+            probs += (l - lse[:, None]).exp().sum(0)
+            squares += float((lse * lse).sum())
+        probs /= e - b
+        assert torch.all((out.mean_probs[s] - probs).abs() <= (K + 32) * U * probs)
+        balance += float((out.counts[s].double() / (e - b) * probs).sum())
+        n += e - b
+    losses = to_np(out.losses)
+    want = (alpha * E * balance / S, z * squares / n)
+    assert abs(losses[0] - want[0]) <= (K + 34) * U * want[0]
+    assert abs(losses[1] - want[1]) <= 2 * (K + 34) * U * (2 * want[1] + z)
+    # rows at the start, on both sides of 2^31 values (row 2^21), at a sequence's end and at the batch's
+    for i in (0, 2 ** 20 - 8, 2 ** 21 - 8, T - 16):
+        rows = slice(i, i + 16)
+        seq = None
+        if off is not None:
+            seq = torch.tensor([min(max(o - i, 0), 16) for o in off], dtype=torch.int32, device=DEV)
+        part = torch.full((16, E), 7.0, device=DEV)
+        ops.moe_balance_loss_backward(ops.make_desc(16, 64, 64, E, 1, None), lg[rows], out.counts, out.seq_tokens,
+                                      alpha, z, part, seq_offsets=seq)
+        assert torch.equal(part, out.dlogits[rows]) and bool(part.any())
+
+
 def test_balance_loss_equals_the_aux_loss_and_needs_no_gradient():
     say("balance against moe_router_aux_loss; without dlogits")
     for T, E, k in [(64, 8, 2), (1000, 64, 1)]:
