@@ -471,7 +471,8 @@ moe_status moe_balance_loss(const moe_desc *desc, const float *logits, const int
 /* The gradient alone, for upstream gradients known only after the forward pass:
  *   dlogits = dloss[0] * d losses[0] / d logits + dloss[1] * d losses[1] / d logits
  *   counts, seq_tokens  as moe_balance_loss wrote them
- *   dloss               [2] float (device) or NULL (both 1)
+ *   dloss               [2] float (device) or NULL (both 1); whatever they hold, a token that
+ *                       is not counted or has no finite logit gets zeros
  *   dlogits             [T, E] float, written in full; not overlapping logits (refused)
  * Other arguments as for moe_balance_loss; no workspace. */
 moe_status moe_balance_loss_backward(const moe_desc *desc, const float *logits, const uint8_t *token_mask,

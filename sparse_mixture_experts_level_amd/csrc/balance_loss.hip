@@ -496,10 +496,13 @@ __global__ __launch_bounds__(BL_THREADS) void balance_main_kernel(BalanceArgs a)
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int t = t0 + n * TPW + sub;
-      const float inv = sum[n] == 0.f ? 0.f : __builtin_amdgcn_rcpf(sum[n]);  // sum is in [1, E]
-      const float z = sum[n] == 0.f ? 0.f : base[n] + __logf(sum[n]);
+      const bool none = sum[n] == 0.f;
+      const float inv = none ? 0.f : __builtin_amdgcn_rcpf(sum[n]);  // sum is in [1, E]
+      const float z = none ? 0.f : base[n] + __logf(sum[n]);
       const float mean_f = dot[n] * inv;  // sum_i f_i p_i
-      const float shift = __builtin_fmaf(ca, mean_f, -(cb * z));
+      // factors of zero too: upstream gradients may be infinite or NaN
+      const float can = none ? 0.f : ca;
+      const float shift = none ? 0.f : __builtin_fmaf(ca, mean_f, -(cb * z));
       if constexpr (LOSS) {
         if (li == 0) {
           bacc += (double)mean_f;
@@ -519,14 +522,14 @@ __global__ __launch_bounds__(BL_THREADS) void balance_main_kernel(BalanceArgs a)
           for (int v = 0; v < VPL; v += 4) {
             f32x4 q;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) q[i] = l[n][v + i] * __builtin_fmaf(ca, f[v + i], -shift);
+            for (int i = 0; i < 4; ++i) q[i] = l[n][v + i] * __builtin_fmaf(can, f[v + i], -shift);
             if (expert(v) < E) __builtin_nontemporal_store(q, reinterpret_cast<f32x4 *>(drow + expert(v)));
           }
         } else {
 #pragma unroll
           for (int v = 0; v < VPL; ++v)
             if (expert(v) < E)
-              __builtin_nontemporal_store(l[n][v] * __builtin_fmaf(ca, f[v], -shift), drow + expert(v));
+              __builtin_nontemporal_store(l[n][v] * __builtin_fmaf(can, f[v], -shift), drow + expert(v));
         }
       }
     }

@@ -293,6 +293,32 @@ def test_balance_loss_past_32_bits(off):
         assert torch.equal(part, out.dlogits[rows]) and bool(part.any())
 
 
+@pytest.mark.parametrize("T,E,k,off", [(200, 32, 4, None), (300, 33, 3, [4, 100, 100, 290]), (70, 64, 2, [0, 70]),
+                                       (40, 1, 1, None), (40, 700, 8, None), (40, 1023, 8, None)])
+def test_balance_gradient_of_uncounted_tokens_is_zero_whatever_comes_from_above(T, E, k, off):
+    """An upstream gradient that is not finite (an overflowed loss scale) or a product of coefficients past the floats:
+    zero for masked tokens, for tokens of no sequence and for those without a finite logit, all the same."""
+    say(f"balance gradient under infinite factors T={T} E={E}")
+    rng, l, ids = _draw(70, T, E, k)
+    mask = rng.random(T) < 0.6
+    l[10:13] = -np.inf
+    mask[10:13] = [True, False, True]
+    none = ~mask
+    none[10:13] = True
+    if off is not None:
+        none[:off[0]] = none[off[-1]:] = True
+    desc, lg, ig, mg, og, out = _balance(l, ids, 0.3, 0.05, mask, off)
+    dl = torch.full_like(out.dlogits, 7.0)
+    for up in ((float("inf"), 1.0), (1.0, -float("inf")), (float("nan"), float("nan"))):
+        ops.moe_balance_loss_backward(desc, lg, out.counts, out.seq_tokens, 0.3, 0.05, dl, token_mask=mg, seq_offsets=og,
+                                      dloss=torch.tensor(up, device=DEV))
+        got = to_np(dl)
+        assert np.all(got[none] == 0.0)
+        assert not np.isfinite(got[~none]).all()
+    _, _, _, _, _, out = _balance(l, ids, 3e38, 3e38, mask, off)
+    assert np.all(to_np(out.dlogits)[none] == 0.0)
+
+
 def test_balance_loss_equals_the_aux_loss_and_needs_no_gradient():
     say("balance against moe_router_aux_loss; without dlogits")
     for T, E, k in [(64, 8, 2), (1000, 64, 1)]:
