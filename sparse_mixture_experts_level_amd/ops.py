@@ -632,7 +632,9 @@ class MoEAdamW:
     Parameters and gradients are float or bf16; weight_decay is one value or one per tensor.
     state_bits 32 or 8; master_weights keeps a float copy of each bf16 parameter.  `states`
     (one dict of m, v, m_scale, v_scale, master per tensor) takes existing state tensors
-    instead of new zeros; `step` is the number of steps already done.  With capturable=True
+    instead of new zeros: a master in it is used whatever master_weights says, and one that
+    master_weights asks for and it lacks is made from the parameter (`optimizer.states` then
+    holds it, not the caller's dict).  `step` is the number of steps already done.  With capturable=True
     the step number and lr live on the device, so that a step captured into a HIP graph
     counts on at every replay (step_count only counts calls); set the rate with set_lr() then.
     A step skipped because the norm was not finite counts too.
@@ -654,7 +656,8 @@ class MoEAdamW:
         if len(decay) != n:
             raise ValueError("weight_decay must be one value or one per tensor")
         self.state_bits, self.max_grad_norm, self.step_count = state_bits, max_grad_norm, int(step)
-        self.states = states if states is not None else [self._new_state(p, master_weights) for p in self.params]
+        self.states = ([self._new_state(p, master_weights) for p in self.params] if states is None else
+                       [self._given_state(p, s, master_weights) for p, s in zip(self.params, states)])
         self.tensors = (MoeAdamwTensor * max(n, 1))()
         fp = (torch.float32, torch.bfloat16)
         kinds = (torch.float32, torch.float32) if state_bits == 32 else (torch.int8, torch.uint8)
@@ -708,6 +711,12 @@ class MoEAdamW:
                  "v_scale": z((blocks,), torch.float32)}
         if master_weights and p.dtype != torch.float32:
             s["master"] = p.detach().float()
+        return s
+
+    @staticmethod
+    def _given_state(p, s, master_weights):
+        if master_weights and p.dtype != torch.float32 and s.get("master") is None:
+            s = dict(s, master=p.detach().float())
         return s
 
     @staticmethod

@@ -905,6 +905,31 @@ def test_adamw_and_norm_past_32_bits():
     assert int(torch.count_nonzero(p)) <= tail + 1
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_given_states_with_master_weights(bits):
+    """States without a float copy of the weights, as a checkpoint of bf16 weights leaves them: master_weights makes
+    it, and steps far below a weight's last place add up.  A copy that the states hold is taken as it is."""
+    say(f"adamw given states and master_weights bits={bits}")
+    for lacking in ({}, dict(master=None)):
+        _, params, grads, states = _make([300, 40], bits, "bf", "b", False, seed=63, zero_state=True)
+        given = [dict(s, **lacking) for s in states]
+        start = [p.clone() for p in params]
+        opt = ops.MoEAdamW(params, grads, weight_decay=0.0, state_bits=bits, states=given, master_weights=True,
+                           lr=2.0 ** -20, betas=(0.0, 0.0), eps=1e-30)
+        assert opt.states[1].get("master") is None and given[0].get("master") is None
+        assert torch.equal(opt.states[0]["master"], start[0].float())
+        opt.step()
+        torch.cuda.synchronize()
+        # betas of zero: the step is lr times the gradient's sign, off by 16 u of it; the copy rounds itself
+        moved = to_np(opt.states[0]["master"]).astype(np.float64) - to_np(start[0]).astype(np.float64)
+        want = -2.0 ** -20 * np.sign(to_np(grads[0]).astype(np.float64))
+        assert np.all(np.abs(moved - want) <= 2.0 ** -20 * 16 * U + 2 * U * np.abs(to_np(start[0])))
+    _, params, grads, states = _make([300], bits, "b", "b", True, seed=64)
+    for asked in (False, True):
+        opt = ops.MoEAdamW(params, grads, state_bits=bits, states=states, master_weights=asked, **H)
+        assert opt.states[0]["master"] is states[0]["master"]
+
+
 # ------------------------------------------------------------------------------ the run together
 
 def _layer(T=300, d=128, E=8, k=2, f=192, cf=1.25, fs=64, seed=4, **kw):
