@@ -539,10 +539,14 @@ typedef struct moe_adamw_hparams {
   /* Optional device scalars, read when the step runs (a captured step then follows them on
    * every replay): lr and t in the place of the two fields above (a t below 1 counts as 1),
    * and moe_grad_norm's `out`, whose out[1] every gradient is multiplied by.  When out[1] is
-   * NaN the step writes nothing. */
+   * NaN the step leaves every tensor as it is. */
   const float *lr_dev;     /* [1] or NULL */
   const int64_t *step_dev; /* [1] or NULL */
   const float *norm;       /* [2] or NULL */
+  /* How many of the steps so far were left undone so (device): t is the step's number less
+   * this (1 at least), so that the bias corrections count the updates that m and v have seen,
+   * and a step left undone adds one to it.  NULL: t is the step's number. */
+  int64_t *skipped; /* [1] or NULL */
 } moe_adamw_hparams;
 
 /* The conditions on a list of tensors that moe_adamw_step checks (pointers, alignment,

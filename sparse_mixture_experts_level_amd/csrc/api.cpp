@@ -1447,6 +1447,7 @@ moe_status moe_adamw_step(const moe_adamw_tensor *tensors, int32_t num_tensors, 
   MOE_TRY(check_opt_ptr(H.lr_dev, "lr_dev"));
   MOE_TRY(check_opt_ptr(H.step_dev, "step_dev"));
   MOE_TRY(check_opt_ptr(H.norm, "norm"));
+  MOE_TRY(check_opt_ptr(H.skipped, "skipped"));
   MOE_TRY(check_adamw(tensors, num_tensors, false));
 #ifdef MOE_DEBUG_CHECKS
   MOE_TRY(check_adamw_disjoint(tensors, num_tensors, false));
@@ -1454,7 +1455,8 @@ moe_status moe_adamw_step(const moe_adamw_tensor *tensors, int32_t num_tensors, 
   MOE_TRY(check_adamw_disjoint(tensors, num_tensors, true));  // the same tensor twice
 #endif
   const auto t = adam_tensors(tensors, num_tensors);
-  const moe::AdamScalars h{H.lr, H.beta1, H.beta2, H.eps, H.step, H.lr_dev, H.step_dev, H.norm ? H.norm + 1 : nullptr};
+  const moe::AdamScalars h{H.lr,     H.beta1,    H.beta2,  H.eps, H.step,
+                           H.lr_dev, H.step_dev, H.norm ? H.norm + 1 : nullptr, H.skipped};
   MOE_TRY_HIP(moe::launch_adamw(t.data(), num_tensors, h, stream), "AdamW step");
   return ok();
 } catch (const std::exception &e) {

@@ -209,6 +209,7 @@ struct AdamScalars {
   const float *lr_dev;
   const int64_t *step_dev;
   const float *grad_scale;
+  int64_t *skipped;  // steps left undone so far, or NULL
 };
 hipError_t launch_adamw(const AdamTensor *t, int count, const AdamScalars &h, hipStream_t s);
 hipError_t launch_adamw_read(const AdamTensor *t, int count, float *const *m_out, float *const *v_out, hipStream_t s);

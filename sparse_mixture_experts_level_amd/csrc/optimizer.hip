@@ -242,6 +242,7 @@ struct AdamArgs {
   Tensor t[N];
   int32_t first[N];
   int32_t count;
+  int32_t last;         // the step's last launch
   float step, inv_bc2;  // from the host's lr and t
   AdamScalars h;
   double log_beta1, log_beta2;
@@ -259,17 +260,24 @@ struct Rates {
   float gscale;
 };
 
-// False: a gradient scale that is not a number (the norm was not finite) leaves everything.
+// False: a gradient scale that is not a number (the norm was not finite) leaves everything, and
+// the step's last launch, of which then no block looks at the count, counts it.
 template <typename Args>
 __device__ __forceinline__ bool rates(const Args &a, float decay, Rates &r) {
   double lr = a.h.lr;
   r.step = a.step;
   r.inv_bc2 = a.inv_bc2;
-  if (a.h.lr_dev || a.h.step_dev) {  // equal for the whole launch
+  r.gscale = a.h.grad_scale ? *a.h.grad_scale : 1.f;
+  if (r.gscale != r.gscale) {
+    if (a.last && a.h.skipped && blockIdx.x == 0 && threadIdx.x == 0) ++*a.h.skipped;
+    return false;
+  }
+  const int64_t skipped = a.h.skipped ? *a.h.skipped : 0;
+  if (a.h.lr_dev || a.h.step_dev || skipped) {  // equal for the whole launch
     __shared__ float s_rates[2];
     if (a.h.lr_dev) lr = (double)*a.h.lr_dev;
     if (threadIdx.x < 64) {  // some hundred instructions: for one wavefront
-      const int64_t t = a.h.step_dev ? max(*a.h.step_dev, (int64_t)1) : a.h.step;
+      const int64_t t = max((a.h.step_dev ? *a.h.step_dev : a.h.step) - skipped, (int64_t)1);
       s_rates[0] = (float)(lr / -expm1((double)t * a.log_beta1));
       s_rates[1] = (float)(1.0 / sqrt(-expm1((double)t * a.log_beta2)));
     }
@@ -278,8 +286,7 @@ __device__ __forceinline__ bool rates(const Args &a, float decay, Rates &r) {
     r.inv_bc2 = s_rates[1];
   }
   r.keep = (float)(1.0 - lr * (double)decay);
-  r.gscale = a.h.grad_scale ? *a.h.grad_scale : 1.f;
-  return r.gscale == r.gscale;
+  return true;
 }
 
 // The weight after a step, from m' and the root of v' (hardware reciprocal: one in the last
@@ -680,11 +687,16 @@ Adam8 as_argument(const AdamTensor &t, Adam8 *) {
   return Adam8{as_argument(t, static_cast<Adam32 *>(nullptr)), t.m_scale, t.v_scale};
 }
 
-// Launches for the tensors with 32-bit or with 8-bit states.
+// Whether any value of the tensors has its states in 8 (or in 32) bits.
+bool any_of_kind(bool eight, const AdamTensor *t, int count) {
+  return std::any_of(t, t + count, [&](const AdamTensor &x) { return x.eight == eight && x.n > 0; });
+}
+
+// Launches for the tensors with 32-bit or with 8-bit states.  last: no launch of the step follows.
 template <typename Tensor, int N>
 hipError_t launch_adamw_of(void (*kernel)(AdamArgs<Tensor, N>), bool eight, int64_t chunk, const AdamTensor *t,
-                           int count, const AdamScalars &h, hipStream_t s) {
-  if (std::none_of(t, t + count, [&](const AdamTensor &x) { return x.eight == eight && x.n > 0; })) return hipSuccess;
+                           int count, const AdamScalars &h, bool last, hipStream_t s) {
+  if (!any_of_kind(eight, t, count)) return hipSuccess;
   AdamArgs<Tensor, N> a{};
   a.h = h;
   a.log_beta1 = std::log(h.beta1);
@@ -710,15 +722,17 @@ hipError_t launch_adamw_of(void (*kernel)(AdamArgs<Tensor, N>), bool eight, int6
     a.first[a.count++] = (int32_t)blocks;
     blocks += nb;
   }
+  a.last = last;
   return flush();
 }
 
 }  // namespace
 
 hipError_t launch_adamw(const AdamTensor *t, int count, const AdamScalars &h, hipStream_t s) {
-  const hipError_t e = launch_adamw_of(adamw32_kernel, false, kAdam32Chunk, t, count, h, s);
+  const hipError_t e =
+      launch_adamw_of(adamw32_kernel, false, kAdam32Chunk, t, count, h, !any_of_kind(true, t, count), s);
   if (e != hipSuccess) return e;
-  return launch_adamw_of(adamw8_kernel, true, kAdamChunk, t, count, h, s);
+  return launch_adamw_of(adamw8_kernel, true, kAdamChunk, t, count, h, true, s);
 }
 
 hipError_t launch_adamw_read(const AdamTensor *t, int count, float *const *m_out, float *const *v_out, hipStream_t s) {

@@ -93,7 +93,7 @@ class MoeAdamwTensor(ctypes.Structure):
 class MoeAdamwHparams(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("step", ctypes.c_int64), ("lr_dev", ctypes.c_void_p),
-                ("step_dev", ctypes.c_void_p), ("norm", ctypes.c_void_p)]
+                ("step_dev", ctypes.c_void_p), ("norm", ctypes.c_void_p), ("skipped", ctypes.c_void_p)]
 
 
 _lib = None
@@ -634,10 +634,11 @@ class MoEAdamW:
     (one dict of m, v, m_scale, v_scale, master per tensor) takes existing state tensors
     instead of new zeros: a master in it is used whatever master_weights says, and one that
     master_weights asks for and it lacks is made from the parameter (`optimizer.states` then
-    holds it, not the caller's dict).  `step` is the number of steps already done.  With capturable=True
+    holds it, not the caller's dict).  `step` is the number of updates already done.  With capturable=True
     the step number and lr live on the device, so that a step captured into a HIP graph
     counts on at every replay (step_count only counts calls); set the rate with set_lr() then.
-    A step skipped because the norm was not finite counts too.
+    A step whose norm is not finite changes no tensor; `skipped` counts these on the device, and the
+    bias corrections go by the updates made (updates_done()).
 
     Tensors are used on the stream of the call, on the GPU that is current when the optimizer is
     built; allocation happens here, never in step().  The optimizer reads the memory that the
@@ -682,7 +683,7 @@ class MoEAdamW:
         self._memory = [t.detach() for s in self.states for t in s.values() if t is not None]
         self._memory += [p.detach() for p in self.params]
         self.hparams = MoeAdamwHparams(float(lr), float(betas[0]), float(betas[1]), float(eps), self.step_count, None,
-                                       None, None)
+                                       None, None, None)
         self._check_lr(lr)
         if max_grad_norm is not None and not max_grad_norm > 0:
             raise ValueError(f"max_grad_norm {max_grad_norm}: above 0, or None")
@@ -695,11 +696,13 @@ class MoEAdamW:
             self.step_dev = torch.full((1,), self.step_count, dtype=torch.int64, device=device)
             self.hparams.lr_dev, self.hparams.step_dev = self.lr_dev.data_ptr(), self.step_dev.data_ptr()
         self.grad_norm = None  # [2]: the norm before clipping, the factor applied
+        self.skipped = None    # [1]: steps left undone since the norm was not finite
         if max_grad_norm is not None:
             self._grad_list = grad_list(self.grads)
             self._ws = workspace(moe_grad_norm_workspace_size(self._grad_list), device)
             self.grad_norm = torch.zeros(2, dtype=torch.float32, device=device)
-            self.hparams.norm = self.grad_norm.data_ptr()
+            self.skipped = torch.zeros(1, dtype=torch.int64, device=device)
+            self.hparams.norm, self.hparams.skipped = self.grad_norm.data_ptr(), self.skipped.data_ptr()
 
     def _new_state(self, p, master_weights):
         z = lambda shape, dt: torch.zeros(shape, dtype=dt, device=p.device)  # noqa: E731
@@ -750,6 +753,12 @@ class MoEAdamW:
         self.hparams.step = self.step_count + 1
         moe_adamw_step(self.tensors, n, self.hparams, stream=stream)
         self.step_count += 1
+
+    def updates_done(self) -> int:
+        """Steps that updated the tensors, those before `step` included: the `step` to resume with.
+        Reads the device (waits for the current stream)."""
+        steps = int(self.step_dev) if self.capturable else self.step_count
+        return steps - (0 if self.skipped is None else int(self.skipped))
 
     def read_states(self, m_out=None, v_out=None, stream=None):
         """8-bit states as the floats they stand for, into the given tensors or new ones (which

@@ -930,6 +930,90 @@ def test_adamw_given_states_with_master_weights(bits):
         assert opt.states[0]["master"] is states[0]["master"]
 
 
+def _norm_of(grads, to):
+    """Writes value `to` over the first of the gradients: a norm that is not finite, or the way back."""
+    grads[0].view(-1)[0] = to
+
+
+@pytest.mark.parametrize("bits,n", [(32, 3), (8, 3), (32, 137), (8, 137)])
+@pytest.mark.parametrize("capturable", [False, True])
+def test_adamw_bias_corrections_count_the_updates_made(bits, n, capturable):
+    """A step that the norm's infinity or NaN leaves undone does not count in t (one launch, and several)."""
+    say(f"adamw t after skipped steps bits={bits} tensors={n} capturable={capturable}")
+    sizes = [300, 5, 4000] + [1 + (i * 37) % 700 for i in range(n - 3)]
+    whole, params, grads, states = _make(sizes, bits, "b", "b", True, seed=65, zero_state=True)
+    opt = ops.MoEAdamW(params, grads, weight_decay=0.0, state_bits=bits, states=states, max_grad_norm=1.0,
+                       capturable=capturable, **{**H, "lr": 2.0 ** -7})
+    kept = float(grads[0][0])
+    done = 0
+    for bad in (float("inf"), None, float("nan"), -float("inf"), None, None):
+        _norm_of(grads, kept if bad is None else bad)
+        start = [w.clone() for w in whole]
+        before = _snapshot(params, grads, states)
+        opt.step()
+        torch.cuda.synchronize()
+        if bad is not None:
+            assert all(torch.equal(a, b) for a, b, g in zip(start, whole, whole) if not torch.isnan(g.float()).any())
+            assert all(np.array_equal(to_np(p), b[0]) for p, b in zip(params, before))
+            continue
+        done += 1
+        _check_step(before, params, states, bits, [0.0] * n, done, scale=float(opt.grad_norm[1]), lr=2.0 ** -7)
+        assert opt.updates_done() == done
+    assert opt.step_count == 6 and int(opt.skipped) == 3
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_captured_steps_that_are_skipped(bits):
+    say(f"adamw graph with skipped steps bits={bits}")
+    whole, params, grads, states = _make([700, 3, 5000], bits, "b", "b", True, seed=66, zero_state=True)
+    opt = ops.MoEAdamW(params, grads, weight_decay=0.1, state_bits=bits, states=states, max_grad_norm=0.05,
+                       capturable=True, **H)
+    kept = float(grads[0][0])
+    _norm_of(grads, float("inf"))
+    opt.step()  # warms up, and leaves everything as it is
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        opt.step()
+    opt.step_dev.zero_()
+    opt.skipped.zero_()
+    for i, bad in enumerate((float("inf"), float("nan"), None, float("inf"), None)):
+        _norm_of(grads, kept if bad is None else bad)
+        before = _snapshot(params, grads, states)
+        graph.replay()
+        torch.cuda.synchronize()
+        if bad is None:
+            _check_step(before, params, states, bits, [0.1] * 3, {2: 1, 4: 2}[i], scale=float(opt.grad_norm[1]))
+    assert int(opt.step_dev) == 5 and int(opt.skipped) == 3 and opt.updates_done() == 2
+
+
+def test_adamw_skipped_counts_once_a_step_of_both_kinds():
+    """Tensors with 32-bit and with 8-bit states in one call: two launches, one step."""
+    say("adamw skipped steps of both kinds")
+    made = [_make([3000, 40], bits, "b", "b", True, seed=67 + bits) for bits in (32, 8)]
+    opts = [ops.MoEAdamW(p, g, state_bits=bits, states=s, **H) for bits, (_, p, g, s) in zip((32, 8), made)]
+    norm = torch.tensor([float("inf"), float("nan")], device=DEV)
+    skipped = torch.full((1,), 4, dtype=torch.int64, device=DEV)
+    start = [w.clone() for m in made for w in m[0]]
+    for order in ((0, 1), (1, 0), (0,), (1,)):
+        tensors = [opts[o].tensors[i] for o in order for i in range(2)]
+        arr = (ops.MoeAdamwTensor * len(tensors))(*tensors)
+        skipped.fill_(4)
+        h = ops.MoeAdamwHparams(1e-2, 0.9, 0.99, 1e-8, 7, None, None, norm.data_ptr(), skipped.data_ptr())
+        ops.moe_adamw_step(arr, len(tensors), h)
+        assert int(skipped) == 5, order
+    assert all(torch.equal(a, b) for a, b in zip(start, (w for m in made for w in m[0])))
+    # a norm to go by again: t is 7 - 5 for both kinds
+    norm.copy_(torch.tensor([1.0, 0.5]))
+    before = [_snapshot(p, g, s) for _, p, g, s in made]
+    tensors = [o.tensors[i] for o in opts for i in range(2)]
+    ops.moe_adamw_step((ops.MoeAdamwTensor * 4)(*tensors), 4, h)
+    torch.cuda.synchronize()
+    assert int(skipped) == 5
+    for bits, b, (_, p, _, s) in zip((32, 8), before, made):
+        _check_step(b, p, s, bits, [0.01, 0.01], 2, scale=0.5)
+
+
 # ------------------------------------------------------------------------------ the run together
 
 def _layer(T=300, d=128, E=8, k=2, f=192, cf=1.25, fs=64, seed=4, **kw):

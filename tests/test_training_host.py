@@ -311,6 +311,13 @@ def test_adamw_hparam_refusals(kw, word):
 
 
 @needs_lib
+def test_adamw_refuses_a_count_of_skipped_steps_that_is_not_aligned():
+    h = ops.MoeAdamwHparams(1e-3, 0.9, 0.999, 1e-8, 1, None, None, FAKE, FAKE + 8)
+    assert ops.lib().moe_adamw_step(_tensors(_tensor()), 1, ctypes.byref(h), None) == ops.MOE_ERR_INVALID
+    assert "skipped" in _last()
+
+
+@needs_lib
 def test_adamw_read_refusals():
     L = ops.lib()
     out = (ctypes.c_void_p * 1)(FAKE)
