@@ -643,11 +643,12 @@ class MoEAdamW:
     Tensors are used on the stream of the call, on the GPU that is current when the optimizer is
     built; allocation happens here, never in step().  The optimizer reads the memory that the
     gradients have when it is built, and keeps it alive: write gradients in place.  A parameter
-    whose memory has been replaced since is refused by step()."""
+    or gradient tensor whose memory has been replaced since is refused by step()."""
 
     def __init__(self, params, grads, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, max_grad_norm=None,
                  state_bits=32, master_weights=False, states=None, step=0, capturable=False):
-        self.params, self.grads = list(params), [g.detach() for g in grads]
+        self.params, given = list(params), list(grads)
+        self.grads = [g.detach() for g in given]
         n = len(self.params)
         if len(self.grads) != n or (states is not None and len(states) != n):
             raise ValueError("params, grads and states must have one entry per tensor")
@@ -678,7 +679,8 @@ class MoEAdamW:
                 p.numel(), dtype_code(p.dtype), dtype_code(g.dtype), state_bits, float(decay[i]))
         moe_adamw_check_tensors(self.tensors, n)
         self._device = _device()
-        self._pointers = list(map(torch.Tensor.data_ptr, self.params))
+        self._watched = self.params + given  # (a detached tensor keeps the memory it was made with)
+        self._pointers = list(map(torch.Tensor.data_ptr, self._watched))
         # what the host array points at stays alive, whatever becomes of the caller's tensors
         self._memory = [t.detach() for s in self.states for t in s.values() if t is not None]
         self._memory += [p.detach() for p in self.params]
@@ -740,8 +742,10 @@ class MoEAdamW:
     def step(self, stream=None) -> None:
         n = len(self.params)
         self._check_device()
-        if list(map(torch.Tensor.data_ptr, self.params)) != self._pointers:
-            raise RuntimeError("a parameter's memory has been replaced: build the optimizer again")
+        now = list(map(torch.Tensor.data_ptr, self._watched))
+        if now != self._pointers:
+            what = "parameter" if now[:n] != self._pointers[:n] else "gradient"
+            raise RuntimeError(f"a {what}'s memory has been replaced: build the optimizer again")
         if self.capturable:
             if stream is not None:
                 raise ValueError("a capturable step runs on the current stream")

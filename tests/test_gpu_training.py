@@ -1014,6 +1014,24 @@ def test_adamw_skipped_counts_once_a_step_of_both_kinds():
         _check_step(b, p, s, bits, [0.01, 0.01], 2, scale=0.5)
 
 
+def test_adamw_refuses_gradients_whose_memory_was_replaced():
+    """As for parameters: the memory that the optimizer was built with would be read, an old gradient."""
+    say("adamw refuses replaced gradients")
+    for kw in (dict(), dict(max_grad_norm=1.0), dict(capturable=True)):
+        p, g = torch.ones(100, device=DEV), torch.ones(100, device=DEV)
+        opt = ops.MoEAdamW([p], [g], **{**H, **kw})
+        opt.step()
+        kept, old = p.clone(), g.data
+        g.data = torch.full((100,), 7.0, device=DEV)
+        with pytest.raises(RuntimeError, match="gradient's memory has been replaced"):
+            opt.step()
+        assert torch.equal(p, kept) and opt.step_count == 1
+        assert not opt.capturable or int(opt.step_dev) == 1
+        g.data = old
+        opt.step()
+        assert opt.step_count == 2
+
+
 # ------------------------------------------------------------------------------ the run together
 
 def _layer(T=300, d=128, E=8, k=2, f=192, cf=1.25, fs=64, seed=4, **kw):
