@@ -830,7 +830,9 @@ class MoETrainer:
 
     Buffers are allocated here, once; the optimizer's options (lr, weight_decay, max_grad_norm,
     state_bits, master_weights, capturable, ...) are MoEAdamW's.  The router is not decayed unless
-    weight_decay is given per tensor (router, gate_up, down[, shared gate_up, shared down])."""
+    weight_decay is given per tensor (router, gate_up, down[, shared gate_up, shared down]).  The
+    optimizer holds the weights of `inputs` and the `grads` that the trainer was built with: change
+    them in place; step() refuses others."""
 
     def __init__(self, inputs, capacity, device="cuda", fill_order="token", overflow="drop", tiled=False,
                  shared_tiled=False, alpha=0.01, z_coeff=0.001, seq_offsets=None, token_mask=None, weight_decay=0.01,
@@ -856,6 +858,7 @@ class MoETrainer:
         self.backward_ws = workspace(moe_backward_workspace_size(desc), device)
         if not isinstance(weight_decay, (list, tuple)):
             weight_decay = [0.0] + [weight_decay] * (len(names) - 1)
+        self._names = names
         self.optimizer = MoEAdamW(weights, [self.grads["dw_" + n] for n in names], weight_decay=weight_decay, **adamw)
 
     def forward(self):
@@ -873,6 +876,11 @@ class MoETrainer:
         return self.dx
 
     def step(self) -> None:
+        for n, p, g in zip(self._names, self.optimizer.params, self.optimizer.grads):
+            if getattr(self.layer.inputs, "w_" + n).data_ptr() != p.data_ptr():
+                raise RuntimeError(f"inputs.w_{n} is not the tensor that the optimizer updates: build the trainer again")
+            if self.grads["dw_" + n].data_ptr() != g.data_ptr():
+                raise RuntimeError(f"grads['dw_{n}'] is not the tensor that the optimizer reads: build the trainer again")
         self.optimizer.step()
         i, L = self.layer.inputs, self.layer
         if L.tiled is not None:

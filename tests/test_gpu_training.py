@@ -1146,6 +1146,28 @@ def test_training_step_replays_from_a_graph():
         assert torch.equal(eager.losses, other.losses) and torch.equal(eager.dx, other.dx)
 
 
+def test_training_step_refuses_weights_and_gradients_that_were_replaced():
+    """The optimizer holds the tensors that the trainer was built with: the layer would run on others."""
+    say("trainer refuses replaced weights and gradients")
+    w, inp, cap = _layer(T=40, d=128, E=4, f=128)
+    tr = ops.MoETrainer(inp, cap)
+    dy = torch.randn((40, 128), device=DEV).bfloat16()
+    tr.train_step(dy)
+    for name in ("w_router", "w_gate_up", "w_down", "w_shared_gate_up", "w_shared_down"):
+        old = getattr(inp, name)
+        setattr(inp, name, old.clone())
+        with pytest.raises(RuntimeError, match=name):
+            tr.step()
+        setattr(inp, name, old)
+    old = tr.grads["dw_down"]
+    tr.grads["dw_down"] = old.clone()
+    with pytest.raises(RuntimeError, match="dw_down"):
+        tr.step()
+    tr.grads["dw_down"] = old
+    tr.train_step(dy)
+    assert tr.optimizer.step_count == 2
+
+
 def test_binding_refuses_wrong_tensors():
     say("binding refusals on the device")
     desc = ops.make_desc(10, 64, 64, 4, 2, None)
