@@ -687,8 +687,8 @@ class MoEAdamW:
         self.hparams = MoeAdamwHparams(float(lr), float(betas[0]), float(betas[1]), float(eps), self.step_count, None,
                                        None, None, None)
         self._check_lr(lr)
-        if max_grad_norm is not None and not max_grad_norm > 0:
-            raise ValueError(f"max_grad_norm {max_grad_norm}: above 0, or None")
+        if max_grad_norm is not None and not ctypes.c_float(max_grad_norm).value > 0:
+            raise ValueError(f"max_grad_norm {max_grad_norm}: above 0 as a float, or None")
         self.hparams.step += 1
         moe_adamw_step(self.tensors, 0, self.hparams)  # of no tensor: only the checks
         device = self.params[0].device if n else "cuda"
@@ -749,11 +749,12 @@ class MoEAdamW:
         if self.capturable:
             if stream is not None:
                 raise ValueError("a capturable step runs on the current stream")
-            self.step_dev.add_(1)
         elif _capturing(stream):
             raise RuntimeError("a captured step would repeat its step number: construct MoEAdamW with capturable=True")
         if self.max_grad_norm is not None:
             moe_grad_norm(self._grad_list, self.max_grad_norm, self.grad_norm, self._ws, stream=stream)
+        if self.capturable:  # behind what may refuse the call
+            self.step_dev.add_(1)
         self.hparams.step = self.step_count + 1
         moe_adamw_step(self.tensors, n, self.hparams, stream=stream)
         self.step_count += 1

@@ -1032,6 +1032,20 @@ def test_adamw_refuses_gradients_whose_memory_was_replaced():
         assert opt.step_count == 2
 
 
+def test_adamw_refuses_a_norm_that_is_no_float_and_counts_no_refused_step():
+    say("adamw max_grad_norm below the floats")
+    p, g = torch.ones(100, device=DEV), torch.ones(100, device=DEV)
+    for capturable in (False, True):
+        with pytest.raises(ValueError, match="max_grad_norm"):
+            ops.MoEAdamW([p], [g], max_grad_norm=1e-60, capturable=capturable, **H)
+        ops.MoEAdamW([p], [g], max_grad_norm=1e60, capturable=capturable, **H).step()  # infinity: no clipping
+    opt = ops.MoEAdamW([p], [g], max_grad_norm=1.0, capturable=True, **H)
+    opt.max_grad_norm = -1.0
+    with pytest.raises(ops.MoEError, match="max_norm"):
+        opt.step()
+    assert int(opt.step_dev) == 0 and opt.step_count == 0
+
+
 # ------------------------------------------------------------------------------ the run together
 
 def _layer(T=300, d=128, E=8, k=2, f=192, cf=1.25, fs=64, seed=4, **kw):
