@@ -495,8 +495,10 @@ size_t moe_grad_norm_workspace_size(const moe_grad_view *grads, int32_t num_tens
 
 /* Norm over every value of every tensor, and the factor that clips it:
  *   out[0] = sqrt(sum g^2),  out[1] = min(1, max_norm / (out[0] + 1e-6))
- * summed in 64 bits in a fixed order.  A norm that is not finite has out[1] = NaN, which
- * moe_adamw_step takes as "leave everything as it is".  out stays on the device:
+ * summed in 64 bits in a fixed order.  Where a gradient is not finite out[1] = NaN, which
+ * moe_adamw_step takes as "leave everything as it is".  Finite gradients whose norm is past
+ * the largest float have infinity in out[0] and their factor in out[1] all the same (g' is
+ * finite, the step is made): out[1] alone tells.  out stays on the device:
  * moe_adamw_hparams.norm takes it as it is.
  *   grads     HOST array of num_tensors views (read during the call only)
  *   max_norm  above 0; infinity: no clipping

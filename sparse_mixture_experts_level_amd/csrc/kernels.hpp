@@ -191,7 +191,8 @@ struct NormTensor {
   int32_t pad;
 };
 size_t grad_norm_workspace_bytes(const NormTensor *t, int count);
-// out[0] = the norm, out[1] = min(1, max_norm / (norm + 1e-6)), NaN when the norm is not finite.
+// out[0] = the norm, out[1] = min(1, max_norm / (norm + 1e-6)) from the norm in 64 bits, NaN when
+// that is not finite (finite gradients of 2^33 values and less never reach it).
 hipError_t launch_grad_norm(const NormTensor *t, int count, float max_norm, float *out, void *ws, hipStream_t s);
 struct AdamTensor {
   void *param;

@@ -207,7 +207,8 @@ __global__ __launch_bounds__(1024) void grad_norm_finish_kernel(const double *__
     const double norm = sqrt(all);
     out[0] = (float)norm;
     const double scale = (double)max_norm / (norm + 1e-6);
-    // a norm that is not finite has no scale; AdamW then leaves everything as it was
+    // a gradient that is not finite leaves no scale, and AdamW everything as it was; a norm that is
+    // finite here but past the floats has its scale
     out[1] = norm < INFINITY ? (float)(scale < 1.0 ? scale : 1.0) : NAN;
   }
 }

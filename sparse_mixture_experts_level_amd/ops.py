@@ -584,7 +584,8 @@ def moe_grad_norm_workspace_size(grads: GradList) -> int:
 
 
 def moe_grad_norm(grads: GradList, max_norm: float, out, ws, stream=None) -> None:
-    """out [2] float: the norm over every gradient, and min(1, max_norm / (norm + 1e-6))."""
+    """out [2] float: the norm over every gradient (infinity past the floats), and min(1, max_norm / (norm +
+    1e-6)), NaN where a gradient is not finite."""
     dev = _device()
     if dev != grads.device:
         raise RuntimeError(f"the gradients are on GPU {grads.device}, which is not the current one")
@@ -637,8 +638,10 @@ class MoEAdamW:
     holds it, not the caller's dict).  `step` is the number of updates already done.  With capturable=True
     the step number and lr live on the device, so that a step captured into a HIP graph
     counts on at every replay (step_count only counts calls); set the rate with set_lr() then.
-    A step whose norm is not finite changes no tensor; `skipped` counts these on the device, and the
-    bias corrections go by the updates made (updates_done()).
+    A step with a gradient that is not finite changes no tensor if max_grad_norm is given: grad_norm[1]
+    is NaN then (grad_norm[0] can be infinite for finite gradients, whose step is made).  `skipped`
+    counts these steps on the device, and the bias corrections go by the updates made
+    (updates_done()).
 
     Tensors are used on the stream of the call, on the GPU that is current when the optimizer is
     built; allocation happens here, never in step().  The optimizer reads the memory that the
@@ -698,7 +701,7 @@ class MoEAdamW:
             self.step_dev = torch.full((1,), self.step_count, dtype=torch.int64, device=device)
             self.hparams.lr_dev, self.hparams.step_dev = self.lr_dev.data_ptr(), self.step_dev.data_ptr()
         self.grad_norm = None  # [2]: the norm before clipping, the factor applied
-        self.skipped = None    # [1]: steps left undone since the norm was not finite
+        self.skipped = None    # [1]: steps left undone for a gradient that was not finite
         if max_grad_norm is not None:
             self._grad_list = grad_list(self.grads)
             self._ws = workspace(moe_grad_norm_workspace_size(self._grad_list), device)

@@ -1046,6 +1046,25 @@ def test_adamw_refuses_a_norm_that_is_no_float_and_counts_no_refused_step():
     assert int(opt.step_dev) == 0 and opt.step_count == 0
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_steps_under_a_norm_past_the_floats(bits):
+    """Finite gradients whose norm no float holds: grad_norm[0] is infinite, the factor and the step are not."""
+    say(f"adamw norm past the floats bits={bits}")
+    n = 3000
+    gen = torch.Generator(device=DEV).manual_seed(71)
+    p = torch.randn(n, generator=gen, device=DEV)
+    g = torch.where(torch.rand(n, generator=gen, device=DEV) < 0.5, -1e38, 1e38)
+    opt = ops.MoEAdamW([p], [g], weight_decay=0.1, state_bits=bits, max_grad_norm=1.0, **H)
+    before = _snapshot([p], [g], opt.states)
+    opt.step()
+    torch.cuda.synchronize()
+    norm, scale = oracle.grad_norm([before[0][1]], 1.0)
+    got = to_np(opt.grad_norm)
+    assert np.isinf(got[0]) and abs(got[1] - scale) <= 1.5e-45  # one step among the smallest floats
+    assert int(opt.skipped) == 0
+    _check_step(before, [p], opt.states, bits, [0.1], 1, scale=float(got[1]))
+
+
 # ------------------------------------------------------------------------------ the run together
 
 def _layer(T=300, d=128, E=8, k=2, f=192, cf=1.25, fs=64, seed=4, **kw):
