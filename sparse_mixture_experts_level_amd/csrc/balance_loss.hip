@@ -703,22 +703,13 @@ hipError_t launch_main(const BalanceArgs &a, int blocks, hipStream_t s) {
     return hipGetLastError();                                                                                       \
   } while (0)
   const int v = values_per_lane(E);
-#define BL_CASE(L)                                  \
-  case L:                                           \
-    if (E % 4 == 0) {                               \
-      if (v == 4) BL_LAUNCH(L, 4, true);            \
-      if (v == 8) BL_LAUNCH(L, 8, true);            \
-      if (L < 64) return hipErrorInvalidValue;      \
-      if (v == 12) BL_LAUNCH(64, 12, true);         \
-      BL_LAUNCH(64, 16, true);                      \
-    }                                               \
-    if (v == 4) BL_LAUNCH(L, 4, false);             \
-    if (v == 6) BL_LAUNCH(L, 6, false);             \
-    if (v == 8) BL_LAUNCH(L, 8, false);             \
-    if (v == 10) BL_LAUNCH(L, 10, false);           \
-    if (v == 12) BL_LAUNCH(L, 12, false);           \
-    if (L < 64) return hipErrorInvalidValue;        \
-    BL_LAUNCH(64, 16, false);
+  // fewer than 64 lanes: as few values as lanes_per_token() asks for, no more
+#define BL_CASE(L)                                     \
+  case L:                                              \
+    if (E % 4 == 0 && v == 4) BL_LAUNCH(L, 4, true);   \
+    if (E % 4 != 0 && v == 4) BL_LAUNCH(L, 4, false);  \
+    if (E % 4 != 0 && v == 6) BL_LAUNCH(L, 6, false);  \
+    if (L < 64) return hipErrorInvalidValue;
   switch (lanes_per_token(E)) {
     BL_CASE(1)
     BL_CASE(2)
@@ -727,6 +718,15 @@ hipError_t launch_main(const BalanceArgs &a, int blocks, hipStream_t s) {
     BL_CASE(16)
     BL_CASE(32)
     BL_CASE(64)
+      if (E % 4 == 0) {
+        if (v == 8) BL_LAUNCH(64, 8, true);
+        if (v == 12) BL_LAUNCH(64, 12, true);
+        BL_LAUNCH(64, 16, true);
+      }
+      if (v == 8) BL_LAUNCH(64, 8, false);
+      if (v == 10) BL_LAUNCH(64, 10, false);
+      if (v == 12) BL_LAUNCH(64, 12, false);
+      BL_LAUNCH(64, 16, false);
   }
   return hipErrorInvalidValue;
 #undef BL_CASE

@@ -177,6 +177,15 @@ def test_balance_loss_sequences(T, E, k, off, masked):
         assert not to_np(out.losses).any() and not to_np(out.dlogits).any()
 
 
+@pytest.mark.parametrize("E", [6, 7, 9, 11, 12, 13, 15, 17, 20, 23, 25, 31, 36, 47, 49, 63, 68, 95, 97, 127, 132, 191, 193,
+                               255, 260, 383, 385, 511, 516, 639, 641, 767, 768, 769, 772, 1023])
+def test_balance_loss_at_the_ends_of_each_way_to_hold_a_row(E):
+    """Fewest and most experts of each number of lanes and values a row is held in."""
+    say(f"balance E={E}")
+    rng, l, ids = _draw(72 + E, 70, E, min(E, 5))
+    _check_balance(l, ids, mask=rng.random(70) < 0.8, off=[3, 40, 66])
+
+
 def test_balance_loss_masked_rows_may_hold_anything():
     say("balance masked rows with NaN and infinities")
     rng, l, ids = _draw(5, 200, 20, 3)
