@@ -451,7 +451,9 @@ size_t moe_balance_workspace_size(const moe_desc *desc, int32_t num_seqs);
  *   token_mask  [T] uint8 or NULL: zero = not counted (padding); its logits may hold
  *               anything, NaN included
  *   seq_offsets [num_seqs + 1] int32 or NULL (one sequence of all T tokens, num_seqs 1):
- *               non-decreasing within [0, T] (precondition); sequence s holds tokens
+ *               non-decreasing within [0, T] (precondition; checked by the debug build,
+ *               which synchronises the stream; others read and write nothing out of range
+ *               but give no meaningful result); sequence s holds tokens
  *               seq_offsets[s] .. seq_offsets[s + 1] - 1, possibly none; tokens before the
  *               first and behind the last sequence are not counted
  *   counts      [num_seqs, E] int32, written

@@ -1209,6 +1209,25 @@ moe_status check_num_seqs(int32_t num_seqs, const int32_t *seq_offsets) {
   return check_opt_ptr(seq_offsets, "seq_offsets");
 }
 
+#ifdef MOE_DEBUG_CHECKS
+// Debug builds: the offsets' precondition (non-decreasing within [0, T]) on a synchronous copy.
+moe_status debug_check_offsets(const moe_desc &D, const int32_t *off_dev, int32_t num_seqs, hipStream_t s) {
+  if (!off_dev) return MOE_OK;
+  std::vector<int32_t> h((size_t)num_seqs + 1);
+  MOE_TRY_HIP(hipMemcpyAsync(h.data(), off_dev, h.size() * sizeof(int32_t), hipMemcpyDeviceToHost, s),
+              "debug check: copy seq_offsets to the host");
+  MOE_TRY_HIP(hipStreamSynchronize(s), "debug check: synchronise");
+  for (int32_t i = 0; i <= num_seqs; ++i)
+    if (h[i] < (i ? h[i - 1] : 0) || h[i] > D.num_tokens)
+      return fail(MOE_ERR_INVALID, "seq_offsets[%d] = %d: must be non-decreasing within [0, num_tokens=%d]", i, h[i],
+                  D.num_tokens);
+  return MOE_OK;
+}
+#define MOE_DEBUG_CHECK_OFFSETS(D, off, n, s) MOE_TRY(debug_check_offsets((D), (off), (n), (s)))
+#else
+#define MOE_DEBUG_CHECK_OFFSETS(D, off, n, s) ((void)0)
+#endif
+
 moe_status check_dlogits(const moe_desc &D, const float *logits, const float *dlogits) {
   const uint8_t *a = reinterpret_cast<const uint8_t *>(logits), *b = reinterpret_cast<const uint8_t *>(dlogits);
   const size_t bytes = (size_t)D.num_tokens * D.num_experts * 4;
@@ -1373,6 +1392,7 @@ moe_status moe_balance_loss(const moe_desc *desc, const float *logits, const int
     return fail(MOE_ERR_WORKSPACE, "moe_balance_loss needs %zu workspace bytes, got %zu", need,
                 ws ? ws_bytes : (size_t)0);
   MOE_TRY(check_ptr(ws, "ws"));
+  MOE_DEBUG_CHECK_OFFSETS(D, seq_offsets, num_seqs, stream);
   const moe::BalanceCall c{logits,       topk_ids,      token_mask, seq_offsets, nullptr, dlogits,
                            D.num_tokens, D.num_experts, D.top_k,    num_seqs,    alpha,   z_coeff};
   MOE_TRY_HIP(moe::launch_balance_loss(c, counts, seq_tokens, mean_probs, losses, ws, stream), "balance loss");
@@ -1396,6 +1416,7 @@ moe_status moe_balance_loss_backward(const moe_desc *desc, const float *logits, 
   MOE_TRY(check_opt_ptr(dloss, "dloss"));
   MOE_TRY(check_ptr(dlogits, "dlogits"));
   MOE_TRY(check_dlogits(D, logits, dlogits));
+  MOE_DEBUG_CHECK_OFFSETS(D, seq_offsets, num_seqs, stream);
   const moe::BalanceCall c{logits,       nullptr,       token_mask, seq_offsets, dloss, dlogits,
                            D.num_tokens, D.num_experts, D.top_k,    num_seqs,    alpha, z_coeff};
   MOE_TRY_HIP(moe::launch_balance_backward(c, counts, seq_tokens, stream), "balance loss backward");

@@ -186,6 +186,34 @@ def test_balance_loss_at_the_ends_of_each_way_to_hold_a_row(E):
     _check_balance(l, ids, mask=rng.random(70) < 0.8, off=[3, 40, 66])
 
 
+def test_balance_debug_library_rejects_offsets_that_are_none():
+    """libmoe_debug.so checks the offsets on the host before any launch, in both directions."""
+    say("balance offsets refused by the debug library")
+    T, E, k, S = 50, 8, 2, 3
+    _, l, ids = _draw(73, T, E, k)
+    desc, lg, ig, _, _, out = _balance(l, ids, off=[0, 20, 20, 50])
+    D = ops.debug_lib()
+    ws = ops.workspace(ops.moe_balance_workspace_size(desc, S))
+    kept = {n: w.clone() for n, w in out.whole.items()}
+    for off, ok in [([0, 20, 20, 50], True), ([4, 20, 21, 47], True), ([0, 21, 20, 50], False), ([-1, 20, 20, 50], False),
+                    ([0, 20, 20, 51], False)]:
+        og = torch.tensor(off, dtype=torch.int32, device=DEV)
+        fwd = D.moe_balance_loss(ops.ctypes.byref(desc), lg.data_ptr(), ig.data_ptr(), None, og.data_ptr(), S, 0.3, 0.05,
+                                 out.counts.data_ptr(), out.seq_tokens.data_ptr(), out.mean_probs.data_ptr(),
+                                 out.losses.data_ptr(), out.dlogits.data_ptr(), ws.data_ptr(), ws.numel(), None)
+        torch.cuda.synchronize()
+        bwd = D.moe_balance_loss_backward(ops.ctypes.byref(desc), lg.data_ptr(), None, og.data_ptr(), S,
+                                          out.counts.data_ptr(), out.seq_tokens.data_ptr(), 0.3, 0.05, None,
+                                          out.dlogits.data_ptr(), None)
+        torch.cuda.synchronize()
+        if ok:
+            assert fwd == bwd == ops.MOE_OK
+            kept = {n: w.clone() for n, w in out.whole.items()}
+        else:
+            assert fwd == bwd == ops.MOE_ERR_INVALID and b"seq_offsets" in D.moe_last_error()
+            assert all(torch.equal(w, kept[n]) for n, w in out.whole.items())
+
+
 def test_balance_loss_masked_rows_may_hold_anything():
     say("balance masked rows with NaN and infinities")
     rng, l, ids = _draw(5, 200, 20, 3)
