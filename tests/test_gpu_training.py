@@ -330,6 +330,37 @@ def test_balance_loss_past_32_bits(off):
         assert torch.equal(part, out.dlogits[rows]) and bool(part.any())
 
 
+def test_balance_sums_past_32_bits():
+    """More than 2^31 logits, R their largest range within a row.  A probability is off by 4 R + 41 u (twice the
+    exponential's 2 R + 8, 22 roundings of the row's sum, reciprocal and product); a mean adds what one lane adds up in
+    floats (a quarter of a 512th of the rows) and 8 u.  The losses are sums in 64 bits: 25 u for the row's dot product,
+    and z off by (2 R + 33) u (|z| + 1)."""
+    say("balance sums T=2^21+77 E=1024")
+    T, E, alpha, z = 2 ** 21 + 77, 1024, 0.3, 0.05
+    gen = torch.Generator(device=DEV).manual_seed(75)
+    lg = torch.randn((T, E), generator=gen, device=DEV)
+    ids = torch.randint(0, E, (T, 1), generator=gen, device=DEV, dtype=torch.int32)
+    desc, out = ops.make_desc(T, 64, 64, E, 1, None), Outputs(1, E, 1)
+    ops.moe_balance_loss(desc, lg, ids, alpha, z, out.counts, out.seq_tokens, out.mean_probs, out.losses,
+                         ops.workspace(ops.moe_balance_workspace_size(desc)))
+    torch.cuda.synchronize()
+    out.check_guards()
+    probs, squares, R = torch.zeros(E, dtype=torch.float64, device=DEV), 0.0, 0.0
+    for i in range(0, T, 1 << 16):
+        l = lg[i:min(i + (1 << 16), T)].double()
+        lse = torch.logsumexp(l, 1)
+        probs += (l - lse[:, None]).exp().sum(0)
+        squares += float((lse * lse).sum())
+        R = max(R, float((l.amax(1) - l.amin(1)).max()))
+    probs /= T
+    rows = -(--(-T // 512) // 4)
+    assert torch.all((out.mean_probs[0] - probs).abs() <= (4 * R + 41 + rows + 8) * U * probs)
+    losses = to_np(out.losses)
+    want = alpha * E * float((out.counts[0].double() / T * probs).sum()), z * squares / T
+    assert abs(losses[0] - want[0]) <= (4 * R + 41 + 25) * U * want[0]
+    assert abs(losses[1] - want[1]) <= 2 * (2 * R + 34) * U * (2 * want[1] + z)
+
+
 @pytest.mark.parametrize("T,E,k,off", [(200, 32, 4, None), (300, 33, 3, [4, 100, 100, 290]), (70, 64, 2, [0, 70]),
                                        (40, 1, 1, None), (40, 700, 8, None), (40, 1023, 8, None)])
 def test_balance_gradient_of_uncounted_tokens_is_zero_whatever_comes_from_above(T, E, k, off):
@@ -1100,6 +1131,42 @@ def test_adamw_steps_under_a_norm_past_the_floats(bits):
     assert np.isinf(got[0]) and abs(got[1] - scale) <= 1.5e-45  # one step among the smallest floats
     assert int(opt.skipped) == 0
     _check_step(before, [p], opt.states, bits, [0.1], 1, scale=float(got[1]))
+
+
+@pytest.mark.parametrize("bits,gdt", [(32, torch.float32), (32, torch.bfloat16), (8, torch.float32)])
+def test_adamw_steps_and_states_past_32_bits(bits, gdt):
+    """More than 2^31 values, zero but for four places: the start, one far before 2^31, the values around it, the end.
+    Two steps of weights, copies, both states and their scales against the oracle's, and the states read back."""
+    n = 2 ** 31 + 777
+    say(f"adamw bits={bits} gradients {gdt}, 2^31 + 777 values")
+    places = [(0, 512), (2 ** 30 + 256, 2 ** 30 + 1024), (2 ** 31 - 512, 2 ** 31 + 256), (2 ** 31 + 512, n)]
+    gen = torch.Generator(device=DEV).manual_seed(74)
+    p, g = torch.zeros(n, dtype=torch.bfloat16, device=DEV), torch.zeros(n, dtype=gdt, device=DEV)
+    for a, b in places:
+        p[a:b] = torch.randn(b - a, generator=gen, device=DEV).bfloat16()
+        g[a:b] = torch.randn(b - a, generator=gen, device=DEV).to(gdt)
+    opt = ops.MoEAdamW([p], [g], weight_decay=0.1, state_bits=bits, master_weights=True, max_grad_norm=1.0, **H)
+    s = opt.states[0]
+    parts = [(p[a:b], g[a:b], {k: t[a // 256:-(-b // 256)] if k.endswith("scale") else t[a:b] for k, t in s.items()})
+             for a, b in places]
+    cut = [list(x) for x in zip(*parts)]
+    for t in (1, 2):
+        before = _snapshot(*cut)
+        opt.step()
+        torch.cuda.synchronize()
+        norm, _ = oracle.grad_norm([b[1] for b in before], 1.0)
+        assert abs(float(opt.grad_norm[0]) - norm) <= 2 * U * norm
+        _check_step(before, cut[0], cut[2], bits, [0.1] * len(places), t, scale=float(opt.grad_norm[1]))
+        g.mul_(-0.75)
+    live = sum(b - a for a, b in places)
+    for name, x in [("param", p)] + list(s.items()):
+        assert int(torch.count_nonzero(x)) <= (live + 255 if name.endswith("scale") else live), name
+    if bits == 8:
+        m, v = opt.read_states()
+        for (a, b), st in zip(places, cut[2]):
+            assert np.array_equal(to_np(m[0][a:b]), oracle.read_m(to_np(st["m"]), to_np(st["m_scale"])).astype(np.float32))
+            assert np.array_equal(to_np(v[0][a:b]), oracle.read_v(to_np(st["v"]), to_np(st["v_scale"])).astype(np.float32))
+        assert int(torch.count_nonzero(m[0])) <= live and int(torch.count_nonzero(v[0])) <= live
 
 
 # ------------------------------------------------------------------------------ the run together
