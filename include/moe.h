@@ -520,7 +520,16 @@ moe_status moe_grad_norm(const moe_grad_view *grads, int32_t num_tensors, float 
  * are the same for any program that follows them.  A block whose largest is below the
  * smallest normal float is held as zeros; one with a value that is not finite gets a NaN
  * scale, with which all its values count as NaN from the next step on.  Zeros everywhere are
- * the initial state of both forms. */
+ * the initial state of both forms.
+ * Take beta2 <= 0.98 with states in 8 bits.  Rounding to the nearest code undoes a step's
+ * change that is below half the way to the next one: while its block's scale stays, a v of
+ * code c without gradients falls only if beta2 < (1 - 1 / c + 1 / (2 c^2))^2 (0.95: c >= 39,
+ * v above 5e-4 of the block's largest; 0.99: c >= 199; 0.9922 and above: never), and it rises
+ * only at gradients whose square is some 1 + 2 / (c (1 - beta2)) times v.  Simulated against
+ * states in 32 bits, sqrt(v') of stationary gradients is in the median the same up to beta2 =
+ * 0.99; with 0.999 it is 1.5 times too high in a block of equal variances, and 4 times too
+ * high 3000 steps after half of a block's gradients fell to a tenth (0.98: 1.01 times).  m
+ * with beta1 = 0.9 falls from c = 10 on, 0.6% of its block's largest. */
 typedef struct moe_adamw_tensor {
   void *param;      /* [n] param_dtype, updated */
   const void *grad; /* [n] grad_dtype */

@@ -23,6 +23,8 @@
 // block's largest, 0.9 scale + 0.1 g, lies halfway between two floats in some percent of
 // the blocks, and the last place then decides the scale.  A v' above zero takes one code at
 // least: held as zero, it would let the next step divide by eps alone.
+// What rounding to nearest costs: a v without gradients leaves its code only if beta2 < (1 - 1 / c
+// + 1 / (2 c^2))^2, never from 0.9922 on: beta2 = 0.999 is for states in 32 bits.
 #include <algorithm>
 #include <cmath>
 

@@ -631,7 +631,8 @@ class MoEAdamW:
     clipping by the gradients' norm when max_grad_norm is given (moe_grad_norm).
 
     Parameters and gradients are float or bf16; weight_decay is one value or one per tensor.
-    state_bits 32 or 8; master_weights keeps a float copy of each bf16 parameter.  `states`
+    state_bits 32 or 8; with 8 take a beta2 of at most 0.98 (with 0.999 rounding to the nearest code
+    keeps v from falling with its own decay; include/moe.h has the borders); master_weights keeps a float copy of each bf16 parameter.  `states`
     (one dict of m, v, m_scale, v_scale, master per tensor) takes existing state tensors
     instead of new zeros: a master in it is used whatever master_weights says, and one that
     master_weights asks for and it lacks is made from the parameter (`optimizer.states` then

@@ -1169,6 +1169,61 @@ def test_adamw_steps_and_states_past_32_bits(bits, gdt):
         assert int(torch.count_nonzero(m[0])) <= live and int(torch.count_nonzero(v[0])) <= live
 
 
+@pytest.mark.parametrize("beta2", [0.9, 0.95, 0.98, 0.99, 0.992, 0.993, 0.999])
+def test_adamw_8bit_v_falls_where_the_formula_says(beta2):
+    """Codes 1 .. 255 of v without gradients, beside a largest that stays: a step lowers a code where its v' = beta2 v
+    is past the border (c (c - 1) + 1/2)^2 below it, and nowhere else; after many steps the codes above are gone."""
+    say(f"adamw 8-bit v falling, beta2={beta2}")
+    codes = np.arange(256)
+    codes[0] = 255  # the block's largest, under a gradient that keeps it
+    p, g = torch.ones(256, device=DEV), torch.zeros(256, device=DEV)
+    g[0] = 1.0
+    s = dict(m=torch.zeros(256, dtype=torch.int8, device=DEV), m_scale=torch.zeros(1, device=DEV),
+             v=torch.tensor(codes, dtype=torch.uint8, device=DEV), v_scale=torch.ones(1, device=DEV))
+    opt = ops.MoEAdamW([p], [g], lr=0.0, betas=(0.9, beta2), state_bits=8, states=[s])
+    opt.step()
+    c = np.arange(1, 256).astype(np.float64)
+    falls = beta2 * c ** 4 < (c * (c - 1) + 0.5) ** 2  # no code is within 1e-8 of it
+    falls[0] = False                                   # above zero: one at least
+    assert np.array_equal(to_np(s["v"])[1:] < codes[1:], falls)
+    assert falls.any() == (beta2 < 0.9922) and (beta2 != 0.95 or falls.nonzero()[0][0] + 1 == 39)
+    for _ in range(260):
+        opt.step()
+    left = to_np(s["v"])[1:]
+    if falls.any():
+        assert np.array_equal(left, np.minimum(codes[1:], falls.nonzero()[0][0]))  # codes below the lowest that falls
+    else:
+        assert np.array_equal(left, codes[1:])
+
+
+@pytest.mark.parametrize("beta2", [0.95, 0.98])
+def test_adamw_8bit_v_follows_32_bits_over_many_steps(beta2):
+    """300 steps of the same gradients, half of which shrink tenfold: v in 8 bits is off from v in 32 by no more than
+    each step's half cell (c^2 + c + 1/2)^2 - c^4 of scale / 255^4, carried on by beta2 (and 6 u of v a step)."""
+    n, steps = 256 * 40, 300
+    gen = torch.Generator(device=DEV).manual_seed(76)
+    p = torch.zeros(n, device=DEV)
+    grad = torch.zeros(n, device=DEV)
+    opts = [ops.MoEAdamW([p.clone()], [grad], lr=0.0, betas=(0.9, beta2), state_bits=bits) for bits in (8, 32)]
+    size = torch.exp(torch.randn(n, generator=gen, device=DEV))
+    bound = torch.zeros(n, dtype=torch.float64, device=DEV)
+    s8, s32 = opts[0].states[0], opts[1].states[0]
+    for t in range(steps):
+        if t == 100:
+            size[::2] *= 0.1
+        grad.copy_(torch.randn(n, generator=gen, device=DEV) * size)
+        for o in opts:
+            o.step()
+        c = s8["v"].double()
+        cell = ((c * c + c + 0.5) ** 2 - c ** 4) * (s8["v_scale"].double() / 255.0 ** 4).repeat_interleave(256)
+        bound = beta2 * bound + cell * (1 + 4 * U)  # (the scale is the largest rounded to a float)
+    v8 = opts[0].read_states()[1][0].double()
+    v32 = s32["v"].double()
+    assert torch.all((v8 - v32).abs() <= bound + 2 * U * v8 + 6 * U * steps * v32)
+    off = (v8.sqrt() / v32.sqrt() - 1).abs()
+    print(f"root of v off: median {float(off.median()):.4f}")
+
+
 # ------------------------------------------------------------------------------ the run together
 
 def _layer(T=300, d=128, E=8, k=2, f=192, cf=1.25, fs=64, seed=4, **kw):
