@@ -318,7 +318,8 @@ moe_status moe_combine_unpermute(const moe_desc *desc, const void *y_perm, const
  *   expert_counts [E] int32 (as written by moe_dispatch_permute)
  *   loss          [1] float, written (device)
  *   ws            at least moe_workspace_size(desc) bytes
- * Float accumulation in fixed orders: bit-reproducible. */
+ * Float accumulation in fixed orders: bit-reproducible.  A value to report; moe_balance_loss
+ * has the gradient, and counts for itself. */
 moe_status moe_router_aux_loss(const moe_desc *desc, const float *logits, const int32_t *expert_counts, float alpha,
                                float *loss, void *ws, size_t ws_bytes, hipStream_t stream);
 
@@ -442,8 +443,9 @@ size_t moe_balance_workspace_size(const moe_desc *desc, int32_t num_seqs);
  *   losses[1] = z_coeff / N sum_t z_t^2
  *   dlogits_ti = p_ti (alpha E / (S' N_s) (f_si - sum_j f_sj p_tj) + 2 z_coeff / N z_t)
  * (f held fixed: counts are piecewise constant).  One sequence of all tokens gives
- * moe_router_aux_loss's value.  Only descriptor fields num_tokens, num_experts and top_k
- * matter.
+ * moe_router_aux_loss's value: that call takes counts that the dispatch has written and gives
+ * the value alone, to report; this one counts for itself and is the one to train with.  Of a
+ * valid descriptor only num_tokens, num_experts and top_k matter.
  *   logits      [T, E] float; -inf is an expert with probability 0; a counted token with
  *               no finite logit has no probabilities: it adds nothing to P and the z loss
  *               and gets a zero gradient (its ids are counted)

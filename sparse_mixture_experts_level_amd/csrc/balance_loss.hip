@@ -10,10 +10,14 @@
 // The gradient needs the counts but not the probabilities' means, so one pass over the
 // logits gives both.  Counts come first (their own launch, or inside the main pass), the
 // column sums' ends last.  Large batches are bound by reading the logits and writing the
-// gradient once (gradient of 60001 x 161 alone 18.3 us, 4.2 TB/s; 65536 x 128 14.3 us, 4.7
+// gradient once (gradient of 60001 x 161 alone 18.0 us, 4.3 TB/s; 65536 x 128 14.3 us, 4.7
 // TB/s), smaller ones by the launches and the chains of loads in them (16384 x 256 in nine
 // sequences with the losses 21 us in three launches; 8192 x 64 9.8 us in two; 16 x 32 5.0 us
-// in one).  Every sum has a fixed order (bit-reproducible); counts are whole numbers.
+// in one).  Without the gradient: 4.8, 9.3 and 19 us.  Many sequences cost blocks: a piece is one
+// however short, and with more than 64 sequences each block of the gradient alone adds up every
+// sequence's tokens (65536 x 64 in 512, 4096, 16384 and 65536 sequences: 29, 99, 340 and 1240 us
+// with the losses; 11, 25, 111 and 820 alone).  Every sum has a fixed order (bit-reproducible);
+// counts are whole numbers.
 #include <algorithm>
 
 #include "common.hpp"
@@ -657,8 +661,10 @@ __global__ __launch_bounds__(BL_FIN_THREADS) void balance_finish_kernel(FinishAr
 
 // Values a lane takes at most (16 past 64 lanes).  One 16-byte load where rows allow it: 8 values
 // measured 5.9 against 5.1 us on 16 x 32 and 9.5 against 9.3 on 16384 x 256 (gradient alone),
-// 16 values 8.4 and 13.0.  Odd rows, where a value is a load and few lanes save reductions: up
-// to 6 or 8 values 17.6 us on 60001 x 161, up to 4 24.4, up to 12 24.8.
+// 16 values 8.4 and 13.0.  Odd rows, where a value is a load and few lanes save reductions, up to 4,
+// 6, 8 and 12 values (gradient alone): 52103 x 161 19.3, 15.6, 15.6, 16.6 us; 43919 x 191 17.9,
+// 15.5, 15.7, 16.7; 129055 x 65 19.3, 17.8, 18.9, 37.9.  Large batches of 17 to 47 experts are the
+// exception: 254200 x 33 19.6, 36.6, 36.9, 86.4 (4000 rows: the same for all but 12).
 constexpr int kVecValues = 4, kOddValues = 6;
 // Lanes a token takes: a power of two.
 int lanes_per_token(int E) {
@@ -757,8 +763,9 @@ BalanceWs balance_ws(int T, int E, int S) {
 }
 
 // One sequence with at most this many choices is counted by every block of the main pass for
-// itself, against a launch that counts: 8192 choices 11.7 against 13.4 us, 16384 13.3 against
-// 12.8 (and a launch less for the host), 32768 17.8 against 13.3.
+// itself, against a launch that counts: 8192 x 64, one choice, 9.6 against 11.9 us; 16384 choices
+// of 16384 x 64 11.4 against 12.2, of 2048 x 256 11.6 against 12.0, of 8192 x 256 13.2 against
+// 14.5; 32768 of 32768 x 64 16.5 against 14.1, of 4096 x 256 15.3 against 12.4.
 constexpr int64_t kSelfCount = 16384;
 // Up to 64 sequences, and at most this many partial counts: every block of the main pass adds
 // up its sequence's for itself, and no launch for the tables is made: 65536 x 32 15.9 against

@@ -8,8 +8,9 @@
 // finds its tensor from the blocks' prefix sums.  Measured, where a copy of 4 GiB reaches
 // 5.9 TB/s read and written and a plain read 7.0: the norm of 176 M bf16 gradients 57 us (6.2
 // TB/s); AdamW with 32-bit states and a float copy on as many bf16 weights 880 us (5.6 TB/s);
-// with 8-bit states on 201 M 573 us (5.6 TB/s, its arithmetic of some 80 instructions a value
-// nearly as long), 1014 us with the norm before it and both states read back after it.
+// with 8-bit states on 201 M and a float copy 564 us (5.9 TB/s beyond L2, its arithmetic of some 80
+// instructions a value nearly as long), 1008 us with the norm before it and both states read back
+// after it.  Without a float copy the arithmetic is what bounds it (13 M values: 40 us, 3.3 TB/s).
 //
 // States in 8 bits: 256 values share a float scale, the block's largest magnitude.  m is a
 // signed code c that stands for scale c |c| / 127^2, v an unsigned one for scale (c/255)^4,
@@ -455,8 +456,9 @@ __device__ __forceinline__ float held_scale(uint32_t bits) {
 }
 
 // Codes of eight neighbouring values.  They are a small part of the traffic, and cached: what
-// reads the states next finds them there (a step of 13 M values with its states read back 67
-// -> 58 us; 201 M values: 1007 -> 1014).
+// reads the states next finds them there (13 M values, step and states read back: 60 against 69
+// us past the caches).  A step alone does not care: 13 M values 39.9 against 38.5 us, with a float
+// copy 42.9 against 43.3; 201 M 497 against 497, with a copy 595 against 587.
 struct Codes {
   uint32_t w[2];
   __device__ __forceinline__ uint32_t u(int j) const { return (w[j >> 2] >> (8 * (j & 3))) & 0xffu; }
