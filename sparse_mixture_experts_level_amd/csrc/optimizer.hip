@@ -528,9 +528,10 @@ __device__ __forceinline__ void adamw8(const Adam8Args &a, const Adam8 &t, const
     t.m_scale[q] = hm;
     t.v_scale[q] = hv;
   }
-  // Roots are taken of v' times 2^64 in blocks below one, so that the smallest floats, which
-  // the instruction takes for zeros, do not come up.
-  const bool small = hv < 1.f;
+  // Roots are taken of v' times 2^64 unless the block's largest would leave the floats, so that the
+  // smallest floats, which the instruction takes for zeros, do not come up (they would beside an
+  // eps below 1e-12).  Powers of two: the same roots otherwise.
+  const bool small = hv < 0x1p60f;
   const double up = small ? 0x1p64 : 1.0;
   Rates rr = r;
   rr.inv_bc2 = small ? r.inv_bc2 * 0x1p-32f : r.inv_bc2;

@@ -1224,6 +1224,29 @@ def test_adamw_8bit_v_follows_32_bits_over_many_steps(beta2):
     print(f"root of v off: median {float(off.median()):.4f}")
 
 
+@pytest.mark.parametrize("largest", [1e-3, 0.5, 100.0, 3e4, 1e9])
+def test_adamw_8bit_tiny_values_beside_large_ones(largest):
+    """A block's smallest v' may be below the smallest normal float while its largest is above one: roots of 1e-20 and
+    up weigh against an eps of 1e-16 all the same."""
+    say(f"adamw 8-bit tiny values beside {largest}")
+    rng = np.random.default_rng(77)
+    n, lr, b1, b2, eps = 512, 1.0, 0.9, 0.99, 1e-16
+    g = rng.standard_normal(n) * 10.0 ** -rng.uniform(15, 20, n)
+    g[[5, 300]] = largest
+    p, gd = torch.zeros(n, device=DEV), torch.tensor(g, dtype=torch.float32, device=DEV)
+    opt = ops.MoEAdamW([p], [gd], lr=lr, betas=(b1, b2), eps=eps, weight_decay=0.0, state_bits=8)
+    opt.step()
+    torch.cuda.synchronize()
+    z = np.zeros(n)
+    w, m, v = oracle.adamw_step(z, to_np(gd).astype(np.float64), z, z, 1, lr, b1, b2, eps, 0.0)
+    assert v.min() < 1e-38
+    bound = 16 * U * lr / (1 - b1) * np.abs(m) / (np.sqrt(v) / np.sqrt(1 - b2) + eps) + 1e-44
+    assert np.all(np.abs(to_np(p) - w) <= bound), (np.abs(to_np(p) - w) / bound).max()
+    (cm, sm), (cv, sv), s = oracle.held_m(m), oracle.held_v(v), opt.states[0]
+    assert np.array_equal(to_np(s["m_scale"]), sm) and np.array_equal(to_np(s["v_scale"]), sv)
+    assert np.array_equal(to_np(s["m"]), cm) and np.array_equal(to_np(s["v"]), cv)
+
+
 # ------------------------------------------------------------------------------ the run together
 
 def _layer(T=300, d=128, E=8, k=2, f=192, cf=1.25, fs=64, seed=4, **kw):
