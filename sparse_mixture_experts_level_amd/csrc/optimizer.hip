@@ -538,11 +538,12 @@ __device__ __forceinline__ void adamw8(const Adam8Args &a, const Adam8 &t, const
   // u as floats.  |m'| 127^2 / scale: the reciprocal (one in the last place), two products and
   // m' rounded, at most 3e-7; for v' the root of v' times 255^2 over the root of scale: two
   // instructions of one in the last place, two products and half of v's rounding, at most
-  // 4e-7.  A scale of m so small that its reciprocal leaves the floats is for 64 bits.
+  // 4e-7.  A scale of m so small or large that its reciprocal leaves the normal floats is for 64
+  // bits (a reciprocal below them is taken for zero).
   const bool none_m = !(hm > 0.f), none_v = !(hv > 0.f);  // zero or NaN: codes of zero
   const float imf = none_m ? 0.f : 16129.f * __builtin_amdgcn_rcpf(hm);
   const float ivf = none_v ? 0.f : 65025.f * __builtin_amdgcn_rsqf(hv) * (small ? 0x1p-32f : 1.f);
-  bool sure_m = none_m || hm > 0x1p-90f, sure_v = true;
+  bool sure_m = none_m || (hm > 0x1p-90f && hm < 0x1p120f), sure_v = true;
   Codes nm{{0u, 0u}}, nv{{0u, 0u}};
 #pragma unroll
   for (int j = 0; j < 8; ++j) {

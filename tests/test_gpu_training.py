@@ -1247,6 +1247,24 @@ def test_adamw_8bit_tiny_values_beside_large_ones(largest):
     assert np.array_equal(to_np(s["m"]), cm) and np.array_equal(to_np(s["v"]), cv)
 
 
+def test_adamw_8bit_scales_next_to_the_largest_float():
+    """A block of m whose scale's reciprocal is below the smallest normal float (states that were given so)."""
+    say("adamw 8-bit m_scale 3e38")
+    n = 512
+    c = (np.arange(n) % 255 - 127).astype(np.int8)
+    c[[0, 256]] = 127
+    s = dict(m=torch.tensor(c, device=DEV), m_scale=torch.tensor([3e38, 9e37], device=DEV),
+             v=torch.full((n,), 255, dtype=torch.uint8, device=DEV), v_scale=torch.full((2,), 1e38, device=DEV))
+    p, g = torch.zeros(n, device=DEV), torch.zeros(n, device=DEV)
+    before = _snapshot([p], [g], [s])
+    opt = ops.MoEAdamW([p], [g], lr=1e-2, betas=(0.99, 0.99), eps=1e-8, weight_decay=0.0, state_bits=8, states=[s])
+    opt.step()
+    torch.cuda.synchronize()
+    m = 0.99 * oracle.read_m(before[0][2]["m"], before[0][2]["m_scale"])
+    cm, sm = oracle.held_m(m)
+    assert np.array_equal(to_np(s["m_scale"]), sm) and np.array_equal(to_np(s["m"]), cm) and np.abs(cm).max() == 127
+
+
 # ------------------------------------------------------------------------------ the run together
 
 def _layer(T=300, d=128, E=8, k=2, f=192, cf=1.25, fs=64, seed=4, **kw):
