@@ -58,6 +58,8 @@ extern "C" {
 #define MOE_MAX_EXPERTS 1024
 #define MOE_MAX_SEQS 65536                         /* sequences of one balance loss */
 #define MOE_MAX_TENSOR_VALUES ((int64_t)1 << 33)   /* values of one optimizer tensor */
+#define MOE_FP8_BLOCK 128                          /* values (of a row) that share a scale in 8 bits */
+#define MOE_NORM_MAX_WIDTH 32768                   /* values of one row of the norm */
 #define MOE_ADAMW_BLOCK 256                        /* values that share a scale in 8-bit optimizer states */
 
 typedef enum moe_status {
@@ -590,6 +592,135 @@ moe_status moe_adamw_step(const moe_adamw_tensor *tensors, int32_t num_tensors, 
  *            an entry): not wanted */
 moe_status moe_adamw_read_states(const moe_adamw_tensor *tensors, int32_t num_tensors, float *const *m_out,
                                  float *const *v_out, hipStream_t stream);
+
+/* ------------------------------------------------- 8-bit floating point, norm, 8-bit experts */
+
+/* Rows in 8 bits.  Codes are e4m3 (largest 448, one NaN, no infinity), scales powers of two held
+ * as a byte, exponent + 127 (255: NaN); each MOE_FP8_BLOCK consecutive values of a row share one:
+ *   value[r][k] = code[r][k] * 2^(scale[r][k / 128] - 127)
+ *   codes [rows, moe_fp8_row_bytes(K)] uint8, ZERO behind column K
+ *   scale [rows, moe_fp8_scale_bytes(K)] uint8, a byte for each 128 columns; the bytes behind
+ *         the last block pad the row to a multiple of four and are not looked at
+ * The quantising calls take the least scale with which the block's largest finite magnitude is at
+ * most 448 (at least 2^-126; 1 for a block of zeros), so that no finite value saturates, and for
+ * each value the nearest code, ties to the even one; a value that is not finite gets the NaN
+ * code and has no part in the scale.  Powers of two, because the matrix instructions of gfx950
+ * apply them for nothing; against a float scale they cost no precision but that of values far
+ * below their block's largest (e4m3 is a floating format).  Both helpers: host only; 0 for K < 1. */
+int32_t moe_fp8_row_bytes(int32_t k);
+int32_t moe_fp8_scale_bytes(int32_t k);
+
+/* Rows to 8 bits.  x [rows, K] dtype; codes, scale as above, written in full (codes behind
+ * column K zeros, padding scales ones).  0 <= rows <= INT32_MAX. */
+moe_status moe_quantize_rows_fp8(int64_t rows, int32_t k, int32_t dtype, const void *x, uint8_t *codes, uint8_t *scale,
+                                 hipStream_t stream);
+
+/* The values that codes stand for.  out [rows, K] dtype, written (bf16: exact but for values
+ * past its range). */
+moe_status moe_dequantize_rows_fp8(int64_t rows, int32_t k, int32_t dtype, const uint8_t *codes, const uint8_t *scale,
+                                   void *out, hipStream_t stream);
+
+/* Weights of num_groups matrices in 8 bits, a scale for each 128 x 128 block, in the layout that
+ * the products read (written once, when weights are loaded).  swiglu 0: w [G, n_out, K];
+ * 1: w [G, 2 n_out, K], gate rows then up rows (moe_weights.w_gate_up with n_out = f), whose
+ * blocks are those of the gate rows and of the up rows apart.
+ *   codes  per group, blocks of 16 rows by 128 of K, 2 KB each, ordered [ceil(n_out / 16)][ceil(K /
+ *          128)] (swiglu: [ceil(n_out / 16)][2][ceil(K / 128)], gate then up); within one, byte
+ *          1024 p + 256 c + 16 r + i is row r, k = 64 p + 16 c + i; zeros where the matrix has ended
+ *   scale  per group [ceil(n_out / 128)][moe_fp8_scale_bytes(K)] (swiglu: [ceil(n_out / 128)][2][...])
+ * Sizes in bytes from the two helpers (host only; 0 for invalid arguments).  Scales and codes
+ * as for rows.  One group's codes must be below 2 GiB (MOE_ERR_UNSUPPORTED). */
+size_t moe_fp8_weights_bytes(int32_t num_groups, int32_t n_out, int32_t k, int32_t swiglu);
+size_t moe_fp8_weight_scales_bytes(int32_t num_groups, int32_t n_out, int32_t k, int32_t swiglu);
+moe_status moe_quantize_weights_fp8(int32_t num_groups, int32_t n_out, int32_t k, int32_t swiglu, int32_t dtype,
+                                    const void *w, uint8_t *codes, uint8_t *scale, hipStream_t stream);
+
+/* Root-mean-square norm of the residual stream in front of a layer:
+ *   h = x + residual, rounded to dtype (x itself without a residual)
+ *   rstd = 1 / sqrt(mean of h^2 over the row + eps), the mean formed in 64 bits
+ *   y = (h rstd) weight, in float; y rounded to dtype, and y8 quantised from the float
+ *   x, residual  [T, d] dtype; residual may be NULL
+ *   weight       [d] dtype
+ *   eps          finite, >= 0 (a row of zeros with eps 0 gives NaN)
+ *   h            [T, d] dtype or NULL; may be x or residual
+ *   y            [T, d] dtype or NULL; may be x or residual, not h
+ *   y8, y_scale  y in 8 bits (layout above), both or neither NULL
+ *   rstd         [T] float or NULL, what the backward takes
+ * d <= MOE_NORM_MAX_WIDTH (MOE_ERR_UNSUPPORTED past it).  T == 0: no-op.  A row that holds a value
+ * that is not finite gives NaN (or, where h rstd weight is one, zeros) in that row alone. */
+moe_status moe_rms_norm(int32_t num_tokens, int32_t d_model, int32_t dtype, const void *x, const void *residual,
+                        const void *weight, float eps, void *h, void *y, uint8_t *y8, uint8_t *y_scale, float *rstd,
+                        hipStream_t stream);
+
+/* Its gradients, with g = dy weight and xhat = h rstd (rounding to 8 bits passed through):
+ *   dx = dh + rstd (g - xhat mean(g xhat)): the gradient of x and of residual
+ *   dweight = sum over the tokens of dy xhat
+ *   dy, h    [T, d] dtype (the gradient of y; the forward's h, or x without a residual)
+ *   rstd     [T] float, the forward's
+ *   dh       [T, d] dtype or NULL: the gradient that reaches h on the residual stream
+ *   dx       [T, d] dtype, written; may be dy, h or dh
+ *   dweight  [d] float, written (zeros when T == 0)
+ *   ws       at least moe_rms_norm_backward_workspace_size(T, d) bytes (0: invalid sizes)
+ * Float sums in fixed orders (bit-reproducible). */
+size_t moe_rms_norm_backward_workspace_size(int32_t num_tokens, int32_t d_model);
+moe_status moe_rms_norm_backward(int32_t num_tokens, int32_t d_model, int32_t dtype, const void *dy, const void *h,
+                                 const void *weight, const float *rstd, const void *dh, void *dx, float *dweight,
+                                 void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* Grouped products of rows and weights in 8 bits, beside moe_grouped_down and
+ * moe_grouped_swiglu_gemm.  For every group g and row r in [group_offsets[g], group_offsets[g+1]):
+ *   moe_grouped_linear_fp8:       y_rows[r] = W[g] a_r
+ *   moe_grouped_swiglu_gemm_fp8:  y_rows[r] = W_d[g] q(silu(W_g[g] a_r) * (W_u[g] a_r))
+ * in float sums, y_rows bf16 (rounded once); q is the rounding to 8 bits of
+ * moe_quantize_rows_fp8, formed from the float values.  a_r = row r of x8, or, with row_index, its
+ * row row_index[r] (an index outside [0, x_row_count): a row of zeros).  One group of all rows is
+ * a dense product.
+ *   num_groups, rows_max, group_rows_max  as for moe_grouped_swiglu_gemm; rows_max <= INT32_MAX
+ *   x8, x_scale     rows in 8 bits: rows_max of them, or x_row_count, which must be below 2 GiB
+ *   group_offsets   [G+1] int32 DEVICE array, non-decreasing within [0, rows_max] (entries
+ *                   outside count as its ends)
+ *   w8, w_scale     from moe_quantize_weights_fp8
+ *   y_rows          [rows_max, n_out] bf16, written for rows inside a group, others left as they are
+ *   ws              at least the bytes of the helper beside (0: invalid arguments)
+ * Any n_out, d, f, K >= 1.  A NaN in a row makes that row NaN, one in a weight that output column.  The
+ * matrix instruction drops, of 16 products at a time, what lies some 2^-14 below the
+ * largest: about 1.5e-5 of a result's size, a hundredth of its bf16 rounding.  Only kernel
+ * launches on `stream`; every sum in a fixed order (bit-reproducible). */
+size_t moe_grouped_linear_fp8_workspace_size(int32_t num_groups, int64_t rows_max, int32_t group_rows_max,
+                                             int32_t n_out, int32_t k);
+moe_status moe_grouped_linear_fp8(int32_t num_groups, int64_t rows_max, int32_t group_rows_max, int32_t n_out, int32_t k,
+                                  const uint8_t *x8, const uint8_t *x_scale, const int32_t *row_index,
+                                  int64_t x_row_count, const int32_t *group_offsets, const uint8_t *w8,
+                                  const uint8_t *w_scale, void *y_rows, void *ws, size_t ws_bytes, hipStream_t stream);
+size_t moe_grouped_swiglu_gemm_fp8_workspace_size(int32_t num_groups, int64_t rows_max, int32_t group_rows_max,
+                                                  int32_t d_model, int32_t d_ff);
+moe_status moe_grouped_swiglu_gemm_fp8(int32_t num_groups, int64_t rows_max, int32_t group_rows_max, int32_t d_model,
+                                       int32_t d_ff, const uint8_t *x8, const uint8_t *x_scale,
+                                       const int32_t *row_index, int64_t x_row_count, const int32_t *group_offsets,
+                                       const uint8_t *w_gate_up8, const uint8_t *w_gate_up_scale,
+                                       const uint8_t *w_down8, const uint8_t *w_down_scale, void *y_rows, void *ws,
+                                       size_t ws_bytes, hipStream_t stream);
+
+/* A matrix of moe_quantize_weights_fp8, and a layer's (swiglu 1 for the gate_up ones; the shared
+ * expert's are one group of width d_ff_shared, NULL when that is 0). */
+typedef struct moe_fp8_matrix {
+  const uint8_t *codes, *scale;
+} moe_fp8_matrix;
+typedef struct moe_weights_fp8 {
+  const void *w_router; /* [E, d] bf16 */
+  moe_fp8_matrix gate_up, down, shared_gate_up, shared_down;
+} moe_weights_fp8;
+
+/* moe_forward with the experts (and the shared expert) in 8 bits: routing, dispatch and combine as
+ * there, in bf16 and float, the FFNs as in moe_grouped_swiglu_gemm_fp8.  bf16 layers.
+ *   x            [T, d] bf16, what the router reads
+ *   x8, x_scale  x in 8 bits (moe_rms_norm writes both), or both NULL: quantised here from x
+ *   ws           at least moe_forward_fp8_workspace_size(desc) bytes
+ * Other arguments, results and errors as for moe_forward. */
+size_t moe_forward_fp8_workspace_size(const moe_desc *desc);
+moe_status moe_forward_fp8(const moe_desc *desc, const moe_weights_fp8 *weights, const void *x, const uint8_t *x8,
+                           const uint8_t *x_scale, const float *logit_offset, void *out, moe_routing *routing, void *ws,
+                           size_t ws_bytes, hipStream_t stream);
 
 /* Bytes of the tile-major copy of num_experts experts' gate_up (which = 0) or down
  * (which = 1) weights for desc's shapes: per expert, ceil(f / 128) gate_up tiles (128 gate

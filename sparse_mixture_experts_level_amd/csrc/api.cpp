@@ -168,7 +168,8 @@ size_t align_up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 // Workspace layout of moe_forward; every region starts on a 256-byte boundary.
 struct Layout {
   size_t logits, ids, gates, counts, offsets, slot, row_token, spare, assigned, hist, x_packed, hidden, hidden_tail,
-      y_perm, sh_x_packed, sh_hidden, sh_hidden_tail, sh_out, sh_offsets, router_part, down_split, total;
+      y_perm, sh_x_packed, sh_hidden, sh_hidden_tail, sh_out, sh_offsets, router_part, down_split, x8, x_scale, ffn8,
+      total;
 };
 
 // Whether copying the x rows into the packed tile layout pays in the large-tile regime: each
@@ -198,7 +199,10 @@ bool shared_packable(const moe_desc &D) {
 
 bool rerouting(const moe_desc &D) { return D.overflow == MOE_OVERFLOW_REROUTE && D.capacity != MOE_NO_CAPACITY; }
 
-Layout layout(const moe_desc &D) {
+size_t swiglu_fp8_ws_bytes(int32_t G, int64_t rows_max, int32_t group_rows_max, int32_t d, int32_t f);
+
+// fp8: of moe_forward_fp8, whose FFNs keep x (unless it is given so) and H in 8 bits.
+Layout layout(const moe_desc &D, bool fp8 = false) {
   Layout L{};
   const size_t T = D.num_tokens, E = D.num_experts, k = D.top_k, d = D.d_model, f = D.d_ff, fs = D.d_ff_shared;
   const size_t R = (size_t)max_rows(D), s = elem_bytes(D.dtype);
@@ -220,6 +224,19 @@ Layout layout(const moe_desc &D) {
   L.assigned = take(D.overflow == MOE_OVERFLOW_REROUTE ? T * k * 4 : 0);
   L.hist = take(std::max(moe::dispatch_workspace_bytes((int)T, (int)k, (int)E, D.overflow == MOE_OVERFLOW_REROUTE),
                          moe::aux_loss_workspace_bytes((int)T, (int)E)));
+  if (fp8) {
+    L.x8 = take(T * moe::fp8_row_bytes((int)d));
+    L.x_scale = take(T * moe::fp8_scale_bytes((int)d));
+    // the routed experts are done with theirs when the shared one begins
+    L.ffn8 = take(std::max(R ? swiglu_fp8_ws_bytes((int)E, (int64_t)R, std::max(1, group_rows_bound(D)), (int)d, (int)f) : 0,
+                           fs && T ? swiglu_fp8_ws_bytes(1, (int64_t)T, (int)T, (int)d, (int)fs) : 0));
+    L.y_perm = take(R * d * s);
+    L.sh_out = take(fs ? T * d * s : 0);
+    L.sh_offsets = take(fs ? 2 * 4 : 0);
+    L.router_part = take(moe::router_partials_bytes((int)T, (int)d, (int)E));
+    L.total = o;
+    return L;
+  }
   // packed tile layouts of the gathered x rows and of H when a group can reach the
   // large-tile regime (any expert range holds all of a group's rows)
   const bool pack = packable(D);
@@ -663,26 +680,122 @@ moe_status moe_router_aux_loss(const moe_desc *desc, const float *logits, const 
 
 namespace {
 
+// ---- products in 8 bits
+
+moe_status check_dtype(int32_t dtype) {
+  if (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16) return fail(MOE_ERR_UNSUPPORTED, "dtype %d", (int)dtype);
+  return MOE_OK;
+}
+
+moe_status check_fp8_pair(const uint8_t *codes, const uint8_t *scale, const char *codes_name, const char *scale_name) {
+  if (!codes && !scale) return MOE_OK;
+  if (!codes || !scale) return fail(MOE_ERR_INVALID, "%s and %s: give both or neither", codes_name, scale_name);
+  MOE_TRY(check_ptr(codes, codes_name));
+  return check_ptr(scale, scale_name);
+}
+
+moe_status check_matrix(const moe_fp8_matrix &m, const char *name) {
+  if (!m.codes || !m.scale) return fail(MOE_ERR_INVALID, "%s is NULL", name);
+  return check_fp8_pair(m.codes, m.scale, name, name);
+}
+
+// Sizes of a matrix in 8 bits: one group's codes are addressed through 32-bit buffer offsets.
+moe_status check_fp8_shape(int32_t G, int32_t n_out, int32_t k, bool swiglu) {
+  if (G < 1 || G > MOE_MAX_EXPERTS) return fail(MOE_ERR_INVALID, "num_groups %d outside [1, %d]", G, MOE_MAX_EXPERTS);
+  if (n_out < 1 || k < 1) return fail(MOE_ERR_INVALID, "n_out and k must be >= 1");
+  // (the first two keep the third's product and the kernels' 32-bit counts of columns in range)
+  if (n_out >= (1 << 24) || k >= (1 << 24) || moe::fp8_weights_bytes(n_out, k, swiglu) >= ((int64_t)1 << 31))
+    return fail(MOE_ERR_UNSUPPORTED, "one group's weights in 8 bits must be smaller than 2 GiB");
+  return MOE_OK;
+}
+
+moe_status check_fp8_rows(int64_t rows_max, int32_t group_rows_max) {
+  if (rows_max < 0 || rows_max > INT32_MAX)
+    return fail(MOE_ERR_INVALID, "rows_max %lld outside [0, 2^31)", (long long)rows_max);
+  if (group_rows_max < 1) return fail(MOE_ERR_INVALID, "group_rows_max %d must be >= 1", group_rows_max);
+  return MOE_OK;
+}
+
+moe_status check_fp8_gather(int64_t x_rows, int32_t k) {
+  if (x_rows < 0 || x_rows > INT32_MAX) return fail(MOE_ERR_INVALID, "x_row_count %lld outside [0, 2^31)", (long long)x_rows);
+  if (x_rows * moe::fp8_row_bytes(k) >= ((int64_t)1 << 31))
+    return fail(MOE_ERR_UNSUPPORTED, "x8 must be smaller than 2 GiB (32-bit row gather offsets)");
+  return MOE_OK;
+}
+
+// Workspace of the FFN in 8 bits: H's codes, then its scales.
+size_t swiglu_fp8_ws_bytes(int32_t, int64_t rows_max, int32_t, int32_t, int32_t f) {
+  return align_up((size_t)rows_max * moe::fp8_row_bytes(f)) + align_up((size_t)rows_max * moe::fp8_scale_bytes(f));
+}
+
+moe::Fp8GemmArgs fp8_args(int32_t G, int64_t rows_max, int32_t group_rows_max, int32_t n_out, int32_t k, const uint8_t *x8,
+                          const uint8_t *x_scale, const int32_t *row_index, int64_t x_rows, const int32_t *offsets,
+                          const uint8_t *w8, const uint8_t *w_scale) {
+  moe::Fp8GemmArgs a{};
+  a.x8 = x8;
+  a.x_scale = x_scale;
+  a.row_index = row_index;
+  a.offsets = offsets;
+  a.w8 = w8;
+  a.w_scale = w_scale;
+  a.num_groups = G;
+  a.rows_max = (int)rows_max;
+  a.group_rows_max = group_rows_max;
+  a.x_rows = (int)x_rows;
+  a.n_out = n_out;
+  a.K = k;
+  return a;
+}
+
+// The FFN in 8 bits (arguments checked).
+moe_status run_swiglu_fp8(int32_t G, int64_t rows_max, int32_t group_rows_max, int32_t d, int32_t f, const uint8_t *x8,
+                          const uint8_t *x_scale, const int32_t *row_index, int64_t x_rows, const int32_t *offsets,
+                          const moe_fp8_matrix &gate_up, const moe_fp8_matrix &down, void *y, void *ws,
+                          hipStream_t stream) {
+  uint8_t *h8 = at<uint8_t>(ws, 0), *h_scale = at<uint8_t>(ws, align_up((size_t)rows_max * moe::fp8_row_bytes(f)));
+  moe::Fp8GemmArgs a = fp8_args(G, rows_max, group_rows_max, f, d, x8, x_scale, row_index, x_rows, offsets,
+                                gate_up.codes, gate_up.scale);
+  a.h8 = h8;
+  a.h_scale = h_scale;
+  MOE_TRY_HIP(moe::launch_fp8_gemm(a, stream), "gate_up in 8 bits");
+  a = fp8_args(G, rows_max, group_rows_max, d, f, h8, h_scale, nullptr, rows_max, offsets, down.codes, down.scale);
+  a.y = static_cast<uint16_t *>(y);
+  return hip_status(moe::launch_fp8_gemm(a, stream), "down in 8 bits");
+}
+
 // The layer for experts [e_begin, e_end) of the routing: routing, capacity and dispatch
 // over all experts (so slots are those of the whole layer), the FFN of the range's
 // experts with its weights (index 0 = expert e_begin), and the combine of their
-// contributions, plus the shared expert when add_shared.
+// contributions, plus the shared expert when add_shared.  With `fp8` the experts' weights are
+// those, in 8 bits, and `weights` holds the router's alone.
+struct Fp8Layer {
+  const moe_weights_fp8 *weights;
+  const uint8_t *x8, *x_scale;
+};
 moe_status forward_range(const moe_desc &D, const moe_weights *weights, const void *x, const float *logit_offset,
                          void *out, moe_routing *routing, void *ws, size_t ws_bytes, hipStream_t stream,
-                         int32_t e_begin, int32_t e_end, bool add_shared, StageMarks *marks = nullptr) {
+                         int32_t e_begin, int32_t e_end, bool add_shared, StageMarks *marks = nullptr,
+                         const Fp8Layer *fp8 = nullptr) {
   if (!weights) return fail(MOE_ERR_INVALID, "weights is NULL");
   if (D.num_tokens == 0) return ok();
   MOE_TRY(check_ptr(x, "x"));
   MOE_TRY(check_ptr(out, "out"));
   MOE_TRY(check_ptr(weights->w_router, "w_router"));
   const bool any_local = e_end > e_begin;
-  if (any_local) {
+  if (fp8) {
+    MOE_TRY(check_matrix(fp8->weights->gate_up, "gate_up"));
+    MOE_TRY(check_matrix(fp8->weights->down, "down"));
+    MOE_TRY(check_fp8_pair(fp8->x8, fp8->x_scale, "x8", "x_scale"));
+  } else if (any_local) {
     MOE_TRY(check_ptr(weights->w_gate_up, "w_gate_up"));
     MOE_TRY(check_ptr(weights->w_down, "w_down"));
     MOE_TRY(check_tiled(*weights, D.dtype));
   }
   MOE_TRY(check_opt_ptr(logit_offset, "logit_offset"));
-  if (D.d_ff_shared > 0 && add_shared) {
+  if (D.d_ff_shared > 0 && fp8) {
+    MOE_TRY(check_matrix(fp8->weights->shared_gate_up, "shared_gate_up"));
+    MOE_TRY(check_matrix(fp8->weights->shared_down, "shared_down"));
+  } else if (D.d_ff_shared > 0 && add_shared) {
     MOE_TRY(check_ptr(weights->w_shared_gate_up, "w_shared_gate_up"));
     MOE_TRY(check_ptr(weights->w_shared_down, "w_shared_down"));
     MOE_TRY(check_shared_tiled(*weights, D.dtype));
@@ -699,9 +812,10 @@ moe_status forward_range(const moe_desc &D, const moe_weights *weights, const vo
     MOE_TRY(check_opt_ptr(R.row_token, "routing.row_token"));
     MOE_TRY(check_opt_ptr(R.assigned_ids, "routing.assigned_ids"));
   }
-  const Layout L = layout(D);
+  const Layout L = layout(D, fp8 != nullptr);
   if (!ws || ws_bytes < L.total)
-    return fail(MOE_ERR_WORKSPACE, "moe_forward needs %zu workspace bytes, got %zu", L.total, ws ? ws_bytes : (size_t)0);
+    return fail(MOE_ERR_WORKSPACE, "%s needs %zu workspace bytes, got %zu", fp8 ? "moe_forward_fp8" : "moe_forward",
+                L.total, ws ? ws_bytes : (size_t)0);
   MOE_TRY(check_ptr(ws, "ws"));
 
   float *logits = R.logits ? R.logits : at<float>(ws, L.logits);
@@ -752,7 +866,21 @@ moe_status forward_range(const moe_desc &D, const moe_weights *weights, const vo
                   "assigned ids");
   }
   mark_end(marks, MOE_STAGE_DISPATCH);
-  if (rmax > 0 && any_local) {
+  const uint8_t *x8 = nullptr, *x_scale = nullptr;
+  if (fp8) {
+    x8 = fp8->x8;
+    x_scale = fp8->x_scale;
+    if (!x8) {
+      MOE_TRY_HIP(moe::launch_quantize_rows(x, false, T, d, at<uint8_t>(ws, L.x8), at<uint8_t>(ws, L.x_scale), stream),
+                  "x in 8 bits");
+      x8 = at<uint8_t>(ws, L.x8);
+      x_scale = at<uint8_t>(ws, L.x_scale);
+    }
+  }
+  if (fp8 && rmax > 0) {
+    MOE_TRY(run_swiglu_fp8(E, rmax, std::max(1, group_rows_bound(D)), d, f, x8, x_scale, row_token, T, offsets,
+                           fp8->weights->gate_up, fp8->weights->down, y_perm, at<void>(ws, L.ffn8), stream));
+  } else if (rmax > 0 && any_local) {
     // the gate_up projection gathers each expert's token rows from x through row_token,
     // so the permuted copy of x is never materialised; a range of experts is the slice
     // [e_begin, e_end] of the offsets (rows stay in the whole layer's row space)
@@ -768,7 +896,11 @@ moe_status forward_range(const moe_desc &D, const moe_weights *weights, const vo
     int32_t *sh_off = at<int32_t>(ws, L.sh_offsets);
     MOE_TRY_HIP(moe::launch_fill_i32(sh_off, 2, 0, T, stream), "shared offsets");
     const bool sp = shared_packable(D);
-    MOE_TRY(run_grouped_ffn(1, T, T, d, fs, D.dtype, x, sh_off, weights->w_shared_gate_up, weights->w_shared_down,
+    if (fp8)
+      MOE_TRY(run_swiglu_fp8(1, T, T, d, fs, x8, x_scale, nullptr, T, sh_off, fp8->weights->shared_gate_up,
+                             fp8->weights->shared_down, at<void>(ws, L.sh_out), at<void>(ws, L.ffn8), stream));
+    else
+      MOE_TRY(run_grouped_ffn(1, T, T, d, fs, D.dtype, x, sh_off, weights->w_shared_gate_up, weights->w_shared_down,
                             at<void>(ws, L.sh_out), at<void>(ws, L.sh_hidden), stream, nullptr, 0, nullptr,
                             sp && pack_rows_wins(fs) ? at<void>(ws, L.sh_x_packed) : nullptr,
                             sp ? at<void>(ws, L.sh_hidden_tail) : nullptr,
@@ -1498,6 +1630,262 @@ moe_status moe_adamw_read_states(const moe_adamw_tensor *tensors, int32_t num_te
   return ok();
 } catch (const std::exception &e) {
   return fail(MOE_ERR_INVALID, "moe_adamw_read_states: %s", e.what());
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------- 8-bit floating point, norm, 8-bit experts
+
+namespace {
+
+// Whether [a, a + n) and [b, b + n) overlap without being the same.
+bool shifted(const void *a, const void *b, size_t n) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return a && b && p != q && p < q + n && q < p + n;
+}
+
+moe_status check_norm_shape(int32_t T, int32_t d, int32_t dtype) {
+  if (T < 0) return fail(MOE_ERR_INVALID, "num_tokens %d < 0", T);
+  if (d < 1) return fail(MOE_ERR_INVALID, "d_model must be >= 1");
+  if (d > MOE_NORM_MAX_WIDTH) return fail(MOE_ERR_UNSUPPORTED, "d_model %d: the norm takes at most %d", d, MOE_NORM_MAX_WIDTH);
+  return check_dtype(dtype);
+}
+
+// moe_forward_fp8's descriptor: bf16, matrices below 2 GiB.
+moe_status check_fp8_desc(const moe_desc *desc) {
+  MOE_TRY(check_desc(desc));
+  const moe_desc &D = *desc;
+  if (D.dtype != MOE_DTYPE_BF16) return fail(MOE_ERR_UNSUPPORTED, "experts in 8 bits: bf16 layers only");
+  MOE_TRY(check_fp8_shape(D.num_experts, D.d_ff, D.d_model, true));
+  MOE_TRY(check_fp8_shape(D.num_experts, D.d_model, D.d_ff, false));
+  if (D.d_ff_shared) {
+    MOE_TRY(check_fp8_shape(1, D.d_ff_shared, D.d_model, true));
+    MOE_TRY(check_fp8_shape(1, D.d_model, D.d_ff_shared, false));
+  }
+  return check_fp8_gather(D.num_tokens, D.d_model);
+}
+
+}  // namespace
+
+static_assert(MOE_NORM_MAX_WIDTH == moe::kNormMaxWidth, "the width of the norm");
+
+extern "C" {
+
+int32_t moe_fp8_row_bytes(int32_t k) { return k < 1 || k > INT32_MAX - 127 ? 0 : (k + 127) / 128 * 128; }
+int32_t moe_fp8_scale_bytes(int32_t k) { return k < 1 || k > INT32_MAX - 127 ? 0 : ((k + 127) / 128 + 3) / 4 * 4; }
+
+static moe_status check_fp8_convert(int64_t rows, int32_t k, int32_t dtype) {
+  MOE_TRY(check_dtype(dtype));
+  if (rows < 0 || rows > INT32_MAX) return fail(MOE_ERR_INVALID, "rows %lld outside [0, 2^31)", (long long)rows);
+  if (k < 1 || k >= (1 << 24)) return fail(MOE_ERR_INVALID, "k %d outside [1, 2^24)", k);
+  return MOE_OK;
+}
+
+moe_status moe_quantize_rows_fp8(int64_t rows, int32_t k, int32_t dtype, const void *x, uint8_t *codes, uint8_t *scale,
+                                 hipStream_t stream) {
+  MOE_TRY(check_fp8_convert(rows, k, dtype));
+  if (rows == 0) return ok();
+  MOE_TRY(check_ptr(x, "x"));
+  MOE_TRY(check_ptr(codes, "codes"));
+  MOE_TRY(check_ptr(scale, "scale"));
+  MOE_TRY_HIP(moe::launch_quantize_rows(x, dtype == MOE_DTYPE_F32, rows, k, codes, scale, stream), "rows to 8 bits");
+  return ok();
+}
+
+moe_status moe_dequantize_rows_fp8(int64_t rows, int32_t k, int32_t dtype, const uint8_t *codes, const uint8_t *scale,
+                                   void *out, hipStream_t stream) {
+  MOE_TRY(check_fp8_convert(rows, k, dtype));
+  if (rows == 0) return ok();
+  MOE_TRY(check_ptr(codes, "codes"));
+  MOE_TRY(check_ptr(scale, "scale"));
+  MOE_TRY(check_ptr(out, "out"));
+  MOE_TRY_HIP(moe::launch_dequantize_rows(codes, scale, rows, k, out, dtype == MOE_DTYPE_F32, stream),
+              "rows from 8 bits");
+  return ok();
+}
+
+size_t moe_fp8_weights_bytes(int32_t num_groups, int32_t n_out, int32_t k, int32_t swiglu) {
+  if (check_fp8_shape(num_groups, n_out, k, swiglu != 0) != MOE_OK) return 0;
+  return (size_t)num_groups * (size_t)moe::fp8_weights_bytes(n_out, k, swiglu != 0);
+}
+
+size_t moe_fp8_weight_scales_bytes(int32_t num_groups, int32_t n_out, int32_t k, int32_t swiglu) {
+  if (check_fp8_shape(num_groups, n_out, k, swiglu != 0) != MOE_OK) return 0;
+  return (size_t)num_groups * (size_t)moe::fp8_weight_scales_bytes(n_out, k, swiglu != 0);
+}
+
+moe_status moe_quantize_weights_fp8(int32_t num_groups, int32_t n_out, int32_t k, int32_t swiglu, int32_t dtype,
+                                    const void *w, uint8_t *codes, uint8_t *scale, hipStream_t stream) {
+  MOE_TRY(check_dtype(dtype));
+  MOE_TRY(check_fp8_shape(num_groups, n_out, k, swiglu != 0));
+  if (moe::fp8_blocks(n_out) * (swiglu ? 2 : 1) > 65535) return fail(MOE_ERR_UNSUPPORTED, "n_out %d: too many rows", n_out);
+  MOE_TRY(check_ptr(w, "w"));
+  MOE_TRY(check_ptr(codes, "codes"));
+  MOE_TRY(check_ptr(scale, "scale"));
+  MOE_TRY_HIP(moe::launch_quantize_weights(w, dtype == MOE_DTYPE_F32, num_groups, n_out, k, swiglu != 0, codes, scale,
+                                           stream),
+              "weights to 8 bits");
+  return ok();
+}
+
+moe_status moe_rms_norm(int32_t num_tokens, int32_t d_model, int32_t dtype, const void *x, const void *residual,
+                        const void *weight, float eps, void *h, void *y, uint8_t *y8, uint8_t *y_scale, float *rstd,
+                        hipStream_t stream) {
+  MOE_TRY(check_norm_shape(num_tokens, d_model, dtype));
+  if (!(eps >= 0.0f) || !(eps <= FLT_MAX)) return fail(MOE_ERR_INVALID, "eps must be finite and >= 0");
+  if (num_tokens == 0) return ok();
+  MOE_TRY(check_ptr(x, "x"));
+  MOE_TRY(check_opt_ptr(residual, "residual"));
+  MOE_TRY(check_ptr(weight, "weight"));
+  MOE_TRY(check_opt_ptr(h, "h"));
+  MOE_TRY(check_opt_ptr(y, "y"));
+  MOE_TRY(check_fp8_pair(y8, y_scale, "y8", "y_scale"));
+  MOE_TRY(check_opt_ptr(rstd, "rstd"));
+  const size_t n = (size_t)num_tokens * d_model * elem_bytes(dtype);
+  if (shifted(h, x, n) || shifted(h, residual, n) || shifted(y, x, n) || shifted(y, residual, n))
+    return fail(MOE_ERR_INVALID, "h and y may be x or residual, but not overlap them otherwise");
+  if (h && (h == y || shifted(h, y, n))) return fail(MOE_ERR_INVALID, "h and y overlap");
+  moe::NormCall c{};
+  c.x = x;
+  c.residual = residual;
+  c.weight = weight;
+  c.h = h;
+  c.y = y;
+  c.y8 = y8;
+  c.y_scale = y_scale;
+  c.rstd = rstd;
+  c.T = num_tokens;
+  c.d = d_model;
+  c.eps = eps;
+  c.f32 = dtype == MOE_DTYPE_F32;
+  MOE_TRY_HIP(moe::launch_rms_norm(c, stream), "norm");
+  return ok();
+}
+
+size_t moe_rms_norm_backward_workspace_size(int32_t num_tokens, int32_t d_model) {
+  if (check_norm_shape(num_tokens, d_model, MOE_DTYPE_F32) != MOE_OK) return 0;
+  return std::max<size_t>(align_up(moe::rms_norm_backward_workspace_bytes(num_tokens, d_model)), kAlign);
+}
+
+moe_status moe_rms_norm_backward(int32_t num_tokens, int32_t d_model, int32_t dtype, const void *dy, const void *h,
+                                 const void *weight, const float *rstd, const void *dh, void *dx, float *dweight,
+                                 void *ws, size_t ws_bytes, hipStream_t stream) {
+  MOE_TRY(check_norm_shape(num_tokens, d_model, dtype));
+  MOE_TRY(check_ptr(dweight, "dweight"));
+  if (num_tokens > 0) {
+    MOE_TRY(check_ptr(dy, "dy"));
+    MOE_TRY(check_ptr(h, "h"));
+    MOE_TRY(check_ptr(weight, "weight"));
+    MOE_TRY(check_ptr(rstd, "rstd"));
+    MOE_TRY(check_opt_ptr(dh, "dh"));
+    MOE_TRY(check_ptr(dx, "dx"));
+    const size_t n = (size_t)num_tokens * d_model * elem_bytes(dtype);
+    if (shifted(dx, dy, n) || shifted(dx, h, n) || shifted(dx, dh, n))
+      return fail(MOE_ERR_INVALID, "dx may be dy, h or dh, but not overlap them otherwise");
+  }
+  const size_t need = moe::rms_norm_backward_workspace_bytes(num_tokens, d_model);
+  if (!ws || ws_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "the norm's backward needs %zu workspace bytes, got %zu", need, ws ? ws_bytes : (size_t)0);
+  MOE_TRY(check_ptr(ws, "ws"));
+  moe::NormBwdCall c{};
+  c.dy = dy;
+  c.h = h;
+  c.weight = weight;
+  c.dh = dh;
+  c.rstd = rstd;
+  c.dx = dx;
+  c.dweight = dweight;
+  c.T = num_tokens;
+  c.d = d_model;
+  c.f32 = dtype == MOE_DTYPE_F32;
+  MOE_TRY_HIP(moe::launch_rms_norm_backward(c, ws, stream), "norm backward");
+  return ok();
+}
+
+size_t moe_grouped_linear_fp8_workspace_size(int32_t num_groups, int64_t rows_max, int32_t group_rows_max,
+                                             int32_t n_out, int32_t k) {
+  if (check_fp8_shape(num_groups, n_out, k, false) != MOE_OK || check_fp8_rows(rows_max, group_rows_max) != MOE_OK) return 0;
+  return kAlign;
+}
+
+moe_status moe_grouped_linear_fp8(int32_t num_groups, int64_t rows_max, int32_t group_rows_max, int32_t n_out, int32_t k,
+                                  const uint8_t *x8, const uint8_t *x_scale, const int32_t *row_index,
+                                  int64_t x_row_count, const int32_t *group_offsets, const uint8_t *w8,
+                                  const uint8_t *w_scale, void *y_rows, void *ws, size_t ws_bytes, hipStream_t stream) {
+  MOE_TRY(check_fp8_shape(num_groups, n_out, k, false));
+  MOE_TRY(check_fp8_rows(rows_max, group_rows_max));
+  if (row_index) MOE_TRY(check_fp8_gather(x_row_count, k));
+  if (rows_max == 0) return ok();
+  MOE_TRY(check_ptr(x8, "x8"));
+  MOE_TRY(check_ptr(x_scale, "x_scale"));
+  MOE_TRY(check_opt_ptr(row_index, "row_index"));
+  MOE_TRY(check_ptr(group_offsets, "group_offsets"));
+  MOE_TRY(check_ptr(w8, "w8"));
+  MOE_TRY(check_ptr(w_scale, "w_scale"));
+  MOE_TRY(check_ptr(y_rows, "y_rows"));
+  const size_t need = moe_grouped_linear_fp8_workspace_size(num_groups, rows_max, group_rows_max, n_out, k);
+  if (!ws || ws_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "moe_grouped_linear_fp8 needs %zu workspace bytes, got %zu", need, ws ? ws_bytes : (size_t)0);
+  MOE_TRY(check_ptr(ws, "ws"));
+  moe::Fp8GemmArgs a = fp8_args(num_groups, rows_max, group_rows_max, n_out, k, x8, x_scale, row_index,
+                                row_index ? x_row_count : rows_max, group_offsets, w8, w_scale);
+  a.y = static_cast<uint16_t *>(y_rows);
+  MOE_TRY_HIP(moe::launch_fp8_gemm(a, stream), "grouped product in 8 bits");
+  return ok();
+}
+
+size_t moe_grouped_swiglu_gemm_fp8_workspace_size(int32_t num_groups, int64_t rows_max, int32_t group_rows_max,
+                                                  int32_t d_model, int32_t d_ff) {
+  if (check_fp8_shape(num_groups, d_ff, d_model, true) != MOE_OK || check_fp8_shape(num_groups, d_model, d_ff, false) != MOE_OK ||
+      check_fp8_rows(rows_max, group_rows_max) != MOE_OK)
+    return 0;
+  return std::max<size_t>(swiglu_fp8_ws_bytes(num_groups, rows_max, group_rows_max, d_model, d_ff), kAlign);
+}
+
+moe_status moe_grouped_swiglu_gemm_fp8(int32_t num_groups, int64_t rows_max, int32_t group_rows_max, int32_t d_model,
+                                       int32_t d_ff, const uint8_t *x8, const uint8_t *x_scale,
+                                       const int32_t *row_index, int64_t x_row_count, const int32_t *group_offsets,
+                                       const uint8_t *w_gate_up8, const uint8_t *w_gate_up_scale,
+                                       const uint8_t *w_down8, const uint8_t *w_down_scale, void *y_rows, void *ws,
+                                       size_t ws_bytes, hipStream_t stream) {
+  MOE_TRY(check_fp8_shape(num_groups, d_ff, d_model, true));
+  MOE_TRY(check_fp8_shape(num_groups, d_model, d_ff, false));
+  MOE_TRY(check_fp8_rows(rows_max, group_rows_max));
+  if (row_index) MOE_TRY(check_fp8_gather(x_row_count, d_model));
+  if (rows_max == 0) return ok();
+  MOE_TRY(check_ptr(x8, "x8"));
+  MOE_TRY(check_ptr(x_scale, "x_scale"));
+  MOE_TRY(check_opt_ptr(row_index, "row_index"));
+  MOE_TRY(check_ptr(group_offsets, "group_offsets"));
+  const moe_fp8_matrix gate_up{w_gate_up8, w_gate_up_scale}, down{w_down8, w_down_scale};
+  MOE_TRY(check_matrix(gate_up, "w_gate_up8"));
+  MOE_TRY(check_matrix(down, "w_down8"));
+  MOE_TRY(check_ptr(y_rows, "y_rows"));
+  const size_t need = moe_grouped_swiglu_gemm_fp8_workspace_size(num_groups, rows_max, group_rows_max, d_model, d_ff);
+  if (!ws || ws_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "moe_grouped_swiglu_gemm_fp8 needs %zu workspace bytes, got %zu", need,
+                ws ? ws_bytes : (size_t)0);
+  MOE_TRY(check_ptr(ws, "ws"));
+  MOE_TRY(run_swiglu_fp8(num_groups, rows_max, group_rows_max, d_model, d_ff, x8, x_scale, row_index,
+                         row_index ? x_row_count : rows_max, group_offsets, gate_up, down, y_rows, ws, stream));
+  return ok();
+}
+
+size_t moe_forward_fp8_workspace_size(const moe_desc *desc) {
+  if (check_fp8_desc(desc) != MOE_OK) return 0;
+  return std::max<size_t>(layout(*desc, true).total, kAlign);
+}
+
+moe_status moe_forward_fp8(const moe_desc *desc, const moe_weights_fp8 *weights, const void *x, const uint8_t *x8,
+                           const uint8_t *x_scale, const float *logit_offset, void *out, moe_routing *routing, void *ws,
+                           size_t ws_bytes, hipStream_t stream) {
+  MOE_TRY(check_fp8_desc(desc));
+  if (!weights) return fail(MOE_ERR_INVALID, "weights is NULL");
+  moe_weights w{};
+  w.w_router = weights->w_router;
+  const Fp8Layer layer{weights, x8, x_scale};
+  return forward_range(*desc, &w, x, logit_offset, out, routing, ws, ws_bytes, stream, 0, desc->num_experts, true, nullptr,
+                       &layer);
 }
 
 }  // extern "C"

@@ -215,6 +215,58 @@ struct AdamScalars {
 hipError_t launch_adamw(const AdamTensor *t, int count, const AdamScalars &h, hipStream_t s);
 hipError_t launch_adamw_read(const AdamTensor *t, int count, float *const *m_out, float *const *v_out, hipStream_t s);
 
+// ---- 8-bit floating point with a scale for each block of 128 (quantize.hip, gemm_fp8.hip)
+// Blocks of 128 of k values; bytes of a row's codes and of its scales (layouts in fp8.hpp).
+inline constexpr int kFp8Block = 128;
+__host__ __device__ inline int fp8_blocks(int k) { return (k + kFp8Block - 1) / kFp8Block; }
+__host__ __device__ inline int fp8_row_bytes(int k) { return fp8_blocks(k) * kFp8Block; }
+__host__ __device__ inline int fp8_scale_bytes(int k) { return (fp8_blocks(k) + 3) / 4 * 4; }
+hipError_t launch_quantize_rows(const void *x, bool f32, int64_t rows, int K, uint8_t *codes, uint8_t *scale,
+                                hipStream_t s);
+hipError_t launch_dequantize_rows(const uint8_t *codes, const uint8_t *scale, int64_t rows, int K, void *out, bool f32,
+                                  hipStream_t s);
+// Bytes of one group's codes and scales.
+int64_t fp8_weights_bytes(int n_out, int K, bool swiglu);
+int64_t fp8_weight_scales_bytes(int n_out, int K, bool swiglu);
+hipError_t launch_quantize_weights(const void *w, bool f32, int G, int n_out, int K, bool swiglu, uint8_t *codes,
+                                   uint8_t *scale, hipStream_t s);
+// Grouped product of rows and weights in 8 bits: out bf16 [rows_max, n_out] in y, or, with h8, the
+// SwiGLU of the gate and up products in 8 bits again.  Offsets outside [0, rows_max] count as its
+// ends; a row index outside [0, x_rows) as a row of zeros.
+struct Fp8GemmArgs {
+  const uint8_t *x8, *x_scale;
+  const int32_t *row_index;  // or NULL: the rows stand in order
+  const int32_t *offsets;    // [num_groups + 1]
+  const uint8_t *w8, *w_scale;
+  uint16_t *y;
+  uint8_t *h8, *h_scale;
+  int num_groups, rows_max, group_rows_max, x_rows, n_out, K;
+};
+hipError_t launch_fp8_gemm(const Fp8GemmArgs &a, hipStream_t s);
+
+// ---- root-mean-square norm (norm.hip)
+struct NormCall {
+  const void *x, *residual, *weight;  // residual or NULL
+  void *h, *y;                        // each or NULL
+  uint8_t *y8, *y_scale;              // both or NULL
+  float *rstd;                        // or NULL
+  int T, d;
+  float eps;
+  bool f32;
+};
+hipError_t launch_rms_norm(const NormCall &c, hipStream_t s);
+struct NormBwdCall {
+  const void *dy, *h, *weight, *dh;  // dh or NULL
+  const float *rstd;
+  void *dx;
+  float *dweight;
+  int T, d;
+  bool f32;
+};
+size_t rms_norm_backward_workspace_bytes(int T, int d);
+hipError_t launch_rms_norm_backward(const NormBwdCall &c, void *ws, hipStream_t s);
+constexpr int kNormMaxWidth = 32768;  // values of a row
+
 // ---- small utilities (combine.hip)
 hipError_t launch_fill_i32(int32_t *p, int n, int32_t v0, int32_t step, hipStream_t s);
 

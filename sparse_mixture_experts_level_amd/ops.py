@@ -36,10 +36,16 @@ SYMBOLS = [
     "moe_check_topk_ids", "moe_debug_checks", "moe_forward_staged", "moe_forward_noalloc",
     "moe_backward_with_dlogits", "moe_balance_workspace_size", "moe_balance_loss", "moe_balance_loss_backward",
     "moe_grad_norm_workspace_size", "moe_grad_norm", "moe_adamw_check_tensors", "moe_adamw_step",
-    "moe_adamw_read_states",
+    "moe_adamw_read_states", "moe_fp8_row_bytes", "moe_fp8_scale_bytes", "moe_quantize_rows_fp8",
+    "moe_dequantize_rows_fp8", "moe_fp8_weights_bytes", "moe_fp8_weight_scales_bytes", "moe_quantize_weights_fp8",
+    "moe_rms_norm", "moe_rms_norm_backward_workspace_size", "moe_rms_norm_backward",
+    "moe_grouped_linear_fp8_workspace_size", "moe_grouped_linear_fp8", "moe_grouped_swiglu_gemm_fp8_workspace_size",
+    "moe_grouped_swiglu_gemm_fp8", "moe_forward_fp8_workspace_size", "moe_forward_fp8",
 ]
 MOE_MAX_SEQS = 65536
 MOE_ADAMW_BLOCK = 256
+MOE_FP8_BLOCK = 128
+MOE_NORM_MAX_WIDTH = 32768
 MOE_NOALLOC_WORKSPACE_BYTES = 128 << 20
 
 # moe_stage: the stages moe_forward_staged marks, in launch order
@@ -76,6 +82,15 @@ class MoeRouting(ctypes.Structure):
     _fields_ = [("logits", ctypes.c_void_p), ("topk_ids", ctypes.c_void_p), ("topk_gates", ctypes.c_void_p),
                 ("expert_counts", ctypes.c_void_p), ("expert_offsets", ctypes.c_void_p), ("slot", ctypes.c_void_p),
                 ("row_token", ctypes.c_void_p), ("assigned_ids", ctypes.c_void_p)]
+
+
+class MoeFp8Matrix(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+class MoeWeightsFp8(ctypes.Structure):
+    _fields_ = [("w_router", ctypes.c_void_p), ("gate_up", MoeFp8Matrix), ("down", MoeFp8Matrix),
+                ("shared_gate_up", MoeFp8Matrix), ("shared_down", MoeFp8Matrix)]
 
 
 class MoeGradView(ctypes.Structure):
@@ -179,6 +194,31 @@ def _load(path: str) -> ctypes.CDLL:
     L.moe_adamw_step.argtypes, L.moe_adamw_step.restype = [tp, i32, ctypes.POINTER(MoeAdamwHparams), vp], st
     L.moe_adamw_read_states.argtypes = [tp, i32, ctypes.POINTER(vp), ctypes.POINTER(vp), vp]
     L.moe_adamw_read_states.restype = st
+    L.moe_fp8_row_bytes.argtypes, L.moe_fp8_row_bytes.restype = [i32], i32
+    L.moe_fp8_scale_bytes.argtypes, L.moe_fp8_scale_bytes.restype = [i32], i32
+    L.moe_quantize_rows_fp8.argtypes, L.moe_quantize_rows_fp8.restype = [i64, i32, i32, vp, vp, vp, vp], st
+    L.moe_dequantize_rows_fp8.argtypes, L.moe_dequantize_rows_fp8.restype = [i64, i32, i32, vp, vp, vp, vp], st
+    L.moe_fp8_weights_bytes.argtypes, L.moe_fp8_weights_bytes.restype = [i32, i32, i32, i32], sz
+    L.moe_fp8_weight_scales_bytes.argtypes, L.moe_fp8_weight_scales_bytes.restype = [i32, i32, i32, i32], sz
+    L.moe_quantize_weights_fp8.argtypes = [i32, i32, i32, i32, i32, vp, vp, vp, vp]
+    L.moe_quantize_weights_fp8.restype = st
+    L.moe_rms_norm.argtypes, L.moe_rms_norm.restype = [i32, i32, i32, vp, vp, vp, f32, vp, vp, vp, vp, vp, vp], st
+    L.moe_rms_norm_backward_workspace_size.argtypes = [i32, i32]
+    L.moe_rms_norm_backward_workspace_size.restype = sz
+    L.moe_rms_norm_backward.argtypes = [i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.moe_rms_norm_backward.restype = st
+    L.moe_grouped_linear_fp8_workspace_size.argtypes = [i32, i64, i32, i32, i32]
+    L.moe_grouped_linear_fp8_workspace_size.restype = sz
+    L.moe_grouped_linear_fp8.argtypes = [i32, i64, i32, i32, i32, vp, vp, vp, i64, vp, vp, vp, vp, vp, sz, vp]
+    L.moe_grouped_linear_fp8.restype = st
+    L.moe_grouped_swiglu_gemm_fp8_workspace_size.argtypes = [i32, i64, i32, i32, i32]
+    L.moe_grouped_swiglu_gemm_fp8_workspace_size.restype = sz
+    L.moe_grouped_swiglu_gemm_fp8.argtypes = [i32, i64, i32, i32, i32, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.moe_grouped_swiglu_gemm_fp8.restype = st
+    L.moe_forward_fp8_workspace_size.argtypes, L.moe_forward_fp8_workspace_size.restype = [dp], sz
+    L.moe_forward_fp8.argtypes = [dp, ctypes.POINTER(MoeWeightsFp8), vp, vp, vp, vp, vp, ctypes.POINTER(MoeRouting), vp,
+                                  sz, vp]
+    L.moe_forward_fp8.restype = st
     return L
 
 
@@ -781,18 +821,215 @@ class MoEAdamW:
         return m_out, v_out
 
 
+# ------------------------------------------------- 8-bit floating point, norm, 8-bit experts
+
+_FP = (torch.float32, torch.bfloat16)
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def moe_fp8_row_bytes(k: int) -> int:
+    return int(lib().moe_fp8_row_bytes(k))
+
+
+def moe_fp8_scale_bytes(k: int) -> int:
+    return int(lib().moe_fp8_scale_bytes(k))
+
+
+def _rows8(codes, scale, names, rows, k, dev):
+    """Pointers of rows in 8 bits: codes [rows, moe_fp8_row_bytes(k)], scale [rows, moe_fp8_scale_bytes(k)]."""
+    blocks = -(-k // MOE_FP8_BLOCK)
+    return (_tensor(codes, names[0], _CODES, (rows, blocks * MOE_FP8_BLOCK), dev),
+            _tensor(scale, names[1], torch.uint8, (rows, -(-blocks // 4) * 4), dev))
+
+
+def fp8_rows(rows: int, k: int, device="cuda"):
+    """New (codes, scale) for rows of k values in 8 bits."""
+    return (torch.empty((rows, moe_fp8_row_bytes(k)), dtype=torch.uint8, device=device),
+            torch.empty((rows, moe_fp8_scale_bytes(k)), dtype=torch.uint8, device=device))
+
+
+def moe_quantize_rows_fp8(x, codes, scale, stream=None) -> None:
+    rows, k = x.shape
+    dev = _device()
+    _check(lib().moe_quantize_rows_fp8(rows, k, dtype_code(x.dtype), _tensor(x, "x", _FP, None, dev),
+                                       *_rows8(codes, scale, ("codes", "scale"), rows, k, dev), _stream(stream)),
+           "moe_quantize_rows_fp8")
+
+
+def moe_dequantize_rows_fp8(codes, scale, out, stream=None) -> None:
+    rows, k = out.shape
+    dev = _device()
+    _check(lib().moe_dequantize_rows_fp8(rows, k, dtype_code(out.dtype),
+                                         *_rows8(codes, scale, ("codes", "scale"), rows, k, dev),
+                                         _tensor(out, "out", _FP, None, dev), _stream(stream)),
+           "moe_dequantize_rows_fp8")
+
+
+def moe_fp8_weights_bytes(num_groups: int, n_out: int, k: int, swiglu: bool) -> int:
+    return int(lib().moe_fp8_weights_bytes(int(num_groups), int(n_out), int(k), int(bool(swiglu))))
+
+
+def moe_fp8_weight_scales_bytes(num_groups: int, n_out: int, k: int, swiglu: bool) -> int:
+    return int(lib().moe_fp8_weight_scales_bytes(int(num_groups), int(n_out), int(k), int(bool(swiglu))))
+
+
+def moe_quantize_weights_fp8(num_groups, n_out, k, swiglu, w, codes, scale, stream=None) -> None:
+    """w [G, n_out, k], or with swiglu [G, 2 n_out, k] (gate rows, then up rows), float or bf16."""
+    dev = _device()
+    _check(lib().moe_quantize_weights_fp8(
+        int(num_groups), int(n_out), int(k), int(bool(swiglu)), dtype_code(w.dtype),
+        _tensor(w, "w", _FP, (num_groups, n_out * (2 if swiglu else 1), k), dev),
+        *_matrix8(codes, scale, "codes", num_groups, n_out, k, swiglu, dev), _stream(stream)), "moe_quantize_weights_fp8")
+
+
+def _matrix8(codes, scale, name, num_groups, n_out, k, swiglu, dev):
+    """Pointers of a matrix in 8 bits, whose tensors must have the sizes of its shape."""
+    halves, kb, nb = 2 if swiglu else 1, -(-k // MOE_FP8_BLOCK), -(-n_out // MOE_FP8_BLOCK)
+    return (_tensor(codes, name, torch.uint8, (num_groups * -(-n_out // 16) * halves * kb * 2048,), dev),
+            _tensor(scale, name + "'s scale", torch.uint8, (num_groups * nb * halves * (-(-kb // 4) * 4),), dev))
+
+
+def fp8_weights(w, swiglu=False, stream=None):
+    """(codes, scale) of w [G, n, k] in 8 bits, allocated here as flat uint8 tensors; swiglu: w is a gate_up matrix."""
+    g, n, k = w.shape
+    if swiglu and n % 2:
+        raise ValueError(f"a gate_up matrix has as many gate as up rows: got {n}")
+    n_out = n // 2 if swiglu else n
+    with _on(stream):
+        codes = torch.empty(moe_fp8_weights_bytes(g, n_out, k, swiglu), dtype=torch.uint8, device=w.device)
+        scale = torch.empty(moe_fp8_weight_scales_bytes(g, n_out, k, swiglu), dtype=torch.uint8, device=w.device)
+    moe_quantize_weights_fp8(g, n_out, k, swiglu, w, codes, scale, stream=stream)
+    return codes, scale
+
+
+def moe_rms_norm(x, weight, eps, residual=None, h=None, y=None, y8=None, y_scale=None, rstd=None, stream=None) -> None:
+    """h = x + residual, rstd [T] float, y = h rstd weight, also in 8 bits (y8, y_scale): what is given is written."""
+    T, d = x.shape
+    dev, dt, shape = _device(), x.dtype, x.shape
+    _check(lib().moe_rms_norm(
+        T, d, dtype_code(dt), _tensor(x, "x", _FP, None, dev), _tensor(residual, "residual", dt, shape, dev),
+        _tensor(weight, "weight", dt, (d,), dev), eps, _tensor(h, "h", dt, shape, dev), _tensor(y, "y", dt, shape, dev),
+        *_rows8(y8, y_scale, ("y8", "y_scale"), T, d, dev), _tensor(rstd, "rstd", torch.float32, (T,), dev),
+        _stream(stream)), "moe_rms_norm")
+
+
+def moe_rms_norm_backward_workspace_size(num_tokens: int, d_model: int) -> int:
+    return int(lib().moe_rms_norm_backward_workspace_size(int(num_tokens), int(d_model)))
+
+
+def moe_rms_norm_backward(dy, h, weight, rstd, dx, dweight, ws, dh=None, stream=None) -> None:
+    """dx (of x and of residual) and dweight [d] float from dy, the forward's h and rstd, and dh, the gradient that
+    reaches h itself."""
+    T, d = h.shape
+    dev, dt, shape = _device(), h.dtype, h.shape
+    _check(lib().moe_rms_norm_backward(
+        T, d, dtype_code(dt), _tensor(dy, "dy", dt, shape, dev), _tensor(h, "h", _FP, None, dev),
+        _tensor(weight, "weight", dt, (d,), dev), _tensor(rstd, "rstd", torch.float32, (T,), dev),
+        _tensor(dh, "dh", dt, shape, dev), _tensor(dx, "dx", dt, shape, dev),
+        _tensor(dweight, "dweight", torch.float32, (d,), dev), _tensor(ws, "ws", torch.uint8, None, dev),
+        0 if ws is None else ws.numel(), _stream(stream)), "moe_rms_norm_backward")
+
+
+def _fp8_operands(num_groups, rows_max, k, x8, x_scale, group_offsets, row_index, dev):
+    rows = int(rows_max) if row_index is None else x8.shape[0]
+    codes, scale = _rows8(x8, x_scale, ("x8", "x_scale"), rows, k, dev)
+    return (codes, scale, _tensor(row_index, "row_index", torch.int32, (int(rows_max),), dev), rows,
+            _tensor(group_offsets, "group_offsets", torch.int32, (num_groups + 1,), dev))
+
+
+def moe_grouped_linear_fp8_workspace_size(num_groups, rows_max, group_rows_max, n_out, k) -> int:
+    return int(lib().moe_grouped_linear_fp8_workspace_size(int(num_groups), int(rows_max), int(group_rows_max),
+                                                           int(n_out), int(k)))
+
+
+def moe_grouped_linear_fp8(num_groups, rows_max, group_rows_max, n_out, k, x8, x_scale, group_offsets, w8, w_scale,
+                           y_rows, ws, row_index=None, stream=None) -> None:
+    """y_rows[r] = W[g] x8[r] for the rows of each group; w8, w_scale from fp8_weights(w [G, n_out, k])."""
+    dev = _device()
+    _check(lib().moe_grouped_linear_fp8(
+        num_groups, rows_max, group_rows_max, n_out, k,
+        *_fp8_operands(num_groups, rows_max, k, x8, x_scale, group_offsets, row_index, dev),
+        *_matrix8(w8, w_scale, "w8", num_groups, n_out, k, False, dev),
+        _tensor(y_rows, "y_rows", torch.bfloat16, (rows_max, n_out), dev), _tensor(ws, "ws", torch.uint8, None, dev),
+        0 if ws is None else ws.numel(), _stream(stream)), "moe_grouped_linear_fp8")
+
+
+def moe_grouped_swiglu_gemm_fp8_workspace_size(num_groups, rows_max, group_rows_max, d_model, d_ff) -> int:
+    return int(lib().moe_grouped_swiglu_gemm_fp8_workspace_size(int(num_groups), int(rows_max), int(group_rows_max),
+                                                                int(d_model), int(d_ff)))
+
+
+def moe_grouped_swiglu_gemm_fp8(num_groups, rows_max, group_rows_max, d_model, d_ff, x8, x_scale, group_offsets,
+                                w_gate_up8, w_gate_up_scale, w_down8, w_down_scale, y_rows, ws, row_index=None,
+                                stream=None) -> None:
+    """The experts' FFN in 8 bits: fp8_weights(w_gate_up, swiglu=True) and fp8_weights(w_down)."""
+    dev = _device()
+    _check(lib().moe_grouped_swiglu_gemm_fp8(
+        num_groups, rows_max, group_rows_max, d_model, d_ff,
+        *_fp8_operands(num_groups, rows_max, d_model, x8, x_scale, group_offsets, row_index, dev),
+        *_matrix8(w_gate_up8, w_gate_up_scale, "w_gate_up8", num_groups, d_ff, d_model, True, dev),
+        *_matrix8(w_down8, w_down_scale, "w_down8", num_groups, d_model, d_ff, False, dev),
+        _tensor(y_rows, "y_rows", torch.bfloat16, (rows_max, d_model), dev), _tensor(ws, "ws", torch.uint8, None, dev),
+        0 if ws is None else ws.numel(), _stream(stream)), "moe_grouped_swiglu_gemm_fp8")
+
+
+def moe_forward_fp8_workspace_size(desc: MoeDesc) -> int:
+    return int(lib().moe_forward_fp8_workspace_size(ctypes.byref(desc)))
+
+
+def moe_forward_fp8(desc, w_router, gate_up, down, x, logit_offset, out, ws, routing: Optional[dict] = None,
+                    shared_gate_up=None, shared_down=None, x8=None, x_scale=None, stream=None) -> None:
+    """moe_forward with experts in 8 bits: gate_up, down (and the shared expert's) are the pairs that fp8_weights()
+    returns; x8, x_scale: x in 8 bits, or None (quantised here)."""
+    dev, T, d, E, f, fs = _device(), desc.num_tokens, desc.d_model, desc.num_experts, desc.d_ff, desc.d_ff_shared
+    m = lambda pair, name, g, n, k, s: (  # noqa: E731
+        MoeFp8Matrix(None, None) if pair is None else MoeFp8Matrix(*_matrix8(*pair, name, g, n, k, s, dev)))
+    W = MoeWeightsFp8(_tensor(w_router, "w_router", torch.bfloat16, (E, d), dev), m(gate_up, "gate_up", E, f, d, True),
+                      m(down, "down", E, d, f, False), m(shared_gate_up, "shared_gate_up", 1, fs, d, True),
+                      m(shared_down, "shared_down", 1, d, fs, False))
+    R = None
+    if routing is not None:
+        R = MoeRouting(*(_ptr(routing.get(n)) for n, _ in MoeRouting._fields_))
+    _check(lib().moe_forward_fp8(
+        ctypes.byref(desc), ctypes.byref(W), _tensor(x, "x", torch.bfloat16, (T, d), dev),
+        *_rows8(x8, x_scale, ("x8", "x_scale"), T, d, dev), _tensor(logit_offset, "logit_offset", torch.float32, (E,), dev),
+        _tensor(out, "out", torch.bfloat16, (T, d), dev), ctypes.byref(R) if R is not None else None,
+        _tensor(ws, "ws", torch.uint8, None, dev), 0 if ws is None else ws.numel(), _stream(stream)), "moe_forward_fp8")
+
+
 class MoELayer:
     """Holds one layer's device tensors and a workspace, and runs moe_forward.
+
+    fp8: the experts (and the shared expert) in 8 bits, quantised here once (moe_forward_fp8).
+    norm_weight [d]: a norm in front of the layer (moe_rms_norm with norm_eps): forward(residual) takes
+    inputs.x + residual, kept in `h` (the next block's residual), and the layer runs on its norm, `normed`, which it
+    gets in 8 bits too with fp8.
 
     Convenience only: allocation happens here, once, never inside a forward call."""
 
     def __init__(self, inputs, capacity, device="cuda", fill_order="token", overflow="drop", tiled=False,
-                 shared_tiled=False):
+                 shared_tiled=False, fp8=False, norm_weight=None, norm_eps=1e-6):
         w = inputs.workload
         self.inputs = inputs
         self.desc = make_desc(w.num_tokens, w.d_model, w.d_ff, w.num_experts, w.top_k, capacity,
                               w.d_ff_shared, w.torch_dtype, fill_order=fill_order, overflow=overflow)
-        self.ws = workspace(moe_workspace_size(self.desc), device)
+        if fp8 and (tiled or shared_tiled):
+            raise ValueError("tile-major copies are of bf16 weights: not with fp8")
+        if fp8 and self.desc.dtype != MOE_DTYPE_BF16:
+            raise ValueError("experts in 8 bits are implemented for bf16 layers")
+        self.fp8, self.norm_weight, self.norm_eps = None, norm_weight, norm_eps
+        if fp8:
+            self.fp8 = dict(gate_up=fp8_weights(inputs.w_gate_up, swiglu=True), down=fp8_weights(inputs.w_down))
+            if w.d_ff_shared:
+                self.fp8.update(shared_gate_up=fp8_weights(inputs.w_shared_gate_up.unsqueeze(0), swiglu=True),
+                                shared_down=fp8_weights(inputs.w_shared_down.unsqueeze(0)))
+        self.x8 = self.x_scale = None
+        if norm_weight is not None:
+            self.h, self.normed = torch.empty_like(inputs.x), torch.empty_like(inputs.x)
+            self.rstd = torch.empty((w.num_tokens,), dtype=torch.float32, device=device)
+            if fp8:
+                self.x8, self.x_scale = fp8_rows(w.num_tokens, w.d_model, device)
+        self.ws = workspace((moe_forward_fp8_workspace_size if fp8 else moe_workspace_size)(self.desc), device)
         self.out = torch.empty_like(inputs.x)
         T, E, k = w.num_tokens, w.num_experts, w.top_k
         R = moe_max_rows(self.desc)
@@ -812,7 +1049,19 @@ class MoELayer:
         self.shared_tiled = (tiled_shared_weights(self.desc, inputs.w_shared_gate_up, inputs.w_shared_down)
                              if shared_tiled and w.d_ff_shared else None)
 
+    def _layer_input(self, residual, stream):
+        """What the layer runs on: inputs.x, or the norm of inputs.x + residual."""
+        if self.norm_weight is None:
+            if residual is not None:
+                raise ValueError("a residual is added by the norm: construct MoELayer with norm_weight")
+            return self.inputs.x
+        moe_rms_norm(self.inputs.x, self.norm_weight, self.norm_eps, residual=residual, h=self.h, y=self.normed,
+                     y8=self.x8, y_scale=self.x_scale, rstd=self.rstd, stream=stream)
+        return self.normed
+
     def forward_staged(self, events, with_routing=False, stream=None):
+        if self.fp8 is not None or self.norm_weight is not None:
+            raise ValueError("forward_staged times moe_forward: not with fp8 or a norm")
         i = self.inputs
         moe_forward_staged(self.desc, i.w_router, i.w_gate_up, i.w_down, i.x, i.logit_offset, self.out, self.ws,
                            events, routing=self.routing if with_routing else None,
@@ -820,9 +1069,16 @@ class MoELayer:
                            tiled=self.tiled, shared_tiled=self.shared_tiled)
         return self.out
 
-    def forward(self, with_routing=True, stream=None):
+    def forward(self, with_routing=True, stream=None, residual=None):
         i = self.inputs
-        moe_forward(self.desc, i.w_router, i.w_gate_up, i.w_down, i.x, i.logit_offset, self.out, self.ws,
+        x = self._layer_input(residual, stream)
+        if self.fp8 is not None:
+            moe_forward_fp8(self.desc, i.w_router, self.fp8["gate_up"], self.fp8["down"], x, i.logit_offset, self.out,
+                            self.ws, routing=self.routing if with_routing else None,
+                            shared_gate_up=self.fp8.get("shared_gate_up"), shared_down=self.fp8.get("shared_down"),
+                            x8=self.x8, x_scale=self.x_scale, stream=stream)
+            return self.out
+        moe_forward(self.desc, i.w_router, i.w_gate_up, i.w_down, x, i.logit_offset, self.out, self.ws,
                     routing=self.routing if with_routing else None, w_shared_gate_up=i.w_shared_gate_up,
                     w_shared_down=i.w_shared_down, stream=stream, tiled=self.tiled, shared_tiled=self.shared_tiled)
         return self.out
@@ -835,15 +1091,17 @@ class MoETrainer:
 
     Buffers are allocated here, once; the optimizer's options (lr, weight_decay, max_grad_norm,
     state_bits, master_weights, capturable, ...) are MoEAdamW's.  The router is not decayed unless
-    weight_decay is given per tensor (router, gate_up, down[, shared gate_up, shared down]).  The
+    weight_decay is given per tensor (router, gate_up, down[, shared gate_up, shared down][, norm]).
+    norm_weight, norm_eps: a norm in front of the layer, as MoELayer's, trained with it (not decayed either).  The
     optimizer holds the weights of `inputs` and the `grads` that the trainer was built with: change
     them in place; step() refuses others."""
 
     def __init__(self, inputs, capacity, device="cuda", fill_order="token", overflow="drop", tiled=False,
                  shared_tiled=False, alpha=0.01, z_coeff=0.001, seq_offsets=None, token_mask=None, weight_decay=0.01,
-                 **adamw):
+                 norm_weight=None, norm_eps=1e-6, **adamw):
         w = inputs.workload
-        self.layer = MoELayer(inputs, capacity, device, fill_order, overflow, tiled, shared_tiled)
+        self.layer = MoELayer(inputs, capacity, device, fill_order, overflow, tiled, shared_tiled,
+                              norm_weight=norm_weight, norm_eps=norm_eps)
         desc = self.layer.desc
         if desc.dtype != MOE_DTYPE_BF16:
             raise ValueError("training is implemented for bf16 layers")
@@ -862,28 +1120,42 @@ class MoETrainer:
         self.balance_ws = workspace(moe_balance_workspace_size(desc, S), device)
         self.backward_ws = workspace(moe_backward_workspace_size(desc), device)
         if not isinstance(weight_decay, (list, tuple)):
-            weight_decay = [0.0] + [weight_decay] * (len(names) - 1)
+            weight_decay = [0.0] + [weight_decay] * (len(names) - 1) + [0.0] * (norm_weight is not None)
+        if norm_weight is not None:
+            self.grads["dw_norm"] = torch.zeros((w.d_model,), **f32)
+            self.norm_ws = workspace(moe_rms_norm_backward_workspace_size(T, w.d_model), device)
+            names, weights = names + ["norm"], weights + [norm_weight]
         self._names = names
         self.optimizer = MoEAdamW(weights, [self.grads["dw_" + n] for n in names], weight_decay=weight_decay, **adamw)
 
-    def forward(self):
-        return self.layer.forward(with_routing=True)
+    def forward(self, residual=None):
+        return self.layer.forward(with_routing=True, residual=residual)
 
-    def backward(self, dy):
-        """Gradients of sum(dy * out) + losses[0] + losses[1] of the last forward; returns dx."""
+    def backward(self, dy, dh=None):
+        """Gradients of sum(dy * out) + losses[0] + losses[1] of the last forward; returns dx.  With a norm dx is the
+        gradient of inputs.x and of the residual; dh, the gradient that reaches the layer's h, adds to it."""
         i, r, desc = self.layer.inputs, self.layer.routing, self.layer.desc
+        norm = self.layer.norm_weight
+        if dh is not None and norm is None:
+            raise ValueError("dh is a gradient on the norm's h: construct MoETrainer with norm_weight")
+        x = i.x if norm is None else self.layer.normed
         moe_balance_loss(desc, r["logits"], r["topk_ids"], self.alpha, self.z_coeff, self.counts, self.seq_tokens,
                          self.mean_probs, self.losses, self.balance_ws, token_mask=self.token_mask,
                          seq_offsets=self.seq_offsets, dlogits=self.dlogits)
-        moe_backward(desc, i.w_router, i.w_gate_up, i.w_down, i.x, r, dy, self.dx, self.grads, self.backward_ws,
+        moe_backward(desc, i.w_router, i.w_gate_up, i.w_down, x, r, dy, self.dx, self.grads, self.backward_ws,
                      w_shared_gate_up=i.w_shared_gate_up, w_shared_down=i.w_shared_down, tiled=self.layer.tiled,
                      shared_tiled=self.layer.shared_tiled, dlogits=self.dlogits)
+        if norm is not None:
+            moe_rms_norm_backward(self.dx, self.layer.h, norm, self.layer.rstd, self.dx, self.grads["dw_norm"],
+                                  self.norm_ws, dh=dh)
         return self.dx
 
     def step(self) -> None:
         for n, p, g in zip(self._names, self.optimizer.params, self.optimizer.grads):
-            if getattr(self.layer.inputs, "w_" + n).data_ptr() != p.data_ptr():
-                raise RuntimeError(f"inputs.w_{n} is not the tensor that the optimizer updates: build the trainer again")
+            now = self.layer.norm_weight if n == "norm" else getattr(self.layer.inputs, "w_" + n)
+            if now.data_ptr() != p.data_ptr():
+                raise RuntimeError(f"{'norm_weight' if n == 'norm' else 'inputs.w_' + n} is not the tensor that the "
+                                   "optimizer updates: build the trainer again")
             if self.grads["dw_" + n].data_ptr() != g.data_ptr():
                 raise RuntimeError(f"grads['dw_{n}'] is not the tensor that the optimizer reads: build the trainer again")
         self.optimizer.step()
@@ -893,9 +1165,9 @@ class MoETrainer:
         if L.shared_tiled is not None:
             tile_shared_weights(L.desc, i.w_shared_gate_up, i.w_shared_down, *L.shared_tiled)
 
-    def train_step(self, dy):
-        """forward, backward(dy), step; returns the forward's out."""
-        out = self.forward()
-        self.backward(dy)
+    def train_step(self, dy, residual=None, dh=None):
+        """forward(residual), backward(dy, dh), step; returns the forward's out."""
+        out = self.forward(residual)
+        self.backward(dy, dh)
         self.step()
         return out
