@@ -46,19 +46,18 @@ __device__ __forceinline__ uint32_t fp8_codes(float a, float b, float c, float d
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
 }
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-__device__ __forceinline__ i32x8 fp8_operand(u32x4 lo, u32x4 hi) {
-  return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+// Eight codes as bf16, times 2^(e) for a scale 2^e given as a float: exact (bf16 has a float's exponents).
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u32x4 fp8_to_bf16(uint32_t lo, uint32_t hi, float scale) {
+  return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true))};
 }
-// c + (A 2^sa) (B 2^sb), 16 x 16 over 128 of K, the scales byte J of sa and sb.  Lane l holds row l % 16
-// of each operand, k = 16 (l / 16) .. + 15 and 64 + 16 (l / 16) .. + 15 (any order shared by the two
-// operands gives the same sum); c: columns (of B) l % 16, rows (of A) 4 (l / 16) .. + 3.
-// Within a lane's 16 products the instruction drops what lies about 2^-14 below the largest
-// of them; the accumulator is a full float.  Against 64 bits the sums of Gaussian rows are off by 1.2e-5 to
-// 1.6e-5 of their size, over any length: a hundredth of the bf16 rounding that follows.
+// Byte J of four blocks' scales as the float 2^(byte - 127).
 template <int J>
-__device__ __forceinline__ f32x4 mfma_fp8_16(i32x8 a, i32x8 b, f32x4 c, uint32_t sa, uint32_t sb) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, J, (int)sa, J, (int)sb);
+__device__ __forceinline__ float fp8_scale(uint32_t four) {
+  return __uint_as_float(((four >> (8 * J)) & 0xffu) << 23);
 }
 
 }  // namespace moe

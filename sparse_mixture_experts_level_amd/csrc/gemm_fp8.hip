@@ -3,7 +3,15 @@
 // for the rows r of each group, bf16; and the gate_up form, whose epilogue forms
 //   H[r][n] = silu(G[r][n]) U[r][n],  silu(z) = z / (1 + exp(-z))
 // from the float sums and quantises it again, a scale for each 128 columns of a row.
+//
+// Few rows a group: bound by the weights' bytes.  Weights go from memory straight to registers (their
+// layout is the matrix instruction's), whole lines, non-temporal, several steps ahead; codes become
+// bf16 times their scale there (an exact conversion, two values an instruction) and meet the rows in the bf16 matrix
+// instruction: at half the 8-bit one's rate it still has time to spare, and its sums are those of
+// floats, where the 8-bit instruction drops what lies 2^-14 below the largest of 16 products (1.5e-5 of a
+// sum: enough to move one code of H in two thousand).
 #include <algorithm>
+#include <climits>
 
 #include "fp8.hpp"
 #include "kernels.hpp"
@@ -12,120 +20,381 @@ namespace moe {
 
 namespace {
 
-// One workgroup: 128 output columns of one group, eight waves of 16 columns (and, for gate_up, the 16 gate
-// and the 16 up rows of each), row blocks of 16 MS rows one after the other.  The weights are the
+// What a workgroup has of its group: the rows, clamped to the buffers.
+__device__ __forceinline__ void group_rows(const Fp8GemmArgs &a, int g, int &begin, int &end) {
+  begin = min(max(a.offsets[g], 0), a.rows_max);
+  end = min(max(a.offsets[g + 1], begin), a.rows_max);
+}
+
+// Where row m0 + r of a group stands: byte offsets of its codes and scales in xres and sres, kOob past the group's
+// end and for an index outside the rows.
+struct Fp8Rows {
+  rsrc_t xres, sres;
+  bool gather;
+  __device__ __forceinline__ Fp8Rows(const Fp8GemmArgs &a, int m0, int rows) : gather(a.row_index != nullptr) {
+    const int kp = fp8_row_bytes(a.K), ks = fp8_scale_bytes(a.K);
+    const int64_t first = gather ? 0 : m0, n = gather ? a.x_rows : rows;
+    xres = make_rsrc(a.x8 + first * kp, (uint32_t)(n * kp));
+    sres = make_rsrc(a.x_scale + first * ks, (uint32_t)(n * ks));
+  }
+  __device__ __forceinline__ uint32_t row(const Fp8GemmArgs &a, int m0, int r, bool in) const {
+    uint32_t src = (uint32_t)r;
+    if (gather && in) {
+      src = (uint32_t)a.row_index[m0 + r];
+      in = src < (uint32_t)a.x_rows;
+    }
+    return in ? src : kOob;
+  }
+};
+
+// H's 8 bits from a lane's four columns of one row: `top` is the largest magnitude of the row's 128.
+__device__ __forceinline__ void store_h(const Fp8GemmArgs &a, const float *h, float top, int64_t row, int nb, int col,
+                                        bool first) {
+  const uint32_t byte = fp8_scale_byte(top);
+  const float inv = fp8_inverse(byte);
+  *reinterpret_cast<uint32_t *>(a.h8 + row * fp8_row_bytes(a.n_out) + col) =
+      fp8_codes(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv);
+  if (first) a.h_scale[row * fp8_scale_bytes(a.n_out) + nb] = (uint8_t)byte;
+}
+
+// A lane's four columns of one output row.
+__device__ __forceinline__ void store_y(const Fp8GemmArgs &a, f32x4 v, int64_t row, int col) {
+  uint16_t *o = a.y + row * a.n_out + col;
+  if (a.n_out % 4 == 0) {
+    if (col < a.n_out) *reinterpret_cast<uint2 *>(o) = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (col + j < a.n_out) o[j] = f32_to_bf16(v[j]);
+  }
+}
+
+// Few rows: 16 MS of them at a time, one block after the other.  A workgroup has 16 U output columns; each wave 16
+// of them (for gate_up the 16 gate and the 16 up rows) and one of KS parts of K, whose sums the first
+// part's waves add in order.  Rows are read from the caches in the operand layout, with the weights: no
+// LDS, no barrier, R steps of 128 in flight in registers.  The weights are the
 // matrix instruction's first operand, so that a lane holds four consecutive columns of one row.
-template <bool SWIGLU, int MS>
-__global__ __launch_bounds__(512) void fp8_stream_kernel(const Fp8GemmArgs a) {
+template <bool SWIGLU, int MS, int U, int KS>
+__global__ __launch_bounds__(64 * U * KS) void fp8_small_kernel(const Fp8GemmArgs a) {
   constexpr int NB = SWIGLU ? 2 : 1;
-  __shared__ float tops[8][16 * MS];
+  constexpr int R = SWIGLU || MS > 1 ? 4 : 8;
+  static_assert(!SWIGLU || U == 8, "a block of H's columns a workgroup");
+  __shared__ float tops[SWIGLU ? 8 : 1][16 * MS];
+  __shared__ f32x4 parts[KS > 1 ? (KS - 1) * U * MS * NB * 64 : 1];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lr = lane & 15, lg = lane >> 4;
-  const int n_blocks = fp8_blocks(a.n_out);
+  const int u = wave % U, part = wave / U;
+  const int n_blocks = (a.n_out + 16 * U - 1) / (16 * U);
   const int g = blockIdx.x / n_blocks, nb = blockIdx.x - g * n_blocks;
-  const int begin = min(max(a.offsets[g], 0), a.rows_max), end = min(max(a.offsets[g + 1], begin), a.rows_max);
-  if (begin >= end) return;
+  int begin, end;
+  group_rows(a, g, begin, end);
+  if (end - begin <= a.rows_above || end - begin > a.rows_most) return;
   const int kt = fp8_blocks(a.K), kp = fp8_row_bytes(a.K), ks = fp8_scale_bytes(a.K);
-  const int unit = nb * 8 + wave, units = (a.n_out + 15) / 16;
+  const int quads = ks / 4, tb = 4 * (quads * part / KS), te = min(kt, 4 * (quads * (part + 1) / KS));
+  const int unit = nb * U + u, units = (a.n_out + 15) / 16;
   const int64_t wbytes = (int64_t)units * NB * kt * kFp8Tile;
   const rsrc_t wres = make_rsrc(a.w8 + g * wbytes, (uint32_t)wbytes);
   const uint32_t woff = unit < units ? (uint32_t)(unit * NB * kt * kFp8Tile + lane * 16) : kOob;
-  const uint8_t *wscale = a.w_scale + (int64_t)(g * n_blocks + nb) * NB * ks;
+  const uint8_t *wscale =
+      a.w_scale + ((int64_t)g * fp8_blocks(a.n_out) + __builtin_amdgcn_readfirstlane(min(unit, units - 1) / 8)) * NB * ks;
   for (int m0 = begin; m0 < end; m0 += 16 * MS) {
-    const bool gather = a.row_index != nullptr;
-    const rsrc_t xres = gather ? make_rsrc(a.x8, (uint32_t)((int64_t)a.x_rows * kp))
-                               : make_rsrc(a.x8 + (int64_t)m0 * kp, (uint32_t)(min(16 * MS, end - m0) * kp));
-    const rsrc_t sres = gather ? make_rsrc(a.x_scale, (uint32_t)((int64_t)a.x_rows * ks))
-                               : make_rsrc(a.x_scale + (int64_t)m0 * ks, (uint32_t)(min(16 * MS, end - m0) * ks));
+    const Fp8Rows rows(a, m0, min(16 * MS, end - m0));
     uint32_t xoff[MS], soff[MS];
 #pragma unroll
     for (int i = 0; i < MS; ++i) {
-      const int r = i * 16 + lr;
-      uint32_t src = (uint32_t)r;
-      bool ok = m0 + r < end;
-      if (gather && ok) {
-        src = (uint32_t)a.row_index[m0 + r];
-        ok = src < (uint32_t)a.x_rows;
-      }
-      xoff[i] = ok ? src * (uint32_t)kp + (uint32_t)lg * 16u : kOob;
-      soff[i] = ok ? src * (uint32_t)ks : kOob;
+      const uint32_t src = rows.row(a, m0, i * 16 + lr, m0 + i * 16 + lr < end);
+      xoff[i] = src != kOob ? src * (uint32_t)kp + (uint32_t)lg * 16u : kOob;
+      soff[i] = src != kOob ? src * (uint32_t)ks : kOob;
     }
+    u32x4 w[R][NB][2], x[R][MS][2];
+    uint32_t sx[R / 4][MS], sw[R / 4][NB];
+    auto load = [&](int j, int t) {  // steps past the part's end read zeros
+      const bool in = t < te;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const uint32_t o = in && woff != kOob ? woff + (uint32_t)((b * kt + t) * kFp8Tile) : kOob;
+        w[j][b][0] = buf_ld16_nt(wres, o);
+        w[j][b][1] = buf_ld16_nt(wres, o == kOob ? kOob : o + 1024u);
+      }
+#pragma unroll
+      for (int i = 0; i < MS; ++i) {
+        const uint32_t o = in && xoff[i] != kOob ? xoff[i] + (uint32_t)t * 128u : kOob;
+        x[j][i][0] = buf_ld16(rows.xres, o);
+        x[j][i][1] = buf_ld16(rows.xres, o == kOob ? kOob : o + 64u);
+      }
+    };
+    auto load_scales = [&](int q, int t) {
+      const int left = kt - t;  // blocks that exist: the padding's scales are not looked at
+      const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+#pragma unroll
+      for (int i = 0; i < MS; ++i)
+        sx[q][i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
+                       rows.sres, soff[i] == kOob || left <= 0 ? kOob : soff[i] + (uint32_t)t, 0, 0) & keep;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        sw[q][b] = *reinterpret_cast<const uint32_t *>(wscale + b * ks + (left <= 0 ? 0 : t)) & keep;
+    };
     f32x4 acc[MS][NB];
 #pragma unroll
     for (int i = 0; i < MS; ++i)
 #pragma unroll
       for (int b = 0; b < NB; ++b) acc[i][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int k0 = 0; k0 < kt; k0 += 4) {
-      const uint32_t keep = kt - k0 >= 4 ? ~0u : (1u << (8 * (kt - k0))) - 1u;  // scales of blocks that exist
-      uint32_t sx[MS], sw[NB];
 #pragma unroll
-      for (int i = 0; i < MS; ++i)
-        sx[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(sres, soff[i] == kOob ? kOob : soff[i] + k0, 0, 0) & keep;
+    for (int j = 0; j < R; ++j) load(j, tb + j);
 #pragma unroll
-      for (int b = 0; b < NB; ++b) sw[b] = *reinterpret_cast<const uint32_t *>(wscale + b * ks + k0) & keep;
+    for (int q = 0; q < R / 4; ++q) load_scales(q, tb + 4 * q);
+    for (int t0 = tb; t0 < te; t0 += R) {
       auto step = [&](auto jc) {
-        constexpr int J = decltype(jc)::value;
-        const bool in = k0 + J < kt;
-        i32x8 w[NB], x[MS];
+        constexpr int J = decltype(jc)::value, Q = J / 4, S = J % 4;
+        float fx[MS], fw[NB];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const uint32_t o = in && woff != kOob ? woff + (uint32_t)((b * kt + k0 + J) * kFp8Tile) : kOob;
-          w[b] = fp8_operand(buf_ld16_nt(wres, o), buf_ld16_nt(wres, o == kOob ? kOob : o + 1024u));
-        }
+        for (int i = 0; i < MS; ++i) fx[i] = fp8_scale<S>(sx[Q][i]);
 #pragma unroll
-        for (int i = 0; i < MS; ++i) {
-          const uint32_t o = in && xoff[i] != kOob ? xoff[i] + (uint32_t)((k0 + J) * 128) : kOob;
-          x[i] = fp8_operand(buf_ld16(xres, o), buf_ld16(xres, o == kOob ? kOob : o + 64u));
+        for (int b = 0; b < NB; ++b) fw[b] = fp8_scale<S>(sw[Q][b]);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {  // 32 of K: eight of each lane's 32 codes
+          u32x4 xb[MS], wb[NB];
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            wb[b] = fp8_to_bf16(w[J][b][m / 2][2 * (m % 2)], w[J][b][m / 2][2 * (m % 2) + 1], fw[b]);
+#pragma unroll
+          for (int i = 0; i < MS; ++i)
+            xb[i] = fp8_to_bf16(x[J][i][m / 2][2 * (m % 2)], x[J][i][m / 2][2 * (m % 2) + 1], fx[i]);
+#pragma unroll
+          for (int i = 0; i < MS; ++i)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) acc[i][b] = mfma16(wb[b], xb[i], acc[i][b]);
         }
+        load(J, t0 + J + R);
+        if constexpr (S == 3) load_scales(Q, t0 + R + 4 * Q);
+      };
+      step(std::integral_constant<int, 0>{});
+      step(std::integral_constant<int, 1>{});
+      step(std::integral_constant<int, 2>{});
+      step(std::integral_constant<int, 3>{});
+      if constexpr (R == 8) {
+        step(std::integral_constant<int, 4>{});
+        step(std::integral_constant<int, 5>{});
+        step(std::integral_constant<int, 6>{});
+        step(std::integral_constant<int, 7>{});
+      }
+    }
+    if constexpr (KS > 1) {
+      if (part > 0)
 #pragma unroll
         for (int i = 0; i < MS; ++i)
 #pragma unroll
-          for (int b = 0; b < NB; ++b) acc[i][b] = mfma_fp8_16<J>(w[b], x[i], acc[i][b], sw[b], sx[i]);
+          for (int b = 0; b < NB; ++b) parts[((((part - 1) * U + u) * MS + i) * NB + b) * 64 + lane] = acc[i][b];
+      __syncthreads();
+      if (part == 0)
+#pragma unroll
+        for (int p = 1; p < KS; ++p)
+#pragma unroll
+          for (int i = 0; i < MS; ++i)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) acc[i][b] += parts[((((p - 1) * U + u) * MS + i) * NB + b) * 64 + lane];
+    }
+    const int col = unit * 16 + lg * 4;
+    if constexpr (SWIGLU) {
+      float h[MS][4];
+      if (part == 0)
+#pragma unroll
+        for (int i = 0; i < MS; ++i) {
+          float top = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            h[i][j] = silu_f32(acc[i][0][j]) * acc[i][1][j];
+            top = fmaxf(top, fp8_magnitude(h[i][j]));
+          }
+          top = fmaxf(top, __shfl_xor(top, 16, 64));
+          top = fmaxf(top, __shfl_xor(top, 32, 64));
+          if (lg == 0) tops[u][i * 16 + lr] = top;
+        }
+      __syncthreads();
+      if (part == 0)
+#pragma unroll
+        for (int i = 0; i < MS; ++i) {
+          float top = 0.0f;
+#pragma unroll
+          for (int v = 0; v < 8; ++v) top = fmaxf(top, tops[v][i * 16 + lr]);
+          const int64_t row = m0 + i * 16 + lr;
+          if (row < end) store_h(a, h[i], top, row, nb, col, u == 0 && lg == 0);
+        }
+    } else if (part == 0) {
+#pragma unroll
+      for (int i = 0; i < MS; ++i) {
+        const int64_t row = m0 + i * 16 + lr;
+        if (row < end) store_y(a, acc[i][0], row, col);
+      }
+    }
+    if (SWIGLU || KS > 1) __syncthreads();  // the next rows use the same LDS
+  }
+}
+
+// Some rows, up to 128 at a time: a workgroup has 128 columns of H or 256 of y, each of its eight waves two
+// blocks of 16 weight rows (gate and up, or neighbours).  The rows are read by all eight waves from LDS, as bf16
+// times their scale: each step's 128 of K are loaded a step ahead by the whole workgroup,
+// converted once and stored in the operand layout (4 KB for 16 rows), two stages.
+template <bool SWIGLU>
+__global__ __launch_bounds__(512) void fp8_medium_kernel(const Fp8GemmArgs a) {
+  constexpr int MS = 8, R = 4;
+  __shared__ __attribute__((aligned(16))) uint8_t stage[2][MS * 4096];
+  __shared__ float tops[SWIGLU ? 8 : 1][16 * MS];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lr = lane & 15, lg = lane >> 4;
+  constexpr int COLS = SWIGLU ? 128 : 256;
+  const int n_blocks = (a.n_out + COLS - 1) / COLS;
+  const int g = blockIdx.x / n_blocks, nb = blockIdx.x - g * n_blocks;
+  int begin, end;
+  group_rows(a, g, begin, end);
+  if (end - begin <= a.rows_above || end - begin > a.rows_most) return;
+  const int kt = fp8_blocks(a.K), kp = fp8_row_bytes(a.K), ks = fp8_scale_bytes(a.K);
+  const int units = (a.n_out + 15) / 16 * (SWIGLU ? 2 : 1);  // blocks of 16 weight rows
+  const int unit = nb * 16 + wave * 2;
+  const int64_t wbytes = (int64_t)units * kt * kFp8Tile;
+  const rsrc_t wres = make_rsrc(a.w8 + g * wbytes, (uint32_t)wbytes);
+  uint32_t woff[2];
+#pragma unroll
+  for (int b = 0; b < 2; ++b) woff[b] = unit + b < units ? (uint32_t)((unit + b) * kt * kFp8Tile + lane * 16) : kOob;
+  const int sblocks = fp8_blocks(a.n_out);
+  const uint8_t *wscale =
+      a.w_scale + ((int64_t)g * sblocks + (SWIGLU ? nb : min(nb * 2 + __builtin_amdgcn_readfirstlane(wave) / 4, sblocks - 1))) *
+                      (SWIGLU ? 2 : 1) * ks;
+  for (int m0 = begin; m0 < end; m0 += 16 * MS) {
+    const int n = min(16 * MS, end - m0), ms = (n + 15) / 16;
+    const Fp8Rows rows(a, m0, n);
+    // this thread's pieces of a step: 16 codes, row q % 16 of subtile q / 128, k = 64 p + 16 c ..
+    uint32_t xoff[2], soff[2];
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      const int q = threadIdx.x + 512 * v, r = (q >> 7) * 16 + (q & 15);
+      const uint32_t src = rows.row(a, m0, r, r < n);
+      xoff[v] = src != kOob ? src * (uint32_t)kp + (uint32_t)((q >> 6 & 1) * 64 + (q >> 4 & 3) * 16) : kOob;
+      soff[v] = src != kOob ? src * (uint32_t)ks : kOob;
+    }
+    u32x4 w[R][2][2], x[2];
+    uint32_t sx[2], sw[2];
+    auto load_w = [&](int j, int t) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const uint32_t o = t < kt && woff[b] != kOob ? woff[b] + (uint32_t)(t * kFp8Tile) : kOob;
+        w[j][b][0] = buf_ld16_nt(wres, o);
+        w[j][b][1] = buf_ld16_nt(wres, o == kOob ? kOob : o + 1024u);
+      }
+    };
+    auto load_x = [&](int t) {
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const bool in = t < kt && xoff[v] != kOob;
+        x[v] = buf_ld16(rows.xres, in ? xoff[v] + (uint32_t)t * 128u : kOob);
+        sx[v] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rows.sres, in ? soff[v] + (uint32_t)t : kOob, 0, 0);
+      }
+    };
+    auto put_x = [&](int s) {
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const int q = threadIdx.x + 512 * v;
+        if ((q >> 7) < ms) {
+          const float f = __uint_as_float((sx[v] & 0xffu) << 23);
+          uint8_t *o = stage[s] + (q >> 7) * 4096 + (q >> 6 & 1) * 2048 + (q & 63) * 16;
+          *reinterpret_cast<u32x4 *>(o) = fp8_to_bf16(x[v][0], x[v][1], f);
+          *reinterpret_cast<u32x4 *>(o + 1024) = fp8_to_bf16(x[v][2], x[v][3], f);
+        }
+      }
+    };
+    auto load_sw = [&](int t) {
+      const int left = kt - t;
+      const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        sw[b] = *reinterpret_cast<const uint32_t *>(wscale + (SWIGLU ? b * ks : 0) + (left <= 0 ? 0 : t)) & keep;
+    };
+    auto bar = [&]() {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    f32x4 acc[MS][2];
+#pragma unroll
+    for (int i = 0; i < MS; ++i)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) acc[i][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    load_x(0);
+#pragma unroll
+    for (int j = 0; j < R; ++j) load_w(j, j);
+    load_sw(0);
+    put_x(0);
+    load_x(1);
+    bar();
+    for (int t0 = 0; t0 < kt; t0 += R) {
+      auto step = [&](auto jc) {
+        constexpr int J = decltype(jc)::value;
+        const int t = t0 + J;
+        // stage t + 1: last read in step t - 1, which every wave has left
+        if (t + 1 < kt) put_x((J + 1) & 1);
+        load_x(t + 2);
+        if (t < kt) {
+          float fw[2];
+#pragma unroll
+          for (int b = 0; b < 2; ++b) fw[b] = fp8_scale<J>(sw[b]);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            u32x4 wb[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+              wb[b] = fp8_to_bf16(w[J][b][m / 2][2 * (m % 2)], w[J][b][m / 2][2 * (m % 2) + 1], fw[b]);
+#pragma unroll
+            for (int i = 0; i < MS; ++i) {
+              if (i >= ms) break;
+              const u32x4 xb = *reinterpret_cast<const u32x4 *>(stage[J & 1] + i * 4096 + m * 1024 + lane * 16);
+#pragma unroll
+              for (int b = 0; b < 2; ++b) acc[i][b] = mfma16(wb[b], xb, acc[i][b]);
+            }
+          }
+        }
+        load_w(J, t + R);
+        if constexpr (J == 3) load_sw(t0 + R);
+        bar();
       };
       step(std::integral_constant<int, 0>{});
       step(std::integral_constant<int, 1>{});
       step(std::integral_constant<int, 2>{});
       step(std::integral_constant<int, 3>{});
     }
-    const int col = nb * 128 + wave * 16 + lg * 4;
     if constexpr (SWIGLU) {
-      float h[MS][4];
+      const int col = nb * 128 + wave * 16 + lg * 4;
 #pragma unroll
       for (int i = 0; i < MS; ++i) {
+        if (i >= ms) break;
         float top = 0.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          h[i][j] = silu_f32(acc[i][0][j]) * acc[i][1][j];
-          top = fmaxf(top, fp8_magnitude(h[i][j]));
+          acc[i][0][j] = silu_f32(acc[i][0][j]) * acc[i][1][j];
+          top = fmaxf(top, fp8_magnitude(acc[i][0][j]));
         }
         top = fmaxf(top, __shfl_xor(top, 16, 64));
         top = fmaxf(top, __shfl_xor(top, 32, 64));
         if (lg == 0) tops[wave][i * 16 + lr] = top;
       }
       __syncthreads();
-      const int hp = fp8_row_bytes(a.n_out), hs = fp8_scale_bytes(a.n_out);
 #pragma unroll
       for (int i = 0; i < MS; ++i) {
+        if (i >= ms) break;
         float top = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) top = fmaxf(top, tops[w][i * 16 + lr]);
-        const uint32_t byte = fp8_scale_byte(top);
-        const float inv = fp8_inverse(byte);
+        for (int v = 0; v < 8; ++v) top = fmaxf(top, tops[v][i * 16 + lr]);
         const int64_t row = m0 + i * 16 + lr;
-        if (row < end) {
-          *reinterpret_cast<uint32_t *>(a.h8 + row * hp + col) =
-              fp8_codes(h[i][0] * inv, h[i][1] * inv, h[i][2] * inv, h[i][3] * inv);
-          if (wave == 0 && lg == 0) a.h_scale[row * hs + nb] = (uint8_t)byte;
-        }
+        const float h[4] = {acc[i][0][0], acc[i][0][1], acc[i][0][2], acc[i][0][3]};
+        if (row < end) store_h(a, h, top, row, nb, col, wave == 0 && lg == 0);
       }
       __syncthreads();
     } else {
 #pragma unroll
       for (int i = 0; i < MS; ++i) {
+        if (i >= ms) break;
         const int64_t row = m0 + i * 16 + lr;
-        if (row >= end) continue;
+        if (row < end)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (col + j < a.n_out) a.y[row * a.n_out + col + j] = f32_to_bf16(acc[i][0][j]);
+          for (int b = 0; b < 2; ++b) store_y(a, acc[i][b], row, (unit + b) * 16 + lg * 4);
       }
     }
   }
@@ -133,12 +402,24 @@ __global__ __launch_bounds__(512) void fp8_stream_kernel(const Fp8GemmArgs a) {
 
 }  // namespace
 
-hipError_t launch_fp8_gemm(const Fp8GemmArgs &a, hipStream_t s) {
-  const unsigned grid = (unsigned)(a.num_groups * fp8_blocks(a.n_out));
-  if (a.h8)
-    hipLaunchKernelGGL((fp8_stream_kernel<true, 2>), dim3(grid), dim3(512), 0, s, a);
-  else
-    hipLaunchKernelGGL((fp8_stream_kernel<false, 2>), dim3(grid), dim3(512), 0, s, a);
+hipError_t launch_fp8_gemm(const Fp8GemmArgs &a0, hipStream_t s) {
+  Fp8GemmArgs a = a0;
+  const int most = std::min(a.group_rows_max, a.rows_max);
+  const bool swiglu = a.h8 != nullptr;
+  a.rows_above = 0;
+  a.rows_most = INT_MAX;
+  auto grid = [&](int cols) { return dim3((unsigned)(a.num_groups * ((a.n_out + cols - 1) / cols))); };
+  if (most <= 16) {
+    if (swiglu)
+      hipLaunchKernelGGL((fp8_small_kernel<true, 1, 8, 1>), grid(128), dim3(512), 0, s, a);
+    else
+      hipLaunchKernelGGL((fp8_small_kernel<false, 1, 8, 1>), grid(128), dim3(512), 0, s, a);
+  } else {
+    if (swiglu)
+      hipLaunchKernelGGL((fp8_medium_kernel<true>), grid(128), dim3(512), 0, s, a);
+    else
+      hipLaunchKernelGGL((fp8_medium_kernel<false>), grid(256), dim3(512), 0, s, a);
+  }
   return hipGetLastError();
 }
 

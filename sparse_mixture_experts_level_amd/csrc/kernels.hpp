@@ -241,6 +241,7 @@ struct Fp8GemmArgs {
   uint16_t *y;
   uint8_t *h8, *h_scale;
   int num_groups, rows_max, group_rows_max, x_rows, n_out, K;
+  int rows_above, rows_most;  // set by the launch: groups of more rows than this, and of at most these
 };
 hipError_t launch_fp8_gemm(const Fp8GemmArgs &a, hipStream_t s);
 
