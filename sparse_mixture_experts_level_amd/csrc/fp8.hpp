@@ -23,6 +23,62 @@ namespace moe {
 
 constexpr int kFp8Tile = 2048;  // bytes of a 16 x 128 block of weights
 
+// Eight consecutive values as they are held, loaded and stored as 16-byte pieces at any alignment of the
+// element's own size (the vector memory path takes unaligned addresses).  `n` of them exist (n <= 0: none; the
+// rest read as zeros and are not stored); WHOLE: rows are whole vectors, n is at least eight or
+// at most zero.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+template <typename T>
+struct Raw8 {
+  u32x4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void to(float *f) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (sizeof(T) == 2)
+        f[i] = __uint_as_float(i % 2 ? v[0][i / 2] & 0xffff0000u : v[0][i / 2] << 16);
+      else
+        f[i] = __uint_as_float(v[i / 4][i % 4]);
+    }
+  }
+};
+template <typename T, bool WHOLE>
+__device__ __forceinline__ Raw8<T> load8(const T *p, int n) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = u32x4{0u, 0u, 0u, 0u};
+  if (n >= 8) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = reinterpret_cast<const u32x4_any *>(p)[i];
+  } else if (!WHOLE && n > 0) {
+    T t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = i < n ? p[i] : T(0);
+    __builtin_memcpy(r.v, t, sizeof t);
+  }
+  return r;
+}
+template <typename T, bool WHOLE>
+__device__ __forceinline__ void store8(T *p, int n, const float *f) {
+  if (n >= 8) {
+    u32x4 v[sizeof(T) / 2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 2) {
+        v[0][i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+      } else {
+        v[0][i] = __float_as_uint(f[i]);
+        v[1][i] = __float_as_uint(f[4 + i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<u32x4_any *>(p)[i] = v[i];
+  } else if (!WHOLE && n > 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) store_out(p + i, f[i]);
+  }
+}
+
 // |v| where it is finite, else 0: values that are not finite have no part in a block's scale.
 __device__ __forceinline__ float fp8_magnitude(float v) {
   const float a = fabsf(v);

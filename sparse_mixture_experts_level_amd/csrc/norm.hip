@@ -15,48 +15,40 @@ namespace moe {
 
 namespace {
 
-// Eight consecutive values at any alignment of the element's own size (the vector memory path takes
-// unaligned addresses); `n` of them exist, the rest read as zeros.
-template <typename T>
-__device__ __forceinline__ void load8(const T *p, int n, float *v) {
-  T t[8];
-  if (n >= 8) {
-    __builtin_memcpy(t, p, sizeof t);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = i < n ? p[i] : T(0);
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if constexpr (sizeof(T) == 2)
-      v[i] = bf16_to_f32(t[i]);
-    else
-      v[i] = t[i];
-  }
+// Sum over the wavefront in every lane, by lane moves (two 32-bit halves of a double).
+__device__ __forceinline__ float wave_sum(float v) {
+  return group_reduce<64>(v, [](float a, float b) { return a + b; });
+}
+template <int CTRL>
+__device__ __forceinline__ double double_move(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint64_t lo = lane_move<CTRL>((uint32_t)u), hi = lane_move<CTRL>((uint32_t)(u >> 32));
+  return __builtin_bit_cast(double, lo | hi << 32);
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  v += double_move<0xb1>(v);
+  v += double_move<0x4e>(v);
+  v += double_move<0x141>(v);
+  v += double_move<0x140>(v);
+  auto pair = [](auto lo, auto hi) {
+    return __builtin_bit_cast(double, (uint64_t)lo[0] | (uint64_t)hi[0] << 32) +
+           __builtin_bit_cast(double, (uint64_t)lo[1] | (uint64_t)hi[1] << 32);
+  };
+  uint64_t u = __builtin_bit_cast(uint64_t, v);
+  uint32_t lo = (uint32_t)u, hi = (uint32_t)(u >> 32);
+  v = pair(__builtin_amdgcn_permlane16_swap(lo, lo, false, false), __builtin_amdgcn_permlane16_swap(hi, hi, false, false));
+  u = __builtin_bit_cast(uint64_t, v);
+  lo = (uint32_t)u;
+  hi = (uint32_t)(u >> 32);
+  return pair(__builtin_amdgcn_permlane32_swap(lo, lo, false, false), __builtin_amdgcn_permlane32_swap(hi, hi, false, false));
 }
 
-template <typename T>
-__device__ __forceinline__ void store8(T *p, int n, const float *v) {
-  T t[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) store_out(&t[i], v[i]);
-  if (n >= 8) {
-    __builtin_memcpy(p, t, sizeof t);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = t[i];
-  }
-}
-
-// The sum over the TPR threads that share a row, in every one of them; `part` has room for
-// the waves of the workgroup.  TPR is 64 (one wave) or the whole workgroup.
+// The sum over the TPR threads that share a row, in every one of them; TPR is 64 (one wave) or the
+// whole workgroup, whose waves leave their sums in `part` (the caller's next use is of another array).
 template <typename V, int TPR>
 __device__ __forceinline__ V row_sum(V v, V *part) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  v = wave_sum(v);
   if constexpr (TPR > 64) {
-    __syncthreads();  // the sums of the row before are read
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
     __syncthreads();
     v = part[0];
@@ -66,10 +58,11 @@ __device__ __forceinline__ V row_sum(V v, V *part) {
   return v;
 }
 
-// TPR threads a row, NV vectors of eight a thread: vector i of thread t at column 8 (t + i TPR).  The mean of
+// TPR threads a row, NV vectors of eight a thread: vector i of thread t at column 8 (t + i TPR).  Everything is
+// loaded before the sum, the weight too, so that its latency is waited for once.  The mean of
 // squares is formed in 64 bits, and h rstd and its product with w are each rounded to float, so
 // that the codes, which jump next to a border, are the same in any order of the sum.
-template <typename T, int TPR, int NV>
+template <typename T, int TPR, int NV, bool WHOLE>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rms_norm_kernel(const NormCall c) {
   constexpr int RPB = TPR >= 256 ? 1 : 256 / TPR;
   __shared__ double part[TPR > 64 ? TPR / 64 : 1];
@@ -79,20 +72,22 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rms_norm_kernel(const N
   const int d = c.d;
   const T *x = static_cast<const T *>(c.x) + row * d;
   const T *res = c.residual ? static_cast<const T *>(c.residual) + row * d : nullptr;
+  Raw8<T> xr[NV], rr[NV], wr[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int col = 8 * (t + i * TPR);
+    xr[i] = load8<T, WHOLE>(x + col, d - col);
+    if (res) rr[i] = load8<T, WHOLE>(res + col, d - col);
+    wr[i] = load8<T, WHOLE>(static_cast<const T *>(c.weight) + col, d - col);
+  }
   float h[NV][8];
   double sum = 0.0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int col = 8 * (t + i * TPR), n = d - col;
-    if (n <= 0) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[i][j] = 0.0f;
-      continue;
-    }
-    load8(x + col, n, h[i]);
+    xr[i].to(h[i]);
     if (res) {
       float r[8];
-      load8(res + col, n, r);
+      rr[i].to(r);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         h[i][j] += r[j];
@@ -101,6 +96,8 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rms_norm_kernel(const N
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum += (double)h[i][j] * (double)h[i][j];
+    const int col = 8 * (t + i * TPR);
+    if (c.h) store8<T, WHOLE>(static_cast<T *>(c.h) + row * d + col, d - col, h[i]);
   }
   sum = row_sum<double, TPR>(sum, part);
   const float rstd = (float)(1.0 / sqrt(sum / (double)d + (double)c.eps));
@@ -108,24 +105,21 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rms_norm_kernel(const N
   const int row_bytes = fp8_row_bytes(d), scale_bytes = fp8_scale_bytes(d);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int col = 8 * (t + i * TPR), n = d - col;
+    const int col = 8 * (t + i * TPR);
     float y[8];
-    if (n > 0) {
-      load8(static_cast<const T *>(c.weight) + col, n, y);
+    wr[i].to(y);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] *= h[i][j] * rstd;
-      if (c.h) store8(static_cast<T *>(c.h) + row * d + col, n, h[i]);
-      if (c.y) store8(static_cast<T *>(c.y) + row * d + col, n, y);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = 0.0f;
-    }
+    for (int j = 0; j < 8; ++j) y[j] *= h[i][j] * rstd;
+    if (c.y) store8<T, WHOLE>(static_cast<T *>(c.y) + row * d + col, d - col, y);
     if (c.y8) {
+      if (d - col < 8) {  // behind the row: zeros, whatever rstd is
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = col + j < d ? y[j] : 0.0f;
+      }
       float top = 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) top = fmaxf(top, fp8_magnitude(y[j]));
-#pragma unroll
-      for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+      top = group_reduce<16>(top, [](float a, float b) { return fmaxf(a, b); });
       const uint32_t byte = fp8_scale_byte(top);
       const float inv = fp8_inverse(byte);
       if (col < row_bytes) {
@@ -140,81 +134,125 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rms_norm_kernel(const N
   }
 }
 
-// Each workgroup takes rows b, b + blocks, ...; a thread keeps its columns' part of dw over them, and the
-// finish kernel adds the workgroups' parts in order.
-template <typename T, int TPR, int NV>
+// Each workgroup takes rows b, b + blocks, ...; a thread keeps its columns' part of dw over them. Waves with rows
+// of their own add theirs up in LDS at the end, and the finish kernel adds the workgroups' parts, all in order.
+template <typename T, int TPR, int NV, bool WHOLE>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rms_norm_backward_kernel(const NormBwdCall c,
                                                                                   float *__restrict__ parts) {
   constexpr int RPB = TPR >= 256 ? 1 : 256 / TPR;
-  __shared__ float part[TPR > 64 ? TPR / 64 : 1];
+  __shared__ float part[2][TPR > 64 ? TPR / 64 : 1];
+  __shared__ float rows_dw[RPB > 1 ? RPB - 1 : 1][RPB > 1 ? TPR * NV * 8 : 1];
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   const int d = c.d;
   float dw[NV][8];
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
-  for (int64_t row = (int64_t)blockIdx.x * RPB + sub; row < c.T; row += (int64_t)gridDim.x * RPB) {
-    const float rstd = c.rstd[row];
-    float g[NV][8], xh[NV][8], sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int col = 8 * (t + i * TPR), n = d - col;
-      if (n <= 0) continue;
-      float w[8];
-      load8(static_cast<const T *>(c.dy) + row * d + col, n, g[i]);
-      load8(static_cast<const T *>(c.h) + row * d + col, n, xh[i]);
-      load8(static_cast<const T *>(c.weight) + col, n, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        xh[i][j] *= rstd;
-        dw[i][j] += g[i][j] * xh[i][j];
-        g[i][j] *= w[j];
-        sum += g[i][j] * xh[i][j];
-      }
-    }
-    const float mean = row_sum<float, TPR>(sum, part) / (float)d;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int col = 8 * (t + i * TPR), n = d - col;
-      if (n <= 0) continue;
-      float o[8];
-      if (c.dh)
-        load8(static_cast<const T *>(c.dh) + row * d + col, n, o);
-      else
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] += rstd * (g[i][j] - xh[i][j] * mean);
-      store8(static_cast<T *>(c.dx) + row * d + col, n, o);
-    }
-  }
-  float *p = parts + ((int64_t)blockIdx.x * RPB + sub) * d;
+  Raw8<T> wr[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int col = 8 * (t + i * TPR), n = d - col;
-    if (n > 0) store8(p + col, n, dw[i]);
+    const int col = 8 * (t + i * TPR);
+    wr[i] = load8<T, WHOLE>(static_cast<const T *>(c.weight) + col, d - col);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+  }
+  int turn = 0;
+  for (int64_t row = (int64_t)blockIdx.x * RPB + sub; row < c.T; row += (int64_t)gridDim.x * RPB, turn ^= 1) {
+    const float rstd = c.rstd[row];
+    Raw8<T> gr[NV], hr[NV], ar[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = 8 * (t + i * TPR);
+      gr[i] = load8<T, WHOLE>(static_cast<const T *>(c.dy) + row * d + col, d - col);
+      hr[i] = load8<T, WHOLE>(static_cast<const T *>(c.h) + row * d + col, d - col);
+      if (c.dh) ar[i] = load8<T, WHOLE>(static_cast<const T *>(c.dh) + row * d + col, d - col);
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float g[8], xh[8], w[8];
+      gr[i].to(g);
+      hr[i].to(xh);
+      wr[i].to(w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        xh[j] *= rstd;
+        dw[i][j] += g[j] * xh[j];
+        sum += g[j] * w[j] * xh[j];
+      }
+    }
+    const float mean = row_sum<float, TPR>(sum, part[turn]) / (float)d;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float g[8], xh[8], w[8], o[8];
+      gr[i].to(g);
+      hr[i].to(xh);
+      wr[i].to(w);
+      if (c.dh) {
+        ar[i].to(o);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] += rstd * (g[j] * w[j] - xh[j] * rstd * mean);
+      const int col = 8 * (t + i * TPR);
+      store8<T, WHOLE>(static_cast<T *>(c.dx) + row * d + col, d - col, o);
+    }
+  }
+  if constexpr (RPB > 1) {
+    if (sub > 0)
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) rows_dw[sub - 1][(i * 8 + j) * TPR + t] = dw[i][j];
+    __syncthreads();
+    if (sub > 0) return;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int q = 0; q < RPB - 1; ++q) dw[i][j] += rows_dw[q][(i * 8 + j) * TPR + t];
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int col = 8 * (t + i * TPR);
+    store8<float, WHOLE>(parts + (int64_t)blockIdx.x * d + col, d - col, dw[i]);
   }
 }
 
+// 16 columns a workgroup, sixteen rows of parts at a time, eight loads of each thread in flight.
 __global__ __launch_bounds__(256) void rms_norm_dweight_kernel(const float *__restrict__ parts, int n, int d,
                                                                float *__restrict__ dweight) {
-  __shared__ float s[4][64];
-  const int col = blockIdx.x * 64 + (threadIdx.x & 63), q = threadIdx.x >> 6;
+  __shared__ float s[16][17];
+  const int q = threadIdx.x >> 4, l = threadIdx.x & 15, col = blockIdx.x * 16 + l;
   float sum = 0.0f;
-  if (col < d)
-    for (int r = q; r < n; r += 4) sum += parts[(int64_t)r * d + col];
-  s[q][threadIdx.x & 63] = sum;
+  for (int r0 = q; r0 < n; r0 += 16 * 8) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = col < d && r0 + 16 * j < n ? parts[(int64_t)(r0 + 16 * j) * d + col] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += v[j];
+  }
+  s[q][l] = sum;
   __syncthreads();
-  if (q == 0 && col < d) dweight[col] = (s[0][threadIdx.x] + s[1][threadIdx.x]) + (s[2][threadIdx.x] + s[3][threadIdx.x]);
+  if (q == 0 && col < d) {
+    for (int r = 1; r < 16; ++r) sum += s[r][l];
+    dweight[col] = sum;
+  }
 }
 
-// Threads a row and vectors a thread for rows of d values (whole blocks of 128, the 8-bit output's padding).
+// Threads a row and vectors a thread for rows of d values (whole blocks of 128, the 8-bit output's padding), and
+// whether rows are whole vectors.
 template <typename F>
-auto by_width(int d, F f) {
+void by_width(int d, F f) {
   const int vecs = fp8_row_bytes(d) / 8;
+  const auto whole = [&](auto tpr, auto nv) {
+    if (d % 8 == 0)
+      f(tpr, nv, std::true_type{});
+    else
+      f(tpr, nv, std::false_type{});
+  };
 #define MOE_WIDTH(TPR, NV) \
-  if (vecs <= TPR * NV) return f(std::integral_constant<int, TPR>{}, std::integral_constant<int, NV>{})
+  if (vecs <= TPR * NV) return whole(std::integral_constant<int, TPR>{}, std::integral_constant<int, NV>{})
   MOE_WIDTH(64, 1);
   MOE_WIDTH(64, 2);
   MOE_WIDTH(64, 4);
@@ -222,50 +260,53 @@ auto by_width(int d, F f) {
   MOE_WIDTH(256, 4);
   MOE_WIDTH(256, 8);
 #undef MOE_WIDTH
-  return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
+  whole(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
 }
 
+// Workgroups of the backward: eight rows or more for each thread's part of dw, whose
+// writing and reading again is then at most an eighth of the rows' own bytes, but enough to fill the GPU.
 int backward_blocks(int T, int d) {
-  const int rpb = by_width(d, [](auto tpr, auto) { return tpr.value >= 256 ? 1 : 256 / tpr.value; });
-  return std::min((T + rpb - 1) / rpb, 512);
+  const int rpb = fp8_row_bytes(d) / 8 <= 256 ? 4 : 1;  // rows a workgroup has at once (by_width)
+  const int all = (T + rpb - 1) / rpb;
+  return std::min(all, std::min(1024, std::max(512, all / 8)));
 }
 
 }  // namespace
 
 hipError_t launch_rms_norm(const NormCall &c, hipStream_t s) {
-  by_width(c.d, [&](auto tpr, auto nv) {
+  by_width(c.d, [&](auto tpr, auto nv, auto whole) {
     constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+    constexpr bool WHOLE = decltype(whole)::value;
     constexpr int RPB = TPR >= 256 ? 1 : 256 / TPR;
     const dim3 grid((unsigned)((c.T + RPB - 1) / RPB)), block(TPR > 256 ? TPR : 256);
     if (c.f32)
-      hipLaunchKernelGGL((rms_norm_kernel<float, TPR, NV>), grid, block, 0, s, c);
+      hipLaunchKernelGGL((rms_norm_kernel<float, TPR, NV, WHOLE>), grid, block, 0, s, c);
     else
-      hipLaunchKernelGGL((rms_norm_kernel<bf16_t, TPR, NV>), grid, block, 0, s, c);
+      hipLaunchKernelGGL((rms_norm_kernel<bf16_t, TPR, NV, WHOLE>), grid, block, 0, s, c);
   });
   return hipGetLastError();
 }
 
-size_t rms_norm_backward_workspace_bytes(int T, int d) {
-  const int rpb = by_width(d, [](auto tpr, auto) { return tpr.value >= 256 ? 1 : 256 / tpr.value; });
-  return (size_t)backward_blocks(T, d) * rpb * d * 4;
-}
+size_t rms_norm_backward_workspace_bytes(int T, int d) { return (size_t)backward_blocks(T, d) * d * 4; }
 
 hipError_t launch_rms_norm_backward(const NormBwdCall &c, void *ws, hipStream_t s) {
   const int blocks = backward_blocks(c.T, c.d);
-  int parts = blocks;
-  by_width(c.d, [&](auto tpr, auto nv) {
-    constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-    parts = blocks * (TPR >= 256 ? 1 : 256 / TPR);
-    const dim3 grid((unsigned)blocks), block(TPR > 256 ? TPR : 256);
-    if (c.f32)
-      hipLaunchKernelGGL((rms_norm_backward_kernel<float, TPR, NV>), grid, block, 0, s, c, static_cast<float *>(ws));
-    else
-      hipLaunchKernelGGL((rms_norm_backward_kernel<bf16_t, TPR, NV>), grid, block, 0, s, c, static_cast<float *>(ws));
-  });
+  if (blocks > 0)
+    by_width(c.d, [&](auto tpr, auto nv, auto whole) {
+      constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+      constexpr bool WHOLE = decltype(whole)::value;
+      const dim3 grid((unsigned)blocks), block(TPR > 256 ? TPR : 256);
+      if (c.f32)
+        hipLaunchKernelGGL((rms_norm_backward_kernel<float, TPR, NV, WHOLE>), grid, block, 0, s, c,
+                           static_cast<float *>(ws));
+      else
+        hipLaunchKernelGGL((rms_norm_backward_kernel<bf16_t, TPR, NV, WHOLE>), grid, block, 0, s, c,
+                           static_cast<float *>(ws));
+    });
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(rms_norm_dweight_kernel, dim3((unsigned)((c.d + 63) / 64)), dim3(256), 0, s,
-                     static_cast<const float *>(ws), parts, c.d, c.dweight);
+  hipLaunchKernelGGL(rms_norm_dweight_kernel, dim3((unsigned)((c.d + 15) / 16)), dim3(256), 0, s,
+                     static_cast<const float *>(ws), blocks, c.d, c.dweight);
   return hipGetLastError();
 }
 

@@ -28,13 +28,10 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const T *__restrict_
     const int64_t row = q / scale_bytes;
     const int b = (int)(q - row * scale_bytes), c0 = b * kFp8Block + l * 8;
     float v[8], top = 0.0f;
+    load8<T, false>(x + row * K + c0, K - c0).to(v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = c0 + i < K ? to_f32(x[row * K + c0 + i]) : 0.0f;
-      top = fmaxf(top, fp8_magnitude(v[i]));
-    }
-#pragma unroll
-    for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, fp8_magnitude(v[i]));
+    top = group_reduce<16>(top, [](float a, float b) { return fmaxf(a, b); });
     const uint32_t byte = fp8_scale_byte(top);
     const float inv = fp8_inverse(byte);
     if (b < blocks) {
@@ -63,9 +60,10 @@ __global__ __launch_bounds__(256) void dequantize_rows_kernel(const uint8_t *__r
                         __builtin_amdgcn_cvt_f32_fp8((int)w.x, 2), __builtin_amdgcn_cvt_f32_fp8((int)w.x, 3),
                         __builtin_amdgcn_cvt_f32_fp8((int)w.y, 0), __builtin_amdgcn_cvt_f32_fp8((int)w.y, 1),
                         __builtin_amdgcn_cvt_f32_fp8((int)w.y, 2), __builtin_amdgcn_cvt_f32_fp8((int)w.y, 3)};
+    float o[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c0 + i < K) store_out(out + row * K + c0 + i, e == 128 ? __builtin_nanf("") : ldexpf(v[i], e));
+    for (int i = 0; i < 8; ++i) o[i] = e == 128 ? __builtin_nanf("") : ldexpf(v[i], e);
+    store8<T, false>(out + row * K + c0, K - c0, o);
   }
 }
 
