@@ -723,9 +723,36 @@ moe_status check_fp8_gather(int64_t x_rows, int32_t k) {
   return MOE_OK;
 }
 
-// Workspace of the FFN in 8 bits: H's codes, then its scales.
-size_t swiglu_fp8_ws_bytes(int32_t, int64_t rows_max, int32_t, int32_t, int32_t f) {
-  return align_up((size_t)rows_max * moe::fp8_row_bytes(f)) + align_up((size_t)rows_max * moe::fp8_scale_bytes(f));
+// Whether a group can have more rows than the kernels for few take at once: its tiles then go through packed copies.
+bool fp8_large(int64_t rows_max, int32_t group_rows_max) {
+  return std::min<int64_t>(rows_max, group_rows_max) > moe::kFp8LargeTail;
+}
+
+// Workspace of the products in 8 bits: packed tiles of the rows and, for the FFN (f > 0), H in rows and in packed tiles.
+struct Fp8Layout {
+  size_t xp, xp_scale, h8, h_scale, hp, hp_scale, total;
+};
+Fp8Layout fp8_layout(int64_t rows_max, int32_t group_rows_max, int32_t k, int32_t f) {
+  Fp8Layout L{};
+  size_t o = 0;
+  auto take = [&](int64_t bytes) {
+    const size_t at = o;
+    o += align_up((size_t)bytes);
+    return at;
+  };
+  const bool large = fp8_large(rows_max, group_rows_max);
+  L.xp = take(large ? moe::fp8_packed_bytes(rows_max, k) : 0);
+  L.xp_scale = take(large ? moe::fp8_packed_scale_bytes(rows_max, k) : 0);
+  L.h8 = take(f ? rows_max * moe::fp8_row_bytes(f) : 0);
+  L.h_scale = take(f ? rows_max * moe::fp8_scale_bytes(f) : 0);
+  L.hp = take(f && large ? moe::fp8_packed_bytes(rows_max, f) : 0);
+  L.hp_scale = take(f && large ? moe::fp8_packed_scale_bytes(rows_max, f) : 0);
+  L.total = o;
+  return L;
+}
+
+size_t swiglu_fp8_ws_bytes(int32_t, int64_t rows_max, int32_t group_rows_max, int32_t d, int32_t f) {
+  return fp8_layout(rows_max, group_rows_max, d, f).total;
 }
 
 moe::Fp8GemmArgs fp8_args(int32_t G, int64_t rows_max, int32_t group_rows_max, int32_t n_out, int32_t k, const uint8_t *x8,
@@ -747,20 +774,36 @@ moe::Fp8GemmArgs fp8_args(int32_t G, int64_t rows_max, int32_t group_rows_max, i
   return a;
 }
 
+// The packed tiles of a product's rows, where a group can have that many.
+moe_status pack_fp8(moe::Fp8GemmArgs &a, void *ws, const Fp8Layout &L, hipStream_t stream) {
+  if (!fp8_large(a.rows_max, a.group_rows_max)) return MOE_OK;
+  MOE_TRY_HIP(moe::launch_fp8_pack_rows(a, at<uint8_t>(ws, L.xp), at<uint8_t>(ws, L.xp_scale), stream), "rows to tiles");
+  a.xp = at<uint8_t>(ws, L.xp);
+  a.xp_scale = at<uint8_t>(ws, L.xp_scale);
+  return MOE_OK;
+}
+
 // The FFN in 8 bits (arguments checked).
 moe_status run_swiglu_fp8(int32_t G, int64_t rows_max, int32_t group_rows_max, int32_t d, int32_t f, const uint8_t *x8,
                           const uint8_t *x_scale, const int32_t *row_index, int64_t x_rows, const int32_t *offsets,
                           const moe_fp8_matrix &gate_up, const moe_fp8_matrix &down, void *y, void *ws,
                           hipStream_t stream) {
-  uint8_t *h8 = at<uint8_t>(ws, 0), *h_scale = at<uint8_t>(ws, align_up((size_t)rows_max * moe::fp8_row_bytes(f)));
+  const Fp8Layout L = fp8_layout(rows_max, group_rows_max, d, f);
+  const bool large = fp8_large(rows_max, group_rows_max);
   moe::Fp8GemmArgs a = fp8_args(G, rows_max, group_rows_max, f, d, x8, x_scale, row_index, x_rows, offsets,
                                 gate_up.codes, gate_up.scale);
-  a.h8 = h8;
-  a.h_scale = h_scale;
+  MOE_TRY(pack_fp8(a, ws, L, stream));
+  a.h8 = at<uint8_t>(ws, L.h8);
+  a.h_scale = at<uint8_t>(ws, L.h_scale);
+  a.hp = large ? at<uint8_t>(ws, L.hp) : nullptr;
+  a.hp_scale = large ? at<uint8_t>(ws, L.hp_scale) : nullptr;
   MOE_TRY_HIP(moe::launch_fp8_gemm(a, stream), "gate_up in 8 bits");
-  a = fp8_args(G, rows_max, group_rows_max, d, f, h8, h_scale, nullptr, rows_max, offsets, down.codes, down.scale);
-  a.y = static_cast<uint16_t *>(y);
-  return hip_status(moe::launch_fp8_gemm(a, stream), "down in 8 bits");
+  moe::Fp8GemmArgs b = fp8_args(G, rows_max, group_rows_max, d, f, a.h8, a.h_scale, nullptr, rows_max, offsets, down.codes,
+                                down.scale);
+  b.xp = a.hp;
+  b.xp_scale = a.hp_scale;
+  b.y = static_cast<uint16_t *>(y);
+  return hip_status(moe::launch_fp8_gemm(b, stream), "down in 8 bits");
 }
 
 // The layer for experts [e_begin, e_end) of the routing: routing, capacity and dispatch
@@ -1805,7 +1848,7 @@ moe_status moe_rms_norm_backward(int32_t num_tokens, int32_t d_model, int32_t dt
 size_t moe_grouped_linear_fp8_workspace_size(int32_t num_groups, int64_t rows_max, int32_t group_rows_max,
                                              int32_t n_out, int32_t k) {
   if (check_fp8_shape(num_groups, n_out, k, false) != MOE_OK || check_fp8_rows(rows_max, group_rows_max) != MOE_OK) return 0;
-  return kAlign;
+  return std::max<size_t>(fp8_layout(rows_max, group_rows_max, k, 0).total, kAlign);
 }
 
 moe_status moe_grouped_linear_fp8(int32_t num_groups, int64_t rows_max, int32_t group_rows_max, int32_t n_out, int32_t k,
@@ -1830,6 +1873,7 @@ moe_status moe_grouped_linear_fp8(int32_t num_groups, int64_t rows_max, int32_t 
   moe::Fp8GemmArgs a = fp8_args(num_groups, rows_max, group_rows_max, n_out, k, x8, x_scale, row_index,
                                 row_index ? x_row_count : rows_max, group_offsets, w8, w_scale);
   a.y = static_cast<uint16_t *>(y_rows);
+  MOE_TRY(pack_fp8(a, ws, fp8_layout(rows_max, group_rows_max, k, 0), stream));
   MOE_TRY_HIP(moe::launch_fp8_gemm(a, stream), "grouped product in 8 bits");
   return ok();
 }

@@ -102,6 +102,21 @@ __device__ __forceinline__ uint32_t fp8_codes(float a, float b, float c, float d
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
 }
 
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ i32x8 fp8_operand(u32x4 lo, u32x4 hi) {
+  return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+}
+
+// What a group has of the rows, clamped to the buffers.
+__device__ __forceinline__ void fp8_group_rows(const Fp8GemmArgs &a, int g, int &begin, int &end) {
+  begin = min(max(a.offsets[g], 0), a.rows_max);
+  end = min(max(a.offsets[g + 1], begin), a.rows_max);
+}
+// Bytes of one group's codes.
+__host__ __device__ __forceinline__ int64_t fp8_group_bytes(int n_out, int k, bool swiglu) {
+  return (int64_t)((n_out + 15) / 16) * (swiglu ? 2 : 1) * fp8_blocks(k) * kFp8Tile;
+}
+
 // Eight codes as bf16, times 2^(e) for a scale 2^e given as a float: exact (bf16 has a float's exponents).
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ u32x4 fp8_to_bf16(uint32_t lo, uint32_t hi, float scale) {

@@ -11,7 +11,6 @@
 // floats, where the 8-bit instruction drops what lies 2^-14 below the largest of 16 products (1.5e-5 of a
 // sum: enough to move one code of H in two thousand).
 #include <algorithm>
-#include <climits>
 
 #include "fp8.hpp"
 #include "kernels.hpp"
@@ -19,12 +18,6 @@
 namespace moe {
 
 namespace {
-
-// What a workgroup has of its group: the rows, clamped to the buffers.
-__device__ __forceinline__ void group_rows(const Fp8GemmArgs &a, int g, int &begin, int &end) {
-  begin = min(max(a.offsets[g], 0), a.rows_max);
-  end = min(max(a.offsets[g + 1], begin), a.rows_max);
-}
 
 // Where row m0 + r of a group stands: byte offsets of its codes and scales in xres and sres, kOob past the group's
 // end and for an index outside the rows.
@@ -86,12 +79,12 @@ __global__ __launch_bounds__(64 * U * KS) void fp8_small_kernel(const Fp8GemmArg
   const int n_blocks = (a.n_out + 16 * U - 1) / (16 * U);
   const int g = blockIdx.x / n_blocks, nb = blockIdx.x - g * n_blocks;
   int begin, end;
-  group_rows(a, g, begin, end);
-  if (end - begin <= a.rows_above || end - begin > a.rows_most) return;
+  fp8_group_rows(a, g, begin, end);
+  if (begin >= end) return;
   const int kt = fp8_blocks(a.K), kp = fp8_row_bytes(a.K), ks = fp8_scale_bytes(a.K);
   const int quads = ks / 4, tb = 4 * (quads * part / KS), te = min(kt, 4 * (quads * (part + 1) / KS));
   const int unit = nb * U + u, units = (a.n_out + 15) / 16;
-  const int64_t wbytes = (int64_t)units * NB * kt * kFp8Tile;
+  const int64_t wbytes = fp8_group_bytes(a.n_out, a.K, SWIGLU);
   const rsrc_t wres = make_rsrc(a.w8 + g * wbytes, (uint32_t)wbytes);
   const uint32_t woff = unit < units ? (uint32_t)(unit * NB * kt * kFp8Tile + lane * 16) : kOob;
   const uint8_t *wscale =
@@ -244,12 +237,13 @@ __global__ __launch_bounds__(512) void fp8_medium_kernel(const Fp8GemmArgs a) {
   const int n_blocks = (a.n_out + COLS - 1) / COLS;
   const int g = blockIdx.x / n_blocks, nb = blockIdx.x - g * n_blocks;
   int begin, end;
-  group_rows(a, g, begin, end);
-  if (end - begin <= a.rows_above || end - begin > a.rows_most) return;
+  fp8_group_rows(a, g, begin, end);
+  if (a.xp) begin += fp8_large_tiles(end - begin) * kFp8LargeRows;  // the kernel for many rows has the others
+  if (begin >= end) return;
   const int kt = fp8_blocks(a.K), kp = fp8_row_bytes(a.K), ks = fp8_scale_bytes(a.K);
   const int units = (a.n_out + 15) / 16 * (SWIGLU ? 2 : 1);  // blocks of 16 weight rows
   const int unit = nb * 16 + wave * 2;
-  const int64_t wbytes = (int64_t)units * kt * kFp8Tile;
+  const int64_t wbytes = fp8_group_bytes(a.n_out, a.K, SWIGLU);
   const rsrc_t wres = make_rsrc(a.w8 + g * wbytes, (uint32_t)wbytes);
   uint32_t woff[2];
 #pragma unroll
@@ -402,14 +396,14 @@ __global__ __launch_bounds__(512) void fp8_medium_kernel(const Fp8GemmArgs a) {
 
 }  // namespace
 
-hipError_t launch_fp8_gemm(const Fp8GemmArgs &a0, hipStream_t s) {
-  Fp8GemmArgs a = a0;
-  const int most = std::min(a.group_rows_max, a.rows_max);
+hipError_t launch_fp8_gemm(const Fp8GemmArgs &a, hipStream_t s) {
   const bool swiglu = a.h8 != nullptr;
-  a.rows_above = 0;
-  a.rows_most = INT_MAX;
   auto grid = [&](int cols) { return dim3((unsigned)(a.num_groups * ((a.n_out + cols - 1) / cols))); };
-  if (most <= 16) {
+  if (a.xp) {
+    const hipError_t e = launch_fp8_gemm_large(a, s);
+    if (e != hipSuccess) return e;
+  }
+  if (std::min(a.group_rows_max, a.rows_max) <= 16) {
     if (swiglu)
       hipLaunchKernelGGL((fp8_small_kernel<true, 1, 8, 1>), grid(128), dim3(512), 0, s, a);
     else

@@ -1,0 +1,368 @@
+// Grouped products in 8 bits for groups of many rows (layouts in fp8.hpp), bound by the matrix cores.
+//
+// 256 rows x 256 weight rows a workgroup (for gate_up 128 columns of H: 16 gate and 16 up rows in turn), eight
+// waves of 128 x 64, 32x32x64 instructions with their operands' scales (the
+// blocks' scales cost nothing).  Both operands go from memory to LDS without registers, a step of 64 of K as
+// 1 KB pieces that are consecutive in memory and lie in LDS as the instruction reads them: for 16 rows, [4 chunks of
+// 16 codes][16 rows], so that sixteen lanes read 256 consecutive bytes.  The rows are copied into that
+// layout beforehand (fp8_pack_rows_kernel); H is written in it.  Four stages, three steps ahead; the
+// two waves of each SIMD take turns, one computing while the other loads and reads
+// (the bf16 kernel's schedule for groups of many rows: the same bytes and cycles a step, twice the products).
+#include <algorithm>
+
+#include "fp8.hpp"
+#include "kernels.hpp"
+
+namespace moe {
+
+namespace {
+
+constexpr int LG_TILE = kFp8LargeRows * 64;  // bytes of an operand's stage: 256 rows, 64 of K
+
+// The tiles of a group of n rows: whole ones, and a last one of more rows than the tails of another launch.
+__device__ __forceinline__ int large_tiles(const Fp8GemmArgs &a, int g) {
+  int begin, end;
+  fp8_group_rows(a, g, begin, end);
+  return fp8_large_tiles(end - begin);
+}
+
+// Tile m -> its group (-1 past the last), the group's first tile and count, and the number of all tiles; the
+// same in every lane.
+__device__ __forceinline__ void find_tile(const Fp8GemmArgs &a, int m, int &group, int &first, int &count) {
+  const int lane = threadIdx.x & 63;
+  int base = 0;
+  group = -1;
+  first = count = 0;
+  for (int g0 = 0; g0 < a.num_groups; g0 += 64) {
+    const int mine = g0 + lane < a.num_groups ? large_tiles(a, g0 + lane) : 0;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(incl, o, 64);
+      if (lane >= o) incl += v;
+    }
+    const uint64_t hit = __ballot(base + incl > m);
+    if (hit) {
+      const int l = __ffsll((unsigned long long)hit) - 1;
+      group = __builtin_amdgcn_readfirstlane(g0 + l);
+      first = __builtin_amdgcn_readfirstlane(base + __shfl(incl - mine, l, 64));
+      count = __builtin_amdgcn_readfirstlane(__shfl(mine, l, 64));
+      return;
+    }
+    base += __shfl(incl, 63, 64);
+  }
+}
+
+__device__ __forceinline__ int all_tiles(const Fp8GemmArgs &a) {
+  int sum = 0;
+  for (int g = threadIdx.x & 63; g < a.num_groups; g += 64) sum += large_tiles(a, g);
+  return __builtin_amdgcn_readfirstlane(group_reduce<64>(sum, [](int x, int y) { return x + y; }));
+}
+
+__device__ __forceinline__ f32x16 mfma_fp8_32(i32x8 a, i32x8 b, f32x16 c, uint32_t sa, uint32_t sb, int byte) {
+  switch (byte) {
+    case 0: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, (int)sa, 0, (int)sb);
+    case 1: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 1, (int)sa, 1, (int)sb);
+    case 2: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 2, (int)sa, 2, (int)sb);
+    default: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 3, (int)sa, 3, (int)sb);
+  }
+}
+
+template <bool SWIGLU>
+__global__ __launch_bounds__(512, 1) void fp8_large_kernel(const Fp8GemmArgs a, int n_tiles) {
+  constexpr int NBUF = 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t sA0[LG_TILE], sA1[LG_TILE], sA2[LG_TILE], sA3[LG_TILE];
+  __shared__ __attribute__((aligned(1024))) uint8_t sB0[LG_TILE], sB1[LG_TILE], sB2[LG_TILE], sB3[LG_TILE];
+  auto bufA = [&](int b) -> uint8_t * { return b == 0 ? sA0 : b == 1 ? sA1 : b == 2 ? sA2 : sA3; };
+  auto bufB = [&](int b) -> uint8_t * { return b == 0 ? sB0 : b == 1 ? sB1 : b == 2 ? sB2 : sB3; };
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / 4, wn = wave % 4, lr = lane & 31, lh = lane >> 5;
+  // (offsets that decrease could count rows twice: no tile past those that the packed copies have room for)
+  const int tiles_max = gridDim.x / n_tiles, tiles = min(all_tiles(a), tiles_max), blocks = tiles * n_tiles;
+  if ((int)blockIdx.x >= blocks) return;
+  const int lin = xcd_remap(blockIdx.x, blocks);
+  int g, mt_first, mt_count;
+  find_tile(a, lin / n_tiles, g, mt_first, mt_count);
+  if (g < 0) return;
+  const int local = lin - mt_first * n_tiles;
+  int begin, end;
+  fp8_group_rows(a, g, begin, end);
+  int mt, nt;
+  if (end - begin <= (SWIGLU ? 2 : 1) * a.n_out) {  // the weights are larger: their tile outermost
+    nt = local / mt_count;
+    mt = local - nt * mt_count;
+  } else {  // bands of four row tiles, weight tile outer within a band
+    constexpr int BAND = 4;
+    const int band = local / (BAND * n_tiles), r = local - band * BAND * n_tiles;
+    const int bm = min(BAND, mt_count - band * BAND);
+    nt = r / bm;
+    mt = band * BAND + (r - nt * bm);
+  }
+  const int m0 = begin + mt * kFp8LargeRows, rows = min(kFp8LargeRows, end - m0), m_tile = mt_first + mt;
+  if (m_tile >= tiles_max) return;
+  const int kt = fp8_blocks(a.K), nk = 2 * kt, ks = fp8_scale_bytes(a.K);
+  const int64_t abytes = (int64_t)kFp8LargeRows * kt * kFp8Block;
+  const int64_t wbytes = fp8_group_bytes(a.n_out, a.K, SWIGLU);
+  const rsrc_t ares = make_rsrc(a.xp + m_tile * abytes, (uint32_t)abytes);
+  const rsrc_t wres = make_rsrc(a.w8 + g * wbytes, (uint32_t)wbytes);
+  const rsrc_t sres = make_rsrc(a.xp_scale + (int64_t)m_tile * kFp8LargeRows * ks, (uint32_t)(kFp8LargeRows * ks));
+  // this wave's pieces of a stage: 16-row blocks 2 wave and 2 wave + 1 of both operands
+  uint32_t aoff[2], boff[2];
+  const uint32_t stride = (uint32_t)kt * kFp8Tile;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    aoff[i] = (uint32_t)(2 * wave + i) * stride + (uint32_t)lane * 16u;
+    const int64_t w = (int64_t)(nt * 16 + 2 * wave + i) * stride;
+    boff[i] = w < wbytes ? (uint32_t)w + (uint32_t)lane * 16u : kOob;
+  }
+  auto issue = [&](int s, int b) {
+    const uint32_t k = (uint32_t)s * 1024u;
+    const bool in = s < nk;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      buf_ld16_lds(ares, in ? aoff[i] + k : kOob, bufA(b) + (2 * wave + i) * 1024);
+      buf_ld16_lds(wres, in && boff[i] != kOob ? boff[i] + k : kOob, bufB(b) + (2 * wave + i) * 1024);
+    }
+  };
+  const int sblocks = fp8_blocks(a.n_out);
+  const uint8_t *wscale = a.w_scale + ((int64_t)g * sblocks + (SWIGLU ? nt : min(nt * 2 + wn / 2, sblocks - 1))) *
+                                          (SWIGLU ? 2 : 1) * ks;
+  uint32_t sx[4], sw[2];
+  auto load_scales = [&](int q) {  // four blocks of K: eight steps
+    const int left = kt - 4 * q;
+    const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      sx[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
+          sres, left > 0 ? (uint32_t)(q * kFp8LargeRows + wm * 128 + i * 32 + lr) * 4u : kOob, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      sw[j] = *reinterpret_cast<const uint32_t *>(wscale + (SWIGLU ? j * ks : 0) + (left > 0 ? 4 * q : 0)) & keep;
+  };
+
+  f32x16 acc[4][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
+  // this lane's 32 codes of a row of block blk: chunks 2 lh and 2 lh + 1
+  const int at = (2 * lh) * 256 + (lane & 15) * 16, half = (lane >> 4) & 1;
+  {
+    // A wave in mem(s) issues step s + 3 and completes its own loads of step s + 1, before the barrier that
+    // precedes every read of them; a stage is refilled only after the barrier that follows both groups' reads.
+    const bool second = wave >= 4;
+    u32x4 af[4][2], bf[2][2];
+    uint32_t cx[4], cw[2];
+    auto mem = [&](int s, int b) {
+      issue(s + 3, (b + 3) % NBUF);
+      asm volatile("s_waitcnt vmcnt(8)" ::: "memory");  // the two younger steps' may stay in flight
+      const uint8_t *la = bufA(b % NBUF), *lb = bufB(b % NBUF);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint8_t *p = la + (wm * 8 + i * 2 + half) * 1024 + at;
+        af[i][0] = *reinterpret_cast<const u32x4 *>(p);
+        af[i][1] = *reinterpret_cast<const u32x4 *>(p + 256);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint8_t *p = lb + (wn * 4 + (SWIGLU ? 2 * half + j : 2 * j + half)) * 1024 + at;
+        bf[j][0] = *reinterpret_cast<const u32x4 *>(p);
+        bf[j][1] = *reinterpret_cast<const u32x4 *>(p + 256);
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    };
+    auto comp = [&](int b) {
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = mfma_fp8_32(fp8_operand(bf[j][0], bf[j][1]), fp8_operand(af[i][0], af[i][1]), acc[i][j], cw[j], cx[i],
+                                  b / 2);
+      __builtin_amdgcn_s_setprio(0);
+    };
+    auto bar = [&]() {
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto next_scales = [&](int q) {  // those of the eight steps that begin; the following ones are loaded
+#pragma unroll
+      for (int i = 0; i < 4; ++i) cx[i] = sx[i];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) cw[j] = sw[j];
+      load_scales(q + 1);
+    };
+    load_scales(0);
+#pragma unroll
+    for (int b = 0; b < 3; ++b) issue(b, b);
+    asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+    bar();
+    if (second) bar();
+    int s0 = 0;
+    for (; s0 + 8 <= nk; s0 += 8) {
+      next_scales(s0 / 8);
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        mem(s0 + b, b);
+        bar();
+        comp(b);
+        bar();
+      }
+    }
+    if (s0 < nk) {
+      next_scales(s0 / 8);
+#pragma unroll
+      for (int b = 0; b < 7; ++b) {
+        if (s0 + b >= nk) break;
+        mem(s0 + b, b);
+        bar();
+        comp(b);
+        bar();
+      }
+    }
+    if (!second) bar();
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no LDS write may outlive the block
+  __syncthreads();
+
+  // Block (i, j): lane l holds row wm * 128 + i * 32 + l % 32 and, per q = 0..3, columns 8 q + 4 (l / 32) .. + 3 of its 32.
+  if constexpr (SWIGLU) {
+    float *tops = reinterpret_cast<float *>(sB0);  // [4 waves of columns][256 rows]
+    float top[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      top[i] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        acc[i][0][e] = silu_f32(acc[i][0][e]) * acc[i][1][e];
+        top[i] = fmaxf(top[i], fp8_magnitude(acc[i][0][e]));
+      }
+      top[i] = fmaxf(top[i], __shfl_xor(top[i], 32, 64));
+      if (lh == 0) tops[wn * 256 + wm * 128 + i * 32 + lr] = top[i];
+    }
+    __syncthreads();
+    // the tile's 256 x 128 codes in H's packed layout: 16-row blocks' first KB (columns below 64) in sA0, second in sA1
+    const int hs = fp8_scale_bytes(a.n_out), ht = fp8_blocks(a.n_out);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = wm * 128 + i * 32 + lr;
+      const float t = fmaxf(fmaxf(tops[row], tops[256 + row]), fmaxf(tops[512 + row], tops[768 + row]));
+      const uint32_t byte = fp8_scale_byte(t);
+      const float inv = fp8_inverse(byte);
+      uint8_t *o = (wn < 2 ? sA0 : sA1) + (row >> 4) * 1024 + (wn & 1) * 512 + (row & 15) * 16 + lh * 4;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint32_t *>(o + (q >> 1) * 256 + (q & 1) * 8) =
+            fp8_codes(acc[i][0][4 * q] * inv, acc[i][0][4 * q + 1] * inv, acc[i][0][4 * q + 2] * inv,
+                      acc[i][0][4 * q + 3] * inv);
+      if (wn == 0 && lh == 0)
+        a.hp_scale[(int64_t)m_tile * kFp8LargeRows * hs + ((nt / 4) * kFp8LargeRows + row) * 4 + nt % 4] = (uint8_t)byte;
+    }
+    __syncthreads();
+    uint8_t *hp = a.hp + ((int64_t)m_tile * 16 * ht + nt) * kFp8Tile;
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const int q = threadIdx.x + 512 * v;  // 16-byte piece of the 16 KB
+        stg16(hp + (int64_t)(q >> 6) * ht * kFp8Tile + p * 1024 + (q & 63) * 16,
+              *reinterpret_cast<const u32x4 *>((p ? sA1 : sA0) + q * 16));
+      }
+  } else {
+    // bf16: each wave's 128 rows x 64 columns through its own 16 KB, 128-byte rows, 16-byte chunk c of row r at
+    // c ^ ((r >> 1) & 7), out as whole pieces along the rows
+    uint8_t *stage = wave < 4 ? bufA(wave) : bufB(wave - 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = i * 32 + lr;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint2 *>(stage + row * 128 + (((j * 4 + q) ^ ((row >> 1) & 7)) << 4) + lh * 8) =
+              uint2{pack_bf16x2(acc[i][j][4 * q], acc[i][j][4 * q + 1]), pack_bf16x2(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3])};
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    const int c = lane & 7, col = nt * 256 + wn * 64 + c * 8;
+#pragma unroll
+    for (int it = 0; it < 16; ++it) {
+      const int row = it * 8 + (lane >> 3), grow = wm * 128 + row;
+      const u32x4 v = *reinterpret_cast<const u32x4 *>(stage + row * 128 + ((c ^ ((row >> 1) & 7)) << 4));
+      if (grow >= rows) continue;
+      bf16_t *o = a.y + (int64_t)(m0 + grow) * a.n_out + col;
+      if (col + 8 <= a.n_out) {
+        *reinterpret_cast<u32x4_any *>(o) = v;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (col + e < a.n_out) o[e] = (bf16_t)(v[e / 2] >> (16 * (e % 2)));
+      }
+    }
+  }
+}
+
+// The rows of the tiles, and their scales as [4 blocks of K][256 rows] words, for fp8_large_kernel: one
+// workgroup a tile and block of 128 of K, whole lines of the rows in.
+__global__ __launch_bounds__(256) void fp8_pack_rows_kernel(const Fp8GemmArgs a, uint8_t *__restrict__ xp,
+                                                            uint8_t *__restrict__ xp_scale) {
+  const int kt = fp8_blocks(a.K), kp = fp8_row_bytes(a.K), ks = fp8_scale_bytes(a.K);
+  const int m_tile = blockIdx.x / kt, b = blockIdx.x - m_tile * kt;
+  int g, first, count, begin, end;
+  find_tile(a, m_tile, g, first, count);
+  if (g < 0) return;
+  fp8_group_rows(a, g, begin, end);
+  const int m0 = begin + (m_tile - first) * kFp8LargeRows;
+  auto source = [&](int r) -> int64_t {  // -1: zeros
+    if (m0 + r >= end) return -1;
+    if (!a.row_index) return m0 + r;
+    const int s = a.row_index[m0 + r];
+    return (uint32_t)s < (uint32_t)a.x_rows ? s : -1;
+  };
+  u32x4 v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int q = threadIdx.x + 256 * i;
+    const int64_t s = source(q >> 3);
+    v[i] = u32x4{0u, 0u, 0u, 0u};
+    if (s >= 0) v[i] = ldg16(a.x8 + s * kp + b * 128 + (q & 7) * 16);
+  }
+  uint8_t *o = xp + ((int64_t)m_tile * 16 * kt + b) * kFp8Tile;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int q = threadIdx.x + 256 * i, r = q >> 3, c = q & 7;
+    stg16(o + (int64_t)(r >> 4) * kt * kFp8Tile + c * 256 + (r & 15) * 16, v[i]);
+  }
+  if (b % 4 == 0) {
+    const int64_t s = source(threadIdx.x);
+    const int left = kt - b;
+    const uint32_t keep = left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
+    const uint32_t w = s >= 0 ? *reinterpret_cast<const uint32_t *>(a.x_scale + s * ks + b) & keep : 0u;
+    reinterpret_cast<uint32_t *>(xp_scale)[((int64_t)m_tile * (ks / 4) + b / 4) * kFp8LargeRows + threadIdx.x] = w;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_fp8_pack_rows(const Fp8GemmArgs &a, uint8_t *xp, uint8_t *xp_scale, hipStream_t s) {
+  const int64_t grid = fp8_large_tiles_max(a.rows_max) * fp8_blocks(a.K);
+  if (grid == 0) return hipSuccess;
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(fp8_pack_rows_kernel, dim3((unsigned)grid), dim3(256), 0, s, a, xp, xp_scale);
+  return hipGetLastError();
+}
+
+hipError_t launch_fp8_gemm_large(const Fp8GemmArgs &a, hipStream_t s) {
+  const bool swiglu = a.hp != nullptr;
+  const int n_tiles = (a.n_out + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256);
+  const int64_t grid = fp8_large_tiles_max(a.rows_max) * n_tiles;
+  if (grid == 0) return hipSuccess;
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  if (swiglu)
+    hipLaunchKernelGGL((fp8_large_kernel<true>), dim3((unsigned)grid), dim3(512), 0, s, a, n_tiles);
+  else
+    hipLaunchKernelGGL((fp8_large_kernel<false>), dim3((unsigned)grid), dim3(512), 0, s, a, n_tiles);
+  return hipGetLastError();
+}
+
+}  // namespace moe

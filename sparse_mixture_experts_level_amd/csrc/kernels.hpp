@@ -241,9 +241,26 @@ struct Fp8GemmArgs {
   uint16_t *y;
   uint8_t *h8, *h_scale;
   int num_groups, rows_max, group_rows_max, x_rows, n_out, K;
-  int rows_above, rows_most;  // set by the launch: groups of more rows than this, and of at most these
+  // Groups that can have more rows than kFp8LargeTail: the rows of whole tiles of kFp8LargeRows, and of a last one of
+  // more than kFp8LargeTail, go through a kernel for many rows, which reads them (and writes H) in packed
+  // tiles of fp8_packed_bytes(); xp and hp are NULL where no group can.
+  const uint8_t *xp, *xp_scale;
+  uint8_t *hp, *hp_scale;
 };
+constexpr int kFp8LargeRows = 256, kFp8LargeTail = 128;
+__host__ __device__ inline int fp8_large_tiles(int rows) {
+  return rows / kFp8LargeRows + (rows % kFp8LargeRows > kFp8LargeTail ? 1 : 0);
+}
+// Bounds on the tiles of rows in all (each has more than kFp8LargeTail), and their bytes: codes, scales.
+inline int64_t fp8_large_tiles_max(int64_t rows) { return rows / (kFp8LargeTail + 1); }
+inline int64_t fp8_packed_bytes(int64_t rows, int k) { return fp8_large_tiles_max(rows) * kFp8LargeRows * fp8_row_bytes(k); }
+inline int64_t fp8_packed_scale_bytes(int64_t rows, int k) {
+  return fp8_large_tiles_max(rows) * kFp8LargeRows * fp8_scale_bytes(k);
+}
+// x8 (through row_index) and its scales to packed tiles.
+hipError_t launch_fp8_pack_rows(const Fp8GemmArgs &a, uint8_t *xp, uint8_t *xp_scale, hipStream_t s);
 hipError_t launch_fp8_gemm(const Fp8GemmArgs &a, hipStream_t s);
+hipError_t launch_fp8_gemm_large(const Fp8GemmArgs &a, hipStream_t s);  // its tiles alone
 
 // ---- root-mean-square norm (norm.hip)
 struct NormCall {

@@ -150,9 +150,7 @@ hipError_t launch_dequantize_rows(const uint8_t *codes, const uint8_t *scale, in
   return hipGetLastError();
 }
 
-int64_t fp8_weights_bytes(int n_out, int K, bool swiglu) {
-  return (int64_t)((n_out + 15) / 16) * (swiglu ? 2 : 1) * fp8_blocks(K) * kFp8Tile;
-}
+int64_t fp8_weights_bytes(int n_out, int K, bool swiglu) { return fp8_group_bytes(n_out, K, swiglu); }
 int64_t fp8_weight_scales_bytes(int n_out, int K, bool swiglu) {
   return (int64_t)fp8_blocks(n_out) * (swiglu ? 2 : 1) * fp8_scale_bytes(K);
 }
