@@ -107,6 +107,12 @@ __device__ __forceinline__ i32x8 fp8_operand(u32x4 lo, u32x4 hi) {
   return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
+// A word at an address that is the same in every lane, by the scalar unit (the compiler takes the vector path for memory
+// that it cannot prove unwritten).
+__device__ __forceinline__ uint32_t scalar_load(const uint8_t *p) {
+  return *reinterpret_cast<const __attribute__((address_space(4))) uint32_t *>(reinterpret_cast<uintptr_t>(p));
+}
+
 // What a group has of the rows, clamped to the buffers.
 __device__ __forceinline__ void fp8_group_rows(const Fp8GemmArgs &a, int g, int &begin, int &end) {
   begin = min(max(a.offsets[g], 0), a.rows_max);

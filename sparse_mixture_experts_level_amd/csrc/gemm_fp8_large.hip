@@ -44,9 +44,9 @@ __device__ __forceinline__ void find_tile(const Fp8GemmArgs &a, int m, int &grou
     const uint64_t hit = __ballot(base + incl > m);
     if (hit) {
       const int l = __ffsll((unsigned long long)hit) - 1;
-      group = __builtin_amdgcn_readfirstlane(g0 + l);
-      first = __builtin_amdgcn_readfirstlane(base + __shfl(incl - mine, l, 64));
-      count = __builtin_amdgcn_readfirstlane(__shfl(mine, l, 64));
+      group = g0 + l;
+      first = base + __shfl(incl - mine, l, 64);
+      count = __shfl(mine, l, 64);
       return;
     }
     base += __shfl(incl, 63, 64);
@@ -84,9 +84,15 @@ __global__ __launch_bounds__(512, 1) void fp8_large_kernel(const Fp8GemmArgs a, 
   int g, mt_first, mt_count;
   find_tile(a, lin / n_tiles, g, mt_first, mt_count);
   if (g < 0) return;
+  g = __builtin_amdgcn_readfirstlane(g);
+  mt_first = __builtin_amdgcn_readfirstlane(mt_first);
+  mt_count = __builtin_amdgcn_readfirstlane(mt_count);
   const int local = lin - mt_first * n_tiles;
   int begin, end;
   fp8_group_rows(a, g, begin, end);
+  // equal in every lane: kept, with all that derives from them, in scalar registers
+  begin = __builtin_amdgcn_readfirstlane(begin);
+  end = __builtin_amdgcn_readfirstlane(end);
   int mt, nt;
   if (end - begin <= (SWIGLU ? 2 : 1) * a.n_out) {  // the weights are larger: their tile outermost
     nt = local / mt_count;
@@ -98,6 +104,8 @@ __global__ __launch_bounds__(512, 1) void fp8_large_kernel(const Fp8GemmArgs a, 
     nt = r / bm;
     mt = band * BAND + (r - nt * bm);
   }
+  mt = __builtin_amdgcn_readfirstlane(mt);
+  nt = __builtin_amdgcn_readfirstlane(nt);
   const int m0 = begin + mt * kFp8LargeRows, rows = min(kFp8LargeRows, end - m0), m_tile = mt_first + mt;
   if (m_tile >= tiles_max) return;
   const int kt = fp8_blocks(a.K), nk = 2 * kt, ks = fp8_scale_bytes(a.K);
@@ -128,16 +136,14 @@ __global__ __launch_bounds__(512, 1) void fp8_large_kernel(const Fp8GemmArgs a, 
   const uint8_t *wscale = a.w_scale + ((int64_t)g * sblocks + (SWIGLU ? nt : min(nt * 2 + wn / 2, sblocks - 1))) *
                                           (SWIGLU ? 2 : 1) * ks;
   uint32_t sx[4], sw[2];
-  auto load_scales = [&](int q) {  // four blocks of K: eight steps
-    const int left = kt - 4 * q;
-    const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+  // four blocks of K, eight steps; past K zeros, or the last ones again
+  auto load_scales = [&](int q) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       sx[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
-          sres, left > 0 ? (uint32_t)(q * kFp8LargeRows + wm * 128 + i * 32 + lr) * 4u : kOob, 0, 0);
+          sres, (uint32_t)(q * kFp8LargeRows + wm * 128 + i * 32 + lr) * 4u, 0, 0);
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      sw[j] = *reinterpret_cast<const uint32_t *>(wscale + (SWIGLU ? j * ks : 0) + (left > 0 ? 4 * q : 0)) & keep;
+    for (int j = 0; j < 2; ++j) sw[j] = scalar_load(wscale + (SWIGLU ? j * ks : 0) + min(4 * q, ks - 4));
   };
 
   f32x16 acc[4][2];
@@ -145,8 +151,11 @@ __global__ __launch_bounds__(512, 1) void fp8_large_kernel(const Fp8GemmArgs a, 
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
-  // this lane's 32 codes of a row of block blk: chunks 2 lh and 2 lh + 1
-  const int at = (2 * lh) * 256 + (lane & 15) * 16, half = (lane >> 4) & 1;
+  // This lane's 32 codes of a row, chunks 2 lh and 2 lh + 1, in the first of the wave's row and weight blocks (one offset
+  // and constants from there: with the sums formed anew for each read the compiler lost track of which
+  // stage a read is of, and waited for every load in flight).
+  const int half = (lane >> 4) & 1, at = (2 * lh) * 256 + (lane & 15) * 16;
+  const int a_at = (wm * 8 + half) * 1024 + at, b_at = (wn * 4 + (SWIGLU ? 2 : 1) * half) * 1024 + at;
   {
     // A wave in mem(s) issues step s + 3 and completes its own loads of step s + 1, before the barrier that
     // precedes every read of them; a stage is refilled only after the barrier that follows both groups' reads.
@@ -157,17 +166,16 @@ __global__ __launch_bounds__(512, 1) void fp8_large_kernel(const Fp8GemmArgs a, 
       issue(s + 3, (b + 3) % NBUF);
       asm volatile("s_waitcnt vmcnt(8)" ::: "memory");  // the two younger steps' may stay in flight
       const uint8_t *la = bufA(b % NBUF), *lb = bufB(b % NBUF);
+      const uint8_t *pa = la + a_at, *pb = lb + b_at;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint8_t *p = la + (wm * 8 + i * 2 + half) * 1024 + at;
-        af[i][0] = *reinterpret_cast<const u32x4 *>(p);
-        af[i][1] = *reinterpret_cast<const u32x4 *>(p + 256);
+        af[i][0] = *reinterpret_cast<const u32x4 *>(pa + i * 2048);
+        af[i][1] = *reinterpret_cast<const u32x4 *>(pa + i * 2048 + 256);
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const uint8_t *p = lb + (wn * 4 + (SWIGLU ? 2 * half + j : 2 * j + half)) * 1024 + at;
-        bf[j][0] = *reinterpret_cast<const u32x4 *>(p);
-        bf[j][1] = *reinterpret_cast<const u32x4 *>(p + 256);
+        bf[j][0] = *reinterpret_cast<const u32x4 *>(pb + j * (SWIGLU ? 1024 : 2048));
+        bf[j][1] = *reinterpret_cast<const u32x4 *>(pb + j * (SWIGLU ? 1024 : 2048) + 256);
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     };
@@ -335,9 +343,7 @@ __global__ __launch_bounds__(256) void fp8_pack_rows_kernel(const Fp8GemmArgs a,
   }
   if (b % 4 == 0) {
     const int64_t s = source(threadIdx.x);
-    const int left = kt - b;
-    const uint32_t keep = left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
-    const uint32_t w = s >= 0 ? *reinterpret_cast<const uint32_t *>(a.x_scale + s * ks + b) & keep : 0u;
+    const uint32_t w = s >= 0 ? *reinterpret_cast<const uint32_t *>(a.x_scale + s * ks + b) : 0u;
     reinterpret_cast<uint32_t *>(xp_scale)[((int64_t)m_tile * (ks / 4) + b / 4) * kFp8LargeRows + threadIdx.x] = w;
   }
 }
