@@ -725,7 +725,7 @@ moe_status check_fp8_gather(int64_t x_rows, int32_t k) {
 
 // Whether a group can have more rows than the kernels for few take at once: its tiles then go through packed copies.
 bool fp8_large(int64_t rows_max, int32_t group_rows_max) {
-  return std::min<int64_t>(rows_max, group_rows_max) > moe::kFp8LargeTail;
+  return std::min<int64_t>(rows_max, group_rows_max) > moe::kFp8FewRows;
 }
 
 // Workspace of the products in 8 bits: packed tiles of the rows and, for the FFN (f > 0), H in rows and in packed tiles.

@@ -62,19 +62,23 @@ __device__ __forceinline__ void store_y(const Fp8GemmArgs &a, f32x4 v, int64_t r
   }
 }
 
-// Few rows: 16 MS of them at a time, one block after the other.  A workgroup has 16 U output columns; each wave 16
+// The compiler sinks conversions to their uses, past the loads that refill their operands' registers, which would
+// then get other registers and be copied after a wait: this keeps a value where it is formed.
+__device__ __forceinline__ void formed_here(u32x4 &v) { asm volatile("" : "+v"(v)); }
+
+// Few rows: 16 of them at a time, one block after the other.  A workgroup has 16 U output columns; each wave 16
 // of them (for gate_up the 16 gate and the 16 up rows) and one of KS parts of K, whose sums the first
-// part's waves add in order.  Rows are read from the caches in the operand layout, with the weights: no
-// LDS, no barrier, R steps of 128 in flight in registers.  The weights are the
+// part's waves add in order.  Rows are read from the caches in the operand layout, two steps ahead, with the weights,
+// R steps of 128 ahead, all in registers: no LDS, no barrier.  The weights are the
 // matrix instruction's first operand, so that a lane holds four consecutive columns of one row.
-template <bool SWIGLU, int MS, int U, int KS>
+template <bool SWIGLU, int U, int KS>
 __global__ __launch_bounds__(64 * U * KS) void fp8_small_kernel(const Fp8GemmArgs a) {
-  constexpr int NB = SWIGLU ? 2 : 1;
-  constexpr int R = SWIGLU || MS > 1 ? 4 : 8;
+  constexpr int NB = SWIGLU ? 2 : 1, R = SWIGLU ? 4 : 8, XR = 2;
   static_assert(!SWIGLU || U == 8, "a block of H's columns a workgroup");
-  __shared__ float tops[SWIGLU ? 8 : 1][16 * MS];
-  __shared__ f32x4 parts[KS > 1 ? (KS - 1) * U * MS * NB * 64 : 1];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lr = lane & 15, lg = lane >> 4;
+  __shared__ float tops[SWIGLU ? 8 : 1][16];
+  __shared__ f32x4 parts[KS > 1 ? (KS - 1) * U * NB * 64 : 1];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lr = lane & 15,
+            lg = lane >> 4;
   const int u = wave % U, part = wave / U;
   const int n_blocks = (a.n_out + 16 * U - 1) / (16 * U);
   const int g = blockIdx.x / n_blocks, nb = blockIdx.x - g * n_blocks;
@@ -87,78 +91,74 @@ __global__ __launch_bounds__(64 * U * KS) void fp8_small_kernel(const Fp8GemmArg
   const int64_t wbytes = fp8_group_bytes(a.n_out, a.K, SWIGLU);
   const rsrc_t wres = make_rsrc(a.w8 + g * wbytes, (uint32_t)wbytes);
   const uint32_t woff = unit < units ? (uint32_t)(unit * NB * kt * kFp8Tile + lane * 16) : kOob;
-  const uint8_t *wscale =
-      a.w_scale + ((int64_t)g * fp8_blocks(a.n_out) + __builtin_amdgcn_readfirstlane(min(unit, units - 1) / 8)) * NB * ks;
-  for (int m0 = begin; m0 < end; m0 += 16 * MS) {
-    const Fp8Rows rows(a, m0, min(16 * MS, end - m0));
-    uint32_t xoff[MS], soff[MS];
-#pragma unroll
-    for (int i = 0; i < MS; ++i) {
-      const uint32_t src = rows.row(a, m0, i * 16 + lr, m0 + i * 16 + lr < end);
-      xoff[i] = src != kOob ? src * (uint32_t)kp + (uint32_t)lg * 16u : kOob;
-      soff[i] = src != kOob ? src * (uint32_t)ks : kOob;
-    }
-    u32x4 w[R][NB][2], x[R][MS][2];
-    uint32_t sx[R / 4][MS], sw[R / 4][NB];
-    auto load = [&](int j, int t) {  // steps past the part's end read zeros
-      const bool in = t < te;
+  const uint8_t *wscale = a.w_scale + ((int64_t)g * fp8_blocks(a.n_out) + min(unit, units - 1) / 8) * NB * ks;
+  for (int m0 = begin; m0 < end; m0 += 16) {
+    u32x4 w[R][NB][2], x[XR][2];
+    uint32_t sx, nx, sw[NB], nw[NB];
+    auto load_w = [&](int j, int t) {  // steps past the part's end read zeros
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const uint32_t o = in && woff != kOob ? woff + (uint32_t)((b * kt + t) * kFp8Tile) : kOob;
+        const uint32_t o = t < te && woff != kOob ? woff + (uint32_t)((b * kt + t) * kFp8Tile) : kOob;
         w[j][b][0] = buf_ld16_nt(wres, o);
         w[j][b][1] = buf_ld16_nt(wres, o == kOob ? kOob : o + 1024u);
       }
-#pragma unroll
-      for (int i = 0; i < MS; ++i) {
-        const uint32_t o = in && xoff[i] != kOob ? xoff[i] + (uint32_t)t * 128u : kOob;
-        x[j][i][0] = buf_ld16(rows.xres, o);
-        x[j][i][1] = buf_ld16(rows.xres, o == kOob ? kOob : o + 64u);
-      }
     };
-    auto load_scales = [&](int q, int t) {
-      const int left = kt - t;  // blocks that exist: the padding's scales are not looked at
-      const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
 #pragma unroll
-      for (int i = 0; i < MS; ++i)
-        sx[q][i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
-                       rows.sres, soff[i] == kOob || left <= 0 ? kOob : soff[i] + (uint32_t)t, 0, 0) & keep;
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-        sw[q][b] = *reinterpret_cast<const uint32_t *>(wscale + b * ks + (left <= 0 ? 0 : t)) & keep;
+    for (int j = 0; j < R; ++j) load_w(j, tb + j);
+    const Fp8Rows rows(a, m0, min(16, end - m0));
+    const uint32_t src = rows.row(a, m0, lr, m0 + lr < end);
+    const uint32_t xoff = src != kOob ? src * (uint32_t)kp + (uint32_t)lg * 16u : kOob;
+    const uint32_t soff = src != kOob ? src * (uint32_t)ks : kOob;
+    auto load_x = [&](int j, int t) {
+      const uint32_t o = t < te && xoff != kOob ? xoff + (uint32_t)t * 128u : kOob;
+      x[j][0] = buf_ld16(rows.xres, o);
+      x[j][1] = buf_ld16(rows.xres, o == kOob ? kOob : o + 64u);
     };
-    f32x4 acc[MS][NB];
+    auto load_scales = [&](int t) {  // of four steps; past K those of the last four again (their codes are zeros)
+      const int at = min(t, ks - 4);
+      nx = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rows.sres, soff == kOob ? kOob : soff + (uint32_t)at, 0, 0);
 #pragma unroll
-    for (int i = 0; i < MS; ++i)
+      for (int b = 0; b < NB; ++b) nw[b] = scalar_load(wscale + b * ks + at);
+    };
+    load_scales(tb);
 #pragma unroll
-      for (int b = 0; b < NB; ++b) acc[i][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < XR; ++j) load_x(j, tb + j);
+    // All of the first loads, by a wait that the compiler counts: it would otherwise take the loop's entry, where few
+    // loads follow those of step 0, for the rule, and wait for nearly all in flight on every trip.
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+    f32x4 acc[NB];
 #pragma unroll
-    for (int j = 0; j < R; ++j) load(j, tb + j);
-#pragma unroll
-    for (int q = 0; q < R / 4; ++q) load_scales(q, tb + 4 * q);
+    for (int b = 0; b < NB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
     for (int t0 = tb; t0 < te; t0 += R) {
       auto step = [&](auto jc) {
-        constexpr int J = decltype(jc)::value, Q = J / 4, S = J % 4;
-        float fx[MS], fw[NB];
+        constexpr int J = decltype(jc)::value, S = J % 4;
+        const int t = t0 + J;
+        if constexpr (S == 0) {
+          const int left = kt - t;  // blocks that exist: the padding's scales are not looked at
+          const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+          sx = nx & keep;
 #pragma unroll
-        for (int i = 0; i < MS; ++i) fx[i] = fp8_scale<S>(sx[Q][i]);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) fw[b] = fp8_scale<S>(sw[Q][b]);
+          for (int b = 0; b < NB; ++b) sw[b] = nw[b] & keep;
+          load_scales(t + 4);
+        }
+        u32x4 xb[4], wb[4][NB];
 #pragma unroll
         for (int m = 0; m < 4; ++m) {  // 32 of K: eight of each lane's 32 codes
-          u32x4 xb[MS], wb[NB];
+          xb[m] = fp8_to_bf16(x[J % XR][m / 2][2 * (m % 2)], x[J % XR][m / 2][2 * (m % 2) + 1], fp8_scale<S>(sx));
+          formed_here(xb[m]);
 #pragma unroll
-          for (int b = 0; b < NB; ++b)
-            wb[b] = fp8_to_bf16(w[J][b][m / 2][2 * (m % 2)], w[J][b][m / 2][2 * (m % 2) + 1], fw[b]);
-#pragma unroll
-          for (int i = 0; i < MS; ++i)
-            xb[i] = fp8_to_bf16(x[J][i][m / 2][2 * (m % 2)], x[J][i][m / 2][2 * (m % 2) + 1], fx[i]);
-#pragma unroll
-          for (int i = 0; i < MS; ++i)
-#pragma unroll
-            for (int b = 0; b < NB; ++b) acc[i][b] = mfma16(wb[b], xb[i], acc[i][b]);
+          for (int b = 0; b < NB; ++b) {
+            wb[m][b] = fp8_to_bf16(w[J][b][m / 2][2 * (m % 2)], w[J][b][m / 2][2 * (m % 2) + 1], fp8_scale<S>(sw[b]));
+            formed_here(wb[m][b]);
+          }
         }
-        load(J, t0 + J + R);
-        if constexpr (S == 3) load_scales(Q, t0 + R + 4 * Q);
+        __builtin_amdgcn_sched_barrier(0);
+        load_x(J % XR, t + XR);
+        load_w(J, t + R);
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) acc[b] = mfma16(wb[m][b], xb[m], acc[b]);
       };
       step(std::integral_constant<int, 0>{});
       step(std::integral_constant<int, 1>{});
@@ -174,72 +174,59 @@ __global__ __launch_bounds__(64 * U * KS) void fp8_small_kernel(const Fp8GemmArg
     if constexpr (KS > 1) {
       if (part > 0)
 #pragma unroll
-        for (int i = 0; i < MS; ++i)
-#pragma unroll
-          for (int b = 0; b < NB; ++b) parts[((((part - 1) * U + u) * MS + i) * NB + b) * 64 + lane] = acc[i][b];
+        for (int b = 0; b < NB; ++b) parts[(((part - 1) * U + u) * NB + b) * 64 + lane] = acc[b];
       __syncthreads();
       if (part == 0)
 #pragma unroll
         for (int p = 1; p < KS; ++p)
 #pragma unroll
-          for (int i = 0; i < MS; ++i)
-#pragma unroll
-            for (int b = 0; b < NB; ++b) acc[i][b] += parts[((((p - 1) * U + u) * MS + i) * NB + b) * 64 + lane];
+          for (int b = 0; b < NB; ++b) acc[b] += parts[(((p - 1) * U + u) * NB + b) * 64 + lane];
     }
     const int col = unit * 16 + lg * 4;
+    const int64_t row = m0 + lr;
     if constexpr (SWIGLU) {
-      float h[MS][4];
-      if (part == 0)
+      float h[4], top = 0.0f;
+      if (part == 0) {
 #pragma unroll
-        for (int i = 0; i < MS; ++i) {
-          float top = 0.0f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            h[i][j] = silu_f32(acc[i][0][j]) * acc[i][1][j];
-            top = fmaxf(top, fp8_magnitude(h[i][j]));
-          }
-          top = fmaxf(top, __shfl_xor(top, 16, 64));
-          top = fmaxf(top, __shfl_xor(top, 32, 64));
-          if (lg == 0) tops[u][i * 16 + lr] = top;
+        for (int j = 0; j < 4; ++j) {
+          h[j] = silu_f32(acc[0][j]) * acc[1][j];
+          top = fmaxf(top, fp8_magnitude(h[j]));
         }
-      __syncthreads();
-      if (part == 0)
-#pragma unroll
-        for (int i = 0; i < MS; ++i) {
-          float top = 0.0f;
-#pragma unroll
-          for (int v = 0; v < 8; ++v) top = fmaxf(top, tops[v][i * 16 + lr]);
-          const int64_t row = m0 + i * 16 + lr;
-          if (row < end) store_h(a, h[i], top, row, nb, col, u == 0 && lg == 0);
-        }
-    } else if (part == 0) {
-#pragma unroll
-      for (int i = 0; i < MS; ++i) {
-        const int64_t row = m0 + i * 16 + lr;
-        if (row < end) store_y(a, acc[i][0], row, col);
+        top = fmaxf(top, __shfl_xor(top, 16, 64));
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        if (lg == 0) tops[u][lr] = top;
       }
+      __syncthreads();
+      if (part == 0 && row < end) {
+#pragma unroll
+        for (int v = 0; v < 8; ++v) top = fmaxf(top, tops[v][lr]);
+        store_h(a, h, top, row, nb, col, u == 0 && lg == 0);
+      }
+    } else if (part == 0 && row < end) {
+      store_y(a, acc[0], row, col);
     }
     if (SWIGLU || KS > 1) __syncthreads();  // the next rows use the same LDS
   }
 }
 
-// Some rows, up to 128 at a time: a workgroup has 128 columns of H or 256 of y, each of its eight waves two
-// blocks of 16 weight rows (gate and up, or neighbours).  The rows are read by all eight waves from LDS, as bf16
-// times their scale: each step's 128 of K are loaded a step ahead by the whole workgroup,
-// converted once and stored in the operand layout (4 KB for 16 rows), two stages.
+// Some rows, up to 16 MS at a time: a workgroup has 128 columns of H or 256 of y, each of its eight waves two
+// blocks of 16 weight rows (gate and up, or neighbours).  The rows are read by all eight waves from LDS, where
+// loads without registers put them as codes, a step of 128 of K a stage, in the operand layout (2 KB for 16 rows:
+// sixteen lanes read 256 consecutive bytes); four stages, three steps ahead, one barrier a step.
 template <bool SWIGLU>
 __global__ __launch_bounds__(512) void fp8_medium_kernel(const Fp8GemmArgs a) {
-  constexpr int MS = 8, R = 4;
-  __shared__ __attribute__((aligned(16))) uint8_t stage[2][MS * 4096];
+  constexpr int MS = 8, R = 4, D = 3;
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[MS * 2048], s1[MS * 2048], s2[MS * 2048], s3[MS * 2048];
   __shared__ float tops[SWIGLU ? 8 : 1][16 * MS];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lr = lane & 15, lg = lane >> 4;
+  auto stage = [&](int b) -> uint8_t * { return b == 0 ? s0 : b == 1 ? s1 : b == 2 ? s2 : s3; };
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lr = lane & 15,
+            lg = lane >> 4;
   constexpr int COLS = SWIGLU ? 128 : 256;
   const int n_blocks = (a.n_out + COLS - 1) / COLS;
   const int g = blockIdx.x / n_blocks, nb = blockIdx.x - g * n_blocks;
   int begin, end;
   fp8_group_rows(a, g, begin, end);
-  if (a.xp) begin += fp8_large_tiles(end - begin) * kFp8LargeRows;  // the kernel for many rows has the others
-  if (begin >= end) return;
+  if (begin >= end || (a.xp && end - begin > kFp8FewRows)) return;  // the kernel for many rows has those
   const int kt = fp8_blocks(a.K), kp = fp8_row_bytes(a.K), ks = fp8_scale_bytes(a.K);
   const int units = (a.n_out + 15) / 16 * (SWIGLU ? 2 : 1);  // blocks of 16 weight rows
   const int unit = nb * 16 + wave * 2;
@@ -250,103 +237,102 @@ __global__ __launch_bounds__(512) void fp8_medium_kernel(const Fp8GemmArgs a) {
   for (int b = 0; b < 2; ++b) woff[b] = unit + b < units ? (uint32_t)((unit + b) * kt * kFp8Tile + lane * 16) : kOob;
   const int sblocks = fp8_blocks(a.n_out);
   const uint8_t *wscale =
-      a.w_scale + ((int64_t)g * sblocks + (SWIGLU ? nb : min(nb * 2 + __builtin_amdgcn_readfirstlane(wave) / 4, sblocks - 1))) *
-                      (SWIGLU ? 2 : 1) * ks;
+      a.w_scale + ((int64_t)g * sblocks + (SWIGLU ? nb : min(nb * 2 + wave / 4, sblocks - 1))) * (SWIGLU ? 2 : 1) * ks;
+  u32x4 w[R][2][2];
+  auto load_w = [&](int j, int t) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const uint32_t o = t < kt && woff[b] != kOob ? woff[b] + (uint32_t)(t * kFp8Tile) : kOob;
+      w[j][b][0] = buf_ld16_nt(wres, o);
+      w[j][b][1] = buf_ld16_nt(wres, o == kOob ? kOob : o + 1024u);
+    }
+  };
   for (int m0 = begin; m0 < end; m0 += 16 * MS) {
     const int n = min(16 * MS, end - m0), ms = (n + 15) / 16;
     const Fp8Rows rows(a, m0, n);
-    // this thread's pieces of a step: 16 codes, row q % 16 of subtile q / 128, k = 64 p + 16 c ..
-    uint32_t xoff[2], soff[2];
+    // this wave's pieces of a stage, one for each half of K's 128: subtile `wave`, row lr, codes 64 p + 16 lg ..
+    const uint32_t src = rows.row(a, m0, wave * 16 + lr, wave * 16 + lr < n);
+    const uint32_t xoff = src != kOob ? src * (uint32_t)kp + (uint32_t)lg * 16u : kOob;
+    auto load_x = [&](int t, int b) {
+      const uint32_t o = t < kt && xoff != kOob ? xoff + (uint32_t)t * 128u : kOob;
+      buf_ld16_lds(rows.xres, o, stage(b) + wave * 2048);
+      buf_ld16_lds(rows.xres, o == kOob ? kOob : o + 64u, stage(b) + wave * 2048 + 1024);
+    };
+    uint32_t soff[MS], sx[MS], nx[MS], sw[2], nw[2];
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const int q = threadIdx.x + 512 * v, r = (q >> 7) * 16 + (q & 15);
-      const uint32_t src = rows.row(a, m0, r, r < n);
-      xoff[v] = src != kOob ? src * (uint32_t)kp + (uint32_t)((q >> 6 & 1) * 64 + (q >> 4 & 3) * 16) : kOob;
-      soff[v] = src != kOob ? src * (uint32_t)ks : kOob;
+    for (int i = 0; i < MS; ++i) {
+      const uint32_t r = rows.row(a, m0, i * 16 + lr, i * 16 + lr < n);
+      soff[i] = r != kOob ? r * (uint32_t)ks : kOob;
     }
-    u32x4 w[R][2][2], x[2];
-    uint32_t sx[2], sw[2];
-    auto load_w = [&](int j, int t) {
+    auto load_scales = [&](int t) {  // of four steps; past K those of the last four again (their codes are zeros)
+      const int at = min(t, ks - 4);
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const uint32_t o = t < kt && woff[b] != kOob ? woff[b] + (uint32_t)(t * kFp8Tile) : kOob;
-        w[j][b][0] = buf_ld16_nt(wres, o);
-        w[j][b][1] = buf_ld16_nt(wres, o == kOob ? kOob : o + 1024u);
-      }
-    };
-    auto load_x = [&](int t) {
+      for (int i = 0; i < MS; ++i)
+        nx[i] =
+            (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rows.sres, soff[i] == kOob ? kOob : soff[i] + (uint32_t)at, 0, 0);
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const bool in = t < kt && xoff[v] != kOob;
-        x[v] = buf_ld16(rows.xres, in ? xoff[v] + (uint32_t)t * 128u : kOob);
-        sx[v] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rows.sres, in ? soff[v] + (uint32_t)t : kOob, 0, 0);
-      }
-    };
-    auto put_x = [&](int s) {
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const int q = threadIdx.x + 512 * v;
-        if ((q >> 7) < ms) {
-          const float f = __uint_as_float((sx[v] & 0xffu) << 23);
-          uint8_t *o = stage[s] + (q >> 7) * 4096 + (q >> 6 & 1) * 2048 + (q & 63) * 16;
-          *reinterpret_cast<u32x4 *>(o) = fp8_to_bf16(x[v][0], x[v][1], f);
-          *reinterpret_cast<u32x4 *>(o + 1024) = fp8_to_bf16(x[v][2], x[v][3], f);
-        }
-      }
-    };
-    auto load_sw = [&](int t) {
-      const int left = kt - t;
-      const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-        sw[b] = *reinterpret_cast<const uint32_t *>(wscale + (SWIGLU ? b * ks : 0) + (left <= 0 ? 0 : t)) & keep;
-    };
-    auto bar = [&]() {
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      __builtin_amdgcn_sched_barrier(0);
-      __builtin_amdgcn_s_barrier();
-      __builtin_amdgcn_sched_barrier(0);
+      for (int b = 0; b < 2; ++b) nw[b] = scalar_load(wscale + (SWIGLU ? b * ks : 0) + at);
     };
     f32x4 acc[MS][2];
 #pragma unroll
     for (int i = 0; i < MS; ++i)
 #pragma unroll
       for (int b = 0; b < 2; ++b) acc[i][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-    load_x(0);
+    load_scales(0);
+#pragma unroll
+    for (int b = 0; b < D; ++b) load_x(b, b);
+    __builtin_amdgcn_sched_barrier(0);  // the waits count on rows before weights
 #pragma unroll
     for (int j = 0; j < R; ++j) load_w(j, j);
-    load_sw(0);
-    put_x(0);
-    load_x(1);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(4 * R) : "memory");  // the first stages are there
+    auto bar = [&]() {
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+    };
     bar();
     for (int t0 = 0; t0 < kt; t0 += R) {
+      const uint32_t keep = kt - t0 >= 4 ? ~0u : (1u << (8 * (kt - t0))) - 1u;  // the padding's scales are not looked at
+#pragma unroll
+      for (int i = 0; i < MS; ++i) sx[i] = nx[i] & keep;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) sw[b] = nw[b] & keep;
+      load_scales(t0 + R);
       auto step = [&](auto jc) {
         constexpr int J = decltype(jc)::value;
         const int t = t0 + J;
-        // stage t + 1: last read in step t - 1, which every wave has left
-        if (t + 1 < kt) put_x((J + 1) & 1);
-        load_x(t + 2);
-        if (t < kt) {
-          float fw[2];
+        load_x(t + D, (J + D) % R);  // the stage read in step t - 1, which every wave has left
+        __builtin_amdgcn_sched_barrier(0);
+        float fw[2];
 #pragma unroll
-          for (int b = 0; b < 2; ++b) fw[b] = fp8_scale<J>(sw[b]);
+        for (int b = 0; b < 2; ++b) fw[b] = fp8_scale<J>(sw[b]);
+        u32x4 wb[4][2];
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            wb[m][b] = fp8_to_bf16(w[J][b][m / 2][2 * (m % 2)], w[J][b][m / 2][2 * (m % 2) + 1], fw[b]);
+            formed_here(wb[m][b]);
+          }
+        __builtin_amdgcn_sched_barrier(0);
+        load_w(J, t + R);
+        const uint8_t *st = stage(J) + lane * 16;
+#pragma unroll
+        for (int i = 0; i < MS; ++i) {
+          if (i && i >= ms) break;
+          const float fx = fp8_scale<J>(sx[i]);
+          const u32x4 x[2] = {*reinterpret_cast<const u32x4 *>(st + i * 2048),
+                              *reinterpret_cast<const u32x4 *>(st + i * 2048 + 1024)};
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
-            u32x4 wb[2];
+            const u32x4 xb = fp8_to_bf16(x[m / 2][2 * (m % 2)], x[m / 2][2 * (m % 2) + 1], fx);
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
-              wb[b] = fp8_to_bf16(w[J][b][m / 2][2 * (m % 2)], w[J][b][m / 2][2 * (m % 2) + 1], fw[b]);
-#pragma unroll
-            for (int i = 0; i < MS; ++i) {
-              if (i >= ms) break;
-              const u32x4 xb = *reinterpret_cast<const u32x4 *>(stage[J & 1] + i * 4096 + m * 1024 + lane * 16);
-#pragma unroll
-              for (int b = 0; b < 2; ++b) acc[i][b] = mfma16(wb[b], xb, acc[i][b]);
-            }
+            for (int b = 0; b < 2; ++b) acc[i][b] = mfma16(wb[m][b], xb, acc[i][b]);
           }
         }
-        load_w(J, t + R);
-        if constexpr (J == 3) load_sw(t0 + R);
+        // step t + 1's rows, loaded in step t + 1 - D, are there when at most the loads behind them are in flight
+        // (weights of that step, rows and weights of the steps since; the scales may lie between as well)
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(4 + 6 * (D - 1)) : "memory");
         bar();
       };
       step(std::integral_constant<int, 0>{});
@@ -354,6 +340,8 @@ __global__ __launch_bounds__(512) void fp8_medium_kernel(const Fp8GemmArgs a) {
       step(std::integral_constant<int, 2>{});
       step(std::integral_constant<int, 3>{});
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no write to LDS may outlive its rows
+    __syncthreads();
     if constexpr (SWIGLU) {
       const int col = nb * 128 + wave * 16 + lg * 4;
 #pragma unroll
@@ -405,9 +393,9 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs &a, hipStream_t s) {
   }
   if (std::min(a.group_rows_max, a.rows_max) <= 16) {
     if (swiglu)
-      hipLaunchKernelGGL((fp8_small_kernel<true, 1, 8, 1>), grid(128), dim3(512), 0, s, a);
+      hipLaunchKernelGGL((fp8_small_kernel<true, 8, 1>), grid(128), dim3(512), 0, s, a);
     else
-      hipLaunchKernelGGL((fp8_small_kernel<false, 1, 8, 1>), grid(128), dim3(512), 0, s, a);
+      hipLaunchKernelGGL((fp8_small_kernel<false, 8, 1>), grid(128), dim3(512), 0, s, a);
   } else {
     if (swiglu)
       hipLaunchKernelGGL((fp8_medium_kernel<true>), grid(128), dim3(512), 0, s, a);

@@ -19,7 +19,6 @@ namespace {
 
 constexpr int LG_TILE = kFp8LargeRows * 64;  // bytes of an operand's stage: 256 rows, 64 of K
 
-// The tiles of a group of n rows: whole ones, and a last one of more rows than the tails of another launch.
 __device__ __forceinline__ int large_tiles(const Fp8GemmArgs &a, int g) {
   int begin, end;
   fp8_group_rows(a, g, begin, end);
@@ -106,8 +105,10 @@ __global__ __launch_bounds__(512, 1) void fp8_large_kernel(const Fp8GemmArgs a, 
   }
   mt = __builtin_amdgcn_readfirstlane(mt);
   nt = __builtin_amdgcn_readfirstlane(nt);
-  const int m0 = begin + mt * kFp8LargeRows, rows = min(kFp8LargeRows, end - m0), m_tile = mt_first + mt;
+  const int per = fp8_tile_rows(end - begin, mt_count);
+  const int m0 = begin + mt * per, rows = min(per, end - m0), m_tile = mt_first + mt;
   if (m_tile >= tiles_max) return;
+  const int row_blocks = (rows + 31) / 32, mine = max(0, min(4, row_blocks - wm * 4));  // of 32 rows: the tile's, this wave's
   const int kt = fp8_blocks(a.K), nk = 2 * kt, ks = fp8_scale_bytes(a.K);
   const int64_t abytes = (int64_t)kFp8LargeRows * kt * kFp8Block;
   const int64_t wbytes = fp8_group_bytes(a.n_out, a.K, SWIGLU);
@@ -119,7 +120,7 @@ __global__ __launch_bounds__(512, 1) void fp8_large_kernel(const Fp8GemmArgs a, 
   const uint32_t stride = (uint32_t)kt * kFp8Tile;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    aoff[i] = (uint32_t)(2 * wave + i) * stride + (uint32_t)lane * 16u;
+    aoff[i] = wave < row_blocks ? (uint32_t)(2 * wave + i) * stride + (uint32_t)lane * 16u : kOob;
     const int64_t w = (int64_t)(nt * 16 + 2 * wave + i) * stride;
     boff[i] = w < wbytes ? (uint32_t)w + (uint32_t)lane * 16u : kOob;
   }
@@ -128,7 +129,7 @@ __global__ __launch_bounds__(512, 1) void fp8_large_kernel(const Fp8GemmArgs a, 
     const bool in = s < nk;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      buf_ld16_lds(ares, in ? aoff[i] + k : kOob, bufA(b) + (2 * wave + i) * 1024);
+      buf_ld16_lds(ares, in && aoff[i] != kOob ? aoff[i] + k : kOob, bufA(b) + (2 * wave + i) * 1024);
       buf_ld16_lds(wres, in && boff[i] != kOob ? boff[i] + k : kOob, bufB(b) + (2 * wave + i) * 1024);
     }
   };
@@ -169,6 +170,7 @@ __global__ __launch_bounds__(512, 1) void fp8_large_kernel(const Fp8GemmArgs a, 
       const uint8_t *pa = la + a_at, *pb = lb + b_at;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        if (i >= mine) break;
         af[i][0] = *reinterpret_cast<const u32x4 *>(pa + i * 2048);
         af[i][1] = *reinterpret_cast<const u32x4 *>(pa + i * 2048 + 256);
       }
@@ -182,11 +184,13 @@ __global__ __launch_bounds__(512, 1) void fp8_large_kernel(const Fp8GemmArgs a, 
     auto comp = [&](int b) {
       __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i) {
+        if (i >= mine) break;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
           acc[i][j] = mfma_fp8_32(fp8_operand(bf[j][0], bf[j][1]), fp8_operand(af[i][0], af[i][1]), acc[i][j], cw[j], cx[i],
                                   b / 2);
+      }
       __builtin_amdgcn_s_setprio(0);
     };
     auto bar = [&]() {
@@ -311,47 +315,49 @@ __global__ __launch_bounds__(512, 1) void fp8_large_kernel(const Fp8GemmArgs a, 
 }
 
 // The rows of the tiles, and their scales as [4 blocks of K][256 rows] words, for fp8_large_kernel: one
-// workgroup a tile and block of 128 of K, whole lines of the rows in.
+// workgroup a tile and four blocks of K, 512 bytes of a row by 32 threads.
 __global__ __launch_bounds__(256) void fp8_pack_rows_kernel(const Fp8GemmArgs a, uint8_t *__restrict__ xp,
                                                             uint8_t *__restrict__ xp_scale) {
-  const int kt = fp8_blocks(a.K), kp = fp8_row_bytes(a.K), ks = fp8_scale_bytes(a.K);
-  const int m_tile = blockIdx.x / kt, b = blockIdx.x - m_tile * kt;
+  const int kt = fp8_blocks(a.K), kp = fp8_row_bytes(a.K), ks = fp8_scale_bytes(a.K), quads = ks / 4;
+  const int b0 = (blockIdx.x % quads) * 4, m_tile = blockIdx.x / quads;
   int g, first, count, begin, end;
   find_tile(a, m_tile, g, first, count);
   if (g < 0) return;
   fp8_group_rows(a, g, begin, end);
-  const int m0 = begin + (m_tile - first) * kFp8LargeRows;
+  const int per = fp8_tile_rows(end - begin, count), m0 = begin + (m_tile - first) * per, rows = min(per, end - m0);
   auto source = [&](int r) -> int64_t {  // -1: zeros
-    if (m0 + r >= end) return -1;
+    if (r >= rows) return -1;
     if (!a.row_index) return m0 + r;
     const int s = a.row_index[m0 + r];
     return (uint32_t)s < (uint32_t)a.x_rows ? s : -1;
   };
-  u32x4 v[8];
+  const int r0 = threadIdx.x >> 5, c = threadIdx.x & 31, b = b0 + (c >> 3);  // a block's 16-byte piece c & 7
+  for (int i0 = 0; i0 < rows; i0 += 64) {
+    u32x4 v[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int q = threadIdx.x + 256 * i;
-    const int64_t s = source(q >> 3);
-    v[i] = u32x4{0u, 0u, 0u, 0u};
-    if (s >= 0) v[i] = ldg16(a.x8 + s * kp + b * 128 + (q & 7) * 16);
-  }
-  uint8_t *o = xp + ((int64_t)m_tile * 16 * kt + b) * kFp8Tile;
+    for (int i = 0; i < 8; ++i) {
+      const int64_t s = source(i0 + i * 8 + r0);
+      v[i] = u32x4{0u, 0u, 0u, 0u};
+      if (s >= 0 && b < kt) v[i] = ldg16(a.x8 + s * kp + b0 * 128 + c * 16);
+    }
+    if (b < kt) {
+      uint8_t *o = xp + ((int64_t)m_tile * 16 * kt + b) * kFp8Tile + (c & 7) * 256;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int q = threadIdx.x + 256 * i, r = q >> 3, c = q & 7;
-    stg16(o + (int64_t)(r >> 4) * kt * kFp8Tile + c * 256 + (r & 15) * 16, v[i]);
+      for (int i = 0; i < 8; ++i) {
+        const int r = i0 + i * 8 + r0;
+        if (r < 256) stg16(o + (int64_t)(r >> 4) * kt * kFp8Tile + (r & 15) * 16, v[i]);
+      }
+    }
   }
-  if (b % 4 == 0) {
-    const int64_t s = source(threadIdx.x);
-    const uint32_t w = s >= 0 ? *reinterpret_cast<const uint32_t *>(a.x_scale + s * ks + b) : 0u;
-    reinterpret_cast<uint32_t *>(xp_scale)[((int64_t)m_tile * (ks / 4) + b / 4) * kFp8LargeRows + threadIdx.x] = w;
-  }
+  const int64_t s = source(threadIdx.x);
+  const uint32_t w = s >= 0 ? *reinterpret_cast<const uint32_t *>(a.x_scale + s * ks + b0) : 0u;
+  reinterpret_cast<uint32_t *>(xp_scale)[((int64_t)m_tile * quads + b0 / 4) * kFp8LargeRows + threadIdx.x] = w;
 }
 
 }  // namespace
 
 hipError_t launch_fp8_pack_rows(const Fp8GemmArgs &a, uint8_t *xp, uint8_t *xp_scale, hipStream_t s) {
-  const int64_t grid = fp8_large_tiles_max(a.rows_max) * fp8_blocks(a.K);
+  const int64_t grid = fp8_large_tiles_max(a.rows_max) * (fp8_scale_bytes(a.K) / 4);
   if (grid == 0) return hipSuccess;
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
   hipLaunchKernelGGL(fp8_pack_rows_kernel, dim3((unsigned)grid), dim3(256), 0, s, a, xp, xp_scale);

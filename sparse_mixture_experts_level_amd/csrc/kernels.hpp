@@ -241,18 +241,22 @@ struct Fp8GemmArgs {
   uint16_t *y;
   uint8_t *h8, *h_scale;
   int num_groups, rows_max, group_rows_max, x_rows, n_out, K;
-  // Groups that can have more rows than kFp8LargeTail: the rows of whole tiles of kFp8LargeRows, and of a last one of
-  // more than kFp8LargeTail, go through a kernel for many rows, which reads them (and writes H) in packed
-  // tiles of fp8_packed_bytes(); xp and hp are NULL where no group can.
+  // Groups of more than kFp8FewRows go through a kernel for many rows, which reads them (and writes H) in packed
+  // tiles of fp8_packed_bytes(); xp and hp are NULL where no group can have that many.
   const uint8_t *xp, *xp_scale;
   uint8_t *hp, *hp_scale;
 };
-constexpr int kFp8LargeRows = 256, kFp8LargeTail = 128;
+// A group of many rows is cut into the least number of tiles of at most kFp8LargeRows, equal but for whole 32s: the
+// matrix instructions of 32 rows past a tile's end are left out, so that a group of 1040 rows costs five tiles of
+// 224 and less (the last has 144), not four of 256 and a nearly empty one.
+constexpr int kFp8LargeRows = 256, kFp8FewRows = 128;
 __host__ __device__ inline int fp8_large_tiles(int rows) {
-  return rows / kFp8LargeRows + (rows % kFp8LargeRows > kFp8LargeTail ? 1 : 0);
+  return rows <= kFp8FewRows ? 0 : (rows + kFp8LargeRows - 1) / kFp8LargeRows;
 }
-// Bounds on the tiles of rows in all (each has more than kFp8LargeTail), and their bytes: codes, scales.
-inline int64_t fp8_large_tiles_max(int64_t rows) { return rows / (kFp8LargeTail + 1); }
+__host__ __device__ inline int fp8_tile_rows(int rows, int tiles) { return (rows + 32 * tiles - 1) / (32 * tiles) * 32; }
+// A bound on the tiles of rows in all: two of 257 rows are the most for their number.
+inline int64_t fp8_large_tiles_max(int64_t rows) { return 2 * rows / 257; }
+// Their bytes: codes, scales.
 inline int64_t fp8_packed_bytes(int64_t rows, int k) { return fp8_large_tiles_max(rows) * kFp8LargeRows * fp8_row_bytes(k); }
 inline int64_t fp8_packed_scale_bytes(int64_t rows, int k) {
   return fp8_large_tiles_max(rows) * kFp8LargeRows * fp8_scale_bytes(k);
