@@ -730,9 +730,9 @@ bool fp8_large(int64_t rows_max, int32_t group_rows_max) {
 
 // Workspace of the products in 8 bits: packed tiles of the rows and, for the FFN (f > 0), H in rows and in packed tiles.
 struct Fp8Layout {
-  size_t xp, xp_scale, h8, h_scale, hp, hp_scale, total;
+  size_t xp, xp_scale, h8, h_scale, h32, hp, hp_scale, total;
 };
-Fp8Layout fp8_layout(int64_t rows_max, int32_t group_rows_max, int32_t k, int32_t f) {
+Fp8Layout fp8_layout(int32_t G, int64_t rows_max, int32_t group_rows_max, int32_t k, int32_t f) {
   Fp8Layout L{};
   size_t o = 0;
   auto take = [&](int64_t bytes) {
@@ -741,18 +741,20 @@ Fp8Layout fp8_layout(int64_t rows_max, int32_t group_rows_max, int32_t k, int32_
     return at;
   };
   const bool large = fp8_large(rows_max, group_rows_max);
-  L.xp = take(large ? moe::fp8_packed_bytes(rows_max, k) : 0);
-  L.xp_scale = take(large ? moe::fp8_packed_scale_bytes(rows_max, k) : 0);
+  L.xp = take(large ? moe::fp8_packed_bytes(rows_max, G, k) : 0);
+  L.xp_scale = take(large ? moe::fp8_packed_scale_bytes(rows_max, G, k) : 0);
   L.h8 = take(f ? rows_max * moe::fp8_row_bytes(f) : 0);
   L.h_scale = take(f ? rows_max * moe::fp8_scale_bytes(f) : 0);
-  L.hp = take(f && large ? moe::fp8_packed_bytes(rows_max, f) : 0);
-  L.hp_scale = take(f && large ? moe::fp8_packed_scale_bytes(rows_max, f) : 0);
+  const bool few = std::min<int64_t>(rows_max, group_rows_max) <= 16;
+  L.h32 = take(f && few ? 4 * rows_max * moe::fp8_row_bytes(f) : 0);
+  L.hp = take(f && large ? moe::fp8_packed_bytes(rows_max, G, f) : 0);
+  L.hp_scale = take(f && large ? moe::fp8_packed_scale_bytes(rows_max, G, f) : 0);
   L.total = o;
   return L;
 }
 
-size_t swiglu_fp8_ws_bytes(int32_t, int64_t rows_max, int32_t group_rows_max, int32_t d, int32_t f) {
-  return fp8_layout(rows_max, group_rows_max, d, f).total;
+size_t swiglu_fp8_ws_bytes(int32_t G, int64_t rows_max, int32_t group_rows_max, int32_t d, int32_t f) {
+  return fp8_layout(G, rows_max, group_rows_max, d, f).total;
 }
 
 moe::Fp8GemmArgs fp8_args(int32_t G, int64_t rows_max, int32_t group_rows_max, int32_t n_out, int32_t k, const uint8_t *x8,
@@ -788,13 +790,14 @@ moe_status run_swiglu_fp8(int32_t G, int64_t rows_max, int32_t group_rows_max, i
                           const uint8_t *x_scale, const int32_t *row_index, int64_t x_rows, const int32_t *offsets,
                           const moe_fp8_matrix &gate_up, const moe_fp8_matrix &down, void *y, void *ws,
                           hipStream_t stream) {
-  const Fp8Layout L = fp8_layout(rows_max, group_rows_max, d, f);
+  const Fp8Layout L = fp8_layout(G, rows_max, group_rows_max, d, f);
   const bool large = fp8_large(rows_max, group_rows_max);
   moe::Fp8GemmArgs a = fp8_args(G, rows_max, group_rows_max, f, d, x8, x_scale, row_index, x_rows, offsets,
                                 gate_up.codes, gate_up.scale);
   MOE_TRY(pack_fp8(a, ws, L, stream));
   a.h8 = at<uint8_t>(ws, L.h8);
   a.h_scale = at<uint8_t>(ws, L.h_scale);
+  a.h32 = std::min<int64_t>(rows_max, group_rows_max) <= 16 ? at<float>(ws, L.h32) : nullptr;
   a.hp = large ? at<uint8_t>(ws, L.hp) : nullptr;
   a.hp_scale = large ? at<uint8_t>(ws, L.hp_scale) : nullptr;
   MOE_TRY_HIP(moe::launch_fp8_gemm(a, stream), "gate_up in 8 bits");
@@ -1848,7 +1851,7 @@ moe_status moe_rms_norm_backward(int32_t num_tokens, int32_t d_model, int32_t dt
 size_t moe_grouped_linear_fp8_workspace_size(int32_t num_groups, int64_t rows_max, int32_t group_rows_max,
                                              int32_t n_out, int32_t k) {
   if (check_fp8_shape(num_groups, n_out, k, false) != MOE_OK || check_fp8_rows(rows_max, group_rows_max) != MOE_OK) return 0;
-  return std::max<size_t>(fp8_layout(rows_max, group_rows_max, k, 0).total, kAlign);
+  return std::max<size_t>(fp8_layout(num_groups, rows_max, group_rows_max, k, 0).total, kAlign);
 }
 
 moe_status moe_grouped_linear_fp8(int32_t num_groups, int64_t rows_max, int32_t group_rows_max, int32_t n_out, int32_t k,
@@ -1873,7 +1876,7 @@ moe_status moe_grouped_linear_fp8(int32_t num_groups, int64_t rows_max, int32_t 
   moe::Fp8GemmArgs a = fp8_args(num_groups, rows_max, group_rows_max, n_out, k, x8, x_scale, row_index,
                                 row_index ? x_row_count : rows_max, group_offsets, w8, w_scale);
   a.y = static_cast<uint16_t *>(y_rows);
-  MOE_TRY(pack_fp8(a, ws, fp8_layout(rows_max, group_rows_max, k, 0), stream));
+  MOE_TRY(pack_fp8(a, ws, fp8_layout(num_groups, rows_max, group_rows_max, k, 0), stream));
   MOE_TRY_HIP(moe::launch_fp8_gemm(a, stream), "grouped product in 8 bits");
   return ok();
 }

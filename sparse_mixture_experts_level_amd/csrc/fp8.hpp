@@ -118,9 +118,46 @@ __device__ __forceinline__ void fp8_group_rows(const Fp8GemmArgs &a, int g, int 
   begin = min(max(a.offsets[g], 0), a.rows_max);
   end = min(max(a.offsets[g + 1], begin), a.rows_max);
 }
+// The same for a group that is the same in every lane, in scalar registers, with all that derives from it (the compiler does
+// not see that the offsets stay as they are, and runs a loop over the lanes around every buffer load).
+__device__ __forceinline__ void fp8_group_rows_uniform(const Fp8GemmArgs &a, int g, int &begin, int &end) {
+  fp8_group_rows(a, g, begin, end);
+  begin = __builtin_amdgcn_readfirstlane(begin);
+  end = __builtin_amdgcn_readfirstlane(end);
+}
+// The n-th group (from 0) of more than 0 and at most `most` rows, the same in every lane; -1: there are not that many.  A
+// launch has as many workgroups as groups can have rows, not as there are groups: one of an empty group holds
+// its CU until it has read the offsets (a decode step of one token, 4 of 32 experts: 20 us for 12).
+__device__ __forceinline__ int fp8_nth_group(const Fp8GemmArgs &a, int n, int most) {
+  const int lane = threadIdx.x & 63;
+  int seen = 0;
+  for (int g0 = 0; g0 < a.num_groups; g0 += 64) {
+    int begin = 0, end = 0;
+    if (g0 + lane < a.num_groups) fp8_group_rows(a, g0 + lane, begin, end);
+    const uint64_t some = __ballot(end > begin && end - begin <= most);
+    const int count = __popcll(some);
+    if (n < seen + count) {
+      const bool mine = (some >> lane & 1) && __popcll(some & ((1ull << lane) - 1)) == n - seen;
+      return __builtin_amdgcn_readfirstlane(g0 + __ffsll((unsigned long long)__ballot(mine)) - 1);
+    }
+    seen += count;
+  }
+  return -1;
+}
 // Bytes of one group's codes.
 __host__ __device__ __forceinline__ int64_t fp8_group_bytes(int n_out, int k, bool swiglu) {
   return (int64_t)((n_out + 15) / 16) * (swiglu ? 2 : 1) * fp8_blocks(k) * kFp8Tile;
+}
+
+// c + (A 2^sa) (B 2^sb), 16 x 16 over 128 of K, the scales byte J of sa and sb.  Lane l holds row l % 16
+// of each operand, k = 16 (l / 16) .. + 15 and 64 + 16 (l / 16) .. + 15 (any order shared by the two
+// operands gives the same sum); c: columns (of B) l % 16, rows (of A) 4 (l / 16) .. + 3.
+// Within a lane's 16 products the instruction drops what lies about 2^-14 below the largest
+// of them; the accumulator is a full float.  Against 64 bits the sums of Gaussian rows are off by 1.2e-5 to
+// 1.6e-5 of their size, over any length: a hundredth of the bf16 rounding that follows.
+template <int J>
+__device__ __forceinline__ f32x4 mfma_fp8_16(i32x8 a, i32x8 b, f32x4 c, uint32_t sa, uint32_t sb) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, J, (int)sa, J, (int)sb);
 }
 
 // Eight codes as bf16, times 2^(e) for a scale 2^e given as a float: exact (bf16 has a float's exponents).

@@ -11,6 +11,7 @@
 // floats, where the 8-bit instruction drops what lies 2^-14 below the largest of 16 products (1.5e-5 of a
 // sum: enough to move one code of H in two thousand).
 #include <algorithm>
+#include <climits>
 
 #include "fp8.hpp"
 #include "kernels.hpp"
@@ -30,13 +31,14 @@ struct Fp8Rows {
     xres = make_rsrc(a.x8 + first * kp, (uint32_t)(n * kp));
     sres = make_rsrc(a.x_scale + first * ks, (uint32_t)(n * ks));
   }
-  __device__ __forceinline__ uint32_t row(const Fp8GemmArgs &a, int m0, int r, bool in) const {
-    uint32_t src = (uint32_t)r;
-    if (gather && in) {
-      src = (uint32_t)a.row_index[m0 + r];
-      in = src < (uint32_t)a.x_rows;
+  // (the index of a row past the end is read from the last row's place, so that no load waits for a branch)
+  __device__ __forceinline__ uint32_t row(const Fp8GemmArgs &a, int m0, int r, int n) const {
+    uint32_t src = (uint32_t)r, most = (uint32_t)n;
+    if (gather) {
+      src = (uint32_t)a.row_index[m0 + min(r, n - 1)];
+      most = (uint32_t)a.x_rows;
     }
-    return in ? src : kOob;
+    return r < n && src < most ? src : kOob;
   }
 };
 
@@ -74,19 +76,18 @@ __device__ __forceinline__ void formed_here(u32x4 &v) { asm volatile("" : "+v"(v
 template <bool SWIGLU, int U, int KS>
 __global__ __launch_bounds__(64 * U * KS) void fp8_small_kernel(const Fp8GemmArgs a) {
   constexpr int NB = SWIGLU ? 2 : 1, R = SWIGLU ? 4 : 8, XR = 2;
-  static_assert(!SWIGLU || U == 8, "a block of H's columns a workgroup");
-  __shared__ float tops[SWIGLU ? 8 : 1][16];
+  constexpr bool QUANTISE = SWIGLU && U == 8;  // a block of H's columns a workgroup
+  __shared__ float tops[QUANTISE ? 8 : 1][16];
   __shared__ f32x4 parts[KS > 1 ? (KS - 1) * U * NB * 64 : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lr = lane & 15,
             lg = lane >> 4;
   const int u = wave % U, part = wave / U;
-  const int n_blocks = (a.n_out + 16 * U - 1) / (16 * U);
-  const int g = blockIdx.x / n_blocks, nb = blockIdx.x - g * n_blocks;
+  const int nb = blockIdx.x, g = fp8_nth_group(a, blockIdx.y, INT_MAX);
+  if (g < 0) return;
   int begin, end;
-  fp8_group_rows(a, g, begin, end);
-  if (begin >= end) return;
+  fp8_group_rows_uniform(a, g, begin, end);
   const int kt = fp8_blocks(a.K), kp = fp8_row_bytes(a.K), ks = fp8_scale_bytes(a.K);
-  const int quads = ks / 4, tb = 4 * (quads * part / KS), te = min(kt, 4 * (quads * (part + 1) / KS));
+  const int tb = kt * part / KS, te = kt * (part + 1) / KS;
   const int unit = nb * U + u, units = (a.n_out + 15) / 16;
   const int64_t wbytes = fp8_group_bytes(a.n_out, a.K, SWIGLU);
   const rsrc_t wres = make_rsrc(a.w8 + g * wbytes, (uint32_t)wbytes);
@@ -106,7 +107,7 @@ __global__ __launch_bounds__(64 * U * KS) void fp8_small_kernel(const Fp8GemmArg
 #pragma unroll
     for (int j = 0; j < R; ++j) load_w(j, tb + j);
     const Fp8Rows rows(a, m0, min(16, end - m0));
-    const uint32_t src = rows.row(a, m0, lr, m0 + lr < end);
+    const uint32_t src = rows.row(a, m0, lr, min(16, end - m0));
     const uint32_t xoff = src != kOob ? src * (uint32_t)kp + (uint32_t)lg * 16u : kOob;
     const uint32_t soff = src != kOob ? src * (uint32_t)ks : kOob;
     auto load_x = [&](int j, int t) {
@@ -114,11 +115,15 @@ __global__ __launch_bounds__(64 * U * KS) void fp8_small_kernel(const Fp8GemmArg
       x[j][0] = buf_ld16(rows.xres, o);
       x[j][1] = buf_ld16(rows.xres, o == kOob ? kOob : o + 64u);
     };
-    auto load_scales = [&](int t) {  // of four steps; past K those of the last four again (their codes are zeros)
-      const int at = min(t, ks - 4);
-      nx = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rows.sres, soff == kOob ? kOob : soff + (uint32_t)at, 0, 0);
+    // Scales of four steps from any one on, out of two aligned words; past K some others (their codes are zeros).
+    auto load_scales = [&](int t) {
+      const int lo = min(t & ~3, ks - 4), hi = min(lo + 4, ks - 4);
+      nx = __builtin_amdgcn_alignbyte(
+          (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rows.sres, soff == kOob ? kOob : soff + (uint32_t)hi, 0, 0),
+          (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rows.sres, soff == kOob ? kOob : soff + (uint32_t)lo, 0, 0), t & 3);
 #pragma unroll
-      for (int b = 0; b < NB; ++b) nw[b] = scalar_load(wscale + b * ks + at);
+      for (int b = 0; b < NB; ++b)
+        nw[b] = (uint32_t)(((uint64_t)scalar_load(wscale + b * ks + hi) << 32 | scalar_load(wscale + b * ks + lo)) >> (8 * (t & 3)));
     };
     load_scales(tb);
 #pragma unroll
@@ -134,7 +139,7 @@ __global__ __launch_bounds__(64 * U * KS) void fp8_small_kernel(const Fp8GemmArg
         constexpr int J = decltype(jc)::value, S = J % 4;
         const int t = t0 + J;
         if constexpr (S == 0) {
-          const int left = kt - t;  // blocks that exist: the padding's scales are not looked at
+          const int left = te - t;  // blocks of this part: the padding's scales are not looked at
           const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
           sx = nx & keep;
 #pragma unroll
@@ -184,7 +189,7 @@ __global__ __launch_bounds__(64 * U * KS) void fp8_small_kernel(const Fp8GemmArg
     }
     const int col = unit * 16 + lg * 4;
     const int64_t row = m0 + lr;
-    if constexpr (SWIGLU) {
+    if constexpr (QUANTISE) {
       float h[4], top = 0.0f;
       if (part == 0) {
 #pragma unroll
@@ -202,34 +207,37 @@ __global__ __launch_bounds__(64 * U * KS) void fp8_small_kernel(const Fp8GemmArg
         for (int v = 0; v < 8; ++v) top = fmaxf(top, tops[v][lr]);
         store_h(a, h, top, row, nb, col, u == 0 && lg == 0);
       }
+    } else if constexpr (SWIGLU) {
+      if (part == 0 && row < end) {
+        f32x4 h;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = silu_f32(acc[0][j]) * acc[1][j];
+        if (col < fp8_row_bytes(a.n_out)) *reinterpret_cast<f32x4 *>(a.h32 + row * (int64_t)fp8_row_bytes(a.n_out) + col) = h;
+      }
     } else if (part == 0 && row < end) {
       store_y(a, acc[0], row, col);
     }
-    if (SWIGLU || KS > 1) __syncthreads();  // the next rows use the same LDS
+    if (QUANTISE || KS > 1) __syncthreads();  // the next rows use the same LDS
   }
 }
 
-// Some rows, up to 16 MS at a time: a workgroup has 128 columns of H or 256 of y, each of its eight waves two
+// Some rows, up to 128 at a time: a workgroup has 128 columns of H or 256 of y, each of its eight waves two
 // blocks of 16 weight rows (gate and up, or neighbours).  The rows are read by all eight waves from LDS, where
 // loads without registers put them as codes, a step of 128 of K a stage, in the operand layout (2 KB for 16 rows:
-// sixteen lanes read 256 consecutive bytes); four stages, three steps ahead, one barrier a step.
-template <bool SWIGLU>
-__global__ __launch_bounds__(512) void fp8_medium_kernel(const Fp8GemmArgs a) {
-  constexpr int MS = 8, R = 4, D = 3;
-  __shared__ __attribute__((aligned(1024))) uint8_t s0[MS * 2048], s1[MS * 2048], s2[MS * 2048], s3[MS * 2048];
-  __shared__ float tops[SWIGLU ? 8 : 1][16 * MS];
+// sixteen lanes read 256 consecutive bytes); four stages, three steps ahead, one barrier a step.  The 8-bit matrix
+// instruction: converted to bf16 by each wave, 128 rows took 1.7 us a step of the 1.2 that its weights take.
+constexpr int MD_R = 4, MD_D = 3, MD_ROWS = 128, MD_STAGE = MD_ROWS * 128;
+
+// One block of n <= 16 MS rows from m0 on; MS is exact, so that no branch is in the loop.
+template <bool SWIGLU, int MS>
+__device__ __forceinline__ void medium_rows(const Fp8GemmArgs &a, int g, int nb, int m0, int n, uint8_t *s0, uint8_t *s1,
+                                            uint8_t *s2, uint8_t *s3, float (*tops)[MD_ROWS]) {
+  constexpr int R = MD_R, D = MD_D;
   auto stage = [&](int b) -> uint8_t * { return b == 0 ? s0 : b == 1 ? s1 : b == 2 ? s2 : s3; };
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lr = lane & 15,
             lg = lane >> 4;
-  constexpr int COLS = SWIGLU ? 128 : 256;
-  const int n_blocks = (a.n_out + COLS - 1) / COLS;
-  const int g = blockIdx.x / n_blocks, nb = blockIdx.x - g * n_blocks;
-  int begin, end;
-  fp8_group_rows(a, g, begin, end);
-  if (begin >= end || (a.xp && end - begin > kFp8FewRows)) return;  // the kernel for many rows has those
   const int kt = fp8_blocks(a.K), kp = fp8_row_bytes(a.K), ks = fp8_scale_bytes(a.K);
-  const int units = (a.n_out + 15) / 16 * (SWIGLU ? 2 : 1);  // blocks of 16 weight rows
-  const int unit = nb * 16 + wave * 2;
+  const int units = (a.n_out + 15) / 16 * (SWIGLU ? 2 : 1), unit = nb * 16 + wave * 2;  // blocks of 16 weight rows
   const int64_t wbytes = fp8_group_bytes(a.n_out, a.K, SWIGLU);
   const rsrc_t wres = make_rsrc(a.w8 + g * wbytes, (uint32_t)wbytes);
   uint32_t woff[2];
@@ -238,146 +246,147 @@ __global__ __launch_bounds__(512) void fp8_medium_kernel(const Fp8GemmArgs a) {
   const int sblocks = fp8_blocks(a.n_out);
   const uint8_t *wscale =
       a.w_scale + ((int64_t)g * sblocks + (SWIGLU ? nb : min(nb * 2 + wave / 4, sblocks - 1))) * (SWIGLU ? 2 : 1) * ks;
-  u32x4 w[R][2][2];
+  i32x8 w[R][2];
   auto load_w = [&](int j, int t) {
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const uint32_t o = t < kt && woff[b] != kOob ? woff[b] + (uint32_t)(t * kFp8Tile) : kOob;
-      w[j][b][0] = buf_ld16_nt(wres, o);
-      w[j][b][1] = buf_ld16_nt(wres, o == kOob ? kOob : o + 1024u);
+      w[j][b] = fp8_operand(buf_ld16_nt(wres, o), buf_ld16_nt(wres, o == kOob ? kOob : o + 1024u));
     }
   };
-  for (int m0 = begin; m0 < end; m0 += 16 * MS) {
-    const int n = min(16 * MS, end - m0), ms = (n + 15) / 16;
-    const Fp8Rows rows(a, m0, n);
-    // this wave's pieces of a stage, one for each half of K's 128: subtile `wave`, row lr, codes 64 p + 16 lg ..
-    const uint32_t src = rows.row(a, m0, wave * 16 + lr, wave * 16 + lr < n);
-    const uint32_t xoff = src != kOob ? src * (uint32_t)kp + (uint32_t)lg * 16u : kOob;
-    auto load_x = [&](int t, int b) {
-      const uint32_t o = t < kt && xoff != kOob ? xoff + (uint32_t)t * 128u : kOob;
-      buf_ld16_lds(rows.xres, o, stage(b) + wave * 2048);
-      buf_ld16_lds(rows.xres, o == kOob ? kOob : o + 64u, stage(b) + wave * 2048 + 1024);
-    };
-    uint32_t soff[MS], sx[MS], nx[MS], sw[2], nw[2];
+  const Fp8Rows rows(a, m0, n);
+  // this wave's pieces of a stage, one for each half of K's 128: subtile `wave`, row lr, codes 64 p + 16 lg ..
+  const uint32_t src = rows.row(a, m0, wave * 16 + lr, n);
+  const uint32_t xoff = src != kOob ? src * (uint32_t)kp + (uint32_t)lg * 16u : kOob;
+  auto load_x = [&](int t, int b) {
+    const uint32_t o = t < kt && xoff != kOob ? xoff + (uint32_t)t * 128u : kOob;
+    buf_ld16_lds(rows.xres, o, stage(b) + wave * 2048);
+    buf_ld16_lds(rows.xres, o == kOob ? kOob : o + 64u, stage(b) + wave * 2048 + 1024);
+  };
+  uint32_t soff[MS], sx[MS], nx[MS], sw[2], nw[2];
 #pragma unroll
-    for (int i = 0; i < MS; ++i) {
-      const uint32_t r = rows.row(a, m0, i * 16 + lr, i * 16 + lr < n);
-      soff[i] = r != kOob ? r * (uint32_t)ks : kOob;
-    }
-    auto load_scales = [&](int t) {  // of four steps; past K those of the last four again (their codes are zeros)
-      const int at = min(t, ks - 4);
-#pragma unroll
-      for (int i = 0; i < MS; ++i)
-        nx[i] =
-            (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rows.sres, soff[i] == kOob ? kOob : soff[i] + (uint32_t)at, 0, 0);
-#pragma unroll
-      for (int b = 0; b < 2; ++b) nw[b] = scalar_load(wscale + (SWIGLU ? b * ks : 0) + at);
-    };
-    f32x4 acc[MS][2];
+  for (int i = 0; i < MS; ++i) {
+    const uint32_t r = rows.row(a, m0, i * 16 + lr, n);
+    soff[i] = r != kOob ? r * (uint32_t)ks : kOob;
+  }
+  auto load_scales = [&](int t) {  // of four steps; past K those of the last four again (their codes are zeros)
+    const int at = min(t, ks - 4);
 #pragma unroll
     for (int i = 0; i < MS; ++i)
+      nx[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rows.sres, soff[i] == kOob ? kOob : soff[i] + (uint32_t)at, 0, 0);
 #pragma unroll
-      for (int b = 0; b < 2; ++b) acc[i][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-    load_scales(0);
+    for (int b = 0; b < 2; ++b) nw[b] = scalar_load(wscale + (SWIGLU ? b * ks : 0) + at);
+  };
+  f32x4 acc[MS][2];
 #pragma unroll
-    for (int b = 0; b < D; ++b) load_x(b, b);
-    __builtin_amdgcn_sched_barrier(0);  // the waits count on rows before weights
+  for (int i = 0; i < MS; ++i)
 #pragma unroll
-    for (int j = 0; j < R; ++j) load_w(j, j);
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(4 * R) : "memory");  // the first stages are there
-    auto bar = [&]() {
+    for (int b = 0; b < 2; ++b) acc[i][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  load_scales(0);
+#pragma unroll
+  for (int b = 0; b < D; ++b) load_x(b, b);
+  __builtin_amdgcn_sched_barrier(0);  // the waits count on rows before weights
+#pragma unroll
+  for (int j = 0; j < R; ++j) load_w(j, j);
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(4 * R) : "memory");  // the first stages are there
+  auto bar = [&]() {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  bar();
+  for (int t0 = 0; t0 < kt; t0 += R) {
+    const uint32_t keep = kt - t0 >= 4 ? ~0u : (1u << (8 * (kt - t0))) - 1u;  // the padding's scales are not looked at
+#pragma unroll
+    for (int i = 0; i < MS; ++i) sx[i] = nx[i] & keep;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) sw[b] = nw[b] & keep;
+    load_scales(t0 + R);
+    auto step = [&](auto jc) {
+      constexpr int J = decltype(jc)::value;
+      const int t = t0 + J;
+      load_x(t + D, (J + D) % R);  // the stage read in step t - 1, which every wave has left
       __builtin_amdgcn_sched_barrier(0);
-      __builtin_amdgcn_s_barrier();
-      __builtin_amdgcn_sched_barrier(0);
+      const uint8_t *st = stage(J) + lane * 16;
+#pragma unroll
+      for (int i = 0; i < MS; ++i) {
+        const i32x8 x = fp8_operand(*reinterpret_cast<const u32x4 *>(st + i * 2048),
+                                    *reinterpret_cast<const u32x4 *>(st + i * 2048 + 1024));
+#pragma unroll
+        for (int b = 0; b < 2; ++b) acc[i][b] = mfma_fp8_16<J>(w[J][b], x, acc[i][b], sw[b], sx[i]);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // loads into registers still in use would get others, copied after a wait
+      load_w(J, t + R);
+      // step t + 1's rows, loaded in step t + 1 - D, are there when at most the loads behind them are in flight
+      // (weights of that step, rows and weights of the steps since; the scales may lie between as well)
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(4 + 6 * (D - 1)) : "memory");
+      bar();
     };
-    bar();
-    for (int t0 = 0; t0 < kt; t0 += R) {
-      const uint32_t keep = kt - t0 >= 4 ? ~0u : (1u << (8 * (kt - t0))) - 1u;  // the padding's scales are not looked at
+    step(std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 1>{});
+    step(std::integral_constant<int, 2>{});
+    step(std::integral_constant<int, 3>{});
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no write to LDS may outlive its rows
+  __syncthreads();
+  if constexpr (SWIGLU) {
+    const int col = nb * 128 + wave * 16 + lg * 4;
 #pragma unroll
-      for (int i = 0; i < MS; ++i) sx[i] = nx[i] & keep;
+    for (int i = 0; i < MS; ++i) {
+      float top = 0.0f;
 #pragma unroll
-      for (int b = 0; b < 2; ++b) sw[b] = nw[b] & keep;
-      load_scales(t0 + R);
-      auto step = [&](auto jc) {
-        constexpr int J = decltype(jc)::value;
-        const int t = t0 + J;
-        load_x(t + D, (J + D) % R);  // the stage read in step t - 1, which every wave has left
-        __builtin_amdgcn_sched_barrier(0);
-        float fw[2];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) fw[b] = fp8_scale<J>(sw[b]);
-        u32x4 wb[4][2];
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            wb[m][b] = fp8_to_bf16(w[J][b][m / 2][2 * (m % 2)], w[J][b][m / 2][2 * (m % 2) + 1], fw[b]);
-            formed_here(wb[m][b]);
-          }
-        __builtin_amdgcn_sched_barrier(0);
-        load_w(J, t + R);
-        const uint8_t *st = stage(J) + lane * 16;
-#pragma unroll
-        for (int i = 0; i < MS; ++i) {
-          if (i && i >= ms) break;
-          const float fx = fp8_scale<J>(sx[i]);
-          const u32x4 x[2] = {*reinterpret_cast<const u32x4 *>(st + i * 2048),
-                              *reinterpret_cast<const u32x4 *>(st + i * 2048 + 1024)};
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const u32x4 xb = fp8_to_bf16(x[m / 2][2 * (m % 2)], x[m / 2][2 * (m % 2) + 1], fx);
-#pragma unroll
-            for (int b = 0; b < 2; ++b) acc[i][b] = mfma16(wb[m][b], xb, acc[i][b]);
-          }
-        }
-        // step t + 1's rows, loaded in step t + 1 - D, are there when at most the loads behind them are in flight
-        // (weights of that step, rows and weights of the steps since; the scales may lie between as well)
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(4 + 6 * (D - 1)) : "memory");
-        bar();
-      };
-      step(std::integral_constant<int, 0>{});
-      step(std::integral_constant<int, 1>{});
-      step(std::integral_constant<int, 2>{});
-      step(std::integral_constant<int, 3>{});
+      for (int j = 0; j < 4; ++j) {
+        acc[i][0][j] = silu_f32(acc[i][0][j]) * acc[i][1][j];
+        top = fmaxf(top, fp8_magnitude(acc[i][0][j]));
+      }
+      top = fmaxf(top, __shfl_xor(top, 16, 64));
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      if (lg == 0) tops[wave][i * 16 + lr] = top;
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no write to LDS may outlive its rows
     __syncthreads();
-    if constexpr (SWIGLU) {
-      const int col = nb * 128 + wave * 16 + lg * 4;
 #pragma unroll
-      for (int i = 0; i < MS; ++i) {
-        if (i >= ms) break;
-        float top = 0.0f;
+    for (int i = 0; i < MS; ++i) {
+      float top = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          acc[i][0][j] = silu_f32(acc[i][0][j]) * acc[i][1][j];
-          top = fmaxf(top, fp8_magnitude(acc[i][0][j]));
-        }
-        top = fmaxf(top, __shfl_xor(top, 16, 64));
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
-        if (lg == 0) tops[wave][i * 16 + lr] = top;
-      }
-      __syncthreads();
+      for (int v = 0; v < 8; ++v) top = fmaxf(top, tops[v][i * 16 + lr]);
+      const int64_t row = m0 + i * 16 + lr;
+      const float h[4] = {acc[i][0][0], acc[i][0][1], acc[i][0][2], acc[i][0][3]};
+      if (row < m0 + n) store_h(a, h, top, row, nb, col, wave == 0 && lg == 0);
+    }
+    __syncthreads();
+  } else {
 #pragma unroll
-      for (int i = 0; i < MS; ++i) {
-        if (i >= ms) break;
-        float top = 0.0f;
+    for (int i = 0; i < MS; ++i) {
+      const int64_t row = m0 + i * 16 + lr;
+      if (row < m0 + n)
 #pragma unroll
-        for (int v = 0; v < 8; ++v) top = fmaxf(top, tops[v][i * 16 + lr]);
-        const int64_t row = m0 + i * 16 + lr;
-        const float h[4] = {acc[i][0][0], acc[i][0][1], acc[i][0][2], acc[i][0][3]};
-        if (row < end) store_h(a, h, top, row, nb, col, wave == 0 && lg == 0);
-      }
-      __syncthreads();
-    } else {
-#pragma unroll
-      for (int i = 0; i < MS; ++i) {
-        if (i >= ms) break;
-        const int64_t row = m0 + i * 16 + lr;
-        if (row < end)
-#pragma unroll
-          for (int b = 0; b < 2; ++b) store_y(a, acc[i][b], row, (unit + b) * 16 + lg * 4);
-      }
+        for (int b = 0; b < 2; ++b) store_y(a, acc[i][b], row, (unit + b) * 16 + lg * 4);
+    }
+  }
+}
+
+template <bool SWIGLU>
+__global__ __launch_bounds__(512) void fp8_medium_kernel(const Fp8GemmArgs a) {
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[MD_STAGE], s1[MD_STAGE], s2[MD_STAGE], s3[MD_STAGE];
+  __shared__ float tops[SWIGLU ? 8 : 1][MD_ROWS];
+  const int nb = blockIdx.x, g = fp8_nth_group(a, blockIdx.y, a.xp ? kFp8FewRows : INT_MAX);  // (others: the large kernel's)
+  if (g < 0) return;
+  int begin, end;
+  fp8_group_rows_uniform(a, g, begin, end);
+  for (int m0 = begin; m0 < end; m0 += MD_ROWS) {
+    const int n = min(MD_ROWS, end - m0);
+    switch ((n + 15) / 16) {
+#define MOE_ROWS(MS) \
+  case MS: medium_rows<SWIGLU, MS>(a, g, nb, m0, n, s0, s1, s2, s3, tops); break
+      MOE_ROWS(1);
+      MOE_ROWS(2);
+      MOE_ROWS(3);
+      MOE_ROWS(4);
+      MOE_ROWS(5);
+      MOE_ROWS(6);
+      MOE_ROWS(7);
+      MOE_ROWS(8);
+#undef MOE_ROWS
     }
   }
 }
@@ -386,16 +395,28 @@ __global__ __launch_bounds__(512) void fp8_medium_kernel(const Fp8GemmArgs a) {
 
 hipError_t launch_fp8_gemm(const Fp8GemmArgs &a, hipStream_t s) {
   const bool swiglu = a.h8 != nullptr;
-  auto grid = [&](int cols) { return dim3((unsigned)(a.num_groups * ((a.n_out + cols - 1) / cols))); };
+  const int groups = std::min(a.num_groups, a.rows_max);
+  auto grid = [&](int cols) { return dim3((unsigned)((a.n_out + cols - 1) / cols), (unsigned)groups); };
   if (a.xp) {
     const hipError_t e = launch_fp8_gemm_large(a, s);
     if (e != hipSuccess) return e;
   }
   if (std::min(a.group_rows_max, a.rows_max) <= 16) {
-    if (swiglu)
+#ifndef SMALL_U
+#define SMALL_U 2
+#define SMALL_KS 4
+#endif
+    if (swiglu) {
+      if (a.h32) {
+        // (columns behind the last: zeros of weights that do not exist)
+        hipLaunchKernelGGL((fp8_small_kernel<true, SMALL_U, SMALL_KS>), dim3(fp8_row_bytes(a.n_out) / (16 * SMALL_U), (unsigned)groups), dim3(64 * SMALL_U * SMALL_KS), 0, s, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        return launch_quantize_rows(a.h32, true, a.rows_max, fp8_row_bytes(a.n_out), a.h8, a.h_scale, s);
+      }
       hipLaunchKernelGGL((fp8_small_kernel<true, 8, 1>), grid(128), dim3(512), 0, s, a);
-    else
-      hipLaunchKernelGGL((fp8_small_kernel<false, 8, 1>), grid(128), dim3(512), 0, s, a);
+    } else
+      hipLaunchKernelGGL((fp8_small_kernel<false, SMALL_U, SMALL_KS>), grid(16 * SMALL_U), dim3(64 * SMALL_U * SMALL_KS), 0, s, a);
   } else {
     if (swiglu)
       hipLaunchKernelGGL((fp8_medium_kernel<true>), grid(128), dim3(512), 0, s, a);

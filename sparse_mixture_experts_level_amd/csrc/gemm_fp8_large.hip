@@ -88,10 +88,7 @@ __global__ __launch_bounds__(512, 1) void fp8_large_kernel(const Fp8GemmArgs a, 
   mt_count = __builtin_amdgcn_readfirstlane(mt_count);
   const int local = lin - mt_first * n_tiles;
   int begin, end;
-  fp8_group_rows(a, g, begin, end);
-  // equal in every lane: kept, with all that derives from them, in scalar registers
-  begin = __builtin_amdgcn_readfirstlane(begin);
-  end = __builtin_amdgcn_readfirstlane(end);
+  fp8_group_rows_uniform(a, g, begin, end);
   int mt, nt;
   if (end - begin <= (SWIGLU ? 2 : 1) * a.n_out) {  // the weights are larger: their tile outermost
     nt = local / mt_count;
@@ -357,7 +354,7 @@ __global__ __launch_bounds__(256) void fp8_pack_rows_kernel(const Fp8GemmArgs a,
 }  // namespace
 
 hipError_t launch_fp8_pack_rows(const Fp8GemmArgs &a, uint8_t *xp, uint8_t *xp_scale, hipStream_t s) {
-  const int64_t grid = fp8_large_tiles_max(a.rows_max) * (fp8_scale_bytes(a.K) / 4);
+  const int64_t grid = fp8_large_tiles_max(a.rows_max, a.num_groups) * (fp8_scale_bytes(a.K) / 4);
   if (grid == 0) return hipSuccess;
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
   hipLaunchKernelGGL(fp8_pack_rows_kernel, dim3((unsigned)grid), dim3(256), 0, s, a, xp, xp_scale);
@@ -367,7 +364,7 @@ hipError_t launch_fp8_pack_rows(const Fp8GemmArgs &a, uint8_t *xp, uint8_t *xp_s
 hipError_t launch_fp8_gemm_large(const Fp8GemmArgs &a, hipStream_t s) {
   const bool swiglu = a.hp != nullptr;
   const int n_tiles = (a.n_out + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256);
-  const int64_t grid = fp8_large_tiles_max(a.rows_max) * n_tiles;
+  const int64_t grid = fp8_large_tiles_max(a.rows_max, a.num_groups) * n_tiles;
   if (grid == 0) return hipSuccess;
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
   if (swiglu)

@@ -240,6 +240,7 @@ struct Fp8GemmArgs {
   const uint8_t *w8, *w_scale;
   uint16_t *y;
   uint8_t *h8, *h_scale;
+  float *h32;  // room for H before it is quantised [rows_max, fp8_row_bytes(n_out)], or NULL: few rows in many workgroups
   int num_groups, rows_max, group_rows_max, x_rows, n_out, K;
   // Groups of more than kFp8FewRows go through a kernel for many rows, which reads them (and writes H) in packed
   // tiles of fp8_packed_bytes(); xp and hp are NULL where no group can have that many.
@@ -254,12 +255,18 @@ __host__ __device__ inline int fp8_large_tiles(int rows) {
   return rows <= kFp8FewRows ? 0 : (rows + kFp8LargeRows - 1) / kFp8LargeRows;
 }
 __host__ __device__ inline int fp8_tile_rows(int rows, int tiles) { return (rows + 32 * tiles - 1) / (32 * tiles) * 32; }
-// A bound on the tiles of rows in all: two of 257 rows are the most for their number.
-inline int64_t fp8_large_tiles_max(int64_t rows) { return 2 * rows / 257; }
+// A bound on the tiles of rows in all G groups: a last one each beside whole ones, and two of 257 rows are the most for
+// their number.  (Workgroups past the real tiles only leave, but each holds a CU until it has read the offsets.)
+inline int64_t fp8_large_tiles_max(int64_t rows, int G) {
+  const int64_t a = 2 * rows / 257, b = rows / kFp8LargeRows + G;
+  return a < b ? a : b;
+}
 // Their bytes: codes, scales.
-inline int64_t fp8_packed_bytes(int64_t rows, int k) { return fp8_large_tiles_max(rows) * kFp8LargeRows * fp8_row_bytes(k); }
-inline int64_t fp8_packed_scale_bytes(int64_t rows, int k) {
-  return fp8_large_tiles_max(rows) * kFp8LargeRows * fp8_scale_bytes(k);
+inline int64_t fp8_packed_bytes(int64_t rows, int G, int k) {
+  return fp8_large_tiles_max(rows, G) * kFp8LargeRows * fp8_row_bytes(k);
+}
+inline int64_t fp8_packed_scale_bytes(int64_t rows, int G, int k) {
+  return fp8_large_tiles_max(rows, G) * kFp8LargeRows * fp8_scale_bytes(k);
 }
 // x8 (through row_index) and its scales to packed tiles.
 hipError_t launch_fp8_pack_rows(const Fp8GemmArgs &a, uint8_t *xp, uint8_t *xp_scale, hipStream_t s);
