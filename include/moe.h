@@ -624,9 +624,10 @@ moe_status moe_dequantize_rows_fp8(int64_t rows, int32_t k, int32_t dtype, const
  * the products read (written once, when weights are loaded).  swiglu 0: w [G, n_out, K];
  * 1: w [G, 2 n_out, K], gate rows then up rows (moe_weights.w_gate_up with n_out = f), whose
  * blocks are those of the gate rows and of the up rows apart.
- *   codes  per group, blocks of 16 rows by 128 of K, 2 KB each, ordered [ceil(n_out / 16)][ceil(K /
- *          128)] (swiglu: [ceil(n_out / 16)][2][ceil(K / 128)], gate then up); within one, byte
- *          1024 p + 256 c + 16 r + i is row r, k = 64 p + 16 c + i; zeros where the matrix has ended
+ *   codes  per group, blocks of 16 rows (swiglu: gate and up blocks in turn), B in all, in tiles of 16
+ *          blocks (the last one of the b <= 16 left): tile t begins at byte 16 t ceil(K / 128) 2048 and holds,
+ *          ordered [ceil(K / 128)][2][b], pieces of 1 KB, 16 rows by 64 of K, in which byte
+ *          256 c + 16 r + i is row r, k = 16 c + i of the 64; zeros where the matrix has ended
  *   scale  per group [ceil(n_out / 128)][moe_fp8_scale_bytes(K)] (swiglu: [ceil(n_out / 128)][2][...])
  * Sizes in bytes from the two helpers (host only; 0 for invalid arguments).  Scales and codes
  * as for rows.  One group's codes must be below 2 GiB (MOE_ERR_UNSUPPORTED). */

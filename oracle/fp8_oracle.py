@@ -99,16 +99,18 @@ def fp8_pack_weights(matrices):
     matrix, or of the gate and of the up rows."""
     N, K = matrices[0][0].shape
     H, nt, kt, nb = len(matrices), -(-N // 16), -(-K // BLOCK), -(-N // BLOCK)
-    ks = -(-kt // 4) * 4
-    out = np.zeros((nt, H, kt, 2048), dtype=np.uint8)
+    ks, blocks = -(-kt // 4) * 4, nt * H
+    out = np.zeros(blocks * kt * 2048, dtype=np.uint8)
     scale = np.full((nb, H, ks), 127, dtype=np.uint8)
     for h, (codes, e) in enumerate(matrices):
         for n in range(N):
             for k in range(K):
-                p, c, i = (k % 128) // 64, (k % 64) // 16, k % 16
-                out[n // 16, h, k // 128, 1024 * p + 256 * c + 16 * (n % 16) + i] = codes[n, k]
+                block = n // 16 * H + h
+                tile, b = block // 16, min(16, blocks - block // 16 * 16)
+                piece = (k // 64) * b + block % 16
+                out[tile * 16 * kt * 2048 + piece * 1024 + 256 * (k % 64 // 16) + 16 * (n % 16) + k % 16] = codes[n, k]
         scale[:, h, :kt] = e + 127
-    return out.reshape(-1), scale.reshape(-1)
+    return out, scale.reshape(-1)
 
 
 def rms_norm(x, residual, weight, eps, held=lambda a: a):

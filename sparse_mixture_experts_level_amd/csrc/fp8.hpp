@@ -9,11 +9,13 @@
 // Rows: codes [rows, fp8_row_bytes(K)] with zeros behind K, scales [rows, fp8_scale_bytes(K)], one byte
 // per 128 columns; the bytes behind the last block are padding (to a multiple of four, so that four
 // blocks' scales are one aligned load) and are not looked at.
-// Weights of a group, [N, K]: blocks of 16 rows x 128 of K, 2 KB each, in the order [N / 16][K / 128];
-// within a block the 16 bytes k = 64 p + 16 c .. + 15 of row r stand at 1024 p + 256 c + 16 r, which
-// is the matrix instructions' operand layout: a wave's load of half a block is 1 KB of consecutive
-// bytes.  gate_up matrices alternate blocks of gate rows and of the matching up rows.  Scales
-// [N / 128][fp8_scale_bytes(K)] (gate_up: [f / 128][2][...], gate then up).
+// Weights of a group, [N, K]: blocks of 16 rows (gate_up matrices alternate blocks of gate rows and of the
+// matching up rows), tiles of 16 blocks (the last has what is left, b <= 16), and in a tile the pieces
+// [K / 128][2][b] of 1 KB: 16 rows x 64 of K as [4 chunks of 16 codes][16 rows], the matrix instructions' operand layout.
+// So a wave's load is 1 KB of consecutive bytes, and a workgroup of 256 rows walks one region of memory, 32 KB a step,
+// whatever K is: with each block's K on its own, workgroups in step read addresses a power of two
+// apart for such K, on few memory channels.  Scales [N / 128][fp8_scale_bytes(K)] (gate_up: [f / 128][2][...],
+// gate then up).
 #pragma once
 
 #include "common.hpp"
@@ -21,7 +23,7 @@
 
 namespace moe {
 
-constexpr int kFp8Tile = 2048;  // bytes of a 16 x 128 block of weights
+constexpr int kFp8Tile = 2048;  // bytes of 16 x 128 codes
 
 // Eight consecutive values as they are held, loaded and stored as 16-byte pieces at any alignment of the
 // element's own size (the vector memory path takes unaligned addresses).  `n` of them exist (n <= 0: none; the
@@ -125,24 +127,33 @@ __device__ __forceinline__ void fp8_group_rows_uniform(const Fp8GemmArgs &a, int
   begin = __builtin_amdgcn_readfirstlane(begin);
   end = __builtin_amdgcn_readfirstlane(end);
 }
-// The n-th group (from 0) of more than 0 and at most `most` rows, the same in every lane; -1: there are not that many.  A
-// launch has as many workgroups as groups can have rows, not as there are groups: one of an empty group holds
-// its CU until it has read the offsets (a decode step of one token, 4 of 32 experts: 20 us for 12).
-__device__ __forceinline__ int fp8_nth_group(const Fp8GemmArgs &a, int n, int most) {
+// The n-th group (from 0) of more than 0 and at most `most` rows and its rows, in scalar registers; -1: there are not that
+// many.  A launch has as many workgroups as groups can have rows, not as there are groups: one of an empty group holds its
+// CU until it has read the offsets.
+__device__ __forceinline__ int fp8_nth_group(const Fp8GemmArgs &a, int n, int most, int &begin, int &end) {
   const int lane = threadIdx.x & 63;
   int seen = 0;
   for (int g0 = 0; g0 < a.num_groups; g0 += 64) {
-    int begin = 0, end = 0;
-    if (g0 + lane < a.num_groups) fp8_group_rows(a, g0 + lane, begin, end);
-    const uint64_t some = __ballot(end > begin && end - begin <= most);
+    int b = 0, e = 0;
+    if (g0 + lane < a.num_groups) fp8_group_rows(a, g0 + lane, b, e);
+    const uint64_t some = __ballot(e > b && e - b <= most);
     const int count = __popcll(some);
     if (n < seen + count) {
       const bool mine = (some >> lane & 1) && __popcll(some & ((1ull << lane) - 1)) == n - seen;
-      return __builtin_amdgcn_readfirstlane(g0 + __ffsll((unsigned long long)__ballot(mine)) - 1);
+      const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)__ballot(mine)) - 1);
+      begin = __builtin_amdgcn_readlane(b, l);
+      end = __builtin_amdgcn_readlane(e, l);
+      return g0 + l;
     }
     seen += count;
   }
   return -1;
+}
+// Where a block's piece (k step 0, first half) stands in its group, and the distance from half a step to the next.
+__device__ __forceinline__ uint32_t fp8_block_offset(int block, int blocks, int kt, uint32_t &half) {
+  const int tile = block / 16;
+  half = (uint32_t)min(16, blocks - tile * 16) * 1024u;
+  return (uint32_t)(tile * 16 * kt) * 2048u + (uint32_t)(block % 16) * 1024u;
 }
 // Bytes of one group's codes.
 __host__ __device__ __forceinline__ int64_t fp8_group_bytes(int n_out, int k, bool swiglu) {

@@ -12,6 +12,7 @@
 // sum: enough to move one code of H in two thousand).
 #include <algorithm>
 #include <climits>
+#include <cstdlib>
 
 #include "fp8.hpp"
 #include "kernels.hpp"
@@ -64,17 +65,13 @@ __device__ __forceinline__ void store_y(const Fp8GemmArgs &a, f32x4 v, int64_t r
   }
 }
 
-// The compiler sinks conversions to their uses, past the loads that refill their operands' registers, which would
-// then get other registers and be copied after a wait: this keeps a value where it is formed.
-__device__ __forceinline__ void formed_here(u32x4 &v) { asm volatile("" : "+v"(v)); }
-
 // Few rows: 16 of them at a time, one block after the other.  A workgroup has 16 U output columns; each wave 16
 // of them (for gate_up the 16 gate and the 16 up rows) and one of KS parts of K, whose sums the first
 // part's waves add in order.  Rows are read from the caches in the operand layout, two steps ahead, with the weights,
 // R steps of 128 ahead, all in registers: no LDS, no barrier.  The weights are the
 // matrix instruction's first operand, so that a lane holds four consecutive columns of one row.
 template <bool SWIGLU, int U, int KS>
-__global__ __launch_bounds__(64 * U * KS) void fp8_small_kernel(const Fp8GemmArgs a) {
+__global__ __launch_bounds__(64 * U * KS, 4) void fp8_small_kernel(const Fp8GemmArgs a) {
   constexpr int NB = SWIGLU ? 2 : 1, R = SWIGLU ? 4 : 8, XR = 2;
   constexpr bool QUANTISE = SWIGLU && U == 8;  // a block of H's columns a workgroup
   __shared__ float tops[QUANTISE ? 8 : 1][16];
@@ -82,16 +79,18 @@ __global__ __launch_bounds__(64 * U * KS) void fp8_small_kernel(const Fp8GemmArg
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lr = lane & 15,
             lg = lane >> 4;
   const int u = wave % U, part = wave / U;
-  const int nb = blockIdx.x, g = fp8_nth_group(a, blockIdx.y, INT_MAX);
-  if (g < 0) return;
   int begin, end;
-  fp8_group_rows_uniform(a, g, begin, end);
+  const int nb = blockIdx.x, g = fp8_nth_group(a, blockIdx.y, INT_MAX, begin, end);
+  if (g < 0) return;
   const int kt = fp8_blocks(a.K), kp = fp8_row_bytes(a.K), ks = fp8_scale_bytes(a.K);
-  const int tb = kt * part / KS, te = kt * (part + 1) / KS;
+  // parts of K are whole words of scales: four steps
+  const int quads = ks / 4, tb = 4 * (quads * part / KS), te = min(kt, 4 * (quads * (part + 1) / KS));
   const int unit = nb * U + u, units = (a.n_out + 15) / 16;
   const int64_t wbytes = fp8_group_bytes(a.n_out, a.K, SWIGLU);
   const rsrc_t wres = make_rsrc(a.w8 + g * wbytes, (uint32_t)wbytes);
-  const uint32_t woff = unit < units ? (uint32_t)(unit * NB * kt * kFp8Tile + lane * 16) : kOob;
+  uint32_t half;  // (gate and up blocks are neighbours)
+  const uint32_t wbase = fp8_block_offset(unit * NB, units * NB, kt, half) + (uint32_t)lane * 16u;
+  const int tw = unit < units ? te : 0;  // no weights past the last block
   const uint8_t *wscale = a.w_scale + ((int64_t)g * fp8_blocks(a.n_out) + min(unit, units - 1) / 8) * NB * ks;
   for (int m0 = begin; m0 < end; m0 += 16) {
     u32x4 w[R][NB][2], x[XR][2];
@@ -99,9 +98,9 @@ __global__ __launch_bounds__(64 * U * KS) void fp8_small_kernel(const Fp8GemmArg
     auto load_w = [&](int j, int t) {  // steps past the part's end read zeros
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const uint32_t o = t < te && woff != kOob ? woff + (uint32_t)((b * kt + t) * kFp8Tile) : kOob;
+        const uint32_t o = t < tw ? wbase + (uint32_t)(2 * t) * half + (uint32_t)b * 1024u : kOob;
         w[j][b][0] = buf_ld16_nt(wres, o);
-        w[j][b][1] = buf_ld16_nt(wres, o == kOob ? kOob : o + 1024u);
+        w[j][b][1] = buf_ld16_nt(wres, t < tw ? o + half : kOob);
       }
     };
 #pragma unroll
@@ -115,15 +114,11 @@ __global__ __launch_bounds__(64 * U * KS) void fp8_small_kernel(const Fp8GemmArg
       x[j][0] = buf_ld16(rows.xres, o);
       x[j][1] = buf_ld16(rows.xres, o == kOob ? kOob : o + 64u);
     };
-    // Scales of four steps from any one on, out of two aligned words; past K some others (their codes are zeros).
-    auto load_scales = [&](int t) {
-      const int lo = min(t & ~3, ks - 4), hi = min(lo + 4, ks - 4);
-      nx = __builtin_amdgcn_alignbyte(
-          (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rows.sres, soff == kOob ? kOob : soff + (uint32_t)hi, 0, 0),
-          (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rows.sres, soff == kOob ? kOob : soff + (uint32_t)lo, 0, 0), t & 3);
+    auto load_scales = [&](int t) {  // of four steps; past K those of the last four again (their codes are zeros)
+      const int at = min(t, ks - 4);
+      nx = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rows.sres, soff == kOob ? kOob : soff + (uint32_t)at, 0, 0);
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
-        nw[b] = (uint32_t)(((uint64_t)scalar_load(wscale + b * ks + hi) << 32 | scalar_load(wscale + b * ks + lo)) >> (8 * (t & 3)));
+      for (int b = 0; b < NB; ++b) nw[b] = scalar_load(wscale + b * ks + at);
     };
     load_scales(tb);
 #pragma unroll
@@ -146,24 +141,17 @@ __global__ __launch_bounds__(64 * U * KS) void fp8_small_kernel(const Fp8GemmArg
           for (int b = 0; b < NB; ++b) sw[b] = nw[b] & keep;
           load_scales(t + 4);
         }
-        u32x4 xb[4], wb[4][NB];
 #pragma unroll
         for (int m = 0; m < 4; ++m) {  // 32 of K: eight of each lane's 32 codes
-          xb[m] = fp8_to_bf16(x[J % XR][m / 2][2 * (m % 2)], x[J % XR][m / 2][2 * (m % 2) + 1], fp8_scale<S>(sx));
-          formed_here(xb[m]);
+          const u32x4 xb = fp8_to_bf16(x[J % XR][m / 2][2 * (m % 2)], x[J % XR][m / 2][2 * (m % 2) + 1], fp8_scale<S>(sx));
 #pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            wb[m][b] = fp8_to_bf16(w[J][b][m / 2][2 * (m % 2)], w[J][b][m / 2][2 * (m % 2) + 1], fp8_scale<S>(sw[b]));
-            formed_here(wb[m][b]);
-          }
+          for (int b = 0; b < NB; ++b)
+            acc[b] = mfma16(fp8_to_bf16(w[J][b][m / 2][2 * (m % 2)], w[J][b][m / 2][2 * (m % 2) + 1], fp8_scale<S>(sw[b])), xb,
+                            acc[b]);
         }
-        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_sched_barrier(0);  // loads into registers still in use would get others, copied after a wait
         load_x(J % XR, t + XR);
         load_w(J, t + R);
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-          for (int b = 0; b < NB; ++b) acc[b] = mfma16(wb[m][b], xb[m], acc[b]);
       };
       step(std::integral_constant<int, 0>{});
       step(std::integral_constant<int, 1>{});
@@ -240,9 +228,8 @@ __device__ __forceinline__ void medium_rows(const Fp8GemmArgs &a, int g, int nb,
   const int units = (a.n_out + 15) / 16 * (SWIGLU ? 2 : 1), unit = nb * 16 + wave * 2;  // blocks of 16 weight rows
   const int64_t wbytes = fp8_group_bytes(a.n_out, a.K, SWIGLU);
   const rsrc_t wres = make_rsrc(a.w8 + g * wbytes, (uint32_t)wbytes);
-  uint32_t woff[2];
-#pragma unroll
-  for (int b = 0; b < 2; ++b) woff[b] = unit + b < units ? (uint32_t)((unit + b) * kt * kFp8Tile + lane * 16) : kOob;
+  uint32_t half;
+  const uint32_t wbase = fp8_block_offset(unit, units, kt, half) + (uint32_t)lane * 16u;
   const int sblocks = fp8_blocks(a.n_out);
   const uint8_t *wscale =
       a.w_scale + ((int64_t)g * sblocks + (SWIGLU ? nb : min(nb * 2 + wave / 4, sblocks - 1))) * (SWIGLU ? 2 : 1) * ks;
@@ -250,8 +237,9 @@ __device__ __forceinline__ void medium_rows(const Fp8GemmArgs &a, int g, int nb,
   auto load_w = [&](int j, int t) {
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      const uint32_t o = t < kt && woff[b] != kOob ? woff[b] + (uint32_t)(t * kFp8Tile) : kOob;
-      w[j][b] = fp8_operand(buf_ld16_nt(wres, o), buf_ld16_nt(wres, o == kOob ? kOob : o + 1024u));
+      const bool in = t < kt && unit + b < units;
+      const uint32_t o = wbase + (uint32_t)(2 * t) * half + (uint32_t)b * 1024u;
+      w[j][b] = fp8_operand(buf_ld16_nt(wres, in ? o : kOob), buf_ld16_nt(wres, in ? o + half : kOob));
     }
   };
   const Fp8Rows rows(a, m0, n);
@@ -369,10 +357,9 @@ template <bool SWIGLU>
 __global__ __launch_bounds__(512) void fp8_medium_kernel(const Fp8GemmArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t s0[MD_STAGE], s1[MD_STAGE], s2[MD_STAGE], s3[MD_STAGE];
   __shared__ float tops[SWIGLU ? 8 : 1][MD_ROWS];
-  const int nb = blockIdx.x, g = fp8_nth_group(a, blockIdx.y, a.xp ? kFp8FewRows : INT_MAX);  // (others: the large kernel's)
-  if (g < 0) return;
   int begin, end;
-  fp8_group_rows_uniform(a, g, begin, end);
+  const int nb = blockIdx.x, g = fp8_nth_group(a, blockIdx.y, a.xp ? kFp8FewRows : INT_MAX, begin, end);
+  if (g < 0) return;  // (groups of more rows: the large kernel's)
   for (int m0 = begin; m0 < end; m0 += MD_ROWS) {
     const int n = min(MD_ROWS, end - m0);
     switch ((n + 15) / 16) {
@@ -402,21 +389,15 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs &a, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   if (std::min(a.group_rows_max, a.rows_max) <= 16) {
-#ifndef SMALL_U
-#define SMALL_U 2
-#define SMALL_KS 4
-#endif
-    if (swiglu) {
-      if (a.h32) {
-        // (columns behind the last: zeros of weights that do not exist)
-        hipLaunchKernelGGL((fp8_small_kernel<true, SMALL_U, SMALL_KS>), dim3(fp8_row_bytes(a.n_out) / (16 * SMALL_U), (unsigned)groups), dim3(64 * SMALL_U * SMALL_KS), 0, s, a);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        return launch_quantize_rows(a.h32, true, a.rows_max, fp8_row_bytes(a.n_out), a.h8, a.h_scale, s);
-      }
+    const int ss = getenv("SS") ? atoi(getenv("SS")) : 1;
+    if (swiglu && ss == 2)
+      hipLaunchKernelGGL((fp8_small_kernel<true, 8, 2>), grid(128), dim3(1024), 0, s, a);
+    else if (swiglu)
       hipLaunchKernelGGL((fp8_small_kernel<true, 8, 1>), grid(128), dim3(512), 0, s, a);
-    } else
-      hipLaunchKernelGGL((fp8_small_kernel<false, SMALL_U, SMALL_KS>), grid(16 * SMALL_U), dim3(64 * SMALL_U * SMALL_KS), 0, s, a);
+    else if ((int64_t)groups * ((a.n_out + 63) / 64) < 128)
+      hipLaunchKernelGGL((fp8_small_kernel<false, 2, 2>), grid(32), dim3(256), 0, s, a);
+    else
+      hipLaunchKernelGGL((fp8_small_kernel<false, 4, 1>), grid(64), dim3(256), 0, s, a);
   } else {
     if (swiglu)
       hipLaunchKernelGGL((fp8_medium_kernel<true>), grid(128), dim3(512), 0, s, a);

@@ -113,21 +113,22 @@ __global__ __launch_bounds__(512, 1) void fp8_large_kernel(const Fp8GemmArgs a, 
   const rsrc_t wres = make_rsrc(a.w8 + g * wbytes, (uint32_t)wbytes);
   const rsrc_t sres = make_rsrc(a.xp_scale + (int64_t)m_tile * kFp8LargeRows * ks, (uint32_t)(kFp8LargeRows * ks));
   // this wave's pieces of a stage: 16-row blocks 2 wave and 2 wave + 1 of both operands
-  uint32_t aoff[2], boff[2];
-  const uint32_t stride = (uint32_t)kt * kFp8Tile;
+  uint32_t aoff[2], boff[2], wstep;
+  const int wblocks = (a.n_out + 15) / 16 * (SWIGLU ? 2 : 1);
+  const uint32_t wtile = fp8_block_offset(nt * 16, wblocks, kt, wstep);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    aoff[i] = wave < row_blocks ? (uint32_t)(2 * wave + i) * stride + (uint32_t)lane * 16u : kOob;
-    const int64_t w = (int64_t)(nt * 16 + 2 * wave + i) * stride;
-    boff[i] = w < wbytes ? (uint32_t)w + (uint32_t)lane * 16u : kOob;
+    const uint32_t at = (uint32_t)(2 * wave + i) * 1024u + (uint32_t)lane * 16u;
+    aoff[i] = wave < row_blocks ? at : kOob;
+    boff[i] = nt * 16 + 2 * wave + i < wblocks ? wtile + at : kOob;
   }
   auto issue = [&](int s, int b) {
-    const uint32_t k = (uint32_t)s * 1024u;
+    const uint32_t ka = (uint32_t)s * (uint32_t)LG_TILE, kb = (uint32_t)s * wstep;
     const bool in = s < nk;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      buf_ld16_lds(ares, in && aoff[i] != kOob ? aoff[i] + k : kOob, bufA(b) + (2 * wave + i) * 1024);
-      buf_ld16_lds(wres, in && boff[i] != kOob ? boff[i] + k : kOob, bufB(b) + (2 * wave + i) * 1024);
+      buf_ld16_lds(ares, in && aoff[i] != kOob ? aoff[i] + ka : kOob, bufA(b) + (2 * wave + i) * 1024);
+      buf_ld16_lds(wres, in && boff[i] != kOob ? boff[i] + kb : kOob, bufB(b) + (2 * wave + i) * 1024);
     }
   };
   const int sblocks = fp8_blocks(a.n_out);
@@ -269,14 +270,13 @@ __global__ __launch_bounds__(512, 1) void fp8_large_kernel(const Fp8GemmArgs a, 
         a.hp_scale[(int64_t)m_tile * kFp8LargeRows * hs + ((nt / 4) * kFp8LargeRows + row) * 4 + nt % 4] = (uint8_t)byte;
     }
     __syncthreads();
-    uint8_t *hp = a.hp + ((int64_t)m_tile * 16 * ht + nt) * kFp8Tile;
+    uint8_t *hp = a.hp + ((int64_t)m_tile * ht + nt) * (2 * LG_TILE);
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
         const int q = threadIdx.x + 512 * v;  // 16-byte piece of the 16 KB
-        stg16(hp + (int64_t)(q >> 6) * ht * kFp8Tile + p * 1024 + (q & 63) * 16,
-              *reinterpret_cast<const u32x4 *>((p ? sA1 : sA0) + q * 16));
+        stg16(hp + p * LG_TILE + q * 16, *reinterpret_cast<const u32x4 *>((p ? sA1 : sA0) + q * 16));
       }
   } else {
     // bf16: each wave's 128 rows x 64 columns through its own 16 KB, 128-byte rows, 16-byte chunk c of row r at
@@ -338,11 +338,11 @@ __global__ __launch_bounds__(256) void fp8_pack_rows_kernel(const Fp8GemmArgs a,
       if (s >= 0 && b < kt) v[i] = ldg16(a.x8 + s * kp + b0 * 128 + c * 16);
     }
     if (b < kt) {
-      uint8_t *o = xp + ((int64_t)m_tile * 16 * kt + b) * kFp8Tile + (c & 7) * 256;
+      uint8_t *o = xp + (((int64_t)m_tile * kt + b) * 2 + (c >> 2 & 1)) * LG_TILE + (c & 3) * 256;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int r = i0 + i * 8 + r0;
-        if (r < 256) stg16(o + (int64_t)(r >> 4) * kt * kFp8Tile + (r & 15) * 16, v[i]);
+        if (r < 256) stg16(o + (r >> 4) * 1024 + (r & 15) * 16, v[i]);
       }
     }
   }

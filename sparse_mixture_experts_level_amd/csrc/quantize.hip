@@ -110,8 +110,10 @@ __global__ __launch_bounds__(256) void quantize_weights_kernel(const T *__restri
   for (int q = threadIdx.x; q < 1024; q += 256) {
     const int blk = q >> 7, pc = (q >> 4) & 7, r = q & 15, t = nb * 8 + blk;
     if (t >= nt) continue;
-    uint8_t *o = codes + ((g * nt + t) * halves + half) * (int64_t)kt * kFp8Tile + (int64_t)kb * kFp8Tile;
-    *reinterpret_cast<u32x4 *>(o + pc * 256 + r * 16) =
+    uint32_t step;
+    const uint32_t at = fp8_block_offset(t * halves + half, nt * halves, kt, step);
+    uint8_t *o = codes + g * fp8_group_bytes(n_out, K, swiglu != 0) + at + (int64_t)(kb * 2 + (pc >> 2)) * step;
+    *reinterpret_cast<u32x4 *>(o + (pc & 3) * 256 + r * 16) =
         *reinterpret_cast<const u32x4 *>(tile + (blk * 16 + r) * 128 + pc * 16);
   }
   uint8_t *so = scale + ((g * fp8_blocks(n_out) + nb) * halves + half) * (int64_t)fp8_scale_bytes(K);

@@ -58,12 +58,16 @@ def test_packed_layout_by_hand():
     codes, e = oracle.fp8_quantize_weights(w)
     out, scale = oracle.fp8_pack_weights([(codes, e)])
     assert out.shape == (2 * 2 * 2048,) and scale.shape == (4,)
-    assert out[1 * 2 * 2048 + 2048 + 1] == codes[16, 129]          # row 16, k 129: block (1, 1), byte 1
-    assert out[1024 + 256 * 2 + 16 * 5 + 3] == codes[5, 64 + 35]   # row 5, k 99: p 1, c 2, i 3
+    # two blocks, one tile: pieces [2 steps][2 halves][2 blocks] of 1 KB
+    assert out[(2 * 2 + 0) * 1024 + 1 * 1024 + 1] == codes[16, 129]     # row 16: block 1; k 129: step 1, half 0, byte 1
+    assert out[(1 * 2 + 0) * 1024 + 256 * 2 + 16 * 5 + 3] == codes[5, 99]  # row 5, k 99: half 1, c 2, i 3
     assert scale[:2].tolist() == (e[0] + 127).tolist()
     both, s2 = oracle.fp8_pack_weights([(codes, e), (codes, e)])
-    both = both.reshape(2, 2, 2, 2048)
-    assert np.array_equal(both[:, 0].reshape(-1), out) and np.array_equal(both[:, 1].reshape(-1), out) and len(s2) == 8
+    both = both.reshape(2, 2, 2, 2, 1024)  # [step][half][block of rows][gate, up]
+    assert np.array_equal(both[:, :, :, 0].reshape(-1), out) and np.array_equal(both[:, :, :, 1].reshape(-1), out) and len(s2) == 8
+    tall = oracle.fp8_quantize_weights(np.arange(290 * 64).reshape(290, 64) % 9 - 4.0)
+    out, _ = oracle.fp8_pack_weights([tall])  # 19 blocks: a tile of 16 and one of 3
+    assert out[16 * 2048 + 1024 * 2 + 16 * 1 + 7] == tall[0][16 * 18 + 1, 7]
 
 
 @pytest.mark.parametrize("with_dh", [False, True])
