@@ -22,6 +22,7 @@
 
 #include "common.hpp"
 #include "kernels.hpp"
+#include "lanes.hpp"
 
 namespace moe {
 

@@ -544,15 +544,17 @@ def _tensor(t, name: str, dtypes, shape=None, dev=None):
     GPU (`dev`, where the caller has it); None stays None."""
     if t is None:
         return None
-    if t.dtype is not dtypes and not (isinstance(dtypes, tuple) and t.dtype in dtypes):
-        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtypes}")
+    dt = t.dtype
+    if (dt is dtypes or (type(dtypes) is tuple and dt in dtypes)) and (shape is None or t.shape == shape) \
+            and t.is_contiguous() and t.get_device() == (_device() if dev is None else dev):
+        return t.data_ptr()
+    if dt is not dtypes and not (isinstance(dtypes, tuple) and dt in dtypes):
+        raise ValueError(f"{name} has dtype {dt}, expected {dtypes}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.get_device() != (_device() if dev is None else dev):
-        raise ValueError(f"{name} is on {t.device}; the library runs on the current GPU")
-    return t.data_ptr()
+    raise ValueError(f"{name} is on {t.device}; the library runs on the current GPU")
 
 
 def _num_seqs(seq_offsets) -> int:
@@ -837,9 +839,11 @@ def moe_fp8_scale_bytes(k: int) -> int:
 
 def _rows8(codes, scale, names, rows, k, dev):
     """Pointers of rows in 8 bits: codes [rows, moe_fp8_row_bytes(k)], scale [rows, moe_fp8_scale_bytes(k)]."""
-    blocks = -(-k // MOE_FP8_BLOCK)
-    return (_tensor(codes, names[0], _CODES, (rows, blocks * MOE_FP8_BLOCK), dev),
-            _tensor(scale, names[1], torch.uint8, (rows, -(-blocks // 4) * 4), dev))
+    if codes is None and scale is None:
+        return None, None
+    blocks = (k + 127) >> 7
+    return (_tensor(codes, names[0], _CODES, (rows, blocks << 7), dev),
+            _tensor(scale, names[1], torch.uint8, (rows, (blocks + 3) & ~3), dev))
 
 
 def fp8_rows(rows: int, k: int, device="cuda"):
@@ -884,9 +888,9 @@ def moe_quantize_weights_fp8(num_groups, n_out, k, swiglu, w, codes, scale, stre
 
 def _matrix8(codes, scale, name, num_groups, n_out, k, swiglu, dev):
     """Pointers of a matrix in 8 bits, whose tensors must have the sizes of its shape."""
-    halves, kb, nb = 2 if swiglu else 1, -(-k // MOE_FP8_BLOCK), -(-n_out // MOE_FP8_BLOCK)
-    return (_tensor(codes, name, torch.uint8, (num_groups * -(-n_out // 16) * halves * kb * 2048,), dev),
-            _tensor(scale, name + "'s scale", torch.uint8, (num_groups * nb * halves * (-(-kb // 4) * 4),), dev))
+    kb, parts = (k + 127) >> 7, num_groups << 1 if swiglu else num_groups
+    return (_tensor(codes, name, torch.uint8, (parts * ((n_out + 15) >> 4) * kb * 2048,), dev),
+            _tensor(scale, name + "'s scale", torch.uint8, (parts * ((n_out + 127) >> 7) * ((kb + 3) & ~3),), dev))
 
 
 def fp8_weights(w, swiglu=False, stream=None):
@@ -931,9 +935,9 @@ def moe_rms_norm_backward(dy, h, weight, rstd, dx, dweight, ws, dh=None, stream=
 
 
 def _fp8_operands(num_groups, rows_max, k, x8, x_scale, group_offsets, row_index, dev):
-    rows = int(rows_max) if row_index is None else x8.shape[0]
+    rows = rows_max if row_index is None else x8.shape[0]
     codes, scale = _rows8(x8, x_scale, ("x8", "x_scale"), rows, k, dev)
-    return (codes, scale, _tensor(row_index, "row_index", torch.int32, (int(rows_max),), dev), rows,
+    return (codes, scale, _tensor(row_index, "row_index", torch.int32, (rows_max,), dev), rows,
             _tensor(group_offsets, "group_offsets", torch.int32, (num_groups + 1,), dev))
 
 
