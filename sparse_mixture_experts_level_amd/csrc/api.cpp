@@ -730,7 +730,7 @@ bool fp8_large(int64_t rows_max, int32_t group_rows_max) {
 
 // Workspace of the products in 8 bits: packed tiles of the rows and, for the FFN (f > 0), H in rows and in packed tiles.
 struct Fp8Layout {
-  size_t xp, xp_scale, h8, h_scale, h32, hp, hp_scale, total;
+  size_t xp, xp_scale, h8, h_scale, hp, hp_scale, total;
 };
 Fp8Layout fp8_layout(int32_t G, int64_t rows_max, int32_t group_rows_max, int32_t k, int32_t f) {
   Fp8Layout L{};
@@ -745,8 +745,6 @@ Fp8Layout fp8_layout(int32_t G, int64_t rows_max, int32_t group_rows_max, int32_
   L.xp_scale = take(large ? moe::fp8_packed_scale_bytes(rows_max, G, k) : 0);
   L.h8 = take(f ? rows_max * moe::fp8_row_bytes(f) : 0);
   L.h_scale = take(f ? rows_max * moe::fp8_scale_bytes(f) : 0);
-  const bool few = std::min<int64_t>(rows_max, group_rows_max) <= 16;
-  L.h32 = take(f && few ? 4 * rows_max * moe::fp8_row_bytes(f) : 0);
   L.hp = take(f && large ? moe::fp8_packed_bytes(rows_max, G, f) : 0);
   L.hp_scale = take(f && large ? moe::fp8_packed_scale_bytes(rows_max, G, f) : 0);
   L.total = o;
@@ -797,7 +795,6 @@ moe_status run_swiglu_fp8(int32_t G, int64_t rows_max, int32_t group_rows_max, i
   MOE_TRY(pack_fp8(a, ws, L, stream));
   a.h8 = at<uint8_t>(ws, L.h8);
   a.h_scale = at<uint8_t>(ws, L.h_scale);
-  a.h32 = std::min<int64_t>(rows_max, group_rows_max) <= 16 ? at<float>(ws, L.h32) : nullptr;
   a.hp = large ? at<uint8_t>(ws, L.hp) : nullptr;
   a.hp_scale = large ? at<uint8_t>(ws, L.hp_scale) : nullptr;
   MOE_TRY_HIP(moe::launch_fp8_gemm(a, stream), "gate_up in 8 bits");

@@ -134,6 +134,7 @@ __device__ __forceinline__ void fp8_group_rows_uniform(const Fp8GemmArgs &a, int
 __device__ __forceinline__ int fp8_nth_group(const Fp8GemmArgs &a, int n, int most, int &begin, int &end) {
   const int lane = threadIdx.x & 63;
   int seen = 0;
+#pragma unroll 1
   for (int g0 = 0; g0 < a.num_groups; g0 += 64) {
     int b = 0, e = 0;
     if (g0 + lane < a.num_groups) fp8_group_rows(a, g0 + lane, b, e);

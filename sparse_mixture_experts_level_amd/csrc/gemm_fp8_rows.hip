@@ -1,0 +1,543 @@
+// Grouped products in 8 bits for groups of many rows (layouts in fp8.hpp), bound by the matrix cores.
+//
+// 256 rows x 256 weight rows a workgroup (for gate_up 128 columns of H: 16 gate and 16 up rows in turn), eight
+// waves of 128 x 64, 32x32x64 instructions with their operands' scales (the
+// blocks' scales cost nothing).  Both operands go from memory to LDS without registers, a step of 64 of K as
+// 1 KB pieces that are consecutive in memory and lie in LDS as the instruction reads them: for 16 rows, [4 chunks of
+// 16 codes][16 rows], so that sixteen lanes read 256 consecutive bytes.  The rows are copied into that
+// layout beforehand (fp8_pack_rows_kernel); H is written in it.  Four stages, three steps ahead; the
+// two waves of each SIMD take turns, one computing while the other loads and reads
+// (the bf16 kernel's schedule for groups of many rows: the same bytes and cycles a step, twice the products).
+#include <algorithm>
+#include <climits>
+
+#include "gemm_fp8.hpp"
+
+namespace moe {
+
+namespace {
+
+constexpr int LG_TILE = kFp8LargeRows * 64;  // bytes of an operand's stage: 256 rows, 64 of K
+
+// Tile v of a launch: the tiles of the groups of many rows, group after group, then one for each group of few (any number of
+// rows where there are no packed copies).  One pass over the offsets, two for more than 64 groups; all results
+// in scalar registers.
+struct Fp8Tile {
+  int g, begin, end;           // -1: there is no such tile
+  int first, count, tiles;     // of the group's tiles (count 0: few rows), and all tiles of many rows
+};
+__device__ __forceinline__ Fp8Tile find_tile(const Fp8GemmArgs &a, int tiles_max, int block, int per_tile, bool spread) {
+  const int lane = threadIdx.x & 63, G = a.num_groups;
+  const int few = a.xp ? kFp8FewRows : INT_MAX;
+  Fp8Tile t{-1, 0, 0, 0, 0, 0};
+  int b = 0, e = 0;
+#pragma unroll 1
+  for (int g0 = 0; g0 < G; g0 += 64) {
+    b = e = 0;
+    if (g0 + lane < G) fp8_group_rows(a, g0 + lane, b, e);
+    t.tiles += group_reduce<64>(a.xp ? fp8_large_tiles(e - b) : 0, [](int x, int y) { return x + y; });
+  }
+  // (offsets that decrease could count rows twice: no tile past those that the packed copies have room for)
+  t.tiles = min(__builtin_amdgcn_readfirstlane(t.tiles), tiles_max);
+  // the first tiles' blocks in one contiguous range an XCD, as neighbours share operands
+  const int large = t.tiles * per_tile, lin = spread && block < large ? xcd_remap(block, large) : block;
+  const int v = lin / per_tile;
+  const bool many = v < t.tiles;
+  int seen = 0;
+#pragma unroll 1
+  for (int g0 = 0; g0 < G; g0 += 64) {
+    if (G > 64) {
+      b = e = 0;
+      if (g0 + lane < G) fp8_group_rows(a, g0 + lane, b, e);
+    }
+    const int mine = many ? fp8_large_tiles(e - b) : e > b && e - b <= few ? 1 : 0;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int x = __shfl_up(incl, o, 64);
+      if (lane >= o) incl += x;
+    }
+    const int want = many ? v : v - t.tiles;
+    const uint64_t hit = __ballot(seen + incl > want);
+    if (hit) {
+      const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
+      t.g = g0 + l;
+      t.begin = __builtin_amdgcn_readlane(b, l);
+      t.end = __builtin_amdgcn_readlane(e, l);
+      t.first = __builtin_amdgcn_readfirstlane(seen) + __builtin_amdgcn_readlane(incl - mine, l);
+      t.count = many ? __builtin_amdgcn_readlane(mine, l) : 0;
+      return t;
+    }
+    seen += __builtin_amdgcn_readlane(incl, 63);
+  }
+  return t;
+}
+
+// Some rows, up to 128 at a time: a workgroup has 128 columns of H or 256 of y, each of its eight waves two
+// blocks of 16 weight rows (gate and up, or neighbours).  The rows are read by all eight waves from LDS, where
+// loads without registers put them as codes, a step of 128 of K a stage, in the operand layout (2 KB for 16 rows:
+// sixteen lanes read 256 consecutive bytes); four stages, three steps ahead, one barrier a step.  The 8-bit matrix
+// instruction: converted to bf16 by each wave, 128 rows took 1.7 us a step of the 1.2 that its weights take.
+constexpr int MD_R = 4, MD_D = 3, MD_ROWS = 128;
+
+// One block of n <= 16 MS rows from m0 on; MS is exact, so that no branch is in the loop.
+template <bool SWIGLU, int MS>
+__device__ __forceinline__ void medium_rows(const Fp8GemmArgs &a, int g, int nb, int m0, int n, uint8_t *s0, uint8_t *s1,
+                                            uint8_t *s2, uint8_t *s3, float (*tops)[MD_ROWS]) {
+  constexpr int R = MD_R, D = MD_D;
+  auto stage = [&](int b) -> uint8_t * { return b == 0 ? s0 : b == 1 ? s1 : b == 2 ? s2 : s3; };
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lr = lane & 15,
+            lg = lane >> 4;
+  const int kt = fp8_blocks(a.K), kp = fp8_row_bytes(a.K), ks = fp8_scale_bytes(a.K);
+  const int units = (a.n_out + 15) / 16 * (SWIGLU ? 2 : 1), unit = nb * 16 + wave * 2;  // blocks of 16 weight rows
+  const int64_t wbytes = fp8_group_bytes(a.n_out, a.K, SWIGLU);
+  const rsrc_t wres = make_rsrc(a.w8 + g * wbytes, (uint32_t)wbytes);
+  uint32_t half;
+  const uint32_t wbase = fp8_block_offset(unit, units, kt, half) + (uint32_t)lane * 16u;
+  const int sblocks = fp8_blocks(a.n_out);
+  const uint8_t *wscale =
+      a.w_scale + ((int64_t)g * sblocks + (SWIGLU ? nb : min(nb * 2 + wave / 4, sblocks - 1))) * (SWIGLU ? 2 : 1) * ks;
+  i32x8 w[R][2];
+  auto load_w = [&](int j, int t) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const bool in = t < kt && unit + b < units;
+      const uint32_t o = wbase + (uint32_t)(2 * t) * half + (uint32_t)b * 1024u;
+      w[j][b] = fp8_operand(buf_ld16_nt(wres, in ? o : kOob), buf_ld16_nt(wres, in ? o + half : kOob));
+    }
+  };
+  const Fp8Rows rows(a, m0, n);
+  // this wave's pieces of a stage, one for each half of K's 128: subtile `wave`, row lr, codes 64 p + 16 lg ..
+  const uint32_t src = rows.row(a, m0, wave * 16 + lr, n);
+  const uint32_t xoff = src != kOob ? src * (uint32_t)kp + (uint32_t)lg * 16u : kOob;
+  auto load_x = [&](int t, int b) {
+    const uint32_t o = t < kt && xoff != kOob ? xoff + (uint32_t)t * 128u : kOob;
+    buf_ld16_lds(rows.xres, o, stage(b) + wave * 2048);
+    buf_ld16_lds(rows.xres, o == kOob ? kOob : o + 64u, stage(b) + wave * 2048 + 1024);
+  };
+  uint32_t soff[MS], sx[MS], nx[MS], sw[2], nw[2];
+#pragma unroll
+  for (int i = 0; i < MS; ++i) {
+    const uint32_t r = rows.row(a, m0, i * 16 + lr, n);
+    soff[i] = r != kOob ? r * (uint32_t)ks : kOob;
+  }
+  auto load_scales = [&](int t) {  // of four steps; past K those of the last four again (their codes are zeros)
+    const int at = min(t, ks - 4);
+#pragma unroll
+    for (int i = 0; i < MS; ++i)
+      nx[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rows.sres, soff[i] == kOob ? kOob : soff[i] + (uint32_t)at, 0, 0);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) nw[b] = scalar_load(wscale + (SWIGLU ? b * ks : 0) + at);
+  };
+  f32x4 acc[MS][2];
+#pragma unroll
+  for (int i = 0; i < MS; ++i)
+#pragma unroll
+    for (int b = 0; b < 2; ++b) acc[i][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  load_scales(0);
+#pragma unroll
+  for (int b = 0; b < D; ++b) load_x(b, b);
+  __builtin_amdgcn_sched_barrier(0);  // the waits count on rows before weights
+#pragma unroll
+  for (int j = 0; j < R; ++j) load_w(j, j);
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(4 * R) : "memory");  // the first stages are there
+  auto bar = [&]() {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  bar();
+  for (int t0 = 0; t0 < kt; t0 += R) {
+    const uint32_t keep = kt - t0 >= 4 ? ~0u : (1u << (8 * (kt - t0))) - 1u;  // the padding's scales are not looked at
+#pragma unroll
+    for (int i = 0; i < MS; ++i) sx[i] = nx[i] & keep;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) sw[b] = nw[b] & keep;
+    load_scales(t0 + R);
+    auto step = [&](auto jc) {
+      constexpr int J = decltype(jc)::value;
+      const int t = t0 + J;
+      load_x(t + D, (J + D) % R);  // the stage read in step t - 1, which every wave has left
+      __builtin_amdgcn_sched_barrier(0);
+      const uint8_t *st = stage(J) + lane * 16;
+#pragma unroll
+      for (int i = 0; i < MS; ++i) {
+        const i32x8 x = fp8_operand(*reinterpret_cast<const u32x4 *>(st + i * 2048),
+                                    *reinterpret_cast<const u32x4 *>(st + i * 2048 + 1024));
+#pragma unroll
+        for (int b = 0; b < 2; ++b) acc[i][b] = mfma_fp8_16<J>(w[J][b], x, acc[i][b], sw[b], sx[i]);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // loads into registers still in use would get others, copied after a wait
+      load_w(J, t + R);
+      // step t + 1's rows, loaded in step t + 1 - D, are there when at most the loads behind them are in flight
+      // (weights of that step, rows and weights of the steps since; the scales may lie between as well)
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(4 + 6 * (D - 1)) : "memory");
+      bar();
+    };
+    step(std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 1>{});
+    step(std::integral_constant<int, 2>{});
+    step(std::integral_constant<int, 3>{});
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no write to LDS may outlive its rows
+  __syncthreads();
+  if constexpr (SWIGLU) {
+    const int col = nb * 128 + wave * 16 + lg * 4;
+#pragma unroll
+    for (int i = 0; i < MS; ++i) {
+      float top = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[i][0][j] = silu_f32(acc[i][0][j]) * acc[i][1][j];
+        top = fmaxf(top, fp8_magnitude(acc[i][0][j]));
+      }
+      top = fmaxf(top, __shfl_xor(top, 16, 64));
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      if (lg == 0) tops[wave][i * 16 + lr] = top;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MS; ++i) {
+      float top = 0.0f;
+#pragma unroll
+      for (int v = 0; v < 8; ++v) top = fmaxf(top, tops[v][i * 16 + lr]);
+      const int64_t row = m0 + i * 16 + lr;
+      const float h[4] = {acc[i][0][0], acc[i][0][1], acc[i][0][2], acc[i][0][3]};
+      if (row < m0 + n) store_h(a, h, top, row, nb, col, wave == 0 && lg == 0);
+    }
+    __syncthreads();
+  } else {
+#pragma unroll
+    for (int i = 0; i < MS; ++i) {
+      const int64_t row = m0 + i * 16 + lr;
+      if (row < m0 + n)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) store_y(a, acc[i][b], row, (unit + b) * 16 + lg * 4);
+    }
+  }
+}
+
+__device__ __forceinline__ f32x16 mfma_fp8_32(i32x8 a, i32x8 b, f32x16 c, uint32_t sa, uint32_t sb, int byte) {
+  switch (byte) {
+    case 0: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, (int)sa, 0, (int)sb);
+    case 1: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 1, (int)sa, 1, (int)sb);
+    case 2: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 2, (int)sa, 2, (int)sb);
+    default: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 3, (int)sa, 3, (int)sb);
+  }
+}
+
+template <bool SWIGLU>
+__global__ __launch_bounds__(512, 1) void fp8_rows_kernel(const Fp8GemmArgs a, int n_tiles, int tiles_max) {
+  constexpr int NBUF = 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t sA0[LG_TILE], sA1[LG_TILE], sA2[LG_TILE], sA3[LG_TILE];
+  __shared__ __attribute__((aligned(1024))) uint8_t sB0[LG_TILE], sB1[LG_TILE], sB2[LG_TILE], sB3[LG_TILE];
+  auto bufA = [&](int b) -> uint8_t * { return b == 0 ? sA0 : b == 1 ? sA1 : b == 2 ? sA2 : sA3; };
+  auto bufB = [&](int b) -> uint8_t * { return b == 0 ? sB0 : b == 1 ? sB1 : b == 2 ? sB2 : sB3; };
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / 4, wn = wave % 4, lr = lane & 31, lh = lane >> 5;
+  const Fp8Tile tile = find_tile(a, tiles_max, blockIdx.x, n_tiles, true);
+  if (tile.g < 0) return;
+  const int g = tile.g, begin = tile.begin, end = tile.end, mt_first = tile.first, mt_count = tile.count;
+  const int large = tile.tiles * n_tiles;
+  if (mt_count == 0) {
+    const int nb = ((int)blockIdx.x - large) % n_tiles;
+    for (int m0 = begin; m0 < end; m0 += MD_ROWS) {
+      const int n = min(MD_ROWS, end - m0);
+      switch ((n + 15) / 16) {
+#define MOE_ROWS(MS) \
+  case MS: medium_rows<SWIGLU, MS>(a, g, nb, m0, n, sA0, sA1, sA2, sA3, reinterpret_cast<float(*)[MD_ROWS]>(sB0)); break
+        MOE_ROWS(1);
+        MOE_ROWS(2);
+        MOE_ROWS(3);
+        MOE_ROWS(4);
+        MOE_ROWS(5);
+        MOE_ROWS(6);
+        MOE_ROWS(7);
+        MOE_ROWS(8);
+#undef MOE_ROWS
+      }
+    }
+    return;
+  }
+  const int local = xcd_remap(blockIdx.x, large) - mt_first * n_tiles;
+  int mt, nt;
+  if (end - begin <= (SWIGLU ? 2 : 1) * a.n_out) {  // the weights are larger: their tile outermost
+    nt = local / mt_count;
+    mt = local - nt * mt_count;
+  } else {  // bands of four row tiles, weight tile outer within a band
+    constexpr int BAND = 4;
+    const int band = local / (BAND * n_tiles), r = local - band * BAND * n_tiles;
+    const int bm = min(BAND, mt_count - band * BAND);
+    nt = r / bm;
+    mt = band * BAND + (r - nt * bm);
+  }
+  mt = __builtin_amdgcn_readfirstlane(mt);
+  nt = __builtin_amdgcn_readfirstlane(nt);
+  const int per = fp8_tile_rows(end - begin, mt_count);
+  const int m0 = begin + mt * per, rows = min(per, end - m0), m_tile = mt_first + mt;
+  if (m_tile >= tiles_max) return;
+  const int row_blocks = (rows + 31) / 32, mine = max(0, min(4, row_blocks - wm * 4));  // of 32 rows: the tile's, this wave's
+  const int kt = fp8_blocks(a.K), nk = 2 * kt, ks = fp8_scale_bytes(a.K);
+  const int64_t abytes = (int64_t)kFp8LargeRows * kt * kFp8Block;
+  const int64_t wbytes = fp8_group_bytes(a.n_out, a.K, SWIGLU);
+  const rsrc_t ares = make_rsrc(a.xp + m_tile * abytes, (uint32_t)abytes);
+  const rsrc_t wres = make_rsrc(a.w8 + g * wbytes, (uint32_t)wbytes);
+  const rsrc_t sres = make_rsrc(a.xp_scale + (int64_t)m_tile * kFp8LargeRows * ks, (uint32_t)(kFp8LargeRows * ks));
+  // this wave's pieces of a stage: 16-row blocks 2 wave and 2 wave + 1 of both operands
+  uint32_t aoff[2], boff[2], wstep;
+  const int wblocks = (a.n_out + 15) / 16 * (SWIGLU ? 2 : 1);
+  const uint32_t wtile = fp8_block_offset(nt * 16, wblocks, kt, wstep);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t at = (uint32_t)(2 * wave + i) * 1024u + (uint32_t)lane * 16u;
+    aoff[i] = wave < row_blocks ? at : kOob;
+    boff[i] = nt * 16 + 2 * wave + i < wblocks ? wtile + at : kOob;
+  }
+  auto issue = [&](int s, int b) {
+    const uint32_t ka = (uint32_t)s * (uint32_t)LG_TILE, kb = (uint32_t)s * wstep;
+    const bool in = s < nk;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      buf_ld16_lds(ares, in && aoff[i] != kOob ? aoff[i] + ka : kOob, bufA(b) + (2 * wave + i) * 1024);
+      buf_ld16_lds(wres, in && boff[i] != kOob ? boff[i] + kb : kOob, bufB(b) + (2 * wave + i) * 1024);
+    }
+  };
+  const int sblocks = fp8_blocks(a.n_out);
+  const uint8_t *wscale = a.w_scale + ((int64_t)g * sblocks + (SWIGLU ? nt : min(nt * 2 + wn / 2, sblocks - 1))) *
+                                          (SWIGLU ? 2 : 1) * ks;
+  uint32_t sx[4], sw[2];
+  // four blocks of K, eight steps; past K zeros, or the last ones again
+  auto load_scales = [&](int q) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      sx[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
+          sres, (uint32_t)(q * kFp8LargeRows + wm * 128 + i * 32 + lr) * 4u, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) sw[j] = scalar_load(wscale + (SWIGLU ? j * ks : 0) + min(4 * q, ks - 4));
+  };
+
+  f32x16 acc[4][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
+  // This lane's 32 codes of a row, chunks 2 lh and 2 lh + 1, in the first of the wave's row and weight blocks (one offset
+  // and constants from there: with the sums formed anew for each read the compiler lost track of which
+  // stage a read is of, and waited for every load in flight).
+  const int half = (lane >> 4) & 1, at = (2 * lh) * 256 + (lane & 15) * 16;
+  const int a_at = (wm * 8 + half) * 1024 + at, b_at = (wn * 4 + (SWIGLU ? 2 : 1) * half) * 1024 + at;
+  {
+    // A wave in mem(s) issues step s + 3 and completes its own loads of step s + 1, before the barrier that
+    // precedes every read of them; a stage is refilled only after the barrier that follows both groups' reads.
+    const bool second = wave >= 4;
+    u32x4 af[4][2], bf[2][2];
+    uint32_t cx[4], cw[2];
+    auto mem = [&](int s, int b) {
+      issue(s + 3, (b + 3) % NBUF);
+      asm volatile("s_waitcnt vmcnt(8)" ::: "memory");  // the two younger steps' may stay in flight
+      const uint8_t *la = bufA(b % NBUF), *lb = bufB(b % NBUF);
+      const uint8_t *pa = la + a_at, *pb = lb + b_at;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i >= mine) break;
+        af[i][0] = *reinterpret_cast<const u32x4 *>(pa + i * 2048);
+        af[i][1] = *reinterpret_cast<const u32x4 *>(pa + i * 2048 + 256);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        bf[j][0] = *reinterpret_cast<const u32x4 *>(pb + j * (SWIGLU ? 1024 : 2048));
+        bf[j][1] = *reinterpret_cast<const u32x4 *>(pb + j * (SWIGLU ? 1024 : 2048) + 256);
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    };
+    auto comp = [&](int b) {
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i >= mine) break;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = mfma_fp8_32(fp8_operand(bf[j][0], bf[j][1]), fp8_operand(af[i][0], af[i][1]), acc[i][j], cw[j], cx[i],
+                                  b / 2);
+      }
+      __builtin_amdgcn_s_setprio(0);
+    };
+    auto bar = [&]() {
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto next_scales = [&](int q) {  // those of the eight steps that begin; the following ones are loaded
+#pragma unroll
+      for (int i = 0; i < 4; ++i) cx[i] = sx[i];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) cw[j] = sw[j];
+      load_scales(q + 1);
+    };
+    load_scales(0);
+#pragma unroll
+    for (int b = 0; b < 3; ++b) issue(b, b);
+    asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+    bar();
+    if (second) bar();
+    int s0 = 0;
+    for (; s0 + 8 <= nk; s0 += 8) {
+      next_scales(s0 / 8);
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        mem(s0 + b, b);
+        bar();
+        comp(b);
+        bar();
+      }
+    }
+    if (s0 < nk) {
+      next_scales(s0 / 8);
+#pragma unroll
+      for (int b = 0; b < 7; ++b) {
+        if (s0 + b >= nk) break;
+        mem(s0 + b, b);
+        bar();
+        comp(b);
+        bar();
+      }
+    }
+    if (!second) bar();
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no LDS write may outlive the block
+  __syncthreads();
+
+  // Block (i, j): lane l holds row wm * 128 + i * 32 + l % 32 and, per q = 0..3, columns 8 q + 4 (l / 32) .. + 3 of its 32.
+  if constexpr (SWIGLU) {
+    float *tops = reinterpret_cast<float *>(sB0);  // [4 waves of columns][256 rows]
+    float top[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      top[i] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        acc[i][0][e] = silu_f32(acc[i][0][e]) * acc[i][1][e];
+        top[i] = fmaxf(top[i], fp8_magnitude(acc[i][0][e]));
+      }
+      top[i] = fmaxf(top[i], __shfl_xor(top[i], 32, 64));
+      if (lh == 0) tops[wn * 256 + wm * 128 + i * 32 + lr] = top[i];
+    }
+    __syncthreads();
+    // the tile's 256 x 128 codes in H's packed layout: 16-row blocks' first KB (columns below 64) in sA0, second in sA1
+    const int hs = fp8_scale_bytes(a.n_out), ht = fp8_blocks(a.n_out);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = wm * 128 + i * 32 + lr;
+      const float t = fmaxf(fmaxf(tops[row], tops[256 + row]), fmaxf(tops[512 + row], tops[768 + row]));
+      const uint32_t byte = fp8_scale_byte(t);
+      const float inv = fp8_inverse(byte);
+      uint8_t *o = (wn < 2 ? sA0 : sA1) + (row >> 4) * 1024 + (wn & 1) * 512 + (row & 15) * 16 + lh * 4;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint32_t *>(o + (q >> 1) * 256 + (q & 1) * 8) =
+            fp8_codes(acc[i][0][4 * q] * inv, acc[i][0][4 * q + 1] * inv, acc[i][0][4 * q + 2] * inv,
+                      acc[i][0][4 * q + 3] * inv);
+      if (wn == 0 && lh == 0)
+        a.hp_scale[(int64_t)m_tile * kFp8LargeRows * hs + ((nt / 4) * kFp8LargeRows + row) * 4 + nt % 4] = (uint8_t)byte;
+    }
+    __syncthreads();
+    uint8_t *hp = a.hp + ((int64_t)m_tile * ht + nt) * (2 * LG_TILE);
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const int q = threadIdx.x + 512 * v;  // 16-byte piece of the 16 KB
+        stg16(hp + p * LG_TILE + q * 16, *reinterpret_cast<const u32x4 *>((p ? sA1 : sA0) + q * 16));
+      }
+  } else {
+    // bf16: each wave's 128 rows x 64 columns through its own 16 KB, 128-byte rows, 16-byte chunk c of row r at
+    // c ^ ((r >> 1) & 7), out as whole pieces along the rows
+    uint8_t *stage = wave < 4 ? bufA(wave) : bufB(wave - 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = i * 32 + lr;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint2 *>(stage + row * 128 + (((j * 4 + q) ^ ((row >> 1) & 7)) << 4) + lh * 8) =
+              uint2{pack_bf16x2(acc[i][j][4 * q], acc[i][j][4 * q + 1]), pack_bf16x2(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3])};
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    const int c = lane & 7, col = nt * 256 + wn * 64 + c * 8;
+#pragma unroll
+    for (int it = 0; it < 16; ++it) {
+      const int row = it * 8 + (lane >> 3), grow = wm * 128 + row;
+      const u32x4 v = *reinterpret_cast<const u32x4 *>(stage + row * 128 + ((c ^ ((row >> 1) & 7)) << 4));
+      if (grow >= rows) continue;
+      bf16_t *o = a.y + (int64_t)(m0 + grow) * a.n_out + col;
+      if (col + 8 <= a.n_out) {
+        *reinterpret_cast<u32x4_any *>(o) = v;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (col + e < a.n_out) o[e] = (bf16_t)(v[e / 2] >> (16 * (e % 2)));
+      }
+    }
+  }
+}
+
+// The rows of the tiles, and their scales as [4 blocks of K][256 rows] words, for fp8_rows_kernel: one
+// workgroup 64 rows of a tile and four blocks of K; a wave reads 64 bytes of its 16 rows at a time, the other half of
+// each line next, and writes them as one piece of 1 KB (whole rows a wave, 16 bytes of each written apart: 36 us for
+// 27 at 4096 x 14336).
+__global__ __launch_bounds__(256) void fp8_pack_rows_kernel(const Fp8GemmArgs a, uint8_t *__restrict__ xp,
+                                                            uint8_t *__restrict__ xp_scale, int tiles_max) {
+  const int kt = fp8_blocks(a.K), kp = fp8_row_bytes(a.K), ks = fp8_scale_bytes(a.K), quads = ks / 4;
+  const int b0 = blockIdx.y * 4, m_tile = blockIdx.x / 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int block = (blockIdx.x % 4) * 4 + wave, r = block * 16 + (lane & 15), c = lane >> 4;  // of 16 rows; row, chunk
+  const Fp8Tile t = find_tile(a, tiles_max, m_tile, 1, false);
+  if (t.count == 0) return;
+  const int per = fp8_tile_rows(t.end - t.begin, t.count), m0 = t.begin + (m_tile - t.first) * per;
+  const int rows = min(per, t.end - m0);
+  if (block * 16 >= (rows + 31) / 32 * 32) return;  // the kernel reads whole 32s
+  const Fp8Rows from(a, m0, rows);
+  const uint32_t src = from.row(a, m0, r, rows);
+  u32x4 v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    v[i] = buf_ld16(from.xres, src != kOob && b0 + i / 2 < kt ? src * (uint32_t)kp + (uint32_t)(b0 * 128 + i * 64 + c * 16) : kOob);
+  const uint32_t scales = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
+      from.sres, src != kOob ? src * (uint32_t)ks + (uint32_t)b0 : kOob, 0, 0);
+  uint8_t *o = xp + ((int64_t)m_tile * kt + b0) * 2 * LG_TILE + block * 1024 + lane * 16;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (b0 + i / 2 < kt) stg16(o + i * LG_TILE, v[i]);
+  if (lane < 16)
+    reinterpret_cast<uint32_t *>(xp_scale)[((int64_t)m_tile * quads + blockIdx.y) * kFp8LargeRows + r] = scales;
+}
+
+}  // namespace
+
+hipError_t launch_fp8_pack_rows(const Fp8GemmArgs &a, uint8_t *xp, uint8_t *xp_scale, hipStream_t s) {
+  const int64_t tiles = fp8_large_tiles_max(a.rows_max, a.num_groups);
+  Fp8GemmArgs c = a;
+  c.xp = xp;  // there are packed copies
+  const int quads = fp8_scale_bytes(a.K) / 4;
+  if (tiles > 0x7fffffff / 4 || quads > 65535) return hipErrorInvalidValue;
+  if (tiles > 0)
+    hipLaunchKernelGGL(fp8_pack_rows_kernel, dim3((unsigned)tiles * (kFp8LargeRows / 64), (unsigned)quads), dim3(256), 0, s, c,
+                       xp, xp_scale, (int)tiles);
+  return hipGetLastError();
+}
+
+hipError_t launch_fp8_gemm_rows(const Fp8GemmArgs &a, hipStream_t s) {
+  const bool swiglu = a.h8 != nullptr;
+  const int n_tiles = (a.n_out + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256);
+  const int64_t tiles = a.xp ? fp8_large_tiles_max(a.rows_max, a.num_groups) : 0;
+  const int64_t grid = (tiles + std::min(a.num_groups, a.rows_max)) * n_tiles;
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  if (swiglu)
+    hipLaunchKernelGGL((fp8_rows_kernel<true>), dim3((unsigned)grid), dim3(512), 0, s, a, n_tiles, (int)tiles);
+  else
+    hipLaunchKernelGGL((fp8_rows_kernel<false>), dim3((unsigned)grid), dim3(512), 0, s, a, n_tiles, (int)tiles);
+  return hipGetLastError();
+}
+
+}  // namespace moe

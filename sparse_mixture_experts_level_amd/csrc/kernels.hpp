@@ -240,7 +240,6 @@ struct Fp8GemmArgs {
   const uint8_t *w8, *w_scale;
   uint16_t *y;
   uint8_t *h8, *h_scale;
-  float *h32;  // room for H before it is quantised [rows_max, fp8_row_bytes(n_out)], or NULL: few rows in many workgroups
   int num_groups, rows_max, group_rows_max, x_rows, n_out, K;
   // Groups of more than kFp8FewRows go through a kernel for many rows, which reads them (and writes H) in packed
   // tiles of fp8_packed_bytes(); xp and hp are NULL where no group can have that many.
@@ -250,7 +249,7 @@ struct Fp8GemmArgs {
 // A group of many rows is cut into the least number of tiles of at most kFp8LargeRows, equal but for whole 32s: the
 // matrix instructions of 32 rows past a tile's end are left out, so that a group of 1040 rows costs five tiles of
 // 224 and less (the last has 144), not four of 256 and a nearly empty one.
-constexpr int kFp8LargeRows = 256, kFp8FewRows = 128;
+constexpr int kFp8LargeRows = 256, kFp8FewRows = 128, kFp8SmallRows = 16;
 __host__ __device__ inline int fp8_large_tiles(int rows) {
   return rows <= kFp8FewRows ? 0 : (rows + kFp8LargeRows - 1) / kFp8LargeRows;
 }
@@ -271,7 +270,7 @@ inline int64_t fp8_packed_scale_bytes(int64_t rows, int G, int k) {
 // x8 (through row_index) and its scales to packed tiles.
 hipError_t launch_fp8_pack_rows(const Fp8GemmArgs &a, uint8_t *xp, uint8_t *xp_scale, hipStream_t s);
 hipError_t launch_fp8_gemm(const Fp8GemmArgs &a, hipStream_t s);
-hipError_t launch_fp8_gemm_large(const Fp8GemmArgs &a, hipStream_t s);  // its tiles alone
+hipError_t launch_fp8_gemm_rows(const Fp8GemmArgs &a, hipStream_t s);  // (its part for more than kFp8SmallRows rows a group)
 
 // ---- root-mean-square norm (norm.hip)
 struct NormCall {
