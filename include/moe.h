@@ -630,7 +630,8 @@ moe_status moe_dequantize_rows_fp8(int64_t rows, int32_t k, int32_t dtype, const
  *          256 c + 16 r + i is row r, k = 16 c + i of the 64; zeros where the matrix has ended
  *   scale  per group [ceil(n_out / 128)][moe_fp8_scale_bytes(K)] (swiglu: [ceil(n_out / 128)][2][...])
  * Sizes in bytes from the two helpers (host only; 0 for invalid arguments).  Scales and codes
- * as for rows.  One group's codes must be below 2 GiB (MOE_ERR_UNSUPPORTED). */
+ * as for rows.  One group's codes must be below 2 GiB, n_out and k below 2^23
+ * (MOE_ERR_UNSUPPORTED). */
 size_t moe_fp8_weights_bytes(int32_t num_groups, int32_t n_out, int32_t k, int32_t swiglu);
 size_t moe_fp8_weight_scales_bytes(int32_t num_groups, int32_t n_out, int32_t k, int32_t swiglu);
 moe_status moe_quantize_weights_fp8(int32_t num_groups, int32_t n_out, int32_t k, int32_t swiglu, int32_t dtype,
@@ -679,13 +680,16 @@ moe_status moe_rms_norm_backward(int32_t num_tokens, int32_t d_model, int32_t dt
  *   num_groups, rows_max, group_rows_max  as for moe_grouped_swiglu_gemm; rows_max <= INT32_MAX
  *   x8, x_scale     rows in 8 bits: rows_max of them, or x_row_count, which must be below 2 GiB
  *   group_offsets   [G+1] int32 DEVICE array, non-decreasing within [0, rows_max] (entries
- *                   outside count as its ends)
+ *                   outside count as its ends; where they fall nothing else is touched, but rows may be
+ *                   left out)
  *   w8, w_scale     from moe_quantize_weights_fp8
  *   y_rows          [rows_max, n_out] bf16, written for rows inside a group, others left as they are
  *   ws              at least the bytes of the helper beside (0: invalid arguments)
- * Any n_out, d, f, K >= 1.  A NaN in a row makes that row NaN, one in a weight that output column.  The
- * matrix instruction drops, of 16 products at a time, what lies some 2^-14 below the
- * largest: about 1.5e-5 of a result's size, a hundredth of its bf16 rounding.  Only kernel
+ * Any n_out, d, f, K >= 1.  A NaN in a row makes that row NaN, one in a weight that output column.  Calls
+ * for groups of at most 16 rows (rows_max or group_rows_max) multiply in bf16, exactly; others on the 8-bit matrix
+ * instruction, which drops, of 16 products at a time, what lies some 2^-14 below the largest: about 1.5e-5 of
+ * a result's size, a hundredth of its bf16 rounding.  Calls of few tiles are cut along K, into parts
+ * whose sums are kept in ws and added in order.  Only kernel
  * launches on `stream`; every sum in a fixed order (bit-reproducible). */
 size_t moe_grouped_linear_fp8_workspace_size(int32_t num_groups, int64_t rows_max, int32_t group_rows_max,
                                              int32_t n_out, int32_t k);

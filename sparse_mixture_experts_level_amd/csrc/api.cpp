@@ -703,8 +703,10 @@ moe_status check_matrix(const moe_fp8_matrix &m, const char *name) {
 moe_status check_fp8_shape(int32_t G, int32_t n_out, int32_t k, bool swiglu) {
   if (G < 1 || G > MOE_MAX_EXPERTS) return fail(MOE_ERR_INVALID, "num_groups %d outside [1, %d]", G, MOE_MAX_EXPERTS);
   if (n_out < 1 || k < 1) return fail(MOE_ERR_INVALID, "n_out and k must be >= 1");
-  // (the first two keep the third's product and the kernels' 32-bit counts of columns in range)
-  if (n_out >= (1 << 24) || k >= (1 << 24) || moe::fp8_weights_bytes(n_out, k, swiglu) >= ((int64_t)1 << 31))
+  // (n_out and k: a tile's 256 rows of k within the same offsets, and 32-bit counts of columns)
+  if (n_out >= (1 << 23) || k >= (1 << 23))
+    return fail(MOE_ERR_UNSUPPORTED, "n_out and k of a product in 8 bits must be below 2^23");
+  if (moe::fp8_weights_bytes(n_out, k, swiglu) >= ((int64_t)1 << 31))
     return fail(MOE_ERR_UNSUPPORTED, "one group's weights in 8 bits must be smaller than 2 GiB");
   return MOE_OK;
 }
@@ -730,9 +732,10 @@ bool fp8_large(int64_t rows_max, int32_t group_rows_max) {
 
 // Workspace of the products in 8 bits: packed tiles of the rows and, for the FFN (f > 0), H in rows and in packed tiles.
 struct Fp8Layout {
-  size_t xp, xp_scale, h8, h_scale, hp, hp_scale, total;
+  size_t xp, xp_scale, h8, h_scale, hp, hp_scale, parts, total;
 };
-Fp8Layout fp8_layout(int32_t G, int64_t rows_max, int32_t group_rows_max, int32_t k, int32_t f) {
+// k: the rows' width; n_out: the projection's, or f: the FFN's hidden width (n_out = k).
+Fp8Layout fp8_layout(int32_t G, int64_t rows_max, int32_t group_rows_max, int32_t k, int32_t n_out, int32_t f) {
   Fp8Layout L{};
   size_t o = 0;
   auto take = [&](int64_t bytes) {
@@ -747,12 +750,16 @@ Fp8Layout fp8_layout(int32_t G, int64_t rows_max, int32_t group_rows_max, int32_
   L.h_scale = take(f ? rows_max * moe::fp8_scale_bytes(f) : 0);
   L.hp = take(f && large ? moe::fp8_packed_bytes(rows_max, G, f) : 0);
   L.hp_scale = take(f && large ? moe::fp8_packed_scale_bytes(rows_max, G, f) : 0);
+  if (std::min<int64_t>(rows_max, group_rows_max) > moe::kFp8SmallRows)
+    L.parts = take(f ? std::max(moe::fp8_parts_bytes(rows_max, group_rows_max, f, k, true),
+                                moe::fp8_parts_bytes(rows_max, group_rows_max, n_out, f, false))
+                     : moe::fp8_parts_bytes(rows_max, group_rows_max, n_out, k, false));
   L.total = o;
   return L;
 }
 
 size_t swiglu_fp8_ws_bytes(int32_t G, int64_t rows_max, int32_t group_rows_max, int32_t d, int32_t f) {
-  return fp8_layout(G, rows_max, group_rows_max, d, f).total;
+  return fp8_layout(G, rows_max, group_rows_max, d, d, f).total;
 }
 
 moe::Fp8GemmArgs fp8_args(int32_t G, int64_t rows_max, int32_t group_rows_max, int32_t n_out, int32_t k, const uint8_t *x8,
@@ -774,6 +781,12 @@ moe::Fp8GemmArgs fp8_args(int32_t G, int64_t rows_max, int32_t group_rows_max, i
   return a;
 }
 
+// Room for the sums of a product's parts.
+void parts_fp8(moe::Fp8GemmArgs &a, void *ws, const Fp8Layout &L, bool swiglu) {
+  a.parts_cap = moe::fp8_parts_cap(a.rows_max, a.group_rows_max, a.n_out, a.K, swiglu);
+  a.parts = at<float>(ws, L.parts);
+}
+
 // The packed tiles of a product's rows, where a group can have that many.
 moe_status pack_fp8(moe::Fp8GemmArgs &a, void *ws, const Fp8Layout &L, hipStream_t stream) {
   if (!fp8_large(a.rows_max, a.group_rows_max)) return MOE_OK;
@@ -788,11 +801,12 @@ moe_status run_swiglu_fp8(int32_t G, int64_t rows_max, int32_t group_rows_max, i
                           const uint8_t *x_scale, const int32_t *row_index, int64_t x_rows, const int32_t *offsets,
                           const moe_fp8_matrix &gate_up, const moe_fp8_matrix &down, void *y, void *ws,
                           hipStream_t stream) {
-  const Fp8Layout L = fp8_layout(G, rows_max, group_rows_max, d, f);
+  const Fp8Layout L = fp8_layout(G, rows_max, group_rows_max, d, d, f);
   const bool large = fp8_large(rows_max, group_rows_max);
   moe::Fp8GemmArgs a = fp8_args(G, rows_max, group_rows_max, f, d, x8, x_scale, row_index, x_rows, offsets,
                                 gate_up.codes, gate_up.scale);
   MOE_TRY(pack_fp8(a, ws, L, stream));
+  parts_fp8(a, ws, L, true);
   a.h8 = at<uint8_t>(ws, L.h8);
   a.h_scale = at<uint8_t>(ws, L.h_scale);
   a.hp = large ? at<uint8_t>(ws, L.hp) : nullptr;
@@ -800,6 +814,7 @@ moe_status run_swiglu_fp8(int32_t G, int64_t rows_max, int32_t group_rows_max, i
   MOE_TRY_HIP(moe::launch_fp8_gemm(a, stream), "gate_up in 8 bits");
   moe::Fp8GemmArgs b = fp8_args(G, rows_max, group_rows_max, d, f, a.h8, a.h_scale, nullptr, rows_max, offsets, down.codes,
                                 down.scale);
+  parts_fp8(b, ws, L, false);
   b.xp = a.hp;
   b.xp_scale = a.hp_scale;
   b.y = static_cast<uint16_t *>(y);
@@ -1848,7 +1863,7 @@ moe_status moe_rms_norm_backward(int32_t num_tokens, int32_t d_model, int32_t dt
 size_t moe_grouped_linear_fp8_workspace_size(int32_t num_groups, int64_t rows_max, int32_t group_rows_max,
                                              int32_t n_out, int32_t k) {
   if (check_fp8_shape(num_groups, n_out, k, false) != MOE_OK || check_fp8_rows(rows_max, group_rows_max) != MOE_OK) return 0;
-  return std::max<size_t>(fp8_layout(num_groups, rows_max, group_rows_max, k, 0).total, kAlign);
+  return std::max<size_t>(fp8_layout(num_groups, rows_max, group_rows_max, k, n_out, 0).total, kAlign);
 }
 
 moe_status moe_grouped_linear_fp8(int32_t num_groups, int64_t rows_max, int32_t group_rows_max, int32_t n_out, int32_t k,
@@ -1873,7 +1888,9 @@ moe_status moe_grouped_linear_fp8(int32_t num_groups, int64_t rows_max, int32_t 
   moe::Fp8GemmArgs a = fp8_args(num_groups, rows_max, group_rows_max, n_out, k, x8, x_scale, row_index,
                                 row_index ? x_row_count : rows_max, group_offsets, w8, w_scale);
   a.y = static_cast<uint16_t *>(y_rows);
-  MOE_TRY(pack_fp8(a, ws, fp8_layout(num_groups, rows_max, group_rows_max, k, 0), stream));
+  const Fp8Layout L = fp8_layout(num_groups, rows_max, group_rows_max, k, n_out, 0);
+  MOE_TRY(pack_fp8(a, ws, L, stream));
+  parts_fp8(a, ws, L, false);
   MOE_TRY_HIP(moe::launch_fp8_gemm(a, stream), "grouped product in 8 bits");
   return ok();
 }

@@ -19,29 +19,42 @@ namespace {
 
 constexpr int LG_TILE = kFp8LargeRows * 64;  // bytes of an operand's stage: 256 rows, 64 of K
 
-// Tile v of a launch: the tiles of the groups of many rows, group after group, then one for each group of few (any number of
-// rows where there are no packed copies).  One pass over the offsets, two for more than 64 groups; all results
-// in scalar registers.
+// Block `block` of a launch of per_tile blocks a tile and parts of K: the tiles of the groups of many rows, group after
+// group, then one for each group of few (any number of rows where there are no packed copies), all of them
+// again for each further part.  One pass over the offsets, two for more than 64 groups; all results in scalar registers.
 struct Fp8Tile {
-  int g, begin, end;           // -1: there is no such tile
-  int first, count, tiles;     // of the group's tiles (count 0: few rows), and all tiles of many rows
+  int g, begin, end;  // -1: there is no such tile
+  int first, count;   // the group's tiles, numbered over all groups (count 0: few rows)
+  int lin;            // the block's number among the tiles' (many rows: after the spreading)
+  int tiles;          // of many rows, in all
+  int part, parts;
 };
 __device__ __forceinline__ Fp8Tile find_tile(const Fp8GemmArgs &a, int tiles_max, int block, int per_tile, bool spread) {
   const int lane = threadIdx.x & 63, G = a.num_groups;
   const int few = a.xp ? kFp8FewRows : INT_MAX;
-  Fp8Tile t{-1, 0, 0, 0, 0, 0};
-  int b = 0, e = 0;
+  Fp8Tile t{-1, 0, 0, 0, 0, 0, 0, 0, 1};
+  int b = 0, e = 0, all = 0;
 #pragma unroll 1
   for (int g0 = 0; g0 < G; g0 += 64) {
     b = e = 0;
     if (g0 + lane < G) fp8_group_rows(a, g0 + lane, b, e);
     t.tiles += group_reduce<64>(a.xp ? fp8_large_tiles(e - b) : 0, [](int x, int y) { return x + y; });
+    all += __popcll(__ballot(e > b && e - b <= few));
   }
   // (offsets that decrease could count rows twice: no tile past those that the packed copies have room for)
   t.tiles = min(__builtin_amdgcn_readfirstlane(t.tiles), tiles_max);
+  all = __builtin_amdgcn_readfirstlane(all + t.tiles) * per_tile;
+  if (all == 0) return t;
+  if (spread && a.parts_cap > 1) {
+    t.parts = fp8_parts(all, a.rows_max, per_tile, a.K, a.parts_cap);
+    t.part = block / all;
+    block -= t.part * all;
+  }
+  if (t.part >= t.parts) return t;
   // the first tiles' blocks in one contiguous range an XCD, as neighbours share operands
   const int large = t.tiles * per_tile, lin = spread && block < large ? xcd_remap(block, large) : block;
   const int v = lin / per_tile;
+  t.lin = lin;
   const bool many = v < t.tiles;
   int seen = 0;
 #pragma unroll 1
@@ -73,6 +86,30 @@ __device__ __forceinline__ Fp8Tile find_tile(const Fp8GemmArgs &a, int tiles_max
   return t;
 }
 
+// Row and column tile of a block of a group of many rows.
+__device__ __forceinline__ void place(const Fp8GemmArgs &a, const Fp8Tile &t, int n_tiles, int weight_rows, int &mt, int &nt) {
+  const int local = t.lin - t.first * n_tiles;
+  if (t.end - t.begin <= weight_rows) {  // the weights are larger: their tile outermost
+    nt = local / t.count;
+    mt = local - nt * t.count;
+  } else {  // bands of four row tiles, weight tile outer within a band
+    constexpr int BAND = 4;
+    const int band = local / (BAND * n_tiles), r = local - band * BAND * n_tiles;
+    const int bm = min(BAND, t.count - band * BAND);
+    nt = r / bm;
+    mt = band * BAND + (r - nt * bm);
+  }
+  mt = __builtin_amdgcn_readfirstlane(mt);
+  nt = __builtin_amdgcn_readfirstlane(nt);
+}
+
+// A part's words of scales (four blocks of K each): first and past the last.
+__device__ __forceinline__ void part_of_k(const Fp8GemmArgs &a, const Fp8Tile &t, int &q0, int &q1) {
+  const int words = fp8_scale_bytes(a.K) / 4;
+  q0 = words * t.part / t.parts;
+  q1 = words * (t.part + 1) / t.parts;
+}
+
 // Some rows, up to 128 at a time: a workgroup has 128 columns of H or 256 of y, each of its eight waves two
 // blocks of 16 weight rows (gate and up, or neighbours).  The rows are read by all eight waves from LDS, where
 // loads without registers put them as codes, a step of 128 of K a stage, in the operand layout (2 KB for 16 rows:
@@ -82,14 +119,19 @@ constexpr int MD_R = 4, MD_D = 3, MD_ROWS = 128;
 
 // One block of n <= 16 MS rows from m0 on; MS is exact, so that no branch is in the loop.
 template <bool SWIGLU, int MS>
-__device__ __forceinline__ void medium_rows(const Fp8GemmArgs &a, int g, int nb, int m0, int n, uint8_t *s0, uint8_t *s1,
-                                            uint8_t *s2, uint8_t *s3, float (*tops)[MD_ROWS]) {
+__device__ __forceinline__ void medium_rows(const Fp8GemmArgs &a, const Fp8Tile &tile, int nb, int n_tiles, int m0, int n,
+                                            uint8_t *s0, uint8_t *s1, uint8_t *s2, uint8_t *s3, float (*tops)[MD_ROWS]) {
   constexpr int R = MD_R, D = MD_D;
   auto stage = [&](int b) -> uint8_t * { return b == 0 ? s0 : b == 1 ? s1 : b == 2 ? s2 : s3; };
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lr = lane & 15,
             lg = lane >> 4;
   const int kt = fp8_blocks(a.K), kp = fp8_row_bytes(a.K), ks = fp8_scale_bytes(a.K);
   const int units = (a.n_out + 15) / 16 * (SWIGLU ? 2 : 1), unit = nb * 16 + wave * 2;  // blocks of 16 weight rows
+  int tb, te;  // this part's steps
+  part_of_k(a, tile, tb, te);
+  tb *= 4;
+  te = min(kt, te * 4);
+  const int g = tile.g;
   const int64_t wbytes = fp8_group_bytes(a.n_out, a.K, SWIGLU);
   const rsrc_t wres = make_rsrc(a.w8 + g * wbytes, (uint32_t)wbytes);
   uint32_t half;
@@ -101,7 +143,7 @@ __device__ __forceinline__ void medium_rows(const Fp8GemmArgs &a, int g, int nb,
   auto load_w = [&](int j, int t) {
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      const bool in = t < kt && unit + b < units;
+      const bool in = t < te && unit + b < units;
       const uint32_t o = wbase + (uint32_t)(2 * t) * half + (uint32_t)b * 1024u;
       w[j][b] = fp8_operand(buf_ld16_nt(wres, in ? o : kOob), buf_ld16_nt(wres, in ? o + half : kOob));
     }
@@ -111,7 +153,7 @@ __device__ __forceinline__ void medium_rows(const Fp8GemmArgs &a, int g, int nb,
   const uint32_t src = rows.row(a, m0, wave * 16 + lr, n);
   const uint32_t xoff = src != kOob ? src * (uint32_t)kp + (uint32_t)lg * 16u : kOob;
   auto load_x = [&](int t, int b) {
-    const uint32_t o = t < kt && xoff != kOob ? xoff + (uint32_t)t * 128u : kOob;
+    const uint32_t o = t < te && xoff != kOob ? xoff + (uint32_t)t * 128u : kOob;
     buf_ld16_lds(rows.xres, o, stage(b) + wave * 2048);
     buf_ld16_lds(rows.xres, o == kOob ? kOob : o + 64u, stage(b) + wave * 2048 + 1024);
   };
@@ -134,12 +176,12 @@ __device__ __forceinline__ void medium_rows(const Fp8GemmArgs &a, int g, int nb,
   for (int i = 0; i < MS; ++i)
 #pragma unroll
     for (int b = 0; b < 2; ++b) acc[i][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  load_scales(0);
+  load_scales(tb);
 #pragma unroll
-  for (int b = 0; b < D; ++b) load_x(b, b);
+  for (int b = 0; b < D; ++b) load_x(tb + b, b);
   __builtin_amdgcn_sched_barrier(0);  // the waits count on rows before weights
 #pragma unroll
-  for (int j = 0; j < R; ++j) load_w(j, j);
+  for (int j = 0; j < R; ++j) load_w(j, tb + j);
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(4 * R) : "memory");  // the first stages are there
   auto bar = [&]() {
     __builtin_amdgcn_sched_barrier(0);
@@ -147,7 +189,7 @@ __device__ __forceinline__ void medium_rows(const Fp8GemmArgs &a, int g, int nb,
     __builtin_amdgcn_sched_barrier(0);
   };
   bar();
-  for (int t0 = 0; t0 < kt; t0 += R) {
+  for (int t0 = tb; t0 < te; t0 += R) {
     const uint32_t keep = kt - t0 >= 4 ? ~0u : (1u << (8 * (kt - t0))) - 1u;  // the padding's scales are not looked at
 #pragma unroll
     for (int i = 0; i < MS; ++i) sx[i] = nx[i] & keep;
@@ -181,6 +223,18 @@ __device__ __forceinline__ void medium_rows(const Fp8GemmArgs &a, int g, int nb,
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no write to LDS may outlive its rows
   __syncthreads();
+  if (tile.parts > 1) {
+#pragma unroll
+    for (int i = 0; i < MS; ++i) {
+      const int64_t row = m0 + i * 16 + lr;
+      if (row < m0 + n)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          *reinterpret_cast<f32x4 *>(a.parts + (tile.part * (int64_t)a.rows_max + row) * n_tiles * 256 + nb * 256 +
+                                     (SWIGLU ? b * 128 + wave * 16 : wave * 32 + b * 16) + lg * 4) = acc[i][b];
+    }
+    return;
+  }
   if constexpr (SWIGLU) {
     const int col = nb * 128 + wave * 16 + lg * 4;
 #pragma unroll
@@ -238,14 +292,15 @@ __global__ __launch_bounds__(512, 1) void fp8_rows_kernel(const Fp8GemmArgs a, i
   const Fp8Tile tile = find_tile(a, tiles_max, blockIdx.x, n_tiles, true);
   if (tile.g < 0) return;
   const int g = tile.g, begin = tile.begin, end = tile.end, mt_first = tile.first, mt_count = tile.count;
-  const int large = tile.tiles * n_tiles;
   if (mt_count == 0) {
-    const int nb = ((int)blockIdx.x - large) % n_tiles;
+    const int nb = (tile.lin - tile.tiles * n_tiles) % n_tiles;
     for (int m0 = begin; m0 < end; m0 += MD_ROWS) {
       const int n = min(MD_ROWS, end - m0);
       switch ((n + 15) / 16) {
-#define MOE_ROWS(MS) \
-  case MS: medium_rows<SWIGLU, MS>(a, g, nb, m0, n, sA0, sA1, sA2, sA3, reinterpret_cast<float(*)[MD_ROWS]>(sB0)); break
+#define MOE_ROWS(MS)                                                                       \
+  case MS:                                                                                 \
+    medium_rows<SWIGLU, MS>(a, tile, nb, n_tiles, m0, n, sA0, sA1, sA2, sA3, reinterpret_cast<float(*)[MD_ROWS]>(sB0)); \
+    break
         MOE_ROWS(1);
         MOE_ROWS(2);
         MOE_ROWS(3);
@@ -259,25 +314,16 @@ __global__ __launch_bounds__(512, 1) void fp8_rows_kernel(const Fp8GemmArgs a, i
     }
     return;
   }
-  const int local = xcd_remap(blockIdx.x, large) - mt_first * n_tiles;
   int mt, nt;
-  if (end - begin <= (SWIGLU ? 2 : 1) * a.n_out) {  // the weights are larger: their tile outermost
-    nt = local / mt_count;
-    mt = local - nt * mt_count;
-  } else {  // bands of four row tiles, weight tile outer within a band
-    constexpr int BAND = 4;
-    const int band = local / (BAND * n_tiles), r = local - band * BAND * n_tiles;
-    const int bm = min(BAND, mt_count - band * BAND);
-    nt = r / bm;
-    mt = band * BAND + (r - nt * bm);
-  }
-  mt = __builtin_amdgcn_readfirstlane(mt);
-  nt = __builtin_amdgcn_readfirstlane(nt);
+  place(a, tile, n_tiles, (SWIGLU ? 2 : 1) * a.n_out, mt, nt);
   const int per = fp8_tile_rows(end - begin, mt_count);
   const int m0 = begin + mt * per, rows = min(per, end - m0), m_tile = mt_first + mt;
   if (m_tile >= tiles_max) return;
   const int row_blocks = (rows + 31) / 32, mine = max(0, min(4, row_blocks - wm * 4));  // of 32 rows: the tile's, this wave's
-  const int kt = fp8_blocks(a.K), nk = 2 * kt, ks = fp8_scale_bytes(a.K);
+  const int kt = fp8_blocks(a.K), ks = fp8_scale_bytes(a.K);
+  int q0, q1;  // this part's words of scales, and its steps of 64
+  part_of_k(a, tile, q0, q1);
+  const int kfirst = 8 * q0, nk = min(2 * kt, 8 * q1) - kfirst;
   const int64_t abytes = (int64_t)kFp8LargeRows * kt * kFp8Block;
   const int64_t wbytes = fp8_group_bytes(a.n_out, a.K, SWIGLU);
   const rsrc_t ares = make_rsrc(a.xp + m_tile * abytes, (uint32_t)abytes);
@@ -294,7 +340,7 @@ __global__ __launch_bounds__(512, 1) void fp8_rows_kernel(const Fp8GemmArgs a, i
     boff[i] = nt * 16 + 2 * wave + i < wblocks ? wtile + at : kOob;
   }
   auto issue = [&](int s, int b) {
-    const uint32_t ka = (uint32_t)s * (uint32_t)LG_TILE, kb = (uint32_t)s * wstep;
+    const uint32_t ka = (uint32_t)(kfirst + s) * (uint32_t)LG_TILE, kb = (uint32_t)(kfirst + s) * wstep;
     const bool in = s < nk;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -374,7 +420,7 @@ __global__ __launch_bounds__(512, 1) void fp8_rows_kernel(const Fp8GemmArgs a, i
       for (int j = 0; j < 2; ++j) cw[j] = sw[j];
       load_scales(q + 1);
     };
-    load_scales(0);
+    load_scales(q0);
 #pragma unroll
     for (int b = 0; b < 3; ++b) issue(b, b);
     asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
@@ -382,7 +428,7 @@ __global__ __launch_bounds__(512, 1) void fp8_rows_kernel(const Fp8GemmArgs a, i
     if (second) bar();
     int s0 = 0;
     for (; s0 + 8 <= nk; s0 += 8) {
-      next_scales(s0 / 8);
+      next_scales(q0 + s0 / 8);
 #pragma unroll
       for (int b = 0; b < 8; ++b) {
         mem(s0 + b, b);
@@ -392,7 +438,7 @@ __global__ __launch_bounds__(512, 1) void fp8_rows_kernel(const Fp8GemmArgs a, i
       }
     }
     if (s0 < nk) {
-      next_scales(s0 / 8);
+      next_scales(q0 + s0 / 8);
 #pragma unroll
       for (int b = 0; b < 7; ++b) {
         if (s0 + b >= nk) break;
@@ -408,6 +454,22 @@ __global__ __launch_bounds__(512, 1) void fp8_rows_kernel(const Fp8GemmArgs a, i
   __syncthreads();
 
   // Block (i, j): lane l holds row wm * 128 + i * 32 + l % 32 and, per q = 0..3, columns 8 q + 4 (l / 32) .. + 3 of its 32.
+  if (tile.parts > 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = wm * 128 + i * 32 + lr;
+      if (row >= rows) continue;
+      float *o = a.parts + (tile.part * (int64_t)a.rows_max + m0 + row) * n_tiles * 256 + nt * 256 + lh * 4 +
+                 (SWIGLU ? wn * 32 : wn * 64);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<f32x4 *>(o + j * (SWIGLU ? 128 : 32) + q * 8) =
+              f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    }
+    return;
+  }
   if constexpr (SWIGLU) {
     float *tops = reinterpret_cast<float *>(sB0);  // [4 waves of columns][256 rows]
     float top[4];
@@ -482,6 +544,70 @@ __global__ __launch_bounds__(512, 1) void fp8_rows_kernel(const Fp8GemmArgs a, i
   }
 }
 
+// The parts' sums in order, and what the product's own epilogue does with them: sixteen workgroups a tile of
+// fp8_rows_kernel.
+template <bool SWIGLU>
+__global__ __launch_bounds__(256) void fp8_add_parts_kernel(const Fp8GemmArgs a, int n_tiles, int tiles_max) {
+  const Fp8Tile tile = find_tile(a, tiles_max, blockIdx.x, n_tiles, true);
+  if (tile.g < 0 || tile.parts == 1 || tile.part > 0) return;
+  int nt, mt = 0, m0 = tile.begin, n = tile.end - tile.begin, last = n;
+  if (tile.count) {
+    place(a, tile, n_tiles, (SWIGLU ? 2 : 1) * a.n_out, mt, nt);
+    const int per = fp8_tile_rows(n, tile.count);
+    m0 += mt * per;
+    n = min(per, tile.end - m0);
+    last = (n + 31) / 32 * 32;  // packed tiles are read by whole 32s
+  } else {
+    nt = (tile.lin - tile.tiles * n_tiles) % n_tiles;
+  }
+  const int m_tile = tile.first + mt;
+  if (tile.count && m_tile >= tiles_max) return;
+  constexpr int LANES = SWIGLU ? 16 : 32;  // of eight columns each, a row
+  const int l = threadIdx.x % LANES;
+  for (int r = blockIdx.y * (256 / LANES) + threadIdx.x / LANES; r < (SWIGLU ? last : n); r += gridDim.y * (256 / LANES)) {
+    float v[SWIGLU ? 2 : 1][8] = {};
+    if (r < n)
+#pragma unroll 2
+      for (int s = 0; s < tile.parts; ++s) {
+        const float *p = a.parts + (s * (int64_t)a.rows_max + m0 + r) * n_tiles * 256 + nt * 256 + l * 8;
+#pragma unroll
+        for (int h = 0; h < (SWIGLU ? 2 : 1); ++h) {
+          const f32x4 x = *reinterpret_cast<const f32x4 *>(p + h * 128), y = *reinterpret_cast<const f32x4 *>(p + h * 128 + 4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[h][e] += x[e];
+            v[h][4 + e] += y[e];
+          }
+        }
+      }
+    if constexpr (SWIGLU) {
+      float top = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[0][e] = silu_f32(v[0][e]) * v[1][e];
+        top = fmaxf(top, fp8_magnitude(v[0][e]));
+      }
+      top = group_reduce<16>(top, [](float x, float y) { return fmaxf(x, y); });
+      const uint32_t byte = fp8_scale_byte(top);
+      const float inv = fp8_inverse(byte);
+      const uint2 codes{fp8_codes(v[0][0] * inv, v[0][1] * inv, v[0][2] * inv, v[0][3] * inv),
+                        fp8_codes(v[0][4] * inv, v[0][5] * inv, v[0][6] * inv, v[0][7] * inv)};
+      const int ht = fp8_blocks(a.n_out), hs = fp8_scale_bytes(a.n_out);
+      if (tile.count) {
+        uint8_t *o = a.hp + (((int64_t)m_tile * ht + nt) * 2 + l / 8) * LG_TILE;
+        *reinterpret_cast<uint2 *>(o + (r >> 4) * 1024 + (l / 2 % 4) * 256 + (r & 15) * 16 + l % 2 * 8) = codes;
+        if (l == 0) a.hp_scale[(int64_t)m_tile * kFp8LargeRows * hs + ((nt / 4) * kFp8LargeRows + r) * 4 + nt % 4] = (uint8_t)byte;
+      } else {
+        *reinterpret_cast<uint2 *>(a.h8 + (int64_t)(m0 + r) * fp8_row_bytes(a.n_out) + nt * 128 + l * 8) = codes;
+        if (l == 0) a.h_scale[(int64_t)(m0 + r) * hs + nt] = (uint8_t)byte;
+      }
+    } else {
+      const int col = nt * 256 + l * 8;
+      store8<bf16_t, false>(a.y + (int64_t)(m0 + r) * a.n_out + col, a.n_out - col, v[0]);
+    }
+  }
+}
+
 // The rows of the tiles, and their scales as [4 blocks of K][256 rows] words, for fp8_rows_kernel: one
 // workgroup 64 rows of a tile and four blocks of K; a wave reads 64 bytes of its 16 rows at a time, the other half of
 // each line next, and writes them as one piece of 1 KB (whole rows a wave, 16 bytes of each written apart: 36 us for
@@ -531,12 +657,20 @@ hipError_t launch_fp8_gemm_rows(const Fp8GemmArgs &a, hipStream_t s) {
   const bool swiglu = a.h8 != nullptr;
   const int n_tiles = (a.n_out + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256);
   const int64_t tiles = a.xp ? fp8_large_tiles_max(a.rows_max, a.num_groups) : 0;
-  const int64_t grid = (tiles + std::min(a.num_groups, a.rows_max)) * n_tiles;
+  const int64_t blocks = (tiles + std::min(a.num_groups, a.rows_max)) * n_tiles;
+  const int64_t grid = a.parts_cap > 1 ? std::max<int64_t>(blocks, 256) : blocks;  // parts are one round at most
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
   if (swiglu)
     hipLaunchKernelGGL((fp8_rows_kernel<true>), dim3((unsigned)grid), dim3(512), 0, s, a, n_tiles, (int)tiles);
   else
     hipLaunchKernelGGL((fp8_rows_kernel<false>), dim3((unsigned)grid), dim3(512), 0, s, a, n_tiles, (int)tiles);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.parts_cap == 1) return e;
+  const dim3 adding((unsigned)std::min<int64_t>(blocks, 128), 16);  // tiles in parts are half a round at most
+  if (swiglu)
+    hipLaunchKernelGGL((fp8_add_parts_kernel<true>), adding, dim3(256), 0, s, a, n_tiles, (int)tiles);
+  else
+    hipLaunchKernelGGL((fp8_add_parts_kernel<false>), adding, dim3(256), 0, s, a, n_tiles, (int)tiles);
   return hipGetLastError();
 }
 

@@ -241,6 +241,10 @@ struct Fp8GemmArgs {
   uint16_t *y;
   uint8_t *h8, *h_scale;
   int num_groups, rows_max, group_rows_max, x_rows, n_out, K;
+  // Products of few tiles and a long K are cut along K: float sums [parts_cap][rows_max][fp8_part_columns()] of the parts,
+  // added up by a second kernel.  1 and NULL: never.
+  float *parts;
+  int parts_cap;
   // Groups of more than kFp8FewRows go through a kernel for many rows, which reads them (and writes H) in packed
   // tiles of fp8_packed_bytes(); xp and hp are NULL where no group can have that many.
   const uint8_t *xp, *xp_scale;
@@ -266,6 +270,41 @@ inline int64_t fp8_packed_bytes(int64_t rows, int G, int k) {
 }
 inline int64_t fp8_packed_scale_bytes(int64_t rows, int G, int k) {
   return fp8_large_tiles_max(rows, G) * kFp8LargeRows * fp8_scale_bytes(k);
+}
+// Parts of K for `blocks` workgroups (tiles of 256 x 256 or 128 x 256, tiles_n of 256 columns to a row) on 256 CUs: the
+// number, of at most `most` and in one round, with the least estimated time, in 256ths of what 512 of K (a word of
+// scales) takes a tile, 5 us: a part begins and ends in two of them, its sums are written and read again in 5/256 of one
+// for 256 rows, the second launch costs one; an eighth has to be won.  Evaluated alike by the product and by
+// the kernel that adds the parts.  It falls with growing `blocks`.  (us whole and in parts, 1 x 100 rows x 1024 x
+// 7168: 59 and 27; 300 x 4096 x 14336: 118 and 50; 4096 x 1024 x 14336: 143 and 95; 8 x 400 x 1024 x 7168: 75 and 60.)
+constexpr int kFp8Parts = 16;
+__host__ __device__ inline int fp8_parts(int64_t blocks, int64_t rows, int tiles_n, int k, int most) {
+  const int words = fp8_scale_bytes(k) / 4;
+  const int64_t sums = 5 * rows * tiles_n / 256;
+  int best = 1;
+  int64_t least = 224 * (words + 2);
+  for (int s = 2; s <= most && s <= words && blocks * s <= 256; ++s) {
+    const int64_t cost = 256 * ((words + s - 1) / s + 3) + sums * s;
+    if (cost < least) {
+      best = s;
+      least = cost;
+    }
+  }
+  return best;
+}
+inline int64_t fp8_part_columns(int n_out, bool swiglu) {
+  return swiglu ? ((int64_t)n_out + 127) / 128 * 256 : ((int64_t)n_out + 255) / 256 * 256;
+}
+// The most parts of a product of `rows` rows in groups of `group_rows` at most, which are that many tiles at
+// least (with fewer rows than announced there are no more parts than this).
+inline int fp8_parts_cap(int64_t rows, int64_t group_rows, int n_out, int k, bool swiglu) {
+  const int64_t per = std::max<int64_t>(std::min<int64_t>(group_rows, kFp8LargeRows), 1);
+  const int tiles_n = (int)(fp8_part_columns(n_out, swiglu) / 256);
+  return fp8_parts((rows + per - 1) / per * tiles_n, rows, tiles_n, k, kFp8Parts);
+}
+inline int64_t fp8_parts_bytes(int64_t rows, int64_t group_rows, int n_out, int k, bool swiglu) {
+  const int cap = fp8_parts_cap(rows, group_rows, n_out, k, swiglu);
+  return cap > 1 ? 4 * cap * rows * fp8_part_columns(n_out, swiglu) : 0;
 }
 // x8 (through row_index) and its scales to packed tiles.
 hipError_t launch_fp8_pack_rows(const Fp8GemmArgs &a, uint8_t *xp, uint8_t *xp_scale, hipStream_t s);

@@ -204,7 +204,8 @@ COMMON = [(dict(G=0), INVALID), (dict(G=1025), INVALID), (dict(rows=-1), INVALID
 @needs_lib
 @pytest.mark.parametrize("kw,status", COMMON + [
     (dict(n=0), INVALID), (dict(k=0), INVALID), (dict(n=1 << 16, k=1 << 15), UNSUPPORTED), (dict(w8=None), INVALID),
-    (dict(ws8=None), INVALID), (dict(ws8=FAKE + 4), INVALID), (dict(k=1 << 24), UNSUPPORTED)])
+    (dict(ws8=None), INVALID), (dict(ws8=FAKE + 4), INVALID), (dict(k=1 << 24), UNSUPPORTED),
+    (dict(k=1 << 23, n=1), UNSUPPORTED), (dict(k=1, n=1 << 23), UNSUPPORTED)])
 def test_linear_refusals(kw, status):
     L = ops.lib()
     assert _linear(L, **kw) == status and L.moe_last_error()
