@@ -744,8 +744,9 @@ Fp8Layout fp8_layout(int32_t G, int64_t rows_max, int32_t group_rows_max, int32_
     return at;
   };
   const bool large = fp8_large(rows_max, group_rows_max);
-  L.xp = take(large ? moe::fp8_packed_bytes(rows_max, G, k) : 0);
-  L.xp_scale = take(large ? moe::fp8_packed_scale_bytes(rows_max, G, k) : 0);
+  const bool packs = large && moe::fp8_packs(f ? f : n_out, f);
+  L.xp = take(packs ? moe::fp8_packed_bytes(rows_max, G, k) : 0);
+  L.xp_scale = take(packs ? moe::fp8_packed_scale_bytes(rows_max, G, k) : 0);
   L.h8 = take(f ? rows_max * moe::fp8_row_bytes(f) : 0);
   L.h_scale = take(f ? rows_max * moe::fp8_scale_bytes(f) : 0);
   L.hp = take(f && large ? moe::fp8_packed_bytes(rows_max, G, f) : 0);
@@ -778,6 +779,7 @@ moe::Fp8GemmArgs fp8_args(int32_t G, int64_t rows_max, int32_t group_rows_max, i
   a.x_rows = (int)x_rows;
   a.n_out = n_out;
   a.K = k;
+  a.large = fp8_large(rows_max, group_rows_max);
   return a;
 }
 
@@ -787,9 +789,9 @@ void parts_fp8(moe::Fp8GemmArgs &a, void *ws, const Fp8Layout &L, bool swiglu) {
   a.parts = at<float>(ws, L.parts);
 }
 
-// The packed tiles of a product's rows, where a group can have that many.
-moe_status pack_fp8(moe::Fp8GemmArgs &a, void *ws, const Fp8Layout &L, hipStream_t stream) {
-  if (!fp8_large(a.rows_max, a.group_rows_max)) return MOE_OK;
+// The packed tiles of a product's rows, where there are to be any.
+moe_status pack_fp8(moe::Fp8GemmArgs &a, void *ws, const Fp8Layout &L, bool swiglu, hipStream_t stream) {
+  if (!a.large || !moe::fp8_packs(a.n_out, swiglu)) return MOE_OK;
   MOE_TRY_HIP(moe::launch_fp8_pack_rows(a, at<uint8_t>(ws, L.xp), at<uint8_t>(ws, L.xp_scale), stream), "rows to tiles");
   a.xp = at<uint8_t>(ws, L.xp);
   a.xp_scale = at<uint8_t>(ws, L.xp_scale);
@@ -802,15 +804,14 @@ moe_status run_swiglu_fp8(int32_t G, int64_t rows_max, int32_t group_rows_max, i
                           const moe_fp8_matrix &gate_up, const moe_fp8_matrix &down, void *y, void *ws,
                           hipStream_t stream) {
   const Fp8Layout L = fp8_layout(G, rows_max, group_rows_max, d, d, f);
-  const bool large = fp8_large(rows_max, group_rows_max);
   moe::Fp8GemmArgs a = fp8_args(G, rows_max, group_rows_max, f, d, x8, x_scale, row_index, x_rows, offsets,
                                 gate_up.codes, gate_up.scale);
-  MOE_TRY(pack_fp8(a, ws, L, stream));
+  MOE_TRY(pack_fp8(a, ws, L, true, stream));
   parts_fp8(a, ws, L, true);
   a.h8 = at<uint8_t>(ws, L.h8);
   a.h_scale = at<uint8_t>(ws, L.h_scale);
-  a.hp = large ? at<uint8_t>(ws, L.hp) : nullptr;
-  a.hp_scale = large ? at<uint8_t>(ws, L.hp_scale) : nullptr;
+  a.hp = a.large ? at<uint8_t>(ws, L.hp) : nullptr;
+  a.hp_scale = a.large ? at<uint8_t>(ws, L.hp_scale) : nullptr;
   MOE_TRY_HIP(moe::launch_fp8_gemm(a, stream), "gate_up in 8 bits");
   moe::Fp8GemmArgs b = fp8_args(G, rows_max, group_rows_max, d, f, a.h8, a.h_scale, nullptr, rows_max, offsets, down.codes,
                                 down.scale);
@@ -1889,7 +1890,7 @@ moe_status moe_grouped_linear_fp8(int32_t num_groups, int64_t rows_max, int32_t 
                                 row_index ? x_row_count : rows_max, group_offsets, w8, w_scale);
   a.y = static_cast<uint16_t *>(y_rows);
   const Fp8Layout L = fp8_layout(num_groups, rows_max, group_rows_max, k, n_out, 0);
-  MOE_TRY(pack_fp8(a, ws, L, stream));
+  MOE_TRY(pack_fp8(a, ws, L, false, stream));
   parts_fp8(a, ws, L, false);
   MOE_TRY_HIP(moe::launch_fp8_gemm(a, stream), "grouped product in 8 bits");
   return ok();

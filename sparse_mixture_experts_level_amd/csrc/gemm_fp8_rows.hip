@@ -31,14 +31,14 @@ struct Fp8Tile {
 };
 __device__ __forceinline__ Fp8Tile find_tile(const Fp8GemmArgs &a, int tiles_max, int block, int per_tile, bool spread) {
   const int lane = threadIdx.x & 63, G = a.num_groups;
-  const int few = a.xp ? kFp8FewRows : INT_MAX;
+  const int few = a.large ? kFp8FewRows : INT_MAX;
   Fp8Tile t{-1, 0, 0, 0, 0, 0, 0, 0, 1};
   int b = 0, e = 0, all = 0;
 #pragma unroll 1
   for (int g0 = 0; g0 < G; g0 += 64) {
     b = e = 0;
     if (g0 + lane < G) fp8_group_rows(a, g0 + lane, b, e);
-    t.tiles += group_reduce<64>(a.xp ? fp8_large_tiles(e - b) : 0, [](int x, int y) { return x + y; });
+    t.tiles += group_reduce<64>(a.large ? fp8_large_tiles(e - b) : 0, [](int x, int y) { return x + y; });
     all += __popcll(__ballot(e > b && e - b <= few));
   }
   // (offsets that decrease could count rows twice: no tile past those that the packed copies have room for)
@@ -326,9 +326,14 @@ __global__ __launch_bounds__(512, 1) void fp8_rows_kernel(const Fp8GemmArgs a, i
   const int kfirst = 8 * q0, nk = min(2 * kt, 8 * q1) - kfirst;
   const int64_t abytes = (int64_t)kFp8LargeRows * kt * kFp8Block;
   const int64_t wbytes = fp8_group_bytes(a.n_out, a.K, SWIGLU);
-  const rsrc_t ares = make_rsrc(a.xp + m_tile * abytes, (uint32_t)abytes);
+  // the rows as they are, or packed
+  const Fp8Rows from(a, m0, rows);
+  const bool packed = a.xp != nullptr;
+  const rsrc_t ares = packed ? make_rsrc(a.xp + m_tile * abytes, (uint32_t)abytes) : from.xres;
+  const rsrc_t sres = packed ? make_rsrc(a.xp_scale + (int64_t)m_tile * kFp8LargeRows * ks, (uint32_t)(kFp8LargeRows * ks))
+                             : from.sres;
+  const uint32_t astep = packed ? (uint32_t)LG_TILE : 64u, sstep = packed ? kFp8LargeRows * 4u : 4u;
   const rsrc_t wres = make_rsrc(a.w8 + g * wbytes, (uint32_t)wbytes);
-  const rsrc_t sres = make_rsrc(a.xp_scale + (int64_t)m_tile * kFp8LargeRows * ks, (uint32_t)(kFp8LargeRows * ks));
   // this wave's pieces of a stage: 16-row blocks 2 wave and 2 wave + 1 of both operands
   uint32_t aoff[2], boff[2], wstep;
   const int wblocks = (a.n_out + 15) / 16 * (SWIGLU ? 2 : 1);
@@ -336,11 +341,16 @@ __global__ __launch_bounds__(512, 1) void fp8_rows_kernel(const Fp8GemmArgs a, i
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const uint32_t at = (uint32_t)(2 * wave + i) * 1024u + (uint32_t)lane * 16u;
-    aoff[i] = wave < row_blocks ? at : kOob;
+    if (packed) {
+      aoff[i] = wave < row_blocks ? at : kOob;
+    } else {
+      const uint32_t src = from.row(a, m0, (2 * wave + i) * 16 + (lane & 15), rows);
+      aoff[i] = src != kOob ? src * (uint32_t)fp8_row_bytes(a.K) + (uint32_t)(lane >> 4) * 16u : kOob;
+    }
     boff[i] = nt * 16 + 2 * wave + i < wblocks ? wtile + at : kOob;
   }
   auto issue = [&](int s, int b) {
-    const uint32_t ka = (uint32_t)(kfirst + s) * (uint32_t)LG_TILE, kb = (uint32_t)(kfirst + s) * wstep;
+    const uint32_t ka = (uint32_t)(kfirst + s) * astep, kb = (uint32_t)(kfirst + s) * wstep;
     const bool in = s < nk;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -351,13 +361,21 @@ __global__ __launch_bounds__(512, 1) void fp8_rows_kernel(const Fp8GemmArgs a, i
   const int sblocks = fp8_blocks(a.n_out);
   const uint8_t *wscale = a.w_scale + ((int64_t)g * sblocks + (SWIGLU ? nt : min(nt * 2 + wn / 2, sblocks - 1))) *
                                           (SWIGLU ? 2 : 1) * ks;
-  uint32_t sx[4], sw[2];
+  uint32_t sx[4], sw[2], soff[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = wm * 128 + i * 32 + lr;
+    soff[i] = (uint32_t)row * 4u;
+    if (!packed) {
+      const uint32_t src = from.row(a, m0, row, rows);
+      soff[i] = src != kOob ? src * (uint32_t)ks : kOob;
+    }
+  }
   // four blocks of K, eight steps; past K zeros, or the last ones again
   auto load_scales = [&](int q) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      sx[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
-          sres, (uint32_t)(q * kFp8LargeRows + wm * 128 + i * 32 + lr) * 4u, 0, 0);
+      sx[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(sres, soff[i] != kOob ? soff[i] + (uint32_t)q * sstep : kOob, 0, 0);
 #pragma unroll
     for (int j = 0; j < 2; ++j) sw[j] = scalar_load(wscale + (SWIGLU ? j * ks : 0) + min(4 * q, ks - 4));
   };
@@ -643,12 +661,10 @@ __global__ __launch_bounds__(256) void fp8_pack_rows_kernel(const Fp8GemmArgs a,
 
 hipError_t launch_fp8_pack_rows(const Fp8GemmArgs &a, uint8_t *xp, uint8_t *xp_scale, hipStream_t s) {
   const int64_t tiles = fp8_large_tiles_max(a.rows_max, a.num_groups);
-  Fp8GemmArgs c = a;
-  c.xp = xp;  // there are packed copies
   const int quads = fp8_scale_bytes(a.K) / 4;
   if (tiles > 0x7fffffff / 4 || quads > 65535) return hipErrorInvalidValue;
   if (tiles > 0)
-    hipLaunchKernelGGL(fp8_pack_rows_kernel, dim3((unsigned)tiles * (kFp8LargeRows / 64), (unsigned)quads), dim3(256), 0, s, c,
+    hipLaunchKernelGGL(fp8_pack_rows_kernel, dim3((unsigned)tiles * (kFp8LargeRows / 64), (unsigned)quads), dim3(256), 0, s, a,
                        xp, xp_scale, (int)tiles);
   return hipGetLastError();
 }
@@ -656,7 +672,7 @@ hipError_t launch_fp8_pack_rows(const Fp8GemmArgs &a, uint8_t *xp, uint8_t *xp_s
 hipError_t launch_fp8_gemm_rows(const Fp8GemmArgs &a, hipStream_t s) {
   const bool swiglu = a.h8 != nullptr;
   const int n_tiles = (a.n_out + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256);
-  const int64_t tiles = a.xp ? fp8_large_tiles_max(a.rows_max, a.num_groups) : 0;
+  const int64_t tiles = a.large ? fp8_large_tiles_max(a.rows_max, a.num_groups) : 0;
   const int64_t blocks = (tiles + std::min(a.num_groups, a.rows_max)) * n_tiles;
   const int64_t grid = a.parts_cap > 1 ? std::max<int64_t>(blocks, 256) : blocks;  // parts are one round at most
   if (grid > 0x7fffffff) return hipErrorInvalidValue;

@@ -245,8 +245,9 @@ struct Fp8GemmArgs {
   // added up by a second kernel.  1 and NULL: never.
   float *parts;
   int parts_cap;
-  // Groups of more than kFp8FewRows go through a kernel for many rows, which reads them (and writes H) in packed
-  // tiles of fp8_packed_bytes(); xp and hp are NULL where no group can have that many.
+  // Groups of more than kFp8FewRows go in tiles of up to 256 rows (large: a group can have that many); their rows are read
+  // from xp, packed tiles of fp8_packed_bytes(), or, NULL, as they are; H goes to packed tiles.
+  bool large;
   const uint8_t *xp, *xp_scale;
   uint8_t *hp, *hp_scale;
 };
@@ -306,6 +307,12 @@ inline int64_t fp8_parts_bytes(int64_t rows, int64_t group_rows, int n_out, int 
   const int cap = fp8_parts_cap(rows, group_rows, n_out, k, swiglu);
   return cap > 1 ? 4 * cap * rows * fp8_part_columns(n_out, swiglu) : 0;
 }
+// Whether the rows of large tiles are packed first: a stage of 64 of K is half of each row's line, which every column tile
+// then reads twice, but packing is a launch and a copy.  us as they are and packed: 4096 x 1024 x 14336 (4
+// column tiles) 83 and 99, 8 x 300 x 2048 x 2048 (8) 30 and 36, 1024 x 4096 x 4096 (16) 57 and 52, 4096 x 8192 x 14336 (32)
+// 384 and 375, (56) 789 and 682.
+constexpr int kFp8PackTiles = 8;
+inline bool fp8_packs(int n_out, bool swiglu) { return fp8_part_columns(n_out, swiglu) / 256 > kFp8PackTiles; }
 // x8 (through row_index) and its scales to packed tiles.
 hipError_t launch_fp8_pack_rows(const Fp8GemmArgs &a, uint8_t *xp, uint8_t *xp_scale, hipStream_t s);
 hipError_t launch_fp8_gemm(const Fp8GemmArgs &a, hipStream_t s);
