@@ -110,6 +110,11 @@ __device__ __forceinline__ i32x8 fp8_operand(u32x4 lo, u32x4 hi) {
   return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
+// 4 bytes per lane from a buffer straight into LDS, as buf_ld16_lds.
+__device__ __forceinline__ void buf_ld4_lds(rsrc_t r, uint32_t off, void *lds_wave_base) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)lds_wave_base, 4, off, 0, 0, 0);
+}
+
 // A word at an address that is the same in every lane, by the scalar unit (the compiler takes the vector path for memory
 // that it cannot prove unwritten).
 __device__ __forceinline__ uint32_t scalar_load(const uint8_t *p) {

@@ -120,7 +120,8 @@ constexpr int MD_R = 4, MD_D = 3, MD_ROWS = 128;
 // One block of n <= 16 MS rows from m0 on; MS is exact, so that no branch is in the loop.
 template <bool SWIGLU, int MS>
 __device__ __forceinline__ void medium_rows(const Fp8GemmArgs &a, const Fp8Tile &tile, int nb, int n_tiles, int m0, int n,
-                                            uint8_t *s0, uint8_t *s1, uint8_t *s2, uint8_t *s3, float (*tops)[MD_ROWS]) {
+                                            uint8_t *s0, uint8_t *s1, uint8_t *s2, uint8_t *s3, uint8_t *row_scales,
+                                            float (*tops)[MD_ROWS]) {
   constexpr int R = MD_R, D = MD_D;
   auto stage = [&](int b) -> uint8_t * { return b == 0 ? s0 : b == 1 ? s1 : b == 2 ? s2 : s3; };
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lr = lane & 15,
@@ -157,19 +158,17 @@ __device__ __forceinline__ void medium_rows(const Fp8GemmArgs &a, const Fp8Tile 
     buf_ld16_lds(rows.xres, o, stage(b) + wave * 2048);
     buf_ld16_lds(rows.xres, o == kOob ? kOob : o + 64u, stage(b) + wave * 2048 + 1024);
   };
-  uint32_t soff[MS], sx[MS], nx[MS], sw[2], nw[2];
+  // The rows' scales of four steps go through LDS too, each wave's 16 rows by one load: read by every wave from memory they
+  // are MS loads of 16 lines each, behind which the waits below found too few weights still in flight.
+  const uint32_t soff = src != kOob && lg == 0 ? src * (uint32_t)ks : kOob;
+  uint32_t sx[MS], sw[2], nw[2];
+  // of four steps; past K those of the last four again (their codes are zeros)
+  auto load_row_scales = [&](int t) {
+    buf_ld4_lds(rows.sres, soff == kOob ? kOob : soff + (uint32_t)min(t, ks - 4), row_scales + wave * 256);
+  };
+  auto load_scales = [&](int t) {
 #pragma unroll
-  for (int i = 0; i < MS; ++i) {
-    const uint32_t r = rows.row(a, m0, i * 16 + lr, n);
-    soff[i] = r != kOob ? r * (uint32_t)ks : kOob;
-  }
-  auto load_scales = [&](int t) {  // of four steps; past K those of the last four again (their codes are zeros)
-    const int at = min(t, ks - 4);
-#pragma unroll
-    for (int i = 0; i < MS; ++i)
-      nx[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rows.sres, soff[i] == kOob ? kOob : soff[i] + (uint32_t)at, 0, 0);
-#pragma unroll
-    for (int b = 0; b < 2; ++b) nw[b] = scalar_load(wscale + (SWIGLU ? b * ks : 0) + at);
+    for (int b = 0; b < 2; ++b) nw[b] = scalar_load(wscale + (SWIGLU ? b * ks : 0) + min(t, ks - 4));
   };
   f32x4 acc[MS][2];
 #pragma unroll
@@ -177,6 +176,7 @@ __device__ __forceinline__ void medium_rows(const Fp8GemmArgs &a, const Fp8Tile 
 #pragma unroll
     for (int b = 0; b < 2; ++b) acc[i][b] = f32x4{0.f, 0.f, 0.f, 0.f};
   load_scales(tb);
+  load_row_scales(tb);
 #pragma unroll
   for (int b = 0; b < D; ++b) load_x(tb + b, b);
   __builtin_amdgcn_sched_barrier(0);  // the waits count on rows before weights
@@ -192,13 +192,17 @@ __device__ __forceinline__ void medium_rows(const Fp8GemmArgs &a, const Fp8Tile 
   for (int t0 = tb; t0 < te; t0 += R) {
     const uint32_t keep = kt - t0 >= 4 ? ~0u : (1u << (8 * (kt - t0))) - 1u;  // the padding's scales are not looked at
 #pragma unroll
-    for (int i = 0; i < MS; ++i) sx[i] = nx[i] & keep;
+    for (int i = 0; i < MS; ++i) sx[i] = *reinterpret_cast<const uint32_t *>(row_scales + i * 256 + lr * 4) & keep;
 #pragma unroll
     for (int b = 0; b < 2; ++b) sw[b] = nw[b] & keep;
     load_scales(t0 + R);
     auto step = [&](auto jc) {
       constexpr int J = decltype(jc)::value;
       const int t = t0 + J;
+      if constexpr (J == 1) {  // every wave has read the former ones
+        load_row_scales(t0 + R);
+        __builtin_amdgcn_sched_barrier(0);
+      }
       load_x(t + D, (J + D) % R);  // the stage read in step t - 1, which every wave has left
       __builtin_amdgcn_sched_barrier(0);
       const uint8_t *st = stage(J) + lane * 16;
@@ -212,8 +216,8 @@ __device__ __forceinline__ void medium_rows(const Fp8GemmArgs &a, const Fp8Tile 
       __builtin_amdgcn_sched_barrier(0);  // loads into registers still in use would get others, copied after a wait
       load_w(J, t + R);
       // step t + 1's rows, loaded in step t + 1 - D, are there when at most the loads behind them are in flight
-      // (weights of that step, rows and weights of the steps since; the scales may lie between as well)
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(4 + 6 * (D - 1)) : "memory");
+      // (weights of that step, rows and weights of the steps since, and the scales where those lie behind)
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(4 + 6 * (D - 1) + (J == 1 || J == 2)) : "memory");
       bar();
     };
     step(std::integral_constant<int, 0>{});
@@ -299,7 +303,7 @@ __global__ __launch_bounds__(512, 1) void fp8_rows_kernel(const Fp8GemmArgs a, i
       switch ((n + 15) / 16) {
 #define MOE_ROWS(MS)                                                                       \
   case MS:                                                                                 \
-    medium_rows<SWIGLU, MS>(a, tile, nb, n_tiles, m0, n, sA0, sA1, sA2, sA3, reinterpret_cast<float(*)[MD_ROWS]>(sB0)); \
+    medium_rows<SWIGLU, MS>(a, tile, nb, n_tiles, m0, n, sA0, sA1, sA2, sA3, sB1, reinterpret_cast<float(*)[MD_ROWS]>(sB0)); \
     break
         MOE_ROWS(1);
         MOE_ROWS(2);
