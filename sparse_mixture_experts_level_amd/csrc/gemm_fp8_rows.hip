@@ -289,6 +289,7 @@ __global__ __launch_bounds__(512, 1) void fp8_rows_kernel(const Fp8GemmArgs a, i
   constexpr int NBUF = 4;
   __shared__ __attribute__((aligned(1024))) uint8_t sA0[LG_TILE], sA1[LG_TILE], sA2[LG_TILE], sA3[LG_TILE];
   __shared__ __attribute__((aligned(1024))) uint8_t sB0[LG_TILE], sB1[LG_TILE], sB2[LG_TILE], sB3[LG_TILE];
+  __shared__ uint8_t row_scales[8 * 256];
   auto bufA = [&](int b) -> uint8_t * { return b == 0 ? sA0 : b == 1 ? sA1 : b == 2 ? sA2 : sA3; };
   auto bufB = [&](int b) -> uint8_t * { return b == 0 ? sB0 : b == 1 ? sB1 : b == 2 ? sB2 : sB3; };
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -303,7 +304,7 @@ __global__ __launch_bounds__(512, 1) void fp8_rows_kernel(const Fp8GemmArgs a, i
       switch ((n + 15) / 16) {
 #define MOE_ROWS(MS)                                                                       \
   case MS:                                                                                 \
-    medium_rows<SWIGLU, MS>(a, tile, nb, n_tiles, m0, n, sA0, sA1, sA2, sA3, sB1, reinterpret_cast<float(*)[MD_ROWS]>(sB0)); \
+    medium_rows<SWIGLU, MS>(a, tile, nb, n_tiles, m0, n, sA0, sA1, sA2, sA3, row_scales, reinterpret_cast<float(*)[MD_ROWS]>(sB0)); \
     break
         MOE_ROWS(1);
         MOE_ROWS(2);
@@ -365,21 +366,19 @@ __global__ __launch_bounds__(512, 1) void fp8_rows_kernel(const Fp8GemmArgs a, i
   const int sblocks = fp8_blocks(a.n_out);
   const uint8_t *wscale = a.w_scale + ((int64_t)g * sblocks + (SWIGLU ? nt : min(nt * 2 + wn / 2, sblocks - 1))) *
                                           (SWIGLU ? 2 : 1) * ks;
-  uint32_t sx[4], sw[2], soff[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = wm * 128 + i * 32 + lr;
-    soff[i] = (uint32_t)row * 4u;
-    if (!packed) {
-      const uint32_t src = from.row(a, m0, row, rows);
-      soff[i] = src != kOob ? src * (uint32_t)ks : kOob;
-    }
+  // four blocks of K, eight steps; past K zeros, or the last ones again.  The rows' go through LDS, one load a wave for 64
+  // rows (two waves write the same): each wave's own 128 were four loads, behind which the waits counted too few others.
+  uint32_t sw[2];
+  const int srow = (wave & 3) * 64 + lane;
+  uint32_t soff = (uint32_t)srow * 4u;
+  if (!packed) {
+    const uint32_t src = from.row(a, m0, srow, rows);
+    soff = src != kOob ? src * (uint32_t)ks : kOob;
   }
-  // four blocks of K, eight steps; past K zeros, or the last ones again
+  auto load_row_scales = [&](int q) {
+    buf_ld4_lds(sres, soff != kOob ? soff + (uint32_t)q * sstep : kOob, row_scales + (wave & 3) * 256);
+  };
   auto load_scales = [&](int q) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      sx[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(sres, soff[i] != kOob ? soff[i] + (uint32_t)q * sstep : kOob, 0, 0);
 #pragma unroll
     for (int j = 0; j < 2; ++j) sw[j] = scalar_load(wscale + (SWIGLU ? j * ks : 0) + min(4 * q, ks - 4));
   };
@@ -400,9 +399,15 @@ __global__ __launch_bounds__(512, 1) void fp8_rows_kernel(const Fp8GemmArgs a, i
     const bool second = wave >= 4;
     u32x4 af[4][2], bf[2][2];
     uint32_t cx[4], cw[2];
-    auto mem = [&](int s, int b) {
+    auto mem = [&](int q, int s, auto bc) {
+      constexpr int b = decltype(bc)::value;
+      if constexpr (b == 2) {  // both groups have read the former ones
+        load_row_scales(q + 1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
       issue(s + 3, (b + 3) % NBUF);
-      asm volatile("s_waitcnt vmcnt(8)" ::: "memory");  // the two younger steps' may stay in flight
+      // the two younger steps' may stay in flight, and the scales where they lie between
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(8 + (b == 2 || b == 3)) : "memory");
       const uint8_t *la = bufA(b % NBUF), *lb = bufB(b % NBUF);
       const uint8_t *pa = la + a_at, *pb = lb + b_at;
 #pragma unroll
@@ -437,39 +442,52 @@ __global__ __launch_bounds__(512, 1) void fp8_rows_kernel(const Fp8GemmArgs a, i
     };
     auto next_scales = [&](int q) {  // those of the eight steps that begin; the following ones are loaded
 #pragma unroll
-      for (int i = 0; i < 4; ++i) cx[i] = sx[i];
+      for (int i = 0; i < 4; ++i) cx[i] = *reinterpret_cast<const uint32_t *>(row_scales + (wm * 128 + i * 32 + lr) * 4);
 #pragma unroll
       for (int j = 0; j < 2; ++j) cw[j] = sw[j];
       load_scales(q + 1);
     };
     load_scales(q0);
+    load_row_scales(q0);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int b = 0; b < 3; ++b) issue(b, b);
     asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
     bar();
     if (second) bar();
-    int s0 = 0;
-    for (; s0 + 8 <= nk; s0 += 8) {
-      next_scales(q0 + s0 / 8);
-#pragma unroll
-      for (int b = 0; b < 8; ++b) {
-        mem(s0 + b, b);
-        bar();
-        comp(b);
-        bar();
+    int s0 = 0, q = q0;
+    auto step = [&](auto bc) {
+      mem(q, s0 + decltype(bc)::value, bc);
+      bar();
+      comp(decltype(bc)::value);
+      bar();
+    };
+#define MOE_STEP(B) step(std::integral_constant<int, B>{})
+    for (; s0 + 8 <= nk; s0 += 8, ++q) {
+      next_scales(q);
+      MOE_STEP(0);
+      MOE_STEP(1);
+      MOE_STEP(2);
+      MOE_STEP(3);
+      MOE_STEP(4);
+      MOE_STEP(5);
+      MOE_STEP(6);
+      MOE_STEP(7);
+    }
+    if (s0 < nk) {  // two, four or six: K is whole blocks of 128
+      next_scales(q);
+      MOE_STEP(0);
+      MOE_STEP(1);
+      if (s0 + 2 < nk) {
+        MOE_STEP(2);
+        MOE_STEP(3);
+        if (s0 + 4 < nk) {
+          MOE_STEP(4);
+          MOE_STEP(5);
+        }
       }
     }
-    if (s0 < nk) {
-      next_scales(q0 + s0 / 8);
-#pragma unroll
-      for (int b = 0; b < 7; ++b) {
-        if (s0 + b >= nk) break;
-        mem(s0 + b, b);
-        bar();
-        comp(b);
-        bar();
-      }
-    }
+#undef MOE_STEP
     if (!second) bar();
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no LDS write may outlive the block
