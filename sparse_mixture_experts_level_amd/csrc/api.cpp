@@ -744,7 +744,7 @@ Fp8Layout fp8_layout(int32_t G, int64_t rows_max, int32_t group_rows_max, int32_
     return at;
   };
   const bool large = fp8_large(rows_max, group_rows_max);
-  const bool packs = large && moe::fp8_packs(f ? f : n_out, f);
+  const bool packs = large && moe::fp8_packs(rows_max, G, f ? f : n_out, f);
   L.xp = take(packs ? moe::fp8_packed_bytes(rows_max, G, k) : 0);
   L.xp_scale = take(packs ? moe::fp8_packed_scale_bytes(rows_max, G, k) : 0);
   L.h8 = take(f ? rows_max * moe::fp8_row_bytes(f) : 0);
@@ -791,7 +791,7 @@ void parts_fp8(moe::Fp8GemmArgs &a, void *ws, const Fp8Layout &L, bool swiglu) {
 
 // The packed tiles of a product's rows, where there are to be any.
 moe_status pack_fp8(moe::Fp8GemmArgs &a, void *ws, const Fp8Layout &L, bool swiglu, hipStream_t stream) {
-  if (!a.large || !moe::fp8_packs(a.n_out, swiglu)) return MOE_OK;
+  if (!a.large || !moe::fp8_packs(a.rows_max, a.num_groups, a.n_out, swiglu)) return MOE_OK;
   MOE_TRY_HIP(moe::launch_fp8_pack_rows(a, at<uint8_t>(ws, L.xp), at<uint8_t>(ws, L.xp_scale), stream), "rows to tiles");
   a.xp = at<uint8_t>(ws, L.xp);
   a.xp_scale = at<uint8_t>(ws, L.xp_scale);

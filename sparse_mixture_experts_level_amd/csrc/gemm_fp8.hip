@@ -19,15 +19,15 @@ namespace moe {
 
 namespace {
 
-// Few rows: 16 of them at a time, one block after the other.  A workgroup has 16 U output columns; each wave 16
-// of them (for gate_up the 16 gate and the 16 up rows) and one of KS parts of K, whose sums the first
-// part's waves add in order.  Rows are read from the caches in the operand layout, two steps ahead, with the weights,
+// Few rows: 16 of them at a time, one block after the other.  A workgroup has 16 U columns of H (each wave 16, NB = 2
+// blocks of weights: gate and up) or 16 U NB of y; each wave one of KS parts of K, whose sums the first part's waves add
+// in order.  Rows are read from the caches in the operand layout, two steps ahead, with the weights,
 // R steps of 128 ahead, all in registers: no LDS, no barrier.  The weights are the
 // matrix instruction's first operand, so that a lane holds four consecutive columns of one row.
-template <bool SWIGLU, int U, int KS>
+template <bool SWIGLU, int U, int KS, int NB>
 __global__ __launch_bounds__(64 * U * KS, 4) void fp8_small_kernel(const Fp8GemmArgs a) {
-  constexpr int NB = SWIGLU ? 2 : 1, R = SWIGLU ? 4 : 8, XR = 2;
-  static_assert(!SWIGLU || U == 8, "a block of H's columns a workgroup");
+  constexpr int R = 8 / NB, XR = 2, NS = SWIGLU ? 2 : 1;  // NS: scales a wave
+  static_assert(!SWIGLU || (U == 8 && NB == 2), "a block of H's columns a workgroup");
   __shared__ float tops[SWIGLU ? 8 : 1][16];
   __shared__ f32x4 parts[KS > 1 ? (KS - 1) * U * NB * 64 : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lr = lane & 15,
@@ -39,19 +39,21 @@ __global__ __launch_bounds__(64 * U * KS, 4) void fp8_small_kernel(const Fp8Gemm
   const int kt = fp8_blocks(a.K), kp = fp8_row_bytes(a.K), ks = fp8_scale_bytes(a.K);
   // parts of K are whole words of scales: four steps
   const int quads = ks / 4, tb = 4 * (quads * part / KS), te = min(kt, 4 * (quads * (part + 1) / KS));
-  const int unit = nb * U + u, units = (a.n_out + 15) / 16;
+  const int unit = nb * U + u, blocks = (a.n_out + 15) / 16 * NS;  // of 16 weight rows
   const int64_t wbytes = fp8_group_bytes(a.n_out, a.K, SWIGLU);
   const rsrc_t wres = make_rsrc(a.w8 + g * wbytes, (uint32_t)wbytes);
   uint32_t half;  // (gate and up blocks are neighbours)
-  const uint32_t wbase = fp8_block_offset(unit * NB, units * NB, kt, half) + (uint32_t)lane * 16u;
-  const int tw = unit < units ? te : 0;  // no weights past the last block
-  const uint8_t *wscale = a.w_scale + ((int64_t)g * fp8_blocks(a.n_out) + min(unit, units - 1) / 8) * NB * ks;
+  const uint32_t wbase = fp8_block_offset(unit * NB, blocks, kt, half) + (uint32_t)lane * 16u;
+  const int tw0 = unit * NB < blocks ? te : 0, tw1 = unit * NB + 1 < blocks ? te : 0;  // no weights past the last block
+  const int sblocks = fp8_blocks(a.n_out);
+  const uint8_t *wscale = a.w_scale + ((int64_t)g * sblocks + min(unit * NB / NS / 8, sblocks - 1)) * NS * ks;
   for (int m0 = begin; m0 < end; m0 += 16) {
     u32x4 w[R][NB][2], x[XR][2];
-    uint32_t sx, nx, sw[NB], nw[NB];
+    uint32_t sx, nx, sw[NS], nw[NS];
     auto load_w = [&](int j, int t) {  // steps past the part's end read zeros
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
+        const int tw = SWIGLU || b == 0 ? tw0 : tw1;
         const uint32_t o = t < tw ? wbase + (uint32_t)(2 * t) * half + (uint32_t)b * 1024u : kOob;
         w[j][b][0] = buf_ld16_nt(wres, o);
         w[j][b][1] = buf_ld16_nt(wres, t < tw ? o + half : kOob);
@@ -72,7 +74,7 @@ __global__ __launch_bounds__(64 * U * KS, 4) void fp8_small_kernel(const Fp8Gemm
       const int at = min(t, ks - 4);
       nx = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rows.sres, soff == kOob ? kOob : soff + (uint32_t)at, 0, 0);
 #pragma unroll
-      for (int b = 0; b < NB; ++b) nw[b] = scalar_load(wscale + b * ks + at);
+      for (int b = 0; b < NS; ++b) nw[b] = scalar_load(wscale + b * ks + at);
     };
     load_scales(tb);
 #pragma unroll
@@ -92,7 +94,7 @@ __global__ __launch_bounds__(64 * U * KS, 4) void fp8_small_kernel(const Fp8Gemm
           const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
           sx = nx & keep;
 #pragma unroll
-          for (int b = 0; b < NB; ++b) sw[b] = nw[b] & keep;
+          for (int b = 0; b < NS; ++b) sw[b] = nw[b] & keep;
           load_scales(t + 4);
         }
 #pragma unroll
@@ -100,7 +102,7 @@ __global__ __launch_bounds__(64 * U * KS, 4) void fp8_small_kernel(const Fp8Gemm
           const u32x4 xb = fp8_to_bf16(x[J % XR][m / 2][2 * (m % 2)], x[J % XR][m / 2][2 * (m % 2) + 1], fp8_scale<S>(sx));
 #pragma unroll
           for (int b = 0; b < NB; ++b)
-            acc[b] = mfma16(fp8_to_bf16(w[J][b][m / 2][2 * (m % 2)], w[J][b][m / 2][2 * (m % 2) + 1], fp8_scale<S>(sw[b])), xb,
+            acc[b] = mfma16(fp8_to_bf16(w[J][b][m / 2][2 * (m % 2)], w[J][b][m / 2][2 * (m % 2) + 1], fp8_scale<S>(sw[b % NS])), xb,
                             acc[b]);
         }
         __builtin_amdgcn_sched_barrier(0);  // loads into registers still in use would get others, copied after a wait
@@ -129,7 +131,7 @@ __global__ __launch_bounds__(64 * U * KS, 4) void fp8_small_kernel(const Fp8Gemm
 #pragma unroll
           for (int b = 0; b < NB; ++b) acc[b] += parts[(((p - 1) * U + u) * NB + b) * 64 + lane];
     }
-    const int col = unit * 16 + lg * 4;
+    const int col = unit * 16 * NB / NS + lg * 4;
     const int64_t row = m0 + lr;
     if constexpr (SWIGLU) {
       float h[4], top = 0.0f;
@@ -150,7 +152,8 @@ __global__ __launch_bounds__(64 * U * KS, 4) void fp8_small_kernel(const Fp8Gemm
         store_h(a, h, top, row, nb, col, u == 0 && lg == 0);
       }
     } else if (part == 0 && row < end) {
-      store_y(a, acc[0], row, col);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) store_y(a, acc[b], row, col + b * 16);
     }
     if (SWIGLU || KS > 1) __syncthreads();  // the next rows use the same LDS
   }
@@ -162,12 +165,17 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs &a, hipStream_t s) {
   if (std::min(a.group_rows_max, a.rows_max) > kFp8SmallRows) return launch_fp8_gemm_rows(a, s);
   const int groups = std::min(a.num_groups, a.rows_max);
   auto grid = [&](int cols) { return dim3((unsigned)((a.n_out + cols - 1) / cols), (unsigned)groups); };
+  // Linear: a wave takes two blocks of 16 columns, so that the rows are read half as often, where that leaves a workgroup a
+  // CU (32 groups of 16 rows, 2048 x 7168: 114 -> 101 us; of one row: 83 -> 79; but 4 groups, 2880 x 2880, 92 workgroups:
+  // 11.0 -> 12.2), and a part of K where even one block leaves half of them idle (1 x 2048 x 7168: 8.6 -> 7.9).
   if (a.h8)
-    hipLaunchKernelGGL((fp8_small_kernel<true, 8, 1>), grid(128), dim3(512), 0, s, a);
+    hipLaunchKernelGGL((fp8_small_kernel<true, 8, 1, 2>), grid(128), dim3(512), 0, s, a);
   else if ((int64_t)groups * ((a.n_out + 63) / 64) < 128)
-    hipLaunchKernelGGL((fp8_small_kernel<false, 2, 2>), grid(32), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((fp8_small_kernel<false, 2, 2, 1>), grid(32), dim3(256), 0, s, a);
+  else if ((int64_t)groups * ((a.n_out + 127) / 128) < 256)
+    hipLaunchKernelGGL((fp8_small_kernel<false, 4, 1, 1>), grid(64), dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((fp8_small_kernel<false, 4, 1>), grid(64), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((fp8_small_kernel<false, 4, 1, 2>), grid(128), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

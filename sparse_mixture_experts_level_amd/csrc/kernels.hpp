@@ -310,9 +310,12 @@ inline int64_t fp8_parts_bytes(int64_t rows, int64_t group_rows, int n_out, int 
 // Whether the rows of large tiles are packed first: a stage of 64 of K is half of each row's line, which every column tile
 // then reads twice, but packing is a launch and a copy.  us as they are and packed: 4096 x 1024 x 14336 (4
 // column tiles) 83 and 99, 8 x 300 x 2048 x 2048 (8) 30 and 36, 1024 x 4096 x 4096 (16) 57 and 52, 4096 x 8192 x 14336 (32)
-// 384 and 375, (56) 789 and 682.
+// 384 and 375, (56) 789 and 682.  And where groups are of few rows on average, most have no such tiles: 32 x 80 rows,
+// announced as up to 320 a group, spent 4.6 us on a launch that packed nothing.
 constexpr int kFp8PackTiles = 8;
-inline bool fp8_packs(int n_out, bool swiglu) { return fp8_part_columns(n_out, swiglu) / 256 > kFp8PackTiles; }
+inline bool fp8_packs(int64_t rows, int G, int n_out, bool swiglu) {
+  return rows > (int64_t)kFp8FewRows * G && fp8_part_columns(n_out, swiglu) / 256 > kFp8PackTiles;
+}
 // x8 (through row_index) and its scales to packed tiles.
 hipError_t launch_fp8_pack_rows(const Fp8GemmArgs &a, uint8_t *xp, uint8_t *xp_scale, hipStream_t s);
 hipError_t launch_fp8_gemm(const Fp8GemmArgs &a, hipStream_t s);
