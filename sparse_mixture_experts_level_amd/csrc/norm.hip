@@ -219,12 +219,13 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rms_norm_backward_kerne
   }
 }
 
-// 16 columns a workgroup, sixteen rows of parts at a time, eight loads of each thread in flight.
+// 16 columns a workgroup, sixteen rows of parts at a time, eight loads of each thread in flight; sums in 64 bits, as the
+// parts' float sums lose a third as much as adding them in floats does (5003 rows: 1.5e-7 of dweight's norm).
 __global__ __launch_bounds__(256) void rms_norm_dweight_kernel(const float *__restrict__ parts, int n, int d,
                                                                float *__restrict__ dweight) {
-  __shared__ float s[16][17];
+  __shared__ double s[16][17];
   const int q = threadIdx.x >> 4, l = threadIdx.x & 15, col = blockIdx.x * 16 + l;
-  float sum = 0.0f;
+  double sum = 0.0;
   for (int r0 = q; r0 < n; r0 += 16 * 8) {
     float v[8];
 #pragma unroll
@@ -236,7 +237,7 @@ __global__ __launch_bounds__(256) void rms_norm_dweight_kernel(const float *__re
   __syncthreads();
   if (q == 0 && col < d) {
     for (int r = 1; r < 16; ++r) sum += s[r][l];
-    dweight[col] = sum;
+    dweight[col] = (float)sum;
   }
 }
 
