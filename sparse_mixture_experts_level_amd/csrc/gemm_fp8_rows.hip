@@ -19,20 +19,21 @@ namespace {
 
 constexpr int LG_TILE = kFp8LargeRows * 64;  // bytes of an operand's stage: 256 rows, 64 of K
 
-// Block `block` of a launch of per_tile blocks a tile and parts of K: the tiles of the groups of many rows, group after
-// group, then one for each group of few (any number of rows where there are no packed copies), all of them
-// again for each further part.  One pass over the offsets, two for more than 64 groups; all results in scalar registers.
+// Block `block` of a launch of per_tile column tiles: the tiles of the groups of many rows, group after group, a block for
+// each column tile; then the groups of few (any number of rows where none is announced to have many), a block for each of
+// `chunks` ranges of column tiles; all of them again for each further part of K.  One pass over the offsets, two for more than 64 groups; all results in scalar registers.
 struct Fp8Tile {
   int g, begin, end;  // -1: there is no such tile
   int first, count;   // the group's tiles, numbered over all groups (count 0: few rows)
   int lin;            // the block's number among the tiles' (many rows: after the spreading)
   int tiles;          // of many rows, in all
   int part, parts;
+  int col0, col1;     // few rows: the column tiles
 };
 __device__ __forceinline__ Fp8Tile find_tile(const Fp8GemmArgs &a, int tiles_max, int block, int per_tile, bool spread) {
   const int lane = threadIdx.x & 63, G = a.num_groups;
   const int few = a.large ? kFp8FewRows : INT_MAX;
-  Fp8Tile t{-1, 0, 0, 0, 0, 0, 0, 0, 1};
+  Fp8Tile t{-1, 0, 0, 0, 0, 0, 0, 0, 1, 0, 0};
   int b = 0, e = 0, all = 0;
 #pragma unroll 1
   for (int g0 = 0; g0 < G; g0 += 64) {
@@ -43,7 +44,14 @@ __device__ __forceinline__ Fp8Tile find_tile(const Fp8GemmArgs &a, int tiles_max
   }
   // (offsets that decrease could count rows twice: no tile past those that the packed copies have room for)
   t.tiles = min(__builtin_amdgcn_readfirstlane(t.tiles), tiles_max);
-  all = __builtin_amdgcn_readfirstlane(all + t.tiles) * per_tile;
+  all = __builtin_amdgcn_readfirstlane(all);
+  int chunks = per_tile, columns = 1;
+  if (spread && a.few_blocks && all > 0) {
+    columns = (per_tile + max(1, a.few_blocks / all) - 1) / max(1, a.few_blocks / all);
+    chunks = (per_tile + columns - 1) / columns;
+  }
+  const int large = t.tiles * per_tile;
+  all = large + all * chunks;
   if (all == 0) return t;
   if (spread && a.parts_cap > 1) {
     t.parts = fp8_parts(all, a.rows_max, per_tile, a.K, a.parts_cap);
@@ -52,10 +60,12 @@ __device__ __forceinline__ Fp8Tile find_tile(const Fp8GemmArgs &a, int tiles_max
   }
   if (t.part >= t.parts) return t;
   // the first tiles' blocks in one contiguous range an XCD, as neighbours share operands
-  const int large = t.tiles * per_tile, lin = spread && block < large ? xcd_remap(block, large) : block;
-  const int v = lin / per_tile;
+  const bool many = block < large;
+  const int lin = spread && many ? xcd_remap(block, large) : block;
+  const int v = many ? lin / per_tile : t.tiles + (lin - large) / chunks;
   t.lin = lin;
-  const bool many = v < t.tiles;
+  t.col0 = __builtin_amdgcn_readfirstlane((lin - large) % chunks * columns);
+  t.col1 = min(per_tile, t.col0 + __builtin_amdgcn_readfirstlane(columns));
   int seen = 0;
 #pragma unroll 1
   for (int g0 = 0; g0 < G; g0 += 64) {
@@ -117,17 +127,19 @@ __device__ __forceinline__ void part_of_k(const Fp8GemmArgs &a, const Fp8Tile &t
 // instruction: converted to bf16 by each wave, 128 rows took 1.7 us a step of the 1.2 that its weights take.
 constexpr int MD_R = 4, MD_D = 3, MD_ROWS = 128;
 
-// One block of n <= 16 MS rows from m0 on; MS is exact, so that no branch is in the loop.
+// One block of n <= 16 MS rows from m0 on, column tiles nb0 .. nb1 - 1 one after the other without a pause of the loads: in a
+// tile's last four steps those of the next one's first are loaded.  MS is exact, so that no branch is in the loop.
 template <bool SWIGLU, int MS>
-__device__ __forceinline__ void medium_rows(const Fp8GemmArgs &a, const Fp8Tile &tile, int nb, int n_tiles, int m0, int n,
+__device__ __forceinline__ void medium_rows(const Fp8GemmArgs &a, const Fp8Tile &tile, int n_tiles, int m0, int n,
                                             uint8_t *s0, uint8_t *s1, uint8_t *s2, uint8_t *s3, uint8_t *row_scales,
                                             float (*tops)[MD_ROWS]) {
   constexpr int R = MD_R, D = MD_D;
+  static_assert(R == 4 && D == 3, "a word of scales and the stages");
   auto stage = [&](int b) -> uint8_t * { return b == 0 ? s0 : b == 1 ? s1 : b == 2 ? s2 : s3; };
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lr = lane & 15,
             lg = lane >> 4;
   const int kt = fp8_blocks(a.K), kp = fp8_row_bytes(a.K), ks = fp8_scale_bytes(a.K);
-  const int units = (a.n_out + 15) / 16 * (SWIGLU ? 2 : 1), unit = nb * 16 + wave * 2;  // blocks of 16 weight rows
+  const int units = (a.n_out + 15) / 16 * (SWIGLU ? 2 : 1);  // blocks of 16 weight rows
   int tb, te;  // this part's steps
   part_of_k(a, tile, tb, te);
   tb *= 4;
@@ -135,16 +147,23 @@ __device__ __forceinline__ void medium_rows(const Fp8GemmArgs &a, const Fp8Tile 
   const int g = tile.g;
   const int64_t wbytes = fp8_group_bytes(a.n_out, a.K, SWIGLU);
   const rsrc_t wres = make_rsrc(a.w8 + g * wbytes, (uint32_t)wbytes);
-  uint32_t half;
-  const uint32_t wbase = fp8_block_offset(unit, units, kt, half) + (uint32_t)lane * 16u;
   const int sblocks = fp8_blocks(a.n_out);
-  const uint8_t *wscale =
-      a.w_scale + ((int64_t)g * sblocks + (SWIGLU ? nb : min(nb * 2 + wave / 4, sblocks - 1))) * (SWIGLU ? 2 : 1) * ks;
+  // the column tile that is loaded
+  uint32_t half, wbase;
+  int end0, end1;  // its steps, of this wave's two blocks
+  const uint8_t *wscale;
+  auto columns = [&](int nb) {
+    const int unit = nb * 16 + wave * 2;
+    wbase = fp8_block_offset(unit, units, kt, half) + (uint32_t)lane * 16u;
+    end0 = nb < tile.col1 && unit < units ? te : 0;
+    end1 = nb < tile.col1 && unit + 1 < units ? te : 0;
+    wscale = a.w_scale + ((int64_t)g * sblocks + min(SWIGLU ? nb : nb * 2 + wave / 4, sblocks - 1)) * (SWIGLU ? 2 : 1) * ks;
+  };
   i32x8 w[R][2];
   auto load_w = [&](int j, int t) {
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      const bool in = t < te && unit + b < units;
+      const bool in = t < (b ? end1 : end0);
       const uint32_t o = wbase + (uint32_t)(2 * t) * half + (uint32_t)b * 1024u;
       w[j][b] = fp8_operand(buf_ld16_nt(wres, in ? o : kOob), buf_ld16_nt(wres, in ? o + half : kOob));
     }
@@ -153,8 +172,8 @@ __device__ __forceinline__ void medium_rows(const Fp8GemmArgs &a, const Fp8Tile 
   // this wave's pieces of a stage, one for each half of K's 128: subtile `wave`, row lr, codes 64 p + 16 lg ..
   const uint32_t src = rows.row(a, m0, wave * 16 + lr, n);
   const uint32_t xoff = src != kOob ? src * (uint32_t)kp + (uint32_t)lg * 16u : kOob;
-  auto load_x = [&](int t, int b) {
-    const uint32_t o = t < te && xoff != kOob ? xoff + (uint32_t)t * 128u : kOob;
+  auto load_x = [&](int t, int end, int b) {
+    const uint32_t o = t < end && xoff != kOob ? xoff + (uint32_t)t * 128u : kOob;
     buf_ld16_lds(rows.xres, o, stage(b) + wave * 2048);
     buf_ld16_lds(rows.xres, o == kOob ? kOob : o + 64u, stage(b) + wave * 2048 + 1024);
   };
@@ -171,39 +190,103 @@ __device__ __forceinline__ void medium_rows(const Fp8GemmArgs &a, const Fp8Tile 
     for (int b = 0; b < 2; ++b) nw[b] = scalar_load(wscale + (SWIGLU ? b * ks : 0) + min(t, ks - 4));
   };
   f32x4 acc[MS][2];
+  auto clear = [&]() {
 #pragma unroll
-  for (int i = 0; i < MS; ++i)
+    for (int i = 0; i < MS; ++i)
 #pragma unroll
-    for (int b = 0; b < 2; ++b) acc[i][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  load_scales(tb);
-  load_row_scales(tb);
-#pragma unroll
-  for (int b = 0; b < D; ++b) load_x(tb + b, b);
-  __builtin_amdgcn_sched_barrier(0);  // the waits count on rows before weights
-#pragma unroll
-  for (int j = 0; j < R; ++j) load_w(j, tb + j);
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(4 * R) : "memory");  // the first stages are there
+      for (int b = 0; b < 2; ++b) acc[i][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  };
+  clear();
   auto bar = [&]() {
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
   };
+  auto lds_bar = [&]() {  // and LDS written before it can be read after it; loads stay in flight
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    bar();
+    asm volatile("" ::: "memory");
+  };
+  auto finish = [&](int nb) {
+    int first = m0;
+    asm volatile("" : "+s"(first));  // no rows' addresses kept in registers over the loop
+    if (tile.parts > 1) {
+#pragma unroll
+      for (int i = 0; i < MS; ++i) {
+        const int64_t row = first + i * 16 + lr;
+        if (row < first + n)
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+            *reinterpret_cast<f32x4 *>(a.parts + (tile.part * (int64_t)a.rows_max + row) * n_tiles * 256 + nb * 256 +
+                                       (SWIGLU ? b * 128 + wave * 16 : wave * 32 + b * 16) + lg * 4) = acc[i][b];
+      }
+    } else if constexpr (SWIGLU) {
+      const int col = nb * 128 + wave * 16 + lg * 4;
+#pragma unroll
+      for (int i = 0; i < MS; ++i) {
+        float top = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          acc[i][0][j] = silu_f32(acc[i][0][j]) * acc[i][1][j];
+          top = fmaxf(top, fp8_magnitude(acc[i][0][j]));
+        }
+        top = fmaxf(top, __shfl_xor(top, 16, 64));
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        if (lg == 0) tops[wave][i * 16 + lr] = top;
+      }
+      lds_bar();
+#pragma unroll
+      for (int i = 0; i < MS; ++i) {
+        float top = 0.0f;
+#pragma unroll
+        for (int v = 0; v < 8; ++v) top = fmaxf(top, tops[v][i * 16 + lr]);
+        const int64_t row = first + i * 16 + lr;
+        const float h[4] = {acc[i][0][0], acc[i][0][1], acc[i][0][2], acc[i][0][3]};
+        if (row < first + n) store_h(a, h, top, row, nb, col, wave == 0 && lg == 0);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < MS; ++i) {
+        const int64_t row = first + i * 16 + lr;
+        if (row < first + n)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) store_y(a, acc[i][b], row, (nb * 16 + wave * 2 + b) * 16 + lg * 4);
+      }
+    }
+  };
+  int nb = tile.col0, t0 = tb;
+  columns(nb);
+  load_scales(tb);
+  load_row_scales(tb);
+#pragma unroll
+  for (int b = 0; b < D; ++b) load_x(tb + b, te, b);
+  __builtin_amdgcn_sched_barrier(0);  // the waits count on rows before weights
+#pragma unroll
+  for (int j = 0; j < R; ++j) load_w(j, tb + j);
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(4 * R) : "memory");  // the first stages are there
   bar();
-  for (int t0 = tb; t0 < te; t0 += R) {
+  for (;;) {
     const uint32_t keep = kt - t0 >= 4 ? ~0u : (1u << (8 * (kt - t0))) - 1u;  // the padding's scales are not looked at
 #pragma unroll
     for (int i = 0; i < MS; ++i) sx[i] = *reinterpret_cast<const uint32_t *>(row_scales + i * 256 + lr * 4) & keep;
 #pragma unroll
     for (int b = 0; b < 2; ++b) sw[b] = nw[b] & keep;
-    load_scales(t0 + R);
+    // the four steps that are loaded meanwhile
+    const bool last = t0 + R >= te;
+    const int next = nb + (last ? 1 : 0), n0 = last ? tb : t0 + R, nend = next < tile.col1 ? te : 0;
+    if (last) columns(next);
+    load_scales(n0);
     auto step = [&](auto jc) {
       constexpr int J = decltype(jc)::value;
-      const int t = t0 + J;
       if constexpr (J == 1) {  // every wave has read the former ones
-        load_row_scales(t0 + R);
+        load_row_scales(n0);
         __builtin_amdgcn_sched_barrier(0);
       }
-      load_x(t + D, (J + D) % R);  // the stage read in step t - 1, which every wave has left
+      // the stage read in the step before, which every wave has left
+      if constexpr (J == 0)
+        load_x(t0 + D, te, D);
+      else
+        load_x(n0 + J - 1, nend, J - 1);
       __builtin_amdgcn_sched_barrier(0);
       const uint8_t *st = stage(J) + lane * 16;
 #pragma unroll
@@ -214,9 +297,10 @@ __device__ __forceinline__ void medium_rows(const Fp8GemmArgs &a, const Fp8Tile 
         for (int b = 0; b < 2; ++b) acc[i][b] = mfma_fp8_16<J>(w[J][b], x, acc[i][b], sw[b], sx[i]);
       }
       __builtin_amdgcn_sched_barrier(0);  // loads into registers still in use would get others, copied after a wait
-      load_w(J, t + R);
+      load_w(J, n0 + J);
       // step t + 1's rows, loaded in step t + 1 - D, are there when at most the loads behind them are in flight
-      // (weights of that step, rows and weights of the steps since, and the scales where those lie behind)
+      // (weights of that step, rows and weights of the steps since, and the scales where those lie behind; stores of a tile
+      // that ended among them only make it wait for more)
       asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(4 + 6 * (D - 1) + (J == 1 || J == 2)) : "memory");
       bar();
     };
@@ -224,55 +308,16 @@ __device__ __forceinline__ void medium_rows(const Fp8GemmArgs &a, const Fp8Tile 
     step(std::integral_constant<int, 1>{});
     step(std::integral_constant<int, 2>{});
     step(std::integral_constant<int, 3>{});
+    t0 = n0;
+    if (last) {
+      finish(nb);
+      if (next == tile.col1) break;
+      nb = next;
+      clear();
+    }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no write to LDS may outlive its rows
   __syncthreads();
-  if (tile.parts > 1) {
-#pragma unroll
-    for (int i = 0; i < MS; ++i) {
-      const int64_t row = m0 + i * 16 + lr;
-      if (row < m0 + n)
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-          *reinterpret_cast<f32x4 *>(a.parts + (tile.part * (int64_t)a.rows_max + row) * n_tiles * 256 + nb * 256 +
-                                     (SWIGLU ? b * 128 + wave * 16 : wave * 32 + b * 16) + lg * 4) = acc[i][b];
-    }
-    return;
-  }
-  if constexpr (SWIGLU) {
-    const int col = nb * 128 + wave * 16 + lg * 4;
-#pragma unroll
-    for (int i = 0; i < MS; ++i) {
-      float top = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        acc[i][0][j] = silu_f32(acc[i][0][j]) * acc[i][1][j];
-        top = fmaxf(top, fp8_magnitude(acc[i][0][j]));
-      }
-      top = fmaxf(top, __shfl_xor(top, 16, 64));
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
-      if (lg == 0) tops[wave][i * 16 + lr] = top;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < MS; ++i) {
-      float top = 0.0f;
-#pragma unroll
-      for (int v = 0; v < 8; ++v) top = fmaxf(top, tops[v][i * 16 + lr]);
-      const int64_t row = m0 + i * 16 + lr;
-      const float h[4] = {acc[i][0][0], acc[i][0][1], acc[i][0][2], acc[i][0][3]};
-      if (row < m0 + n) store_h(a, h, top, row, nb, col, wave == 0 && lg == 0);
-    }
-    __syncthreads();
-  } else {
-#pragma unroll
-    for (int i = 0; i < MS; ++i) {
-      const int64_t row = m0 + i * 16 + lr;
-      if (row < m0 + n)
-#pragma unroll
-        for (int b = 0; b < 2; ++b) store_y(a, acc[i][b], row, (unit + b) * 16 + lg * 4);
-    }
-  }
 }
 
 __device__ __forceinline__ f32x16 mfma_fp8_32(i32x8 a, i32x8 b, f32x16 c, uint32_t sa, uint32_t sb, int byte) {
@@ -298,13 +343,13 @@ __global__ __launch_bounds__(512, 1) void fp8_rows_kernel(const Fp8GemmArgs a, i
   if (tile.g < 0) return;
   const int g = tile.g, begin = tile.begin, end = tile.end, mt_first = tile.first, mt_count = tile.count;
   if (mt_count == 0) {
-    const int nb = (tile.lin - tile.tiles * n_tiles) % n_tiles;
     for (int m0 = begin; m0 < end; m0 += MD_ROWS) {
       const int n = min(MD_ROWS, end - m0);
       switch ((n + 15) / 16) {
 #define MOE_ROWS(MS)                                                                       \
   case MS:                                                                                 \
-    medium_rows<SWIGLU, MS>(a, tile, nb, n_tiles, m0, n, sA0, sA1, sA2, sA3, row_scales, reinterpret_cast<float(*)[MD_ROWS]>(sB0)); \
+    medium_rows<SWIGLU, MS>(a, tile, n_tiles, m0, n, sA0, sA1, sA2, sA3, row_scales,       \
+                            reinterpret_cast<float(*)[MD_ROWS]>(sB0));                     \
     break
         MOE_ROWS(1);
         MOE_ROWS(2);
@@ -598,7 +643,7 @@ __global__ __launch_bounds__(256) void fp8_add_parts_kernel(const Fp8GemmArgs a,
     n = min(per, tile.end - m0);
     last = (n + 31) / 32 * 32;  // packed tiles are read by whole 32s
   } else {
-    nt = (tile.lin - tile.tiles * n_tiles) % n_tiles;
+    nt = tile.col0;
   }
   const int m_tile = tile.first + mt;
   if (tile.count && m_tile >= tiles_max) return;
@@ -691,11 +736,35 @@ hipError_t launch_fp8_pack_rows(const Fp8GemmArgs &a, uint8_t *xp, uint8_t *xp_s
   return hipGetLastError();
 }
 
-hipError_t launch_fp8_gemm_rows(const Fp8GemmArgs &a, hipStream_t s) {
+// Blocks for the groups of few rows, each a range of a group's column tiles: as many whole rounds of 256 as cost least,
+// counted for as many groups as there can be, in steps of 128 of K, of which a block's begin and end take eight (10 us); a
+// tenth has to be won.  32 x 80 rows, 7168 x 2048, 28 tiles of 16 steps: 896 blocks 115 us, 224 of four tiles 104; 4096 x
+// 7168, 16 tiles of 56 steps: 512 and 256 blocks 162.5 us, 4096 x 14336: 355 and 376.  0: a block for each tile.
+static int few_blocks(int groups, int n_tiles, int k) {
+  const int64_t steps = fp8_scale_bytes(k), all = (int64_t)groups * n_tiles;
+  int64_t least = (all + 255) / 256 * (steps + 8) * 9 / 10;
+  int best = 0;
+  for (int target = 256; target <= 2048 && target < all; target += 256) {
+    if (groups > target) continue;
+    const int columns = (n_tiles + target / groups - 1) / (target / groups);
+    const int64_t blocks = (int64_t)groups * ((n_tiles + columns - 1) / columns);
+    const int64_t cost = (blocks + 255) / 256 * (columns * steps + 8);
+    if (cost < least) {
+      best = target;
+      least = cost;
+    }
+  }
+  return best;
+}
+
+hipError_t launch_fp8_gemm_rows(const Fp8GemmArgs &call, hipStream_t s) {
+  Fp8GemmArgs a = call;
   const bool swiglu = a.h8 != nullptr;
   const int n_tiles = (a.n_out + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256);
   const int64_t tiles = a.large ? fp8_large_tiles_max(a.rows_max, a.num_groups) : 0;
-  const int64_t blocks = (tiles + std::min(a.num_groups, a.rows_max)) * n_tiles;
+  const int groups = std::min(a.num_groups, a.rows_max);
+  a.few_blocks = a.parts_cap > 1 ? 0 : few_blocks(groups, n_tiles, a.K);
+  const int64_t blocks = tiles * n_tiles + (a.few_blocks ? std::max(a.few_blocks, groups) : (int64_t)groups * n_tiles);
   const int64_t grid = a.parts_cap > 1 ? std::max<int64_t>(blocks, 256) : blocks;  // parts are one round at most
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
   if (swiglu)

@@ -245,6 +245,7 @@ struct Fp8GemmArgs {
   // added up by a second kernel.  1 and NULL: never.
   float *parts;
   int parts_cap;
+  int few_blocks;  // of the groups of up to kFp8FewRows, set by the launch; 0: one for each column tile
   // Groups of more than kFp8FewRows go in tiles of up to 256 rows (large: a group can have that many); their rows are read
   // from xp, packed tiles of fp8_packed_bytes(), or, NULL, as they are; H goes to packed tiles.
   bool large;
