@@ -21,13 +21,17 @@ namespace {
 
 // Few rows: 16 of them at a time, one block after the other.  A workgroup has 16 U columns of H (each wave 16, NB = 2
 // blocks of weights: gate and up) or 16 U NB of y; each wave one of KS parts of K, whose sums the first part's waves add
-// in order.  Rows are read from the caches in the operand layout, two steps ahead, with the weights,
-// R steps of 128 ahead, all in registers: no LDS, no barrier.  The weights are the
+// in order.  Rows are read from the caches in the operand layout, two steps ahead, with the weights, R steps of 128
+// ahead (8 KB a wave; twice as many made the FFN of 32 x 8 rows x 2880 x 2880 147 us for 141, one token's gate_up
+// 21.1 for 20.1: memory serves fewer requests at a time better), all in registers: no LDS, no barrier.  The weights are the
 // matrix instruction's first operand, so that a lane holds four consecutive columns of one row.
-template <bool SWIGLU, int U, int KS, int NB>
+// Measured: one token, 4 of 32 experts of 2880 x 2880, gate_up 20.1 us and down 11.0 (66 and 33 MB: 3.3 and 3.0 TB/s from 92 and
+// 180 workgroups, of which one CU takes in 50 GB/s at most, after 4.5 us of launch and lookups); 16 tokens 5.6 TB/s.
+template <bool SWIGLU, int U, int KS, int NB, int R>
 __global__ __launch_bounds__(64 * U * KS, 4) void fp8_small_kernel(const Fp8GemmArgs a) {
-  constexpr int R = 8 / NB, XR = 2, NS = SWIGLU ? 2 : 1;  // NS: scales a wave
+  constexpr int XR = 2, NS = SWIGLU ? 2 : 1;  // NS: scales a wave
   static_assert(!SWIGLU || (U == 8 && NB == 2), "a block of H's columns a workgroup");
+  static_assert(4 % R == 0, "a word of scales a trip");
   __shared__ float tops[SWIGLU ? 8 : 1][16];
   __shared__ f32x4 parts[KS > 1 ? (KS - 1) * U * NB * 64 : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lr = lane & 15,
@@ -85,11 +89,11 @@ __global__ __launch_bounds__(64 * U * KS, 4) void fp8_small_kernel(const Fp8Gemm
     f32x4 acc[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int t0 = tb; t0 < te; t0 += R) {
+    for (int t0 = tb; t0 < te; t0 += 4) {
       auto step = [&](auto jc) {
-        constexpr int J = decltype(jc)::value, S = J % 4;
+        constexpr int J = decltype(jc)::value;
         const int t = t0 + J;
-        if constexpr (S == 0) {
+        if constexpr (J == 0) {
           const int left = te - t;  // blocks of this part: the padding's scales are not looked at
           const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
           sx = nx & keep;
@@ -99,26 +103,20 @@ __global__ __launch_bounds__(64 * U * KS, 4) void fp8_small_kernel(const Fp8Gemm
         }
 #pragma unroll
         for (int m = 0; m < 4; ++m) {  // 32 of K: eight of each lane's 32 codes
-          const u32x4 xb = fp8_to_bf16(x[J % XR][m / 2][2 * (m % 2)], x[J % XR][m / 2][2 * (m % 2) + 1], fp8_scale<S>(sx));
+          const u32x4 xb = fp8_to_bf16(x[J % XR][m / 2][2 * (m % 2)], x[J % XR][m / 2][2 * (m % 2) + 1], fp8_scale<J>(sx));
 #pragma unroll
           for (int b = 0; b < NB; ++b)
-            acc[b] = mfma16(fp8_to_bf16(w[J][b][m / 2][2 * (m % 2)], w[J][b][m / 2][2 * (m % 2) + 1], fp8_scale<S>(sw[b % NS])), xb,
+            acc[b] = mfma16(fp8_to_bf16(w[J % R][b][m / 2][2 * (m % 2)], w[J % R][b][m / 2][2 * (m % 2) + 1], fp8_scale<J>(sw[b % NS])), xb,
                             acc[b]);
         }
         __builtin_amdgcn_sched_barrier(0);  // loads into registers still in use would get others, copied after a wait
         load_x(J % XR, t + XR);
-        load_w(J, t + R);
+        load_w(J % R, t + R);
       };
       step(std::integral_constant<int, 0>{});
       step(std::integral_constant<int, 1>{});
       step(std::integral_constant<int, 2>{});
       step(std::integral_constant<int, 3>{});
-      if constexpr (R == 8) {
-        step(std::integral_constant<int, 4>{});
-        step(std::integral_constant<int, 5>{});
-        step(std::integral_constant<int, 6>{});
-        step(std::integral_constant<int, 7>{});
-      }
     }
     if constexpr (KS > 1) {
       if (part > 0)
@@ -169,13 +167,13 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs &a, hipStream_t s) {
   // CU (32 groups of 16 rows, 2048 x 7168: 114 -> 101 us; of one row: 83 -> 79; but 4 groups, 2880 x 2880, 92 workgroups:
   // 11.0 -> 12.2), and a part of K where even one block leaves half of them idle (1 x 2048 x 7168: 8.6 -> 7.9).
   if (a.h8)
-    hipLaunchKernelGGL((fp8_small_kernel<true, 8, 1, 2>), grid(128), dim3(512), 0, s, a);
+    hipLaunchKernelGGL((fp8_small_kernel<true, 8, 1, 2, 2>), grid(128), dim3(512), 0, s, a);
   else if ((int64_t)groups * ((a.n_out + 63) / 64) < 128)
-    hipLaunchKernelGGL((fp8_small_kernel<false, 2, 2, 1>), grid(32), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((fp8_small_kernel<false, 2, 2, 1, 4>), grid(32), dim3(256), 0, s, a);
   else if ((int64_t)groups * ((a.n_out + 127) / 128) < 256)
-    hipLaunchKernelGGL((fp8_small_kernel<false, 4, 1, 1>), grid(64), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((fp8_small_kernel<false, 4, 1, 1, 4>), grid(64), dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((fp8_small_kernel<false, 4, 1, 2>), grid(128), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((fp8_small_kernel<false, 4, 1, 2, 2>), grid(128), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
