@@ -76,22 +76,31 @@ __global__ __launch_bounds__(256) void quantize_weights_kernel(const T *__restri
   __shared__ float part[4];
   __shared__ __attribute__((aligned(16))) uint8_t tile[128 * 128];
   const int kb = blockIdx.x, halves = swiglu ? 2 : 1;
-  const int nb = blockIdx.y / halves, half = blockIdx.y - nb * halves;
+  const int nb = __builtin_amdgcn_readfirstlane(blockIdx.y / halves), half = blockIdx.y - nb * halves;
   const int64_t g = blockIdx.z;
   const int kt = fp8_blocks(K), nt = (n_out + 15) / 16;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const T *m = w + (g * halves + half) * (int64_t)n_out * K;
+  // this wave's 32 rows; past the matrix zeros (range-checked loads: behind a branch each they would go one at a time)
+  const int first = nb * 128 + wave * 32, rows = __builtin_amdgcn_readfirstlane(max(0, min(32, n_out - first)));
+  const rsrc_t from = make_rsrc(m + (int64_t)first * K, (uint32_t)rows * (uint32_t)K * (uint32_t)sizeof(T));
   float v[32][2], top = 0.0f;
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
-    const int r = nb * 128 + wave * 32 + i;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int c = kb * 128 + h * 64 + lane;
-      v[i][h] = r < n_out && c < K ? to_f32(m[(int64_t)r * K + c]) : 0.0f;
-      top = fmaxf(top, fp8_magnitude(v[i][h]));
+      const uint32_t at = c < K ? ((uint32_t)(i * K + c)) * (uint32_t)sizeof(T) : kOob;
+      if constexpr (sizeof(T) == 4)
+        v[i][h] = __builtin_bit_cast(float, (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(from, at, 0, 0));
+      else
+        v[i][h] = to_f32((T)__builtin_amdgcn_raw_buffer_load_b16(from, at, 0, 0));
     }
   }
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) top = fmaxf(top, fp8_magnitude(v[i][h]));
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
   if (lane == 0) part[wave] = top;
