@@ -26,10 +26,11 @@ namespace moe {
 
 constexpr int kFp8Tile = 2048;  // bytes of 16 x 128 codes
 
-// Eight consecutive values as they are held, loaded and stored as 16-byte pieces at any alignment of the
+// Eight consecutive values of a row of d as they are held, loaded and stored as 16-byte pieces at any alignment of the
 // element's own size (the vector memory path takes unaligned addresses).  `n` of them exist (n <= 0: none; the
-// rest read as zeros and are not stored); WHOLE: rows are whole vectors, n is at least eight or
-// at most zero.
+// rest count as zeros and are not stored); WHOLE: rows are whole vectors, n is at least eight or
+// at most zero.  A row's last n < 8 are loaded one by one, each behind a branch and its own wait, or (BACK) as the
+// row's last eight, which front() moves to their places once all loads are under way.
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 template <typename T>
 struct Raw8 {
@@ -43,19 +44,34 @@ struct Raw8 {
         f[i] = __uint_as_float(v[i / 4][i % 4]);
     }
   }
+  __device__ __forceinline__ void front(int n) {
+    static_assert(sizeof(T) == 2, "of bf16");
+    if (n <= 0 || n >= 8) return;
+    const int by = 8 - n;
+#pragma unroll
+    for (int o = 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (by / 2 & o) v[0][i] = i + o < 4 ? v[0][(i + o) % 4] : 0u;
+    if (by % 2)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[0][i] = v[0][i] >> 16 | (i < 3 ? v[0][(i + 1) % 4] << 16 : 0u);
+  }
 };
-template <typename T, bool WHOLE>
-__device__ __forceinline__ Raw8<T> load8(const T *p, int n) {
+template <typename T, bool WHOLE, bool BACK = false>
+__device__ __forceinline__ Raw8<T> load8(const T *p, int n, int d) {
   Raw8<T> r;
 #pragma unroll
   for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = u32x4{0u, 0u, 0u, 0u};
-  if (n >= 8) {
+  if (n >= 8 || (BACK && n > 0 && d >= 8)) {
+    const T *q = BACK ? p + min(n - 8, 0) : p;
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = reinterpret_cast<const u32x4_any *>(p)[i];
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = reinterpret_cast<const u32x4_any *>(q)[i];
   } else if (!WHOLE && n > 0) {
+    const int by = BACK ? 8 - n : 0;
     T t[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = i < n ? p[i] : T(0);
+    for (int i = 0; i < 8; ++i) t[i] = i >= by && i - by < n ? p[i - by] : T(0);
     __builtin_memcpy(r.v, t, sizeof t);
   }
   return r;

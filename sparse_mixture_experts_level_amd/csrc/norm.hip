@@ -70,20 +70,28 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rms_norm_kernel(const N
   const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
   if (row >= c.T) return;  // whole waves, and whole workgroups where a barrier follows
   const int d = c.d;
+  // TB/s one by one and back: 45829 x 1091 of bf16 4.64 and 5.41, 17355 x 2881 4.22 and 4.84; of floats 5.07 and 4.24
+  constexpr bool BACK = !WHOLE && sizeof(T) == 2;
   const T *x = static_cast<const T *>(c.x) + row * d;
   const T *res = c.residual ? static_cast<const T *>(c.residual) + row * d : nullptr;
   Raw8<T> xr[NV], rr[NV], wr[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int col = 8 * (t + i * TPR);
-    xr[i] = load8<T, WHOLE>(x + col, d - col);
-    if (res) rr[i] = load8<T, WHOLE>(res + col, d - col);
-    wr[i] = load8<T, WHOLE>(static_cast<const T *>(c.weight) + col, d - col);
+    xr[i] = load8<T, WHOLE, BACK>(x + col, d - col, d);
+    if (res) rr[i] = load8<T, WHOLE, BACK>(res + col, d - col, d);
+    wr[i] = load8<T, WHOLE, BACK>(static_cast<const T *>(c.weight) + col, d - col, d);
   }
   float h[NV][8];
   double sum = 0.0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
+    if constexpr (BACK) {
+      const int n = d - 8 * (t + i * TPR);
+      xr[i].front(n);
+      if (res) rr[i].front(n);
+      wr[i].front(n);
+    }
     xr[i].to(h[i]);
     if (res) {
       float r[8];
@@ -144,25 +152,32 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rms_norm_backward_kerne
   __shared__ float rows_dw[RPB > 1 ? RPB - 1 : 1][RPB > 1 ? TPR * NV * 8 : 1];
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   const int d = c.d;
+  // From 64 sums a thread on the weight and dh are loaded where they are used, the weight from the caches: held over the
+  // rows they did not fit.
+  constexpr bool LEAN = NV >= 8;
   float dw[NV][8];
-  Raw8<T> wr[NV];
+  Raw8<T> wr[LEAN ? 1 : NV];
+  auto weight = [&](int i) -> Raw8<T> {
+    const int col = 8 * (t + i * TPR);
+    return load8<T, WHOLE>(static_cast<const T *>(c.weight) + col, d - col, d);
+  };
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int col = 8 * (t + i * TPR);
-    wr[i] = load8<T, WHOLE>(static_cast<const T *>(c.weight) + col, d - col);
+    if constexpr (!LEAN) wr[i] = weight(i);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
   }
   int turn = 0;
   for (int64_t row = (int64_t)blockIdx.x * RPB + sub; row < c.T; row += (int64_t)gridDim.x * RPB, turn ^= 1) {
     const float rstd = c.rstd[row];
-    Raw8<T> gr[NV], hr[NV], ar[NV];
+    Raw8<T> gr[NV], hr[NV], ar[LEAN ? 1 : NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = 8 * (t + i * TPR);
-      gr[i] = load8<T, WHOLE>(static_cast<const T *>(c.dy) + row * d + col, d - col);
-      hr[i] = load8<T, WHOLE>(static_cast<const T *>(c.h) + row * d + col, d - col);
-      if (c.dh) ar[i] = load8<T, WHOLE>(static_cast<const T *>(c.dh) + row * d + col, d - col);
+      gr[i] = load8<T, WHOLE>(static_cast<const T *>(c.dy) + row * d + col, d - col, d);
+      hr[i] = load8<T, WHOLE>(static_cast<const T *>(c.h) + row * d + col, d - col, d);
+      if constexpr (!LEAN)
+        if (c.dh) ar[i] = load8<T, WHOLE>(static_cast<const T *>(c.dh) + row * d + col, d - col, d);
     }
     float sum = 0.0f;
 #pragma unroll
@@ -170,7 +185,10 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rms_norm_backward_kerne
       float g[8], xh[8], w[8];
       gr[i].to(g);
       hr[i].to(xh);
-      wr[i].to(w);
+      if constexpr (LEAN)
+        weight(i).to(w);
+      else
+        wr[i].to(w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         xh[j] *= rstd;
@@ -184,16 +202,24 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rms_norm_backward_kerne
       float g[8], xh[8], w[8], o[8];
       gr[i].to(g);
       hr[i].to(xh);
-      wr[i].to(w);
+      if constexpr (LEAN)
+        weight(i).to(w);
+      else
+        wr[i].to(w);
+      const int col = 8 * (t + i * TPR);
       if (c.dh) {
-        ar[i].to(o);
+        Raw8<T> r;
+        if constexpr (LEAN)
+          r = load8<T, WHOLE>(static_cast<const T *>(c.dh) + row * d + col, d - col, d);
+        else
+          r = ar[i];
+        r.to(o);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) o[j] = 0.0f;
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] += rstd * (g[j] * w[j] - xh[j] * rstd * mean);
-      const int col = 8 * (t + i * TPR);
       store8<T, WHOLE>(static_cast<T *>(c.dx) + row * d + col, d - col, o);
     }
   }
@@ -247,7 +273,7 @@ __global__ __launch_bounds__(256) void rms_norm_dweight_kernel(const float *__re
 
 // Threads a row and vectors a thread for rows of d values (whole blocks of 128, the 8-bit output's padding), and
 // whether rows are whole vectors.
-template <typename F>
+template <bool BACKWARD, typename F>
 void by_width(int d, F f) {
   const int vecs = fp8_row_bytes(d) / 8;
   const auto whole = [&](auto tpr, auto nv) {
@@ -265,7 +291,10 @@ void by_width(int d, F f) {
   MOE_WIDTH(256, 4);
   MOE_WIDTH(256, 8);
 #undef MOE_WIDTH
-  whole(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
+  if constexpr (BACKWARD)  // (1024 x 4 have 128 registers each: it spilled, 3050 x 16391 of bf16 at 0.9 TB/s for 2.4)
+    whole(std::integral_constant<int, 512>{}, std::integral_constant<int, 8>{});
+  else
+    whole(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
 }
 
 // Workgroups of the backward: eight rows or more for each thread's part of dw, whose
@@ -279,7 +308,7 @@ int backward_blocks(int T, int d) {
 }  // namespace
 
 hipError_t launch_rms_norm(const NormCall &c, hipStream_t s) {
-  by_width(c.d, [&](auto tpr, auto nv, auto whole) {
+  by_width<false>(c.d, [&](auto tpr, auto nv, auto whole) {
     constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
     constexpr bool WHOLE = decltype(whole)::value;
     constexpr int RPB = TPR >= 256 ? 1 : 256 / TPR;
@@ -297,7 +326,7 @@ size_t rms_norm_backward_workspace_bytes(int T, int d) { return (size_t)backward
 hipError_t launch_rms_norm_backward(const NormBwdCall &c, void *ws, hipStream_t s) {
   const int blocks = backward_blocks(c.T, c.d);
   if (blocks > 0)
-    by_width(c.d, [&](auto tpr, auto nv, auto whole) {
+    by_width<true>(c.d, [&](auto tpr, auto nv, auto whole) {
       constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
       constexpr bool WHOLE = decltype(whole)::value;
       const dim3 grid((unsigned)blocks), block(TPR > 256 ? TPR : 256);

@@ -28,7 +28,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const T *__restrict_
     const int64_t row = q / scale_bytes;
     const int b = (int)(q - row * scale_bytes), c0 = b * kFp8Block + l * 8;
     float v[8], top = 0.0f;
-    load8<T, false>(x + row * K + c0, K - c0).to(v);
+    load8<T, false>(x + row * K + c0, K - c0, K).to(v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = fmaxf(top, fp8_magnitude(v[i]));
     top = group_reduce<16>(top, [](float a, float b) { return fmaxf(a, b); });
