@@ -130,6 +130,38 @@ def test_weights_to_8_bits(dt, G, n, K, swiglu):
     c1(), c2()
 
 
+def test_rows_past_2_to_31_values():
+    x = dev(np.random.default_rng(6).standard_normal((1000, 512)), torch.bfloat16)
+    codes, scale = ops.fp8_rows(1000, 512)
+    ops.moe_quantize_rows_fp8(x, codes, scale)
+    X = x.repeat(4300, 1)
+    C, S = ops.fp8_rows(len(X), 512)
+    ops.moe_quantize_rows_fp8(X, C, S)
+    assert torch.all(C.view(4300, 1000, 512) == codes) and torch.all(S.view(4300, 1000, 4) == scale)
+    back = torch.empty_like(x)
+    ops.moe_dequantize_rows_fp8(codes, scale, back)
+    ops.moe_dequantize_rows_fp8(C, S, X)
+    assert torch.all(X.view(4300, 1000, 512) == back)
+
+
+def test_calls_without_rows():
+    """Nothing is written but the gradient of the weight, which is zeros."""
+    none, w = torch.empty((0, 200), dtype=torch.bfloat16, device=DEV), torch.ones(200, dtype=torch.bfloat16, device=DEV)
+    codes, scale = ops.fp8_rows(0, 200)
+    ops.moe_quantize_rows_fp8(none, codes, scale)
+    ops.moe_dequantize_rows_fp8(codes, scale, none)
+    ops.moe_rms_norm(none, w, 1e-6, y=torch.empty_like(none))
+    dw = torch.full((200,), 7.0, device=DEV)
+    ops.moe_rms_norm_backward(none, none, w, torch.empty(0, device=DEV), torch.empty_like(none), dw,
+                              ops.workspace(ops.moe_rms_norm_backward_workspace_size(0, 200)))
+    assert torch.all(dw == 0)
+    off = torch.zeros(3, dtype=torch.int32, device=DEV)
+    w8 = ops.fp8_weights(torch.ones((2, 30, 200), dtype=torch.bfloat16, device=DEV))
+    ws = ops.workspace(ops.moe_grouped_linear_fp8_workspace_size(2, 0, 1, 30, 200))
+    ops.moe_grouped_linear_fp8(2, 0, 1, 30, 200, codes, scale, off, *w8, none[:, :30].contiguous(), ws)
+    torch.cuda.synchronize()
+
+
 # ------------------------------------------------------------------------------ norm
 
 def _held(dt):
@@ -424,6 +456,14 @@ def test_linear_of_many_groups(counts):
     _linear(counts, 40, 130, True, True, len(counts))
 
 
+@pytest.mark.parametrize("counts,n,K", [([20, 0, 3] * 30, 1100, 130), ([17, 128] * 60 + [129, 300], 900, 130),
+                                        ([1, 40] * 130, 300, 260)])
+def test_linear_of_several_column_tiles_a_workgroup(counts, n, K):
+    say(f"linear, {len(counts)} groups, {n} x {K}")
+    _linear(counts, n, K, True, True, len(counts), hint=max(counts))
+    _linear(counts, n, K, False, False, len(counts) + 1, hint=128)
+
+
 @pytest.mark.parametrize("scale_rows,k", [(1, 200), (5, 200), (30, 200), (30, 2700)])
 def test_offsets_that_decrease(scale_rows, k):
     """Not allowed, and harmless: rows are left out or one of their groups', and nothing else is written."""
@@ -582,7 +622,7 @@ FFNS = [([1], 1, 1), ([2, 0, 1], 64, 64), ([16, 5], 130, 200), ([33, 0, 1], 256,
 
 
 LONG_FFNS = [([100], 2700, 130), ([300, 0, 20], 2700, 257), ([90, 30], 140, 2700), ([300, 129], 130, 2700),
-             ([1, 0, 2] * 50, 130, 200), ([20, 0, 3] * 30, 130, 200), ([140, 3] * 40, 130, 200)]
+             ([1, 0, 2] * 50, 130, 200), ([20, 0, 3] * 30, 130, 200), ([140, 3] * 40, 130, 200), ([20, 0, 3] * 30, 530, 300)]
 
 
 @pytest.mark.parametrize("i", range(len(FFNS) + len(LONG_FFNS)))
