@@ -301,23 +301,37 @@ void by_width(int d, F f) {
 // writing and reading again is then at most an eighth of the rows' own bytes, but enough to fill the GPU.
 int backward_blocks(int T, int d) {
   const int rpb = fp8_row_bytes(d) / 8 <= 256 ? 4 : 1;  // rows a workgroup has at once (by_width)
-  const int all = (T + rpb - 1) / rpb;
+  const int all = T / rpb + (T % rpb != 0);
   return std::min(all, std::min(1024, std::max(512, all / 8)));
 }
 
 }  // namespace
 
-hipError_t launch_rms_norm(const NormCall &c, hipStream_t s) {
-  by_width<false>(c.d, [&](auto tpr, auto nv, auto whole) {
-    constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-    constexpr bool WHOLE = decltype(whole)::value;
-    constexpr int RPB = TPR >= 256 ? 1 : 256 / TPR;
-    const dim3 grid((unsigned)((c.T + RPB - 1) / RPB)), block(TPR > 256 ? TPR : 256);
-    if (c.f32)
-      hipLaunchKernelGGL((rms_norm_kernel<float, TPR, NV, WHOLE>), grid, block, 0, s, c);
-    else
-      hipLaunchKernelGGL((rms_norm_kernel<bf16_t, TPR, NV, WHOLE>), grid, block, 0, s, c);
-  });
+hipError_t launch_rms_norm(const NormCall &call, hipStream_t s) {
+  constexpr int64_t kRows = 1 << 22;  // a launch: the threads of one are counted in 32 bits
+  const int64_t size = call.f32 ? 4 : 2, row_bytes = fp8_row_bytes(call.d), scale_bytes = fp8_scale_bytes(call.d);
+  for (int64_t first = 0; first < call.T; first += kRows) {
+    NormCall c = call;
+    auto from = [&](auto p, int64_t bytes) { return p ? (decltype(p))((uintptr_t)p + (size_t)(first * bytes)) : p; };
+    c.x = from(call.x, call.d * size);
+    c.residual = from(call.residual, call.d * size);
+    c.h = from(call.h, call.d * size);
+    c.y = from(call.y, call.d * size);
+    c.y8 = from(call.y8, row_bytes);
+    c.y_scale = from(call.y_scale, scale_bytes);
+    c.rstd = from(call.rstd, 4);
+    c.T = (int)std::min<int64_t>(kRows, call.T - first);
+    by_width<false>(c.d, [&](auto tpr, auto nv, auto whole) {
+      constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+      constexpr bool WHOLE = decltype(whole)::value;
+      constexpr int RPB = TPR >= 256 ? 1 : 256 / TPR;
+      const dim3 grid((unsigned)((c.T + RPB - 1) / RPB)), block(TPR > 256 ? TPR : 256);
+      if (c.f32)
+        hipLaunchKernelGGL((rms_norm_kernel<float, TPR, NV, WHOLE>), grid, block, 0, s, c);
+      else
+        hipLaunchKernelGGL((rms_norm_kernel<bf16_t, TPR, NV, WHOLE>), grid, block, 0, s, c);
+    });
+  }
   return hipGetLastError();
 }
 

@@ -202,6 +202,17 @@ COMMON = [(dict(G=0), INVALID), (dict(G=1025), INVALID), (dict(rows=-1), INVALID
 
 
 @needs_lib
+def test_workspaces_of_the_most_rows():
+    top = 2 ** 31 - 1
+    assert 512 * 4 <= ops.moe_rms_norm_backward_workspace_size(top, 1) <= 1024 * 4
+    assert ops.moe_rms_norm_backward_workspace_size(top, 32768) <= 1024 * 32768 * 4
+    # codes packed for every tile that there can be, no more than a tile a group above the rows' own
+    need = ops.moe_grouped_linear_fp8_workspace_size(1024, top, top, 4096, 128)
+    assert top * 132 <= need <= (2 * top + 1025 * 256) * 132
+    assert ops.moe_grouped_linear_fp8_workspace_size(1024, top, 16, 4096, 128) <= 256
+
+
+@needs_lib
 @pytest.mark.parametrize("kw,status", COMMON + [
     (dict(n=0), INVALID), (dict(k=0), INVALID), (dict(n=1 << 16, k=1 << 15), UNSUPPORTED), (dict(w8=None), INVALID),
     (dict(ws8=None), INVALID), (dict(ws8=FAKE + 4), INVALID), (dict(k=1 << 24), UNSUPPORTED),

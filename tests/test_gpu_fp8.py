@@ -348,6 +348,34 @@ def test_norm_and_gradients_past_2_to_31_values():
     assert np.all(np.abs(f64(DW) - want) <= (T / 512 + 140) * U * size)
 
 
+def test_norm_of_more_rows_than_a_launch_takes():
+    n, d, times = 1000, 9, 9001  # 2^22 rows a launch
+    rng = np.random.default_rng(13)
+    x, r = (dev(rng.standard_normal((n, d)), torch.bfloat16).repeat(times, 1) for _ in range(2))
+    w = dev(1 + 0.3 * rng.standard_normal(d), torch.bfloat16)
+    T = n * times
+    h, y, rstd, (y8, ys) = torch.empty_like(x), torch.empty_like(x), torch.empty(T, device=DEV), ops.fp8_rows(T, d)
+    ops.moe_rms_norm(x, w, 1e-6, residual=r, h=h, y=y, rstd=rstd, y8=y8, y_scale=ys)
+    want = [torch.empty_like(t[:n]) for t in (h, y, rstd, y8, ys)]
+    ops.moe_rms_norm(x[:n], w, 1e-6, residual=r[:n], h=want[0], y=want[1], rstd=want[2], y8=want[3], y_scale=want[4])
+    for big, small in zip((h, y, rstd, y8, ys), want):
+        assert torch.all(big.view(times, *small.shape) == small)
+
+
+def test_codes_as_torch_holds_them():
+    """float8_e4m3fn tensors are taken for codes."""
+    x = dev(np.random.default_rng(14).standard_normal((5, 256)), torch.bfloat16)
+    codes, scale = ops.fp8_rows(5, 256)
+    ops.moe_quantize_rows_fp8(x, codes, scale)
+    own, scale2 = torch.empty((5, 256), dtype=torch.float8_e4m3fn, device=DEV), torch.empty_like(scale)
+    ops.moe_quantize_rows_fp8(x, own, scale2)
+    assert torch.equal(own.view(torch.uint8), codes) and torch.equal(scale, scale2)
+    values = torch.empty((5, 256), device=DEV)
+    ops.moe_dequantize_rows_fp8(own, scale, values)
+    want = own.float().view(5, 2, 128) * torch.exp2(scale[:, :2].float() - 127)[:, :, None]
+    assert torch.equal(values, want.view(5, 256))
+
+
 # ------------------------------------------------------------------------------ products
 
 def _offsets(counts, first=0):
