@@ -752,9 +752,9 @@ Fp8Layout fp8_layout(int32_t G, int64_t rows_max, int32_t group_rows_max, int32_
   L.hp = take(f && large ? moe::fp8_packed_bytes(rows_max, G, f) : 0);
   L.hp_scale = take(f && large ? moe::fp8_packed_scale_bytes(rows_max, G, f) : 0);
   if (std::min<int64_t>(rows_max, group_rows_max) > moe::kFp8SmallRows)
-    L.parts = take(f ? std::max(moe::fp8_parts_bytes(rows_max, group_rows_max, f, k, true),
-                                moe::fp8_parts_bytes(rows_max, group_rows_max, n_out, f, false))
-                     : moe::fp8_parts_bytes(rows_max, group_rows_max, n_out, k, false));
+    L.parts = take(f ? std::max(moe::fp8_parts_bytes(rows_max, group_rows_max, G, f, k, true),
+                                moe::fp8_parts_bytes(rows_max, group_rows_max, G, n_out, f, false))
+                     : moe::fp8_parts_bytes(rows_max, group_rows_max, G, n_out, k, false));
   L.total = o;
   return L;
 }
@@ -786,6 +786,7 @@ moe::Fp8GemmArgs fp8_args(int32_t G, int64_t rows_max, int32_t group_rows_max, i
 // Room for the sums of a product's parts.
 void parts_fp8(moe::Fp8GemmArgs &a, void *ws, const Fp8Layout &L, bool swiglu) {
   a.parts_cap = moe::fp8_parts_cap(a.rows_max, a.group_rows_max, a.n_out, a.K, swiglu);
+  a.rounds = moe::fp8_rounds(a.rows_max, a.num_groups, a.n_out, a.K, swiglu, a.large);
   a.parts = at<float>(ws, L.parts);
 }
 

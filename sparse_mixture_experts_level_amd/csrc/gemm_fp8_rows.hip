@@ -21,7 +21,7 @@ constexpr int LG_TILE = kFp8LargeRows * 64;  // bytes of an operand's stage: 256
 
 // Block `block` of a launch of per_tile column tiles: the tiles of the groups of many rows, group after group, a block for
 // each column tile; then the groups of few (any number of rows where none is announced to have many), a block for each of
-// `chunks` ranges of column tiles; all of them again for each further part of K.  One pass over the offsets, two for more than 64 groups; all results in scalar registers.
+// `chunks` ranges of column tiles; all of them, or those past the last whole 256, again for each further part of K.  One pass over the offsets, two for more than 64 groups; all results in scalar registers.
 struct Fp8Tile {
   int g, begin, end;  // -1: there is no such tile
   int first, count;   // the group's tiles, numbered over all groups (count 0: few rows)
@@ -29,11 +29,14 @@ struct Fp8Tile {
   int tiles;          // of many rows, in all
   int part, parts;
   int col0, col1;     // few rows: the column tiles
+  int slot, cut;      // the tile's place among the `cut` tiles that are cut, where those are the last round's; -1: by rows
 };
-__device__ __forceinline__ Fp8Tile find_tile(const Fp8GemmArgs &a, int tiles_max, int block, int per_tile, bool spread) {
+enum Fp8Blocks { kPack, kProduct, kAdd };  // block: a tile; of the product's launch; of the tiles that are cut
+__device__ __forceinline__ Fp8Tile find_tile(const Fp8GemmArgs &a, int tiles_max, int block, int per_tile, Fp8Blocks kind) {
+  const bool spread = kind != kPack;
   const int lane = threadIdx.x & 63, G = a.num_groups;
   const int few = a.large ? kFp8FewRows : INT_MAX;
-  Fp8Tile t{-1, 0, 0, 0, 0, 0, 0, 0, 1, 0, 0};
+  Fp8Tile t{-1, 0, 0, 0, 0, 0, 0, 0, 1, 0, 0, -1, 0};
   int b = 0, e = 0, all = 0;
 #pragma unroll 1
   for (int g0 = 0; g0 < G; g0 += 64) {
@@ -53,15 +56,31 @@ __device__ __forceinline__ Fp8Tile find_tile(const Fp8GemmArgs &a, int tiles_max
   const int large = t.tiles * per_tile;
   all = large + all * chunks;
   if (all == 0) return t;
-  if (spread && a.parts_cap > 1) {
-    t.parts = fp8_parts(all, a.rows_max, per_tile, a.K, a.parts_cap);
-    t.part = block / all;
-    block -= t.part * all;
+  int whole = 0;  // tiles of the whole rounds
+  if (spread && (a.parts_cap > 1 || a.rounds)) {
+    const int full = a.rounds && all == large ? all / 256 * 256 : 0, rest = all - full;
+    if (full > 0 && rest > 0)
+      t.parts = fp8_parts(rest, rest, 256, a.K, kFp8Parts);
+    else if (full == 0 && a.parts_cap > 1)
+      t.parts = fp8_parts(all, a.rows_max, per_tile, a.K, a.parts_cap);
+    if (kind == kAdd) block += full;
+    if (t.parts > 1) {
+      whole = full;
+      if (block < whole) {
+        t.parts = 1;
+      } else {
+        t.part = (block - whole) / rest;
+        block -= t.part * rest;
+        t.cut = rest;
+        if (full > 0) t.slot = block - whole;
+      }
+    }
   }
-  if (t.part >= t.parts) return t;
+  if (block >= all || t.part >= t.parts) return t;
   // the first tiles' blocks in one contiguous range an XCD, as neighbours share operands
   const bool many = block < large;
-  const int lin = spread && many ? xcd_remap(block, large) : block;
+  const int spreads = whole > 0 ? whole : large;
+  const int lin = spread && block < spreads ? xcd_remap(block, spreads) : block;
   const int v = many ? lin / per_tile : t.tiles + (lin - large) / chunks;
   t.lin = lin;
   t.col0 = __builtin_amdgcn_readfirstlane((lin - large) % chunks * columns);
@@ -339,7 +358,7 @@ __global__ __launch_bounds__(512, 1) void fp8_rows_kernel(const Fp8GemmArgs a, i
   auto bufB = [&](int b) -> uint8_t * { return b == 0 ? sB0 : b == 1 ? sB1 : b == 2 ? sB2 : sB3; };
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / 4, wn = wave % 4, lr = lane & 31, lh = lane >> 5;
-  const Fp8Tile tile = find_tile(a, tiles_max, blockIdx.x, n_tiles, true);
+  const Fp8Tile tile = find_tile(a, tiles_max, blockIdx.x, n_tiles, kProduct);
   if (tile.g < 0) return;
   const int g = tile.g, begin = tile.begin, end = tile.end, mt_first = tile.first, mt_count = tile.count;
   if (mt_count == 0) {
@@ -544,8 +563,9 @@ __global__ __launch_bounds__(512, 1) void fp8_rows_kernel(const Fp8GemmArgs a, i
     for (int i = 0; i < 4; ++i) {
       const int row = wm * 128 + i * 32 + lr;
       if (row >= rows) continue;
-      float *o = a.parts + (tile.part * (int64_t)a.rows_max + m0 + row) * n_tiles * 256 + nt * 256 + lh * 4 +
-                 (SWIGLU ? wn * 32 : wn * 64);
+      float *o = (tile.slot < 0 ? a.parts + (tile.part * (int64_t)a.rows_max + m0 + row) * n_tiles * 256 + nt * 256
+                                : a.parts + ((int64_t)(tile.part * tile.cut + tile.slot) * kFp8LargeRows + row) * 256) +
+                 lh * 4 + (SWIGLU ? wn * 32 : wn * 64);
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -633,7 +653,7 @@ __global__ __launch_bounds__(512, 1) void fp8_rows_kernel(const Fp8GemmArgs a, i
 // fp8_rows_kernel.
 template <bool SWIGLU>
 __global__ __launch_bounds__(256) void fp8_add_parts_kernel(const Fp8GemmArgs a, int n_tiles, int tiles_max) {
-  const Fp8Tile tile = find_tile(a, tiles_max, blockIdx.x, n_tiles, true);
+  const Fp8Tile tile = find_tile(a, tiles_max, blockIdx.x, n_tiles, kAdd);
   if (tile.g < 0 || tile.parts == 1 || tile.part > 0) return;
   int nt, mt = 0, m0 = tile.begin, n = tile.end - tile.begin, last = n;
   if (tile.count) {
@@ -654,7 +674,8 @@ __global__ __launch_bounds__(256) void fp8_add_parts_kernel(const Fp8GemmArgs a,
     if (r < n)
 #pragma unroll 2
       for (int s = 0; s < tile.parts; ++s) {
-        const float *p = a.parts + (s * (int64_t)a.rows_max + m0 + r) * n_tiles * 256 + nt * 256 + l * 8;
+        const float *p = (tile.slot < 0 ? a.parts + (s * (int64_t)a.rows_max + m0 + r) * n_tiles * 256 + nt * 256
+                                        : a.parts + ((int64_t)(s * tile.cut + tile.slot) * kFp8LargeRows + r) * 256) + l * 8;
 #pragma unroll
         for (int h = 0; h < (SWIGLU ? 2 : 1); ++h) {
           const f32x4 x = *reinterpret_cast<const f32x4 *>(p + h * 128), y = *reinterpret_cast<const f32x4 *>(p + h * 128 + 4);
@@ -703,7 +724,7 @@ __global__ __launch_bounds__(256) void fp8_pack_rows_kernel(const Fp8GemmArgs a,
   const int b0 = blockIdx.y * 4, m_tile = blockIdx.x / 4;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int block = (blockIdx.x % 4) * 4 + wave, r = block * 16 + (lane & 15), c = lane >> 4;  // of 16 rows; row, chunk
-  const Fp8Tile t = find_tile(a, tiles_max, m_tile, 1, false);
+  const Fp8Tile t = find_tile(a, tiles_max, m_tile, 1, kPack);
   if (t.count == 0) return;
   const int per = fp8_tile_rows(t.end - t.begin, t.count), m0 = t.begin + (m_tile - t.first) * per;
   const int rows = min(per, t.end - m0);
@@ -765,15 +786,16 @@ hipError_t launch_fp8_gemm_rows(const Fp8GemmArgs &call, hipStream_t s) {
   const int groups = std::min(a.num_groups, a.rows_max);
   a.few_blocks = a.parts_cap > 1 ? 0 : few_blocks(groups, n_tiles, a.K);
   const int64_t blocks = tiles * n_tiles + (a.few_blocks ? std::max(a.few_blocks, groups) : (int64_t)groups * n_tiles);
-  const int64_t grid = a.parts_cap > 1 ? std::max<int64_t>(blocks, 256) : blocks;  // parts are one round at most
+  // parts are one round at most
+  const int64_t grid = a.rounds ? blocks + 256 : a.parts_cap > 1 ? std::max<int64_t>(blocks, 256) : blocks;
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
   if (swiglu)
     hipLaunchKernelGGL((fp8_rows_kernel<true>), dim3((unsigned)grid), dim3(512), 0, s, a, n_tiles, (int)tiles);
   else
     hipLaunchKernelGGL((fp8_rows_kernel<false>), dim3((unsigned)grid), dim3(512), 0, s, a, n_tiles, (int)tiles);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.parts_cap == 1) return e;
-  const dim3 adding((unsigned)std::min<int64_t>(blocks, 128), 16);  // tiles in parts are half a round at most
+  if (e != hipSuccess || (a.parts_cap == 1 && !a.rounds)) return e;
+  const dim3 adding((unsigned)std::min<int64_t>(blocks, 128), 16);  // tiles that are cut: half a round at most
   if (swiglu)
     hipLaunchKernelGGL((fp8_add_parts_kernel<true>), adding, dim3(256), 0, s, a, n_tiles, (int)tiles);
   else

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 namespace moe {
 
 // ---- router (router.hip)
@@ -245,6 +247,7 @@ struct Fp8GemmArgs {
   // added up by a second kernel.  1 and NULL: never.
   float *parts;
   int parts_cap;
+  bool rounds;  // or, of the tiles of many rows, those past the last whole 256, in [256 parts' tiles][256][256]
   int few_blocks;  // of the groups of up to kFp8FewRows, set by the launch; 0: one for each column tile
   // Groups of more than kFp8FewRows go in tiles of up to 256 rows (large: a group can have that many); their rows are read
   // from xp, packed tiles of fp8_packed_bytes(), or, NULL, as they are; H goes to packed tiles.
@@ -304,9 +307,21 @@ inline int fp8_parts_cap(int64_t rows, int64_t group_rows, int n_out, int k, boo
   const int tiles_n = (int)(fp8_part_columns(n_out, swiglu) / 256);
   return fp8_parts((rows + per - 1) / per * tiles_n, rows, tiles_n, k, kFp8Parts);
 }
-inline int64_t fp8_parts_bytes(int64_t rows, int64_t group_rows, int n_out, int k, bool swiglu) {
+// Whether the tiles of many rows past the last whole 256 are looked at for that: K past 7168, where a second launch with
+// nothing to add is a twentieth of a round or less; few enough rounds; and for one group, whose tiles are known,
+// only if they are cut.  us whole and cut: 8 x 1024 rows, 4096 x 14336 (576 tiles, 2.25 rounds) 474 and 425; 4096 x 14336 x
+// 14336 (896, 3.5) 686 and 658.
+inline bool fp8_rounds(int64_t rows, int G, int n_out, int k, bool swiglu, bool large) {
+  const int64_t tiles_n = fp8_part_columns(n_out, swiglu) / 256, least = (rows + kFp8LargeRows - 1) / kFp8LargeRows * tiles_n;
+  if (!large || fp8_scale_bytes(k) / 4 < 15 || least > 8 * 256) return false;
+  if (G == 1) return least > 256 && least % 256 && fp8_parts(least % 256, least % 256, 256, k, kFp8Parts) > 1;
+  return fp8_large_tiles_max(rows, G) * tiles_n > 256;
+}
+inline int64_t fp8_parts_bytes(int64_t rows, int64_t group_rows, int G, int n_out, int k, bool swiglu) {
   const int cap = fp8_parts_cap(rows, group_rows, n_out, k, swiglu);
-  return cap > 1 ? 4 * cap * rows * fp8_part_columns(n_out, swiglu) : 0;
+  const bool large = (rows < group_rows ? rows : group_rows) > kFp8FewRows;
+  return std::max<int64_t>(cap > 1 ? 4 * cap * rows * fp8_part_columns(n_out, swiglu) : 0,
+                           fp8_rounds(rows, G, n_out, k, swiglu, large) ? 256 * 4 * kFp8LargeRows * 256 : 0);
 }
 // Whether the rows of large tiles are packed first: a stage of 64 of K is half of each row's line, which every column tile
 // then reads twice, but packing is a launch and a copy.  us as they are and packed: 4096 x 1024 x 14336 (4

@@ -478,6 +478,71 @@ def test_linear_in_parts_of_k(i, whole):
     _linear(counts, n, K, whole, not i % 2, 300 + i, hint=700)
 
 
+def _whole_on_device(gen, *shape):
+    return torch.randint(-4, 5, shape, generator=gen, device=DEV).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("counts,n", [([5000], 3300), ([2000, 1500, 0, 1500], 3300), ([4900, 100], 3300), ([700, 260], 28000)])
+def test_linear_whose_last_round_is_cut(counts, n):
+    """A few tiles more than whole rounds of 256; sums of whole numbers are the same in any order, so that the call equals
+    calls of 600 rows, whose tiles are not that many.  With a group of few rows nothing is cut."""
+    say(f"linear, last round {counts} x {n}")
+    K, rows, G = 7300, sum(counts), len(counts)
+    gen = torch.Generator(device=DEV).manual_seed(rows)
+    x, w = _whole_on_device(gen, rows, K), _whole_on_device(gen, G, n, K)
+    codes, scale = ops.fp8_rows(rows, K)
+    ops.moe_quantize_rows_fp8(x, codes, scale)
+    c8, s8 = ops.fp8_weights(w)
+    off = _offsets(counts)
+    y, guard = guarded((rows, n), torch.bfloat16, 3)
+    need = ops.moe_grouped_linear_fp8_workspace_size(G, rows, max(counts), n, K)
+    ws = torch.full((need + GUARD,), 255, dtype=torch.uint8, device=DEV)
+    for _ in range(2):
+        ops.moe_grouped_linear_fp8(G, rows, max(counts), n, K, codes, scale, dev(off, torch.int32), c8, s8, y, ws[:need])
+    guard()
+    assert torch.all(ws[need:] == 255)
+    c8, s8 = c8.view(G, -1), s8.view(G, -1)
+    for g in range(G):
+        for a in range(off[g], off[g + 1], 600):
+            b = min(a + 600, off[g + 1])
+            want = torch.empty((b - a, n), dtype=torch.bfloat16, device=DEV)
+            own = ops.workspace(ops.moe_grouped_linear_fp8_workspace_size(1, b - a, b - a, n, K))
+            ops.moe_grouped_linear_fp8(1, b - a, b - a, n, K, codes[a:b].clone(), scale[a:b].clone(), dev([0, b - a], torch.int32),
+                                       c8[g].clone(), s8[g].clone(), want, own)
+            assert torch.equal(y[a:b], want), (g, a)
+    few = torch.arange(0, rows, rows // 40, device=DEV)
+    for g in range(G):
+        r = few[(few >= int(off[g])) & (few < int(off[g + 1]))]
+        assert torch.equal(y[r], (x[r].double() @ w[g].double().T).float().to(torch.bfloat16)), g
+
+
+def test_ffn_whose_last_round_is_cut():
+    """Gate and up sums of whole numbers, so that H, and what it gives, is the same as that of 250 rows at a time."""
+    rows, d, f = 2100, 7300, 3700
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    x, gu = _whole_on_device(gen, rows, d), _whole_on_device(gen, 1, 2 * f, d)
+    dn = torch.randn((1, 300, f), generator=gen, device=DEV).to(torch.bfloat16)
+    gu[:, :, 300:] *= (torch.rand((1, 2 * f, 1), generator=gen, device=DEV) < 0.02)  # sums of a size for silu
+    gu = gu * 2.0 ** -7
+    dn = torch.cat([dn, torch.zeros((1, d - 300, f), dtype=dn.dtype, device=DEV)], dim=1)
+    codes, scale = ops.fp8_rows(rows, d)
+    ops.moe_quantize_rows_fp8(x, codes, scale)
+    gu8, dn8 = ops.fp8_weights(gu, swiglu=True), ops.fp8_weights(dn)
+
+    def run(a, b):
+        y = torch.empty((b - a, d), dtype=torch.bfloat16, device=DEV)
+        ws = ops.workspace(ops.moe_grouped_swiglu_gemm_fp8_workspace_size(1, b - a, b - a, d, f))
+        ops.moe_grouped_swiglu_gemm_fp8(1, b - a, b - a, d, f, codes[a:b].clone(), scale[a:b].clone(), dev([0, b - a], torch.int32),
+                                        *gu8, *dn8, y, ws)
+        return y
+    y = run(0, rows)
+    assert y.isfinite().all() and y[:, :300].abs().mean() > 0
+    for a in range(0, rows, 250):
+        part = run(a, min(a + 250, rows))
+        err = (y[a:a + 250].double() - part.double()).abs()
+        assert torch.all(err <= 2 * B * part.double().abs() + 1e-5 * part.double().abs().max()), a
+
+
 @pytest.mark.parametrize("counts", [[1, 0, 2] * 50, [40, 0, 1, 17] * 35, [0, 140, 3] * 30 + [300] * 12 + [0] * 64 + [5, 129]])
 def test_linear_of_many_groups(counts):
     say(f"linear, {len(counts)} groups, up to {max(counts)} rows")
