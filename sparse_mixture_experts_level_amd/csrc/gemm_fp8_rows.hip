@@ -1,11 +1,14 @@
-// Grouped products in 8 bits for groups of many rows (layouts in fp8.hpp), bound by the matrix cores.
+// Grouped products in 8 bits for groups of more than 16 rows (layouts in fp8.hpp).
 //
+// Many rows, bound by the matrix cores (4096 x 4096 x 14336: 177 us, 2.7 PFLOP/s beside packing; 8 x 1024 rows, 4096 x
+// 14336 gate_up 847 us, 2.3 PFLOP/s at the clock that this long a launch leaves; a tile's begin and end 10 us of its 53):
 // 256 rows x 256 weight rows a workgroup (for gate_up 128 columns of H: 16 gate and 16 up rows in turn), eight
 // waves of 128 x 64, 32x32x64 instructions with their operands' scales (the
 // blocks' scales cost nothing).  Both operands go from memory to LDS without registers, a step of 64 of K as
 // 1 KB pieces that are consecutive in memory and lie in LDS as the instruction reads them: for 16 rows, [4 chunks of
 // 16 codes][16 rows], so that sixteen lanes read 256 consecutive bytes.  The rows are copied into that
-// layout beforehand (fp8_pack_rows_kernel); H is written in it.  Four stages, three steps ahead; the
+// layout beforehand (fp8_pack_rows_kernel) or, for few column tiles, taken as they are, half a line at a time; H is written in
+// it.  Four stages, three steps ahead; the
 // two waves of each SIMD take turns, one computing while the other loads and reads
 // (the bf16 kernel's schedule for groups of many rows: the same bytes and cycles a step, twice the products).
 #include <algorithm>
@@ -144,6 +147,8 @@ __device__ __forceinline__ void part_of_k(const Fp8GemmArgs &a, const Fp8Tile &t
 // loads without registers put them as codes, a step of 128 of K a stage, in the operand layout (2 KB for 16 rows:
 // sixteen lanes read 256 consecutive bytes); four stages, three steps ahead, one barrier a step.  The 8-bit matrix
 // instruction: converted to bf16 by each wave, 128 rows took 1.7 us a step of the 1.2 that its weights take.
+// Bound by the weights' bytes: 32 x 80 rows, 7168 x 2048, gate_up 160 us (5.9 TB/s), down 104 (4.5, of 224 CUs; with
+// rows read again for each column tile 5.9 beyond L2); 32 x 4 rows both in 234 (6.0).
 constexpr int MD_R = 4, MD_D = 3, MD_ROWS = 128;
 
 // One block of n <= 16 MS rows from m0 on, column tiles nb0 .. nb1 - 1 one after the other without a pause of the loads: in a

@@ -258,6 +258,10 @@ struct Fp8GemmArgs {
 // A group of many rows is cut into the least number of tiles of at most kFp8LargeRows, equal but for whole 32s: the
 // matrix instructions of 32 rows past a tile's end are left out, so that a group of 1040 rows costs five tiles of
 // 224 and less (the last has 144), not four of 256 and a nearly empty one.
+// Groups of few rows are those that one pass of the weights serves (us in the kernel for few and in tiles of 256: 32 x 24
+// rows x 4096 x 4096 96 and 132, 32 x 128 117 and 154, 8 x 128 x 2048 x 7168 46.7 and 48.1); calls for groups of at most
+// 16 go without LDS (FFN of 32 x 2 rows x 2880 x 2880 149 and, through LDS, 163; but 32 x 16 x 7168 x 2048 275 and 242: it is for
+// decoding, where most groups have fewer rows than announced, and multiplies exactly).
 constexpr int kFp8LargeRows = 256, kFp8FewRows = 128, kFp8SmallRows = 16;
 __host__ __device__ inline int fp8_large_tiles(int rows) {
   return rows <= kFp8FewRows ? 0 : (rows + kFp8LargeRows - 1) / kFp8LargeRows;

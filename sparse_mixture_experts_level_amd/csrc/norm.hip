@@ -5,7 +5,8 @@
 //   dx = dh + rstd (g - xhat mean(g xhat)),  g = dy w, xhat = h rstd;  dw = sum_t dy xhat
 //
 // Memory bound: a row is read once into registers, as vectors of eight values a thread, and
-// written once.
+// written once.  16384 x 7168 of bf16 with residual, y and codes 189 us (5.6 TB/s beyond L2, a copy's rate 4.9 over more
+// bytes), backward of 4096 x 4096 28 us (5.2) and 5 for dweight.
 #include <algorithm>
 
 #include "fp8.hpp"

@@ -1,6 +1,7 @@
 // Rows and weights between bf16 or float and 8 bits with scales (layouts in fp8.hpp).
 //
-// Memory bound, and off the path of a forward pass but for the rows: x is quantised once for all experts.
+// Memory bound, and off the path of a forward pass but for the rows: x is quantised once for all experts.  16384 x 7168 of bf16
+// 60 us (5.9 TB/s), weights of 32 x 5760 x 2880 from bf16 288 us (5.5).
 #include "fp8.hpp"
 #include "kernels.hpp"
 
