@@ -52,8 +52,9 @@ __device__ __forceinline__ Fp8Tile find_tile(const Fp8GemmArgs &a, int tiles_max
   t.tiles = min(__builtin_amdgcn_readfirstlane(t.tiles), tiles_max);
   all = __builtin_amdgcn_readfirstlane(all);
   int chunks = per_tile, columns = 1;
-  if (spread && a.few_blocks && all > 0) {
-    columns = (per_tile + max(1, a.few_blocks / all) - 1) / max(1, a.few_blocks / all);
+  if (spread && a.few_chunks && all > 0) {  // more, where fewer groups than there can be leave CUs idle
+    chunks = min(per_tile, max(a.few_chunks, 256 / all));
+    columns = (per_tile + chunks - 1) / chunks;
     chunks = (per_tile + columns - 1) / columns;
   }
   const int large = t.tiles * per_tile;
@@ -762,21 +763,19 @@ hipError_t launch_fp8_pack_rows(const Fp8GemmArgs &a, uint8_t *xp, uint8_t *xp_s
   return hipGetLastError();
 }
 
-// Blocks for the groups of few rows, each a range of a group's column tiles: as many whole rounds of 256 as cost least,
-// counted for as many groups as there can be, in steps of 128 of K, of which a block's begin and end take eight (10 us); a
-// tenth has to be won.  32 x 80 rows, 7168 x 2048, 28 tiles of 16 steps: 896 blocks 115 us, 224 of four tiles 104; 4096 x
-// 7168, 16 tiles of 56 steps: 512 and 256 blocks 162.5 us, 4096 x 14336: 355 and 376.  0: a block for each tile.
-static int few_blocks(int groups, int n_tiles, int k) {
-  const int64_t steps = fp8_scale_bytes(k), all = (int64_t)groups * n_tiles;
-  int64_t least = (all + 255) / 256 * (steps + 8) * 9 / 10;
+// Ranges of column tiles, a block each, for the groups of few rows: of as many tiles, up to 64 steps of 128 of K, as cost least
+// in rounds of 256 blocks for as many groups as there can be, counted in steps, of which a block's begin and end take
+// eight (10 us); a tenth has to be won.  Longer ones end unevenly.  us with 1, 2, 4, 7 and all tiles a block: 212 of 256
+// groups of up to 80 rows, 7168 x 2048, 28 tiles of 16 steps, 580, -, 552, 593, 692; 2048 gate_up, 16 of 56 steps, 927, 972,
+// 1017, -, 1069; 32 x 80 rows, 28 of 16 steps, 115 and, with four, 104.  0: a block for each tile.
+static int few_chunks(int groups, int n_tiles, int k) {
+  const int64_t steps = fp8_scale_bytes(k);
+  int64_t least = ((int64_t)groups * n_tiles + 255) / 256 * (steps + 8) * 9 / 10;
   int best = 0;
-  for (int target = 256; target <= 2048 && target < all; target += 256) {
-    if (groups > target) continue;
-    const int columns = (n_tiles + target / groups - 1) / (target / groups);
-    const int64_t blocks = (int64_t)groups * ((n_tiles + columns - 1) / columns);
-    const int64_t cost = (blocks + 255) / 256 * (columns * steps + 8);
+  for (int columns = 2; columns <= n_tiles && columns * steps <= 64; ++columns) {
+    const int64_t chunks = (n_tiles + columns - 1) / columns, cost = (groups * chunks + 255) / 256 * (columns * steps + 8);
     if (cost < least) {
-      best = target;
+      best = (int)chunks;
       least = cost;
     }
   }
@@ -789,8 +788,9 @@ hipError_t launch_fp8_gemm_rows(const Fp8GemmArgs &call, hipStream_t s) {
   const int n_tiles = (a.n_out + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256);
   const int64_t tiles = a.large ? fp8_large_tiles_max(a.rows_max, a.num_groups) : 0;
   const int groups = std::min(a.num_groups, a.rows_max);
-  a.few_blocks = a.parts_cap > 1 ? 0 : few_blocks(groups, n_tiles, a.K);
-  const int64_t blocks = tiles * n_tiles + (a.few_blocks ? std::max(a.few_blocks, groups) : (int64_t)groups * n_tiles);
+  a.few_chunks = a.parts_cap > 1 ? 0 : few_chunks(groups, n_tiles, a.K);
+  const int64_t blocks =
+      tiles * n_tiles + (a.few_chunks ? std::max<int64_t>((int64_t)groups * a.few_chunks, 256) : (int64_t)groups * n_tiles);
   // parts are one round at most
   const int64_t grid = a.rounds ? blocks + 256 : a.parts_cap > 1 ? std::max<int64_t>(blocks, 256) : blocks;
   if (grid > 0x7fffffff) return hipErrorInvalidValue;

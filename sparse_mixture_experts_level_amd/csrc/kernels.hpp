@@ -248,7 +248,7 @@ struct Fp8GemmArgs {
   float *parts;
   int parts_cap;
   bool rounds;  // or, of the tiles of many rows, those past the last whole 256, in [256 parts' tiles][256][256]
-  int few_blocks;  // of the groups of up to kFp8FewRows, set by the launch; 0: one for each column tile
+  int few_chunks;  // blocks of a group of up to kFp8FewRows, set by the launch; 0: one for each column tile
   // Groups of more than kFp8FewRows go in tiles of up to 256 rows (large: a group can have that many); their rows are read
   // from xp, packed tiles of fp8_packed_bytes(), or, NULL, as they are; H goes to packed tiles.
   bool large;
