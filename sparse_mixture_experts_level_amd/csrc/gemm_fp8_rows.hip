@@ -789,8 +789,9 @@ hipError_t launch_fp8_gemm_rows(const Fp8GemmArgs &call, hipStream_t s) {
   const int64_t tiles = a.large ? fp8_large_tiles_max(a.rows_max, a.num_groups) : 0;
   const int groups = std::min(a.num_groups, a.rows_max);
   a.few_chunks = a.parts_cap > 1 ? 0 : few_chunks(groups, n_tiles, a.K);
-  const int64_t blocks =
-      tiles * n_tiles + (a.few_chunks ? std::max<int64_t>((int64_t)groups * a.few_chunks, 256) : (int64_t)groups * n_tiles);
+  // A group has one tile, few rows or many, and one more for each further 256 rows; in ranges, as many as there can be of each.
+  const int64_t blocks = a.few_chunks ? tiles * n_tiles + std::max<int64_t>((int64_t)groups * a.few_chunks, 256)
+                                      : (groups + (a.large ? a.rows_max / kFp8LargeRows : 0)) * (int64_t)n_tiles;
   // parts are one round at most
   const int64_t grid = a.rounds ? blocks + 256 : a.parts_cap > 1 ? std::max<int64_t>(blocks, 256) : blocks;
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
