@@ -680,8 +680,8 @@ moe_status moe_rms_norm_backward(int32_t num_tokens, int32_t d_model, int32_t dt
  *   num_groups, rows_max, group_rows_max  as for moe_grouped_swiglu_gemm; rows_max <= INT32_MAX
  *   x8, x_scale     rows in 8 bits: rows_max of them, or x_row_count, which must be below 2 GiB
  *   group_offsets   [G+1] int32 DEVICE array, non-decreasing within [0, rows_max] (entries
- *                   outside count as its ends; where they fall nothing else is touched, but rows may be
- *                   left out)
+ *                   outside count as its ends; where they fall nothing else is touched, but the rows' results
+ *                   are not defined)
  *   w8, w_scale     from moe_quantize_weights_fp8
  *   y_rows          [rows_max, n_out] bf16, written for rows inside a group, others left as they are
  *   ws              at least the bytes of the helper beside (0: invalid arguments)

@@ -24,7 +24,8 @@ constexpr int LG_TILE = kFp8LargeRows * 64;  // bytes of an operand's stage: 256
 
 // Block `block` of a launch of per_tile column tiles: the tiles of the groups of many rows, group after group, a block for
 // each column tile; then the groups of few (any number of rows where none is announced to have many), a block for each of
-// `chunks` ranges of column tiles; all of them, or those past the last whole 256, again for each further part of K.  One pass over the offsets, two for more than 64 groups; all results in scalar registers.
+// `chunks` ranges of column tiles; all of them, or those past the last whole 256, again for each further part of K.  One
+// pass over the offsets, two for more than 64 groups; all results in scalar registers.
 struct Fp8Tile {
   int g, begin, end;  // -1: there is no such tile
   int first, count;   // the group's tiles, numbered over all groups (count 0: few rows)
