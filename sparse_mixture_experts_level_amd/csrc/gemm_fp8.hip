@@ -51,7 +51,8 @@ __global__ __launch_bounds__(64 * U * KS, 4) void fp8_small_kernel(const Fp8Gemm
   const int tw0 = unit * NB < blocks ? te : 0, tw1 = unit * NB + 1 < blocks ? te : 0;  // no weights past the last block
   const int sblocks = fp8_blocks(a.n_out);
   const uint8_t *wscale = a.w_scale + ((int64_t)g * sblocks + min(unit * NB / NS / 8, sblocks - 1)) * NS * ks;
-  for (int m0 = begin; m0 < end; m0 += 16) {
+  for (int left = end - begin; left > 0; left -= 16) {  // (m0 + 16 may pass 2^31)
+    const int m0 = end - left, n = min(16, left);
     u32x4 w[R][NB][2], x[XR][2];
     uint32_t sx, nx, sw[NS], nw[NS];
     auto load_w = [&](int j, int t) {  // steps past the part's end read zeros
@@ -65,8 +66,8 @@ __global__ __launch_bounds__(64 * U * KS, 4) void fp8_small_kernel(const Fp8Gemm
     };
 #pragma unroll
     for (int j = 0; j < R; ++j) load_w(j, tb + j);
-    const Fp8Rows rows(a, m0, min(16, end - m0));
-    const uint32_t src = rows.row(a, m0, lr, min(16, end - m0));
+    const Fp8Rows rows(a, m0, n);
+    const uint32_t src = rows.row(a, m0, lr, n);
     const uint32_t xoff = src != kOob ? src * (uint32_t)kp + (uint32_t)lg * 16u : kOob;
     const uint32_t soff = src != kOob ? src * (uint32_t)ks : kOob;
     auto load_x = [&](int j, int t) {
@@ -130,7 +131,7 @@ __global__ __launch_bounds__(64 * U * KS, 4) void fp8_small_kernel(const Fp8Gemm
           for (int b = 0; b < NB; ++b) acc[b] += parts[(((p - 1) * U + u) * NB + b) * 64 + lane];
     }
     const int col = unit * 16 * NB / NS + lg * 4;
-    const int64_t row = m0 + lr;
+    const int64_t row = (int64_t)m0 + lr;
     if constexpr (SWIGLU) {
       float h[4], top = 0.0f;
       if (part == 0) {
@@ -144,12 +145,12 @@ __global__ __launch_bounds__(64 * U * KS, 4) void fp8_small_kernel(const Fp8Gemm
         if (lg == 0) tops[u][lr] = top;
       }
       __syncthreads();
-      if (part == 0 && row < end) {
+      if (part == 0 && lr < n) {
 #pragma unroll
         for (int v = 0; v < 8; ++v) top = fmaxf(top, tops[v][lr]);
         store_h(a, h, top, row, nb, col, u == 0 && lg == 0);
       }
-    } else if (part == 0 && row < end) {
+    } else if (part == 0 && lr < n) {
 #pragma unroll
       for (int b = 0; b < NB; ++b) store_y(a, acc[b], row, col + b * 16);
     }

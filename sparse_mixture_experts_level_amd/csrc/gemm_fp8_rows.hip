@@ -46,11 +46,12 @@ __device__ __forceinline__ Fp8Tile find_tile(const Fp8GemmArgs &a, int tiles_max
   for (int g0 = 0; g0 < G; g0 += 64) {
     b = e = 0;
     if (g0 + lane < G) fp8_group_rows(a, g0 + lane, b, e);
-    t.tiles += group_reduce<64>(a.large ? fp8_large_tiles(e - b) : 0, [](int x, int y) { return x + y; });
+    // (offsets that decrease could count rows twice: no tile past those that the packed copies have room for, nor a sum of
+    // 1024 groups past 2^31)
+    t.tiles = min(t.tiles + group_reduce<64>(a.large ? fp8_large_tiles(e - b) : 0, [](int x, int y) { return x + y; }), tiles_max);
     all += __popcll(__ballot(e > b && e - b <= few));
   }
-  // (offsets that decrease could count rows twice: no tile past those that the packed copies have room for)
-  t.tiles = min(__builtin_amdgcn_readfirstlane(t.tiles), tiles_max);
+  t.tiles = __builtin_amdgcn_readfirstlane(t.tiles);
   all = __builtin_amdgcn_readfirstlane(all);
   int chunks = per_tile, columns = 1;
   if (spread && a.few_chunks && all > 0) {  // more, where fewer groups than there can be leave CUs idle
@@ -234,13 +235,13 @@ __device__ __forceinline__ void medium_rows(const Fp8GemmArgs &a, const Fp8Tile 
     asm volatile("" ::: "memory");
   };
   auto finish = [&](int nb) {
-    int first = m0;
-    asm volatile("" : "+s"(first));  // no rows' addresses kept in registers over the loop
+    int first = m0, some = n;
+    asm volatile("" : "+s"(first), "+s"(some));  // no rows' addresses, nor which there are, kept in registers over the loop
     if (tile.parts > 1) {
 #pragma unroll
       for (int i = 0; i < MS; ++i) {
-        const int64_t row = first + i * 16 + lr;
-        if (row < first + n)
+        const int64_t row = (int64_t)first + i * 16 + lr;
+        if (i * 16 + lr < some)
 #pragma unroll
           for (int b = 0; b < 2; ++b)
             *reinterpret_cast<f32x4 *>(a.parts + (tile.part * (int64_t)a.rows_max + row) * n_tiles * 256 + nb * 256 +
@@ -266,15 +267,15 @@ __device__ __forceinline__ void medium_rows(const Fp8GemmArgs &a, const Fp8Tile 
         float top = 0.0f;
 #pragma unroll
         for (int v = 0; v < 8; ++v) top = fmaxf(top, tops[v][i * 16 + lr]);
-        const int64_t row = first + i * 16 + lr;
+        const int64_t row = (int64_t)first + i * 16 + lr;
         const float h[4] = {acc[i][0][0], acc[i][0][1], acc[i][0][2], acc[i][0][3]};
-        if (row < first + n) store_h(a, h, top, row, nb, col, wave == 0 && lg == 0);
+        if (i * 16 + lr < some) store_h(a, h, top, row, nb, col, wave == 0 && lg == 0);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < MS; ++i) {
-        const int64_t row = first + i * 16 + lr;
-        if (row < first + n)
+        const int64_t row = (int64_t)first + i * 16 + lr;
+        if (i * 16 + lr < some)
 #pragma unroll
           for (int b = 0; b < 2; ++b) store_y(a, acc[i][b], row, (nb * 16 + wave * 2 + b) * 16 + lg * 4);
       }
@@ -365,12 +366,12 @@ __global__ __launch_bounds__(512, 1) void fp8_rows_kernel(const Fp8GemmArgs a, i
   auto bufB = [&](int b) -> uint8_t * { return b == 0 ? sB0 : b == 1 ? sB1 : b == 2 ? sB2 : sB3; };
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / 4, wn = wave % 4, lr = lane & 31, lh = lane >> 5;
-  const Fp8Tile tile = find_tile(a, tiles_max, blockIdx.x, n_tiles, kProduct);
+  const Fp8Tile tile = find_tile(a, tiles_max, a.first_block + (int)blockIdx.x, n_tiles, kProduct);
   if (tile.g < 0) return;
   const int g = tile.g, begin = tile.begin, end = tile.end, mt_first = tile.first, mt_count = tile.count;
   if (mt_count == 0) {
-    for (int m0 = begin; m0 < end; m0 += MD_ROWS) {
-      const int n = min(MD_ROWS, end - m0);
+    for (int left = end - begin; left > 0; left -= MD_ROWS) {  // (m0 + MD_ROWS may pass 2^31)
+      const int m0 = end - left, n = min(MD_ROWS, left);
       switch ((n + 15) / 16) {
 #define MOE_ROWS(MS)                                                                       \
   case MS:                                                                                 \
@@ -757,7 +758,7 @@ __global__ __launch_bounds__(256) void fp8_pack_rows_kernel(const Fp8GemmArgs a,
 hipError_t launch_fp8_pack_rows(const Fp8GemmArgs &a, uint8_t *xp, uint8_t *xp_scale, hipStream_t s) {
   const int64_t tiles = fp8_large_tiles_max(a.rows_max, a.num_groups);
   const int quads = fp8_scale_bytes(a.K) / 4;
-  if (tiles > 0x7fffffff / 4 || quads > 65535) return hipErrorInvalidValue;
+  if (tiles >= (1 << 22) || quads > 65535) return hipErrorInvalidValue;  // 2^32 threads
   if (tiles > 0)
     hipLaunchKernelGGL(fp8_pack_rows_kernel, dim3((unsigned)tiles * (kFp8LargeRows / 64), (unsigned)quads), dim3(256), 0, s, a,
                        xp, xp_scale, (int)tiles);
@@ -796,10 +797,15 @@ hipError_t launch_fp8_gemm_rows(const Fp8GemmArgs &call, hipStream_t s) {
   // parts are one round at most
   const int64_t grid = a.rounds ? blocks + 256 : a.parts_cap > 1 ? std::max<int64_t>(blocks, 256) : blocks;
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  if (swiglu)
-    hipLaunchKernelGGL((fp8_rows_kernel<true>), dim3((unsigned)grid), dim3(512), 0, s, a, n_tiles, (int)tiles);
-  else
-    hipLaunchKernelGGL((fp8_rows_kernel<false>), dim3((unsigned)grid), dim3(512), 0, s, a, n_tiles, (int)tiles);
+  constexpr int64_t kBlocks = 1 << 22;  // a launch: its threads are counted in 32 bits
+  for (int64_t first = 0; first < grid; first += kBlocks) {
+    a.first_block = (int)first;
+    const dim3 some((unsigned)std::min(kBlocks, grid - first));
+    if (swiglu)
+      hipLaunchKernelGGL((fp8_rows_kernel<true>), some, dim3(512), 0, s, a, n_tiles, (int)tiles);
+    else
+      hipLaunchKernelGGL((fp8_rows_kernel<false>), some, dim3(512), 0, s, a, n_tiles, (int)tiles);
+  }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || (a.parts_cap == 1 && !a.rounds)) return e;
   const dim3 adding((unsigned)std::min<int64_t>(blocks, 128), 16);  // tiles that are cut: half a round at most

@@ -249,6 +249,7 @@ struct Fp8GemmArgs {
   int parts_cap;
   bool rounds;  // or, of the tiles of many rows, those past the last whole 256, in [256 parts' tiles][256][256]
   int few_chunks;  // blocks of a group of up to kFp8FewRows, set by the launch; 0: one for each column tile
+  int first_block;  // of this launch, where the blocks of a product are more than one takes
   // Groups of more than kFp8FewRows go in tiles of up to 256 rows (large: a group can have that many); their rows are read
   // from xp, packed tiles of fp8_packed_bytes(), or, NULL, as they are; H goes to packed tiles.
   bool large;
@@ -264,9 +265,11 @@ struct Fp8GemmArgs {
 // decoding, where most groups have fewer rows than announced, and multiplies exactly).
 constexpr int kFp8LargeRows = 256, kFp8FewRows = 128, kFp8SmallRows = 16;
 __host__ __device__ inline int fp8_large_tiles(int rows) {
-  return rows <= kFp8FewRows ? 0 : (rows + kFp8LargeRows - 1) / kFp8LargeRows;
+  return rows <= kFp8FewRows ? 0 : rows / kFp8LargeRows + (rows % kFp8LargeRows != 0);
 }
-__host__ __device__ inline int fp8_tile_rows(int rows, int tiles) { return (rows + 32 * tiles - 1) / (32 * tiles) * 32; }
+__host__ __device__ inline int fp8_tile_rows(int rows, int tiles) {  // (unsigned: up to 2^31 and an eighth of it)
+  return (int)(((uint32_t)rows + 32u * tiles - 1u) / (32u * tiles) * 32u);
+}
 // A bound on the tiles of rows in all G groups: a last one each beside whole ones, and two of 257 rows are the most for
 // their number.  (Workgroups past the real tiles only leave, but each holds a CU until it has read the offsets.)
 inline int64_t fp8_large_tiles_max(int64_t rows, int G) {

@@ -3,6 +3,8 @@ differentiation, differences, hand-worked layouts), and the argument checks of t
 which return before any device work."""
 import ctypes
 import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -295,3 +297,33 @@ def test_binding_refuses_other_shapes_types_and_devices():
         ops.fp8_weights(torch.zeros((1, 3, 64), dtype=torch.bfloat16), swiglu=True)
     with pytest.raises(ValueError, match="contiguous"):
         ops.moe_rms_norm(torch.zeros((64, 4), dtype=torch.bfloat16).t(), w, 1e-6)
+
+
+# ------------------------------------------------------------------------------ tiles of rows, compiled for the host
+
+def _host_program(tmp_path, body):
+    """What a program prints that includes the launchers' header, compiled by the host's compiler (signed sums wrap)."""
+    gxx = shutil.which("g++")
+    if gxx is None or not os.path.isdir("/opt/rocm/include/hip"):
+        pytest.skip("needs g++ and HIP's headers")
+    src, exe = tmp_path / "t.cpp", tmp_path / "t"
+    src.write_text('#include "kernels.hpp"\n#include <cstdio>\nusing namespace moe;\nint main() {\n' + body + "\n}\n")
+    csrc = os.path.join(os.path.dirname(ops.__file__), "csrc")
+    subprocess.run([gxx, "-std=c++17", "-O1", "-fwrapv", "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include", "-I" + csrc, str(src),
+                    "-o", str(exe)], check=True)
+    return [[int(v) for v in line.split()] for line in
+            subprocess.run([str(exe)], check=True, capture_output=True, text=True, timeout=60).stdout.splitlines()]
+
+
+def test_tiles_of_groups_up_to_the_most_rows(tmp_path):
+    """Of a group past 128 rows: the least number of tiles of 256, equal but for whole 32s, none of them empty."""
+    rows = [0, 1, 128, 129, 256, 257, 300, 1040, 1537, 2 ** 20 + 1, 2 ** 30 - 1, 2 ** 30, 1_900_000_001, 1_950_000_000,
+            2 ** 31 - 257, 2 ** 31 - 256, 2 ** 31 - 255, 2 ** 31 - 1]
+    body = "".join(f"{{ int t = fp8_large_tiles({r}); std::printf(\"%d %d %d\\n\", {r}, t, t > 0 ? fp8_tile_rows({r}, t) : 0); }}\n"
+                   for r in rows)
+    got = _host_program(tmp_path, body)
+    assert [g[0] for g in got] == rows
+    for r, tiles, per in got:
+        assert tiles == (0 if r <= 128 else -(-r // 256)), r
+        if tiles:
+            assert per % 32 == 0 and 0 < per <= 256 and (tiles - 1) * per < r <= tiles * per, (r, tiles, per)
