@@ -686,7 +686,9 @@ moe_status moe_rms_norm_backward(int32_t num_tokens, int32_t d_model, int32_t dt
  *   y_rows          [rows_max, n_out] bf16, written for rows inside a group, others left as they are
  *   ws              at least the bytes of the helper beside (0: invalid arguments)
  * Any n_out, d, f, K >= 1.  A NaN in a row makes that row NaN, one in a weight that output column.  Calls
- * for groups of at most 16 rows (rows_max or group_rows_max) multiply in bf16, exactly; others on the 8-bit matrix
+ * for groups of at most 16 rows (rows_max or group_rows_max) multiply in bf16, exactly wherever the scales of a row's block
+ * and of a weights' block together are from 2^-121 to 2^119 (past that a result may be NaN, below it products under
+ * 2^-103 lose bits); others on the 8-bit matrix
  * instruction, which drops, of 16 products at a time, what lies some 2^-14 below the largest: about 1.5e-5 of
  * a result's size, a hundredth of its bf16 rounding.  Calls of few tiles are cut along K, into parts
  * whose sums are kept in ws and added in order.  Only kernel

@@ -194,7 +194,9 @@ __device__ __forceinline__ f32x4 mfma_fp8_16(i32x8 a, i32x8 b, f32x4 c, uint32_t
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, J, (int)sa, J, (int)sb);
 }
 
-// Eight codes as bf16, times 2^(e) for a scale 2^e given as a float: exact (bf16 has a float's exponents).
+// Eight codes as bf16, times 2^e for a scale given as a float, of which the instruction takes the exponent field f alone: e is
+// f - 127, 0 (e = -127) and 254 too, and 255 makes every value NaN.  Exact for f from 3 to 246: below, codes of 2^-9 and up fall
+// under bf16's least step of 2^-133; above, those up to 448 pass its range and become infinite.
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ u32x4 fp8_to_bf16(uint32_t lo, uint32_t hi, float scale) {
   return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false)),
@@ -202,10 +204,20 @@ __device__ __forceinline__ u32x4 fp8_to_bf16(uint32_t lo, uint32_t hi, float sca
                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false)),
                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true))};
 }
-// Byte J of four blocks' scales as the float 2^(byte - 127).
+// Such fields, as floats, for products of a row's block and of one or two weight blocks (`w0`, `w1`) whose scale bytes are
+// byte J of those given: the weights' exponents less `shift`, the row's that much more.  The row's byte may be any, and
+// no shift of its own is possible (a weight meets all rows), so that up to 8 of the weights' exponent, towards zero, goes to
+// the rows: with it both factors are in the conversion's exact range wherever row's and weights' exponents together are from -121
+// to 119 (checked for all bytes).  Past 119 a field of 255 gives NaN; below, products of less than 2^-103 lose bits.
 template <int J>
-__device__ __forceinline__ float fp8_scale(uint32_t four) {
-  return __uint_as_float(((four >> (8 * J)) & 0xffu) << 23);
+__device__ __forceinline__ int fp8_shift(uint32_t w0, uint32_t w1) {
+  const int a = (int)(w0 >> (8 * J) & 0xffu) - 127, b = (int)(w1 >> (8 * J) & 0xffu) - 127;
+  return min(min(max(max(a, b), -8), 8), min(a, b) + 121);
+}
+template <int J>
+__device__ __forceinline__ float fp8_shifted(uint32_t four, int by) {
+  const int byte = (int)(four >> (8 * J) & 0xffu);
+  return __uint_as_float((uint32_t)(byte == 255 ? 255 : min(max(byte + by, 0), 255)) << 23);
 }
 
 }  // namespace moe

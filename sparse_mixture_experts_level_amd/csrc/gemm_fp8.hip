@@ -102,12 +102,17 @@ __global__ __launch_bounds__(64 * U * KS, 4) void fp8_small_kernel(const Fp8Gemm
           for (int b = 0; b < NS; ++b) sw[b] = nw[b] & keep;
           load_scales(t + 4);
         }
+        const int shift = fp8_shift<J>(sw[0], sw[NS - 1]);
+        const float fx = fp8_shifted<J>(sx, shift);
+        float fw[NS];
+#pragma unroll
+        for (int b = 0; b < NS; ++b) fw[b] = fp8_shifted<J>(sw[b], -shift);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {  // 32 of K: eight of each lane's 32 codes
-          const u32x4 xb = fp8_to_bf16(x[J % XR][m / 2][2 * (m % 2)], x[J % XR][m / 2][2 * (m % 2) + 1], fp8_scale<J>(sx));
+          const u32x4 xb = fp8_to_bf16(x[J % XR][m / 2][2 * (m % 2)], x[J % XR][m / 2][2 * (m % 2) + 1], fx);
 #pragma unroll
           for (int b = 0; b < NB; ++b)
-            acc[b] = mfma16(fp8_to_bf16(w[J % R][b][m / 2][2 * (m % 2)], w[J % R][b][m / 2][2 * (m % 2) + 1], fp8_scale<J>(sw[b % NS])), xb,
+            acc[b] = mfma16(fp8_to_bf16(w[J % R][b][m / 2][2 * (m % 2)], w[J % R][b][m / 2][2 * (m % 2) + 1], fw[b % NS]), xb,
                             acc[b]);
         }
         __builtin_amdgcn_sched_barrier(0);  // loads into registers still in use would get others, copied after a wait

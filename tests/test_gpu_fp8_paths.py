@@ -1,7 +1,9 @@
-"""GPU tests of what holds on every path of the products in 8 bits (which one a call takes follows its sizes).
+"""GPU tests of what holds on every path of the products in 8 bits (which one a call takes follows its sizes): scale bytes
+from 0 to 255, rows up to the last.
 
 Values are whole numbers by powers of two, whose products and sums are exact in the instruction and in floats (below 2^24
 steps), so results EQUAL the rounded reference's, formed in 64 bits on the GPU."""
+import numpy as np
 import pytest
 import torch
 
@@ -10,6 +12,114 @@ from tests.moe_testlib import say
 pytestmark = pytest.mark.gpu
 ops = pytest.importorskip("sparse_mixture_experts_level_amd.ops")
 DEV = "cuda"
+
+# rows of each group, n_out, K, announced rows (None: the largest group)
+PATHS = {
+    "up to 16 rows, in parts of K": ([5, 3], 140, 700, None),
+    "up to 16 rows": ([5], 8200, 200, None),
+    "up to 16 rows, two blocks a wave": ([5, 0, 16, 1], 8200, 200, None),
+    "up to 128 rows": ([20, 70], 300, 200, None),
+    "up to 128 rows, announced as few": ([20, 70], 300, 200, 16),
+    "up to 128 rows, cut along K": ([20, 70], 300, 2700, None),
+    "up to 128 rows, several column tiles": ([20, 0, 3] * 30, 1100, 130, None),
+    "many rows as they are": ([300, 20], 272, 520, None),
+    "many rows, packed": ([300], 2200, 520, None),
+    "many rows, cut along K": ([300, 20], 257, 2700, None),
+    "many rows, packed, cut along K": ([150], 2200, 4200, None),
+    "many rows, the last round cut": ([5000], 3300, 7300, None),
+}
+
+
+def _draw(gen, *shape):
+    """Codes' values -4, -2, -1, 0, 1, 2, 4, whose products with each other span 2^4."""
+    v = torch.randint(-4, 5, shape, generator=gen, device=DEV)
+    return torch.where(v.abs() == 3, 4 * v.sign(), v).float()
+
+
+class Case:
+    """A grouped product of drawn codes: codes and scales of rows and weights, made by the library from whole numbers whose
+    blocks all have 4 as their largest, so that every scale byte is 121 (4 = 256 2^-6)."""
+
+    def __init__(self, name, seed=0):
+        self.counts, self.n, self.k, hint = PATHS[name]
+        self.hint = hint or max(self.counts)
+        say(f"path: {name}")
+        gen = torch.Generator(device=DEV).manual_seed(seed)
+        self.G, self.rows = len(self.counts), sum(self.counts)
+        self.off = np.concatenate([[0], np.cumsum(self.counts)])
+        self.x, self.w = _draw(gen, self.rows, self.k), _draw(gen, self.G, self.n, self.k)
+        self.x[:, ::128] = 4
+        self.w[:, ::128, ::128] = 4
+        self.quantize()
+
+    def quantize(self):
+        self.codes, self.scale = ops.fp8_rows(self.rows, self.k)
+        ops.moe_quantize_rows_fp8(self.x, self.codes, self.scale)
+        self.w8, self.w_scale = ops.fp8_weights(self.w)
+        self.kb, self.nb = -(-self.k // 128), -(-self.n // 128)
+        self.ws8 = self.w_scale.view(self.G, self.nb, -1)
+
+    def run(self):
+        y = torch.full((self.rows, self.n), 3.0, dtype=torch.bfloat16, device=DEV)
+        need = ops.moe_grouped_linear_fp8_workspace_size(self.G, self.rows, self.hint, self.n, self.k)
+        ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
+        ops.moe_grouped_linear_fp8(self.G, self.rows, self.hint, self.n, self.k, self.codes, self.scale,
+                                   torch.tensor(self.off, dtype=torch.int32, device=DEV), self.w8, self.w_scale, y, ws)
+        return y
+
+    def want(self, times=1.0):
+        y = torch.empty((self.rows, self.n), dtype=torch.float64, device=DEV)
+        for g in range(self.G):
+            a, b = self.off[g], self.off[g + 1]
+            y[a:b] = self.x[a:b].double() @ self.w[g].double().T
+        return (y * times).float().bfloat16()
+
+
+@pytest.mark.parametrize("name", PATHS)
+@pytest.mark.parametrize("total", [250, 254])
+def test_scale_bytes_at_both_ends(name, total):
+    """A product's scale is 2^(row's byte + weight's byte - 254), whatever the two are: pairs of the same total, one a block of
+    K, give what 2^(total - 242) times the product of bytes 121 and 121 is."""
+    c = Case(name)
+    assert torch.all(c.scale[:, :c.kb] == 121) and torch.all(c.ws8[:, :, :c.kb] == 121)
+    pairs = [p for p in ((0, 250), (250, 0), (1, 249), (125, 125), (247, 3), (0, 254), (254, 0), (127, 127)) if sum(p) == total]
+    for b in range(c.kb):
+        c.scale[:, b], c.ws8[:, :, b] = pairs[b % len(pairs)]
+    assert torch.equal(c.run(), c.want(2.0 ** (total - 242)))
+    for b in range(c.kb):  # and the other way round
+        c.scale[:, b], c.ws8[:, :, b] = pairs[-1 - b % len(pairs)]
+    assert torch.equal(c.run(), c.want(2.0 ** (total - 242)))
+
+
+@pytest.mark.parametrize("name", PATHS)
+def test_least_codes_under_the_least_scale(name):
+    """Rows of the codes 1 to 7 (2^-9 and up) under the bytes 0 to 3: below what bf16 can hold, beside weights of 2^120."""
+    c = Case(name, 1)
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    m = torch.randint(1, 8, (c.rows, c.k), generator=gen, device=DEV)
+    c.codes[:, :c.k] = m.to(torch.uint8)
+    for b in range(c.kb):
+        c.scale[:, b], c.ws8[:, :, b] = b % 4, 247 - b % 4
+    c.x = m.float()  # times 2^-9 2^(byte - 127); the weights' codes are 2^6 times their values
+    assert torch.equal(c.run(), c.want(2.0 ** (-9 + 6 + 247 - 254)))
+
+
+@pytest.mark.parametrize("name", PATHS)
+def test_scale_byte_255_is_nan(name):
+    """Of a row's block, that row; of a weights' block, its 128 columns of that group; nothing else."""
+    c = Case(name, 3)
+    good = c.want()
+    bad = torch.zeros_like(good, dtype=torch.bool)
+    for r in {0, c.rows // 2, c.rows - 1}:
+        c.scale[r, r % c.kb] = 255
+        bad[r] = True
+    g = int(np.argmax(c.counts))
+    j, b = c.nb - 1, c.kb - 1
+    c.ws8[g, j, b] = 255
+    bad[c.off[g]:c.off[g + 1], 128 * j:] = True
+    y = c.run()
+    assert torch.equal(y.isnan(), bad)
+    assert torch.equal(y[~bad], good[~bad])
 
 
 @pytest.mark.parametrize("hint,first", [(16, 2 ** 31 - 1 - 43), (128, 2 ** 31 - 1 - 300), (2 ** 31 - 1, 0)])
