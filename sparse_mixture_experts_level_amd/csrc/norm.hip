@@ -309,30 +309,31 @@ int backward_blocks(int T, int d) {
 }  // namespace
 
 hipError_t launch_rms_norm(const NormCall &call, hipStream_t s) {
-  constexpr int64_t kRows = 1 << 22;  // a launch: the threads of one are counted in 32 bits
   const int64_t size = call.f32 ? 4 : 2, row_bytes = fp8_row_bytes(call.d), scale_bytes = fp8_scale_bytes(call.d);
-  for (int64_t first = 0; first < call.T; first += kRows) {
-    NormCall c = call;
-    auto from = [&](auto p, int64_t bytes) { return p ? (decltype(p))((uintptr_t)p + (size_t)(first * bytes)) : p; };
-    c.x = from(call.x, call.d * size);
-    c.residual = from(call.residual, call.d * size);
-    c.h = from(call.h, call.d * size);
-    c.y = from(call.y, call.d * size);
-    c.y8 = from(call.y8, row_bytes);
-    c.y_scale = from(call.y_scale, scale_bytes);
-    c.rstd = from(call.rstd, 4);
-    c.T = (int)std::min<int64_t>(kRows, call.T - first);
-    by_width<false>(c.d, [&](auto tpr, auto nv, auto whole) {
-      constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-      constexpr bool WHOLE = decltype(whole)::value;
-      constexpr int RPB = TPR >= 256 ? 1 : 256 / TPR;
-      const dim3 grid((unsigned)((c.T + RPB - 1) / RPB)), block(TPR > 256 ? TPR : 256);
+  by_width<false>(call.d, [&](auto tpr, auto nv, auto whole) {
+    constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+    constexpr bool WHOLE = decltype(whole)::value;
+    constexpr int RPB = TPR >= 256 ? 1 : 256 / TPR, THREADS = TPR > 256 ? TPR : 256;
+    constexpr int64_t kRows = TPR > 512 ? 1 << 21 : 1 << 22;  // a launch: the threads of one are counted in 32 bits
+    static_assert(kRows / RPB * THREADS <= UINT32_MAX, "threads of a launch");
+    for (int64_t first = 0; first < call.T; first += kRows) {
+      NormCall c = call;
+      auto from = [&](auto p, int64_t bytes) { return p ? (decltype(p))((uintptr_t)p + (size_t)(first * bytes)) : p; };
+      c.x = from(call.x, call.d * size);
+      c.residual = from(call.residual, call.d * size);
+      c.h = from(call.h, call.d * size);
+      c.y = from(call.y, call.d * size);
+      c.y8 = from(call.y8, row_bytes);
+      c.y_scale = from(call.y_scale, scale_bytes);
+      c.rstd = from(call.rstd, 4);
+      c.T = (int)std::min<int64_t>(kRows, call.T - first);
+      const dim3 grid((unsigned)((c.T + RPB - 1) / RPB)), block(THREADS);
       if (c.f32)
         hipLaunchKernelGGL((rms_norm_kernel<float, TPR, NV, WHOLE>), grid, block, 0, s, c);
       else
         hipLaunchKernelGGL((rms_norm_kernel<bf16_t, TPR, NV, WHOLE>), grid, block, 0, s, c);
-    });
-  }
+    }
+  });
   return hipGetLastError();
 }
 

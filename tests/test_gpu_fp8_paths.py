@@ -1,5 +1,5 @@
 """GPU tests of what holds on every path of the products in 8 bits (which one a call takes follows its sizes): scale bytes
-from 0 to 255, rows up to the last.
+from 0 to 255, rows up to the last; and of the norm's widest rows.
 
 Values are whole numbers by powers of two, whose products and sums are exact in the instruction and in floats (below 2^24
 steps), so results EQUAL the rounded reference's, formed in 64 bits on the GPU."""
@@ -153,3 +153,28 @@ def test_rows_up_to_the_last_that_32_bits_count(hint, first):
         assert torch.equal(y[a:b, 0], want), a
     del y, r, want
     torch.cuda.empty_cache()
+
+
+def test_norm_of_the_widest_rows_past_32_bits_of_threads():
+    """2^22 rows of more than 16384 values, in place: rows that are set, the first and last and some between, have what a small
+    call gives them; zeros stay zeros."""
+    T, d = 1 << 22, 16385
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < T * d * 2 + (4 << 30):
+        pytest.skip("needs 142 GB")
+    say("norm of 4194304 x 16385")
+    gen = torch.Generator(device=DEV).manual_seed(7)
+    at = torch.tensor([0, 1, 5000, T // 2 - 1, T // 2, T - 2, T - 1], device=DEV)
+    rows = torch.randn((len(at), d), generator=gen, device=DEV).bfloat16()
+    w = (1 + 0.2 * torch.randn(d, generator=gen, device=DEV)).bfloat16()
+    want, want_r = torch.empty_like(rows), torch.empty(len(at), device=DEV)
+    ops.moe_rms_norm(rows, w, 1e-6, y=want, rstd=want_r)
+    x, rstd = torch.zeros((T, d), dtype=torch.bfloat16, device=DEV), torch.zeros(T, device=DEV)
+    x[at] = rows
+    ops.moe_rms_norm(x, w, 1e-6, y=x, rstd=rstd)
+    got, got_r = x[at], rstd[at]
+    del x
+    torch.cuda.empty_cache()
+    assert torch.equal(got, want) and torch.equal(got_r, want_r)
+    rstd[at] = 1000.0
+    assert torch.all((rstd - 1000.0).abs() < 1e-2)
