@@ -1,5 +1,5 @@
 """GPU tests of what holds on every path of the products in 8 bits (which one a call takes follows its sizes): scale bytes
-from 0 to 255, rows up to the last; and of the norm's widest rows.
+from 0 to 255, rows up to the last, the FFN's error; and of the norm's widest rows.
 
 Values are whole numbers by powers of two, whose products and sums are exact in the instruction and in floats (below 2^24
 steps), so results EQUAL the rounded reference's, formed in 64 bits on the GPU."""
@@ -178,3 +178,45 @@ def test_norm_of_the_widest_rows_past_32_bits_of_threads():
     assert torch.equal(got, want) and torch.equal(got_r, want_r)
     rstd[at] = 1000.0
     assert torch.all((rstd - 1000.0).abs() < 1e-2)
+
+
+def _held(v, rows_a_block):
+    """v in 8 bits and back, in 64 bits: blocks of rows_a_block x 128, e4m3 codes rounded by torch (from floats: other than
+    from 64 bits for values within 2^-24 of a border)."""
+    n, k = v.shape
+    p = torch.nn.functional.pad(v, (0, -k % 128, 0, -n % rows_a_block))
+    p = p.view(-1, rows_a_block, p.shape[1] // 128, 128)
+    top = p.abs().amax((1, 3), keepdim=True)
+    e = torch.ceil(torch.log2(top / 448))
+    e = torch.where(top > 448 * 2.0 ** e, e + 1, e)
+    e = torch.where(top <= 448 * 2.0 ** (e - 1), e - 1, e)
+    e = torch.where(top == 0, 0.0, e)
+    q = (p / 2.0 ** e).float().to(torch.float8_e4m3fn).double() * 2.0 ** e
+    return q.view(-1, p.shape[2] * 128)[:n, :k]
+
+
+@pytest.mark.parametrize("rows,d,f", [(80, 2048, 1024), (300, 1024, 1100), (16, 2048, 1024)])
+def test_error_of_the_ffn_against_64_bits(rows, d, f):
+    """What the header says of the two forms.  The result's rounding alone is computed here.  Beyond it, exact products: H's
+    float sums and silu are off by some 1.5e-6 of H's size, so codes move with probability 2 * 1.5e-6 / 2^-4 = 5e-5, by 2^-3 at
+    most: 2^-3 sqrt(5e-5) = 9e-4 of the norm.  On the 8-bit instruction 1.5e-5, hence 5e-4 and 2.8e-3, and the projection's
+    own 1.5e-5.  Any number of rows is exact where 16 are announced."""
+    say(f"error of the ffn, {rows} rows, {d} x {f}")
+    gen = torch.Generator(device=DEV).manual_seed(rows)
+    x = torch.randn((rows, d), generator=gen, device=DEV).bfloat16()
+    gu = (torch.randn((1, 2 * f, d), generator=gen, device=DEV) / d ** 0.5).bfloat16()
+    dn = (torch.randn((1, d, f), generator=gen, device=DEV) / f ** 0.5).bfloat16()
+    xv, g, u = _held(x.double(), 1), _held(gu[0, :f].double(), 128), _held(gu[0, f:].double(), 128)
+    a, b = xv @ g.T, xv @ u.T
+    want = _held(a / (1 + torch.exp(-a)) * b, 1) @ _held(dn[0].double(), 128).T
+    rounding = ((want.float().bfloat16().double() - want).norm() / want.norm()).item()
+    codes, scale = ops.fp8_rows(rows, d)
+    ops.moe_quantize_rows_fp8(x, codes, scale)
+    gu8, dn8 = ops.fp8_weights(gu, swiglu=True), ops.fp8_weights(dn)
+    off = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+    for hint, more in ((16, 9e-4), (rows, 2.8e-3 if rows > 16 else 9e-4)):
+        y = torch.empty((rows, d), dtype=torch.bfloat16, device=DEV)
+        ws = ops.workspace(ops.moe_grouped_swiglu_gemm_fp8_workspace_size(1, rows, hint, d, f))
+        ops.moe_grouped_swiglu_gemm_fp8(1, rows, hint, d, f, codes, scale, off, *gu8, *dn8, y, ws)
+        err = ((y.double() - want).norm() / want.norm()).item()
+        assert err <= (rounding ** 2 + more ** 2) ** 0.5, (hint, err, rounding)
