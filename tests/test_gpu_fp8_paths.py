@@ -1,5 +1,6 @@
 """GPU tests of what holds on every path of the products in 8 bits (which one a call takes follows its sizes): scale bytes
-from 0 to 255, rows up to the last, the FFN's error; and of the norm's widest rows.
+from 0 to 255, NaN in rows and weights, padding scales, rows up to the last, the FFN's error; and of the norm: sums of its
+weight's gradient that are known exactly, its widest rows.
 
 Values are whole numbers by powers of two, whose products and sums are exact in the instruction and in floats (below 2^24
 steps), so results EQUAL the rounded reference's, formed in 64 bits on the GPU."""
@@ -122,6 +123,35 @@ def test_scale_byte_255_is_nan(name):
     assert torch.equal(y[~bad], good[~bad])
 
 
+@pytest.mark.parametrize("name", PATHS)
+def test_nan_stays_in_its_row_and_column_on_every_path(name):
+    c = Case(name, 4)
+    good = c.want()
+    bad = torch.zeros_like(good, dtype=torch.bool)
+    for r, k, v in ((0, c.k - 1, np.nan), (c.rows // 2, 0, np.inf), (c.rows - 1, c.k // 2, -np.inf)):
+        c.x[r, k] = v
+        bad[r] = True
+    g = int(np.argmax(c.counts))
+    for n, k, v in ((0, 1, np.nan), (c.n // 2, c.k - 1, -np.inf), (c.n - 1, 3, np.nan)):
+        c.w[g, n, k] = v
+        bad[c.off[g]:c.off[g + 1], n] = True
+    c.quantize()
+    y = c.run()
+    assert torch.equal(y.isnan(), bad)
+    assert torch.equal(y[~bad], good[~bad])
+
+
+@pytest.mark.parametrize("name", PATHS)
+def test_padding_scales_are_not_looked_at_on_any_path(name):
+    c = Case(name, 5)
+    if c.scale.shape[1] == c.kb:
+        pytest.skip("no padding")
+    for byte in (255, 254):
+        c.scale[:, c.kb:] = byte
+        c.ws8[:, :, c.kb:] = byte
+        assert torch.equal(c.run(), c.want())
+
+
 @pytest.mark.parametrize("hint,first", [(16, 2 ** 31 - 1 - 43), (128, 2 ** 31 - 1 - 300), (2 ** 31 - 1, 0)])
 def test_rows_up_to_the_last_that_32_bits_count(hint, first):
     """Groups that end at row 2^31 - 1: of 43 and 300 rows announced as 16 and 128, whose last blocks of rows end within one
@@ -153,6 +183,72 @@ def test_rows_up_to_the_last_that_32_bits_count(hint, first):
         assert torch.equal(y[a:b, 0], want), a
     del y, r, want
     torch.cuda.empty_cache()
+
+
+FFNS = {  # rows of each group, d, f
+    "up to 16 rows": ([5, 9], 200, 140), "up to 128 rows": ([20, 70], 200, 300), "up to 128 rows, cut along K": ([100], 2700, 130),
+    "many rows as they are": ([300, 20], 200, 300), "many rows, packed": ([300], 200, 1100),
+    "many rows, cut along K": ([300, 20], 2700, 257), "down cut along K": ([300], 130, 2700),
+}
+
+
+@pytest.mark.parametrize("name", FFNS)
+def test_ffn_keeps_what_is_not_finite_to_itself(name):
+    """A row that holds NaN, or a scale of 255, is NaN and no other; in the down weights it is that column, in gate_up's every
+    row of the group (H holds it); all else is bit for bit what it is without."""
+    counts, d, f = FFNS[name]
+    say(f"ffn: {name}")
+    gen = torch.Generator(device=DEV).manual_seed(6)
+    G, rows, off = len(counts), sum(counts), np.concatenate([[0], np.cumsum(counts)])
+    x = torch.randn((rows, d), generator=gen, device=DEV)
+    gu, dn = (torch.randn(s, generator=gen, device=DEV) / s[2] ** 0.5 for s in ((G, 2 * f, d), (G, d, f)))
+
+    def run(x, gu, dn, nan_scale=None):
+        codes, scale = ops.fp8_rows(rows, d)
+        ops.moe_quantize_rows_fp8(x, codes, scale)
+        if nan_scale is not None:
+            scale[nan_scale, 0] = 255
+        y = torch.empty((rows, d), dtype=torch.bfloat16, device=DEV)
+        need = ops.moe_grouped_swiglu_gemm_fp8_workspace_size(G, rows, max(counts), d, f)
+        ops.moe_grouped_swiglu_gemm_fp8(G, rows, max(counts), d, f, codes, scale,
+                                        torch.tensor(off, dtype=torch.int32, device=DEV), *ops.fp8_weights(gu, swiglu=True),
+                                        *ops.fp8_weights(dn), y, torch.full((need,), 255, dtype=torch.uint8, device=DEV))
+        return y
+    clean = run(x, gu, dn)
+    assert clean.isfinite().all()
+
+    def same_but(y, bad):
+        assert torch.equal(y.isnan(), bad) and torch.equal(y[~bad], clean[~bad])
+    none = torch.zeros_like(clean, dtype=torch.bool)
+    x2, bad = x.clone(), none.clone()
+    x2[1, d - 1], x2[rows - 1, 0] = np.nan, np.inf
+    bad[[1, rows - 1, 2]] = True
+    same_but(run(x2, gu, dn, nan_scale=2), bad)
+    dn2, bad = dn.clone(), none.clone()
+    dn2[0, d // 2, f - 1] = np.nan
+    bad[:off[1], d // 2] = True
+    # the block's other weights keep their codes: the largest of the block is another
+    assert dn[0, d // 2, f - 1].abs() < dn[0, d // 2 // 128 * 128:(d // 2 // 128 + 1) * 128, (f - 1) // 128 * 128:].abs().max()
+    same_but(run(x, gu, dn2), bad)
+    gu2, bad = gu.clone(), none.clone()
+    gu2[0, 2 * f - 1, 3] = np.nan
+    bad[:off[1]] = True
+    same_but(run(x, gu2, dn), bad)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,d", [(40000, 64), (9001, 2100), (70001, 5)])
+def test_weight_gradient_of_whole_numbers_is_exact(T, d, dt):
+    """More than 512 workgroups' parts: each counted, and once.  Sums of T products up to 16 stay below 2^24."""
+    say(f"dweight of whole numbers {T} x {d}")
+    gen = torch.Generator(device=DEV).manual_seed(T)
+    dy, h = (torch.randint(-4, 5, (T, d), generator=gen, device=DEV).to(dt) for _ in range(2))
+    w, rstd = torch.ones(d, dtype=dt, device=DEV), torch.ones(T, device=DEV)
+    dx, dw = torch.empty_like(h), torch.empty(d, device=DEV)
+    need = ops.moe_rms_norm_backward_workspace_size(T, d)
+    assert need >= 513 * d * 4
+    ops.moe_rms_norm_backward(dy, h, w, rstd, dx, dw, ops.workspace(need))
+    assert torch.equal(dw.double(), (dy.double() * h.double()).sum(dim=0))
 
 
 def test_norm_of_the_widest_rows_past_32_bits_of_threads():
