@@ -643,7 +643,8 @@ moe_status moe_quantize_weights_fp8(int32_t num_groups, int32_t n_out, int32_t k
  *   y = (h rstd) weight, in float; y rounded to dtype, and y8 quantised from the float
  *   x, residual  [T, d] dtype; residual may be NULL
  *   weight       [d] dtype
- *   eps          finite, >= 0 (a row of zeros with eps 0 gives NaN)
+ *   eps          finite, >= 0 (with eps 0 a row of zeros gives NaN, and one whose root mean square is below 2^-128, so that
+ *                rstd passes the floats, infinities)
  *   h            [T, d] dtype or NULL; may be x or residual
  *   y            [T, d] dtype or NULL; may be x or residual, not h
  *   y8, y_scale  y in 8 bits (layout above), both or neither NULL

@@ -314,10 +314,12 @@ inline int fp8_parts_cap(int64_t rows, int64_t group_rows, int n_out, int k, boo
   const int tiles_n = (int)(fp8_part_columns(n_out, swiglu) / 256);
   return fp8_parts((rows + per - 1) / per * tiles_n, rows, tiles_n, k, kFp8Parts);
 }
-// Whether the tiles of many rows past the last whole 256 are looked at for that: K past 7168, where a second launch with
-// nothing to add is a twentieth of a round or less; few enough rounds; and for one group, whose tiles are known,
-// only if they are cut.  us whole and cut: 8 x 1024 rows, 4096 x 14336 (576 tiles, 2.25 rounds) 474 and 425; 4096 x 14336 x
-// 14336 (896, 3.5) 686 and 658.
+// Whether the tiles of many rows past the last whole 256 are looked at for that: K past 7168; few enough rounds; and for one
+// group, whose tiles are known, only if they are cut (of several only the device knows, and the second launch follows in
+// any case).  us whole and cut, n_out 4096, K 4096, 7168 and 14336: 288 tiles of one group 107 and 109, 165 and 151, 304 and
+// 250; of three groups 104 and 106, 163 and 150, 308 and 258; 576 of nine 176 and 184, 275 and 266, 510 and 480; 640 of
+// eight 163 and 169, 258 and 263, 483 and 495; 512 of eight, none to cut, 131 and 135, 213 and 216, 397 and 399.  So up to
+// 4096 it loses, by as much as 5%, past 7168 it wins up to 18% or loses 2.5%, and between it does either.
 inline bool fp8_rounds(int64_t rows, int G, int n_out, int k, bool swiglu, bool large) {
   const int64_t tiles_n = fp8_part_columns(n_out, swiglu) / 256, least = (rows + kFp8LargeRows - 1) / kFp8LargeRows * tiles_n;
   if (!large || fp8_scale_bytes(k) / 4 < 15 || least > 8 * 256) return false;

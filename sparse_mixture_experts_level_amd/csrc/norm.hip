@@ -247,8 +247,10 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rms_norm_backward_kerne
 }
 
 // 16 columns a workgroup, sixteen rows of parts at a time, all loads of 512 rows in flight
-// (range-checked: behind a branch each, one at a time, 12 us for 4); sums in 64 bits, as the
-// parts' float sums lose a third as much as adding them in floats does (5003 rows: 1.5e-7 of dweight's norm).
+// (range-checked: behind a branch each, one at a time, 12 us for 4); sums in 64 bits: added in floats the parts lost 1.5e-7 of
+// dweight's norm at 5003 x 1091, for 6e-8 now, half a step of the result.  The parts themselves are floats, as 64 bits would
+// double the registers that they take; they lose more with more rows a thread: 1.1e-7 at 10^5 rows of 64, 3.3e-7 at 10^6,
+// 1.4e-6 at 1.6 10^7 (torch's sums in floats: 1.6e-7, 2.8e-7, 8.0e-7).
 __global__ __launch_bounds__(256) void rms_norm_dweight_kernel(const float *__restrict__ parts, int n, int d,
                                                                float *__restrict__ dweight) {
   __shared__ double s[16][17];
@@ -292,7 +294,8 @@ void by_width(int d, F f) {
   MOE_WIDTH(256, 4);
   MOE_WIDTH(256, 8);
 #undef MOE_WIDTH
-  if constexpr (BACKWARD)  // (1024 x 4 have 128 registers each: it spilled, 3050 x 16391 of bf16 at 0.9 TB/s for 2.4)
+  if constexpr (BACKWARD)  // (1024 x 4 have 128 registers each and spilled: 3050 x 16391 of bf16 at 0.9 TB/s for 2.3. 512 x 8
+                           // still spill 14 to 24 registers of bf16 and 106 to 205 of float rows: 2.0 TB/s)
     whole(std::integral_constant<int, 512>{}, std::integral_constant<int, 8>{});
   else
     whole(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});

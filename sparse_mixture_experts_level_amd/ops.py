@@ -1004,10 +1004,11 @@ def moe_forward_fp8(desc, w_router, gate_up, down, x, logit_offset, out, ws, rou
 class MoELayer:
     """Holds one layer's device tensors and a workspace, and runs moe_forward.
 
-    fp8: the experts (and the shared expert) in 8 bits, quantised here once (moe_forward_fp8).
+    fp8: the experts (and the shared expert) in 8 bits, quantised here once (moe_forward_fp8); the bf16 ones of `inputs` are
+    not read again and may be set to None.
     norm_weight [d]: a norm in front of the layer (moe_rms_norm with norm_eps): forward(residual) takes
-    inputs.x + residual, kept in `h` (the next block's residual), and the layer runs on its norm, `normed`, which it
-    gets in 8 bits too with fp8.
+    inputs.x + residual, kept in `h` (the next block's residual; a copy of inputs.x without a residual), and the layer runs
+    on its norm, `normed`, which it gets in 8 bits too with fp8.
 
     Convenience only: allocation happens here, once, never inside a forward call."""
 

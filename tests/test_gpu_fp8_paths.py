@@ -1,6 +1,6 @@
 """GPU tests of what holds on every path of the products in 8 bits (which one a call takes follows its sizes): scale bytes
 from 0 to 255, NaN in rows and weights, padding scales, rows up to the last, the FFN's error; and of the norm: sums of its
-weight's gradient that are known exactly, its widest rows.
+weight's gradient that are known exactly, its widest rows, rows in place.
 
 Values are whole numbers by powers of two, whose products and sums are exact in the instruction and in floats (below 2^24
 steps), so results EQUAL the rounded reference's, formed in 64 bits on the GPU."""
@@ -8,6 +8,7 @@ import numpy as np
 import pytest
 import torch
 
+from sparse_mixture_experts_level_amd import workloads as wl
 from tests.moe_testlib import say
 
 pytestmark = pytest.mark.gpu
@@ -316,3 +317,41 @@ def test_error_of_the_ffn_against_64_bits(rows, d, f):
         ops.moe_grouped_swiglu_gemm_fp8(1, rows, hint, d, f, codes, scale, off, *gu8, *dn8, y, ws)
         err = ((y.double() - want).norm() / want.norm()).item()
         assert err <= (rounding ** 2 + more ** 2) ** 0.5, (hint, err, rounding)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [2055, 4097, 8203, 16391])
+def test_norm_in_place_with_several_waves_a_row(d, dt):
+    """h over x or the residual, y over x or the other of the two: odd rows, whose last eight values are loaded across the columns
+    of another wave."""
+    gen = torch.Generator(device=DEV).manual_seed(d)
+    x, r = (torch.randn((5, d), generator=gen, device=DEV).to(dt) for _ in range(2))
+    w = (1 + 0.2 * torch.randn(d, generator=gen, device=DEV)).to(dt)
+    h, y = torch.empty_like(x), torch.empty_like(x)
+    ops.moe_rms_norm(x, w, 1e-6, residual=r, h=h, y=y)
+    for h_in, y_in in ((0, None), (1, None), (None, 0), (None, 1), (0, 1), (1, 0)):
+        both = [x.clone(), r.clone()]
+        h2 = None if h_in is None else both[h_in]
+        y2 = torch.empty_like(x) if y_in is None else both[y_in]
+        ops.moe_rms_norm(both[0], w, 1e-6, residual=both[1], h=h2, y=y2)
+        assert torch.equal(y2, y) and (h2 is None or torch.equal(h2, h)), (h_in, y_in)
+
+
+def test_norm_of_tiny_rows_without_eps():
+    """A root mean square of 2^-127 still has its 1 / sqrt in the floats, one of 2^-129 does not."""
+    x = torch.tensor([[2.0 ** -127] * 64, [2.0 ** -129] * 64, [0.0] * 64], device=DEV)
+    y, rstd = torch.empty_like(x), torch.empty(3, device=DEV)
+    ops.moe_rms_norm(x, torch.ones(64, device=DEV), 0.0, y=y, rstd=rstd)
+    assert torch.all(y[0] == 1) and torch.all(y[1] == float("inf")) and torch.all(y[2].isnan())
+    assert rstd.tolist() == [2.0 ** 127, float("inf"), float("inf")]
+
+
+def test_layer_in_8_bits_without_the_bf16_experts():
+    """Once made the layer reads its 8-bit copies alone."""
+    w = wl.Workload("freed", 40, 256, 4, 2, 128, None, "bf16", d_ff_shared=64)
+    inputs = wl.make_inputs(w, seed=0, device=DEV)
+    layer = ops.MoELayer(inputs, None, device=DEV, fp8=True)
+    want = layer.forward().clone()
+    inputs.w_gate_up = inputs.w_down = inputs.w_shared_gate_up = inputs.w_shared_down = None
+    layer.out.zero_()
+    assert torch.equal(layer.forward(), want)
