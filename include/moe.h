@@ -611,7 +611,7 @@ int32_t moe_fp8_row_bytes(int32_t k);
 int32_t moe_fp8_scale_bytes(int32_t k);
 
 /* Rows to 8 bits.  x [rows, K] dtype; codes, scale as above, written in full (codes behind
- * column K zeros, padding scales ones).  0 <= rows <= INT32_MAX. */
+ * column K zeros, padding scales ones).  0 <= rows <= INT32_MAX, 1 <= K < 2^24. */
 moe_status moe_quantize_rows_fp8(int64_t rows, int32_t k, int32_t dtype, const void *x, uint8_t *codes, uint8_t *scale,
                                  hipStream_t stream);
 

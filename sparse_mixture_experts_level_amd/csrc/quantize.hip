@@ -76,10 +76,10 @@ __global__ __launch_bounds__(256) void quantize_weights_kernel(const T *__restri
                                                                uint8_t *__restrict__ scale) {
   __shared__ float part[4];
   __shared__ __attribute__((aligned(16))) uint8_t tile[128 * 128];
-  const int kb = blockIdx.x, halves = swiglu ? 2 : 1;
-  const int nb = __builtin_amdgcn_readfirstlane(blockIdx.y / halves), half = blockIdx.y - nb * halves;
-  const int64_t g = blockIdx.z;
-  const int kt = fp8_blocks(K), nt = (n_out + 15) / 16;
+  const int kt = fp8_blocks(K), nt = (n_out + 15) / 16, halves = swiglu ? 2 : 1;
+  const int block = __builtin_amdgcn_readfirstlane((int)blockIdx.x / kt), kb = (int)blockIdx.x - block * kt;
+  const int nb = __builtin_amdgcn_readfirstlane(block / halves), half = block - nb * halves;
+  const int64_t g = blockIdx.y;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const T *m = w + (g * halves + half) * (int64_t)n_out * K;
   // this wave's 32 rows; past the matrix zeros (range-checked loads: behind a branch each they would go one at a time)
@@ -169,7 +169,8 @@ int64_t fp8_weight_scales_bytes(int n_out, int K, bool swiglu) {
 
 hipError_t launch_quantize_weights(const void *w, bool f32, int G, int n_out, int K, bool swiglu, uint8_t *codes,
                                    uint8_t *scale, hipStream_t s) {
-  const dim3 grid((unsigned)fp8_blocks(K), (unsigned)(fp8_blocks(n_out) * (swiglu ? 2 : 1)), (unsigned)G);
+  // (a group's blocks of 16 KB are below 2^17, as its codes are below 2 GiB)
+  const dim3 grid((unsigned)(fp8_blocks(n_out) * (swiglu ? 2 : 1)) * (unsigned)fp8_blocks(K), (unsigned)G);
   if (f32)
     hipLaunchKernelGGL(quantize_weights_kernel<float>, grid, dim3(256), 0, s, static_cast<const float *>(w), n_out, K,
                        swiglu ? 1 : 0, codes, scale);

@@ -38,6 +38,21 @@ def _draw(gen, *shape):
     return torch.where(v.abs() == 3, 4 * v.sign(), v).float()
 
 
+def _held(v, rows_a_block):
+    """v in 8 bits and back, in 64 bits: blocks of rows_a_block x 128, e4m3 codes rounded by torch (from floats: other than
+    from 64 bits for values within 2^-24 of a border)."""
+    n, k = v.shape
+    p = torch.nn.functional.pad(v, (0, -k % 128, 0, -n % rows_a_block))
+    p = p.view(-1, rows_a_block, p.shape[1] // 128, 128)
+    top = p.abs().amax((1, 3), keepdim=True)
+    e = torch.ceil(torch.log2(top / 448))
+    e = torch.where(top > 448 * 2.0 ** e, e + 1, e)
+    e = torch.where(top <= 448 * 2.0 ** (e - 1), e - 1, e)
+    e = torch.where(top == 0, 0.0, e)
+    q = (p / 2.0 ** e).float().to(torch.float8_e4m3fn).double() * 2.0 ** e
+    return q.view(-1, p.shape[2] * 128)[:n, :k]
+
+
 class Case:
     """A grouped product of drawn codes: codes and scales of rows and weights, made by the library from whole numbers whose
     blocks all have 4 as their largest, so that every scale byte is 121 (4 = 256 2^-6)."""
@@ -186,6 +201,85 @@ def test_rows_up_to_the_last_that_32_bits_count(hint, first):
     torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("n,k,swiglu", [(4194304 + 37, 3, True), (2 ** 23 - 1, 1, False), (20, 2 ** 23 - 1, False)])
+def test_weights_of_the_most_rows_and_the_longest(n, k, swiglu):
+    """More blocks of 128 than 65535 one way: codes and scales are those of torch's own 8-bit type, at every place of the layout."""
+    say(f"weights {n} x {k} swiglu {swiglu}")
+    gen = torch.Generator(device=DEV).manual_seed(8)
+    h = 2 if swiglu else 1
+    w = torch.randn((1, h * n, k), generator=gen, device=DEV).bfloat16()
+    codes, scale = ops.fp8_weights(w, swiglu)
+    nt, nb, kb = -(-n // 16), -(-n // 128), -(-k // 128)
+    p = torch.nn.functional.pad(w.view(h, n, k), (0, kb * 128 - k, 0, nb * 128 - n))
+    p = p.view(h, nb, 128, kb, 128)
+    top = p.abs().amax((2, 4)).double()
+    e = torch.ceil(torch.log2(top / 448))
+    e = torch.where(top > 448 * 2.0 ** e, e + 1, e)
+    e = torch.where(top <= 448 * 2.0 ** (e - 1), e - 1, e)
+    got = scale.view(nb, h, -1).transpose(0, 1)
+    assert torch.equal(got[:, :, :kb].double() - 127, e) and torch.all(got[:, :, kb:] == 127)
+    blocks = nt * h  # tiles of sixteen blocks of 16 rows, the last has what is left
+    for first in range(0, blocks, 1 << 16):
+        last = min(first + (1 << 16), blocks)
+        tiles = codes[first * kb * 2048:last * kb * 2048]
+        b = min(16, last - first)
+        whole = (last - first) // b * b
+        for start, count, size in ((0, whole // b, b), (whole, 1 if last - first > whole else 0, last - first - whole)):
+            if count == 0:
+                continue
+            part = tiles[start * kb * 2048:(start + count * size) * kb * 2048].view(count, kb, 2, size, 4, 16, 16)
+            part = part.permute(0, 3, 5, 1, 2, 4, 6).reshape(count * size, 16, kb * 128)  # [block][row][k]
+            ids = torch.arange(first + start, first + start + count * size, device=DEV)
+            rows = (ids // h * 16)[:, None] + torch.arange(16, device=DEV)
+            there = rows < n
+            src = w.view(h, n, k)[(ids % h)[:, None], rows.clamp(max=n - 1)].float() * there[..., None]
+            s = torch.exp2(e.float())[(ids % h)[:, None], rows.clamp(max=n - 1) // 128]  # [block][row][kb]
+            want = (src / s.repeat_interleave(128, dim=2)[:, :, :k]).to(torch.float8_e4m3fn).view(torch.uint8)
+            assert torch.equal(part[:, :, :k] & torch.where(want == 128, 127, 255).to(torch.uint8), want & torch.where(
+                want == 128, 127, 255).to(torch.uint8)) and not part[:, :, k:].any(), first
+            del part, src, want, s
+    # and a product reads them where they are
+    x = torch.randn((3, k), generator=gen, device=DEV)
+    if not swiglu and k < 128:
+        rc, rs = ops.fp8_rows(3, k)
+        ops.moe_quantize_rows_fp8(x, rc, rs)
+        y = torch.empty((3, n), dtype=torch.bfloat16, device=DEV)
+        off = torch.tensor([0, 3], dtype=torch.int32, device=DEV)
+        for hint in (16, 17):
+            ws = ops.workspace(ops.moe_grouped_linear_fp8_workspace_size(1, 3, hint, n, k))
+            ops.moe_grouped_linear_fp8(1, 3, hint, n, k, rc, rs, off, codes, scale, y, ws)
+            xv, wv = torch.empty((3, k), device=DEV), _held(w[0].double(), 128)
+            ops.moe_dequantize_rows_fp8(rc, rs, xv)
+            want = xv.double() @ wv.T
+            assert torch.all((y.double() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-30)
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("rows", [5, 40, 512])
+def test_products_of_the_longest_rows(rows):
+    """K of 2^23 - 1: rows whose values stand far apart, among them the last, times weights likewise; sums are exact."""
+    k, n = 2 ** 23 - 1, 20
+    say(f"longest rows, {rows}")
+    torch.cuda.empty_cache()
+    gen = torch.Generator(device=DEV).manual_seed(rows)
+    x = torch.zeros((rows, k), dtype=torch.bfloat16, device=DEV)
+    w = torch.zeros((1, n, k), dtype=torch.bfloat16, device=DEV)
+    at = torch.cat([torch.randint(0, k, (4000,), generator=gen, device=DEV), torch.tensor([0, k - 1], device=DEV)]).unique()
+    x[:, at] = torch.randint(1, 5, (rows, len(at)), generator=gen, device=DEV).bfloat16()
+    w[0][:, at] = torch.randint(-4, 5, (n, len(at)), generator=gen, device=DEV).bfloat16()
+    codes, scale = ops.fp8_rows(rows, k)
+    ops.moe_quantize_rows_fp8(x, codes, scale)
+    w8 = ops.fp8_weights(w)
+    y = torch.empty((rows, n), dtype=torch.bfloat16, device=DEV)
+    need = ops.moe_grouped_linear_fp8_workspace_size(1, rows, rows, n, k)
+    ops.moe_grouped_linear_fp8(1, rows, rows, n, k, codes, scale, torch.tensor([0, rows], dtype=torch.int32, device=DEV), *w8, y,
+                               ops.workspace(need))
+    want = x[:, at].double() @ w[0][:, at].double().T
+    assert torch.equal(y, want.float().bfloat16())
+    del x, w, codes, scale, w8
+    torch.cuda.empty_cache()
+
+
 FFNS = {  # rows of each group, d, f
     "up to 16 rows": ([5, 9], 200, 140), "up to 128 rows": ([20, 70], 200, 300), "up to 128 rows, cut along K": ([100], 2700, 130),
     "many rows as they are": ([300, 20], 200, 300), "many rows, packed": ([300], 200, 1100),
@@ -275,21 +369,6 @@ def test_norm_of_the_widest_rows_past_32_bits_of_threads():
     assert torch.equal(got, want) and torch.equal(got_r, want_r)
     rstd[at] = 1000.0
     assert torch.all((rstd - 1000.0).abs() < 1e-2)
-
-
-def _held(v, rows_a_block):
-    """v in 8 bits and back, in 64 bits: blocks of rows_a_block x 128, e4m3 codes rounded by torch (from floats: other than
-    from 64 bits for values within 2^-24 of a border)."""
-    n, k = v.shape
-    p = torch.nn.functional.pad(v, (0, -k % 128, 0, -n % rows_a_block))
-    p = p.view(-1, rows_a_block, p.shape[1] // 128, 128)
-    top = p.abs().amax((1, 3), keepdim=True)
-    e = torch.ceil(torch.log2(top / 448))
-    e = torch.where(top > 448 * 2.0 ** e, e + 1, e)
-    e = torch.where(top <= 448 * 2.0 ** (e - 1), e - 1, e)
-    e = torch.where(top == 0, 0.0, e)
-    q = (p / 2.0 ** e).float().to(torch.float8_e4m3fn).double() * 2.0 ** e
-    return q.view(-1, p.shape[2] * 128)[:n, :k]
 
 
 @pytest.mark.parametrize("rows,d,f", [(80, 2048, 1024), (300, 1024, 1100), (16, 2048, 1024)])
