@@ -1005,7 +1005,7 @@ class MoELayer:
     """Holds one layer's device tensors and a workspace, and runs moe_forward.
 
     fp8: the experts (and the shared expert) in 8 bits, quantised here once (moe_forward_fp8); the bf16 ones of `inputs` are
-    not read again and may be set to None.
+    not read again: they may be set to None, and where they change a layer has to be built again.
     norm_weight [d]: a norm in front of the layer (moe_rms_norm with norm_eps): forward(residual) takes
     inputs.x + residual, kept in `h` (the next block's residual; a copy of inputs.x without a residual), and the layer runs
     on its norm, `normed`, which it gets in 8 bits too with fp8.

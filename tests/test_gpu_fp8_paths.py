@@ -434,3 +434,69 @@ def test_layer_in_8_bits_without_the_bf16_experts():
     inputs.w_gate_up = inputs.w_down = inputs.w_shared_gate_up = inputs.w_shared_down = None
     layer.out.zero_()
     assert torch.equal(layer.forward(), want)
+
+
+def test_training_step_with_a_norm_replays_from_a_graph():
+    """The whole step captured, with a residual and a gradient on h: replays, with eager work between, follow the eager trainer
+    bit for bit."""
+    w = wl.Workload("captured", 72, 128, 4, 2, 128, None, "bf16", d_ff_shared=64)
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    res, dy, dh = (torch.randn((72, 128), generator=gen, device=DEV).bfloat16() for _ in range(3))
+    made = []
+    for _ in range(2):
+        weight = torch.ones(128, dtype=torch.bfloat16, device=DEV)
+        made.append(ops.MoETrainer(wl.make_inputs(w, seed=0, device=DEV), None, device=DEV, norm_weight=weight, state_bits=8,
+                                   master_weights=True, lr=1e-2, max_grad_norm=1.0, capturable=True))
+    eager, other = made
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other.train_step(dy, residual=res, dh=dh)
+    torch.cuda.current_stream().wait_stream(side)
+    eager.train_step(dy, residual=res, dh=dh)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        other.train_step(dy, residual=res, dh=dh)
+    start = eager.layer.norm_weight.clone()
+    for i in range(4):
+        res.mul_(1 + 2.0 ** -5 * i)
+        eager.train_step(dy, residual=res, dh=dh)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(eager.optimizer.params, other.optimizer.params):
+            assert torch.equal(a, b), i
+        assert torch.equal(eager.dx, other.dx) and torch.equal(eager.layer.h, other.layer.h)
+        assert torch.equal(eager.grads["dw_norm"], other.grads["dw_norm"]), i
+    assert not torch.equal(start, eager.layer.norm_weight)
+
+
+def test_norm_and_conversions_on_another_stream():
+    """On a stream that is busy with what they read: they wait for it, and for nothing else."""
+    T, d = 700, 2055
+    gen = torch.Generator(device=DEV).manual_seed(4)
+    x, dy = (torch.randn((T, d), generator=gen, device=DEV).bfloat16() for _ in range(2))
+    w = torch.ones(d, dtype=torch.bfloat16, device=DEV)
+
+    def everything(x, stream):
+        y, rstd, dx, dw = torch.empty_like(x), torch.empty(T, device=DEV), torch.empty_like(x), torch.empty(d, device=DEV)
+        codes, scale = ops.fp8_rows(T, d)
+        back = torch.empty_like(x)
+        ws = ops.workspace(ops.moe_rms_norm_backward_workspace_size(T, d))
+        torch.cuda.synchronize()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                torch.cuda._sleep(20_000_000)
+                x.copy_(keep)
+        ops.moe_rms_norm(x, w, 1e-6, y=y, rstd=rstd, y8=codes, y_scale=scale, stream=stream)
+        ops.moe_rms_norm_backward(dy, x, w, rstd, dx, dw, ws, stream=stream)
+        ops.moe_dequantize_rows_fp8(codes, scale, back, stream=stream)
+        ops.moe_quantize_rows_fp8(back, codes, scale, stream=stream)
+        torch.cuda.synchronize()
+        return y, rstd, dx, dw, codes, scale, back
+    keep = x.clone()
+    want = everything(x, None)
+    other = torch.zeros_like(x)
+    for a, b in zip(everything(other, torch.cuda.Stream()), want):
+        assert torch.equal(a, b)
